@@ -174,6 +174,33 @@ kd_status kd_session_free(kd_model* m, int32_t session_id);
 kd_status kd_session_load_kv(kd_model* m, int32_t session_id, const void* k_fp16,
                              const void* v_fp16, int32_t len, kd_stream stream);
 
+/* Sliding-window attention for the model's steps.  With window >= 1 a row at
+ * position p attends the keys t <= p with t < sinks (the first tokens, which stay
+ * visible) or t > p - window; window 0 (the state after kd_model_load) attends
+ * every key 0..p again.  The caches keep every row.  Waits for the model's
+ * outstanding work and drops the captured steps.
+ * Errors: KD_ERR_INVALID_ARG (null model, window or sinks < 0). */
+kd_status kd_model_set_window(kd_model* m, int32_t window, int32_t sinks);
+
+/* Reorder sessions: for all i < n at once, session ids[i] becomes a copy of what
+ * session parents[i] was before the call (its length and its cache rows, all
+ * layers), in place: what a beam search does with kd_beam_select's parents.
+ * Parents may repeat, be among the ids, or be the id itself; parents[i] = -1
+ * leaves ids[i] as it is.  With a window set, only the rows that a step at or
+ * after the session's length can attend are copied (the first `sinks` and the
+ * last window - 1); a later step that would attend any other row of the copy (a
+ * rewind, a wider or removed window) is refused with KD_ERR_POSITION.
+ * ids, parents: host arrays of n, 1 <= n <= KD_REORDER_MAX (else KD_ERR_BATCH).
+ * Enqueued on `stream` after the model's previous step.
+ * Errors: KD_ERR_BAD_SESSION (an id or parent not bound, an id repeated). */
+#define KD_REORDER_MAX 64
+kd_status kd_session_reorder(kd_model* m, const int32_t* ids, const int32_t* parents, int32_t n, kd_stream stream);
+
+/* Bind a free slot as a copy of session session_id (kd_session_bind, then
+ * kd_session_reorder of that one pair).  On failure nothing stays bound.
+ * Errors: KD_ERR_BAD_SESSION, KD_ERR_NO_FREE_SLOT. */
+kd_status kd_session_fork(kd_model* m, int32_t session_id, int32_t* new_id_out, kd_stream stream);
+
 /* The number of positions a bound session holds: memra's `cache.pos`, which a
  * batched step moves forward by one for every row, as a single-sequence step
  * would (decode_batch.rs `decode_step_batch`); here it becomes the step's
@@ -430,6 +457,102 @@ kd_status kd_attn_append_decode_q8(const float* q, const float* k_new, const flo
                                    const int32_t* slots, const int32_t* positions, int32_t B, int32_t n_heads,
                                    int32_t n_kv_heads, int32_t n_slots, int32_t cap, uint16_t* out,
                                    void* workspace, size_t workspace_bytes, kd_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Windowed attention, beam selection, cache reorder: the operators of long and
+ * branching sessions on their own.  Calls copy nothing to the device, so they
+ * can be captured into a graph; host arrays then belong to the graph.
+ * ---------------------------------------------------------------------- */
+
+/* Bytes of device workspace a windowed attention call needs:
+ *   256 + B * n_heads * items * (head_dim + 4) * 4,
+ *   items = min(ceil(cap / 64), ceil(min(sinks, cap) / 64) + ceil((min(window, cap) + 7) / 64))
+ * (0 for sizes a call refuses). */
+size_t kd_attn_window_workspace_bytes(int32_t B, int32_t n_heads, int32_t head_dim, int32_t cap, int32_t window,
+                                      int32_t sinks);
+
+/* kd_attn_append_decode with a sliding window: append row pos_b, then
+ *   out[b][qh] = fp16(sum_{t in V_b} softmax_t(q[b][qh] . K_t / sqrt(head_dim)) V_t),
+ *   V_b = { t <= pos_b : t < sinks or t > pos_b - window }.
+ * window >= 1 (the new row itself is always seen), sinks >= 0; either may exceed
+ * cap.  Cache rows outside V_b are not used, whatever they hold.  A row's
+ * result depends on its own position, window and sinks, not on the batch.
+ * Workspace: kd_attn_window_workspace_bytes(B, n_heads, head_dim, cap, window,
+ * sinks), used by one call at a time.  n_slots * n_kv_heads * cap < 2^31.  Other
+ * arguments, alignments and errors as for kd_attn_append_decode;
+ * kd_attn_device_status(workspace, ...) reads the call's fault word. */
+kd_status kd_attn_window_append_decode(const float* q, const float* k_new, const float* v_new, uint16_t* k_cache,
+                                       uint16_t* v_cache, const int32_t* slots, const int32_t* positions, int32_t B,
+                                       int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t n_slots,
+                                       int32_t cap, int32_t window, int32_t sinks, uint16_t* out, void* workspace,
+                                       size_t workspace_bytes, kd_stream stream);
+
+/* The same over a Q8_0 cache (head_dim 128, even cap), as
+ * kd_attn_append_decode_q8. */
+kd_status kd_attn_window_append_decode_q8(const float* q, const float* k_new, const float* v_new, uint8_t* k_quants,
+                                          uint16_t* k_scales, uint8_t* v_quants, uint16_t* v_scales,
+                                          const int32_t* slots, const int32_t* positions, int32_t B, int32_t n_heads,
+                                          int32_t n_kv_heads, int32_t n_slots, int32_t cap, int32_t window,
+                                          int32_t sinks, uint16_t* out, void* workspace, size_t workspace_bytes,
+                                          kd_stream stream);
+
+#define KD_BEAM_MAX_BEAMS 16
+#define KD_BEAM_MAX_OUT 32
+#define KD_BEAM_MAX_VOCAB 524288
+
+/* Bytes of device workspace kd_beam_select needs:
+ *   256 + n_groups * n_beams * ceil(V / 4096) * (8 + 8 * n_out). */
+size_t kd_beam_workspace_bytes(int32_t n_groups, int32_t n_beams, int32_t V, int32_t n_out);
+
+/* Beam selection: each group's n_out best continuations over its beams and the
+ * vocabulary.  Row r = g * n_beams + w of the logits is beam w of group g;
+ * continuing it with token v scores
+ *   s(w, v) = scores[r] + x_rv - log sum_u exp(x_ru)
+ * (x - max taken as 0 where x equals the row's maximum, so infinite logits share
+ * the row's mass).  NaN and -inf logits are no candidates and add nothing to the
+ * sum.  A beam whose score is -inf or NaN offers nothing, and its logits are not
+ * read (so a search starts with one beam at 0 and the others at -inf); a finished
+ * beam (done[r] != 0) offers itself alone: token eos at s = scores[r], its logits
+ * not read either.
+ * The best come first: larger s, then the lower beam, then (within a beam) the
+ * larger logit, then the lower token.  s is ordered in fp64 (the row sums are
+ * good to about 1e-8) and stored as fp32; a row's s does not depend on the batch.
+ *   parents_out, tokens_out: device int32 [n_groups][n_out], the beam w (not the
+ *     row) and the token; -1 where fewer candidates exist.
+ *   scores_out: device fp32 [n_groups][n_out], -inf there.
+ *   done_out: NULL or device int32 [n_groups][n_out]: 1 where the parent was
+ *     finished or the token is eos, else 0.
+ * logits: device fp32, row r at logits + r * ld (ld >= V), 4-byte aligned; scores:
+ * NULL (zeros) or device fp32; done: NULL or device int32 (then eos must be a
+ * token); eos: -1 for none.  No output may overlap an input.  workspace: device,
+ * 16-byte aligned, kd_beam_workspace_bytes(...), used by one call at a time.
+ * Errors: KD_ERR_BATCH (n_beams outside [1, KD_BEAM_MAX_BEAMS], n_groups < 1, more
+ * than 65535 rows), KD_ERR_UNSUPPORTED (V above KD_BEAM_MAX_VOCAB),
+ * KD_ERR_INVALID_ARG (null or misaligned pointers, n_out outside
+ * [1, KD_BEAM_MAX_OUT], V < 1, ld < V, eos, a workspace too small). */
+kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int32_t n_beams, int32_t V,
+                         const float* scores, const int32_t* done, int32_t eos, int32_t n_out, int32_t* parents_out,
+                         int32_t* tokens_out, float* scores_out, int32_t* done_out, void* workspace,
+                         size_t workspace_bytes, kd_stream stream);
+
+/* Reorder a slot-indexed cache in place: for all i < n at once, the first lens[i]
+ * rows of slot dst[i] (every layer and head) become what slot src[i] held before
+ * the call; with window >= 1 only the rows t of them with t < sinks or
+ * t > lens[i] - window (those that a windowed step at position lens[i] or later
+ * attends).  Other rows and slots stay as they were.  dst distinct; src may
+ * repeat and may be among dst (swaps, cycles, forks).
+ * planes: host array of n_planes (1..4) device pointers, 16-byte aligned; plane p
+ * is [n_layers][n_slots][n_kv_heads][cap] rows of row_bytes[p] bytes (a multiple
+ * of 8, at most 1024): an fp16 cache has K and V of 2 * head_dim, a Q8_0 cache
+ * quants of 128 and scales of 8 for each.  Planes must not overlap.
+ * dst, src, lens: host arrays of n, 1 <= n <= KD_REORDER_MAX, 0 <= lens[i] <= cap.
+ * Errors: KD_ERR_BATCH (n), KD_ERR_BAD_SESSION (a slot out of range, or written
+ * twice), KD_ERR_POSITION (lens), KD_ERR_UNSUPPORTED (row_bytes, cap above
+ * KD_REORDER_MAX_CAP, n_layers * n_kv_heads above 65535), KD_ERR_INVALID_ARG. */
+#define KD_REORDER_MAX_CAP 131072
+kd_status kd_kv_reorder(void* const* planes, const int32_t* row_bytes, int32_t n_planes, int32_t n_layers,
+                        int32_t n_slots, int32_t n_kv_heads, int32_t cap, const int32_t* dst, const int32_t* src,
+                        const int32_t* lens, int32_t n, int32_t window, int32_t sinks, kd_stream stream);
 
 /* ------------------------------------------------------------------------
  * Allocation-free variant (no counterpart on the batched-decode pages: it

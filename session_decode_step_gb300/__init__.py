@@ -110,6 +110,16 @@ def lib():
                                               i32, _vp, _vp],
             "kd_kv_q8_quantize": [_vp, C.c_int64, _vp, _vp, _vp],
             "kd_debug_fail_alloc": [i32, i32p],
+            "kd_model_set_window": [_vp, i32, i32],
+            "kd_session_reorder": [_vp, i32p, i32p, i32, _vp],
+            "kd_session_fork": [_vp, i32, i32p, _vp],
+            "kd_attn_window_append_decode": [_vp, _vp, _vp, _vp, _vp, i32p, i32p, i32, i32, i32, i32, i32, i32, i32, i32,
+                                             _vp, _vp, C.c_size_t, _vp],
+            "kd_attn_window_append_decode_q8": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, i32p, i32p, i32, i32, i32, i32, i32,
+                                                i32, i32, _vp, _vp, C.c_size_t, _vp],
+            "kd_beam_select": [_vp, C.c_int64, i32, i32, i32, _vp, _vp, i32, i32, _vp, _vp, _vp, _vp, _vp, C.c_size_t,
+                               _vp],
+            "kd_kv_reorder": [_vpp, i32p, i32, i32, i32, i32, i32, i32p, i32p, i32p, i32, i32, i32, _vp],
             "kd_attn_append_decode_q8": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, i32p, i32p, i32, i32, i32, i32, i32,
                                          _vp, _vp, C.c_size_t, _vp],
         }
@@ -121,6 +131,10 @@ def lib():
         L.kd_last_error.restype = C.c_char_p
         L.kd_attn_workspace_bytes.argtypes = [i32, i32, i32, i32]
         L.kd_attn_workspace_bytes.restype = C.c_size_t
+        L.kd_attn_window_workspace_bytes.argtypes = [i32] * 6
+        L.kd_attn_window_workspace_bytes.restype = C.c_size_t
+        L.kd_beam_workspace_bytes.argtypes = [i32] * 4
+        L.kd_beam_workspace_bytes.restype = C.c_size_t
         _lib = L
     return _lib
 
@@ -149,6 +163,11 @@ def _ptr(obj):
             raise ValueError("tensors passed to libkd must be contiguous")
         return obj.data_ptr()
     raise TypeError(f"cannot take the address of {type(obj)}")
+
+
+def _nbytes(buf) -> int:
+    """Bytes of a tensor or array."""
+    return buf.numel() * buf.element_size() if hasattr(buf, "numel") else buf.nbytes
 
 
 def _stream(stream):
@@ -228,6 +247,26 @@ def kd_session_load_kv(m, session_id: int, k, v, length: int, stream=None):
 def kd_session_length(m, session_id: int) -> int:
     out = C.c_int32()
     _check(lib().kd_session_length(m, int(session_id), C.byref(out)))
+    return out.value
+
+
+def kd_model_set_window(m, window: int, sinks: int = 0):
+    """Sliding-window attention for the model's steps (window 0: every key again)."""
+    _check(lib().kd_model_set_window(m, int(window), int(sinks)))
+
+
+def kd_session_reorder(m, session_ids, parents, stream=None):
+    """Session ids[i] becomes a copy of what session parents[i] was (-1: stays as it is), all at once."""
+    ids = _i32(session_ids)
+    par = _i32(parents, ids.size)
+    i32p = C.POINTER(C.c_int32)
+    _check(lib().kd_session_reorder(m, ids.ctypes.data_as(i32p), par.ctypes.data_as(i32p), ids.size, _stream(stream)))
+
+
+def kd_session_fork(m, session_id: int, stream=None) -> int:
+    """Bind a free slot as a copy of the session; returns its id."""
+    out = C.c_int32()
+    _check(lib().kd_session_fork(m, int(session_id), C.byref(out), _stream(stream)))
     return out.value
 
 
@@ -404,6 +443,71 @@ def kd_attn_append_decode_q8(q, k_new, v_new, k_quants, k_scales, v_quants, v_sc
                                           _ptr(v_quants), _ptr(v_scales), sl.ctypes.data_as(i32p),
                                           ps.ctypes.data_as(i32p), B, n_heads, n_kv_heads, n_slots, cap, _ptr(out),
                                           _ptr(workspace), nbytes, _stream(stream)))
+
+
+def kd_attn_window_workspace_bytes(B: int, n_heads: int, head_dim: int, cap: int, window: int, sinks: int) -> int:
+    return int(lib().kd_attn_window_workspace_bytes(B, n_heads, head_dim, cap, window, sinks))
+
+
+def kd_attn_window_append_decode(q, k_new, v_new, k_cache, v_cache, slots, positions, n_heads, n_kv_heads, head_dim,
+                                 n_slots, cap, window, sinks, out, workspace, stream=None):
+    """kd_attn_append_decode with a sliding window: row b attends t < sinks and t > positions[b] - window."""
+    sl = _i32(slots)
+    ps = _i32(positions, sl.size)
+    i32p = C.POINTER(C.c_int32)
+    _check(lib().kd_attn_window_append_decode(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+                                              sl.ctypes.data_as(i32p), ps.ctypes.data_as(i32p), sl.size, n_heads,
+                                              n_kv_heads, head_dim, n_slots, cap, window, sinks, _ptr(out),
+                                              _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def kd_attn_window_append_decode_q8(q, k_new, v_new, k_quants, k_scales, v_quants, v_scales, slots, positions, n_heads,
+                                    n_kv_heads, n_slots, cap, window, sinks, out, workspace, stream=None):
+    """kd_attn_window_append_decode over a Q8_0 cache of head_dim 128 (see include/kd.h)."""
+    sl = _i32(slots)
+    ps = _i32(positions, sl.size)
+    i32p = C.POINTER(C.c_int32)
+    _check(lib().kd_attn_window_append_decode_q8(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_quants), _ptr(k_scales),
+                                                 _ptr(v_quants), _ptr(v_scales), sl.ctypes.data_as(i32p),
+                                                 ps.ctypes.data_as(i32p), sl.size, n_heads, n_kv_heads, n_slots, cap,
+                                                 window, sinks, _ptr(out), _ptr(workspace), _nbytes(workspace),
+                                                 _stream(stream)))
+
+
+KD_BEAM_MAX_BEAMS = 16
+KD_BEAM_MAX_OUT = 32
+KD_BEAM_MAX_VOCAB = 524288
+KD_REORDER_MAX = 64
+
+
+def kd_beam_workspace_bytes(n_groups: int, n_beams: int, V: int, n_out: int) -> int:
+    return int(lib().kd_beam_workspace_bytes(n_groups, n_beams, V, n_out))
+
+
+def kd_beam_select(logits, n_groups: int, n_beams: int, V: int, scores, n_out: int, parents_out, tokens_out, scores_out,
+                   workspace, done=None, done_out=None, eos: int = -1, ld=None, stream=None):
+    """Each group's n_out best (beam, token) continuations (see include/kd.h).  logits: device fp32
+    [n_groups * n_beams] rows, `ld` (default V) apart; scores, done: device fp32 / int32 per row or None."""
+    _check(lib().kd_beam_select(_ptr(logits), V if ld is None else int(ld), n_groups, n_beams, V, _ptr(scores),
+                                _ptr(done), eos, n_out, _ptr(parents_out), _ptr(tokens_out), _ptr(scores_out),
+                                _ptr(done_out), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def kd_kv_reorder(planes, dst, src, lens, n_layers: int, n_slots: int, n_kv_heads: int, cap: int, window: int = 0,
+                  sinks: int = 0, stream=None):
+    """Slot dst[i] becomes what slot src[i] was, all at once and in place.  planes: device tensors
+    [n_layers][n_slots][n_kv_heads][cap][...], the trailing dimensions being a row's bytes."""
+    d = _i32(dst)
+    s, n = _i32(src, d.size), _i32(lens, d.size)
+    rows = n_layers * n_slots * n_kv_heads * cap
+    ptrs = (_vp * len(planes))(*[_ptr(p) for p in planes])
+    nbytes = [_nbytes(p) for p in planes]
+    if rows < 1 or any(b % rows for b in nbytes):
+        raise ValueError("a plane's size must be a whole number of bytes per row")
+    widths = (C.c_int32 * len(planes))(*[b // rows for b in nbytes])
+    i32p = C.POINTER(C.c_int32)
+    _check(lib().kd_kv_reorder(ptrs, widths, len(planes), n_layers, n_slots, n_kv_heads, cap, d.ctypes.data_as(i32p),
+                               s.ctypes.data_as(i32p), n.ctypes.data_as(i32p), d.size, window, sinks, _stream(stream)))
 
 
 def kd_attn_device_status(workspace=None, stream=None) -> int:

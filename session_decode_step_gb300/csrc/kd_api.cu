@@ -26,7 +26,10 @@
 #include <vector>
 
 #include "kd.h"
+#include "kd_host.h"
 #include "kd_kernels.h"
+#include "kd_reorder.h"
+#include "kd_window.h"
 
 using kd::PackedQ8;
 static_assert(KD_TIMELINE_CTAS == kd::TL_CTAS, "timeline record layout");
@@ -63,6 +66,7 @@ cudaError_t init_device_attributes(int dev) {
         if (e == cudaSuccess) e = kd::attn_init_attributes();
         if (e == cudaSuccess) e = kd::attn_q8_init_attributes();
         if (e == cudaSuccess) e = kd::rowops_init_attributes();
+        if (e == cudaSuccess) e = kd::beam_init_attributes();
         g_attr_err[dev] = e;
     });
     return g_attr_err[dev];
@@ -142,6 +146,15 @@ kd_status upload_packed(const std::vector<std::pair<const void*, int>>& parts, i
 }  // namespace
 
 void kd::set_last_error(const char* msg) { g_err = msg ? msg : ""; }
+kd_status kd::failf(kd_status st, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_err = buf;
+    return st;
+}
 cudaError_t kd::ensure_device_attributes(int dev) { return init_device_attributes(dev); }
 
 struct kd_model {
@@ -189,6 +202,11 @@ struct kd_model {
     cudaStream_t cap_stream = nullptr;
     std::vector<uint8_t> bound;
     std::vector<int32_t> len;
+    // Rows [lo, hi) of a session's cache that were not copied when it became a
+    // copy under a window (kd_session_reorder): no step may attend them.
+    struct Gap { int32_t lo = 0, hi = 0; };
+    std::vector<Gap> gap;
+    int window = 0, sinks = 0;  // kd_model_set_window (window 0: every key)
     std::map<std::tuple<int, float*, int*, unsigned long long*, bool>, cudaGraphExec_t> graphs;
     float* hidden_dbg = nullptr;
     int inject_cls = -1;      // debug fault hook: kernel class whose next launch's bounded wait runs out
@@ -380,6 +398,7 @@ static kd_status load_impl(kd_model* m, const kd_weights* w) {
     KD_CK(cudaStreamCreateWithFlags(&m->cap_stream, cudaStreamNonBlocking));
     m->bound.assign(S, 0);
     m->len.assign(S, 0);
+    m->gap.assign(S, {});
     KD_CK(cudaDeviceSynchronize());
     return KD_OK;
 }
@@ -526,17 +545,29 @@ static cudaError_t enqueue_step(kd_model* m, int B, float* lg, int* am, cudaStre
         t.max_splits = m->max_splits; t.out = m->attn; t.err = m->err;
         t.inject_tx = inject(KD_K_ATTN_SPLIT);
         t.tl = tl_next();
-        if (!m->kvq8) {
-            KD_RUN(KD_K_ATTN_SPLIT, kd::launch_attn_split(t, m->kmaps, m->attn_grid, pdl, s));
-        } else {  // quantised append of the new rows, then the attention over the Q8_0 cache
+        if (m->kvq8) {
             t.ks = m->ks;
             t.vs = m->vs;
+        }
+        const bool win = m->window > 0;
+        kd::AttnWinArgs tw{};  // the same for windowed rows, whose records are packed by their own item count
+        if (win) {
+            static_cast<kd::AttnArgs&>(tw) = t;
+            tw.window = m->window;
+            tw.sinks = m->sinks;
+            tw.max_splits = kd::win_max_items(c.max_ctx, m->window, m->sinks);
+        }
+        if (!m->kvq8) {
+            KD_RUN(KD_K_ATTN_SPLIT, win ? kd::launch_attn_split(tw, m->kmaps, m->attn_grid, pdl, s)
+                                        : kd::launch_attn_split(t, m->kmaps, m->attn_grid, pdl, s));
+        } else {  // quantised append of the new rows, then the attention over the Q8_0 cache
             KD_RUN(KD_K_ATTN_SPLIT, kd::launch_kvq8_append(m->knew, m->vnew, m->kq, m->ks, m->vq, m->vs, slot, pos, B,
                                                            nkv, c.max_ctx, t.row0, pdl, s));
-            KD_RUN(KD_K_ATTN_SPLIT, kd::launch_attn_split_q8(t, m->kmaps, m->num_sms, pdl, s));
+            KD_RUN(KD_K_ATTN_SPLIT, win ? kd::launch_attn_split_q8(tw, m->kmaps, m->num_sms, pdl, s)
+                                        : kd::launch_attn_split_q8(t, m->kmaps, m->num_sms, pdl, s));
         }
-        t.tl = tl_next();
-        KD_RUN(KD_K_ATTN_COMBINE, kd::launch_attn_combine(t, pdl, s));
+        t.tl = tw.tl = tl_next();
+        KD_RUN(KD_K_ATTN_COMBINE, win ? kd::launch_attn_combine(tw, pdl, s) : kd::launch_attn_combine(t, pdl, s));
         a = mm(m->wo[l], m->attn);
         resid(a);
         a.inject_tx = inject(KD_K_WO);
@@ -664,6 +695,7 @@ kd_status kd_session_bind(kd_model* m, int32_t* id_out) {
         if (!m->bound[i]) {
             m->bound[i] = 1;
             m->len[i] = 0;
+            m->gap[i] = {};
             *id_out = (int32_t)i;
             return KD_OK;
         }
@@ -725,6 +757,7 @@ kd_status kd_session_load_kv(kd_model* m, int32_t id, const void* k, const void*
         KD_CK(e2);
         KD_CK(cudaEventRecord(m->last_step, s));
         m->len[id] = len;
+        m->gap[id] = {};
         return KD_OK;
     }
     const size_t row = (size_t)c.head_dim * sizeof(__half);
@@ -738,6 +771,7 @@ kd_status kd_session_load_kv(kd_model* m, int32_t id, const void* k, const void*
     }
     KD_CK(cudaEventRecord(m->last_step, s));
     m->len[id] = len;
+    m->gap[id] = {};
     return KD_OK;
 }
 
@@ -756,6 +790,14 @@ static kd_status check_rows(kd_model* m, const char* fn, const int32_t* ids, con
         if (positions[b] < 0 || positions[b] > m->len[ids[b]] || positions[b] >= c.max_ctx)
             return fail(KD_ERR_POSITION, "position %d of session %d: length is %d, capacity %d", positions[b],
                         ids[b], m->len[ids[b]], c.max_ctx);
+        const kd_model::Gap g = m->gap[ids[b]];
+        if (g.lo < g.hi) {  // the rows before p that a step at p attends: [0, a) and [w, p)
+            const int32_t p = positions[b], w = m->window > 0 ? std::max(0, p + 1 - m->window) : 0;
+            const int32_t a = std::min(m->window > 0 ? m->sinks : 0, w);
+            if (g.lo < a || std::max(g.lo, w) < std::min(g.hi, p))
+                return fail(KD_ERR_POSITION, "position %d of session %d attends rows [%d, %d), which its copy left out",
+                            p, ids[b], g.lo, g.hi);
+        }
     }
     return KD_OK;
 }
@@ -820,7 +862,90 @@ static kd_status decode_impl(kd_model* m, const char* fn, const int32_t* ids, co
         }
         KD_CK(cudaEventRecord(m->last_step, s));
     }
-    for (int b = 0; b < B; ++b) m->len[ids[b]] = positions[b] + 1;
+    for (int b = 0; b < B; ++b) {
+        m->len[ids[b]] = positions[b] + 1;
+        m->gap[ids[b]].hi = std::min(m->gap[ids[b]].hi, positions[b]);  // a rewind forgets rows, gap and all
+    }
+    return KD_OK;
+}
+
+kd_status kd_model_set_window(kd_model* m, int32_t window, int32_t sinks) {
+    if (!m || window < 0 || sinks < 0)
+        return fail(KD_ERR_INVALID_ARG, "kd_model_set_window: null model, or window %d, sinks %d", window, sinks);
+    KD_CK(cudaSetDevice(m->dev));
+    KD_CK(cudaStreamSynchronize(m->cap_stream));
+    KD_CK(cudaEventSynchronize(m->last_step));
+    for (auto& g : m->graphs) cudaGraphExecDestroy(g.second);
+    m->graphs.clear();
+    m->window = window;
+    m->sinks = window > 0 ? sinks : 0;
+    return KD_OK;
+}
+
+kd_status kd_session_reorder(kd_model* m, const int32_t* ids, const int32_t* parents, int32_t n, kd_stream stream) {
+    if (!m || !ids || !parents) return fail(KD_ERR_INVALID_ARG, "kd_session_reorder: null argument");
+    if (n < 1 || n > KD_REORDER_MAX) return fail(KD_ERR_BATCH, "kd_session_reorder: n=%d outside [1, %d]", n, KD_REORDER_MAX);
+    int32_t src[KD_REORDER_MAX], len[KD_REORDER_MAX];
+    kd_model::Gap gap[KD_REORDER_MAX];
+    for (int i = 0; i < n; ++i) {
+        kd_status st = check_session(m, ids[i]);
+        if (st != KD_OK) return st;
+        src[i] = parents[i] == -1 ? ids[i] : parents[i];
+        if ((st = check_session(m, src[i])) != KD_OK) return st;
+        for (int j = 0; j < i; ++j)
+            if (ids[j] == ids[i]) return fail(KD_ERR_BAD_SESSION, "session %d appears twice in one reorder", ids[i]);
+        len[i] = m->len[src[i]];
+        gap[i] = m->gap[src[i]];
+        if (m->window > 0 && src[i] != ids[i]) {  // the rows no later step attends stay behind
+            const int32_t hi = std::max(0, len[i] + 1 - m->window), lo = std::min(m->sinks, hi);
+            if (lo < hi) gap[i] = gap[i].lo < gap[i].hi ? kd_model::Gap{std::min(lo, gap[i].lo), std::max(hi, gap[i].hi)}
+                                                       : kd_model::Gap{lo, hi};
+        }
+    }
+    const kd_config& c = m->cfg;
+    if ((int64_t)c.n_layers * c.n_kv_heads > 65535)
+        return fail(KD_ERR_UNSUPPORTED, "kd_session_reorder: n_layers * n_kv_heads exceeds 65535");
+    kd::ReorderPlan p{};
+    if (!m->kvq8) {
+        p.n_planes = 2;
+        p.plane[0] = {m->kc, c.head_dim * (int)sizeof(__half)};
+        p.plane[1] = {m->vc, c.head_dim * (int)sizeof(__half)};
+    } else {
+        p.n_planes = 4;
+        p.plane[0] = {m->kq, 128};
+        p.plane[1] = {m->ks, 8};
+        p.plane[2] = {m->vq, 128};
+        p.plane[3] = {m->vs, 8};
+    }
+    p.layers = c.n_layers;
+    p.slots = c.max_sessions;
+    p.heads = c.n_kv_heads;
+    p.cap = c.max_ctx;
+    p.window = m->window;
+    p.sinks = m->sinks;
+    KD_CK(cudaSetDevice(m->dev));
+    cudaStream_t s = (cudaStream_t)stream;
+    KD_CK(cudaStreamWaitEvent(s, m->last_step, 0));
+    KD_CK(kd::launch_kv_reorder(p, ids, src, len, n, s));
+    KD_CK(cudaEventRecord(m->last_step, s));
+    for (int i = 0; i < n; ++i) {
+        m->len[ids[i]] = len[i];
+        m->gap[ids[i]] = gap[i];
+    }
+    return KD_OK;
+}
+
+kd_status kd_session_fork(kd_model* m, int32_t id, int32_t* new_id_out, kd_stream stream) {
+    if (!m || !new_id_out) return fail(KD_ERR_INVALID_ARG, "kd_session_fork: null argument");
+    kd_status st = check_session(m, id);
+    if (st != KD_OK) return st;
+    int32_t to = -1;
+    if ((st = kd_session_bind(m, &to)) != KD_OK) return st;
+    if ((st = kd_session_reorder(m, &to, &id, 1, stream)) != KD_OK) {
+        m->bound[to] = 0;
+        return st;
+    }
+    *new_id_out = to;
     return KD_OK;
 }
 

@@ -61,9 +61,12 @@ struct AttnSmem {
 // rounded to fp16 and the remainder of that rounding, whose two products add
 // up to the fp32-accurate one.  K tiles are the A operand as stored, V tiles
 // through the transposing ldmatrix.
-template <int HD, int GQ>
+// WIN: windowed rows (AttnWinTable): the items' first keys and hidden keys come
+// from the session's window; hidden keys get no weight and their values count
+// as zero (they may hold anything, NaN included).
+template <int HD, int GQ, bool WIN>
 __global__ void __launch_bounds__(AT_WARPS * 32, 1)
-    attn_split_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tmk,
+    attn_split_kernel(const __grid_constant__ AttnArgsOf<WIN> a, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmk8, const __grid_constant__ CUtensorMap tmv,
                       const __grid_constant__ CUtensorMap tmv8) {
     using L = AttnSmem<HD>;
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
     }
     __syncthreads();
 
-    AttnTable tab;
+    AttnTableOf<WIN> tab;
     tab.build(a, lane);
     const int n_items = tab.n_items;
     const int nk = (int)blockIdx.x < n_items ? (n_items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
     auto issue = [&](const AttnItem& it, int k, int parts) {
         const int st = k % S;
         uint8_t* stg = smem + st * L::STAGE;
-        const int row = (int)(a.row0 + ((long)it.slot * a.nkv + it.kvh) * a.cap + (long)it.s * AT_C);
+        const int row = (int)(a.row0 + ((long)it.slot * a.nkv + it.kvh) * a.cap + item_start<WIN>(it));
         const bool full = it.n == AT_C;
         const int krows = full ? AT_C : (it.n + 7) / 8 * 8;
 #pragma unroll
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
                 for (int e = 0; e < 2; ++e) {
                     const float sc = __fadd_rn(sacc[m][j][2 * e], sacc[m][j][2 * e + 1]);  // both parts
                     const int key = 16 * m + g + 8 * e;
-                    sv[j][m][e] = key < n ? __fmul_rn(sc, a.scale) : -INFINITY;
+                    sv[j][m][e] = item_sees<WIN>(it, key) ? __fmul_rn(sc, a.scale) : -INFINITY;
                     mx[j] = fmaxf(mx[j], sv[j][m][e]);
                 }
 #pragma unroll
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int key = 16 * m + g + 8 * e;
-                    sv[j][m][e] = key < n ? expf(__fsub_rn(sv[j][m][e], mx[j])) : 0.0f;
+                    sv[j][m][e] = item_sees<WIN>(it, key) ? expf(__fsub_rn(sv[j][m][e], mx[j])) : 0.0f;
                     lsum[j] = __fadd_rn(lsum[j], sv[j][m][e]);
                 }
 #pragma unroll
@@ -289,6 +292,14 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
             const int z = ((n + 15) & ~15) - n;
             for (int e = lane; e < z * L::NREG * 8; e += 32) {
                 const int r = n + e / (L::NREG * 8), rem = e % (L::NREG * 8);
+                *reinterpret_cast<uint4*>(stg + L::K_BYTES + (rem >> 3) * L::HALF_BYTES + r * 128 + (rem & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            __syncwarp();
+        }
+        if (WIN && it.h0 < it.h1) {  // hidden rows of the V tile: p = 0 too
+            for (int e = lane; e < (it.h1 - it.h0) * L::NREG * 8; e += 32) {
+                const int r = it.h0 + e / (L::NREG * 8), rem = e % (L::NREG * 8);
                 *reinterpret_cast<uint4*>(stg + L::K_BYTES + (rem >> 3) * L::HALF_BYTES + r * 128 + (rem & 7) * 16) =
                     make_uint4(0u, 0u, 0u, 0u);
             }
@@ -385,8 +396,8 @@ constexpr int COMB_UNROLL = 8;
 // warps of the merge: 4 up to 64 splits (4096 positions) of capacity, 32 beyond
 __host__ __device__ constexpr int comb_warps(int max_splits) { return max_splits <= 64 ? 4 : 32; }
 
-template <int HD, int NW>
-__global__ void __launch_bounds__(NW * 32) attn_combine_kernel(const AttnArgs a) {
+template <int HD, int NW, bool WIN>
+__global__ void __launch_bounds__(NW * 32) attn_combine_kernel(const __grid_constant__ AttnArgsOf<WIN> a) {
     constexpr int DPL = HD / 32;  // dims per lane
     constexpr int NT = NW * 32;
     static_assert(DPL == 2 || DPL == 4, "head_dim 64 or 128");
@@ -399,7 +410,12 @@ __global__ void __launch_bounds__(NW * 32) attn_combine_kernel(const AttnArgs a)
     const int b = blockIdx.y, h = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     // The step's positions were staged before its first kernel: read while the
     // split kernel finishes.
-    const int pos_b = b < a.B ? a.pos[b] : 0;
+    int pos_b = 0;
+    if constexpr (WIN) {
+        if (b < a.B) pos_b = a.slot ? a.pos[b] : a.vpos[b];
+    } else {
+        pos_b = b < a.B ? a.pos[b] : 0;
+    }
     pdl_wait();
     tl_waited(a.tl);
     if (b >= a.B) {
@@ -409,7 +425,8 @@ __global__ void __launch_bounds__(NW * 32) attn_combine_kernel(const AttnArgs a)
     const float* p = a.part + ((size_t)b * a.nh + h) * a.max_splits * ATT_REC(HD);
     // Only the session's own split records are read: records past its split count
     // may be cold (never written).
-    const int ns = (pos_b + ATT_CHUNK) / ATT_CHUNK;
+    int ns = (pos_b + ATT_CHUNK) / ATT_CHUNK;
+    if constexpr (WIN) ns = win_plan(pos_b, a.window, a.sinks).ns;
     // the warp's range of splits, and its first records
     const int s0 = (int)(((long)ns * warp) / NW), s1 = (int)(((long)ns * (warp + 1)) / NW);
     const float* pl = p + lane * DPL;
@@ -502,20 +519,27 @@ bool attn_supported(int hd, int group) {
 
 cudaError_t attn_init_attributes() {
     cudaError_t e = cudaSuccess;
-#define KD_SET(HD_, GQ_)                                                                             \
-    e = cudaFuncSetAttribute(attn_split_kernel<HD_, GQ_>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
-                             AttnSmem<HD_>::TOTAL);                                                  \
-    if (e != cudaSuccess) return e;                                                                  \
-    e = cudaFuncSetAttribute(attn_split_kernel<HD_, GQ_>, cudaFuncAttributePreferredSharedMemoryCarveout, \
-                             cudaSharedmemCarveoutMaxShared);                                        \
+#define KD_SET_ONE(f)                                                                           \
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);             \
+    if (e != cudaSuccess) return e;                                                             \
+    e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,                 \
+                             cudaSharedmemCarveoutMaxShared);                                   \
     if (e != cudaSuccess) return e;
+#define KD_SET(HD_, GQ_)                             \
+    smem = AttnSmem<HD_>::TOTAL;                     \
+    KD_SET_ONE((attn_split_kernel<HD_, GQ_, false>)) \
+    KD_SET_ONE((attn_split_kernel<HD_, GQ_, true>))
+    int smem = 0;
     for (int group : {1, 2, 4, 8}) {
         KD_ATT_DISPATCH(64, KD_SET)
         KD_ATT_DISPATCH(128, KD_SET)
     }
 #undef KD_SET
-    for (const void* f : {(const void*)attn_combine_kernel<64, 4>, (const void*)attn_combine_kernel<128, 4>,
-                          (const void*)attn_combine_kernel<64, 32>, (const void*)attn_combine_kernel<128, 32>,
+#undef KD_SET_ONE
+    for (const void* f : {(const void*)attn_combine_kernel<64, 4, false>, (const void*)attn_combine_kernel<64, 4, true>,
+                          (const void*)attn_combine_kernel<128, 4, false>, (const void*)attn_combine_kernel<128, 4, true>,
+                          (const void*)attn_combine_kernel<64, 32, false>, (const void*)attn_combine_kernel<64, 32, true>,
+                          (const void*)attn_combine_kernel<128, 32, false>, (const void*)attn_combine_kernel<128, 32, true>,
                           (const void*)kv_append_kernel})
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                       cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
@@ -528,7 +552,7 @@ int attn_split_grid(int num_sms, int hd, int group) {
     int per_sm = 1;
     cudaError_t e = cudaSuccess;
 #define KD_OCC(HD_, GQ_)                                                                     \
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_split_kernel<HD_, GQ_>, \
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_split_kernel<HD_, GQ_, false>, \
                                                       AT_WARPS * 32, AttnSmem<HD_>::TOTAL);
     auto run = [&]() -> cudaError_t {
         if (hd == 64) { KD_ATT_DISPATCH(64, KD_OCC) } else { KD_ATT_DISPATCH(128, KD_OCC) }
@@ -583,7 +607,8 @@ static cudaError_t launch_cfg(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr
     return cudaSuccess;
 }
 
-cudaError_t launch_attn_split(const AttnArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s) {
+template <bool WIN>
+static cudaError_t launch_split(const AttnArgsOf<WIN>& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s) {
     const int group = a.nh / a.nkv;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -593,13 +618,20 @@ cudaError_t launch_attn_split(const AttnArgs& a, const AttnMaps& maps, int grid,
 #define KD_LAUNCH(HD_, GQ_)                                 \
     cfg.blockDim = dim3(AT_WARPS * 32);                     \
     cfg.dynamicSmemBytes = AttnSmem<HD_>::TOTAL;            \
-    return cudaLaunchKernelEx(&cfg, attn_split_kernel<HD_, GQ_>, a, maps.k, maps.k8, maps.v, maps.v8);
+    return cudaLaunchKernelEx(&cfg, attn_split_kernel<HD_, GQ_, WIN>, a, maps.k, maps.k8, maps.v, maps.v8);
     if (a.hd == 64) { KD_ATT_DISPATCH(64, KD_LAUNCH) } else if (a.hd == 128) { KD_ATT_DISPATCH(128, KD_LAUNCH) }
 #undef KD_LAUNCH
     return cudaErrorInvalidValue;
 }
+cudaError_t launch_attn_split(const AttnArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s) {
+    return launch_split<false>(a, maps, grid, pdl, s);
+}
+cudaError_t launch_attn_split(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s) {
+    return launch_split<true>(a, maps, grid, pdl, s);
+}
 
-cudaError_t launch_attn_combine(const AttnArgs& a, bool pdl, cudaStream_t s) {
+template <bool WIN>
+static cudaError_t launch_combine(const AttnArgsOf<WIN>& a, bool pdl, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     launch_cfg(cfg, attr, pdl);
@@ -608,13 +640,15 @@ cudaError_t launch_attn_combine(const AttnArgs& a, bool pdl, cudaStream_t s) {
     cfg.blockDim = dim3(nw * 32);
     cfg.stream = s;
     if (a.hd == 64)
-        return nw == 4 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 4>, a)
-                       : cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 32>, a);
+        return nw == 4 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 4, WIN>, a)
+                       : cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 32, WIN>, a);
     if (a.hd == 128)
-        return nw == 4 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 4>, a)
-                       : cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 32>, a);
+        return nw == 4 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 4, WIN>, a)
+                       : cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 32, WIN>, a);
     return cudaErrorInvalidValue;
 }
+cudaError_t launch_attn_combine(const AttnArgs& a, bool pdl, cudaStream_t s) { return launch_combine<false>(a, pdl, s); }
+cudaError_t launch_attn_combine(const AttnWinArgs& a, bool pdl, cudaStream_t s) { return launch_combine<true>(a, pdl, s); }
 
 cudaError_t launch_kv_append(const float* k, const float* v, __half* kc, __half* vc, const int* slot,
                              const int* pos, int B, int nkv, int hd, int cap, cudaStream_t s) {

@@ -6,8 +6,11 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "kd_device.cuh"
 #include "kd_kernels.h"
+#include "kd_window.h"
 
 namespace kd {
 
@@ -19,7 +22,17 @@ static_assert(AT_C % 16 == 0 && AT_C <= 64, "a work item is whole 16-key tiles, 
 // Work items are ordered session-major, then split, then KV head.
 struct AttnItem {
     int b, s, kvh, n, ns, slot;  // session, split, KV head, keys in this split, splits of the session, its slot
+    int start, h0, h1;           // windowed rows: the split's first key, and its hidden keys [h0, h1)
 };
+// The first key of an item, and whether its key is hidden (never without a window).
+template <bool WIN>
+__device__ __forceinline__ int item_start(const AttnItem& it) {
+    return WIN ? it.start : it.s * AT_C;
+}
+template <bool WIN>
+__device__ __forceinline__ bool item_sees(const AttnItem& it, int key) {
+    return key < it.n && !(WIN && key >= it.h0 && key < it.h1);
+}
 
 // The session table of a launch, held one session per lane (B <= 32): the
 // session's slot, position, split count and first item.  Built once per warp
@@ -55,6 +68,57 @@ struct AttnTable {
         return it;
     }
 };
+
+// The same for windowed rows (win_plan): a session's items cover its leading keys,
+// then its window.
+struct AttnWinTable {
+    int slot, pos, base, n_items;
+    __device__ __forceinline__ void build(const AttnWinArgs& a, int lane) {
+        slot = 0;
+        pos = 0;
+        if (lane < a.B) {
+            slot = a.slot ? a.slot[lane] : a.vslot[lane];
+            pos = a.slot ? a.pos[lane] : a.vpos[lane];
+        }
+        const int n = lane < a.B ? win_plan(pos, a.window, a.sinks).ns * a.nkv : 0;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(FULL_MASK, incl, o);
+            if (lane >= o) incl += v;
+        }
+        base = incl - n;
+        n_items = __shfl_sync(FULL_MASK, incl, 31);
+    }
+    __device__ __forceinline__ AttnItem item(const AttnWinArgs& a, int lane, int x) const {
+        const unsigned m = __ballot_sync(FULL_MASK, lane < a.B && base <= x);
+        const int b = 31 - __clz(m);
+        AttnItem it;
+        it.b = b;
+        const int r = x - __shfl_sync(FULL_MASK, base, b);
+        it.s = r / a.nkv;
+        it.kvh = r - it.s * a.nkv;
+        it.slot = __shfl_sync(FULL_MASK, slot, b);
+        const int p = __shfl_sync(FULL_MASK, pos, b);
+        const WinPlan w = win_plan(p, a.window, a.sinks);
+        it.ns = w.ns;
+        if (it.s < w.nsA) {
+            it.start = it.s * ATT_CHUNK;
+            it.n = min(ATT_CHUNK, a.sinks - it.start);
+            it.h0 = it.h1 = 0;
+        } else {
+            it.start = w.startB + (it.s - w.nsA) * ATT_CHUNK;
+            it.n = min(ATT_CHUNK, p + 1 - it.start);
+            it.h0 = max(0, a.sinks - it.start);
+            it.h1 = min(it.n, w.lo - it.start);
+        }
+        return it;
+    }
+};
+template <bool WIN>
+using AttnTableOf = typename std::conditional<WIN, AttnWinTable, AttnTable>::type;
+template <bool WIN>
+using AttnArgsOf = typename std::conditional<WIN, AttnWinArgs, AttnArgs>::type;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"

@@ -91,9 +91,11 @@ __device__ __forceinline__ uint32_t u8x2_odd_to_half2(uint32_t v) {
     return r;
 }
 
-template <int GQ>
+// WIN: windowed rows, as in the fp16 kernel; a hidden key's value scales count as
+// zero (its quants are finite whatever they hold).
+template <int GQ, bool WIN>
 __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
-    attn_split_q8_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tmk,
+    attn_split_q8_kernel(const __grid_constant__ AttnArgsOf<WIN> a, const __grid_constant__ CUtensorMap tmk,
                          const __grid_constant__ CUtensorMap tmk8, const __grid_constant__ CUtensorMap tmv,
                          const __grid_constant__ CUtensorMap tmv8) {
     using L = AttnQ8Smem;
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
     }
     __syncthreads();
 
-    AttnTable tab;
+    AttnTableOf<WIN> tab;
     tab.build(a, lane);
     const int n_items = tab.n_items;
     const int nk = (int)blockIdx.x < n_items ? (n_items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
     // tail); scales by one bulk copy (8 bytes a row, rounded up to 16).
     const uint64_t kv_policy = l2_policy_evict_first();
     auto issue = [&](const AttnItem& it, int k, int parts) {
-        const long row = a.row0 + ((long)it.slot * a.nkv + it.kvh) * a.cap + (long)it.s * AT_C;
+        const long row = a.row0 + ((long)it.slot * a.nkv + it.kvh) * a.cap + item_start<WIN>(it);
         const bool full = it.n == AT_C;
         const int qrows = full ? AT_C : (it.n + 7) / 8 * 8;
         const uint32_t sbytes = (uint32_t)((it.n * L::SROW + 15) / 16 * 16);
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
                 for (int e = 0; e < 2; ++e) {
                     const float sc = __fadd_rn(sacc[m][j][2 * e], sacc[m][j][2 * e + 1]);  // both parts
                     const int key = 16 * m + g + 8 * e;
-                    sv[j][m][e] = key < n ? __fmul_rn(sc, a.scale) : -INFINITY;
+                    sv[j][m][e] = item_sees<WIN>(it, key) ? __fmul_rn(sc, a.scale) : -INFINITY;
                     mx[j] = fmaxf(mx[j], sv[j][m][e]);
                 }
 #pragma unroll
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int key = 16 * m + g + 8 * e;
-                    sv[j][m][e] = key < n ? expf(__fsub_rn(sv[j][m][e], mx[j])) : 0.0f;
+                    sv[j][m][e] = item_sees<WIN>(it, key) ? expf(__fsub_rn(sv[j][m][e], mx[j])) : 0.0f;
                     lsum[j] = __fadd_rn(lsum[j], sv[j][m][e]);
                 }
 #pragma unroll
@@ -344,11 +346,11 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
         {
             const uint4 w = lds_v4(vscale + 2 * lane * L::SROW);  // rows 2 lane, 2 lane + 1
             float dm = 0.0f;
-            if (2 * lane < n) {
+            if (item_sees<WIN>(it, 2 * lane)) {
                 const float2 x = h2bits_to_float2(w.x), y = h2bits_to_float2(w.y);
                 dm = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
             }
-            if (2 * lane + 1 < n) {
+            if (item_sees<WIN>(it, 2 * lane + 1)) {
                 const float2 x = h2bits_to_float2(w.z), y = h2bits_to_float2(w.w);
                 dm = fmaxf(dm, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
             }
@@ -380,14 +382,14 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
                 const int kb = 16 * js + 2 * c;
                 const uint4 wa = lds_v4(vscale + kb * L::SROW), wb = lds_v4(vscale + (kb + 8) * L::SROW);
                 float2 dk[4][2];  // [key r][blocks 0,1 | 2,3]; 0 past the item's keys
-                dk[0][0] = h2bits_to_float2(kb < n ? wa.x : 0u);
-                dk[0][1] = h2bits_to_float2(kb < n ? wa.y : 0u);
-                dk[1][0] = h2bits_to_float2(kb + 1 < n ? wa.z : 0u);
-                dk[1][1] = h2bits_to_float2(kb + 1 < n ? wa.w : 0u);
-                dk[2][0] = h2bits_to_float2(kb + 8 < n ? wb.x : 0u);
-                dk[2][1] = h2bits_to_float2(kb + 8 < n ? wb.y : 0u);
-                dk[3][0] = h2bits_to_float2(kb + 9 < n ? wb.z : 0u);
-                dk[3][1] = h2bits_to_float2(kb + 9 < n ? wb.w : 0u);
+                dk[0][0] = h2bits_to_float2(item_sees<WIN>(it, kb) ? wa.x : 0u);
+                dk[0][1] = h2bits_to_float2(item_sees<WIN>(it, kb) ? wa.y : 0u);
+                dk[1][0] = h2bits_to_float2(item_sees<WIN>(it, kb + 1) ? wa.z : 0u);
+                dk[1][1] = h2bits_to_float2(item_sees<WIN>(it, kb + 1) ? wa.w : 0u);
+                dk[2][0] = h2bits_to_float2(item_sees<WIN>(it, kb + 8) ? wb.x : 0u);
+                dk[2][1] = h2bits_to_float2(item_sees<WIN>(it, kb + 8) ? wb.y : 0u);
+                dk[3][0] = h2bits_to_float2(item_sees<WIN>(it, kb + 9) ? wb.z : 0u);
+                dk[3][1] = h2bits_to_float2(item_sees<WIN>(it, kb + 9) ? wb.w : 0u);
                 uint32_t pb[4][NQ][2];
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
@@ -489,6 +491,44 @@ __global__ void __launch_bounds__(256) kvq8_append_kernel(const float* __restric
     *q = q8_quant_lane(x, lane, (part ? vs : ks) + row * 4 + blk);
 }
 
+// The same for a windowed op-level call: slots and positions come with the launch,
+// and the call's fault word is cleared.
+__global__ void __launch_bounds__(256) win_append_q8_kernel(const __grid_constant__ AttnWinArgs a,
+                                                            const float* __restrict__ knew,
+                                                            const float* __restrict__ vnew, uint8_t* kq, __half* ks,
+                                                            uint8_t* vq, __half* vs) {
+    pdl_launch_dependents();
+    const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (h == 0 && b == 0 && threadIdx.x == 0) *a.err = 0;
+    const int blk = warp & 3, part = warp >> 2;
+    const long row = ((long)a.vslot[b] * a.nkv + h) * a.cap + a.vpos[b];
+    const float x = (part ? vnew : knew)[((size_t)b * a.nkv + h) * 128 + 32 * blk + lane];
+    uint8_t* q = (part ? vq : kq) + row * 128 + 32 * blk + lane;
+    *q = q8_quant_lane(x, lane, (part ? vs : ks) + row * 4 + blk);
+}
+
+// And into fp16 rows of hd = 64 or 128: thread i of block (h, b) converts value i of K, then of V.
+__global__ void __launch_bounds__(256) win_append_fp16_kernel(const __grid_constant__ AttnWinArgs a,
+                                                              const float* __restrict__ k,
+                                                              const float* __restrict__ v, __half* kc, __half* vc) {
+    pdl_launch_dependents();
+    const int h = blockIdx.x, b = blockIdx.y, i = threadIdx.x % a.hd, part = threadIdx.x / a.hd;
+    if (h == 0 && b == 0 && threadIdx.x == 0) *a.err = 0;
+    const size_t dst = (((size_t)a.vslot[b] * a.nkv + h) * a.cap + a.vpos[b]) * a.hd + i;
+    const size_t src = ((size_t)b * a.nkv + h) * a.hd + i;
+    (part ? vc : kc)[dst] = __float2half_rn((part ? v : k)[src]);
+}
+
+cudaError_t launch_win_append(const AttnWinArgs& a, const float* k, const float* v, void* kc, void* vc, __half* ks,
+                              __half* vs, cudaStream_t s) {
+    const dim3 grid(a.nkv, a.B);
+    if (ks)
+        win_append_q8_kernel<<<grid, 256, 0, s>>>(a, k, v, (uint8_t*)kc, ks, (uint8_t*)vc, vs);
+    else
+        win_append_fp16_kernel<<<grid, 2 * a.hd, 0, s>>>(a, k, v, (__half*)kc, (__half*)vc);
+    return cudaGetLastError();
+}
+
 // Rows of fp32 or fp16 values [n_rows][128] into Q8_0 rows: source row r (layer
 // l = r / (nkv * len), head h, position t) goes to arena row
 // l * layer_rows + base + h * cap + t.  A warp per 32-value block.
@@ -579,8 +619,10 @@ bool attn_q8_supported(int hd, int group) {
 
 cudaError_t attn_q8_init_attributes() {
     cudaError_t e = cudaSuccess;
-    for (const void* f : {(const void*)attn_split_q8_kernel<1>, (const void*)attn_split_q8_kernel<2>,
-                          (const void*)attn_split_q8_kernel<4>, (const void*)attn_split_q8_kernel<8>}) {
+    for (const void* f : {(const void*)attn_split_q8_kernel<1, false>, (const void*)attn_split_q8_kernel<1, true>,
+                          (const void*)attn_split_q8_kernel<2, false>, (const void*)attn_split_q8_kernel<2, true>,
+                          (const void*)attn_split_q8_kernel<4, false>, (const void*)attn_split_q8_kernel<4, true>,
+                          (const void*)attn_split_q8_kernel<8, false>, (const void*)attn_split_q8_kernel<8, true>}) {
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnQ8Smem::TOTAL)) != cudaSuccess)
             return e;
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -588,14 +630,16 @@ cudaError_t attn_q8_init_attributes() {
             return e;
     }
     for (const void* f : {(const void*)kvq8_append_kernel, (const void*)kvq8_rows_kernel<__half>,
-                          (const void*)kvq8_rows_kernel<float>})
+                          (const void*)kvq8_rows_kernel<float>, (const void*)win_append_q8_kernel,
+                          (const void*)win_append_fp16_kernel})
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                       cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
             return e;
     return cudaSuccess;
 }
 
-cudaError_t launch_attn_split_q8(const AttnArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s) {
+template <bool WIN>
+static cudaError_t launch_split_q8(const AttnArgsOf<WIN>& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -607,12 +651,18 @@ cudaError_t launch_attn_split_q8(const AttnArgs& a, const AttnMaps& maps, int gr
     cfg.dynamicSmemBytes = AttnQ8Smem::TOTAL;
     cfg.stream = s;
     switch (a.nh / a.nkv) {
-        case 1: return cudaLaunchKernelEx(&cfg, attn_split_q8_kernel<1>, a, maps.k, maps.k8, maps.v, maps.v8);
-        case 2: return cudaLaunchKernelEx(&cfg, attn_split_q8_kernel<2>, a, maps.k, maps.k8, maps.v, maps.v8);
-        case 4: return cudaLaunchKernelEx(&cfg, attn_split_q8_kernel<4>, a, maps.k, maps.k8, maps.v, maps.v8);
-        case 8: return cudaLaunchKernelEx(&cfg, attn_split_q8_kernel<8>, a, maps.k, maps.k8, maps.v, maps.v8);
+        case 1: return cudaLaunchKernelEx(&cfg, attn_split_q8_kernel<1, WIN>, a, maps.k, maps.k8, maps.v, maps.v8);
+        case 2: return cudaLaunchKernelEx(&cfg, attn_split_q8_kernel<2, WIN>, a, maps.k, maps.k8, maps.v, maps.v8);
+        case 4: return cudaLaunchKernelEx(&cfg, attn_split_q8_kernel<4, WIN>, a, maps.k, maps.k8, maps.v, maps.v8);
+        case 8: return cudaLaunchKernelEx(&cfg, attn_split_q8_kernel<8, WIN>, a, maps.k, maps.k8, maps.v, maps.v8);
         default: return cudaErrorInvalidValue;
     }
+}
+cudaError_t launch_attn_split_q8(const AttnArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s) {
+    return launch_split_q8<false>(a, maps, grid, pdl, s);
+}
+cudaError_t launch_attn_split_q8(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s) {
+    return launch_split_q8<true>(a, maps, grid, pdl, s);
 }
 
 }  // namespace kd

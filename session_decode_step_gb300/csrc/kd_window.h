@@ -1,0 +1,64 @@
+// kd_window.h -- windowed attention (library internal): a row at position p sees
+// the keys t <= p with t < sinks (the first tokens, which stay visible) or
+// t > p - window.  The work-item plan, shared by the host and the kernels, and
+// the launch interface.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "kd_kernels.h"
+
+namespace kd {
+
+// The work items of a windowed row at position pos.  Its visible keys are the
+// leading [0, min(sinks, lo)) and the window [lo, pos], lo = max(0, pos + 1 -
+// window).  Items are ATT_CHUNK keys each: nsA over the leading keys, then the
+// window's from startB = lo rounded down to 8 keys (the tails' 8-row boxes and
+// the Q8_0 scales' 16-byte copies stay aligned; at most 7 hidden keys are read).
+// Where that would be more items than the whole row has (or the leading keys
+// reach the window) the items cover [0, pos] and hidden keys are masked: fewer
+// than ATT_CHUNK, so no item is hidden as a whole.  A row never has more items
+// than without a window, and they depend on its own position only.
+struct WinPlan {
+    int lo, nsA, startB, ns;
+};
+__host__ __device__ inline WinPlan win_plan(int pos, int window, int sinks) {
+    WinPlan w;
+    w.lo = pos + 1 > window ? pos + 1 - window : 0;
+    const int lo8 = w.lo & ~7, all = pos / ATT_CHUNK + 1;
+    w.nsA = 0;
+    w.startB = 0;
+    w.ns = all;
+    if (lo8 > sinks) {
+        const int a = (sinks + ATT_CHUNK - 1) / ATT_CHUNK, b = (pos + 1 - lo8 + ATT_CHUNK - 1) / ATT_CHUNK;
+        if (a + b <= all) {
+            w.nsA = a;
+            w.startB = lo8;
+            w.ns = a + b;
+        }
+    }
+    return w;
+}
+// The most items a row of a slot of cap positions can have.
+__host__ __device__ inline int win_max_items(int cap, int window, int sinks) {
+    const int a = sinks < cap ? sinks : cap, b = window < cap ? window : cap;
+    const int all = (cap + ATT_CHUNK - 1) / ATT_CHUNK;
+    const int part = (a + ATT_CHUNK - 1) / ATT_CHUNK + (b + 7 + ATT_CHUNK - 1) / ATT_CHUNK;
+    return part < all ? part : all;
+}
+
+// slot == nullptr: the rows' slots and positions are in vslot and vpos, passed
+// with the launch (nothing has to be staged in device memory first).
+struct AttnWinArgs : AttnArgs {
+    int window, sinks;  // window >= 1, sinks >= 0
+    int vslot[16], vpos[16];
+};
+cudaError_t launch_attn_split(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s);
+cudaError_t launch_attn_split_q8(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s);
+cudaError_t launch_attn_combine(const AttnWinArgs& a, bool pdl, cudaStream_t s);
+// Append the new rows of a windowed call (slots and positions in a.vslot, a.vpos)
+// and clear its fault word a.err, in one launch: fp16 rows into kc, vc, or, with
+// ks and vs, Q8_0 rows (quants kc, vc; block scales ks, vs).
+cudaError_t launch_win_append(const AttnWinArgs& a, const float* k, const float* v, void* kc, void* vc, __half* ks,
+                              __half* vs, cudaStream_t s);
+
+}  // namespace kd
