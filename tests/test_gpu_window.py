@@ -75,15 +75,15 @@ class Case:
                 both = np.concatenate([x, new[b][:, None]], 1)
                 if not q8:
                     val = both.astype(np.float16)
-                    self.dev[i][slot, :, dt] = torch.from_numpy(val[:, :-1]).cuda()
+                    self.dev[i][slot][:, dt] = torch.from_numpy(val[:, :-1]).cuda()
                     self.rows[b, i] = val.astype(np.float64)
                 else:
                     blk = oracle.q8_0_quantize_f32(both).reshape(nkv, len(t) + 1, 4, 34)
                     quant = np.ascontiguousarray(blk[..., 2:]).view(np.int8)
                     scale = np.ascontiguousarray(blk[..., :2]).view(np.float16)
                     u = (quant.astype(np.int16) + 128).astype(np.uint8).reshape(nkv, -1, 128)[:, :-1]
-                    self.dev[2 * i][slot, :, dt] = torch.from_numpy(np.ascontiguousarray(u)).cuda()
-                    self.dev[2 * i + 1][slot, :, dt] = torch.from_numpy(scale.reshape(nkv, -1, 4)[:, :-1].copy()).cuda()
+                    self.dev[2 * i][slot][:, dt] = torch.from_numpy(np.ascontiguousarray(u)).cuda()
+                    self.dev[2 * i + 1][slot][:, dt] = torch.from_numpy(scale.reshape(nkv, -1, 4)[:, :-1].copy()).cuda()
                     self.rows[b, i] = (quant.astype(np.float64) * scale.astype(np.float64)).reshape(nkv, -1, 128)
         self.dq, self.dk, self.dv = (torch.from_numpy(x).cuda() for x in (self.q, self.kn, self.vn))
 
