@@ -9,6 +9,7 @@ only to hand over device memory and streams.
 from __future__ import annotations
 
 import ctypes as C
+import sys
 from pathlib import Path
 
 import numpy as np
@@ -152,36 +153,44 @@ def _ptr(obj):
     """Address of a numpy array, a torch tensor, an int, or None."""
     if obj is None:
         return None
+    data_ptr = getattr(obj, "data_ptr", None)
+    if data_ptr is not None:
+        if not obj.is_contiguous():
+            raise ValueError("tensors passed to libkd must be contiguous")
+        return data_ptr()
     if isinstance(obj, int):
         return obj
     if isinstance(obj, np.ndarray):
         if not obj.flags["C_CONTIGUOUS"]:
             raise ValueError("arrays passed to libkd must be C-contiguous")
         return obj.ctypes.data
-    if hasattr(obj, "data_ptr"):
-        if not obj.is_contiguous():
-            raise ValueError("tensors passed to libkd must be contiguous")
-        return obj.data_ptr()
     raise TypeError(f"cannot take the address of {type(obj)}")
 
 
 def _nbytes(buf) -> int:
     """Bytes of a tensor or array."""
-    return buf.numel() * buf.element_size() if hasattr(buf, "numel") else buf.nbytes
+    return buf.nbytes
 
 
 def _stream(stream):
+    """The cudaStream_t of `stream`; None: the current stream of torch's current device (the default
+    stream if torch, or its CUDA side, is not in use)."""
     if stream is None:
-        try:
-            import torch
-            if torch.cuda.is_available():
-                return torch.cuda.current_stream().cuda_stream
-        except ImportError:
-            pass
-        return None
+        torch = sys.modules.get("torch")
+        if torch is None or not torch.cuda.is_initialized():
+            return None
+        return _current_raw_stream(torch)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_raw_stream(torch):
+    # torch.cuda.current_stream() builds a Stream object (about 3 us); the raw handle is enough.
+    try:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
 
 
 def _i32(a, n=None):
@@ -189,6 +198,23 @@ def _i32(a, n=None):
     if n is not None and arr.size != n:
         raise ValueError(f"expected {n} entries, got {arr.size}")
     return arr
+
+
+_ARRAYS: dict = {}
+
+
+def _c32(a, n=None):
+    """A ctypes int32 array of a host sequence or array (passed to an int32 pointer argument as it is)."""
+    if isinstance(a, np.ndarray) and a.dtype == np.int32:
+        v = a.ravel().tolist()
+    else:
+        v = _i32(a).tolist()
+    if n is not None and len(v) != n:
+        raise ValueError(f"expected {n} entries, got {len(v)}")
+    t = _ARRAYS.get(len(v))
+    if t is None:
+        t = _ARRAYS[len(v)] = C.c_int32 * len(v)
+    return t(*v)
 
 
 # ----------------------------------------------------------------- model ---
@@ -257,10 +283,8 @@ def kd_model_set_window(m, window: int, sinks: int = 0):
 
 def kd_session_reorder(m, session_ids, parents, stream=None):
     """Session ids[i] becomes a copy of what session parents[i] was (-1: stays as it is), all at once."""
-    ids = _i32(session_ids)
-    par = _i32(parents, ids.size)
-    i32p = C.POINTER(C.c_int32)
-    _check(lib().kd_session_reorder(m, ids.ctypes.data_as(i32p), par.ctypes.data_as(i32p), ids.size, _stream(stream)))
+    ids = _c32(session_ids)
+    _check(lib().kd_session_reorder(m, ids, _c32(parents, len(ids)), len(ids), _stream(stream)))
 
 
 def kd_session_fork(m, session_id: int, stream=None) -> int:
@@ -452,26 +476,23 @@ def kd_attn_window_workspace_bytes(B: int, n_heads: int, head_dim: int, cap: int
 def kd_attn_window_append_decode(q, k_new, v_new, k_cache, v_cache, slots, positions, n_heads, n_kv_heads, head_dim,
                                  n_slots, cap, window, sinks, out, workspace, stream=None):
     """kd_attn_append_decode with a sliding window: row b attends t < sinks and t > positions[b] - window."""
-    sl = _i32(slots)
-    ps = _i32(positions, sl.size)
-    i32p = C.POINTER(C.c_int32)
-    _check(lib().kd_attn_window_append_decode(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
-                                              sl.ctypes.data_as(i32p), ps.ctypes.data_as(i32p), sl.size, n_heads,
-                                              n_kv_heads, head_dim, n_slots, cap, window, sinks, _ptr(out),
-                                              _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    sl = _c32(slots)
+    B = len(sl)
+    _check(lib().kd_attn_window_append_decode(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), sl,
+                                              _c32(positions, B), B, n_heads, n_kv_heads, head_dim, n_slots, cap,
+                                              window, sinks, _ptr(out), _ptr(workspace), _nbytes(workspace),
+                                              _stream(stream)))
 
 
 def kd_attn_window_append_decode_q8(q, k_new, v_new, k_quants, k_scales, v_quants, v_scales, slots, positions, n_heads,
                                     n_kv_heads, n_slots, cap, window, sinks, out, workspace, stream=None):
     """kd_attn_window_append_decode over a Q8_0 cache of head_dim 128 (see include/kd.h)."""
-    sl = _i32(slots)
-    ps = _i32(positions, sl.size)
-    i32p = C.POINTER(C.c_int32)
+    sl = _c32(slots)
+    B = len(sl)
     _check(lib().kd_attn_window_append_decode_q8(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_quants), _ptr(k_scales),
-                                                 _ptr(v_quants), _ptr(v_scales), sl.ctypes.data_as(i32p),
-                                                 ps.ctypes.data_as(i32p), sl.size, n_heads, n_kv_heads, n_slots, cap,
-                                                 window, sinks, _ptr(out), _ptr(workspace), _nbytes(workspace),
-                                                 _stream(stream)))
+                                                 _ptr(v_quants), _ptr(v_scales), sl, _c32(positions, B), B, n_heads,
+                                                 n_kv_heads, n_slots, cap, window, sinks, _ptr(out), _ptr(workspace),
+                                                 _nbytes(workspace), _stream(stream)))
 
 
 KD_BEAM_MAX_BEAMS = 16
@@ -497,17 +518,16 @@ def kd_kv_reorder(planes, dst, src, lens, n_layers: int, n_slots: int, n_kv_head
                   sinks: int = 0, stream=None):
     """Slot dst[i] becomes what slot src[i] was, all at once and in place.  planes: device tensors
     [n_layers][n_slots][n_kv_heads][cap][...], the trailing dimensions being a row's bytes."""
-    d = _i32(dst)
-    s, n = _i32(src, d.size), _i32(lens, d.size)
+    d = _c32(dst)
+    m = len(d)
     rows = n_layers * n_slots * n_kv_heads * cap
     ptrs = (_vp * len(planes))(*[_ptr(p) for p in planes])
     nbytes = [_nbytes(p) for p in planes]
     if rows < 1 or any(b % rows for b in nbytes):
         raise ValueError("a plane's size must be a whole number of bytes per row")
     widths = (C.c_int32 * len(planes))(*[b // rows for b in nbytes])
-    i32p = C.POINTER(C.c_int32)
-    _check(lib().kd_kv_reorder(ptrs, widths, len(planes), n_layers, n_slots, n_kv_heads, cap, d.ctypes.data_as(i32p),
-                               s.ctypes.data_as(i32p), n.ctypes.data_as(i32p), d.size, window, sinks, _stream(stream)))
+    _check(lib().kd_kv_reorder(ptrs, widths, len(planes), n_layers, n_slots, n_kv_heads, cap, d, _c32(src, m),
+                               _c32(lens, m), m, window, sinks, _stream(stream)))
 
 
 def kd_attn_device_status(workspace=None, stream=None) -> int:

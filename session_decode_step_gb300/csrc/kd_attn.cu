@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kd_attn_common.cuh"
 
@@ -48,6 +49,26 @@ struct AttnSmem {
         return (uint32_t)((chunk >> 3) * HALF_BYTES + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
     }
 };
+
+// Part 0 (K) or 1 (V) of the item's new row: fp16 of the fp32 row, into the cache
+// and into the item's tile (tile: the lane's 16-byte chunk of the row there).
+template <int HD>
+__device__ __forceinline__ void win_append_row(const AttnWinArgs& a, const AttnItem& it, int lane, int part,
+                                               uint32_t tile) {
+    if (lane < HD / 8) {
+        const float* src = (part ? a.v_new : a.k_new) + ((size_t)it.b * a.nkv + it.kvh) * HD + 8 * lane;
+        uint4 w;
+        w.x = f2_hi(src[0], src[1]);
+        w.y = f2_hi(src[2], src[3]);
+        w.z = f2_hi(src[4], src[5]);
+        w.w = f2_hi(src[6], src[7]);
+        const size_t row = ((size_t)it.slot * a.nkv + it.kvh) * a.cap + it.start + it.n - 1;
+        *reinterpret_cast<uint4*>((__half*)(part ? a.v_dst : a.k_dst) + row * HD + 8 * lane) = w;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                     : "memory");
+    }
+    __syncwarp();
+}
 
 // A CTA takes the items blockIdx.x + k * gridDim.x, k = 0, 1, ...: item k goes
 // through stage k % STAGES and is computed by warp k % AT_WARPS, which then
@@ -93,6 +114,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
         *cta_failed = 0;
         mbar_init_fence();
         if (a.inject_tx && blockIdx.x == 0) mbar_expect_tx(&bar[0], (uint32_t)a.inject_tx);  // debug fault hook
+        if constexpr (WIN)
+            if (a.clear_err && blockIdx.x == 0) *a.err = 0;
     }
     __syncthreads();
 
@@ -207,12 +230,17 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
         ok = ok && mbar_wait_bounded(&bar[st], par);  // the K tile
         if (__any_sync(FULL_MASK, !ok)) {
             if (lane == 0) {
-                atomicOr(a.err, ERR_WAIT_TIMEOUT);
+                report_wait<WIN>(a);
                 *cta_failed = 1;
             }
             break;
         }
         const int n = it.n;
+        bool appends = false;
+        if constexpr (WIN) {
+            appends = a.k_new && it.s == it.ns - 1;
+            if (appends) win_append_row<HD>(a, it, lane, 0, kbase + (lane < HD / 8 ? L::off(n - 1, lane) : 0u));
+        }
         const bool refill = k + S < nk;
         AttnItem nx{};
         if (refill) nx = tab.item(a, lane, gitem(k + S));
@@ -281,7 +309,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
         ok = ok && mbar_wait_bounded(&bar[S + st], par);
         if (__any_sync(FULL_MASK, !ok)) {
             if (lane == 0) {
-                atomicOr(a.err, ERR_WAIT_TIMEOUT);
+                report_wait<WIN>(a);
                 *cta_failed = 1;
             }
             break;
@@ -297,6 +325,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
             }
             __syncwarp();
         }
+        if constexpr (WIN)
+            if (appends) win_append_row<HD>(a, it, lane, 1, vbase + (lane < HD / 8 ? L::off(n - 1, lane) : 0u));
         if (WIN && it.h0 < it.h1) {  // hidden rows of the V tile: p = 0 too
             for (int e = lane; e < (it.h1 - it.h0) * L::NREG * 8; e += 32) {
                 const int r = it.h0 + e / (L::NREG * 8), rem = e % (L::NREG * 8);
@@ -357,7 +387,11 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
                     dst[16 * mt + g] = __fadd_rn(oacc[mt][j][0], oacc[mt][j][1]);
                     dst[16 * mt + g + 8] = __fadd_rn(oacc[mt][j][2], oacc[mt][j][3]);
                 }
-                if (g == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(mx[j], lsum[j]);
+                if constexpr (WIN) {
+                    if (g == 0) *reinterpret_cast<float4*>(dst + HD) = make_float4(mx[j], lsum[j], __int_as_float(REC_VALID), 0.0f);
+                } else {
+                    if (g == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(mx[j], lsum[j]);
+                }
             }
         }
 
@@ -376,6 +410,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
             const int k = stage_item[i];
             if (k >= 0) (void)mbar_wait_bounded(&bar[i], (uint32_t)(k / S) & 1u);
         }
+    if constexpr (WIN)
+        if (*cta_failed) mark_records(a, tab, lane, warp, AT_WARPS, nk, GQ, HD);
     tl_exit(a.tl);
 }
 
@@ -436,7 +472,14 @@ __global__ void __launch_bounds__(NW * 32) attn_combine_kernel(const __grid_cons
         if (s0 + u < s1) o[u] = __ldcg(reinterpret_cast<const VecT*>(pl + (size_t)(s0 + u) * ATT_REC(HD)));
     float mloc = -INFINITY;
     for (int s = t; s < ns; s += NT) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + (size_t)s * ATT_REC(HD) + HD));
+        float2 ml;
+        if constexpr (WIN) {
+            const float4 r = __ldcg(reinterpret_cast<const float4*>(p + (size_t)s * ATT_REC(HD) + HD));
+            ml = make_float2(r.x, r.y);
+            if (__float_as_int(r.z) != REC_VALID) atomicOr(a.err, ERR_WAIT_TIMEOUT);
+        } else {
+            ml = __ldcg(reinterpret_cast<const float2*>(p + (size_t)s * ATT_REC(HD) + HD));
+        }
         wts[s] = ml.x;
         ls[s] = ml.y;
         mloc = fmaxf(mloc, ml.x);
@@ -548,10 +591,13 @@ cudaError_t attn_init_attributes() {
 }
 
 int attn_split_grid(int num_sms, int hd, int group) {
-    // persistent: as many CTAs as fit on every SM at once
-    int per_sm = 1;
+    // persistent: as many CTAs as fit on every SM at once (asked once per kernel)
+    static std::atomic<int> known[2][4];
+    std::atomic<int>& k = known[hd == 128][group == 1 ? 0 : group == 2 ? 1 : group == 4 ? 2 : 3];
+    int per_sm = k.load(std::memory_order_relaxed);
+    if (per_sm > 0) return num_sms * per_sm;
     cudaError_t e = cudaSuccess;
-#define KD_OCC(HD_, GQ_)                                                                     \
+#define KD_OCC(HD_, GQ_)                                                                            \
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_split_kernel<HD_, GQ_, false>, \
                                                       AT_WARPS * 32, AttnSmem<HD_>::TOTAL);
     auto run = [&]() -> cudaError_t {
@@ -559,7 +605,8 @@ int attn_split_grid(int num_sms, int hd, int group) {
         return e;
     };
 #undef KD_OCC
-    if (run() != cudaSuccess || per_sm < 1) per_sm = 1;
+    if (run() != cudaSuccess || per_sm < 1) return num_sms;
+    k.store(per_sm, std::memory_order_relaxed);
     return num_sms * per_sm;
 }
 

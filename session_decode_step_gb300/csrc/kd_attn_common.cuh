@@ -120,6 +120,27 @@ using AttnTableOf = typename std::conditional<WIN, AttnWinTable, AttnTable>::typ
 template <bool WIN>
 using AttnArgsOf = typename std::conditional<WIN, AttnWinArgs, AttnArgs>::type;
 
+// A bounded wait ran out: reported at once where the fault word lives across calls;
+// a call's own word is set by the merge, from the CTA's marked records.
+template <bool WIN>
+__device__ __forceinline__ void report_wait(const AttnArgsOf<WIN>& a) {
+    if constexpr (WIN) {
+        if (a.clear_err) return;
+    }
+    atomicOr(a.err, ERR_WAIT_TIMEOUT);
+}
+// Mark the records of all of a CTA's items: their contents are not to be trusted.
+__device__ __forceinline__ void mark_records(const AttnWinArgs& a, const AttnWinTable& tab, int lane, int warp, int warps,
+                                             int nk, int gq, int hd) {
+    for (int k = warp; k < nk; k += warps) {
+        const AttnItem it = tab.item(a, lane, (int)blockIdx.x + k * (int)gridDim.x);
+        if (lane < gq) {
+            float* dst = a.part + (((size_t)it.b * a.nh + (size_t)it.kvh * gq + lane) * a.max_splits + it.s) * ATT_REC(hd);
+            *reinterpret_cast<float4*>(dst + hd) = make_float4(0.0f, 1.0f, __int_as_float(REC_FAULT), 0.0f);
+        }
+    }
+}
+
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)

@@ -91,6 +91,50 @@ __device__ __forceinline__ uint32_t u8x2_odd_to_half2(uint32_t v) {
     return r;
 }
 
+// ---- quantisation ------------------------------------------------------------
+// One warp per 32-value block, a lane per value: d = max|x| / 127 (fp32), stored
+// as fp16; q = x / d rounded half away from zero, within [-127, 127]; 0 for an
+// all-zero block.  Returns the stored quant byte u = q + 128 and the scale.
+__device__ __forceinline__ uint8_t q8_quant(float x, __half& scale) {
+    float amax = fabsf(x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, o));
+    const float d = __fdiv_rn(amax, 127.0f);
+    int q = 0;
+    if (d > 0.0f) q = max(-127, min(127, (int)roundf(__fdiv_rn(x, d))));
+    scale = __float2half_rn(d);
+    return (uint8_t)(q + 128);
+}
+__device__ __forceinline__ uint8_t q8_quant_lane(float x, int lane, __half* scale_out) {
+    __half d;
+    const uint8_t u = q8_quant(x, d);
+    if (lane == 0) *scale_out = d;
+    return u;
+}
+
+// Part 0 (K) or 1 (V) of a windowed item's new row (head_dim 128): quantised into
+// the cache's planes and into the item's tile (quants tq as swizzled rows, scales ts).
+__device__ __forceinline__ void win_append_row_q8(const AttnWinArgs& a, const AttnItem& it, int lane, int part,
+                                                  uint8_t* tq, uint8_t* ts) {
+    using L = AttnQ8Smem;
+    const float* src = (part ? a.v_new : a.k_new) + ((size_t)it.b * a.nkv + it.kvh) * 128 + lane;
+    const size_t row = ((size_t)it.slot * a.nkv + it.kvh) * a.cap + it.start + it.n - 1;
+    uint8_t* q = (uint8_t*)(part ? a.v_dst : a.k_dst) + row * 128 + lane;
+    __half* sc = (part ? a.vs_dst : a.ks_dst) + row * 4;
+#pragma unroll
+    for (int blk = 0; blk < 4; ++blk) {
+        __half d;
+        const uint8_t u = q8_quant(src[32 * blk], d);
+        q[32 * blk] = u;
+        tq[L::qoff(it.n - 1, 2 * blk + (lane >> 4)) + (lane & 15)] = u;
+        if (lane == 0) {
+            sc[blk] = d;
+            *reinterpret_cast<__half*>(ts + (it.n - 1) * L::SROW + 2 * blk) = d;
+        }
+    }
+    __syncwarp();
+}
+
 // WIN: windowed rows, as in the fp16 kernel; a hidden key's value scales count as
 // zero (its quants are finite whatever they hold).
 template <int GQ, bool WIN>
@@ -121,6 +165,8 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
         *cta_failed = 0;
         mbar_init_fence();
         if (a.inject_tx && blockIdx.x == 0) mbar_expect_tx(&bar[0], (uint32_t)a.inject_tx);  // debug fault hook
+        if constexpr (WIN)
+            if (a.clear_err && blockIdx.x == 0) *a.err = 0;
     }
     __syncthreads();
 
@@ -242,12 +288,18 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
         ok = ok && mbar_wait_bounded(&bar[kst], (uint32_t)(k / SK) & 1u);  // the K part
         if (__any_sync(FULL_MASK, !ok)) {
             if (lane == 0) {
-                atomicOr(a.err, ERR_WAIT_TIMEOUT);
+                report_wait<WIN>(a);
                 *cta_failed = 1;
             }
             break;
         }
         const int n = it.n;
+        bool appends = false;
+        if constexpr (WIN) {
+            appends = a.k_new && it.s == it.ns - 1;
+            if (appends)
+                win_append_row_q8(a, it, lane, 0, smem + L::KQ_OFF + kst * L::TILE, smem + L::KS_OFF + kst * L::STILE);
+        }
 
         // ---- scores: per 16-key tile m and 32-dim block, two MMAs, then the keys' block scales
         float sacc[AT_KT][NQ][4];
@@ -333,12 +385,15 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
         ok = ok && mbar_wait_bounded(&bar[SK + vst], (uint32_t)(k / SV) & 1u);
         if (__any_sync(FULL_MASK, !ok)) {
             if (lane == 0) {
-                atomicOr(a.err, ERR_WAIT_TIMEOUT);
+                report_wait<WIN>(a);
                 *cta_failed = 1;
             }
             break;
         }
 
+        if constexpr (WIN)
+            if (appends)
+                win_append_row_q8(a, it, lane, 1, smem + L::VQ_OFF + vst * L::TILE, smem + L::VS_OFF + vst * L::STILE);
         // p d_t,blk would fall below fp16's normal range for small p: the item's
         // products carry an exact power-of-two factor 2^e, taken from its largest
         // value scale so that p d 2^e < 2^14, and the output drops it again in fp32.
@@ -437,7 +492,11 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
                     *reinterpret_cast<float2*>(dst + 16 * mt + 2 * g) =
                         make_float2(__fmul_rn(__fadd_rn(oacc[mt][j][0], oacc[mt][j][1]), pinv),
                                     __fmul_rn(__fadd_rn(oacc[mt][j][2], oacc[mt][j][3]), pinv));
-                if (g == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(mx[j], lsum[j]);
+                if constexpr (WIN) {
+                    if (g == 0) *reinterpret_cast<float4*>(dst + HD) = make_float4(mx[j], lsum[j], __int_as_float(REC_VALID), 0.0f);
+                } else {
+                    if (g == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(mx[j], lsum[j]);
+                }
             }
         }
         __syncwarp();  // the V part is read: refill it
@@ -457,22 +516,9 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
             const int k = stage_item[i];
             if (k >= 0) (void)mbar_wait_bounded(&bar[i], (uint32_t)(k / (i < SK ? SK : SV)) & 1u);
         }
+    if constexpr (WIN)
+        if (*cta_failed) mark_records(a, tab, lane, warp, W, nk, GQ, HD);
     tl_exit(a.tl);
-}
-
-// ---- quantisation ------------------------------------------------------------
-// One warp per 32-value block, a lane per value: d = max|x| / 127 (fp32), stored
-// as fp16; q = x / d rounded half away from zero, within [-127, 127]; 0 for an
-// all-zero block.  Returns the stored quant byte u = q + 128.
-__device__ __forceinline__ uint8_t q8_quant_lane(float x, int lane, __half* scale_out) {
-    float amax = fabsf(x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, o));
-    const float d = __fdiv_rn(amax, 127.0f);
-    int q = 0;
-    if (d > 0.0f) q = max(-127, min(127, (int)roundf(__fdiv_rn(x, d))));
-    if (lane == 0) *scale_out = __float2half_rn(d);
-    return (uint8_t)(q + 128);
 }
 
 // The step's new K and V rows (fp32 [B][nkv][128], from the q|k|v epilogue) into
@@ -489,44 +535,6 @@ __global__ void __launch_bounds__(256) kvq8_append_kernel(const float* __restric
     const float x = (part ? vnew : knew)[((size_t)b * nkv + h) * 128 + 32 * blk + lane];
     uint8_t* q = (part ? vq : kq) + row * 128 + 32 * blk + lane;
     *q = q8_quant_lane(x, lane, (part ? vs : ks) + row * 4 + blk);
-}
-
-// The same for a windowed op-level call: slots and positions come with the launch,
-// and the call's fault word is cleared.
-__global__ void __launch_bounds__(256) win_append_q8_kernel(const __grid_constant__ AttnWinArgs a,
-                                                            const float* __restrict__ knew,
-                                                            const float* __restrict__ vnew, uint8_t* kq, __half* ks,
-                                                            uint8_t* vq, __half* vs) {
-    pdl_launch_dependents();
-    const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (h == 0 && b == 0 && threadIdx.x == 0) *a.err = 0;
-    const int blk = warp & 3, part = warp >> 2;
-    const long row = ((long)a.vslot[b] * a.nkv + h) * a.cap + a.vpos[b];
-    const float x = (part ? vnew : knew)[((size_t)b * a.nkv + h) * 128 + 32 * blk + lane];
-    uint8_t* q = (part ? vq : kq) + row * 128 + 32 * blk + lane;
-    *q = q8_quant_lane(x, lane, (part ? vs : ks) + row * 4 + blk);
-}
-
-// And into fp16 rows of hd = 64 or 128: thread i of block (h, b) converts value i of K, then of V.
-__global__ void __launch_bounds__(256) win_append_fp16_kernel(const __grid_constant__ AttnWinArgs a,
-                                                              const float* __restrict__ k,
-                                                              const float* __restrict__ v, __half* kc, __half* vc) {
-    pdl_launch_dependents();
-    const int h = blockIdx.x, b = blockIdx.y, i = threadIdx.x % a.hd, part = threadIdx.x / a.hd;
-    if (h == 0 && b == 0 && threadIdx.x == 0) *a.err = 0;
-    const size_t dst = (((size_t)a.vslot[b] * a.nkv + h) * a.cap + a.vpos[b]) * a.hd + i;
-    const size_t src = ((size_t)b * a.nkv + h) * a.hd + i;
-    (part ? vc : kc)[dst] = __float2half_rn((part ? v : k)[src]);
-}
-
-cudaError_t launch_win_append(const AttnWinArgs& a, const float* k, const float* v, void* kc, void* vc, __half* ks,
-                              __half* vs, cudaStream_t s) {
-    const dim3 grid(a.nkv, a.B);
-    if (ks)
-        win_append_q8_kernel<<<grid, 256, 0, s>>>(a, k, v, (uint8_t*)kc, ks, (uint8_t*)vc, vs);
-    else
-        win_append_fp16_kernel<<<grid, 2 * a.hd, 0, s>>>(a, k, v, (__half*)kc, (__half*)vc);
-    return cudaGetLastError();
 }
 
 // Rows of fp32 or fp16 values [n_rows][128] into Q8_0 rows: source row r (layer
@@ -630,8 +638,7 @@ cudaError_t attn_q8_init_attributes() {
             return e;
     }
     for (const void* f : {(const void*)kvq8_append_kernel, (const void*)kvq8_rows_kernel<__half>,
-                          (const void*)kvq8_rows_kernel<float>, (const void*)win_append_q8_kernel,
-                          (const void*)win_append_fp16_kernel})
+                          (const void*)kvq8_rows_kernel<float>})
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                       cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
             return e;

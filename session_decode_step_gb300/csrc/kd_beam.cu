@@ -4,18 +4,24 @@
 // Beam w of a group has the cumulative log probability score_w; continuing it
 // with token v gives
 //   s(w, v) = score_w + x_wv - L_w,   L_w = log sum_u e^{x_wu},
-// and the group's n_out best pairs are wanted, larger s first, then lower w, then
+// and the group's K best pairs are wanted, larger s first, then lower w, then
 // lower v.  Within a row the order is the logits' own, so one pass over the
-// logits does everything that touches all of them: a block takes 4096 logits of
-// one row, leaves (m, sum e^{x-m}) and its n_out best logits, sorted.  A second
-// kernel, one CTA per group and one warp per beam, forms L_w, merges the row's
-// lists, and merges the rows by s.
+// logits does everything that touches all of them: a CTA walks a segment of one
+// row in blocks of 4096, leaves (m, sum e^{x-m}) of every block and the
+// segment's K best logits, sorted.  A second kernel, one CTA per group, forms
+// L_w, merges each row's lists, and merges the rows by s.
+//
+// The selection costs next to nothing once a warp knows K candidates: a block
+// whose largest logit does not exceed the warp's K-th best is passed over, so a
+// random row brings about K ln(blocks) late candidates.  The first block's are
+// found through the lanes' own maxima: the K-th largest of them bounds the K-th
+// largest logit from below, and few logits lie above it.
 //
 // s decides between rows, where two candidates can lie as close as fp32 rounds:
-// L_w's last steps and s are fp64 (a handful of operations per row), the sums of
-// exponentials fp32 inside a warp and exact 64-bit fixed point across blocks, so
-// the order of blocks never matters and a row's result does not depend on the
-// rest of the batch.
+// L_w's last steps and s are fp64 (a handful of operations per row); the sums of
+// exponentials are fp32 inside a block, in an order that depends on nothing but
+// the block, and exact 64-bit fixed point across blocks.  So a row's result does
+// not depend on the segments, hence not on the rest of the batch.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -27,38 +33,48 @@ namespace kd {
 
 constexpr int BS_THREADS = 256;
 constexpr int BS_WARPS = BS_THREADS / 32;
-constexpr int BS_VPT = 16;                      // logits per thread
+constexpr int BS_VPT = 16;                      // logits per thread and block
 constexpr int BS_BLOCK = BS_THREADS * BS_VPT;   // logits per block
 constexpr int BS_MAX_BLOCKS = 128;              // vocabulary up to 524288
+constexpr int BS_MAX_SEGS = 32;                 // segments (lists) per row: one per lane of the merge
 constexpr int BS_MAX_OUT = 32;
-constexpr int BS_CAP = 512;                     // candidates a block ranks at once
-constexpr int BS_AHEAD = 4;                     // list entries the merge stages in shared memory
+// A warp's candidates: up to 2 K kept, and at most all 512 of a block on top.
+constexpr int BS_CAP = 2 * BS_MAX_OUT + 32 * BS_VPT;
 static_assert(KD_BEAM_MAX_VOCAB == BS_BLOCK * BS_MAX_BLOCKS && KD_BEAM_MAX_OUT == BS_MAX_OUT, "kd.h limits");
 
 // (x, index) as a 64-bit key whose unsigned order is: larger x, then lower index
 // (-0 equals +0).  0 is no candidate.
-__device__ __forceinline__ unsigned long long beam_key(float x, int i) {
+__device__ __forceinline__ unsigned beam_ord(float x) {
     const unsigned u = __float_as_uint(x + 0.0f);
-    const unsigned ord = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return ((unsigned long long)ord << 32) | (unsigned)~i;
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-__device__ __forceinline__ float beam_key_x(unsigned long long k) {
-    const unsigned ord = (unsigned)(k >> 32);
+__device__ __forceinline__ float beam_unord(unsigned ord) {
     return __uint_as_float((ord & 0x80000000u) ? (ord & 0x7fffffffu) : ~ord);
 }
+__device__ __forceinline__ unsigned long long beam_key(float x, int i) {
+    return ((unsigned long long)beam_ord(x) << 32) | (unsigned)~i;
+}
+__device__ __forceinline__ float beam_key_x(unsigned long long k) { return beam_unord((unsigned)(k >> 32)); }
 __device__ __forceinline__ int beam_key_i(unsigned long long k) { return (int)~(unsigned)k; }
 
-// Warp maximum / minimum of 64-bit keys, high words first.
-__device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long k) {
+// The lanes holding the warp's largest key: by high words, then, among equals, low words.  0: no lane holds one.
+__device__ __forceinline__ unsigned warp_best(unsigned long long k) {
     const unsigned hi = (unsigned)(k >> 32), mh = __reduce_max_sync(FULL_MASK, hi);
-    const unsigned ml = __reduce_max_sync(FULL_MASK, hi == mh ? (unsigned)k : 0u);
-    return ((unsigned long long)mh << 32) | ml;
+    if (mh == 0) return 0u;
+    unsigned who = __ballot_sync(FULL_MASK, hi == mh);
+    if (who & (who - 1)) {
+        const unsigned ml = __reduce_max_sync(FULL_MASK, hi == mh ? (unsigned)k : 0u);
+        who = __ballot_sync(FULL_MASK, hi == mh && (unsigned)k == ml);
+    }
+    return who;
 }
-__device__ __forceinline__ unsigned long long warp_min_u64(unsigned long long k) {
-    const unsigned hi = (unsigned)(k >> 32), mh = __reduce_min_sync(FULL_MASK, hi);
-    const unsigned ml = __reduce_min_sync(FULL_MASK, hi == mh ? (unsigned)k : 0xffffffffu);
-    return ((unsigned long long)mh << 32) | ml;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
+constexpr float LOG2E = 1.44269504088896341f;
 
 // A beam's row is read only if the beam can continue: not finished, score > -inf (a NaN score is dead too).
 __device__ __forceinline__ bool beam_live(const float* scores, const int* done, int r) {
@@ -69,218 +85,284 @@ struct BeamArgs {
     const float* logits;  // [rows][ld]
     long ld;
     int V, W, K, nblk;    // vocabulary, beams per group, candidates kept, blocks per row
+    int nseg, seg_blocks; // segments per row, blocks per segment
     const float* scores;  // [rows], or nullptr (zeros)
     const int* done;      // [rows], or nullptr
     int eos;
     float2* part;              // [rows][nblk] (m, sum e^{x - m})
-    unsigned long long* keys;  // [rows][nblk][K] sorted, 0-padded
+    unsigned long long* keys;  // [rows][nseg][K] sorted, 0-padded
     int *parents, *tokens, *done_out;
     float* scores_out;
 };
 
-__global__ void __launch_bounds__(BS_THREADS) beam_scan_kernel(const BeamArgs a) {
-    __shared__ unsigned long long cand[BS_CAP];
-    __shared__ unsigned long long subset[32];
-    __shared__ float wm[BS_WARPS], wsum[BS_WARPS];
-    __shared__ int cnt;
-    pdl_launch_dependents();
-    const int r = blockIdx.y, blk = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    if (!beam_live(a.scores, a.done, r)) return;
-    const float* p = a.logits + (size_t)r * a.ld + (size_t)blk * BS_BLOCK;
-    const int n = min(BS_BLOCK, a.V - blk * BS_BLOCK);
-    float x[BS_VPT];
+// Thread t's logits of a block: 4t .. 4t + 3 of each quarter.  VEC: 16-byte loads (every row 16-byte aligned).
+template <bool VEC>
+__device__ __forceinline__ void beam_load(const float* p, int n, int t, float (&x)[BS_VPT]) {
+    if (VEC && n >= BS_BLOCK) {
 #pragma unroll
-    for (int i = 0; i < BS_VPT; ++i) x[i] = i * BS_THREADS + t < n ? __ldg(p + i * BS_THREADS + t) : -INFINITY;
-    // NaN counts as -inf; the thread's largest value and its first place
-    float m = -INFINITY;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < BS_VPT; ++i) {
-        x[i] = fmaxf(x[i], -INFINITY);
-        if (x[i] > m) {
-            m = x[i];
-            at = i;
+        for (int i = 0; i < BS_VPT / 4; ++i) {
+            const float4 v = __ldcs(reinterpret_cast<const float4*>(p + i * 4 * BS_THREADS + 4 * t));
+            x[4 * i] = v.x;
+            x[4 * i + 1] = v.y;
+            x[4 * i + 2] = v.z;
+            x[4 * i + 3] = v.w;
         }
-    }
-    float s = 0.0f;
-    if (m == INFINITY) {  // x - m taken as 0 where x == m
+    } else {
 #pragma unroll
-        for (int i = 0; i < BS_VPT; ++i) s += x[i] == INFINITY ? 1.0f : 0.0f;
-    } else if (m > -INFINITY) {
-#pragma unroll
-        for (int i = 0; i < BS_VPT; ++i) s += exp2f((x[i] - m) * 1.44269504088896341f);
-    }
-    const unsigned long long best = m > -INFINITY ? beam_key(m, blk * BS_BLOCK + at * BS_THREADS + t) : 0ull;
-    // The warp's (m, sum), and the largest key of each subset of 8 threads: 32
-    // subsets, so at least 32 logits are no less than the smallest of these.
-    float mw = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mw = fmaxf(mw, __shfl_xor_sync(FULL_MASK, mw, o));
-    s = m == mw ? s : s * expf(m - mw);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(FULL_MASK, s, o);
-    unsigned long long k8 = best;
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) k8 = max(k8, __shfl_xor_sync(FULL_MASK, k8, o));
-    if ((lane & 7) == 0) subset[t >> 3] = k8;
-    if (lane == 0) {
-        wm[warp] = mw;
-        wsum[warp] = mw > -INFINITY ? s : 0.0f;
-    }
-    if (t == 0) cnt = 0;
-    __syncthreads();
-    const unsigned long long thr = warp_min_u64(subset[lane]);
-    if (t == 0) {
-        float mb = wm[0], sb = 0.0f;
-        for (int w = 1; w < BS_WARPS; ++w) mb = fmaxf(mb, wm[w]);
-        for (int w = 0; w < BS_WARPS; ++w) sb += wm[w] == mb ? wsum[w] : wsum[w] * expf(wm[w] - mb);
-        a.part[(size_t)r * a.nblk + blk] = make_float2(mb, mb > -INFINITY ? sb : 0.0f);
-    }
-    const float tv = thr ? beam_key_x(thr) : -INFINITY;
-#pragma unroll
-    for (int i = 0; i < BS_VPT; ++i)
-        if (x[i] >= tv && x[i] > -INFINITY) {
-            const unsigned long long k = beam_key(x[i], blk * BS_BLOCK + i * BS_THREADS + t);
-            if (k >= thr) {
-                const int j = atomicAdd(&cnt, 1);
-                if (j < BS_CAP) cand[j] = k;
-            }
-        }
-    __syncthreads();
-    unsigned long long* out = a.keys + ((size_t)r * a.nblk + blk) * a.K;
-    const int c = cnt;
-    if (c <= BS_CAP) {
-        for (int j = t; j < c; j += BS_THREADS) {
-            const unsigned long long k = cand[j];
-            int rank = 0;
-            for (int i = 0; i < c; ++i) rank += cand[i] > k ? 1 : 0;
-            if (rank < a.K) out[rank] = k;
-        }
-        for (int j = c + t; j < a.K; j += BS_THREADS) out[j] = 0ull;
-    } else {  // too many to rank (a subset without a value): one block maximum per candidate
-        unsigned long long last = ~0ull;
-        for (int j = 0; j < a.K; ++j) {
-            unsigned long long b = 0ull;
-#pragma unroll
-            for (int i = 0; i < BS_VPT; ++i)
-                if (x[i] > -INFINITY) {
-                    const unsigned long long k = beam_key(x[i], blk * BS_BLOCK + i * BS_THREADS + t);
-                    if (k < last) b = max(b, k);
-                }
-            b = warp_max_u64(b);
-            __syncthreads();
-            if (lane == 0) subset[warp] = b;
-            __syncthreads();
-            last = warp_max_u64(lane < BS_WARPS ? subset[lane] : 0ull);
-            if (t == 0) out[j] = last;
+        for (int i = 0; i < BS_VPT; ++i) {
+            const int e = (i >> 2) * 4 * BS_THREADS + 4 * t + (i & 3);
+            x[i] = e < n ? __ldg(p + e) : -INFINITY;
         }
     }
 }
 
-// One CTA per group, one warp per beam.
-__global__ void __launch_bounds__(32 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(const BeamArgs a) {
-    extern __shared__ unsigned long long staged[];  // [W][nblk][ahead] the lists' first entries
+// The warp's candidates, sorted and cut to the K best; returns their number.
+__device__ __forceinline__ int beam_compact(unsigned long long* buf, unsigned long long* best, int n, int K, int lane) {
+    __syncwarp();
+    for (int q = lane; q < n; q += 32) {
+        const unsigned long long k = buf[q];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += buf[j] > k ? 1 : 0;
+        if (rank < K) best[rank] = k;
+    }
+    __syncwarp();
+    const int c = min(n, K);
+    if (lane < c) buf[lane] = best[lane];
+    __syncwarp();
+    return c;
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
+    __shared__ unsigned long long cand[BS_WARPS][BS_CAP];
+    __shared__ unsigned long long best[BS_WARPS][BS_MAX_OUT];
+    __shared__ float2 wpart[BS_MAX_BLOCKS][BS_WARPS];
+    __shared__ int count[BS_WARPS];
+    pdl_launch_dependents();
+    const int r = blockIdx.y, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    if (!beam_live(a.scores, a.done, r)) return;
+    const int K = a.K, b0 = blockIdx.x * a.seg_blocks, nb = min(a.seg_blocks, a.nblk - b0);
+    const float* row = a.logits + (size_t)r * a.ld;
+    unsigned long long* buf = cand[warp];
+    int cnt = 0;
+    float thr = -INFINITY;  // the warp's K-th best once it has K: later equals lose to it (higher indices)
+    float nx[BS_VPT];
+    beam_load<VEC>(row + (size_t)b0 * BS_BLOCK, a.V - b0 * BS_BLOCK, t, nx);
+    for (int b = 0; b < nb; ++b) {
+        const int e0 = (b0 + b) * BS_BLOCK;
+        float x[BS_VPT];
+#pragma unroll
+        for (int i = 0; i < BS_VPT; ++i) x[i] = nx[i];
+        if (b + 1 < nb) beam_load<VEC>(row + e0 + BS_BLOCK, a.V - e0 - BS_BLOCK, t, nx);
+        float m = x[0];
+#pragma unroll
+        for (int i = 1; i < BS_VPT; ++i) m = fmaxf(m, x[i]);
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < BS_VPT; i += 2) {
+            s0 += ex2((x[i] - m) * LOG2E);
+            s1 += ex2((x[i + 1] - m) * LOG2E);
+        }
+        float s = s0 + s1;
+        if (s != s) {  // a NaN, or the largest is infinite: NaN counts as -inf, x - m as 0 where x == m
+            m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < BS_VPT; ++i) {
+                x[i] = fmaxf(x[i], -INFINITY);
+                m = fmaxf(m, x[i]);
+            }
+            s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < BS_VPT; ++i) s += x[i] == m ? 1.0f : ex2((x[i] - m) * LOG2E);
+            if (m == -INFINITY) s = 0.0f;
+        }
+        const float mw = beam_unord(__reduce_max_sync(FULL_MASK, beam_ord(m)));
+        s = m == mw ? s : s * ex2((m - mw) * LOG2E);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(FULL_MASK, s, o);
+        if (lane == 0) wpart[b][warp] = make_float2(mw, s);
+
+        const unsigned hot = __ballot_sync(FULL_MASK, m > thr);
+        if (hot) {
+            float lo = beam_unord(beam_ord(thr) + 1u);  // the next value above: x >= lo is x > thr
+            if (__popc(hot) >= K) {  // at least K logits are no less than the K-th largest lane maximum
+                int rank = 0;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float o = __shfl_sync(FULL_MASK, m, j);
+                    rank += o > m || (o == m && j < lane) ? 1 : 0;
+                }
+                lo = __shfl_sync(FULL_MASK, m, __ffs(__ballot_sync(FULL_MASK, rank == K - 1)) - 1);
+            }
+#pragma unroll
+            for (int i = 0; i < BS_VPT; ++i) {
+                const unsigned who = __ballot_sync(FULL_MASK, x[i] >= lo);
+                if (who) {
+                    if (x[i] >= lo)
+                        buf[cnt + __popc(who & ((1u << lane) - 1u))] =
+                            beam_key(x[i], e0 + (i >> 2) * 4 * BS_THREADS + 4 * t + (i & 3));
+                    cnt += __popc(who);
+                }
+            }
+            if (cnt >= K && (thr == -INFINITY || cnt >= K + 24)) {
+                cnt = beam_compact(buf, best[warp], cnt, K, lane);
+                thr = beam_key_x(buf[K - 1]);
+            }
+        }
+    }
+    cnt = beam_compact(buf, best[warp], cnt, K, lane);
+    if (lane >= cnt) buf[lane] = 0ull;
+    if (lane == 0) count[warp] = cnt;
+    __syncthreads();
+    // the warps' sorted lists into the segment's: a key's rank is its own place plus the larger keys of the others
+    unsigned long long* out = a.keys + ((size_t)r * a.nseg + blockIdx.x) * K;
+    if (lane < cnt) {
+        const unsigned long long k = buf[lane];
+        int rank = lane;
+#pragma unroll
+        for (int w = 0; w < BS_WARPS; ++w) {
+            if (w == warp) continue;
+            int c = 0;  // larger keys in cand[w][0..31], found by halving
+#pragma unroll
+            for (int h = 16; h > 0; h >>= 1)
+                if (cand[w][c + h - 1] > k) c += h;
+            if (cand[w][c] > k) ++c;
+            rank += c;
+        }
+        if (rank < K) out[rank] = k;
+    }
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < BS_WARPS; ++w) total += count[w];
+    if (t < K && t >= total) out[t] = 0ull;
+    if (t < nb) {  // the blocks' sums, warps in order
+        float mb = -INFINITY, sb = 0.0f;
+#pragma unroll
+        for (int w = 0; w < BS_WARPS; ++w) mb = fmaxf(mb, wpart[t][w].x);
+#pragma unroll
+        for (int w = 0; w < BS_WARPS; ++w) {
+            const float2 p = wpart[t][w];
+            sb += p.x == mb ? p.y : p.y * ex2((p.x - mb) * LOG2E);
+        }
+        a.part[(size_t)r * a.nblk + b0 + t] = make_float2(mb, mb > -INFINITY ? sb : 0.0f);
+    }
+}
+
+// One CTA per group: warps 0 .. W - 1 merge the rows' lists while warps W .. 2W - 1
+// form the rows' log sums; then warp 0 merges the rows.
+__global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(const __grid_constant__ BeamArgs a) {
+    extern __shared__ unsigned long long staged[];  // [W][nseg][K] the rows' lists
+    __shared__ unsigned long long row_key[KD_BEAM_MAX_BEAMS][BS_MAX_OUT];
     __shared__ double row_s[KD_BEAM_MAX_BEAMS][BS_MAX_OUT];
-    __shared__ int row_v[KD_BEAM_MAX_BEAMS][BS_MAX_OUT];
+    __shared__ double row_lg[KD_BEAM_MAX_BEAMS];
+    __shared__ float row_m[KD_BEAM_MAX_BEAMS];
     __shared__ int row_n[KD_BEAM_MAX_BEAMS];
     pdl_wait();
-    const int g = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5, r = g * a.W + w;
-    const int ahead = min(a.K, BS_AHEAD);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp < a.W ? warp : warp - a.W;
+    const int g = blockIdx.x, r = g * a.W + w, K = a.K;
+    const bool live = beam_live(a.scores, a.done, r);
     const float score = a.scores ? a.scores[r] : 0.0f;
-    if (!beam_live(a.scores, a.done, r)) {
-        if (lane == 0) {  // a finished beam stands for itself; a dead one offers nothing
-            const bool fin = a.done && a.done[r] && score > -INFINITY;
-            row_n[w] = fin ? 1 : 0;
-            row_s[w][0] = (double)score;
-            row_v[w][0] = a.eos;
-        }
-    } else {
-        const unsigned long long* lists = a.keys + (size_t)r * a.nblk * a.K;
-        unsigned long long* st = staged + (size_t)w * a.nblk * ahead;
-        for (int i = lane; i < a.nblk * ahead; i += 32) st[i] = __ldcg(lists + (size_t)(i / ahead) * a.K + i % ahead);
-        // L = M + log sum_b s_b e^{m_b - M}; the sum in units of 2^-40 (each term at most 4096, the largest at least 1)
-        const float2* part = a.part + (size_t)r * a.nblk;
-        float M = -INFINITY;
-        for (int b = lane; b < a.nblk; b += 32) M = fmaxf(M, __ldcg(part + b).x);
+    if (warp >= a.W) {
+        // L = M + log sum_b s_b e^{m_b - M}; the sum in units of 2^-40 (a block's is at most 4096, the largest's at least 1)
+        if (live) {
+            const float2* part = a.part + (size_t)r * a.nblk;
+            float2 p[BS_MAX_BLOCKS / 32];
+            float M = -INFINITY;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, o));
-        long long sum = 0;
-        for (int b = lane; b < a.nblk; b += 32) {
-            const float2 ms = __ldcg(part + b);
-            const float f = ms.x == M ? ms.y : ms.y * expf(ms.x - M);
-            sum += __float2ll_rn(f * 0x1p40f);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
-        const double lg = log((double)sum * 0x1p-40);
-        __syncwarp();
-        // The row's K best: lane l holds the heads of lists l, l + 32, ...
-        unsigned long long head[BS_MAX_BLOCKS / 32];
-        int next[BS_MAX_BLOCKS / 32];
-#pragma unroll
-        for (int q = 0; q < BS_MAX_BLOCKS / 32; ++q) {
-            const int b = lane + 32 * q;
-            head[q] = b < a.nblk ? st[b * ahead] : 0ull;
-            next[q] = 1;
-        }
-        int n = 0;
-        for (; n < a.K; ++n) {
-            unsigned long long best = head[0];
-#pragma unroll
-            for (int q = 1; q < BS_MAX_BLOCKS / 32; ++q) best = max(best, head[q]);
-            const unsigned long long k = warp_max_u64(best);
-            if (!k) break;
+            for (int q = 0; q < BS_MAX_BLOCKS / 32; ++q) {
+                const int b = lane + 32 * q;
+                p[q] = b < a.nblk ? __ldcg(part + b) : make_float2(-INFINITY, 0.0f);
+                M = fmaxf(M, p[q].x);
+            }
+            M = beam_unord(__reduce_max_sync(FULL_MASK, beam_ord(M)));
+            long long sum = 0;
 #pragma unroll
             for (int q = 0; q < BS_MAX_BLOCKS / 32; ++q)
-                if (head[q] == k) {
-                    const int b = lane + 32 * q, e = next[q]++;
-                    head[q] = e >= a.K ? 0ull : e < ahead ? st[b * ahead + e] : __ldcg(lists + (size_t)b * a.K + e);
-                }
+                sum += __float2ll_rn((p[q].x == M ? p[q].y : p[q].y * expf(p[q].x - M)) * 0x1p40f);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
+            const double lg = log((double)sum * 0x1p-40);
             if (lane == 0) {
-                const float xv = beam_key_x(k);
-                // x == M first: M may be +inf
-                row_s[w][n] = (double)score + ((xv == M ? 0.0 : (double)xv - (double)M) - lg);
-                row_v[w][n] = beam_key_i(k);
+                row_lg[w] = lg;
+                row_m[w] = M;
+            }
+        }
+    } else if (live) {
+        const unsigned long long* lists = a.keys + (size_t)r * a.nseg * K;
+        unsigned long long* st = staged + (size_t)w * a.nseg * K;
+        for (int i = lane; i < a.nseg * K; i += 32) st[i] = __ldcg(lists + i);
+        __syncwarp();
+        // lane l holds the head of list l
+        const unsigned long long* at = st + lane * K;
+        const unsigned long long* end = at + K;
+        unsigned long long head = lane < a.nseg ? *at : 0ull;
+        int n = 0;
+        for (; n < K; ++n) {
+            const unsigned who = warp_best(head);
+            if (!who) break;
+            if ((who >> lane) & 1u) {
+                row_key[w][n] = head;
+                head = ++at < end ? *at : 0ull;
             }
         }
         if (lane == 0) row_n[w] = n;
+    } else if (lane == 0) {  // a finished beam stands for itself; a dead one offers nothing
+        const bool fin = a.done && a.done[r] && score > -INFINITY;
+        row_n[w] = fin ? 1 : 0;
+        row_key[w][0] = (unsigned)~a.eos;
+        row_s[w][0] = (double)score;
     }
     __syncthreads();
-    if (w) return;
-    // The group's K best: lane w holds the head of beam w's list (larger s, then the lower beam).
+    if (warp < a.W && live && lane < row_n[w]) {
+        const float xv = beam_key_x(row_key[w][lane]), M = row_m[w];
+        // x == M first: M may be infinite
+        row_s[w][lane] = (double)score + ((xv == M ? 0.0 : (double)xv - (double)M) - row_lg[w]);
+    }
+    __syncthreads();
+    if (warp) return;
+    // Lane w holds the head of beam w's list; larger s first, then the lower beam.
     const int cnt = lane < a.W ? row_n[lane] : 0;
-    int pos = 0;
-    double hs = cnt ? row_s[lane][0] : -INFINITY;
-    for (int j = 0; j < a.K; ++j) {
-        const double v = hs + 0.0;
+    // an order-preserving key of s; -inf and NaN never win
+    auto skey = [&](int pos) -> unsigned long long {
+        if (pos >= cnt) return 0ull;
+        const double v = row_s[lane][pos] + 0.0;
         const unsigned long long u = (unsigned long long)__double_as_longlong(v);
-        // -inf and NaN never win; an order-preserving key of s otherwise
-        const unsigned long long key = !(v > -INFINITY) ? 0ull : (u >> 63) ? ~u : (u | 0x8000000000000000ull);
-        const unsigned long long k = warp_max_u64(key);
-        const int o = g * a.K + j;
-        if (!k) {
-            if (lane == 0) {
-                a.parents[o] = -1;
-                a.tokens[o] = -1;
-                a.scores_out[o] = -INFINITY;
-                if (a.done_out) a.done_out[o] = 0;
-            }
-            continue;
-        }
-        const int win = __ffs(__ballot_sync(FULL_MASK, key == k)) - 1;
-        if (lane == win) {
-            const int tok = row_v[lane][pos];
-            a.parents[o] = lane;
+        return !(v > -INFINITY) ? 0ull : (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+    };
+    int pos = 0, mine = -1;  // mine: the winner (beam, place) of output `lane`
+    unsigned long long key = skey(0);
+    for (int j = 0; j < K; ++j) {
+        const unsigned who = warp_best(key);
+        if (!who) break;
+        const int win = __ffs(who) - 1, wp = __shfl_sync(FULL_MASK, pos, win);
+        if (lane == j) mine = win * BS_MAX_OUT + wp;
+        if (lane == win) key = skey(++pos);
+    }
+    if (lane < K) {
+        const int o = g * K + lane;
+        if (mine < 0) {
+            a.parents[o] = -1;
+            a.tokens[o] = -1;
+            a.scores_out[o] = -INFINITY;
+            if (a.done_out) a.done_out[o] = 0;
+        } else {
+            const int bw = mine / BS_MAX_OUT, tok = beam_key_i(row_key[bw][mine % BS_MAX_OUT]);
+            a.parents[o] = bw;
             a.tokens[o] = tok;
-            a.scores_out[o] = (float)hs;
-            if (a.done_out) a.done_out[o] = (a.eos >= 0 && tok == a.eos) || (a.done && a.done[r + lane]) ? 1 : 0;
-            hs = ++pos < cnt ? row_s[lane][pos] : -INFINITY;
+            a.scores_out[o] = (float)row_s[bw][mine % BS_MAX_OUT];
+            if (a.done_out) a.done_out[o] = tok == a.eos || (a.done && a.done[r + bw]) ? 1 : 0;
         }
     }
 }
 
-constexpr int BS_MERGE_SMEM = KD_BEAM_MAX_BEAMS * BS_MAX_BLOCKS * BS_AHEAD * 8;
+constexpr int BS_MERGE_SMEM = KD_BEAM_MAX_BEAMS * BS_MAX_SEGS * BS_MAX_OUT * 8;
 cudaError_t beam_init_attributes() {
+    cudaError_t e = cudaSuccess;
+    for (const void* f : {(const void*)beam_scan_kernel<true>, (const void*)beam_scan_kernel<false>,
+                          (const void*)beam_merge_kernel})
+        if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                      cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
+            return e;
     return cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BS_MERGE_SMEM);
 }
 
@@ -326,8 +408,6 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
     a.scores = scores;
     a.done = done;
     a.eos = eos < 0 ? -1 : eos;
-    a.keys = reinterpret_cast<unsigned long long*>(workspace);
-    a.part = reinterpret_cast<float2*>(a.keys + (size_t)rows * a.nblk * n_out);
     a.parents = parents_out;
     a.tokens = tokens_out;
     a.scores_out = scores_out;
@@ -336,7 +416,21 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
     int dev = 0;
     KD_TRY(cudaGetDevice(&dev));
     KD_TRY(ensure_device_attributes(dev));
-    beam_scan_kernel<<<dim3(a.nblk, rows), BS_THREADS, 0, s>>>(a);
+    // Segments: as many per row as fill the GPU with four CTAs on every SM, at most
+    // 32 (the merge's lanes) and one block each; more rows than that, one segment.
+    int sms = 0;
+    KD_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    int nseg = 4 * sms / rows;
+    nseg = nseg < 1 ? 1 : nseg > BS_MAX_SEGS ? BS_MAX_SEGS : nseg;
+    a.seg_blocks = (a.nblk + nseg - 1) / nseg;
+    a.nseg = (a.nblk + a.seg_blocks - 1) / a.seg_blocks;
+    a.keys = reinterpret_cast<unsigned long long*>(workspace);
+    a.part = reinterpret_cast<float2*>(a.keys + (size_t)rows * a.nseg * n_out);
+    const dim3 grid(a.nseg, rows);
+    if (ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0)
+        beam_scan_kernel<true><<<grid, BS_THREADS, 0, s>>>(a);
+    else
+        beam_scan_kernel<false><<<grid, BS_THREADS, 0, s>>>(a);
     KD_TRY(cudaGetLastError());
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -345,8 +439,8 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(n_groups);
-    cfg.blockDim = dim3(32 * n_beams);
-    cfg.dynamicSmemBytes = (size_t)n_beams * a.nblk * (n_out < BS_AHEAD ? n_out : BS_AHEAD) * 8;
+    cfg.blockDim = dim3(64 * n_beams);
+    cfg.dynamicSmemBytes = (size_t)n_beams * a.nseg * n_out * 8;
     cfg.stream = s;
     KD_TRY(cudaLaunchKernelEx(&cfg, beam_merge_kernel, a));
     return KD_OK;

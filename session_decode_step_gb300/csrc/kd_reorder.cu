@@ -2,14 +2,18 @@
 //
 // dst_i := src_i for all i at once, the same slots on both sides (what a beam
 // selection asks for: beams trade places, some parents are taken several times,
-// some not at all).  Row t of one slot only ever depends on row t of others, so
-// a thread that owns one 16-byte piece of row t in every slot of a set of
-// connected moves can make them all without a second buffer: it loads before it
-// stores.  The host orders each connected set so that a slot is read before it
-// is overwritten; a set has at most one cycle (every destination has one
-// source), whose first overwritten piece is held in a register.
+// some not at all).  Byte x of one slot's (layer, head) slab only ever depends on
+// byte x of others, so a thread that owns one piece of the slab in every slot of
+// a set of connected moves can make them all without a second buffer: it loads
+// before it stores.  The host orders each connected set so that a slot is read
+// before it is overwritten; a set has at most one cycle (every destination has
+// one source), whose first overwritten piece is held in registers.
+//
 // No arithmetic: bound by HBM, one read per source row (a row taken several
-// times is read once per thread) and one write per destination row.
+// times comes from L1 the second time) and one write per destination row.  What
+// it takes is bytes in flight: a thread issues 8 loads of 16 bytes before it
+// waits for the first -- over 8 pieces of one move, 4 of two, 2 of four, or one
+// piece of eight moves, whichever fits the set.
 #include <cuda_runtime.h>
 
 #include "kd_device.cuh"
@@ -19,77 +23,113 @@
 namespace kd {
 
 constexpr int RO_THREADS = 256;
-constexpr int RO_BATCH = 8;  // moves whose pieces a thread holds at once
 
 struct ReorderMove {
-    int dst, src, len;  // src -1: the piece held from the cycle's first destination
-    int hold;           // hold the destination's old piece first
+    int dst, src;  // src -1: the piece held from the cycle's first destination
+    int lo, len;   // it moves rows t < len that are leading rows (t < sinks) or t >= lo
+    int hold;      // hold the destination's old piece first
 };
-struct ReorderSet {
-    int first, count;    // its moves
-    int row0;            // rows of the sets before it
-    int hi_a, lo_b;      // its rows: [0, hi_a), then lo_b, lo_b + 1, ...
+// One range of rows of one connected set: all leading rows, or none.
+struct ReorderRange {
+    int first, count;   // its set's moves
+    int lo, hi;         // rows [lo, hi)
+    int leading;
+    int tile0[4];       // tiles before it, per plane
 };
+// CAP: the most moves (a call's parameters are copied at every launch, so small
+// calls take the small form).
+template <int CAP>
 struct ReorderArgs {
     ReorderPlane plane[4];
-    int chunk0[4];  // first chunk (blockIdx.x) of each plane
-    int n_planes, slots, heads, cap, window, sinks;
-    int n_sets, rows;
-    ReorderSet set[KD_REORDER_MAX];
-    ReorderMove move[KD_REORDER_MAX];
+    int plane0[4];  // first tile (blockIdx.x) of each plane
+    int n_planes, slots, heads, cap;
+    int n_ranges, tiles;
+    ReorderRange range[2 * CAP];
+    ReorderMove move[CAP];
 };
-static_assert(sizeof(ReorderArgs) <= 4096, "kernel parameters");
 
-template <typename T>
-__device__ __forceinline__ void reorder_piece(const ReorderArgs& a, char* base, int row_bytes, int chunk, int lh) {
-    const int per_row = row_bytes / (int)sizeof(T);
-    const int v = chunk * RO_THREADS + threadIdx.x;
-    const int row = v / per_row;
-    if (row >= a.rows) return;
-    int c = 0;
-    while (c + 1 < a.n_sets && row >= a.set[c + 1].row0) ++c;
-    const ReorderSet s = a.set[c];
-    const int k = row - s.row0, t = k < s.hi_a ? k : s.lo_b + (k - s.hi_a);
-    const int layer = lh / a.heads, head = lh - layer * a.heads;
-    // the thread's piece of row t in slot 0
-    const size_t slot_bytes = (size_t)a.heads * a.cap * row_bytes;
-    char* p0 = base + (size_t)layer * a.slots * slot_bytes + ((size_t)head * a.cap + t) * row_bytes +
-               (size_t)(v - row * per_row) * sizeof(T);
-    T held{};
-    for (int m0 = 0; m0 < s.count; m0 += RO_BATCH) {
-        T x[RO_BATCH];
-        bool on[RO_BATCH];
+// Pieces of one move (P) that a thread holds at once, by the moves in the set.
+__host__ __device__ constexpr int reorder_pieces(int count) { return count == 1 ? 8 : count == 2 ? 4 : count <= 4 ? 2 : 1; }
+
+template <typename T, int MB, int P>
+__device__ __forceinline__ void reorder_tile(const ReorderMove* moves, const ReorderRange& s, char* slab, size_t slot_bytes,
+                                             int row_bytes, int x0) {
+    const int hi = s.hi * row_bytes;
+    // whether move m covers byte o of the slab
+    auto covers = [&](const ReorderMove& m, int o) {
+        return o >= (s.leading ? 0 : m.lo * row_bytes) && o < min(m.len * row_bytes, hi);
+    };
+    T held[P];
+    for (int m0 = 0; m0 < s.count; m0 += MB) {
+        T x[MB][P];
 #pragma unroll
-        for (int u = 0; u < RO_BATCH; ++u) {
-            on[u] = false;
+        for (int u = 0; u < MB; ++u)
             if (m0 + u < s.count) {
-                const ReorderMove m = a.move[s.first + m0 + u];
-                if (m.hold) held = *reinterpret_cast<const T*>(p0 + m.dst * slot_bytes);
-                on[u] = t < m.len && (!a.window || t < a.sinks || t > m.len - a.window);
-                if (on[u]) x[u] = m.src < 0 ? held : *reinterpret_cast<const T*>(p0 + m.src * slot_bytes);
-            }
-        }
+                const ReorderMove& m = moves[s.first + m0 + u];
 #pragma unroll
-        for (int u = 0; u < RO_BATCH; ++u)
-            if (on[u]) *reinterpret_cast<T*>(p0 + a.move[s.first + m0 + u].dst * slot_bytes) = x[u];
+                for (int j = 0; j < P; ++j) {
+                    const int o = x0 + j * RO_THREADS * (int)sizeof(T);
+                    if (MB > 1 && m.hold && o < hi) held[j] = *reinterpret_cast<const T*>(slab + m.dst * slot_bytes + o);
+                    if (covers(m, o)) {
+                        if (MB > 1 && m.src < 0)
+                            x[u][j] = held[j];
+                        else
+                            x[u][j] = *reinterpret_cast<const T*>(slab + m.src * slot_bytes + o);
+                    }
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < MB; ++u)
+            if (m0 + u < s.count) {
+                const ReorderMove& m = moves[s.first + m0 + u];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const int o = x0 + j * RO_THREADS * (int)sizeof(T);
+                    if (covers(m, o)) *reinterpret_cast<T*>(slab + m.dst * slot_bytes + o) = x[u][j];
+                }
+            }
     }
 }
 
-// Block (x, y): chunk x of the planes' row pieces, (layer, head) y.
-__global__ void __launch_bounds__(RO_THREADS) kv_reorder_kernel(const __grid_constant__ ReorderArgs a) {
-    int p = 0;
-    while (p + 1 < a.n_planes && (int)blockIdx.x >= a.chunk0[p + 1]) ++p;
-    const int chunk = (int)blockIdx.x - a.chunk0[p];
-    const ReorderPlane pl = a.plane[p];
-    if (pl.row_bytes % 16 == 0)
-        reorder_piece<uint4>(a, (char*)pl.base, pl.row_bytes, chunk, blockIdx.y);
+template <typename T>
+__device__ __forceinline__ void reorder_plane(const ReorderMove* moves, const ReorderRange& s, char* slab, size_t slot_bytes,
+                                              int row_bytes, int tile) {
+    const int P = reorder_pieces(s.count);
+    const int x0 = s.lo * row_bytes + (tile * P * RO_THREADS + (int)threadIdx.x) * (int)sizeof(T);
+    if (P == 8)
+        reorder_tile<T, 1, 8>(moves, s, slab, slot_bytes, row_bytes, x0);
+    else if (P == 4)
+        reorder_tile<T, 2, 4>(moves, s, slab, slot_bytes, row_bytes, x0);
+    else if (P == 2)
+        reorder_tile<T, 4, 2>(moves, s, slab, slot_bytes, row_bytes, x0);
     else
-        reorder_piece<uint2>(a, (char*)pl.base, pl.row_bytes, chunk, blockIdx.y);
+        reorder_tile<T, 8, 1>(moves, s, slab, slot_bytes, row_bytes, x0);
+}
+
+// Block (x, y): tile x of the planes' ranges, (layer, head) y.
+template <int CAP>
+__global__ void __launch_bounds__(RO_THREADS, 4) kv_reorder_kernel(const __grid_constant__ ReorderArgs<CAP> a) {
+    int p = 0;
+    while (p + 1 < a.n_planes && (int)blockIdx.x >= a.plane0[p + 1]) ++p;
+    const int t = (int)blockIdx.x - a.plane0[p];
+    int c = 0;
+    while (c + 1 < a.n_ranges && t >= a.range[c + 1].tile0[p]) ++c;
+    const ReorderRange& s = a.range[c];
+    const int row_bytes = a.plane[p].row_bytes;
+    const int layer = blockIdx.y / a.heads, head = blockIdx.y - layer * a.heads;
+    const size_t slab_bytes = (size_t)a.cap * row_bytes, slot_bytes = slab_bytes * a.heads;
+    char* slab = (char*)a.plane[p].base + (size_t)layer * a.slots * slot_bytes + head * slab_bytes;
+    if (row_bytes % 16 == 0)
+        reorder_plane<uint4>(a.move, s, slab, slot_bytes, row_bytes, t - s.tile0[p]);
+    else
+        reorder_plane<uint2>(a.move, s, slab, slot_bytes, row_bytes, t - s.tile0[p]);
 }
 
 // Order the moves into connected sets (see the file comment).
-static void plan_moves(const int32_t* dst, const int32_t* src, const int32_t* len, int n, ReorderArgs& a) {
-    constexpr int N = KD_REORDER_MAX;
+template <int CAP>
+static void plan_moves(const ReorderPlan& p, const int32_t* dst, const int32_t* src, const int32_t* len, int n,
+                       ReorderArgs<CAP>& a) {
+    constexpr int N = CAP;
     int id[N], m = 0;  // the moves that move something
     for (int i = 0; i < n; ++i)
         if (dst[i] != src[i] && len[i] > 0) id[m++] = i;
@@ -132,51 +172,57 @@ static void plan_moves(const int32_t* dst, const int32_t* src, const int32_t* le
             } while (j != i);
             from_held[last] = true;
         }
-    a.n_sets = 0;
-    a.rows = 0;
     int at = 0;
     for (int root = 0; root < m; ++root) {
         if (find(root) != root) continue;
-        ReorderSet& s = a.set[a.n_sets++];
-        s.first = at;
+        const int first = at;
         int hi = 0, lo = 0x7fffffff;
         for (int k = 0; k < no; ++k) {
             const int i = order[k];
             if (find(i) != root) continue;
-            const int l = len[id[i]];
-            a.move[at++] = {dst[id[i]], from_held[i] ? -1 : src[id[i]], l, hold[i]};
+            const int l = len[id[i]], b = p.window && l + 1 > p.window ? l + 1 - p.window : 0;
+            a.move[at++] = {dst[id[i]], from_held[i] ? -1 : src[id[i]], b, l, hold[i]};
             hi = l > hi ? l : hi;
-            const int b = a.window && l + 1 > a.window ? l + 1 - a.window : 0;
             lo = b < lo ? b : lo;
         }
-        s.count = at - s.first;
-        s.hi_a = a.sinks < lo ? a.sinks : lo;
-        s.lo_b = lo;
-        s.row0 = a.rows;
-        a.rows += s.hi_a + hi - lo;
+        // the leading rows, which every move keeps, then the windows from the first of them
+        const int lead = !p.window ? 0 : p.sinks < hi ? p.sinks : hi;
+        const int from = lead > lo ? lead : lo;
+        if (lead > 0) a.range[a.n_ranges++] = {first, at - first, 0, lead, 1, {}};
+        if (from < hi) a.range[a.n_ranges++] = {first, at - first, from, hi, 0, {}};
     }
 }
 
-cudaError_t launch_kv_reorder(const ReorderPlan& p, const int32_t* dst, const int32_t* src, const int32_t* len, int n,
-                              cudaStream_t s) {
-    ReorderArgs a{};
+template <int CAP>
+static cudaError_t launch_reorder(const ReorderPlan& p, const int32_t* dst, const int32_t* src, const int32_t* len, int n,
+                                  cudaStream_t s) {
+    ReorderArgs<CAP> a{};
     a.n_planes = p.n_planes;
     a.slots = p.slots;
     a.heads = p.heads;
     a.cap = p.cap;
-    a.window = p.window;
-    a.sinks = p.sinks;
-    plan_moves(dst, src, len, n, a);
-    if (a.rows == 0) return cudaSuccess;
-    int chunks = 0;
+    plan_moves(p, dst, src, len, n, a);
+    if (a.n_ranges == 0) return cudaSuccess;
     for (int i = 0; i < p.n_planes; ++i) {
         a.plane[i] = p.plane[i];
-        a.chunk0[i] = chunks;
-        const long pieces = (long)a.rows * (p.plane[i].row_bytes / (p.plane[i].row_bytes % 16 ? 8 : 16));
-        chunks += (int)((pieces + RO_THREADS - 1) / RO_THREADS);
+        a.plane0[i] = a.tiles;
+        int tiles = 0;
+        for (int c = 0; c < a.n_ranges; ++c) {
+            ReorderRange& r = a.range[c];
+            r.tile0[i] = tiles;
+            const int piece = p.plane[i].row_bytes % 16 ? 8 : 16;
+            const int tile = reorder_pieces(r.count) * RO_THREADS * piece;
+            tiles += ((r.hi - r.lo) * p.plane[i].row_bytes + tile - 1) / tile;
+        }
+        a.tiles += tiles;
     }
-    kv_reorder_kernel<<<dim3(chunks, p.layers * p.heads), RO_THREADS, 0, s>>>(a);
+    kv_reorder_kernel<CAP><<<dim3(a.tiles, p.layers * p.heads), RO_THREADS, 0, s>>>(a);
     return cudaGetLastError();
+}
+
+cudaError_t launch_kv_reorder(const ReorderPlan& p, const int32_t* dst, const int32_t* src, const int32_t* len, int n,
+                              cudaStream_t s) {
+    return n <= 16 ? launch_reorder<16>(p, dst, src, len, n, s) : launch_reorder<KD_REORDER_MAX>(p, dst, src, len, n, s);
 }
 
 }  // namespace kd

@@ -51,14 +51,21 @@ __host__ __device__ inline int win_max_items(int cap, int window, int sinks) {
 struct AttnWinArgs : AttnArgs {
     int window, sinks;  // window >= 1, sinks >= 0
     int vslot[16], vpos[16];
+    // Op-level calls: the split kernel appends the new rows itself.  The warp whose
+    // item ends in row b's new position converts the row (fp32 [B][nkv][hd]),
+    // writes it to the cache (fp16 rows, or Q8_0 quants and scales) and into its
+    // tile, whose copy may have read the old row.  nullptr: already appended.
+    const float *k_new, *v_new;
+    void *k_dst, *v_dst;
+    __half *ks_dst, *vs_dst;
+    // The call's fault word is its own: the split kernel clears it, marks the
+    // records of a CTA that gave up a wait, and the merge reports them (a word
+    // cleared and set by CTAs of one launch would depend on their order).
+    int clear_err;
 };
+// A record's third padding word marks it (0: valid).
+constexpr int REC_VALID = 0, REC_FAULT = 1;
 cudaError_t launch_attn_split(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s);
 cudaError_t launch_attn_split_q8(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s);
 cudaError_t launch_attn_combine(const AttnWinArgs& a, bool pdl, cudaStream_t s);
-// Append the new rows of a windowed call (slots and positions in a.vslot, a.vpos)
-// and clear its fault word a.err, in one launch: fp16 rows into kc, vc, or, with
-// ks and vs, Q8_0 rows (quants kc, vc; block scales ks, vs).
-cudaError_t launch_win_append(const AttnWinArgs& a, const float* k, const float* v, void* kc, void* vc, __half* ks,
-                              __half* vs, cudaStream_t s);
-
 }  // namespace kd

@@ -1,5 +1,6 @@
-// kd_window_api.cu -- the windowed attention's op-level entry points: KV append,
-// split attention over the leading and the last keys (kd_window.h), merge.
+// kd_window_api.cu -- the windowed attention's op-level entry points: KV append and
+// split attention over the leading and the last keys (kd_window.h) in one launch,
+// then the merge.
 // Slots and positions travel with the launches, so a call copies nothing to the
 // device and can be captured into a graph (they are then part of the graph).
 #include <cmath>
@@ -30,6 +31,7 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     if ((u16 & 15) || ((uintptr_t)q & 7))
         return failf(KD_ERR_INVALID_ARG, "%s: caches and workspace must be 16-byte aligned, q %d-byte", fn, q8 ? 16 : 8);
     AttnWinArgs t{};
+    int64_t items = 0;
     for (int b = 0; b < B; ++b) {
         if (slots[b] < 0 || slots[b] >= n_slots) return failf(KD_ERR_BAD_SESSION, "%s: slot %d", fn, slots[b]);
         for (int j = 0; j < b; ++j)
@@ -38,6 +40,7 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
             return failf(KD_ERR_POSITION, "%s: position %d outside [0, %d)", fn, positions[b], cap);
         t.vslot[b] = slots[b];
         t.vpos[b] = positions[b];
+        items += (int64_t)win_plan(positions[b], window, sinks).ns * nkv;
     }
     int dev = 0, sms = 0;
     KD_TRY(cudaGetDevice(&dev));
@@ -59,6 +62,13 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     t.vs = (const __half*)vs;
     t.window = window;
     t.sinks = sinks;
+    t.k_new = k_new;
+    t.v_new = v_new;
+    t.k_dst = kc;
+    t.v_dst = vc;
+    t.ks_dst = (__half*)ks;
+    t.vs_dst = (__half*)vs;
+    t.clear_err = 1;
     AttnMaps maps;
     const long rows = (long)n_slots * nkv * cap;
     if (q8) {
@@ -66,11 +76,13 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     } else {
         KD_TRY(make_attn_maps((const __half*)kc, (const __half*)vc, rows, hd, &maps));
     }
-    KD_TRY(launch_win_append(t, k_new, v_new, kc, vc, (__half*)ks, (__half*)vs, s));
+    // persistent CTAs, no more than there are items
+    const int per = q8 ? sms : attn_split_grid(sms, hd, nh / nkv);
+    const int grid = items < per ? (int)items : per;
     if (q8) {
-        KD_TRY(launch_attn_split_q8(t, maps, sms, true, s));
+        KD_TRY(launch_attn_split_q8(t, maps, grid, false, s));
     } else {
-        KD_TRY(launch_attn_split(t, maps, attn_split_grid(sms, hd, nh / nkv), true, s));
+        KD_TRY(launch_attn_split(t, maps, grid, false, s));
     }
     KD_TRY(launch_attn_combine(t, true, s));
     return KD_OK;

@@ -298,3 +298,32 @@ def test_model_window_steps(kdlib, name, flags):
     finally:
         kd.kd_model_free(m)
         kd.kd_model_free(plain)
+
+
+@pytest.mark.parametrize("name", ["hd64", "q8"])
+def test_window_wait_timeout_is_reported(kdlib, name):
+    """A bounded wait of the windowed attention made to run out: KD_ERR_DEVICE once, then correct steps again."""
+    kd = kdlib
+    shape = synth.TINY if name == "hd64" else synth.TINY_HD128
+    w = synth.model_weights(shape, 0)
+    m = kd.kd_model_load(kd.make_config(shape, 2, 256, kd.KD_FLAG_KV_Q8_0 if name == "q8" else 0), w)
+    try:
+        kd.kd_model_set_window(m, 70, 3)
+        sid = kd.kd_session_bind(m)
+        kd.kd_session_load_kv(m, sid, *synth.kv_prefill(shape, 0, 0, 150), 150)
+        lg = torch.empty(1, shape.vocab, device="cuda")
+
+        def step():
+            kd.kd_decode_step(m, [sid], [7], [150], lg, None)
+            torch.cuda.synchronize()
+            return lg.cpu().numpy().copy()
+        want = step()
+        kd.kd_debug_inject_wait_timeout(m, "attn_split")
+        step()
+        with pytest.raises(kd.KdError) as e:
+            kd.kd_device_status(m)
+        assert e.value.name == "KD_ERR_DEVICE"
+        assert np.array_equal(step(), want)
+        assert kd.kd_device_status(m) == 0
+    finally:
+        kd.kd_model_free(m)
