@@ -11,11 +11,12 @@
 // segment's K best logits, sorted.  A second kernel, one CTA per group, forms
 // L_w, merges each row's lists, and merges the rows by s.
 //
-// The selection costs next to nothing once a warp knows K candidates: a block
-// whose largest logit does not exceed the warp's K-th best is passed over, so a
-// random row brings about K ln(blocks) late candidates.  The first block's are
-// found through the lanes' own maxima: the K-th largest of them bounds the K-th
-// largest logit from below, and few logits lie above it.
+// The selection costs next to nothing once K candidates are known: a block whose
+// largest logit does not exceed the K-th best so far is passed over, so a random
+// row brings about K ln(blocks) late candidates.  The first block's are found
+// through the threads' own maxima: the K-th largest of the 256 bounds the K-th
+// largest logit from below, and few logits lie above it.  The warps keep their
+// candidates apart and agree on a new bound after 4, 16 and 64 blocks.
 //
 // s decides between rows, where two candidates can lie as close as fp32 rounds:
 // L_w's last steps and s are fp64 (a handful of operations per row); the sums of
@@ -75,6 +76,27 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 constexpr float LOG2E = 1.44269504088896341f;
+// Pairs of fp32 in a 64-bit register.
+__device__ __forceinline__ unsigned long long pack2(float x, float y) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 // A beam's row is read only if the beam can continue: not finished, score > -inf (a NaN score is dead too).
 __device__ __forceinline__ bool beam_live(const float* scores, const int* done, int r) {
@@ -116,7 +138,7 @@ __device__ __forceinline__ void beam_load(const float* p, int n, int t, float (&
     }
 }
 
-// The warp's candidates, sorted and cut to the K best; returns their number.
+// The warp's candidates, sorted and cut to the K best, then zeros up to 32; returns their number.
 __device__ __forceinline__ int beam_compact(unsigned long long* buf, unsigned long long* best, int n, int K, int lane) {
     __syncwarp();
     for (int q = lane; q < n; q += 32) {
@@ -127,9 +149,26 @@ __device__ __forceinline__ int beam_compact(unsigned long long* buf, unsigned lo
     }
     __syncwarp();
     const int c = min(n, K);
-    if (lane < c) buf[lane] = best[lane];
+    buf[lane] = lane < c ? best[lane] : 0ull;
     __syncwarp();
     return c;
+}
+
+// Rank of key k, at place `lane` of its own warp's sorted 32, among all warps' lists (list w at lists + w * stride).
+__device__ __forceinline__ int beam_rank(const unsigned long long* lists, int stride, unsigned long long k, int warp,
+                                         int lane) {
+    int rank = lane;
+#pragma unroll
+    for (int w = 0; w < BS_WARPS; ++w) {
+        if (w == warp) continue;
+        const unsigned long long* l = lists + w * stride;
+        int c = 0;  // larger keys, found by halving
+#pragma unroll
+        for (int h = 16; h > 0; h >>= 1)
+            if (l[c + h - 1] > k) c += h;
+        rank += c + (l[c] > k ? 1 : 0);
+    }
+    return rank;
 }
 
 template <bool VEC>
@@ -138,6 +177,7 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
     __shared__ unsigned long long best[BS_WARPS][BS_MAX_OUT];
     __shared__ float2 wpart[BS_MAX_BLOCKS][BS_WARPS];
     __shared__ int count[BS_WARPS];
+    __shared__ unsigned long long bound;  // the K-th best key known to all warps (0: fewer than K)
     pdl_launch_dependents();
     const int r = blockIdx.y, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     if (!beam_live(a.scores, a.done, r)) return;
@@ -145,9 +185,11 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
     const float* row = a.logits + (size_t)r * a.ld;
     unsigned long long* buf = cand[warp];
     int cnt = 0;
-    float thr = -INFINITY;  // the warp's K-th best once it has K: later equals lose to it (higher indices)
+    float thr = -INFINITY;  // a K-th best: later equals lose to it (higher indices)
     float nx[BS_VPT];
     beam_load<VEC>(row + (size_t)b0 * BS_BLOCK, a.V - b0 * BS_BLOCK, t, nx);
+    if (t == 0) bound = 0ull;
+#pragma unroll 2
     for (int b = 0; b < nb; ++b) {
         const int e0 = (b0 + b) * BS_BLOCK;
         float x[BS_VPT];
@@ -157,13 +199,18 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
         float m = x[0];
 #pragma unroll
         for (int i = 1; i < BS_VPT; ++i) m = fmaxf(m, x[i]);
-        float s0 = 0.0f, s1 = 0.0f;
+        float s;
+        {  // two logits per instruction (packed fp32 adds and products)
+            const unsigned long long nm = pack2(-m, -m), l2 = pack2(LOG2E, LOG2E);
+            unsigned long long acc = 0ull;
 #pragma unroll
-        for (int i = 0; i < BS_VPT; i += 2) {
-            s0 += ex2((x[i] - m) * LOG2E);
-            s1 += ex2((x[i + 1] - m) * LOG2E);
+            for (int i = 0; i < BS_VPT; i += 2) {
+                const float2 d = unpack2(mul2(add2(pack2(x[i], x[i + 1]), nm), l2));
+                acc = add2(acc, pack2(ex2(d.x), ex2(d.y)));
+            }
+            const float2 v = unpack2(acc);
+            s = v.x + v.y;
         }
-        float s = s0 + s1;
         if (s != s) {  // a NaN, or the largest is infinite: NaN counts as -inf, x - m as 0 where x == m
             m = -INFINITY;
 #pragma unroll
@@ -182,12 +229,39 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(FULL_MASK, s, o);
         if (lane == 0) wpart[b][warp] = make_float2(mw, s);
 
-        const unsigned hot = __ballot_sync(FULL_MASK, m > thr);
-        if (hot) {
-            float lo = beam_unord(beam_ord(thr) + 1u);  // the next value above: x >= lo is x > thr
-            if (__popc(hot) >= K) {  // at least K logits are no less than the K-th largest lane maximum
-                int rank = 0;
+        unsigned long long floor_key = 0ull;  // candidates of the first block: keys no less than this
+        if (b == 0) {
+            // the thread's largest key and its place in the warp; the K-th largest of all threads'
+            int at = BS_VPT - 1;
 #pragma unroll
+            for (int i = BS_VPT - 2; i >= 0; --i) at = x[i] == m ? i : at;
+            const unsigned long long k =
+                m > -INFINITY ? beam_key(m, e0 + (at >> 2) * 4 * BS_THREADS + 4 * t + (at & 3)) : 0ull;
+            best[warp][lane] = k;
+            __syncwarp();
+            int rank = 0;
+#pragma unroll 8
+            for (int j = 0; j < 32; ++j) {
+                const unsigned long long o = best[warp][j];
+                rank += o > k || (o == k && j < lane) ? 1 : 0;
+            }
+            __syncwarp();
+            best[warp][rank] = k;
+            __syncwarp();
+            const unsigned long long sk = best[warp][lane];
+            __syncthreads();
+            if (sk && beam_rank(best[0], BS_MAX_OUT, sk, warp, lane) == K - 1) bound = sk;
+            __syncthreads();
+            floor_key = bound;
+            thr = floor_key ? beam_key_x(floor_key) : -INFINITY;
+        }
+        const unsigned hot = __ballot_sync(FULL_MASK, floor_key ? m >= thr : m > thr);
+        if (hot) {
+            // x >= lo: x > thr, by the next value above; in the first block x >= thr
+            float lo = floor_key ? thr : beam_unord(beam_ord(thr) + 1u);
+            if (b > 0 && __popc(hot) >= K) {  // at least K logits are no less than the K-th largest lane maximum
+                int rank = 0;
+#pragma unroll 4
                 for (int j = 0; j < 32; ++j) {
                     const float o = __shfl_sync(FULL_MASK, m, j);
                     rank += o > m || (o == m && j < lane) ? 1 : 0;
@@ -196,39 +270,35 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
             }
 #pragma unroll
             for (int i = 0; i < BS_VPT; ++i) {
-                const unsigned who = __ballot_sync(FULL_MASK, x[i] >= lo);
-                if (who) {
-                    if (x[i] >= lo)
-                        buf[cnt + __popc(who & ((1u << lane) - 1u))] =
-                            beam_key(x[i], e0 + (i >> 2) * 4 * BS_THREADS + 4 * t + (i & 3));
-                    cnt += __popc(who);
-                }
+                if (!__any_sync(FULL_MASK, x[i] >= lo)) continue;
+                const unsigned long long k = beam_key(x[i], e0 + (i >> 2) * 4 * BS_THREADS + 4 * t + (i & 3));
+                const bool in = x[i] >= lo && k >= floor_key;
+                const unsigned who = __ballot_sync(FULL_MASK, in);
+                if (in) buf[cnt + __popc(who & ((1u << lane) - 1u))] = k;
+                cnt += __popc(who);
             }
-            if (cnt >= K && (thr == -INFINITY || cnt >= K + 24)) {
+            if (cnt > K + 24) {
                 cnt = beam_compact(buf, best[warp], cnt, K, lane);
-                thr = beam_key_x(buf[K - 1]);
+                thr = fmaxf(thr, beam_key_x(buf[K - 1]));
             }
+        }
+        if ((b == 3 || b == 15 || b == 63) && b + 1 < nb) {  // a new common bound after 4, 16, 64 blocks
+            cnt = beam_compact(buf, best[warp], cnt, K, lane);
+            __syncthreads();
+            const unsigned long long k = buf[lane];
+            if (k && beam_rank(cand[0], BS_CAP, k, warp, lane) == K - 1) bound = k;
+            __syncthreads();
+            if (bound) thr = fmaxf(thr, beam_key_x(bound));
         }
     }
     cnt = beam_compact(buf, best[warp], cnt, K, lane);
-    if (lane >= cnt) buf[lane] = 0ull;
     if (lane == 0) count[warp] = cnt;
     __syncthreads();
-    // the warps' sorted lists into the segment's: a key's rank is its own place plus the larger keys of the others
+    // the warps' sorted lists into the segment's
     unsigned long long* out = a.keys + ((size_t)r * a.nseg + blockIdx.x) * K;
     if (lane < cnt) {
         const unsigned long long k = buf[lane];
-        int rank = lane;
-#pragma unroll
-        for (int w = 0; w < BS_WARPS; ++w) {
-            if (w == warp) continue;
-            int c = 0;  // larger keys in cand[w][0..31], found by halving
-#pragma unroll
-            for (int h = 16; h > 0; h >>= 1)
-                if (cand[w][c + h - 1] > k) c += h;
-            if (cand[w][c] > k) ++c;
-            rank += c;
-        }
+        const int rank = beam_rank(cand[0], BS_CAP, k, warp, lane);
         if (rank < K) out[rank] = k;
     }
     int total = 0;
@@ -254,6 +324,7 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
     extern __shared__ unsigned long long staged[];  // [W][nseg][K] the rows' lists
     __shared__ unsigned long long row_key[KD_BEAM_MAX_BEAMS][BS_MAX_OUT];
     __shared__ double row_s[KD_BEAM_MAX_BEAMS][BS_MAX_OUT];
+    __shared__ unsigned long long row_o[KD_BEAM_MAX_BEAMS][BS_MAX_OUT + 2];  // row_s as order-preserving keys, 0-padded
     __shared__ double row_lg[KD_BEAM_MAX_BEAMS];
     __shared__ float row_m[KD_BEAM_MAX_BEAMS];
     __shared__ int row_n[KD_BEAM_MAX_BEAMS];
@@ -292,17 +363,19 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
         unsigned long long* st = staged + (size_t)w * a.nseg * K;
         for (int i = lane; i < a.nseg * K; i += 32) st[i] = __ldcg(lists + i);
         __syncwarp();
-        // lane l holds the head of list l
+        // lane l holds the head of list l and the entry after it
         const unsigned long long* at = st + lane * K;
-        const unsigned long long* end = at + K;
-        unsigned long long head = lane < a.nseg ? *at : 0ull;
-        int n = 0;
+        const int have = lane < a.nseg ? K : 0;
+        unsigned long long head = have > 0 ? at[0] : 0ull, after = have > 1 ? at[1] : 0ull;
+        int n = 0, next = 2;
         for (; n < K; ++n) {
             const unsigned who = warp_best(head);
             if (!who) break;
             if ((who >> lane) & 1u) {
                 row_key[w][n] = head;
-                head = ++at < end ? *at : 0ull;
+                head = after;
+                after = next < have ? at[next] : 0ull;
+                ++next;
             }
         }
         if (lane == 0) row_n[w] = n;
@@ -313,30 +386,37 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
         row_s[w][0] = (double)score;
     }
     __syncthreads();
-    if (warp < a.W && live && lane < row_n[w]) {
-        const float xv = beam_key_x(row_key[w][lane]), M = row_m[w];
-        // x == M first: M may be infinite
-        row_s[w][lane] = (double)score + ((xv == M ? 0.0 : (double)xv - (double)M) - row_lg[w]);
+    if (warp < a.W) {
+        unsigned long long o = 0ull;
+        if (lane < row_n[w]) {
+            if (live) {
+                const float xv = beam_key_x(row_key[w][lane]), M = row_m[w];
+                // x == M first: M may be infinite
+                row_s[w][lane] = (double)score + ((xv == M ? 0.0 : (double)xv - (double)M) - row_lg[w]);
+            }
+            const double v = row_s[w][lane] + 0.0;  // -inf and NaN never win
+            const unsigned long long u = (unsigned long long)__double_as_longlong(v);
+            o = !(v > -INFINITY) ? 0ull : (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+        }
+        row_o[w][lane] = o;
+        if (lane < 2) row_o[w][BS_MAX_OUT + lane] = 0ull;
     }
     __syncthreads();
     if (warp) return;
     // Lane w holds the head of beam w's list; larger s first, then the lower beam.
-    const int cnt = lane < a.W ? row_n[lane] : 0;
-    // an order-preserving key of s; -inf and NaN never win
-    auto skey = [&](int pos) -> unsigned long long {
-        if (pos >= cnt) return 0ull;
-        const double v = row_s[lane][pos] + 0.0;
-        const unsigned long long u = (unsigned long long)__double_as_longlong(v);
-        return !(v > -INFINITY) ? 0ull : (u >> 63) ? ~u : (u | 0x8000000000000000ull);
-    };
+    const unsigned long long* mine_o = row_o[lane < a.W ? lane : 0];
+    unsigned long long key = lane < a.W ? mine_o[0] : 0ull, after = lane < a.W ? mine_o[1] : 0ull;
     int pos = 0, mine = -1;  // mine: the winner (beam, place) of output `lane`
-    unsigned long long key = skey(0);
     for (int j = 0; j < K; ++j) {
         const unsigned who = warp_best(key);
         if (!who) break;
         const int win = __ffs(who) - 1, wp = __shfl_sync(FULL_MASK, pos, win);
         if (lane == j) mine = win * BS_MAX_OUT + wp;
-        if (lane == win) key = skey(++pos);
+        if (lane == win) {
+            key = after;
+            ++pos;
+            after = mine_o[min(pos + 1, BS_MAX_OUT + 1)];
+        }
     }
     if (lane < K) {
         const int o = g * K + lane;

@@ -5,15 +5,16 @@
 // some not at all).  Byte x of one slot's (layer, head) slab only ever depends on
 // byte x of others, so a thread that owns one piece of the slab in every slot of
 // a set of connected moves can make them all without a second buffer: it loads
-// before it stores.  The host orders each connected set so that a slot is read
-// before it is overwritten; a set has at most one cycle (every destination has
-// one source), whose first overwritten piece is held in registers.
+// before it stores.  Sets of up to four moves are loaded whole; for larger ones,
+// taken four moves at a time, the host orders the moves so that a slot is read
+// before it is overwritten, and as a set has at most one cycle (every destination
+// has one source), one overwritten piece held in a register is enough.
 //
 // No arithmetic: bound by HBM, one read per source row (a row taken several
 // times comes from L1 the second time) and one write per destination row.  What
 // it takes is bytes in flight: a thread issues 8 loads of 16 bytes before it
-// waits for the first -- over 8 pieces of one move, 4 of two, 2 of four, or one
-// piece of eight moves, whichever fits the set.
+// waits for the first -- over 8 pieces of one move, 4 of two, or 2 of four moves
+// at a time, whichever fits the set.
 #include <cuda_runtime.h>
 
 #include "kd_device.cuh"
@@ -23,6 +24,7 @@
 namespace kd {
 
 constexpr int RO_THREADS = 256;
+constexpr int RO_FULL = 3 * 152;  // blocks resident at once (3 per SM)
 
 struct ReorderMove {
     int dst, src;  // src -1: the piece held from the cycle's first destination
@@ -33,96 +35,122 @@ struct ReorderMove {
 struct ReorderRange {
     int first, count;   // its set's moves
     int lo, hi;         // rows [lo, hi)
-    int leading;
-    int tile0[4];       // tiles before it, per plane
+    int all_lo, all_hi; // of these, the rows that every move of the set covers
+    int leading, kind;
+    int run0[4];        // runs of tiles before it, per plane
 };
 // CAP: the most moves (a call's parameters are copied at every launch, so small
 // calls take the small form).
 template <int CAP>
 struct ReorderArgs {
     ReorderPlane plane[4];
-    int plane0[4];  // first tile (blockIdx.x) of each plane
+    int plane0[4];  // first run (blockIdx.x) of each plane
     int n_planes, slots, heads, cap;
-    int n_ranges, tiles;
+    int n_ranges, runs;
+    int run;        // consecutive tiles a block makes
     ReorderRange range[2 * CAP];
     ReorderMove move[CAP];
 };
 
-// Pieces of one move (P) that a thread holds at once, by the moves in the set.
-__host__ __device__ constexpr int reorder_pieces(int count) { return count == 1 ? 8 : count == 2 ? 4 : count <= 4 ? 2 : 1; }
+// How a set's moves are taken: MB at a time, P pieces of each.
+enum ReorderKind : int { RO_ONE, RO_TWO, RO_FOUR, RO_CYCLE };  // (1, 8), (2, 4), (4, 2), (4, 1) with a held piece
+__host__ __device__ constexpr int reorder_pieces(int kind) {
+    return kind == RO_ONE ? 8 : kind == RO_TWO ? 4 : kind == RO_FOUR ? 2 : 1;
+}
 
-template <typename T, int MB, int P>
+// One tile of a range: pieces x0, x0 + stride, ... of the slab.  ALL: every move
+// covers all of them (almost every tile), so nothing is compared.
+template <typename T, int MB, int P, bool CYC, bool ALL>
 __device__ __forceinline__ void reorder_tile(const ReorderMove* moves, const ReorderRange& s, char* slab, size_t slot_bytes,
                                              int row_bytes, int x0) {
+    constexpr int STRIDE = RO_THREADS * (int)sizeof(T);
     const int hi = s.hi * row_bytes;
-    // whether move m covers byte o of the slab
     auto covers = [&](const ReorderMove& m, int o) {
-        return o >= (s.leading ? 0 : m.lo * row_bytes) && o < min(m.len * row_bytes, hi);
+        return ALL || (o >= (s.leading ? 0 : m.lo * row_bytes) && o < min(m.len * row_bytes, hi));
     };
-    T held[P];
+    slab += x0;
+    T held[P] = {};
+#pragma unroll 1
     for (int m0 = 0; m0 < s.count; m0 += MB) {
         T x[MB][P];
 #pragma unroll
         for (int u = 0; u < MB; ++u)
             if (m0 + u < s.count) {
                 const ReorderMove& m = moves[s.first + m0 + u];
+                const char* src = slab + m.src * slot_bytes;
+                if (CYC && m.hold) {
 #pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const int o = x0 + j * RO_THREADS * (int)sizeof(T);
-                    if (MB > 1 && m.hold && o < hi) held[j] = *reinterpret_cast<const T*>(slab + m.dst * slot_bytes + o);
-                    if (covers(m, o)) {
-                        if (MB > 1 && m.src < 0)
-                            x[u][j] = held[j];
-                        else
-                            x[u][j] = *reinterpret_cast<const T*>(slab + m.src * slot_bytes + o);
-                    }
+                    for (int j = 0; j < P; ++j)
+                        if (ALL || x0 + j * STRIDE < hi)
+                            held[j] = *reinterpret_cast<const T*>(slab + m.dst * slot_bytes + j * STRIDE);
+                }
+                if (CYC && m.src < 0) {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) x[u][j] = held[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < P; ++j)
+                        if (covers(m, x0 + j * STRIDE)) x[u][j] = *reinterpret_cast<const T*>(src + j * STRIDE);
                 }
             }
 #pragma unroll
         for (int u = 0; u < MB; ++u)
             if (m0 + u < s.count) {
                 const ReorderMove& m = moves[s.first + m0 + u];
+                char* dst = slab + m.dst * slot_bytes;
 #pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const int o = x0 + j * RO_THREADS * (int)sizeof(T);
-                    if (covers(m, o)) *reinterpret_cast<T*>(slab + m.dst * slot_bytes + o) = x[u][j];
-                }
+                for (int j = 0; j < P; ++j)
+                    if (covers(m, x0 + j * STRIDE)) *reinterpret_cast<T*>(dst + j * STRIDE) = x[u][j];
             }
+    }
+}
+
+template <typename T, int MB, int P, bool CYC>
+__device__ __forceinline__ void reorder_run(const ReorderMove* moves, const ReorderRange& s, char* slab, size_t slot_bytes,
+                                            int row_bytes, int tile, int tiles) {
+    constexpr int TILE = P * RO_THREADS * (int)sizeof(T);
+#pragma unroll 1
+    for (int k = 0; k < tiles; ++k) {
+        const int t0 = s.lo * row_bytes + (tile + k) * TILE, x0 = t0 + (int)threadIdx.x * (int)sizeof(T);
+        if (t0 >= s.hi * row_bytes) return;
+        if (t0 >= s.all_lo * row_bytes && t0 + TILE <= s.all_hi * row_bytes)
+            reorder_tile<T, MB, P, CYC, true>(moves, s, slab, slot_bytes, row_bytes, x0);
+        else
+            reorder_tile<T, MB, P, CYC, false>(moves, s, slab, slot_bytes, row_bytes, x0);
     }
 }
 
 template <typename T>
 __device__ __forceinline__ void reorder_plane(const ReorderMove* moves, const ReorderRange& s, char* slab, size_t slot_bytes,
-                                              int row_bytes, int tile) {
-    const int P = reorder_pieces(s.count);
-    const int x0 = s.lo * row_bytes + (tile * P * RO_THREADS + (int)threadIdx.x) * (int)sizeof(T);
-    if (P == 8)
-        reorder_tile<T, 1, 8>(moves, s, slab, slot_bytes, row_bytes, x0);
-    else if (P == 4)
-        reorder_tile<T, 2, 4>(moves, s, slab, slot_bytes, row_bytes, x0);
-    else if (P == 2)
-        reorder_tile<T, 4, 2>(moves, s, slab, slot_bytes, row_bytes, x0);
+                                              int row_bytes, int tile, int tiles) {
+    if (s.kind == RO_ONE)
+        reorder_run<T, 1, 8, false>(moves, s, slab, slot_bytes, row_bytes, tile, tiles);
+    else if (s.kind == RO_TWO)
+        reorder_run<T, 2, 4, false>(moves, s, slab, slot_bytes, row_bytes, tile, tiles);
+    else if (s.kind == RO_FOUR)
+        reorder_run<T, 4, 2, false>(moves, s, slab, slot_bytes, row_bytes, tile, tiles);
     else
-        reorder_tile<T, 8, 1>(moves, s, slab, slot_bytes, row_bytes, x0);
+        reorder_run<T, 4, 1, true>(moves, s, slab, slot_bytes, row_bytes, tile, tiles);
 }
 
-// Block (x, y): tile x of the planes' ranges, (layer, head) y.
+// Block (x, y): run x of the planes' ranges' tiles, (layer, head) y.
 template <int CAP>
-__global__ void __launch_bounds__(RO_THREADS, 4) kv_reorder_kernel(const __grid_constant__ ReorderArgs<CAP> a) {
+__global__ void __launch_bounds__(RO_THREADS, 3) kv_reorder_kernel(const __grid_constant__ ReorderArgs<CAP> a) {
     int p = 0;
     while (p + 1 < a.n_planes && (int)blockIdx.x >= a.plane0[p + 1]) ++p;
     const int t = (int)blockIdx.x - a.plane0[p];
     int c = 0;
-    while (c + 1 < a.n_ranges && t >= a.range[c + 1].tile0[p]) ++c;
+    while (c + 1 < a.n_ranges && t >= a.range[c + 1].run0[p]) ++c;
     const ReorderRange& s = a.range[c];
     const int row_bytes = a.plane[p].row_bytes;
     const int layer = blockIdx.y / a.heads, head = blockIdx.y - layer * a.heads;
     const size_t slab_bytes = (size_t)a.cap * row_bytes, slot_bytes = slab_bytes * a.heads;
     char* slab = (char*)a.plane[p].base + (size_t)layer * a.slots * slot_bytes + head * slab_bytes;
+    const int tile = (t - s.run0[p]) * a.run;
     if (row_bytes % 16 == 0)
-        reorder_plane<uint4>(a.move, s, slab, slot_bytes, row_bytes, t - s.tile0[p]);
+        reorder_plane<uint4>(a.move, s, slab, slot_bytes, row_bytes, tile, a.run);
     else
-        reorder_plane<uint2>(a.move, s, slab, slot_bytes, row_bytes, t - s.tile0[p]);
+        reorder_plane<uint2>(a.move, s, slab, slot_bytes, row_bytes, tile, a.run);
 }
 
 // Order the moves into connected sets (see the file comment).
@@ -176,20 +204,31 @@ static void plan_moves(const ReorderPlan& p, const int32_t* dst, const int32_t* 
     for (int root = 0; root < m; ++root) {
         if (find(root) != root) continue;
         const int first = at;
-        int hi = 0, lo = 0x7fffffff;
+        int count = 0;
+        bool cycle = false;
+        for (int k = 0; k < no; ++k)
+            if (find(order[k]) == root) {
+                ++count;
+                cycle = cycle || hold[order[k]];
+            }
+        cycle = cycle && count > 4;  // up to four moves are loaded before the first is stored
+        const int kind = cycle ? RO_CYCLE : count == 1 ? RO_ONE : count == 2 ? RO_TWO : RO_FOUR;
+        int hi = 0, lo = 0x7fffffff, all_hi = 0x7fffffff, all_lo = 0;
         for (int k = 0; k < no; ++k) {
             const int i = order[k];
             if (find(i) != root) continue;
             const int l = len[id[i]], b = p.window && l + 1 > p.window ? l + 1 - p.window : 0;
-            a.move[at++] = {dst[id[i]], from_held[i] ? -1 : src[id[i]], b, l, hold[i]};
+            a.move[at++] = {dst[id[i]], cycle && from_held[i] ? -1 : src[id[i]], b, l, cycle && hold[i]};
             hi = l > hi ? l : hi;
             lo = b < lo ? b : lo;
+            all_hi = l < all_hi ? l : all_hi;
+            all_lo = b > all_lo ? b : all_lo;
         }
         // the leading rows, which every move keeps, then the windows from the first of them
         const int lead = !p.window ? 0 : p.sinks < hi ? p.sinks : hi;
         const int from = lead > lo ? lead : lo;
-        if (lead > 0) a.range[a.n_ranges++] = {first, at - first, 0, lead, 1, {}};
-        if (from < hi) a.range[a.n_ranges++] = {first, at - first, from, hi, 0, {}};
+        if (lead > 0) a.range[a.n_ranges++] = {first, count, 0, lead, 0, lead < all_hi ? lead : all_hi, 1, kind, {}};
+        if (from < hi) a.range[a.n_ranges++] = {first, count, from, hi, all_lo, all_hi, 0, kind, {}};
     }
 }
 
@@ -203,20 +242,28 @@ static cudaError_t launch_reorder(const ReorderPlan& p, const int32_t* dst, cons
     a.cap = p.cap;
     plan_moves(p, dst, src, len, n, a);
     if (a.n_ranges == 0) return cudaSuccess;
+    // Tiles of a range on a plane, and how many a block makes in a row: several once
+    // the blocks fill the GPU a few times over (they share the block's set-up).
+    auto tiles_of = [&](const ReorderRange& r, int row_bytes) -> long {
+        const int tile = reorder_pieces(r.kind) * RO_THREADS * (row_bytes % 16 ? 8 : 16);
+        return ((r.hi - r.lo) * row_bytes + tile - 1) / tile;
+    };
+    long total = 0;
+    for (int i = 0; i < p.n_planes; ++i)
+        for (int c = 0; c < a.n_ranges; ++c) total += tiles_of(a.range[c], p.plane[i].row_bytes);
+    total *= p.layers * p.heads;
+    a.run = total >= 16L * RO_FULL ? 4 : total >= 8L * RO_FULL ? 2 : 1;
     for (int i = 0; i < p.n_planes; ++i) {
         a.plane[i] = p.plane[i];
-        a.plane0[i] = a.tiles;
-        int tiles = 0;
+        a.plane0[i] = a.runs;
+        int runs = 0;
         for (int c = 0; c < a.n_ranges; ++c) {
-            ReorderRange& r = a.range[c];
-            r.tile0[i] = tiles;
-            const int piece = p.plane[i].row_bytes % 16 ? 8 : 16;
-            const int tile = reorder_pieces(r.count) * RO_THREADS * piece;
-            tiles += ((r.hi - r.lo) * p.plane[i].row_bytes + tile - 1) / tile;
+            a.range[c].run0[i] = runs;
+            runs += (int)((tiles_of(a.range[c], p.plane[i].row_bytes) + a.run - 1) / a.run);
         }
-        a.tiles += tiles;
+        a.runs += runs;
     }
-    kv_reorder_kernel<CAP><<<dim3(a.tiles, p.layers * p.heads), RO_THREADS, 0, s>>>(a);
+    kv_reorder_kernel<CAP><<<dim3(a.runs, p.layers * p.heads), RO_THREADS, 0, s>>>(a);
     return cudaGetLastError();
 }
 
