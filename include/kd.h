@@ -511,9 +511,9 @@ size_t kd_beam_workspace_bytes(int32_t n_groups, int32_t n_beams, int32_t V, int
  * (x - max taken as 0 where x equals the row's maximum, so infinite logits share
  * the row's mass).  NaN and -inf logits are no candidates and add nothing to the
  * sum.  A beam whose score is -inf or NaN offers nothing, and its logits are not
- * read (so a search starts with one beam at 0 and the others at -inf); a finished
+ * used (so a search starts with one beam at 0 and the others at -inf); a finished
  * beam (done[r] != 0) offers itself alone: token eos at s = scores[r], its logits
- * not read either.
+ * not used either.
  * The best come first: larger s, then the lower beam, then (within a beam) the
  * larger logit, then the lower token.  s is ordered in fp64 (the row sums are
  * good to about 1e-8) and stored as fp32; a row's s does not depend on the batch.

@@ -14,15 +14,18 @@
 // The selection costs next to nothing once K candidates are known: a block whose
 // largest logit does not exceed the K-th best so far is passed over, so a random
 // row brings about K ln(blocks) late candidates.  The first block's are found
-// through the threads' own maxima: the K-th largest of the 256 bounds the K-th
-// largest logit from below, and few logits lie above it.  The warps keep their
-// candidates apart and agree on a new bound after 4, 16 and 64 blocks.
+// through the maxima of 32 subsets of it: the K-th largest of them bounds the
+// K-th largest logit from below, and few logits lie above it (K = 4: 4.3 of 4096
+// on average, 8: 9, 32: 130).  The warps keep their candidates apart and agree on
+// a new bound after 4, 16 and 64 blocks.
 //
 // s decides between rows, where two candidates can lie as close as fp32 rounds:
-// L_w's last steps and s are fp64 (a handful of operations per row); the sums of
-// exponentials are fp32 inside a block, in an order that depends on nothing but
-// the block, and exact 64-bit fixed point across blocks.  So a row's result does
-// not depend on the segments, hence not on the rest of the batch.
+// L_w's last steps and s are pairs of fp32 whose sum carries about 48 bits (fp64
+// instructions are so slow here that three of them per candidate took 20000
+// cycles of a CTA).  The sums of exponentials are fp32 inside a block, in an order
+// that depends on nothing but the block, and exact 64-bit fixed point across
+// blocks.  So a row's result does not depend on the segments, hence not on the
+// rest of the batch.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -39,8 +42,8 @@ constexpr int BS_BLOCK = BS_THREADS * BS_VPT;   // logits per block
 constexpr int BS_MAX_BLOCKS = 128;              // vocabulary up to 524288
 constexpr int BS_MAX_SEGS = 32;                 // segments (lists) per row: one per lane of the merge
 constexpr int BS_MAX_OUT = 32;
-// A warp's candidates: up to 2 K kept, and at most all 512 of a block on top.
-constexpr int BS_CAP = 2 * BS_MAX_OUT + 32 * BS_VPT;
+constexpr int BS_CAP = 128;                     // a warp's candidates between cuts to the K best
+constexpr int BS_STAGES = 2;                    // blocks in flight behind the one being worked on
 static_assert(KD_BEAM_MAX_VOCAB == BS_BLOCK * BS_MAX_BLOCKS && KD_BEAM_MAX_OUT == BS_MAX_OUT, "kd.h limits");
 
 // (x, index) as a 64-bit key whose unsigned order is: larger x, then lower index
@@ -58,16 +61,83 @@ __device__ __forceinline__ unsigned long long beam_key(float x, int i) {
 __device__ __forceinline__ float beam_key_x(unsigned long long k) { return beam_unord((unsigned)(k >> 32)); }
 __device__ __forceinline__ int beam_key_i(unsigned long long k) { return (int)~(unsigned)k; }
 
-// The lanes holding the warp's largest key: by high words, then, among equals, low words.  0: no lane holds one.
-__device__ __forceinline__ unsigned warp_best(unsigned long long k) {
-    const unsigned hi = (unsigned)(k >> 32), mh = __reduce_max_sync(FULL_MASK, hi);
-    if (mh == 0) return 0u;
-    unsigned who = __ballot_sync(FULL_MASK, hi == mh);
-    if (who & (who - 1)) {
-        const unsigned ml = __reduce_max_sync(FULL_MASK, hi == mh ? (unsigned)k : 0u);
-        who = __ballot_sync(FULL_MASK, hi == mh && (unsigned)k == ml);
+// The 32 largest of two descending lists held a key per lane, descending: the larger
+// of a[i] and b[31 - i] are those 32, a bitonic sequence that five exchanges sort.
+__device__ __forceinline__ unsigned long long warp_merge(unsigned long long a, unsigned long long b, int lane) {
+    unsigned long long c = max(a, __shfl_sync(FULL_MASK, b, 31 - lane));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const unsigned long long p = __shfl_xor_sync(FULL_MASK, c, o);
+        c = (lane & o) ? min(c, p) : max(c, p);
     }
-    return who;
+    return c;
+}
+// The 32 largest of eight lists, merged in a tree (merges of one level overlap).
+__device__ __forceinline__ unsigned long long warp_merge8(unsigned long long (&v)[8], int lane) {
+#pragma unroll
+    for (int h = 4; h > 0; h >>= 1)
+#pragma unroll
+        for (int i = 0; i < h; ++i) v[i] = warp_merge(v[i], v[i + h], lane);
+    return v[0];
+}
+
+// ---- pairs of fp32: hi + lo, hi = fp32(hi + lo) ---------------------------------
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {  // a + b exactly (Knuth)
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+// log(sum 2^-40) for 2^40 <= sum < 2^63, within 3e-11.  sum 2^-40 = 2^n m, m in
+// [1, 2) in two parts; m c = 1 + u with an 8-bit c near 1 / m from the table, so
+// |u| < 1/60: log = n log 2 - log c + u - u^2/2 + ... - u^6/6.
+__device__ const float LOG_TAB[32][3] = {  // c, and -log c in two parts
+    {0.984375f, 1.574835740e-02f, -4.321589475e-10f}, {0.95703125f, 4.391923547e-02f, -1.533075222e-09f},
+    {0.92578125f, 7.711730152e-02f, 1.820745776e-09f}, {0.90234375f, 1.027597338e-01f, 1.616492495e-10f},
+    {0.875f, 1.335313916e-01f, 1.003886640e-09f}, {0.8515625f, 1.606823802e-01f, 1.491041068e-09f},
+    {0.83203125f, 1.838852763e-01f, 2.452540837e-09f}, {0.80859375f, 2.124586552e-01f, -4.023958056e-09f},
+    {0.7890625f, 2.369097471e-01f, -4.536054865e-11f}, {0.76953125f, 2.619737089e-01f, 6.873547065e-09f},
+    {0.75390625f, 2.824872434e-01f, 1.216075152e-08f}, {0.734375f, 3.087354898e-01f, -8.195662815e-09f},
+    {0.71875f, 3.302416801e-01f, 6.725313195e-09f}, {0.703125f, 3.522205949e-01f, -1.293612995e-09f},
+    {0.6875f, 3.746934533e-01f, -3.870509246e-09f}, {0.671875f, 3.976829648e-01f, 2.864321225e-09f},
+    {0.66015625f, 4.152787328e-01f, -3.220152811e-09f}, {0.64453125f, 4.392319620e-01f, 8.613421087e-09f},
+    {0.6328125f, 4.575811028e-01f, 6.399125230e-09f}, {0.62109375f, 4.762732387e-01f, 3.600425957e-09f},
+    {0.609375f, 4.953214228e-01f, 1.441470232e-08f}, {0.59765625f, 5.147395134e-01f, 9.689910208e-09f},
+    {0.5859375f, 5.345421433e-01f, 7.038427619e-09f}, {0.578125f, 5.479651690e-01f, 1.762505475e-09f},
+    {0.56640625f, 5.684437156e-01f, -1.351336909e-08f}, {0.5546875f, 5.893504024e-01f, -1.547689266e-08f},
+    {0.546875f, 6.035349965e-01f, 2.536070554e-08f}, {0.5390625f, 6.179237366e-01f, 2.275009159e-08f},
+    {0.52734375f, 6.399026513e-01f, 1.473116562e-08f}, {0.51953125f, 6.548283100e-01f, 6.244991191e-09f},
+    {0.51171875f, 6.699801087e-01f, 1.254046555e-08f}, {0.50390625f, 6.853650212e-01f, 1.888910006e-08f}
+};
+__device__ __forceinline__ Pair pair_log(unsigned long long sum) {
+    const int k = 63 - __clzll((long long)sum);
+    const unsigned long long m = sum << (63 - k);
+    const unsigned top = (unsigned)(m >> 40);  // 24 bits
+    const float mh = (float)top * 0x1p-23f, ml = (float)((unsigned)(m >> 16) & 0xffffffu) * 0x1p-47f;
+    const float* e = LOG_TAB[(top >> 18) & 31u];
+    const float c = e[0], p = __fmul_rn(mh, c);
+    const float u0 = __fsub_rn(p, 1.0f), u1 = __fmaf_rn(ml, c, __fmaf_rn(mh, c, -p)), u = __fadd_rn(u0, u1);
+    float q = __fmaf_rn(u, -1.0f / 6, 1.0f / 5);
+    q = __fmaf_rn(u, q, -0.25f);
+    q = __fmaf_rn(u, q, 1.0f / 3);
+    q = __fmaf_rn(u, q, -0.5f);
+    q = __fmul_rn(__fmul_rn(u, u), q);
+    const float n = (float)(k - 40);  // log 2 in two parts, the first of 16 bits: its product with n is exact
+    const Pair a = two_sum(__fmul_rn(n, 0.693145751953125f), e[1]), b = two_sum(a.hi, u0);
+    const float lo = __fadd_rn(__fadd_rn(__fadd_rn(__fmaf_rn(n, 1.428606765330187e-06f, e[2]), u1), q),
+                               __fadd_rn(a.lo, b.lo));
+    return two_sum(b.hi, lo);
+}
+// x + y of pairs; not finite: the sum alone.
+__device__ __forceinline__ Pair pair_add(Pair x, Pair y) {
+    const Pair s = two_sum(x.hi, y.hi);
+    if (!(fabsf(s.hi) < INFINITY)) return {s.hi, 0.0f};
+    return two_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(x.lo, y.lo)));
+}
+// Order-preserving key of a pair; 0 for -inf and NaN.
+__device__ __forceinline__ unsigned long long pair_key(Pair s) {
+    return s.hi > -INFINITY ? ((unsigned long long)beam_ord(s.hi) << 32) | beam_ord(s.lo) : 0ull;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -117,88 +187,125 @@ struct BeamArgs {
     float* scores_out;
 };
 
-// Thread t's logits of a block: 4t .. 4t + 3 of each quarter.  VEC: 16-byte loads (every row 16-byte aligned).
+// A block's logits on their way through shared memory: thread t copies, and later
+// reads, elements 4t .. 4t + 3 of each quarter, so no thread waits for another.
+// VEC: 16-byte copies (every row 16-byte aligned).  Elements from n on are not copied.
 template <bool VEC>
-__device__ __forceinline__ void beam_load(const float* p, int n, int t, float (&x)[BS_VPT]) {
-    if (VEC && n >= BS_BLOCK) {
+__device__ __forceinline__ void beam_fetch(float* stage, const float* p, int n, int t) {
 #pragma unroll
-        for (int i = 0; i < BS_VPT / 4; ++i) {
-            const float4 v = __ldcs(reinterpret_cast<const float4*>(p + i * 4 * BS_THREADS + 4 * t));
-            x[4 * i] = v.x;
-            x[4 * i + 1] = v.y;
-            x[4 * i + 2] = v.z;
-            x[4 * i + 3] = v.w;
-        }
-    } else {
+    for (int i = 0; i < BS_VPT / 4; ++i) {
+        const int e = i * 4 * BS_THREADS + 4 * t;
+        const uint32_t dst = smem_u32(stage + e);
+        if (VEC && e + 3 < n) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(p + e) : "memory");
+        } else {
 #pragma unroll
-        for (int i = 0; i < BS_VPT; ++i) {
-            const int e = (i >> 2) * 4 * BS_THREADS + 4 * t + (i & 3);
-            x[i] = e < n ? __ldg(p + e) : -INFINITY;
+            for (int j = 0; j < 4; ++j)
+                if (e + j < n)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * j), "l"(p + e + j) : "memory");
         }
     }
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // The warp's candidates, sorted and cut to the K best, then zeros up to 32; returns their number.
 __device__ __forceinline__ int beam_compact(unsigned long long* buf, unsigned long long* best, int n, int K, int lane) {
     __syncwarp();
-    for (int q = lane; q < n; q += 32) {
-        const unsigned long long k = buf[q];
+    if (n <= 32) {  // a key per lane
+        const unsigned long long k = lane < n ? buf[lane] : 0ull;
         int rank = 0;
+#pragma unroll 4
         for (int j = 0; j < n; ++j) rank += buf[j] > k ? 1 : 0;
-        if (rank < K) best[rank] = k;
+        __syncwarp();
+        if (lane < n) buf[rank] = k;
+        __syncwarp();
+        const int c = min(n, K);
+        if (lane >= c) buf[lane] = 0ull;
+        __syncwarp();
+        return c;
     }
+    unsigned long long k[BS_CAP / 32];
+    int rank[BS_CAP / 32] = {};
+#pragma unroll
+    for (int q = 0; q < BS_CAP / 32; ++q) k[q] = lane + 32 * q < n ? buf[lane + 32 * q] : 0ull;
+    for (int j = 0; j < n; ++j) {
+        const unsigned long long o = buf[j];
+#pragma unroll
+        for (int q = 0; q < BS_CAP / 32; ++q) rank[q] += o > k[q] ? 1 : 0;
+    }
+#pragma unroll
+    for (int q = 0; q < BS_CAP / 32; ++q)
+        if (k[q] && rank[q] < K) best[rank[q]] = k[q];
     __syncwarp();
-    const int c = min(n, K);
-    buf[lane] = lane < c ? best[lane] : 0ull;
+    buf[lane] = lane < K ? best[lane] : 0ull;  // n > 32 >= K
     __syncwarp();
-    return c;
+    return K;
 }
 
-// Rank of key k, at place `lane` of its own warp's sorted 32, among all warps' lists (list w at lists + w * stride).
-__device__ __forceinline__ int beam_rank(const unsigned long long* lists, int stride, unsigned long long k, int warp,
-                                         int lane) {
-    int rank = lane;
+// Warp 0: the 32 best of the warps' lists (each sorted, 0-padded to 32).
+__device__ __forceinline__ unsigned long long beam_merge_lists(const unsigned long long (*lists)[BS_CAP], int lane) {
+    static_assert(BS_WARPS == 8, "merged in a tree of eight");
+    unsigned long long v[8];
 #pragma unroll
-    for (int w = 0; w < BS_WARPS; ++w) {
-        if (w == warp) continue;
-        const unsigned long long* l = lists + w * stride;
-        int c = 0;  // larger keys, found by halving
-#pragma unroll
-        for (int h = 16; h > 0; h >>= 1)
-            if (l[c + h - 1] > k) c += h;
-        rank += c + (l[c] > k ? 1 : 0);
-    }
-    return rank;
+    for (int w = 0; w < 8; ++w) v[w] = lists[w][lane];
+    return warp_merge8(v, lane);
 }
 
 template <bool VEC>
 __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
     __shared__ unsigned long long cand[BS_WARPS][BS_CAP];
     __shared__ unsigned long long best[BS_WARPS][BS_MAX_OUT];
-    __shared__ float2 wpart[BS_MAX_BLOCKS][BS_WARPS];
-    __shared__ int count[BS_WARPS];
+    extern __shared__ __align__(16) float beam_smem[];  // [stages][BS_BLOCK] logits, then the blocks' sums by warp
+    __shared__ float subset[32];          // the first block's maxima by 8 threads
     __shared__ unsigned long long bound;  // the K-th best key known to all warps (0: fewer than K)
     pdl_launch_dependents();
     const int r = blockIdx.y, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    if (!beam_live(a.scores, a.done, r)) return;
     const int K = a.K, b0 = blockIdx.x * a.seg_blocks, nb = min(a.seg_blocks, a.nblk - b0);
     const float* row = a.logits + (size_t)r * a.ld;
     unsigned long long* buf = cand[warp];
     int cnt = 0;
     float thr = -INFINITY;  // a K-th best: later equals lose to it (higher indices)
-    float nx[BS_VPT];
-    beam_load<VEC>(row + (size_t)b0 * BS_BLOCK, a.V - b0 * BS_BLOCK, t, nx);
+    float2(*wpart)[BS_WARPS] = reinterpret_cast<float2(*)[BS_WARPS]>(beam_smem + BS_STAGES * BS_BLOCK);
+    auto fetch = [&](int b) {
+        if (b < nb) {
+            const int e0 = (b0 + b) * BS_BLOCK;
+            beam_fetch<VEC>(beam_smem + (b % BS_STAGES) * BS_BLOCK, row + e0, min(BS_BLOCK, a.V - e0), t);
+        }
+        cp_async_commit();
+    };
+    fetch(0);  // in flight while the beam's state is read
+    if (!beam_live(a.scores, a.done, r)) {
+        cp_async_wait<0>();
+        return;
+    }
+#pragma unroll
+    for (int b = 1; b < BS_STAGES; ++b) fetch(b);
     if (t == 0) bound = 0ull;
-#pragma unroll 2
     for (int b = 0; b < nb; ++b) {
         const int e0 = (b0 + b) * BS_BLOCK;
         float x[BS_VPT];
+        cp_async_wait<BS_STAGES - 1>();
 #pragma unroll
-        for (int i = 0; i < BS_VPT; ++i) x[i] = nx[i];
-        if (b + 1 < nb) beam_load<VEC>(row + e0 + BS_BLOCK, a.V - e0 - BS_BLOCK, t, nx);
+        for (int i = 0; i < BS_VPT / 4; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(beam_smem + (b % BS_STAGES) * BS_BLOCK + i * 4 * BS_THREADS + 4 * t);
+            x[4 * i] = v.x;
+            x[4 * i + 1] = v.y;
+            x[4 * i + 2] = v.z;
+            x[4 * i + 3] = v.w;
+        }
+        if (a.V - e0 < BS_BLOCK) {
+#pragma unroll
+            for (int i = 0; i < BS_VPT; ++i)
+                if ((i >> 2) * 4 * BS_THREADS + 4 * t + (i & 3) >= a.V - e0) x[i] = -INFINITY;
+        }
         float m = x[0];
 #pragma unroll
         for (int i = 1; i < BS_VPT; ++i) m = fmaxf(m, x[i]);
+        fetch(b + BS_STAGES);  // into the stage just read
         float s;
         {  // two logits per instruction (packed fp32 adds and products)
             const unsigned long long nm = pack2(-m, -m), l2 = pack2(LOG2E, LOG2E);
@@ -229,110 +336,94 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(FULL_MASK, s, o);
         if (lane == 0) wpart[b][warp] = make_float2(mw, s);
 
-        unsigned long long floor_key = 0ull;  // candidates of the first block: keys no less than this
+        // Candidates are logits >= lo: those above thr (the next value up), in the first
+        // block those no less than the K-th largest subset maximum.
+        float lo = beam_unord(beam_ord(thr) + 1u);
         if (b == 0) {
-            // the thread's largest key and its place in the warp; the K-th largest of all threads'
-            int at = BS_VPT - 1;
+            float m8 = m;
 #pragma unroll
-            for (int i = BS_VPT - 2; i >= 0; --i) at = x[i] == m ? i : at;
-            const unsigned long long k =
-                m > -INFINITY ? beam_key(m, e0 + (at >> 2) * 4 * BS_THREADS + 4 * t + (at & 3)) : 0ull;
-            best[warp][lane] = k;
-            __syncwarp();
-            int rank = 0;
-#pragma unroll 8
-            for (int j = 0; j < 32; ++j) {
-                const unsigned long long o = best[warp][j];
-                rank += o > k || (o == k && j < lane) ? 1 : 0;
+            for (int o = 4; o > 0; o >>= 1) m8 = fmaxf(m8, __shfl_xor_sync(FULL_MASK, m8, o));
+            if ((lane & 7) == 0) subset[t >> 3] = m8;
+            __syncthreads();
+            const float v = subset[lane];
+            int rank = 0;  // subsets with a larger maximum
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 o = *reinterpret_cast<const float4*>(subset + j);
+                rank += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
             }
-            __syncwarp();
-            best[warp][rank] = k;
-            __syncwarp();
-            const unsigned long long sk = best[warp][lane];
-            __syncthreads();
-            if (sk && beam_rank(best[0], BS_MAX_OUT, sk, warp, lane) == K - 1) bound = sk;
-            __syncthreads();
-            floor_key = bound;
-            thr = floor_key ? beam_key_x(floor_key) : -INFINITY;
+            // the least of those with fewer than K above them: at least K subsets reach it
+            const unsigned kth = __reduce_min_sync(FULL_MASK, rank < K ? beam_ord(v) : 0xffffffffu);
+            lo = fmaxf(lo, beam_unord(kth));
         }
-        const unsigned hot = __ballot_sync(FULL_MASK, floor_key ? m >= thr : m > thr);
-        if (hot) {
-            // x >= lo: x > thr, by the next value above; in the first block x >= thr
-            float lo = floor_key ? thr : beam_unord(beam_ord(thr) + 1u);
-            if (b > 0 && __popc(hot) >= K) {  // at least K logits are no less than the K-th largest lane maximum
-                int rank = 0;
-#pragma unroll 4
-                for (int j = 0; j < 32; ++j) {
-                    const float o = __shfl_sync(FULL_MASK, m, j);
-                    rank += o > m || (o == m && j < lane) ? 1 : 0;
-                }
-                lo = __shfl_sync(FULL_MASK, m, __ffs(__ballot_sync(FULL_MASK, rank == K - 1)) - 1);
-            }
+        if (__any_sync(FULL_MASK, m >= lo)) {
 #pragma unroll
             for (int i = 0; i < BS_VPT; ++i) {
-                if (!__any_sync(FULL_MASK, x[i] >= lo)) continue;
-                const unsigned long long k = beam_key(x[i], e0 + (i >> 2) * 4 * BS_THREADS + 4 * t + (i & 3));
-                const bool in = x[i] >= lo && k >= floor_key;
-                const unsigned who = __ballot_sync(FULL_MASK, in);
-                if (in) buf[cnt + __popc(who & ((1u << lane) - 1u))] = k;
+                if (i > 0 && (i & 3) == 0 && cnt >= K && b == 0) {
+                    // indices grow from quarter to quarter: what only equals a K-th best now loses to it
+                    cnt = beam_compact(buf, best[warp], cnt, K, lane);
+                    lo = fmaxf(lo, beam_unord(beam_ord(beam_key_x(buf[K - 1])) + 1u));
+                }
+                const unsigned who = __ballot_sync(FULL_MASK, x[i] >= lo);
+                if (!who) continue;
+                if (cnt > BS_CAP - 32) cnt = beam_compact(buf, best[warp], cnt, K, lane);
+                if (x[i] >= lo)
+                    buf[cnt + __popc(who & ((1u << lane) - 1u))] =
+                        beam_key(x[i], e0 + (i >> 2) * 4 * BS_THREADS + 4 * t + (i & 3));
                 cnt += __popc(who);
             }
-            if (cnt > K + 24) {
+            if (cnt >= K && (b > 0 || cnt > K + 24)) {
                 cnt = beam_compact(buf, best[warp], cnt, K, lane);
                 thr = fmaxf(thr, beam_key_x(buf[K - 1]));
             }
         }
-        if ((b == 3 || b == 15 || b == 63) && b + 1 < nb) {  // a new common bound after 4, 16, 64 blocks
+        if ((b == 0 || b == 3 || b == 15 || b == 63) && b + 1 < nb) {  // a new common bound
             cnt = beam_compact(buf, best[warp], cnt, K, lane);
             __syncthreads();
-            const unsigned long long k = buf[lane];
-            if (k && beam_rank(cand[0], BS_CAP, k, warp, lane) == K - 1) bound = k;
+            if (warp == 0) {
+                const unsigned long long k = beam_merge_lists(cand, lane);
+                if (lane == K - 1 && k) bound = k;
+            }
             __syncthreads();
             if (bound) thr = fmaxf(thr, beam_key_x(bound));
         }
     }
-    cnt = beam_compact(buf, best[warp], cnt, K, lane);
-    if (lane == 0) count[warp] = cnt;
+    beam_compact(buf, best[warp], cnt, K, lane);
     __syncthreads();
-    // the warps' sorted lists into the segment's
-    unsigned long long* out = a.keys + ((size_t)r * a.nseg + blockIdx.x) * K;
-    if (lane < cnt) {
-        const unsigned long long k = buf[lane];
-        const int rank = beam_rank(cand[0], BS_CAP, k, warp, lane);
-        if (rank < K) out[rank] = k;
+    if (warp == 0) {  // the segment's list
+        const unsigned long long k = beam_merge_lists(cand, lane);
+        if (lane < K) a.keys[((size_t)r * a.nseg + blockIdx.x) * K + lane] = k;
     }
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < BS_WARPS; ++w) total += count[w];
-    if (t < K && t >= total) out[t] = 0ull;
-    if (t < nb) {  // the blocks' sums, warps in order
+    const int b = t - BS_MAX_BLOCKS;  // the blocks' sums, warps in order
+    if (b >= 0 && b < nb) {
         float mb = -INFINITY, sb = 0.0f;
 #pragma unroll
-        for (int w = 0; w < BS_WARPS; ++w) mb = fmaxf(mb, wpart[t][w].x);
+        for (int w = 0; w < BS_WARPS; ++w) mb = fmaxf(mb, wpart[b][w].x);
 #pragma unroll
         for (int w = 0; w < BS_WARPS; ++w) {
-            const float2 p = wpart[t][w];
+            const float2 p = wpart[b][w];
             sb += p.x == mb ? p.y : p.y * ex2((p.x - mb) * LOG2E);
         }
-        a.part[(size_t)r * a.nblk + b0 + t] = make_float2(mb, mb > -INFINITY ? sb : 0.0f);
+        a.part[(size_t)r * a.nblk + b0 + b] = make_float2(mb, mb > -INFINITY ? sb : 0.0f);
     }
 }
+static_assert(BS_THREADS - BS_MAX_BLOCKS >= BS_MAX_BLOCKS, "a thread per block of a segment");
 
 // One CTA per group: warps 0 .. W - 1 merge the rows' lists while warps W .. 2W - 1
-// form the rows' log sums; then warp 0 merges the rows.
+// form the rows' log sums; then the rows are merged in a tree of warps.  Lists are
+// held a key per lane throughout.
 __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(const __grid_constant__ BeamArgs a) {
-    extern __shared__ unsigned long long staged[];  // [W][nseg][K] the rows' lists
-    __shared__ unsigned long long row_key[KD_BEAM_MAX_BEAMS][BS_MAX_OUT];
-    __shared__ double row_s[KD_BEAM_MAX_BEAMS][BS_MAX_OUT];
-    __shared__ unsigned long long row_o[KD_BEAM_MAX_BEAMS][BS_MAX_OUT + 2];  // row_s as order-preserving keys, 0-padded
-    __shared__ double row_lg[KD_BEAM_MAX_BEAMS];
+    __shared__ unsigned long long xkey[KD_BEAM_MAX_BEAMS][32];  // lists on their way to another warp
+    __shared__ int xfrom[KD_BEAM_MAX_BEAMS][32];
+    __shared__ int row_v[KD_BEAM_MAX_BEAMS][32];  // the rows' tokens
+    __shared__ Pair row_lg[KD_BEAM_MAX_BEAMS];
     __shared__ float row_m[KD_BEAM_MAX_BEAMS];
-    __shared__ int row_n[KD_BEAM_MAX_BEAMS];
-    pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp < a.W ? warp : warp - a.W;
     const int g = blockIdx.x, r = g * a.W + w, K = a.K;
     const bool live = beam_live(a.scores, a.done, r);
-    const float score = a.scores ? a.scores[r] : 0.0f;
+    const float score = a.scores ? a.scores[r] : 0.0f;  // the call's own inputs: complete before its first launch
+    pdl_wait();
+    unsigned long long x = 0ull;  // warps < W: the row's 32 best logits
     if (warp >= a.W) {
         // L = M + log sum_b s_b e^{m_b - M}; the sum in units of 2^-40 (a block's is at most 4096, the largest's at least 1)
         if (live) {
@@ -346,96 +437,84 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
                 M = fmaxf(M, p[q].x);
             }
             M = beam_unord(__reduce_max_sync(FULL_MASK, beam_ord(M)));
-            long long sum = 0;
+            unsigned long long sum = 0;
 #pragma unroll
             for (int q = 0; q < BS_MAX_BLOCKS / 32; ++q)
-                sum += __float2ll_rn((p[q].x == M ? p[q].y : p[q].y * expf(p[q].x - M)) * 0x1p40f);
+                if (32 * q < a.nblk)
+                    sum += __float2ull_rn((p[q].x == M ? p[q].y : p[q].y * expf(p[q].x - M)) * 0x1p40f);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
-            const double lg = log((double)sum * 0x1p-40);
+            const Pair lg = pair_log(sum ? sum : 1ull);  // 0: nothing in the row, no candidates either
             if (lane == 0) {
                 row_lg[w] = lg;
                 row_m[w] = M;
             }
         }
     } else if (live) {
-        const unsigned long long* lists = a.keys + (size_t)r * a.nseg * K;
-        unsigned long long* st = staged + (size_t)w * a.nseg * K;
-        for (int i = lane; i < a.nseg * K; i += 32) st[i] = __ldcg(lists + i);
-        __syncwarp();
-        // lane l holds the head of list l and the entry after it
-        const unsigned long long* at = st + lane * K;
-        const int have = lane < a.nseg ? K : 0;
-        unsigned long long head = have > 0 ? at[0] : 0ull, after = have > 1 ? at[1] : 0ull;
-        int n = 0, next = 2;
-        for (; n < K; ++n) {
-            const unsigned who = warp_best(head);
-            if (!who) break;
-            if ((who >> lane) & 1u) {
-                row_key[w][n] = head;
-                head = after;
-                after = next < have ? at[next] : 0ull;
-                ++next;
-            }
+        const unsigned long long* lists = a.keys + (size_t)r * a.nseg * K + lane;
+        for (int l = 0; l < a.nseg; l += 8) {
+            unsigned long long v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = lane < K && l + q < a.nseg ? __ldcg(lists + (size_t)(l + q) * K) : 0ull;
+            x = l ? warp_merge(x, warp_merge8(v, lane), lane) : warp_merge8(v, lane);
         }
-        if (lane == 0) row_n[w] = n;
-    } else if (lane == 0) {  // a finished beam stands for itself; a dead one offers nothing
-        const bool fin = a.done && a.done[r] && score > -INFINITY;
-        row_n[w] = fin ? 1 : 0;
-        row_key[w][0] = (unsigned)~a.eos;
-        row_s[w][0] = (double)score;
+        row_v[w][lane] = beam_key_i(x);
+    } else if (lane == 0) {
+        row_v[w][0] = a.eos;
     }
     __syncthreads();
+    // s of every candidate, as a key; from: its beam and place, which order equals
+    unsigned long long key = 0ull;
+    int from = w * 32 + lane;
     if (warp < a.W) {
-        unsigned long long o = 0ull;
-        if (lane < row_n[w]) {
-            if (live) {
-                const float xv = beam_key_x(row_key[w][lane]), M = row_m[w];
-                // x == M first: M may be infinite
-                row_s[w][lane] = (double)score + ((xv == M ? 0.0 : (double)xv - (double)M) - row_lg[w]);
+        if (live && x) {
+            const float xv = beam_key_x(x), M = row_m[w];
+            const Pair lg = row_lg[w], c = pair_add({score, 0.0f}, {-lg.hi, -lg.lo});
+            key = pair_key(pair_add(xv == M ? Pair{0.0f, 0.0f} : two_sum(xv, -M), c));  // x == M first: M may be infinite
+        } else if (!live && lane == 0 && a.done && a.done[r]) {
+            key = pair_key({score, 0.0f});  // a finished beam stands for itself; a dead one offers nothing
+        }
+    }
+    for (int h = 1; h < a.W; h *= 2) {
+        const bool give = warp < a.W && (warp & (2 * h - 1)) == h, take = (warp & (2 * h - 1)) == 0 && warp + h < a.W;
+        if (give) {
+            xkey[warp][lane] = key;
+            xfrom[warp][lane] = from;
+        }
+        __syncthreads();
+        if (take) {
+            const unsigned long long k = xkey[warp + h][31 - lane];
+            const int f = xfrom[warp + h][31 - lane];
+            auto before = [](unsigned long long k1, int f1, unsigned long long k2, int f2) {
+                return k1 > k2 || (k1 == k2 && f1 < f2);
+            };
+            if (before(k, f, key, from)) {
+                key = k;
+                from = f;
             }
-            const double v = row_s[w][lane] + 0.0;  // -inf and NaN never win
-            const unsigned long long u = (unsigned long long)__double_as_longlong(v);
-            o = !(v > -INFINITY) ? 0ull : (u >> 63) ? ~u : (u | 0x8000000000000000ull);
-        }
-        row_o[w][lane] = o;
-        if (lane < 2) row_o[w][BS_MAX_OUT + lane] = 0ull;
-    }
-    __syncthreads();
-    if (warp) return;
-    // Lane w holds the head of beam w's list; larger s first, then the lower beam.
-    const unsigned long long* mine_o = row_o[lane < a.W ? lane : 0];
-    unsigned long long key = lane < a.W ? mine_o[0] : 0ull, after = lane < a.W ? mine_o[1] : 0ull;
-    int pos = 0, mine = -1;  // mine: the winner (beam, place) of output `lane`
-    for (int j = 0; j < K; ++j) {
-        const unsigned who = warp_best(key);
-        if (!who) break;
-        const int win = __ffs(who) - 1, wp = __shfl_sync(FULL_MASK, pos, win);
-        if (lane == j) mine = win * BS_MAX_OUT + wp;
-        if (lane == win) {
-            key = after;
-            ++pos;
-            after = mine_o[min(pos + 1, BS_MAX_OUT + 1)];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const unsigned long long pk = __shfl_xor_sync(FULL_MASK, key, o);
+                const int pf = __shfl_xor_sync(FULL_MASK, from, o);
+                if (before(pk, pf, key, from) == !(lane & o)) {
+                    key = pk;
+                    from = pf;
+                }
+            }
         }
     }
-    if (lane < K) {
+    if (warp == 0 && lane < K) {
         const int o = g * K + lane;
-        if (mine < 0) {
-            a.parents[o] = -1;
-            a.tokens[o] = -1;
-            a.scores_out[o] = -INFINITY;
-            if (a.done_out) a.done_out[o] = 0;
-        } else {
-            const int bw = mine / BS_MAX_OUT, tok = beam_key_i(row_key[bw][mine % BS_MAX_OUT]);
-            a.parents[o] = bw;
-            a.tokens[o] = tok;
-            a.scores_out[o] = (float)row_s[bw][mine % BS_MAX_OUT];
-            if (a.done_out) a.done_out[o] = tok == a.eos || (a.done && a.done[r + bw]) ? 1 : 0;
-        }
+        const int beam = from / 32, tok = key ? row_v[beam][from % 32] : -1;
+        a.parents[o] = key ? beam : -1;
+        a.tokens[o] = tok;
+        a.scores_out[o] = key ? beam_unord((unsigned)(key >> 32)) : -INFINITY;
+        if (a.done_out) a.done_out[o] = key && (tok == a.eos || (a.done && a.done[g * a.W + beam])) ? 1 : 0;
     }
 }
 
-constexpr int BS_MERGE_SMEM = KD_BEAM_MAX_BEAMS * BS_MAX_SEGS * BS_MAX_OUT * 8;
+// stages, and a warp's (m, sum) per block of a segment
+static int beam_scan_smem(int blocks) { return BS_STAGES * BS_BLOCK * 4 + blocks * BS_WARPS * 8; }
 cudaError_t beam_init_attributes() {
     cudaError_t e = cudaSuccess;
     for (const void* f : {(const void*)beam_scan_kernel<true>, (const void*)beam_scan_kernel<false>,
@@ -443,7 +522,11 @@ cudaError_t beam_init_attributes() {
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                       cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
             return e;
-    return cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BS_MERGE_SMEM);
+    for (const void* f : {(const void*)beam_scan_kernel<true>, (const void*)beam_scan_kernel<false>})
+        if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, beam_scan_smem(BS_MAX_BLOCKS))) !=
+            cudaSuccess)
+            return e;
+    return cudaSuccess;
 }
 
 }  // namespace kd
@@ -507,10 +590,11 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
     a.keys = reinterpret_cast<unsigned long long*>(workspace);
     a.part = reinterpret_cast<float2*>(a.keys + (size_t)rows * a.nseg * n_out);
     const dim3 grid(a.nseg, rows);
+    const int smem = beam_scan_smem(a.seg_blocks);
     if (ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0)
-        beam_scan_kernel<true><<<grid, BS_THREADS, 0, s>>>(a);
+        beam_scan_kernel<true><<<grid, BS_THREADS, smem, s>>>(a);
     else
-        beam_scan_kernel<false><<<grid, BS_THREADS, 0, s>>>(a);
+        beam_scan_kernel<false><<<grid, BS_THREADS, smem, s>>>(a);
     KD_TRY(cudaGetLastError());
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -520,7 +604,6 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(n_groups);
     cfg.blockDim = dim3(64 * n_beams);
-    cfg.dynamicSmemBytes = (size_t)n_beams * a.nseg * n_out * 8;
     cfg.stream = s;
     KD_TRY(cudaLaunchKernelEx(&cfg, beam_merge_kernel, a));
     return KD_OK;

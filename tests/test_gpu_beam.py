@@ -173,7 +173,7 @@ def test_dead_and_finished_beams(kdlib):
     scores[12:16], done[12:16] = [np.nan, -1, -np.inf, -40], [0, 1, 1, 0]
     done[17] = 1
     for r in np.flatnonzero(~(scores > -np.inf) | (done != 0)):
-        x[r] = np.nan if r % 2 else 1e30                # never read
+        x[r] = np.nan if r % 2 else 1e30                # never used
     got = go(kdlib, x, W, n, scores=scores, done=done, eos=2)
     assert got[0][1].tolist() == [-1] * n
     assert got[0][2].tolist() == [1, 2, 0, 3, -1, -1] and got[1][2].tolist() == [2, 2, 2, 2, -1, -1]
