@@ -7,8 +7,8 @@
 // and the group's K best pairs are wanted, larger s first, then lower w, then
 // lower v.  Within a row the order is the logits' own, so one pass over the
 // logits does everything that touches all of them: a CTA walks a segment of one
-// row in blocks of 4096, leaves (m, sum e^{x-m}) of every block and the
-// segment's K best logits, sorted.  A second kernel, one CTA per group, forms
+// row 4096 logits at a time, leaves (m, sum e^{x-m}) of every block (one or two
+// such steps) and the segment's K best logits, sorted.  A second kernel, one CTA per group, forms
 // L_w, merges each row's lists, and merges the rows by s.
 //
 // The selection costs next to nothing once K candidates are known: a block whose
@@ -16,8 +16,8 @@
 // row brings about K ln(blocks) late candidates.  The first block's are found
 // through the maxima of 32 subsets of it: the K-th largest of them bounds the
 // K-th largest logit from below, and few logits lie above it (K = 4: 4.3 of 4096
-// on average, 8: 9, 32: 130).  The warps keep their candidates apart and agree on
-// a new bound after 4, 16 and 64 blocks.
+// on average, 8: 9, 32: 130).  The same of the 4, 16 and 64 blocks seen renews the
+// bound; the warps keep their candidates apart to the end.
 //
 // s decides between rows, where two candidates can lie as close as fp32 rounds:
 // L_w's last steps and s are pairs of fp32 whose sum carries about 48 bits (fp64
@@ -37,14 +37,18 @@ namespace kd {
 
 constexpr int BS_THREADS = 256;
 constexpr int BS_WARPS = BS_THREADS / 32;
-constexpr int BS_VPT = 16;                      // logits per thread and block
-constexpr int BS_BLOCK = BS_THREADS * BS_VPT;   // logits per block
-constexpr int BS_MAX_BLOCKS = 128;              // vocabulary up to 524288
+constexpr int BS_VPT = 16;                      // logits per thread and step
+constexpr int BS_STEP = BS_THREADS * BS_VPT;    // logits per step
+// Steps per block, the unit that sums are kept for: two where rows are long (a
+// block's reduction costs a quarter of a step).  By the vocabulary alone, so that
+// a row's sums do not depend on the batch.
+constexpr int beam_block_steps(int V) { return V > 65536 ? 2 : 1; }
+constexpr int BS_MAX_BLOCKS = 64;               // vocabulary up to 524288
 constexpr int BS_MAX_SEGS = 32;                 // segments (lists) per row: one per lane of the merge
 constexpr int BS_MAX_OUT = 32;
 constexpr int BS_CAP = 128;                     // a warp's candidates between cuts to the K best
-constexpr int BS_STAGES = 2;                    // blocks in flight behind the one being worked on
-static_assert(KD_BEAM_MAX_VOCAB == BS_BLOCK * BS_MAX_BLOCKS && KD_BEAM_MAX_OUT == BS_MAX_OUT, "kd.h limits");
+constexpr int BS_STAGES = 2;                    // steps in flight behind the one being worked on
+static_assert(KD_BEAM_MAX_VOCAB == BS_STEP * beam_block_steps(KD_BEAM_MAX_VOCAB) * BS_MAX_BLOCKS && KD_BEAM_MAX_OUT == BS_MAX_OUT, "kd.h limits");
 
 // (x, index) as a 64-bit key whose unsigned order is: larger x, then lower index
 // (-0 equals +0).  0 is no candidate.
@@ -178,6 +182,7 @@ struct BeamArgs {
     long ld;
     int V, W, K, nblk;    // vocabulary, beams per group, candidates kept, blocks per row
     int nseg, seg_blocks; // segments per row, blocks per segment
+    int block_steps;      // steps per block
     const float* scores;  // [rows], or nullptr (zeros)
     const int* done;      // [rows], or nullptr
     int eos;
@@ -187,22 +192,26 @@ struct BeamArgs {
     float* scores_out;
 };
 
-// A block's logits on their way through shared memory: thread t copies, and later
+// A step's logits on their way through shared memory: thread t copies, and later
 // reads, elements 4t .. 4t + 3 of each quarter, so no thread waits for another.
 // VEC: 16-byte copies (every row 16-byte aligned).  Elements from n on are not copied.
 template <bool VEC>
 __device__ __forceinline__ void beam_fetch(float* stage, const float* p, int n, int t) {
+    const uint32_t dst = smem_u32(stage + 4 * t);
+    p += 4 * t;
+    if (VEC && n >= BS_STEP) {
 #pragma unroll
-    for (int i = 0; i < BS_VPT / 4; ++i) {
-        const int e = i * 4 * BS_THREADS + 4 * t;
-        const uint32_t dst = smem_u32(stage + e);
-        if (VEC && e + 3 < n) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(p + e) : "memory");
-        } else {
+        for (int i = 0; i < BS_VPT / 4; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 16 * BS_THREADS),
+                         "l"(p + i * 4 * BS_THREADS)
+                         : "memory");
+    } else {
+        const int left = n - 4 * t;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (e + j < n)
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * j), "l"(p + e + j) : "memory");
+        for (int i = 0; i < BS_VPT; ++i) {
+            const int o = (i >> 2) * 4 * BS_THREADS + (i & 3);
+            if (o < left)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * o), "l"(p + o) : "memory");
         }
     }
 }
@@ -212,22 +221,26 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The warp's candidates, sorted and cut to the K best, then zeros up to 32; returns their number.
-__device__ __forceinline__ int beam_compact(unsigned long long* buf, unsigned long long* best, int n, int K, int lane) {
+// At most 32 candidates of the warp, sorted and cut to the K best, then zeros up to 32; returns their number.
+__device__ __forceinline__ int beam_sort(unsigned long long* buf, int n, int K, int lane) {
     __syncwarp();
-    if (n <= 32) {  // a key per lane
-        const unsigned long long k = lane < n ? buf[lane] : 0ull;
-        int rank = 0;
+    const unsigned long long k = lane < n ? buf[lane] : 0ull;
+    int rank = 0;
 #pragma unroll 4
-        for (int j = 0; j < n; ++j) rank += buf[j] > k ? 1 : 0;
-        __syncwarp();
-        if (lane < n) buf[rank] = k;
-        __syncwarp();
-        const int c = min(n, K);
-        if (lane >= c) buf[lane] = 0ull;
-        __syncwarp();
-        return c;
-    }
+    for (int j = 0; j < n; ++j) rank += buf[j] > k ? 1 : 0;
+    __syncwarp();
+    const int c = min(n, K);
+    if (lane < n) buf[rank] = k;
+    __syncwarp();
+    if (lane >= c) buf[lane] = 0ull;
+    __syncwarp();
+    return c;
+}
+// Any number of them.  Out of line: inlined at its call sites it made the kernel several times as
+// long, and a CTA that passes through its code once waits for instructions more than for anything else.
+__device__ __noinline__ int beam_cut(unsigned long long* buf, unsigned long long* best, int n, int K, int lane) {
+    if (n <= 32) return beam_sort(buf, n, K, lane);
+    __syncwarp();
     unsigned long long k[BS_CAP / 32];
     int rank[BS_CAP / 32] = {};
 #pragma unroll
@@ -259,22 +272,23 @@ template <bool VEC>
 __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
     __shared__ unsigned long long cand[BS_WARPS][BS_CAP];
     __shared__ unsigned long long best[BS_WARPS][BS_MAX_OUT];
-    extern __shared__ __align__(16) float beam_smem[];  // [stages][BS_BLOCK] logits, then the blocks' sums by warp
-    __shared__ float subset[32];          // the first block's maxima by 8 threads
-    __shared__ unsigned long long bound;  // the K-th best key known to all warps (0: fewer than K)
+    extern __shared__ __align__(16) float beam_smem[];  // [stages][BS_STEP] logits, then the blocks' sums by warp
+    __shared__ __align__(16) float subset[4][32];  // maxima by 8 threads of the blocks seen, at each renewal of the bound
     pdl_launch_dependents();
     const int r = blockIdx.y, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int K = a.K, b0 = blockIdx.x * a.seg_blocks, nb = min(a.seg_blocks, a.nblk - b0);
+    const int K = a.K, c0 = blockIdx.x * a.seg_blocks, nc = min(a.seg_blocks, a.nblk - c0);  // the segment's blocks
+    const int e_end = min(a.V, (c0 + nc) * a.block_steps * BS_STEP), e_begin = c0 * a.block_steps * BS_STEP;
+    const int nb = (e_end - e_begin + BS_STEP - 1) / BS_STEP;  // its steps
     const float* row = a.logits + (size_t)r * a.ld;
     unsigned long long* buf = cand[warp];
     int cnt = 0;
-    float thr = -INFINITY;  // a K-th best: later equals lose to it (higher indices)
-    float2(*wpart)[BS_WARPS] = reinterpret_cast<float2(*)[BS_WARPS]>(beam_smem + BS_STAGES * BS_BLOCK);
+    float thr = -INFINITY;  // K logits seen are no less: later equals lose to them (higher indices)
+    float mrun = -INFINITY; // the thread's largest so far
+    float mt = -INFINITY, st = 0.0f;  // the thread's (m, sum) of the block
+    float2(*wpart)[BS_WARPS] = reinterpret_cast<float2(*)[BS_WARPS]>(beam_smem + BS_STAGES * BS_STEP);
     auto fetch = [&](int b) {
-        if (b < nb) {
-            const int e0 = (b0 + b) * BS_BLOCK;
-            beam_fetch<VEC>(beam_smem + (b % BS_STAGES) * BS_BLOCK, row + e0, min(BS_BLOCK, a.V - e0), t);
-        }
+        const int e0 = e_begin + b * BS_STEP;
+        if (b < nb) beam_fetch<VEC>(beam_smem + (b % BS_STAGES) * BS_STEP, row + e0, a.V - e0, t);
         cp_async_commit();
     };
     fetch(0);  // in flight while the beam's state is read
@@ -284,28 +298,28 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
     }
 #pragma unroll
     for (int b = 1; b < BS_STAGES; ++b) fetch(b);
-    if (t == 0) bound = 0ull;
     for (int b = 0; b < nb; ++b) {
-        const int e0 = (b0 + b) * BS_BLOCK;
+        const int e0 = e_begin + b * BS_STEP;
+        const float* stage = beam_smem + (b % BS_STAGES) * BS_STEP + 4 * t;
         float x[BS_VPT];
         cp_async_wait<BS_STAGES - 1>();
 #pragma unroll
         for (int i = 0; i < BS_VPT / 4; ++i) {
-            const float4 v = *reinterpret_cast<const float4*>(beam_smem + (b % BS_STAGES) * BS_BLOCK + i * 4 * BS_THREADS + 4 * t);
+            const float4 v = *reinterpret_cast<const float4*>(stage + i * 4 * BS_THREADS);
             x[4 * i] = v.x;
             x[4 * i + 1] = v.y;
             x[4 * i + 2] = v.z;
             x[4 * i + 3] = v.w;
         }
-        if (a.V - e0 < BS_BLOCK) {
+        if (a.V - e0 < BS_STEP) {
+            const int left = a.V - e0 - 4 * t;
 #pragma unroll
             for (int i = 0; i < BS_VPT; ++i)
-                if ((i >> 2) * 4 * BS_THREADS + 4 * t + (i & 3) >= a.V - e0) x[i] = -INFINITY;
+                if ((i >> 2) * 4 * BS_THREADS + (i & 3) >= left) x[i] = -INFINITY;
         }
         float m = x[0];
 #pragma unroll
         for (int i = 1; i < BS_VPT; ++i) m = fmaxf(m, x[i]);
-        fetch(b + BS_STAGES);  // into the stage just read
         float s;
         {  // two logits per instruction (packed fp32 adds and products)
             const unsigned long long nm = pack2(-m, -m), l2 = pack2(LOG2E, LOG2E);
@@ -330,72 +344,83 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
             for (int i = 0; i < BS_VPT; ++i) s += x[i] == m ? 1.0f : ex2((x[i] - m) * LOG2E);
             if (m == -INFINITY) s = 0.0f;
         }
-        const float mw = beam_unord(__reduce_max_sync(FULL_MASK, beam_ord(m)));
-        s = m == mw ? s : s * ex2((m - mw) * LOG2E);
+        {  // into the block's
+            const float mn = fmaxf(mt, m);
+            st = (mt == mn ? st : st * ex2((mt - mn) * LOG2E)) + (m == mn ? s : s * ex2((m - mn) * LOG2E));
+            mt = mn;
+        }
+        const int c = b / a.block_steps;
+        if (b + 1 == nb || b + 1 == (c + 1) * a.block_steps) {  // the block is complete
+            const float mw = beam_unord(__reduce_max_sync(FULL_MASK, beam_ord(mt)));
+            st = mt == mw ? st : st * ex2((mt - mw) * LOG2E);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(FULL_MASK, s, o);
-        if (lane == 0) wpart[b][warp] = make_float2(mw, s);
+            for (int o = 16; o > 0; o >>= 1) st += __shfl_xor_sync(FULL_MASK, st, o);
+            if (lane == 0) wpart[c][warp] = make_float2(mw, st);
+            mt = -INFINITY;
+            st = 0.0f;
+        }
 
-        // Candidates are logits >= lo: those above thr (the next value up), in the first
-        // block those no less than the K-th largest subset maximum.
+        // Candidates are logits >= lo: those above thr (the next value up), and no less
+        // than the K-th largest subset maximum of the blocks seen, this one included.
         float lo = beam_unord(beam_ord(thr) + 1u);
-        if (b == 0) {
-            float m8 = m;
+        mrun = fmaxf(mrun, m);
+        if (b == 0 || b == 3 || b == 15 || b == 63) {
+            float* sub = subset[b == 0 ? 0 : b == 3 ? 1 : b == 15 ? 2 : 3];
+            float m8 = mrun;
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) m8 = fmaxf(m8, __shfl_xor_sync(FULL_MASK, m8, o));
-            if ((lane & 7) == 0) subset[t >> 3] = m8;
+            if ((lane & 7) == 0) sub[t >> 3] = m8;
             __syncthreads();
-            const float v = subset[lane];
+            const float v = sub[lane];
             int rank = 0;  // subsets with a larger maximum
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-                const float4 o = *reinterpret_cast<const float4*>(subset + j);
+                const float4 o = *reinterpret_cast<const float4*>(sub + j);
                 rank += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
             }
             // the least of those with fewer than K above them: at least K subsets reach it
-            const unsigned kth = __reduce_min_sync(FULL_MASK, rank < K ? beam_ord(v) : 0xffffffffu);
-            lo = fmaxf(lo, beam_unord(kth));
+            const float kth = beam_unord(__reduce_min_sync(FULL_MASK, rank < K ? beam_ord(v) : 0xffffffffu));
+            lo = fmaxf(lo, kth);
+            thr = fmaxf(thr, kth);
         }
         if (__any_sync(FULL_MASK, m >= lo)) {
+            unsigned mine = 0;
 #pragma unroll
-            for (int i = 0; i < BS_VPT; ++i) {
-                if (i > 0 && (i & 3) == 0 && cnt >= K && b == 0) {
-                    // indices grow from quarter to quarter: what only equals a K-th best now loses to it
-                    cnt = beam_compact(buf, best[warp], cnt, K, lane);
-                    lo = fmaxf(lo, beam_unord(beam_ord(beam_key_x(buf[K - 1])) + 1u));
+            for (int i = 0; i < BS_VPT; ++i) mine |= x[i] >= lo ? 1u << i : 0u;
+            int quarter = 0;
+            for (unsigned bits = __reduce_or_sync(FULL_MASK, mine); bits; bits &= bits - 1) {
+                const int i = __ffs(bits) - 1, o = (i >> 2) * 4 * BS_THREADS + (i & 3);
+                if (b == 0 && i >> 2 != quarter) {
+                    quarter = i >> 2;
+                    if (cnt >= K) {
+                        // indices grow from quarter to quarter: what only equals a K-th best now loses to it
+                        cnt = beam_cut(buf, best[warp], cnt, K, lane);
+                        lo = fmaxf(lo, beam_unord(beam_ord(beam_key_x(buf[K - 1])) + 1u));
+                    }
                 }
-                const unsigned who = __ballot_sync(FULL_MASK, x[i] >= lo);
-                if (!who) continue;
-                if (cnt > BS_CAP - 32) cnt = beam_compact(buf, best[warp], cnt, K, lane);
-                if (x[i] >= lo)
-                    buf[cnt + __popc(who & ((1u << lane) - 1u))] =
-                        beam_key(x[i], e0 + (i >> 2) * 4 * BS_THREADS + 4 * t + (i & 3));
+                const float v = stage[o];
+                const bool in = (mine >> i & 1u) && v >= lo;
+                const unsigned who = __ballot_sync(FULL_MASK, in);
+                if (cnt + __popc(who) > BS_CAP) cnt = beam_cut(buf, best[warp], cnt, K, lane);
+                if (in) buf[cnt + __popc(who & ((1u << lane) - 1u))] = beam_key(v, e0 + o + 4 * t);
                 cnt += __popc(who);
             }
-            if (cnt >= K && (b > 0 || cnt > K + 24)) {
-                cnt = beam_compact(buf, best[warp], cnt, K, lane);
+            if (cnt > K + 8) {
+                cnt = beam_cut(buf, best[warp], cnt, K, lane);
                 thr = fmaxf(thr, beam_key_x(buf[K - 1]));
             }
         }
-        if ((b == 0 || b == 3 || b == 15 || b == 63) && b + 1 < nb) {  // a new common bound
-            cnt = beam_compact(buf, best[warp], cnt, K, lane);
-            __syncthreads();
-            if (warp == 0) {
-                const unsigned long long k = beam_merge_lists(cand, lane);
-                if (lane == K - 1 && k) bound = k;
-            }
-            __syncthreads();
-            if (bound) thr = fmaxf(thr, beam_key_x(bound));
-        }
+        fetch(b + BS_STAGES);  // into the stage just read
     }
-    beam_compact(buf, best[warp], cnt, K, lane);
+    if (cnt > 32) cnt = beam_cut(buf, best[warp], cnt, K, lane);
+    beam_sort(buf, cnt, K, lane);
     __syncthreads();
     if (warp == 0) {  // the segment's list
         const unsigned long long k = beam_merge_lists(cand, lane);
         if (lane < K) a.keys[((size_t)r * a.nseg + blockIdx.x) * K + lane] = k;
     }
-    const int b = t - BS_MAX_BLOCKS;  // the blocks' sums, warps in order
-    if (b >= 0 && b < nb) {
+    const int b = t - BS_THREADS / 2;  // the blocks' sums, warps in order
+    if (b >= 0 && b < nc) {
         float mb = -INFINITY, sb = 0.0f;
 #pragma unroll
         for (int w = 0; w < BS_WARPS; ++w) mb = fmaxf(mb, wpart[b][w].x);
@@ -404,10 +429,10 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
             const float2 p = wpart[b][w];
             sb += p.x == mb ? p.y : p.y * ex2((p.x - mb) * LOG2E);
         }
-        a.part[(size_t)r * a.nblk + b0 + b] = make_float2(mb, mb > -INFINITY ? sb : 0.0f);
+        a.part[(size_t)r * a.nblk + c0 + b] = make_float2(mb, mb > -INFINITY ? sb : 0.0f);
     }
 }
-static_assert(BS_THREADS - BS_MAX_BLOCKS >= BS_MAX_BLOCKS, "a thread per block of a segment");
+static_assert(BS_THREADS / 2 >= BS_MAX_BLOCKS, "a thread per block of a segment");
 
 // One CTA per group: warps 0 .. W - 1 merge the rows' lists while warps W .. 2W - 1
 // form the rows' log sums; then the rows are merged in a tree of warps.  Lists are
@@ -425,7 +450,7 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
     pdl_wait();
     unsigned long long x = 0ull;  // warps < W: the row's 32 best logits
     if (warp >= a.W) {
-        // L = M + log sum_b s_b e^{m_b - M}; the sum in units of 2^-40 (a block's is at most 4096, the largest's at least 1)
+        // L = M + log sum_b s_b e^{m_b - M}; the sum in units of 2^-40 (a block's is at most 8192, the largest's at least 1)
         if (live) {
             const float2* part = a.part + (size_t)r * a.nblk;
             float2 p[BS_MAX_BLOCKS / 32];
@@ -514,7 +539,7 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
 }
 
 // stages, and a warp's (m, sum) per block of a segment
-static int beam_scan_smem(int blocks) { return BS_STAGES * BS_BLOCK * 4 + blocks * BS_WARPS * 8; }
+static int beam_scan_smem(int blocks) { return BS_STAGES * BS_STEP * 4 + blocks * BS_WARPS * 8; }
 cudaError_t beam_init_attributes() {
     cudaError_t e = cudaSuccess;
     for (const void* f : {(const void*)beam_scan_kernel<true>, (const void*)beam_scan_kernel<false>,
@@ -535,7 +560,7 @@ extern "C" {
 
 size_t kd_beam_workspace_bytes(int32_t n_groups, int32_t n_beams, int32_t V, int32_t n_out) {
     if (n_groups < 1 || n_beams < 1 || V < 1 || n_out < 1) return 0;
-    const size_t nblk = ((size_t)V + kd::BS_BLOCK - 1) / kd::BS_BLOCK;
+    const size_t nblk = ((size_t)V + kd::BS_STEP - 1) / kd::BS_STEP;
     return 256 + (size_t)n_groups * n_beams * nblk * (8 + 8 * (size_t)n_out);
 }
 
@@ -567,7 +592,8 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
     a.V = V;
     a.W = n_beams;
     a.K = n_out;
-    a.nblk = (V + BS_BLOCK - 1) / BS_BLOCK;
+    a.block_steps = beam_block_steps(V);
+    a.nblk = (V + a.block_steps * BS_STEP - 1) / (a.block_steps * BS_STEP);
     a.scores = scores;
     a.done = done;
     a.eos = eos < 0 ? -1 : eos;
