@@ -14,9 +14,9 @@
 // The selection costs next to nothing once K candidates are known: a block whose
 // largest logit does not exceed the K-th best so far is passed over, so a random
 // row brings about K ln(blocks) late candidates.  The first block's are found
-// through the maxima of 32 subsets of it: the K-th largest of them bounds the
-// K-th largest logit from below, and few logits lie above it (K = 4: 4.3 of 4096
-// on average, 8: 9, 32: 130).  The same of the 4, 16 and 64 blocks seen renews the
+// through the maxima of 32 or 64 subsets of it: the K-th largest of them bounds
+// the K-th largest logit from below, and few logits lie above it (K = 4: 4.3 of
+// 4096 on average, 8: 9, 32: 45).  The same of the 4, 16 and 64 blocks seen renews the
 // bound; the warps keep their candidates apart to the end.
 //
 // s decides between rows, where two candidates can lie as close as fp32 rounds:
@@ -42,13 +42,13 @@ constexpr int BS_STEP = BS_THREADS * BS_VPT;    // logits per step
 // Steps per block, the unit that sums are kept for: two where rows are long (a
 // block's reduction costs a quarter of a step).  By the vocabulary alone, so that
 // a row's sums do not depend on the batch.
-constexpr int beam_block_steps(int V) { return V > 65536 ? 2 : 1; }
+constexpr int beam_block_shift(int V) { return V > 65536 ? 1 : 0; }
 constexpr int BS_MAX_BLOCKS = 64;               // vocabulary up to 524288
 constexpr int BS_MAX_SEGS = 32;                 // segments (lists) per row: one per lane of the merge
 constexpr int BS_MAX_OUT = 32;
 constexpr int BS_CAP = 128;                     // a warp's candidates between cuts to the K best
 constexpr int BS_STAGES = 2;                    // steps in flight behind the one being worked on
-static_assert(KD_BEAM_MAX_VOCAB == BS_STEP * beam_block_steps(KD_BEAM_MAX_VOCAB) * BS_MAX_BLOCKS && KD_BEAM_MAX_OUT == BS_MAX_OUT, "kd.h limits");
+static_assert(KD_BEAM_MAX_VOCAB == (BS_STEP << beam_block_shift(KD_BEAM_MAX_VOCAB)) * BS_MAX_BLOCKS && KD_BEAM_MAX_OUT == BS_MAX_OUT, "kd.h limits");
 
 // (x, index) as a 64-bit key whose unsigned order is: larger x, then lower index
 // (-0 equals +0).  0 is no candidate.
@@ -76,12 +76,15 @@ __device__ __forceinline__ unsigned long long warp_merge(unsigned long long a, u
     }
     return c;
 }
-// The 32 largest of eight lists, merged in a tree (merges of one level overlap).
-__device__ __forceinline__ unsigned long long warp_merge8(unsigned long long (&v)[8], int lane) {
+// The 32 largest of the first n of eight lists (the others empty), merged in a tree:
+// merges of one level overlap.
+__device__ __forceinline__ unsigned long long warp_merge8(unsigned long long (&v)[8], int n, int lane) {
 #pragma unroll
     for (int h = 4; h > 0; h >>= 1)
+        if (n > h) {
 #pragma unroll
-        for (int i = 0; i < h; ++i) v[i] = warp_merge(v[i], v[i + h], lane);
+            for (int i = 0; i < h; ++i) v[i] = warp_merge(v[i], v[i + h], lane);
+        }
     return v[0];
 }
 
@@ -114,13 +117,18 @@ __device__ const float LOG_TAB[32][3] = {  // c, and -log c in two parts
     {0.52734375f, 6.399026513e-01f, 1.473116562e-08f}, {0.51953125f, 6.548283100e-01f, 6.244991191e-09f},
     {0.51171875f, 6.699801087e-01f, 1.254046555e-08f}, {0.50390625f, 6.853650212e-01f, 1.888910006e-08f}
 };
-__device__ __forceinline__ Pair pair_log(unsigned long long sum) {
+struct LogEntry {  // an entry per lane, loaded ahead of the sum
+    float c, hi, lo;
+};
+__device__ __forceinline__ LogEntry log_entry(int lane) { return {LOG_TAB[lane][0], LOG_TAB[lane][1], LOG_TAB[lane][2]}; }
+__device__ __forceinline__ Pair pair_log(unsigned long long sum, const LogEntry& tab) {  // sum the same in all lanes
     const int k = 63 - __clzll((long long)sum);
     const unsigned long long m = sum << (63 - k);
     const unsigned top = (unsigned)(m >> 40);  // 24 bits
     const float mh = (float)top * 0x1p-23f, ml = (float)((unsigned)(m >> 16) & 0xffffffu) * 0x1p-47f;
-    const float* e = LOG_TAB[(top >> 18) & 31u];
-    const float c = e[0], p = __fmul_rn(mh, c);
+    const int at = (top >> 18) & 31u;
+    const float c = __shfl_sync(FULL_MASK, tab.c, at), chi = __shfl_sync(FULL_MASK, tab.hi, at),
+                clo = __shfl_sync(FULL_MASK, tab.lo, at), p = __fmul_rn(mh, c);
     const float u0 = __fsub_rn(p, 1.0f), u1 = __fmaf_rn(ml, c, __fmaf_rn(mh, c, -p)), u = __fadd_rn(u0, u1);
     float q = __fmaf_rn(u, -1.0f / 6, 1.0f / 5);
     q = __fmaf_rn(u, q, -0.25f);
@@ -128,8 +136,8 @@ __device__ __forceinline__ Pair pair_log(unsigned long long sum) {
     q = __fmaf_rn(u, q, -0.5f);
     q = __fmul_rn(__fmul_rn(u, u), q);
     const float n = (float)(k - 40);  // log 2 in two parts, the first of 16 bits: its product with n is exact
-    const Pair a = two_sum(__fmul_rn(n, 0.693145751953125f), e[1]), b = two_sum(a.hi, u0);
-    const float lo = __fadd_rn(__fadd_rn(__fadd_rn(__fmaf_rn(n, 1.428606765330187e-06f, e[2]), u1), q),
+    const Pair a = two_sum(__fmul_rn(n, 0.693145751953125f), chi), b = two_sum(a.hi, u0);
+    const float lo = __fadd_rn(__fadd_rn(__fadd_rn(__fmaf_rn(n, 1.428606765330187e-06f, clo), u1), q),
                                __fadd_rn(a.lo, b.lo));
     return two_sum(b.hi, lo);
 }
@@ -182,7 +190,7 @@ struct BeamArgs {
     long ld;
     int V, W, K, nblk;    // vocabulary, beams per group, candidates kept, blocks per row
     int nseg, seg_blocks; // segments per row, blocks per segment
-    int block_steps;      // steps per block
+    int block_shift;      // log2 of the steps per block
     const float* scores;  // [rows], or nullptr (zeros)
     const int* done;      // [rows], or nullptr
     int eos;
@@ -265,7 +273,7 @@ __device__ __forceinline__ unsigned long long beam_merge_lists(const unsigned lo
     unsigned long long v[8];
 #pragma unroll
     for (int w = 0; w < 8; ++w) v[w] = lists[w][lane];
-    return warp_merge8(v, lane);
+    return warp_merge8(v, 8, lane);
 }
 
 template <bool VEC>
@@ -273,11 +281,11 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
     __shared__ unsigned long long cand[BS_WARPS][BS_CAP];
     __shared__ unsigned long long best[BS_WARPS][BS_MAX_OUT];
     extern __shared__ __align__(16) float beam_smem[];  // [stages][BS_STEP] logits, then the blocks' sums by warp
-    __shared__ __align__(16) float subset[4][32];  // maxima by 8 threads of the blocks seen, at each renewal of the bound
+    __shared__ __align__(16) float subset[4][64];  // maxima by 8 or 4 threads of the blocks seen, at each renewal of the bound
     pdl_launch_dependents();
     const int r = blockIdx.y, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int K = a.K, c0 = blockIdx.x * a.seg_blocks, nc = min(a.seg_blocks, a.nblk - c0);  // the segment's blocks
-    const int e_end = min(a.V, (c0 + nc) * a.block_steps * BS_STEP), e_begin = c0 * a.block_steps * BS_STEP;
+    const int e_end = min(a.V, ((c0 + nc) << a.block_shift) * BS_STEP), e_begin = (c0 << a.block_shift) * BS_STEP;
     const int nb = (e_end - e_begin + BS_STEP - 1) / BS_STEP;  // its steps
     const float* row = a.logits + (size_t)r * a.ld;
     unsigned long long* buf = cand[warp];
@@ -349,8 +357,8 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
             st = (mt == mn ? st : st * ex2((mt - mn) * LOG2E)) + (m == mn ? s : s * ex2((m - mn) * LOG2E));
             mt = mn;
         }
-        const int c = b / a.block_steps;
-        if (b + 1 == nb || b + 1 == (c + 1) * a.block_steps) {  // the block is complete
+        const int c = b >> a.block_shift;
+        if (b + 1 == nb || b + 1 == (c + 1) << a.block_shift) {  // the block is complete
             const float mw = beam_unord(__reduce_max_sync(FULL_MASK, beam_ord(mt)));
             st = mt == mw ? st : st * ex2((mt - mw) * LOG2E);
 #pragma unroll
@@ -367,19 +375,37 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
         if (b == 0 || b == 3 || b == 15 || b == 63) {
             float* sub = subset[b == 0 ? 0 : b == 3 ? 1 : b == 15 ? 2 : 3];
             float m8 = mrun;
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) m8 = fmaxf(m8, __shfl_xor_sync(FULL_MASK, m8, o));
-            if ((lane & 7) == 0) sub[t >> 3] = m8;
-            __syncthreads();
-            const float v = sub[lane];
-            int rank = 0;  // subsets with a larger maximum
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const float4 o = *reinterpret_cast<const float4*>(sub + j);
-                rank += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
-            }
+            m8 = fmaxf(m8, __shfl_xor_sync(FULL_MASK, m8, 1));
+            m8 = fmaxf(m8, __shfl_xor_sync(FULL_MASK, m8, 2));
             // the least of those with fewer than K above them: at least K subsets reach it
-            const float kth = beam_unord(__reduce_min_sync(FULL_MASK, rank < K ? beam_ord(v) : 0xffffffffu));
+            unsigned least = 0xffffffffu;
+            if (K <= 12) {
+                m8 = fmaxf(m8, __shfl_xor_sync(FULL_MASK, m8, 4));
+                if ((lane & 7) == 0) sub[t >> 3] = m8;
+                __syncthreads();
+                const float v = sub[lane];
+                int rank = 0;  // subsets with a larger maximum
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 o = *reinterpret_cast<const float4*>(sub + j);
+                    rank += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
+                }
+                if (rank < K) least = beam_ord(v);
+            } else {
+                if ((lane & 3) == 0) sub[t >> 2] = m8;
+                __syncthreads();
+                const float v = sub[lane], u = sub[lane + 32];
+                int rv = 0, ru = 0;
+#pragma unroll 4
+                for (int j = 0; j < 64; j += 4) {
+                    const float4 o = *reinterpret_cast<const float4*>(sub + j);
+                    rv += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
+                    ru += (o.x > u ? 1 : 0) + (o.y > u ? 1 : 0) + (o.z > u ? 1 : 0) + (o.w > u ? 1 : 0);
+                }
+                if (rv < K) least = beam_ord(v);
+                if (ru < K) least = min(least, beam_ord(u));
+            }
+            const float kth = beam_unord(__reduce_min_sync(FULL_MASK, least));
             lo = fmaxf(lo, kth);
             thr = fmaxf(thr, kth);
         }
@@ -447,6 +473,7 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
     const int g = blockIdx.x, r = g * a.W + w, K = a.K;
     const bool live = beam_live(a.scores, a.done, r);
     const float score = a.scores ? a.scores[r] : 0.0f;  // the call's own inputs: complete before its first launch
+    const LogEntry tab = log_entry(lane);
     pdl_wait();
     unsigned long long x = 0ull;  // warps < W: the row's 32 best logits
     if (warp >= a.W) {
@@ -469,7 +496,7 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
                     sum += __float2ull_rn((p[q].x == M ? p[q].y : p[q].y * expf(p[q].x - M)) * 0x1p40f);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
-            const Pair lg = pair_log(sum ? sum : 1ull);  // 0: nothing in the row, no candidates either
+            const Pair lg = pair_log(sum ? sum : 1ull, tab);  // 0: nothing in the row, no candidates either
             if (lane == 0) {
                 row_lg[w] = lg;
                 row_m[w] = M;
@@ -481,7 +508,8 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
             unsigned long long v[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = lane < K && l + q < a.nseg ? __ldcg(lists + (size_t)(l + q) * K) : 0ull;
-            x = l ? warp_merge(x, warp_merge8(v, lane), lane) : warp_merge8(v, lane);
+            const unsigned long long y = warp_merge8(v, a.nseg - l, lane);
+            x = l ? warp_merge(x, y, lane) : y;
         }
         row_v[w][lane] = beam_key_i(x);
     } else if (lane == 0) {
@@ -592,8 +620,8 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
     a.V = V;
     a.W = n_beams;
     a.K = n_out;
-    a.block_steps = beam_block_steps(V);
-    a.nblk = (V + a.block_steps * BS_STEP - 1) / (a.block_steps * BS_STEP);
+    a.block_shift = beam_block_shift(V);
+    a.nblk = (V + (BS_STEP << a.block_shift) - 1) / (BS_STEP << a.block_shift);
     a.scores = scores;
     a.done = done;
     a.eos = eos < 0 ? -1 : eos;
