@@ -179,7 +179,8 @@ kd_status kd_session_load_kv(kd_model* m, int32_t session_id, const void* k_fp16
  * visible) or t > p - window; window 0 (the state after kd_model_load) attends
  * every key 0..p again.  The caches keep every row.  Waits for the model's
  * outstanding work and drops the captured steps.
- * Errors: KD_ERR_INVALID_ARG (null model, window or sinks < 0). */
+ * Errors: KD_ERR_INVALID_ARG (null model, window or sinks < 0),
+ * KD_ERR_UNSUPPORTED (more than 1024 KV heads). */
 kd_status kd_model_set_window(kd_model* m, int32_t window, int32_t sinks);
 
 /* Reorder sessions: for all i < n at once, session ids[i] becomes a copy of what
@@ -478,7 +479,8 @@ size_t kd_attn_window_workspace_bytes(int32_t B, int32_t n_heads, int32_t head_d
  * cap.  Cache rows outside V_b are not used, whatever they hold.  A row's
  * result depends on its own position, window and sinks, not on the batch.
  * Workspace: kd_attn_window_workspace_bytes(B, n_heads, head_dim, cap, window,
- * sinks), used by one call at a time.  n_slots * n_kv_heads * cap < 2^31.  Other
+ * sinks), used by one call at a time.  n_slots * n_kv_heads * cap < 2^31 and
+ * n_kv_heads <= 1024 (else KD_ERR_UNSUPPORTED).  Other
  * arguments, alignments and errors as for kd_attn_append_decode;
  * kd_attn_device_status(workspace, ...) reads the call's fault word. */
 kd_status kd_attn_window_append_decode(const float* q, const float* k_new, const float* v_new, uint16_t* k_cache,

@@ -556,6 +556,7 @@ static cudaError_t enqueue_step(kd_model* m, int B, float* lg, int* am, cudaStre
             tw.window = m->window;
             tw.sinks = m->sinks;
             tw.max_splits = kd::win_max_items(c.max_ctx, m->window, m->sinks);
+            kd::win_fill(tw, false);
         }
         if (!m->kvq8) {
             KD_RUN(KD_K_ATTN_SPLIT, win ? kd::launch_attn_split(tw, m->kmaps, m->attn_grid, pdl, s)
@@ -872,6 +873,8 @@ static kd_status decode_impl(kd_model* m, const char* fn, const int32_t* ids, co
 kd_status kd_model_set_window(kd_model* m, int32_t window, int32_t sinks) {
     if (!m || window < 0 || sinks < 0)
         return fail(KD_ERR_INVALID_ARG, "kd_model_set_window: null model, or window %d, sinks %d", window, sinks);
+    if (window > 0 && m->cfg.n_kv_heads > kd::WIN_MAX_KV_HEADS)
+        return fail(KD_ERR_UNSUPPORTED, "kd_model_set_window: more than %d KV heads", kd::WIN_MAX_KV_HEADS);
     KD_CK(cudaSetDevice(m->dev));
     KD_CK(cudaStreamSynchronize(m->cap_stream));
     KD_CK(cudaEventSynchronize(m->last_step));

@@ -53,15 +53,14 @@ struct AttnSmem {
 // Part 0 (K) or 1 (V) of the item's new row: fp16 of the fp32 row, into the cache
 // and into the item's tile (tile: the lane's 16-byte chunk of the row there).
 template <int HD>
+__device__ __forceinline__ uint4 win_new_row(const AttnWinArgs& a, const AttnItem& it, int lane, int part) {
+    const float* src = (part ? a.v_new : a.k_new) + ((size_t)it.b * a.nkv + it.kvh) * HD + 8 * (lane % (HD / 8));
+    return make_uint4(f2_hi(src[0], src[1]), f2_hi(src[2], src[3]), f2_hi(src[4], src[5]), f2_hi(src[6], src[7]));
+}
+template <int HD>
 __device__ __forceinline__ void win_append_row(const AttnWinArgs& a, const AttnItem& it, int lane, int part,
-                                               uint32_t tile) {
+                                               uint32_t tile, const uint4& w) {
     if (lane < HD / 8) {
-        const float* src = (part ? a.v_new : a.k_new) + ((size_t)it.b * a.nkv + it.kvh) * HD + 8 * lane;
-        uint4 w;
-        w.x = f2_hi(src[0], src[1]);
-        w.y = f2_hi(src[2], src[3]);
-        w.z = f2_hi(src[4], src[5]);
-        w.w = f2_hi(src[6], src[7]);
         const size_t row = ((size_t)it.slot * a.nkv + it.kvh) * a.cap + it.start + it.n - 1;
         *reinterpret_cast<uint4*>((__half*)(part ? a.v_dst : a.k_dst) + row * HD + 8 * lane) = w;
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
@@ -106,13 +105,22 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
     volatile int* stage_item = reinterpret_cast<volatile int*>(smem + L::ITEM_OFF);
     volatile int* cta_failed = stage_item + 2 * S;
 
+    if (WIN && warp == 0 && lane < 2 * S) {  // a barrier per lane
+        mbar_init(&bar[lane], 1);
+        stage_item[lane] = -1;
+        mbar_init_fence();
+    }
+    if (WIN) __syncwarp();
+    static_assert(2 * S <= 32, "a lane per barrier");
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2 * S; ++i) {
-            mbar_init(&bar[i], 1);
-            stage_item[i] = -1;
+        if (!WIN) {
+            for (int i = 0; i < 2 * S; ++i) {
+                mbar_init(&bar[i], 1);
+                stage_item[i] = -1;
+            }
+            mbar_init_fence();
         }
         *cta_failed = 0;
-        mbar_init_fence();
         if (a.inject_tx && blockIdx.x == 0) mbar_expect_tx(&bar[0], (uint32_t)a.inject_tx);  // debug fault hook
         if constexpr (WIN)
             if (a.clear_err && blockIdx.x == 0) *a.err = 0;
@@ -133,7 +141,10 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
         const int st = k % S;
         uint8_t* stg = smem + st * L::STAGE;
         const int row = (int)(a.row0 + ((long)it.slot * a.nkv + it.kvh) * a.cap + item_start<WIN>(it));
-        const bool full = it.n == AT_C;
+        // A ragged item is copied in 8-row boxes; a windowed one in the whole box (past
+        // its keys it reads rows that are masked) unless one 8-row box holds it: a box is
+        // about a hundred cycles of one lane, and every row ends in a ragged item.
+        const bool full = WIN ? it.n > 8 : it.n == AT_C;
         const int krows = full ? AT_C : (it.n + 7) / 8 * 8;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
@@ -225,6 +236,15 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
         }
         if (k + AT_WARPS < nk) load_q(tab.item(a, lane, gitem(k + AT_WARPS)));  // lands during this item
 
+        bool appends = false;
+        uint4 k_row{}, v_row{};  // the new row, on its way while the tile's copy lands
+        if constexpr (WIN) {
+            appends = a.k_new && it.s == it.ns - 1;
+            if (appends) {
+                k_row = win_new_row<HD>(a, it, lane, 0);
+                v_row = win_new_row<HD>(a, it, lane, 1);
+            }
+        }
         const uint32_t par = (uint32_t)(k / S) & 1u;
         bool ok = wait_value(stage_item + st, k);
         ok = ok && mbar_wait_bounded(&bar[st], par);  // the K tile
@@ -236,11 +256,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
             break;
         }
         const int n = it.n;
-        bool appends = false;
-        if constexpr (WIN) {
-            appends = a.k_new && it.s == it.ns - 1;
-            if (appends) win_append_row<HD>(a, it, lane, 0, kbase + (lane < HD / 8 ? L::off(n - 1, lane) : 0u));
-        }
+        if constexpr (WIN)
+            if (appends) win_append_row<HD>(a, it, lane, 0, kbase + (lane < HD / 8 ? L::off(n - 1, lane) : 0u), k_row);
         const bool refill = k + S < nk;
         AttnItem nx{};
         if (refill) nx = tab.item(a, lane, gitem(k + S));
@@ -326,7 +343,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
             __syncwarp();
         }
         if constexpr (WIN)
-            if (appends) win_append_row<HD>(a, it, lane, 1, vbase + (lane < HD / 8 ? L::off(n - 1, lane) : 0u));
+            if (appends) win_append_row<HD>(a, it, lane, 1, vbase + (lane < HD / 8 ? L::off(n - 1, lane) : 0u), v_row);
         if (WIN && it.h0 < it.h1) {  // hidden rows of the V tile: p = 0 too
             for (int e = lane; e < (it.h1 - it.h0) * L::NREG * 8; e += 32) {
                 const int r = it.h0 + e / (L::NREG * 8), rem = e % (L::NREG * 8);

@@ -76,9 +76,19 @@ struct AttnWinTable {
     __device__ __forceinline__ void build(const AttnWinArgs& a, int lane) {
         slot = 0;
         pos = 0;
+        if (!a.slot) {  // the rows came with the launch
+            base = a.vitems;
+            if (lane < a.B) {
+                slot = a.vslot[lane];
+                pos = a.vpos[lane];
+                base = a.vbase[lane];
+            }
+            n_items = a.vitems;
+            return;
+        }
         if (lane < a.B) {
-            slot = a.slot ? a.slot[lane] : a.vslot[lane];
-            pos = a.slot ? a.pos[lane] : a.vpos[lane];
+            slot = a.slot[lane];
+            pos = a.pos[lane];
         }
         const int n = lane < a.B ? win_plan(pos, a.window, a.sinks).ns * a.nkv : 0;
         int incl = n;
@@ -96,7 +106,7 @@ struct AttnWinTable {
         AttnItem it;
         it.b = b;
         const int r = x - __shfl_sync(FULL_MASK, base, b);
-        it.s = r / a.nkv;
+        it.s = a.nkv_inv ? (int)__umulhi((unsigned)r, a.nkv_inv) : r;
         it.kvh = r - it.s * a.nkv;
         it.slot = __shfl_sync(FULL_MASK, slot, b);
         const int p = __shfl_sync(FULL_MASK, pos, b);

@@ -157,13 +157,22 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
     volatile int* stage_item = reinterpret_cast<volatile int*>(smem + L::ITEM_OFF);
     volatile int* cta_failed = stage_item + SK + SV;
 
+    if (WIN && warp == 0 && lane < SK + SV) {  // a barrier per lane
+        mbar_init(&bar[lane], 1);
+        stage_item[lane] = -1;
+        mbar_init_fence();
+    }
+    if (WIN) __syncwarp();
+    static_assert(SK + SV <= 32, "a lane per barrier");
     if (threadIdx.x == 0) {
-        for (int i = 0; i < SK + SV; ++i) {
-            mbar_init(&bar[i], 1);
-            stage_item[i] = -1;
+        if (!WIN) {
+            for (int i = 0; i < SK + SV; ++i) {
+                mbar_init(&bar[i], 1);
+                stage_item[i] = -1;
+            }
+            mbar_init_fence();
         }
         *cta_failed = 0;
-        mbar_init_fence();
         if (a.inject_tx && blockIdx.x == 0) mbar_expect_tx(&bar[0], (uint32_t)a.inject_tx);  // debug fault hook
         if constexpr (WIN)
             if (a.clear_err && blockIdx.x == 0) *a.err = 0;
@@ -182,7 +191,7 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
     const uint64_t kv_policy = l2_policy_evict_first();
     auto issue = [&](const AttnItem& it, int k, int parts) {
         const long row = a.row0 + ((long)it.slot * a.nkv + it.kvh) * a.cap + item_start<WIN>(it);
-        const bool full = it.n == AT_C;
+        const bool full = WIN ? it.n > 8 : it.n == AT_C;  // as in the fp16 kernel
         const int qrows = full ? AT_C : (it.n + 7) / 8 * 8;
         const uint32_t sbytes = (uint32_t)((it.n * L::SROW + 15) / 16 * 16);
 #pragma unroll

@@ -48,9 +48,12 @@ __host__ __device__ inline int win_max_items(int cap, int window, int sinks) {
 
 // slot == nullptr: the rows' slots and positions are in vslot and vpos, passed
 // with the launch (nothing has to be staged in device memory first).
+constexpr int WIN_MAX_KV_HEADS = 1024;  // a row's items, at most 1024 per head, stay within nkv_inv's range
 struct AttnWinArgs : AttnArgs {
     int window, sinks;  // window >= 1, sinks >= 0
     int vslot[16], vpos[16];
+    int vbase[16], vitems;  // the rows' first items and the number of items, with vslot
+    unsigned nkv_inv;       // ceil(2^32 / nkv): x / nkv = mulhi(x, nkv_inv) for x < 2^32 / nkv
     // Op-level calls: the split kernel appends the new rows itself.  The warp whose
     // item ends in row b's new position converts the row (fp32 [B][nkv][hd]),
     // writes it to the cache (fp16 rows, or Q8_0 quants and scales) and into its
@@ -65,6 +68,17 @@ struct AttnWinArgs : AttnArgs {
 };
 // A record's third padding word marks it (0: valid).
 constexpr int REC_VALID = 0, REC_FAULT = 1;
+// Set what the kernels take from the shape (nkv_inv) and, for op-level calls, the
+// items of the B rows at vpos.
+inline void win_fill(AttnWinArgs& a, bool rows) {
+    a.nkv_inv = (unsigned)((0x100000000ull + (unsigned)a.nkv - 1) / (unsigned)a.nkv);
+    if (a.nkv == 1) a.nkv_inv = 0;  // 2^32 does not fit: x itself
+    a.vitems = 0;
+    for (int b = 0; rows && b < a.B; ++b) {
+        a.vbase[b] = a.vitems;
+        a.vitems += win_plan(a.vpos[b], a.window, a.sinks).ns * a.nkv;
+    }
+}
 cudaError_t launch_attn_split(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s);
 cudaError_t launch_attn_split_q8(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s);
 cudaError_t launch_attn_combine(const AttnWinArgs& a, bool pdl, cudaStream_t s);

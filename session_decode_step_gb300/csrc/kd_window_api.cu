@@ -19,6 +19,8 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     if (B < 1 || B > KD_MAX_BATCH) return failf(KD_ERR_BATCH, "%s: B=%d outside [1, %d]", fn, B, KD_MAX_BATCH);
     if (nkv < 1 || nh < 1 || nh % nkv || !(q8 ? attn_q8_supported(hd, nh / nkv) : attn_supported(hd, nh / nkv)))
         return failf(KD_ERR_UNSUPPORTED, "%s: head_dim %d, %d query heads, %d KV heads", fn, hd, nh, nkv);
+    if (nkv > WIN_MAX_KV_HEADS)
+        return failf(KD_ERR_UNSUPPORTED, "%s: %d KV heads (at most %d)", fn, nkv, WIN_MAX_KV_HEADS);
     if (n_slots < 1 || cap < 1 || (q8 && cap % 2)) return failf(KD_ERR_INVALID_ARG, "%s: n_slots %d, cap %d", fn, n_slots, cap);
     if (window < 1 || sinks < 0) return failf(KD_ERR_INVALID_ARG, "%s: window %d, sinks %d", fn, window, sinks);
     if (cap > ATT_MAX_SPLITS * ATT_CHUNK)
@@ -31,7 +33,6 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     if ((u16 & 15) || ((uintptr_t)q & 7))
         return failf(KD_ERR_INVALID_ARG, "%s: caches and workspace must be 16-byte aligned, q %d-byte", fn, q8 ? 16 : 8);
     AttnWinArgs t{};
-    int64_t items = 0;
     for (int b = 0; b < B; ++b) {
         if (slots[b] < 0 || slots[b] >= n_slots) return failf(KD_ERR_BAD_SESSION, "%s: slot %d", fn, slots[b]);
         for (int j = 0; j < b; ++j)
@@ -40,7 +41,6 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
             return failf(KD_ERR_POSITION, "%s: position %d outside [0, %d)", fn, positions[b], cap);
         t.vslot[b] = slots[b];
         t.vpos[b] = positions[b];
-        items += (int64_t)win_plan(positions[b], window, sinks).ns * nkv;
     }
     int dev = 0, sms = 0;
     KD_TRY(cudaGetDevice(&dev));
@@ -69,6 +69,7 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     t.ks_dst = (__half*)ks;
     t.vs_dst = (__half*)vs;
     t.clear_err = 1;
+    win_fill(t, true);
     AttnMaps maps;
     const long rows = (long)n_slots * nkv * cap;
     if (q8) {
@@ -78,7 +79,7 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     }
     // persistent CTAs, no more than there are items
     const int per = q8 ? sms : attn_split_grid(sms, hd, nh / nkv);
-    const int grid = items < per ? (int)items : per;
+    const int grid = t.vitems < per ? t.vitems : per;
     if (q8) {
         KD_TRY(launch_attn_split_q8(t, maps, grid, false, s));
     } else {

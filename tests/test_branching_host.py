@@ -43,7 +43,7 @@ def window_q8(lib, q=D, ks=D, B=2, nh=32, nkv=8, n_slots=4, cap=64, win=16, sink
     (dict(q=None), INVALID), (dict(kn=None), INVALID), (dict(kc=None), INVALID), (dict(out=None), INVALID),
     (dict(ws=None), INVALID), (dict(sl=None), INVALID), (dict(ps=None), INVALID),
     (dict(B=0), BATCH), (dict(B=17), BATCH),
-    (dict(hd=96), UNSUPPORTED), (dict(nh=24), UNSUPPORTED), (dict(nh=30), UNSUPPORTED), (dict(nkv=0), UNSUPPORTED),
+    (dict(hd=96), UNSUPPORTED), (dict(nh=24), UNSUPPORTED), (dict(nh=30), UNSUPPORTED), (dict(nkv=0), UNSUPPORTED), (dict(nkv=1025, nh=1025), UNSUPPORTED),
     (dict(n_slots=0), INVALID), (dict(cap=0), INVALID), (dict(cap=65537), UNSUPPORTED),
     (dict(cap=2 ** 31 - 1), UNSUPPORTED),
     (dict(win=0), INVALID), (dict(win=-1), INVALID), (dict(sinks=-1), INVALID),
