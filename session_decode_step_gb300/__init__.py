@@ -153,11 +153,13 @@ def _ptr(obj):
     """Address of a numpy array, a torch tensor, an int, or None."""
     if obj is None:
         return None
-    data_ptr = getattr(obj, "data_ptr", None)
-    if data_ptr is not None:
-        if not obj.is_contiguous():
-            raise ValueError("tensors passed to libkd must be contiguous")
-        return data_ptr()
+    try:  # a torch tensor, the usual case, first
+        if obj.is_contiguous():
+            return obj.data_ptr()
+    except AttributeError:
+        pass
+    else:
+        raise ValueError("tensors passed to libkd must be contiguous")
     if isinstance(obj, int):
         return obj
     if isinstance(obj, np.ndarray):
@@ -185,12 +187,19 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+_raw_stream = None  # (stream of a device, current device) of torch, once found
+
+
 def _current_raw_stream(torch):
     # torch.cuda.current_stream() builds a Stream object (about 3 us); the raw handle is enough.
-    try:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    except AttributeError:
-        return torch.cuda.current_stream().cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        try:
+            _raw_stream = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        except AttributeError:
+            return torch.cuda.current_stream().cuda_stream
+    stream, device = _raw_stream
+    return stream(device())
 
 
 def _i32(a, n=None):
@@ -200,21 +209,33 @@ def _i32(a, n=None):
     return arr
 
 
-_ARRAYS: dict = {}
+class _Arrays(dict):
+    """ctypes array types of one element type, by length."""
+
+    def __init__(self, element):
+        self.element = element
+
+    def __missing__(self, n):
+        t = self[n] = self.element * n
+        return t
+
+
+_ARRAYS, _POINTERS = _Arrays(C.c_int32), _Arrays(_vp)
+_INT32 = np.dtype(np.int32)
 
 
 def _c32(a, n=None):
-    """A ctypes int32 array of a host sequence or array (passed to an int32 pointer argument as it is)."""
-    if isinstance(a, np.ndarray) and a.dtype == np.int32:
-        v = a.ravel().tolist()
-    else:
-        v = _i32(a).tolist()
-    if n is not None and len(v) != n:
-        raise ValueError(f"expected {n} entries, got {len(v)}")
-    t = _ARRAYS.get(len(v))
-    if t is None:
-        t = _ARRAYS[len(v)] = C.c_int32 * len(v)
-    return t(*v)
+    """A ctypes int32 array of a host sequence or array, as an int32 pointer argument takes it.  A
+    contiguous, writable int32 array is handed over where it lies (its memory outlives the call)."""
+    if type(a) is not np.ndarray or a.dtype is not _INT32:
+        a = _i32(a)
+    size = a.size
+    if n is not None and size != n:
+        raise ValueError(f"expected {n} entries, got {size}")
+    try:
+        return _ARRAYS[size].from_buffer(a)
+    except (TypeError, ValueError, BufferError):  # read-only, strided or empty
+        return _ARRAYS[size](*a.ravel().tolist())
 
 
 # ----------------------------------------------------------------- model ---
@@ -521,12 +542,16 @@ def kd_kv_reorder(planes, dst, src, lens, n_layers: int, n_slots: int, n_kv_head
     d = _c32(dst)
     m = len(d)
     rows = n_layers * n_slots * n_kv_heads * cap
-    ptrs = (_vp * len(planes))(*[_ptr(p) for p in planes])
-    nbytes = [_nbytes(p) for p in planes]
-    if rows < 1 or any(b % rows for b in nbytes):
-        raise ValueError("a plane's size must be a whole number of bytes per row")
-    widths = (C.c_int32 * len(planes))(*[b // rows for b in nbytes])
-    _check(lib().kd_kv_reorder(ptrs, widths, len(planes), n_layers, n_slots, n_kv_heads, cap, d, _c32(src, m),
+    if rows < 1:
+        raise ValueError("n_layers, n_slots, n_kv_heads and cap must be positive")
+    k = len(planes)
+    ptrs, widths = _POINTERS[k](), _ARRAYS[k]()
+    for i, p in enumerate(planes):
+        ptrs[i] = _ptr(p)
+        widths[i], rest = divmod(_nbytes(p), rows)
+        if rest:
+            raise ValueError("a plane's size must be a whole number of bytes per row")
+    _check(lib().kd_kv_reorder(ptrs, widths, k, n_layers, n_slots, n_kv_heads, cap, d, _c32(src, m),
                                _c32(lens, m), m, window, sinks, _stream(stream)))
 
 

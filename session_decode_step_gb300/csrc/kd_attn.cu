@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
         }
         // ---- per head 4j + c: scores of keys 16m + g (e = 0) and 16m + g + 8 (e = 1);
         // scale, mask, softmax over the item's keys (the 8 lanes g of a head)
+        const bool hides = WIN && it.h0 < it.h1;  // one item of a row at most has hidden keys, or few
         float sv[NQ][AT_KT][2], mx[NQ], lsum[NQ];
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
@@ -303,7 +304,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
                 for (int e = 0; e < 2; ++e) {
                     const float sc = __fadd_rn(sacc[m][j][2 * e], sacc[m][j][2 * e + 1]);  // both parts
                     const int key = 16 * m + g + 8 * e;
-                    sv[j][m][e] = item_sees<WIN>(it, key) ? __fmul_rn(sc, a.scale) : -INFINITY;
+                    sv[j][m][e] = key < n ? __fmul_rn(sc, a.scale) : -INFINITY;
+                    if (WIN && hides && key >= it.h0 && key < it.h1) sv[j][m][e] = -INFINITY;
                     mx[j] = fmaxf(mx[j], sv[j][m][e]);
                 }
 #pragma unroll
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int key = 16 * m + g + 8 * e;
-                    sv[j][m][e] = item_sees<WIN>(it, key) ? expf(__fsub_rn(sv[j][m][e], mx[j])) : 0.0f;
+                    sv[j][m][e] = key < n ? expf(__fsub_rn(sv[j][m][e], mx[j])) : 0.0f;
                     lsum[j] = __fadd_rn(lsum[j], sv[j][m][e]);
                 }
 #pragma unroll
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
         }
         if constexpr (WIN)
             if (appends) win_append_row<HD>(a, it, lane, 1, vbase + (lane < HD / 8 ? L::off(n - 1, lane) : 0u), v_row);
-        if (WIN && it.h0 < it.h1) {  // hidden rows of the V tile: p = 0 too
+        if (hides) {  // hidden rows of the V tile: p = 0 too
             for (int e = lane; e < (it.h1 - it.h0) * L::NREG * 8; e += 32) {
                 const int r = it.h0 + e / (L::NREG * 8), rem = e % (L::NREG * 8);
                 *reinterpret_cast<uint4*>(stg + L::K_BYTES + (rem >> 3) * L::HALF_BYTES + r * 128 + (rem & 7) * 16) =
@@ -448,6 +450,9 @@ constexpr int COMB_MAX_SPLITS = ATT_MAX_SPLITS;
 constexpr int COMB_UNROLL = 8;
 // warps of the merge: 4 up to 64 splits (4096 positions) of capacity, 32 beyond
 __host__ __device__ constexpr int comb_warps(int max_splits) { return max_splits <= 64 ? 4 : 32; }
+
+// Windowed rows have fewer: 8 warps serve up to 256 splits.
+__host__ __device__ constexpr int win_comb_warps(int max_splits) { return max_splits <= 64 ? 4 : max_splits <= 256 ? 8 : 32; }
 
 template <int HD, int NW, bool WIN>
 __global__ void __launch_bounds__(NW * 32) attn_combine_kernel(const __grid_constant__ AttnArgsOf<WIN> a) {
@@ -600,6 +605,7 @@ cudaError_t attn_init_attributes() {
                           (const void*)attn_combine_kernel<128, 4, false>, (const void*)attn_combine_kernel<128, 4, true>,
                           (const void*)attn_combine_kernel<64, 32, false>, (const void*)attn_combine_kernel<64, 32, true>,
                           (const void*)attn_combine_kernel<128, 32, false>, (const void*)attn_combine_kernel<128, 32, true>,
+                          (const void*)attn_combine_kernel<64, 8, true>, (const void*)attn_combine_kernel<128, 8, true>,
                           (const void*)kv_append_kernel})
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                       cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
@@ -699,10 +705,14 @@ static cudaError_t launch_combine(const AttnArgsOf<WIN>& a, bool pdl, cudaStream
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     launch_cfg(cfg, attr, pdl);
-    const int nw = comb_warps(a.max_splits);
+    const int nw = WIN ? win_comb_warps(a.max_splits) : comb_warps(a.max_splits);
     cfg.gridDim = dim3(a.nh, a.B);
     cfg.blockDim = dim3(nw * 32);
     cfg.stream = s;
+    if constexpr (WIN) {
+        if (nw == 8 && a.hd == 64) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 8, true>, a);
+        if (nw == 8 && a.hd == 128) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 8, true>, a);
+    }
     if (a.hd == 64)
         return nw == 4 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 4, WIN>, a)
                        : cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 32, WIN>, a);

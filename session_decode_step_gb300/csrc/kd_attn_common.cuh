@@ -24,14 +24,10 @@ struct AttnItem {
     int b, s, kvh, n, ns, slot;  // session, split, KV head, keys in this split, splits of the session, its slot
     int start, h0, h1;           // windowed rows: the split's first key, and its hidden keys [h0, h1)
 };
-// The first key of an item, and whether its key is hidden (never without a window).
+// The first key of an item.
 template <bool WIN>
 __device__ __forceinline__ int item_start(const AttnItem& it) {
     return WIN ? it.start : it.s * AT_C;
-}
-template <bool WIN>
-__device__ __forceinline__ bool item_sees(const AttnItem& it, int key) {
-    return key < it.n && !(WIN && key >= it.h0 && key < it.h1);
 }
 
 // The session table of a launch, held one session per lane (B <= 32): the

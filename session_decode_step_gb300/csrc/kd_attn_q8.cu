@@ -135,8 +135,8 @@ __device__ __forceinline__ void win_append_row_q8(const AttnWinArgs& a, const At
     __syncwarp();
 }
 
-// WIN: windowed rows, as in the fp16 kernel; a hidden key's value scales count as
-// zero (its quants are finite whatever they hold).
+// WIN: windowed rows, as in the fp16 kernel; a hidden key's value scales are set to
+// zero in the tile (its quants are finite whatever they hold).
 template <int GQ, bool WIN>
 __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
     attn_split_q8_kernel(const __grid_constant__ AttnArgsOf<WIN> a, const __grid_constant__ CUtensorMap tmk,
@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
             make_qb();
         }
         // ---- softmax over the item's keys (as in the fp16 kernel)
+        const bool hides = WIN && it.h0 < it.h1;  // one item of a row at most has hidden keys, or few
         float sv[NQ][AT_KT][2], mx[NQ], lsum[NQ];
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
@@ -371,7 +372,8 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
                 for (int e = 0; e < 2; ++e) {
                     const float sc = __fadd_rn(sacc[m][j][2 * e], sacc[m][j][2 * e + 1]);  // both parts
                     const int key = 16 * m + g + 8 * e;
-                    sv[j][m][e] = item_sees<WIN>(it, key) ? __fmul_rn(sc, a.scale) : -INFINITY;
+                    sv[j][m][e] = key < n ? __fmul_rn(sc, a.scale) : -INFINITY;
+                    if (WIN && hides && key >= it.h0 && key < it.h1) sv[j][m][e] = -INFINITY;
                     mx[j] = fmaxf(mx[j], sv[j][m][e]);
                 }
 #pragma unroll
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int key = 16 * m + g + 8 * e;
-                    sv[j][m][e] = item_sees<WIN>(it, key) ? expf(__fsub_rn(sv[j][m][e], mx[j])) : 0.0f;
+                    sv[j][m][e] = key < n ? expf(__fsub_rn(sv[j][m][e], mx[j])) : 0.0f;
                     lsum[j] = __fadd_rn(lsum[j], sv[j][m][e]);
                 }
 #pragma unroll
@@ -403,6 +405,11 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
         if constexpr (WIN)
             if (appends)
                 win_append_row_q8(a, it, lane, 1, smem + L::VQ_OFF + vst * L::TILE, smem + L::VS_OFF + vst * L::STILE);
+        if (hides) {  // hidden rows: their value scales may be anything, and p is 0
+            for (int r = it.h0 + lane; r < it.h1; r += 32)
+                *reinterpret_cast<uint2*>(smem + L::VS_OFF + vst * L::STILE + r * L::SROW) = make_uint2(0u, 0u);
+            __syncwarp();
+        }
         // p d_t,blk would fall below fp16's normal range for small p: the item's
         // products carry an exact power-of-two factor 2^e, taken from its largest
         // value scale so that p d 2^e < 2^14, and the output drops it again in fp32.
@@ -410,11 +417,11 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
         {
             const uint4 w = lds_v4(vscale + 2 * lane * L::SROW);  // rows 2 lane, 2 lane + 1
             float dm = 0.0f;
-            if (item_sees<WIN>(it, 2 * lane)) {
+            if (2 * lane < n) {
                 const float2 x = h2bits_to_float2(w.x), y = h2bits_to_float2(w.y);
                 dm = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
             }
-            if (item_sees<WIN>(it, 2 * lane + 1)) {
+            if (2 * lane + 1 < n) {
                 const float2 x = h2bits_to_float2(w.z), y = h2bits_to_float2(w.w);
                 dm = fmaxf(dm, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
             }
@@ -446,14 +453,14 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
                 const int kb = 16 * js + 2 * c;
                 const uint4 wa = lds_v4(vscale + kb * L::SROW), wb = lds_v4(vscale + (kb + 8) * L::SROW);
                 float2 dk[4][2];  // [key r][blocks 0,1 | 2,3]; 0 past the item's keys
-                dk[0][0] = h2bits_to_float2(item_sees<WIN>(it, kb) ? wa.x : 0u);
-                dk[0][1] = h2bits_to_float2(item_sees<WIN>(it, kb) ? wa.y : 0u);
-                dk[1][0] = h2bits_to_float2(item_sees<WIN>(it, kb + 1) ? wa.z : 0u);
-                dk[1][1] = h2bits_to_float2(item_sees<WIN>(it, kb + 1) ? wa.w : 0u);
-                dk[2][0] = h2bits_to_float2(item_sees<WIN>(it, kb + 8) ? wb.x : 0u);
-                dk[2][1] = h2bits_to_float2(item_sees<WIN>(it, kb + 8) ? wb.y : 0u);
-                dk[3][0] = h2bits_to_float2(item_sees<WIN>(it, kb + 9) ? wb.z : 0u);
-                dk[3][1] = h2bits_to_float2(item_sees<WIN>(it, kb + 9) ? wb.w : 0u);
+                dk[0][0] = h2bits_to_float2(kb < n ? wa.x : 0u);
+                dk[0][1] = h2bits_to_float2(kb < n ? wa.y : 0u);
+                dk[1][0] = h2bits_to_float2(kb + 1 < n ? wa.z : 0u);
+                dk[1][1] = h2bits_to_float2(kb + 1 < n ? wa.w : 0u);
+                dk[2][0] = h2bits_to_float2(kb + 8 < n ? wb.x : 0u);
+                dk[2][1] = h2bits_to_float2(kb + 8 < n ? wb.y : 0u);
+                dk[3][0] = h2bits_to_float2(kb + 9 < n ? wb.z : 0u);
+                dk[3][1] = h2bits_to_float2(kb + 9 < n ? wb.w : 0u);
                 uint32_t pb[4][NQ][2];
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
