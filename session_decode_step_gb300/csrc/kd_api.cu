@@ -67,6 +67,7 @@ cudaError_t init_device_attributes(int dev) {
         if (e == cudaSuccess) e = kd::attn_q8_init_attributes();
         if (e == cudaSuccess) e = kd::rowops_init_attributes();
         if (e == cudaSuccess) e = kd::beam_init_attributes();
+        if (e == cudaSuccess) e = kd::attn_chain_init_attributes();
         g_attr_err[dev] = e;
     });
     return g_attr_err[dev];
@@ -415,6 +416,11 @@ static bool fused_norm(const kd_model* m, const PackedQ8& p) {
 static bool embed_norm(const kd_model* m) {
     return !(m->cfg.flags & KD_FLAG_UNFUSED) && !fused_norm(m, m->qkv[0]);
 }
+// A windowed step's attention is one launch (short windows over fp16 rows).
+static bool window_chain(const kd_model* m) {
+    return m->window > 0 && !m->kvq8 &&
+           kd::win_max_items(m->cfg.max_ctx, m->window, m->sinks) <= kd::WIN_CHAIN_ITEMS;
+}
 // The lm_head launch makes each row's pick itself (stream schedule, fused train).
 static bool head_pick(const kd_model* m) {
     return !(m->cfg.flags & KD_FLAG_UNFUSED) && m->head.mode == kd::MMVQ_STREAM;
@@ -558,7 +564,10 @@ static cudaError_t enqueue_step(kd_model* m, int B, float* lg, int* am, cudaStre
             tw.max_splits = kd::win_max_items(c.max_ctx, m->window, m->sinks);
             kd::win_fill(tw, false);
         }
-        if (!m->kvq8) {
+        const bool chain = window_chain(m);
+        if (chain) {
+            KD_RUN(KD_K_ATTN_SPLIT, kd::launch_attn_chain(tw, pdl, s));
+        } else if (!m->kvq8) {
             KD_RUN(KD_K_ATTN_SPLIT, win ? kd::launch_attn_split(tw, m->kmaps, m->attn_grid, pdl, s)
                                         : kd::launch_attn_split(t, m->kmaps, m->attn_grid, pdl, s));
         } else {  // quantised append of the new rows, then the attention over the Q8_0 cache
@@ -567,8 +576,10 @@ static cudaError_t enqueue_step(kd_model* m, int B, float* lg, int* am, cudaStre
             KD_RUN(KD_K_ATTN_SPLIT, win ? kd::launch_attn_split_q8(tw, m->kmaps, m->num_sms, pdl, s)
                                         : kd::launch_attn_split_q8(t, m->kmaps, m->num_sms, pdl, s));
         }
-        t.tl = tw.tl = tl_next();
-        KD_RUN(KD_K_ATTN_COMBINE, win ? kd::launch_attn_combine(tw, pdl, s) : kd::launch_attn_combine(t, pdl, s));
+        if (!chain) {
+            t.tl = tw.tl = tl_next();
+            KD_RUN(KD_K_ATTN_COMBINE, win ? kd::launch_attn_combine(tw, pdl, s) : kd::launch_attn_combine(t, pdl, s));
+        }
         a = mm(m->wo[l], m->attn);
         resid(a);
         a.inject_tx = inject(KD_K_WO);
@@ -1020,7 +1031,8 @@ kd_status kd_profile_timeline(kd_model* m, uint64_t* dev_buf, int32_t max_launch
         cls.push_back(KD_K_EMBED);
         for (int l = 0; l < L; ++l) {
             if (!fused_norm(m, m->qkv[l]) && !(l == 0 && embed_norm(m))) cls.push_back(KD_K_RMSNORM);
-            for (int k : {KD_K_QKV, KD_K_ATTN_SPLIT, KD_K_ATTN_COMBINE, KD_K_WO}) cls.push_back(k);
+            for (int k : {KD_K_QKV, KD_K_ATTN_SPLIT, KD_K_ATTN_COMBINE, KD_K_WO})
+                if (k != KD_K_ATTN_COMBINE || !window_chain(m)) cls.push_back(k);
             if (!fused_norm(m, m->gu[l])) cls.push_back(KD_K_RMSNORM);
             for (int k : {KD_K_GATE_UP, KD_K_DOWN}) cls.push_back(k);
         }
@@ -1075,6 +1087,8 @@ kd_status kd_device_status(kd_model* m, int32_t* flags_out) {
 
 kd_status kd_debug_inject_wait_timeout(kd_model* m, int32_t kernel_class) {
     if (!m) return fail(KD_ERR_INVALID_ARG, "kd_debug_inject_wait_timeout: null model");
+    if (kernel_class == KD_K_ATTN_SPLIT && window_chain(m))
+        return fail(KD_ERR_INVALID_ARG, "kd_debug_inject_wait_timeout: the attention of this window has no bounded wait");
     switch (kernel_class) {
         case KD_K_QKV: case KD_K_ATTN_SPLIT: case KD_K_WO: case KD_K_GATE_UP: case KD_K_DOWN: case KD_K_LM_HEAD:
             m->inject_cls = kernel_class;

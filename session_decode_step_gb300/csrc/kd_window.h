@@ -82,4 +82,11 @@ inline void win_fill(AttnWinArgs& a, bool rows) {
 cudaError_t launch_attn_split(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s);
 cudaError_t launch_attn_split_q8(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s);
 cudaError_t launch_attn_combine(const AttnWinArgs& a, bool pdl, cudaStream_t s);
+// fp16 rows in one launch (kd_attn_chain.cu) where no row has more items than this.
+// By the slot's capacity, window and sinks alone: a row's bits do not depend on the
+// batch.  32 rows of 8 heads over a window of 1024: one launch 9.0 us, split and
+// merge 12.0; from about 2000 keys on, one row's chains take longer than the split.
+constexpr int WIN_CHAIN_ITEMS = 32;
+cudaError_t attn_chain_init_attributes();
+cudaError_t launch_attn_chain(const AttnWinArgs& a, bool pdl, cudaStream_t s);
 }  // namespace kd

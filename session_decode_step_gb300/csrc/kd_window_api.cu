@@ -1,6 +1,6 @@
 // kd_window_api.cu -- the windowed attention's op-level entry points: KV append and
 // split attention over the leading and the last keys (kd_window.h) in one launch,
-// then the merge.
+// then the merge; for short fp16 windows everything in one launch.
 // Slots and positions travel with the launches, so a call copies nothing to the
 // device and can be captured into a graph (they are then part of the graph).
 #include <cmath>
@@ -70,19 +70,22 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     t.vs_dst = (__half*)vs;
     t.clear_err = 1;
     win_fill(t, true);
+    t.kc = (const __half*)kc;
+    t.vc = (const __half*)vc;
+    if (!q8 && t.max_splits <= WIN_CHAIN_ITEMS) {
+        KD_TRY(launch_attn_chain(t, false, s));
+        return KD_OK;
+    }
     AttnMaps maps;
     const long rows = (long)n_slots * nkv * cap;
-    if (q8) {
-        KD_TRY(make_attn_q8_maps((const uint8_t*)kc, (const uint8_t*)vc, rows, &maps));
-    } else {
-        KD_TRY(make_attn_maps((const __half*)kc, (const __half*)vc, rows, hd, &maps));
-    }
     // persistent CTAs, no more than there are items
     const int per = q8 ? sms : attn_split_grid(sms, hd, nh / nkv);
     const int grid = t.vitems < per ? t.vitems : per;
     if (q8) {
+        KD_TRY(make_attn_q8_maps((const uint8_t*)kc, (const uint8_t*)vc, rows, &maps));
         KD_TRY(launch_attn_split_q8(t, maps, grid, false, s));
     } else {
+        KD_TRY(make_attn_maps((const __half*)kc, (const __half*)vc, rows, hd, &maps));
         KD_TRY(launch_attn_split(t, maps, grid, false, s));
     }
     KD_TRY(launch_attn_combine(t, true, s));

@@ -123,11 +123,13 @@ SHAPES = [(32, 8, 128), (8, 8, 128), (6, 3, 128), (16, 2, 128), (4, 4, 64), (14,
 RANGES = [(1, 0), (1, 1), (7, 4), (64, 0), (65, 3), (100, 64), (130, 200), (500, 1), (2 ** 31 - 1, 2 ** 31 - 1)]
 
 
+# cap: up to 2048 visible keys run in one launch, wider windows as split and merge
 @pytest.mark.parametrize("nh,nkv,hd", SHAPES)
-@pytest.mark.parametrize("window,sinks", RANGES)
-def test_window_fp16(kdlib, nh, nkv, hd, window, sinks):
-    c = Case(False, window % 1000 + sinks % 1000 + nh, nh, nkv, hd, 601, [0, 1, 6, 63, 64, 127, 200, 263, 600, 333],
-             window, sinks)
+@pytest.mark.parametrize("window,sinks,cap", [(w, s, 601) for w, s in RANGES] + [
+    (2 ** 31 - 1, 5, 2101), (2500, 0, 2600), (2040, 3, 2301), (2100, 70, 4001), (300, 2000, 2301), (2080, 300, 2500)])
+def test_window_fp16(kdlib, nh, nkv, hd, window, sinks, cap):
+    c = Case(False, window % 1000 + sinks % 1000 + nh, nh, nkv, hd, cap,
+             [0, 1, 6, 63, 64, 127, 200, 263, cap - 1, cap * 5 // 9], window, sinks)
     got = c.run(kdlib)
     c.check(got)
     for i, new in ((0, c.kn), (1, c.vn)):  # the appended rows
@@ -145,13 +147,13 @@ def test_window_q8(kdlib, nh, nkv, window, sinks):
 
 
 def test_window_of_everything_equals_the_plain_call(kdlib):
-    """A window as wide as the slot: the same items, so the same bits as kd_attn_append_decode."""
+    """A wide window that hides nothing: the same items, so the same bits as kd_attn_append_decode."""
     kd = kdlib
-    c = Case(False, 5, 32, 8, 128, 700, [0, 63, 64, 300, 699], 700, 0)
+    c = Case(False, 5, 32, 8, 128, 2300, [0, 63, 64, 300, 2299], 2300, 0)
     got = c.run(kd)
     out = torch.empty(5, 32 * 128, dtype=torch.int16, device="cuda")
-    ws = torch.empty(kd.kd_attn_workspace_bytes(5, 32, 128, 700), dtype=torch.uint8, device="cuda")
-    kd.kd_attn_append_decode(c.dq, c.dk, c.dv, *c.dev, c.slots, c.pos, 32, 8, 128, c.n_slots, 700, out, ws)
+    ws = torch.empty(kd.kd_attn_workspace_bytes(5, 32, 128, 2300), dtype=torch.uint8, device="cuda")
+    kd.kd_attn_append_decode(c.dq, c.dk, c.dv, *c.dev, c.slots, c.pos, 32, 8, 128, c.n_slots, 2300, out, ws)
     torch.cuda.synchronize()
     assert np.array_equal(out.cpu().numpy(), got.view(np.int16))
 
@@ -234,7 +236,7 @@ def windowed_step(shape, w, tok, pos, cache, window, sinks, q8):
     return oracle.matvec_q8_0(w["output"], oracle.rmsnorm_f16(x, w["output_norm"], s.rms_eps))
 
 
-@pytest.mark.parametrize("name,flags", [("hd64", 0), ("hd64", 1), ("hd64", 64), ("hd128", 0), ("q8", 0), ("q8", 1)])
+@pytest.mark.parametrize("name,flags", [("hd64", 0), ("hd64", 1), ("hd64", 64), ("hd128", 0), ("wide", 0), ("q8", 0), ("q8", 1)])
 def test_model_window_steps(kdlib, name, flags):
     """Steps with a window, teacher-forced, logits within the step's gate (5e-2); then each session alone (the
     same bits), and with the window off again the plain step's bits."""
@@ -242,7 +244,7 @@ def test_model_window_steps(kdlib, name, flags):
     q8 = name == "q8"
     shape = synth.TINY if name == "hd64" else synth.TINY_HD128
     w = dict(synth.model_weights(shape, 0), **synth.norm_weights(shape, 5))
-    cap, lens, window, sinks = 256, (150, 20, 201), 70, 3
+    cap, lens, window, sinks = (256, (150, 20, 201), 70, 3) if name != "wide" else (2600, (2450, 20, 2201), 2150, 3)
     flags |= kd.KD_FLAG_KV_Q8_0 if q8 else 0
 
     def load(which):
@@ -306,9 +308,9 @@ def test_window_wait_timeout_is_reported(kdlib, name):
     kd = kdlib
     shape = synth.TINY if name == "hd64" else synth.TINY_HD128
     w = synth.model_weights(shape, 0)
-    m = kd.kd_model_load(kd.make_config(shape, 2, 256, kd.KD_FLAG_KV_Q8_0 if name == "q8" else 0), w)
+    m = kd.kd_model_load(kd.make_config(shape, 2, 4096, kd.KD_FLAG_KV_Q8_0 if name == "q8" else 0), w)
     try:
-        kd.kd_model_set_window(m, 70, 3)
+        kd.kd_model_set_window(m, 3500, 3)  # wide: the split kernel, whose waits are bounded
         sid = kd.kd_session_bind(m)
         kd.kd_session_load_kv(m, sid, *synth.kv_prefill(shape, 0, 0, 150), 150)
         lg = torch.empty(1, shape.vocab, device="cuda")
