@@ -566,7 +566,8 @@ static cudaError_t enqueue_step(kd_model* m, int B, float* lg, int* am, cudaStre
         }
         const bool chain = window_chain(m);
         if (chain) {
-            KD_RUN(KD_K_ATTN_SPLIT, kd::launch_attn_chain(tw, pdl, s));
+            KD_RUN(KD_K_ATTN_SPLIT, kd::launch_attn_chain(
+                                        tw, (int)std::min<int64_t>((int64_t)m->window + m->sinks, c.max_ctx), m->num_sms, pdl, s));
         } else if (!m->kvq8) {
             KD_RUN(KD_K_ATTN_SPLIT, win ? kd::launch_attn_split(tw, m->kmaps, m->attn_grid, pdl, s)
                                         : kd::launch_attn_split(t, m->kmaps, m->attn_grid, pdl, s));

@@ -88,5 +88,6 @@ cudaError_t launch_attn_combine(const AttnWinArgs& a, bool pdl, cudaStream_t s);
 // merge 12.0; from about 2000 keys on, one row's chains take longer than the split.
 constexpr int WIN_CHAIN_ITEMS = 32;
 cudaError_t attn_chain_init_attributes();
-cudaError_t launch_attn_chain(const AttnWinArgs& a, bool pdl, cudaStream_t s);
+// max_keys: no row sees more.
+cudaError_t launch_attn_chain(const AttnWinArgs& a, int max_keys, int num_sms, bool pdl, cudaStream_t s);
 }  // namespace kd

@@ -33,6 +33,7 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     if ((u16 & 15) || ((uintptr_t)q & 7))
         return failf(KD_ERR_INVALID_ARG, "%s: caches and workspace must be 16-byte aligned, q %d-byte", fn, q8 ? 16 : 8);
     AttnWinArgs t{};
+    int max_keys = 0;
     for (int b = 0; b < B; ++b) {
         if (slots[b] < 0 || slots[b] >= n_slots) return failf(KD_ERR_BAD_SESSION, "%s: slot %d", fn, slots[b]);
         for (int j = 0; j < b; ++j)
@@ -41,6 +42,8 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
             return failf(KD_ERR_POSITION, "%s: position %d outside [0, %d)", fn, positions[b], cap);
         t.vslot[b] = slots[b];
         t.vpos[b] = positions[b];
+        const int64_t seen = (int64_t)window + sinks < positions[b] + 1 ? window + sinks : positions[b] + 1;
+        if (seen > max_keys) max_keys = (int)seen;
     }
     int dev = 0, sms = 0;
     KD_TRY(cudaGetDevice(&dev));
@@ -73,7 +76,7 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     t.kc = (const __half*)kc;
     t.vc = (const __half*)vc;
     if (!q8 && t.max_splits <= WIN_CHAIN_ITEMS) {
-        KD_TRY(launch_attn_chain(t, false, s));
+        KD_TRY(launch_attn_chain(t, max_keys, sms, false, s));
         return KD_OK;
     }
     AttnMaps maps;

@@ -158,9 +158,11 @@ def test_window_of_everything_equals_the_plain_call(kdlib):
     assert np.array_equal(out.cpu().numpy(), got.view(np.int16))
 
 
-@pytest.mark.parametrize("q8", [False, True])
-def test_window_rows_do_not_depend_on_the_batch(kdlib, q8):
-    c = Case(q8, 11, 16, 4, 128, 5000, list(range(17, 4900, 305))[:16], 700, 9)
+# short windows run on two CTAs per row and KV head or on one, by the batch; both are met here
+@pytest.mark.parametrize("q8,nh,nkv,hd,window", [(False, 16, 4, 128, 700), (True, 16, 4, 128, 700), (False, 32, 8, 128, 1300),
+                                                 (False, 8, 8, 64, 1990), (False, 64, 8, 128, 1024), (False, 8, 8, 128, 3000)])
+def test_window_rows_do_not_depend_on_the_batch(kdlib, q8, nh, nkv, hd, window):
+    c = Case(q8, 11, nh, nkv, hd, 5000, list(range(17, 4900, 305))[:16], window, 9)
     got = c.run(kdlib)
     c.check(got)
     for b in (0, 1, 7, 15):
