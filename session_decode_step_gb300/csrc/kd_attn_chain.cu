@@ -135,8 +135,9 @@ __global__ void __launch_bounds__(chain_warps(GQ) * 32, 1) attn_chain_kernel(con
         const int nx = item + 2 * NW;
         return PAIR || nx < n_items || item % (2 * NW) >= NW ? nx : first + NW;
     };
-    // The step's new row is written by the kernel before: a piece without it is fetched before the wait.
-    const bool early = append || (first + 1) * CH_KEYS < nvis;
+    // In the step the kernel before writes the new row and nothing else of the cache: a
+    // piece without that row is fetched before the wait.
+    const bool early = !append && (first + 1) * CH_KEYS < nvis;
     pdl_launch_dependents();
     if (!early) pdl_wait();
     issue(first, 0);
@@ -355,9 +356,9 @@ __global__ void __launch_bounds__(chain_warps(GQ) * 32, 1) attn_chain_kernel(con
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, x));
         const float e = lane < chains ? expf(__fsub_rn(ml.x, M == -INFINITY ? 0.0f : M)) : 0.0f;
-        float den = 0.0f;
-        for (int x = 0; x < chains; ++x)
-            den = __fmaf_rn(__shfl_sync(FULL_MASK, e, x), __shfl_sync(FULL_MASK, ml.y, x), den);
+        float den = __fmul_rn(e, ml.y);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) den = __fadd_rn(den, __shfl_xor_sync(FULL_MASK, den, x));
         if (lane < 2 * NW) weight[warp][lane] = e;
         if (lane == 0) denom[warp] = den;
     }

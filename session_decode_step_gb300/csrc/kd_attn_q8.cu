@@ -174,8 +174,6 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
         }
         *cta_failed = 0;
         if (a.inject_tx && blockIdx.x == 0) mbar_expect_tx(&bar[0], (uint32_t)a.inject_tx);  // debug fault hook
-        if constexpr (WIN)
-            if (a.clear_err && blockIdx.x == 0) *a.err = 0;
     }
     __syncthreads();
 
@@ -225,7 +223,9 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
     auto first_parts = [&](int k) { return (k < SK ? 1 : 0) | (k < SV ? 2 : 0); };
     for (int i = 0, k = warp; k < SMAX && k < nk; ++i, k += W) {
         const AttnItem it = tab.item(a, lane, gitem(k));
-        if (it.s != it.ns - 1) {
+        bool history = it.s != it.ns - 1;  // in the step; an op-level call may follow a writer of any row
+        if constexpr (WIN) history = history && !a.k_new;
+        if (history) {
             if (lane == 0) issue(it, k, first_parts(k));
             early |= 1u << i;
         }
@@ -233,6 +233,8 @@ __global__ void __launch_bounds__(AttnQ8Smem::warps(GQ) * 32, 1)
     pdl_launch_dependents();  // dependents may become resident now; they still wait for this grid
     pdl_wait();
     tl_waited(a.tl);
+    if constexpr (WIN)
+        if (a.clear_err && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
     for (int i = 0, k = warp; k < SMAX && k < nk; ++i, k += W)
         if (!((early >> i) & 1u)) {
             const AttnItem it = tab.item(a, lane, gitem(k));

@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
         if (b < nb) beam_fetch<VEC>(beam_smem + (b % BS_STAGES) * BS_STEP, row + e0, a.V - e0, t);
         cp_async_commit();
     };
+    pdl_wait();
     fetch(0);  // in flight while the beam's state is read
     if (!beam_live(a.scores, a.done, r)) {
         cp_async_wait<0>();
@@ -471,10 +472,11 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
     __shared__ float row_m[KD_BEAM_MAX_BEAMS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp < a.W ? warp : warp - a.W;
     const int g = blockIdx.x, r = g * a.W + w, K = a.K;
-    const bool live = beam_live(a.scores, a.done, r);
-    const float score = a.scores ? a.scores[r] : 0.0f;  // the call's own inputs: complete before its first launch
     const LogEntry tab = log_entry(lane);
+    pdl_launch_dependents();
     pdl_wait();
+    const bool live = beam_live(a.scores, a.done, r);
+    const float score = a.scores ? a.scores[r] : 0.0f;
     unsigned long long x = 0ull;  // warps < W: the row's 32 best logits
     if (warp >= a.W) {
         // L = M + log sum_b s_b e^{m_b - M}; the sum in units of 2^-40 (a block's is at most 8192, the largest's at least 1)
@@ -645,20 +647,24 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
     a.part = reinterpret_cast<float2*>(a.keys + (size_t)rows * a.nseg * n_out);
     const dim3 grid(a.nseg, rows);
     const int smem = beam_scan_smem(a.seg_blocks);
-    if (ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0)
-        beam_scan_kernel<true><<<grid, BS_THREADS, smem, s>>>(a);
-    else
-        beam_scan_kernel<false><<<grid, BS_THREADS, smem, s>>>(a);
-    KD_TRY(cudaGetLastError());
+    // Both launches may start while the kernel before them ends; they wait for it first.
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(BS_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    if (ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0)
+        KD_TRY(cudaLaunchKernelEx(&cfg, beam_scan_kernel<true>, a));
+    else
+        KD_TRY(cudaLaunchKernelEx(&cfg, beam_scan_kernel<false>, a));
     cfg.gridDim = dim3(n_groups);
     cfg.blockDim = dim3(64 * n_beams);
-    cfg.stream = s;
+    cfg.dynamicSmemBytes = 0;
     KD_TRY(cudaLaunchKernelEx(&cfg, beam_merge_kernel, a));
     return KD_OK;
 }

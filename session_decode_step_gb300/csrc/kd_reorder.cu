@@ -136,6 +136,7 @@ __device__ __forceinline__ void reorder_plane(const ReorderMove* moves, const Re
 // Block (x, y): run x of the planes' ranges' tiles, (layer, head) y.
 template <int CAP>
 __global__ void __launch_bounds__(RO_THREADS, 3) kv_reorder_kernel(const __grid_constant__ ReorderArgs<CAP> a) {
+    pdl_launch_dependents();
     int p = 0;
     while (p + 1 < a.n_planes && (int)blockIdx.x >= a.plane0[p + 1]) ++p;
     const int t = (int)blockIdx.x - a.plane0[p];
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(RO_THREADS, 3) kv_reorder_kernel(const __grid_
     const size_t slab_bytes = (size_t)a.cap * row_bytes, slot_bytes = slab_bytes * a.heads;
     char* slab = (char*)a.plane[p].base + (size_t)layer * a.slots * slot_bytes + head * slab_bytes;
     const int tile = (t - s.run0[p]) * a.run;
+    pdl_wait();
     if (row_bytes % 16 == 0)
         reorder_plane<uint4>(a.move, s, slab, slot_bytes, row_bytes, tile, a.run);
     else
@@ -263,8 +265,16 @@ static cudaError_t launch_reorder(const ReorderPlan& p, const int32_t* dst, cons
         }
         a.runs += runs;
     }
-    kv_reorder_kernel<CAP><<<dim3(a.runs, p.layers * p.heads), RO_THREADS, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};  // may start while the kernel before it ends; waits for it first
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(a.runs, p.layers * p.heads);
+    cfg.blockDim = dim3(RO_THREADS);
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, kv_reorder_kernel<CAP>, a);
 }
 
 cudaError_t launch_kv_reorder(const ReorderPlan& p, const int32_t* dst, const int32_t* src, const int32_t* len, int n,

@@ -76,7 +76,7 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     t.kc = (const __half*)kc;
     t.vc = (const __half*)vc;
     if (!q8 && t.max_splits <= WIN_CHAIN_ITEMS) {
-        KD_TRY(launch_attn_chain(t, max_keys, sms, false, s));
+        KD_TRY(launch_attn_chain(t, max_keys, sms, true, s));
         return KD_OK;
     }
     AttnMaps maps;
@@ -86,10 +86,10 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     const int grid = t.vitems < per ? t.vitems : per;
     if (q8) {
         KD_TRY(make_attn_q8_maps((const uint8_t*)kc, (const uint8_t*)vc, rows, &maps));
-        KD_TRY(launch_attn_split_q8(t, maps, grid, false, s));
+        KD_TRY(launch_attn_split_q8(t, maps, grid, true, s));
     } else {
         KD_TRY(make_attn_maps((const __half*)kc, (const __half*)vc, rows, hd, &maps));
-        KD_TRY(launch_attn_split(t, maps, grid, false, s));
+        KD_TRY(launch_attn_split(t, maps, grid, true, s));
     }
     KD_TRY(launch_attn_combine(t, true, s));
     return KD_OK;
