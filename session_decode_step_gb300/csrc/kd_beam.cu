@@ -329,6 +329,12 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
         float m = x[0];
 #pragma unroll
         for (int i = 1; i < BS_VPT; ++i) m = fmaxf(m, x[i]);
+        // Candidates are logits >= lo: those above thr (the next value up).  A warp without
+        // any is done with the stage once it holds the logits, and refills it at once.
+        float lo = beam_unord(beam_ord(thr) + 1u);
+        const bool renew = b == 0 || b == 3 || b == 15 || b == 63;
+        const bool none = !renew && !__any_sync(FULL_MASK, m >= lo);
+        if (none) fetch(b + BS_STAGES);
         float s;
         {  // two logits per instruction (packed fp32 adds and products)
             const unsigned long long nm = pack2(-m, -m), l2 = pack2(LOG2E, LOG2E);
@@ -369,11 +375,9 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
             st = 0.0f;
         }
 
-        // Candidates are logits >= lo: those above thr (the next value up), and no less
-        // than the K-th largest subset maximum of the blocks seen, this one included.
-        float lo = beam_unord(beam_ord(thr) + 1u);
         mrun = fmaxf(mrun, m);
-        if (b == 0 || b == 3 || b == 15 || b == 63) {
+        if (none) continue;
+        if (renew) {  // and no less than the K-th largest subset maximum of the blocks seen, this one included
             float* sub = subset[b == 0 ? 0 : b == 3 ? 1 : b == 15 ? 2 : 3];
             float m8 = mrun;
             m8 = fmaxf(m8, __shfl_xor_sync(FULL_MASK, m8, 1));
@@ -613,8 +617,12 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
         return failf(KD_ERR_INVALID_ARG, "kd_beam_select: eos=%d (finished beams need one in [0, %d))", eos, V);
     if (workspace_bytes < kd_beam_workspace_bytes(n_groups, n_beams, V, n_out))
         return failf(KD_ERR_INVALID_ARG, "kd_beam_select: workspace too small");
-    if ((reinterpret_cast<uintptr_t>(workspace) & 15) || (reinterpret_cast<uintptr_t>(logits) & 3))
-        return failf(KD_ERR_INVALID_ARG, "kd_beam_select: the workspace must be 16-byte aligned, logits 4-byte");
+    uintptr_t words = 0;
+    for (const void* p : {(const void*)logits, (const void*)scores, (const void*)done, (const void*)parents_out,
+                          (const void*)tokens_out, (const void*)scores_out, (const void*)done_out})
+        words |= reinterpret_cast<uintptr_t>(p);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 15) || (words & 3))
+        return failf(KD_ERR_INVALID_ARG, "kd_beam_select: the workspace must be 16-byte aligned, the other buffers 4-byte");
     BeamArgs a{};
     const int rows = n_groups * n_beams;
     a.logits = logits;

@@ -32,6 +32,8 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     const uintptr_t u16 = (uintptr_t)ws | (uintptr_t)kc | (uintptr_t)vc | (uintptr_t)ks | (uintptr_t)vs | (q8 ? (uintptr_t)q : 0);
     if ((u16 & 15) || ((uintptr_t)q & 7))
         return failf(KD_ERR_INVALID_ARG, "%s: caches and workspace must be 16-byte aligned, q %d-byte", fn, q8 ? 16 : 8);
+    if ((((uintptr_t)k_new | (uintptr_t)v_new) & 3) || ((uintptr_t)out & 1))
+        return failf(KD_ERR_INVALID_ARG, "%s: k_new and v_new must be 4-byte aligned, out 2-byte", fn);
     AttnWinArgs t{};
     int max_keys = 0;
     for (int b = 0; b < B; ++b) {

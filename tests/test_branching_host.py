@@ -49,6 +49,7 @@ def window_q8(lib, q=D, ks=D, B=2, nh=32, nkv=8, n_slots=4, cap=64, win=16, sink
     (dict(win=0), INVALID), (dict(win=-1), INVALID), (dict(sinks=-1), INVALID),
     (dict(n_slots=1 << 20, cap=65536), UNSUPPORTED),  # 2^39 cache rows
     (dict(ws_bytes=256), INVALID), (dict(ws=D + 8), INVALID), (dict(kc=D + 8), INVALID), (dict(q=D + 4), INVALID),
+    (dict(kn=D + 2), INVALID), (dict(out=D + 1), INVALID),
     (dict(sl=arr(1, 1)), BAD_SESSION), (dict(sl=arr(0, 4)), BAD_SESSION), (dict(sl=arr(-1, 1)), BAD_SESSION),
     (dict(ps=arr(0, 64)), POSITION), (dict(ps=arr(-1, 0)), POSITION),
 ])
@@ -84,6 +85,7 @@ def beam(lib, logits=D, ld=1000, G=2, W=4, V=1000, scores=D, done=None, eos=-1, 
 @pytest.mark.parametrize("change,status", [
     (dict(logits=None), INVALID), (dict(par=None), INVALID), (dict(tok=None), INVALID), (dict(sc=None), INVALID),
     (dict(ws=None), INVALID), (dict(logits=D + 2), INVALID), (dict(ws=D + 8), INVALID),
+    (dict(scores=D + 2), INVALID), (dict(par=D + 1), INVALID), (dict(tok=D + 2), INVALID), (dict(sc=D + 3), INVALID),
     (dict(G=0), BATCH), (dict(W=0), BATCH), (dict(W=17), BATCH), (dict(G=5000, W=16), BATCH),
     (dict(n_out=0), INVALID), (dict(n_out=33), INVALID),
     (dict(V=0), INVALID), (dict(ld=999), INVALID), (dict(V=524289, ld=524289), UNSUPPORTED),

@@ -233,3 +233,19 @@ def test_results_match_bitwise_between_runs(kdlib):
     for _ in range(5):
         for a, b in zip(c.run(), first):
             assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("G,W,dead", [(152, 1, 0.5), (39, 4, 0.3), (64, 16, 0.9), (1024, 1, 0.2), (1025, 1, 0.2),
+                                      (40, 8, 1.0), (40, 8, 0.0)])
+def test_many_rows_of_which_some_offer_nothing(kdlib, G, W, dead):
+    rng = np.random.default_rng(G + W)
+    V, n = 4100, 5
+    x = (rng.standard_normal((G * W, V)) * 2.5).astype(np.float32)
+    scores = (-4 * rng.random(G * W)).astype(np.float32)
+    gone, done = rng.random(G * W) < dead, np.zeros(G * W, np.int32)
+    done[gone & (rng.random(G * W) < 0.5)] = 1
+    scores[gone & (done == 0)] = [-np.inf, np.nan][G % 2]
+    x[gone] = np.nan  # never used
+    go(kdlib, x, W, n, scores=scores, done=done, eos=7)
+    if dead in (0.0, 1.0):
+        go(kdlib, np.where(np.isnan(x), 1, x).astype(np.float32), W, n)  # neither scores nor end marks
