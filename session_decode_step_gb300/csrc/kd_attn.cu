@@ -453,18 +453,20 @@ constexpr int COMB_UNROLL = 8;
 // warps of the merge: 4 up to 64 splits (4096 positions) of capacity, 32 beyond
 __host__ __device__ constexpr int comb_warps(int max_splits) { return max_splits <= 64 ? 4 : 32; }
 
-// Windowed rows have fewer: 8 warps serve up to 256 splits.
+// Windowed rows: 8 warps serve up to 256 splits (16 rows of 130 splits: split and merge
+// 97 us with 8 warps, 103 with 32, 101 with 4).
 __host__ __device__ constexpr int win_comb_warps(int max_splits) { return max_splits <= 64 ? 4 : max_splits <= 256 ? 8 : 32; }
 
-template <int HD, int NW, bool WIN>
+// DPL: dims per lane; below HD / 32 the head's dims are shared by the blocks of the
+// grid's z (each sum is the same, whichever block forms it).
+template <int HD, int NW, bool WIN, int DPL = HD / 32>
 __global__ void __launch_bounds__(NW * 32) attn_combine_kernel(const __grid_constant__ AttnArgsOf<WIN> a) {
-    constexpr int DPL = HD / 32;  // dims per lane
-    constexpr int NT = NW * 32;
-    static_assert(DPL == 2 || DPL == 4, "head_dim 64 or 128");
-    using VecT = typename std::conditional<DPL == 4, float4, float2>::type;
+    constexpr int NT = NW * 32, DIMS = 32 * DPL;
+    static_assert(DPL == 1 || DPL == 2 || DPL == 4, "head_dim 64 or 128");
+    using VecT = typename std::conditional<DPL == 4, float4, typename std::conditional<DPL == 2, float2, float>::type>::type;
     __shared__ float wts[COMB_MAX_SPLITS], ls[COMB_MAX_SPLITS];
     __shared__ float red_m[NW], red_l[NW];
-    __shared__ __align__(16) float part[NW][HD];
+    __shared__ __align__(16) float part[NW][DIMS];
     tl_entry(a.tl);
     pdl_launch_dependents();  // dependents may become resident now; they still wait for this grid
     const int b = blockIdx.y, h = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -489,7 +491,8 @@ __global__ void __launch_bounds__(NW * 32) attn_combine_kernel(const __grid_cons
     if constexpr (WIN) ns = win_plan(pos_b, a.window, a.sinks).ns;
     // the warp's range of splits, and its first records
     const int s0 = (int)(((long)ns * warp) / NW), s1 = (int)(((long)ns * (warp + 1)) / NW);
-    const float* pl = p + lane * DPL;
+    const int d0 = DIMS < HD ? (int)blockIdx.z * DIMS : 0;
+    const float* pl = p + d0 + lane * DPL;
     VecT o[COMB_UNROLL];
 #pragma unroll
     for (int u = 0; u < COMB_UNROLL; ++u)
@@ -549,11 +552,11 @@ __global__ void __launch_bounds__(NW * 32) attn_combine_kernel(const __grid_cons
 #pragma unroll
     for (int i = 0; i < DPL; ++i) part[warp][lane * DPL + i] = num[i];
     __syncthreads();
-    for (int d = t; d < HD; d += NT) {
+    for (int d = t; d < DIMS; d += NT) {
         float n = part[0][d];
 #pragma unroll
         for (int w = 1; w < NW; ++w) n = __fadd_rn(n, part[w][d]);
-        a.out[(size_t)b * a.nh * HD + (size_t)h * HD + d] = __float2half_rn(__fdiv_rn(n, L));
+        a.out[(size_t)b * a.nh * HD + (size_t)h * HD + d0 + d] = __float2half_rn(__fdiv_rn(n, L));
     }
     tl_exit(a.tl);
 }
@@ -608,6 +611,8 @@ cudaError_t attn_init_attributes() {
                           (const void*)attn_combine_kernel<64, 32, false>, (const void*)attn_combine_kernel<64, 32, true>,
                           (const void*)attn_combine_kernel<128, 32, false>, (const void*)attn_combine_kernel<128, 32, true>,
                           (const void*)attn_combine_kernel<64, 8, true>, (const void*)attn_combine_kernel<128, 8, true>,
+                          (const void*)attn_combine_kernel<128, 4, true, 1>, (const void*)attn_combine_kernel<128, 8, true, 1>,
+                          (const void*)attn_combine_kernel<128, 32, true, 1>,
                           (const void*)kv_append_kernel})
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                       cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
@@ -702,6 +707,10 @@ cudaError_t launch_attn_split(const AttnWinArgs& a, const AttnMaps& maps, int gr
     return launch_split<true>(a, maps, grid, pdl, s);
 }
 
+// heads x rows up to which a windowed head's dims are shared by four blocks: one row of
+// 32 heads over 50000 keys 40.2 us against 42.9, over 8192 keys 12.2 against 12.6; at
+// 128 (4 rows, 8192 keys) 28.6 against 26.9, as every block reads the weights.
+constexpr int WIN_COMB_SHARED = 64;
 template <bool WIN>
 static cudaError_t launch_combine(const AttnArgsOf<WIN>& a, bool pdl, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
@@ -712,6 +721,13 @@ static cudaError_t launch_combine(const AttnArgsOf<WIN>& a, bool pdl, cudaStream
     cfg.blockDim = dim3(nw * 32);
     cfg.stream = s;
     if constexpr (WIN) {
+        // Few heads and rows leave most SMs idle: a head's dims go to four blocks then.
+        if (a.hd == 128 && a.nh * a.B <= WIN_COMB_SHARED) {
+            cfg.gridDim.z = 4;
+            return nw == 4   ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 4, true, 1>, a)
+                   : nw == 8 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 8, true, 1>, a)
+                             : cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 32, true, 1>, a);
+        }
         if (nw == 8 && a.hd == 64) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 8, true>, a);
         if (nw == 8 && a.hd == 128) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 8, true>, a);
     }
