@@ -308,8 +308,8 @@ kd_status kd_device_status(kd_model* m, int32_t* flags_out);
  * barrier runs out after its time limit (about half a second), the kernel sets
  * the fault word and returns, and the step's outputs are invalid.  Nothing
  * faults or hangs.  One-shot.  Errors: KD_ERR_INVALID_ARG for another class, and
- * for KD_K_ATTN_SPLIT while a window of at most 2048 keys over fp16 rows is set
- * (that attention waits on no barrier). */
+ * for KD_K_ATTN_SPLIT while a window is set over an fp16 cache (that attention
+ * waits on no barrier). */
 kd_status kd_debug_inject_wait_timeout(kd_model* m, int32_t kernel_class);
 
 /* Measurement (the event-based counterpart of memra's per-phase breakdown,

@@ -416,11 +416,8 @@ static bool fused_norm(const kd_model* m, const PackedQ8& p) {
 static bool embed_norm(const kd_model* m) {
     return !(m->cfg.flags & KD_FLAG_UNFUSED) && !fused_norm(m, m->qkv[0]);
 }
-// A windowed step's attention is one launch (short windows over fp16 rows).
-static bool window_chain(const kd_model* m) {
-    return m->window > 0 && !m->kvq8 &&
-           kd::win_max_items(m->cfg.max_ctx, m->window, m->sinks) <= kd::WIN_CHAIN_ITEMS;
-}
+// A windowed step's attention over fp16 rows is one launch.
+static bool window_chain(const kd_model* m) { return m->window > 0 && !m->kvq8; }
 // The lm_head launch makes each row's pick itself (stream schedule, fused train).
 static bool head_pick(const kd_model* m) {
     return !(m->cfg.flags & KD_FLAG_UNFUSED) && m->head.mode == kd::MMVQ_STREAM;
@@ -569,8 +566,7 @@ static cudaError_t enqueue_step(kd_model* m, int B, float* lg, int* am, cudaStre
             KD_RUN(KD_K_ATTN_SPLIT, kd::launch_attn_chain(
                                         tw, (int)std::min<int64_t>((int64_t)m->window + m->sinks, c.max_ctx), m->num_sms, pdl, s));
         } else if (!m->kvq8) {
-            KD_RUN(KD_K_ATTN_SPLIT, win ? kd::launch_attn_split(tw, m->kmaps, m->attn_grid, pdl, s)
-                                        : kd::launch_attn_split(t, m->kmaps, m->attn_grid, pdl, s));
+            KD_RUN(KD_K_ATTN_SPLIT, kd::launch_attn_split(t, m->kmaps, m->attn_grid, pdl, s));
         } else {  // quantised append of the new rows, then the attention over the Q8_0 cache
             KD_RUN(KD_K_ATTN_SPLIT, kd::launch_kvq8_append(m->knew, m->vnew, m->kq, m->ks, m->vq, m->vs, slot, pos, B,
                                                            nkv, c.max_ctx, t.row0, pdl, s));
@@ -1089,7 +1085,7 @@ kd_status kd_device_status(kd_model* m, int32_t* flags_out) {
 kd_status kd_debug_inject_wait_timeout(kd_model* m, int32_t kernel_class) {
     if (!m) return fail(KD_ERR_INVALID_ARG, "kd_debug_inject_wait_timeout: null model");
     if (kernel_class == KD_K_ATTN_SPLIT && window_chain(m))
-        return fail(KD_ERR_INVALID_ARG, "kd_debug_inject_wait_timeout: the attention of this window has no bounded wait");
+        return fail(KD_ERR_INVALID_ARG, "kd_debug_inject_wait_timeout: windowed attention over fp16 rows has no bounded wait");
     switch (kernel_class) {
         case KD_K_QKV: case KD_K_ATTN_SPLIT: case KD_K_WO: case KD_K_GATE_UP: case KD_K_DOWN: case KD_K_LM_HEAD:
             m->inject_cls = kernel_class;

@@ -21,7 +21,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "kd_attn_common.cuh"
 
@@ -50,25 +49,6 @@ struct AttnSmem {
     }
 };
 
-// Part 0 (K) or 1 (V) of the item's new row: fp16 of the fp32 row, into the cache
-// and into the item's tile (tile: the lane's 16-byte chunk of the row there).
-template <int HD>
-__device__ __forceinline__ uint4 win_new_row(const AttnWinArgs& a, const AttnItem& it, int lane, int part) {
-    const float* src = (part ? a.v_new : a.k_new) + ((size_t)it.b * a.nkv + it.kvh) * HD + 8 * (lane % (HD / 8));
-    return make_uint4(f2_hi(src[0], src[1]), f2_hi(src[2], src[3]), f2_hi(src[4], src[5]), f2_hi(src[6], src[7]));
-}
-template <int HD>
-__device__ __forceinline__ void win_append_row(const AttnWinArgs& a, const AttnItem& it, int lane, int part,
-                                               uint32_t tile, const uint4& w) {
-    if (lane < HD / 8) {
-        const size_t row = ((size_t)it.slot * a.nkv + it.kvh) * a.cap + it.start + it.n - 1;
-        *reinterpret_cast<uint4*>((__half*)(part ? a.v_dst : a.k_dst) + row * HD + 8 * lane) = w;
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
-                     : "memory");
-    }
-    __syncwarp();
-}
-
 // A CTA takes the items blockIdx.x + k * gridDim.x, k = 0, 1, ...: item k goes
 // through stage k % STAGES and is computed by warp k % AT_WARPS, which then
 // refills that stage with item k + STAGES: the K tile right after its scores,
@@ -81,12 +61,9 @@ __device__ __forceinline__ void win_append_row(const AttnWinArgs& a, const AttnI
 // rounded to fp16 and the remainder of that rounding, whose two products add
 // up to the fp32-accurate one.  K tiles are the A operand as stored, V tiles
 // through the transposing ldmatrix.
-// WIN: windowed rows (AttnWinTable): the items' first keys and hidden keys come
-// from the session's window; hidden keys get no weight and their values count
-// as zero (they may hold anything, NaN included).
-template <int HD, int GQ, bool WIN>
+template <int HD, int GQ>
 __global__ void __launch_bounds__(AT_WARPS * 32, 1)
-    attn_split_kernel(const __grid_constant__ AttnArgsOf<WIN> a, const __grid_constant__ CUtensorMap tmk,
+    attn_split_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmk8, const __grid_constant__ CUtensorMap tmv,
                       const __grid_constant__ CUtensorMap tmv8) {
     using L = AttnSmem<HD>;
@@ -105,27 +82,18 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
     volatile int* stage_item = reinterpret_cast<volatile int*>(smem + L::ITEM_OFF);
     volatile int* cta_failed = stage_item + 2 * S;
 
-    if (WIN && warp == 0 && lane < 2 * S) {  // a barrier per lane
-        mbar_init(&bar[lane], 1);
-        stage_item[lane] = -1;
-        mbar_init_fence();
-    }
-    if (WIN) __syncwarp();
-    static_assert(2 * S <= 32, "a lane per barrier");
     if (threadIdx.x == 0) {
-        if (!WIN) {
-            for (int i = 0; i < 2 * S; ++i) {
-                mbar_init(&bar[i], 1);
-                stage_item[i] = -1;
-            }
-            mbar_init_fence();
+        for (int i = 0; i < 2 * S; ++i) {
+            mbar_init(&bar[i], 1);
+            stage_item[i] = -1;
         }
         *cta_failed = 0;
+        mbar_init_fence();
         if (a.inject_tx && blockIdx.x == 0) mbar_expect_tx(&bar[0], (uint32_t)a.inject_tx);  // debug fault hook
     }
     __syncthreads();
 
-    AttnTableOf<WIN> tab;
+    AttnTable tab;
     tab.build(a, lane);
     const int n_items = tab.n_items;
     const int nk = (int)blockIdx.x < n_items ? (n_items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
@@ -138,11 +106,8 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
     auto issue = [&](const AttnItem& it, int k, int parts) {
         const int st = k % S;
         uint8_t* stg = smem + st * L::STAGE;
-        const int row = (int)(a.row0 + ((long)it.slot * a.nkv + it.kvh) * a.cap + item_start<WIN>(it));
-        // A ragged item is copied in 8-row boxes; a windowed one in the whole box (past
-        // its keys it reads rows that are masked) unless one 8-row box holds it: a box is
-        // about a hundred cycles of one lane, and every row ends in a ragged item.
-        const bool full = WIN ? it.n > 8 : it.n == AT_C;
+        const int row = (int)(a.row0 + ((long)it.slot * a.nkv + it.kvh) * a.cap + (long)it.s * AT_C);
+        const bool full = it.n == AT_C;
         const int krows = full ? AT_C : (it.n + 7) / 8 * 8;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
@@ -175,9 +140,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
     unsigned early = 0;
     for (int i = 0, k = warp; k < S && k < nk; ++i, k += AT_WARPS) {
         const AttnItem it = tab.item(a, lane, gitem(k));
-        bool history = it.s != it.ns - 1;  // in the step; an op-level call may follow a writer of any row
-        if constexpr (WIN) history = history && !a.k_new;
-        if (history) {
+        if (it.s != it.ns - 1) {
             if (lane == 0) issue(it, k, 3);
             early |= 1u << i;
         }
@@ -185,8 +148,6 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
     pdl_launch_dependents();  // dependents may become resident now; they still wait for this grid
     pdl_wait();
     tl_waited(a.tl);
-    if constexpr (WIN)
-        if (a.clear_err && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
     for (int i = 0, k = warp; k < S && k < nk; ++i, k += AT_WARPS)
         if (!((early >> i) & 1u)) {
             const AttnItem it = tab.item(a, lane, gitem(k));
@@ -238,28 +199,17 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
         }
         if (k + AT_WARPS < nk) load_q(tab.item(a, lane, gitem(k + AT_WARPS)));  // lands during this item
 
-        bool appends = false;
-        uint4 k_row{}, v_row{};  // the new row, on its way while the tile's copy lands
-        if constexpr (WIN) {
-            appends = a.k_new && it.s == it.ns - 1;
-            if (appends) {
-                k_row = win_new_row<HD>(a, it, lane, 0);
-                v_row = win_new_row<HD>(a, it, lane, 1);
-            }
-        }
         const uint32_t par = (uint32_t)(k / S) & 1u;
         bool ok = wait_value(stage_item + st, k);
         ok = ok && mbar_wait_bounded(&bar[st], par);  // the K tile
         if (__any_sync(FULL_MASK, !ok)) {
             if (lane == 0) {
-                report_wait<WIN>(a);
+                atomicOr(a.err, ERR_WAIT_TIMEOUT);
                 *cta_failed = 1;
             }
             break;
         }
         const int n = it.n;
-        if constexpr (WIN)
-            if (appends) win_append_row<HD>(a, it, lane, 0, kbase + (lane < HD / 8 ? L::off(n - 1, lane) : 0u), k_row);
         const bool refill = k + S < nk;
         AttnItem nx{};
         if (refill) nx = tab.item(a, lane, gitem(k + S));
@@ -295,7 +245,6 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
         }
         // ---- per head 4j + c: scores of keys 16m + g (e = 0) and 16m + g + 8 (e = 1);
         // scale, mask, softmax over the item's keys (the 8 lanes g of a head)
-        const bool hides = WIN && it.h0 < it.h1;  // one item of a row at most has hidden keys, or few
         float sv[NQ][AT_KT][2], mx[NQ], lsum[NQ];
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
@@ -307,7 +256,6 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
                     const float sc = __fadd_rn(sacc[m][j][2 * e], sacc[m][j][2 * e + 1]);  // both parts
                     const int key = 16 * m + g + 8 * e;
                     sv[j][m][e] = key < n ? __fmul_rn(sc, a.scale) : -INFINITY;
-                    if (WIN && hides && key >= it.h0 && key < it.h1) sv[j][m][e] = -INFINITY;
                     mx[j] = fmaxf(mx[j], sv[j][m][e]);
                 }
 #pragma unroll
@@ -330,7 +278,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
         ok = ok && mbar_wait_bounded(&bar[S + st], par);
         if (__any_sync(FULL_MASK, !ok)) {
             if (lane == 0) {
-                report_wait<WIN>(a);
+                atomicOr(a.err, ERR_WAIT_TIMEOUT);
                 *cta_failed = 1;
             }
             break;
@@ -341,16 +289,6 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
             const int z = ((n + 15) & ~15) - n;
             for (int e = lane; e < z * L::NREG * 8; e += 32) {
                 const int r = n + e / (L::NREG * 8), rem = e % (L::NREG * 8);
-                *reinterpret_cast<uint4*>(stg + L::K_BYTES + (rem >> 3) * L::HALF_BYTES + r * 128 + (rem & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            }
-            __syncwarp();
-        }
-        if constexpr (WIN)
-            if (appends) win_append_row<HD>(a, it, lane, 1, vbase + (lane < HD / 8 ? L::off(n - 1, lane) : 0u), v_row);
-        if (hides) {  // hidden rows of the V tile: p = 0 too
-            for (int e = lane; e < (it.h1 - it.h0) * L::NREG * 8; e += 32) {
-                const int r = it.h0 + e / (L::NREG * 8), rem = e % (L::NREG * 8);
                 *reinterpret_cast<uint4*>(stg + L::K_BYTES + (rem >> 3) * L::HALF_BYTES + r * 128 + (rem & 7) * 16) =
                     make_uint4(0u, 0u, 0u, 0u);
             }
@@ -408,11 +346,7 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
                     dst[16 * mt + g] = __fadd_rn(oacc[mt][j][0], oacc[mt][j][1]);
                     dst[16 * mt + g + 8] = __fadd_rn(oacc[mt][j][2], oacc[mt][j][3]);
                 }
-                if constexpr (WIN) {
-                    if (g == 0) *reinterpret_cast<float4*>(dst + HD) = make_float4(mx[j], lsum[j], __int_as_float(REC_VALID), 0.0f);
-                } else {
-                    if (g == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(mx[j], lsum[j]);
-                }
+                if (g == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(mx[j], lsum[j]);
             }
         }
 
@@ -431,8 +365,6 @@ __global__ void __launch_bounds__(AT_WARPS * 32, 1)
             const int k = stage_item[i];
             if (k >= 0) (void)mbar_wait_bounded(&bar[i], (uint32_t)(k / S) & 1u);
         }
-    if constexpr (WIN)
-        if (*cta_failed) mark_records(a, tab, lane, warp, AT_WARPS, nk, GQ, HD);
     tl_exit(a.tl);
 }
 
@@ -453,9 +385,10 @@ constexpr int COMB_UNROLL = 8;
 // warps of the merge: 4 up to 64 splits (4096 positions) of capacity, 32 beyond
 __host__ __device__ constexpr int comb_warps(int max_splits) { return max_splits <= 64 ? 4 : 32; }
 
-// Windowed rows: 8 warps serve up to 256 splits (16 rows of 130 splits: split and merge
-// 97 us with 8 warps, 103 with 32, 101 with 4).
-__host__ __device__ constexpr int win_comb_warps(int max_splits) { return max_splits <= 64 ? 4 : max_splits <= 256 ? 8 : 32; }
+// Windowed rows (of a Q8_0 cache; fp16 ones need no merge), split and merge of 32 heads:
+// 8 rows of 190 splits 48.4 us with 16 warps, 50.6 with 8, 50.5 with 32; 16 rows 93, 92,
+// 98; one row 16.7, 18.0, 15.2.
+__host__ __device__ constexpr int win_comb_warps(int max_splits) { return max_splits <= 64 ? 4 : max_splits <= 512 ? 16 : 32; }
 
 // DPL: dims per lane; below HD / 32 the head's dims are shared by the blocks of the
 // grid's z (each sum is the same, whichever block forms it).
@@ -589,30 +522,23 @@ bool attn_supported(int hd, int group) {
 
 cudaError_t attn_init_attributes() {
     cudaError_t e = cudaSuccess;
-#define KD_SET_ONE(f)                                                                           \
-    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);             \
-    if (e != cudaSuccess) return e;                                                             \
-    e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,                 \
-                             cudaSharedmemCarveoutMaxShared);                                   \
+#define KD_SET(HD_, GQ_)                                                                             \
+    e = cudaFuncSetAttribute(attn_split_kernel<HD_, GQ_>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
+                             AttnSmem<HD_>::TOTAL);                                                  \
+    if (e != cudaSuccess) return e;                                                                  \
+    e = cudaFuncSetAttribute(attn_split_kernel<HD_, GQ_>, cudaFuncAttributePreferredSharedMemoryCarveout, \
+                             cudaSharedmemCarveoutMaxShared);                                        \
     if (e != cudaSuccess) return e;
-#define KD_SET(HD_, GQ_)                             \
-    smem = AttnSmem<HD_>::TOTAL;                     \
-    KD_SET_ONE((attn_split_kernel<HD_, GQ_, false>)) \
-    KD_SET_ONE((attn_split_kernel<HD_, GQ_, true>))
-    int smem = 0;
     for (int group : {1, 2, 4, 8}) {
         KD_ATT_DISPATCH(64, KD_SET)
         KD_ATT_DISPATCH(128, KD_SET)
     }
 #undef KD_SET
-#undef KD_SET_ONE
-    for (const void* f : {(const void*)attn_combine_kernel<64, 4, false>, (const void*)attn_combine_kernel<64, 4, true>,
-                          (const void*)attn_combine_kernel<128, 4, false>, (const void*)attn_combine_kernel<128, 4, true>,
-                          (const void*)attn_combine_kernel<64, 32, false>, (const void*)attn_combine_kernel<64, 32, true>,
-                          (const void*)attn_combine_kernel<128, 32, false>, (const void*)attn_combine_kernel<128, 32, true>,
-                          (const void*)attn_combine_kernel<64, 8, true>, (const void*)attn_combine_kernel<128, 8, true>,
-                          (const void*)attn_combine_kernel<128, 4, true, 1>, (const void*)attn_combine_kernel<128, 8, true, 1>,
-                          (const void*)attn_combine_kernel<128, 32, true, 1>,
+    for (const void* f : {(const void*)attn_combine_kernel<64, 4, false>, (const void*)attn_combine_kernel<128, 4, false>,
+                          (const void*)attn_combine_kernel<64, 32, false>, (const void*)attn_combine_kernel<128, 32, false>,
+                          (const void*)attn_combine_kernel<128, 4, true>, (const void*)attn_combine_kernel<128, 4, true, 1>,
+                          (const void*)attn_combine_kernel<128, 16, true>, (const void*)attn_combine_kernel<128, 16, true, 1>,
+                          (const void*)attn_combine_kernel<128, 32, true>, (const void*)attn_combine_kernel<128, 32, true, 1>,
                           (const void*)kv_append_kernel})
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                       cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
@@ -621,22 +547,18 @@ cudaError_t attn_init_attributes() {
 }
 
 int attn_split_grid(int num_sms, int hd, int group) {
-    // persistent: as many CTAs as fit on every SM at once (asked once per kernel)
-    static std::atomic<int> known[2][4];
-    std::atomic<int>& k = known[hd == 128][group == 1 ? 0 : group == 2 ? 1 : group == 4 ? 2 : 3];
-    int per_sm = k.load(std::memory_order_relaxed);
-    if (per_sm > 0) return num_sms * per_sm;
+    // persistent: as many CTAs as fit on every SM at once
+    int per_sm = 1;
     cudaError_t e = cudaSuccess;
-#define KD_OCC(HD_, GQ_)                                                                            \
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_split_kernel<HD_, GQ_, false>, \
+#define KD_OCC(HD_, GQ_)                                                                     \
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_split_kernel<HD_, GQ_>, \
                                                       AT_WARPS * 32, AttnSmem<HD_>::TOTAL);
     auto run = [&]() -> cudaError_t {
         if (hd == 64) { KD_ATT_DISPATCH(64, KD_OCC) } else { KD_ATT_DISPATCH(128, KD_OCC) }
         return e;
     };
 #undef KD_OCC
-    if (run() != cudaSuccess || per_sm < 1) return num_sms;
-    k.store(per_sm, std::memory_order_relaxed);
+    if (run() != cudaSuccess || per_sm < 1) per_sm = 1;
     return num_sms * per_sm;
 }
 
@@ -684,8 +606,7 @@ static cudaError_t launch_cfg(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr
     return cudaSuccess;
 }
 
-template <bool WIN>
-static cudaError_t launch_split(const AttnArgsOf<WIN>& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s) {
+cudaError_t launch_attn_split(const AttnArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s) {
     const int group = a.nh / a.nkv;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -695,21 +616,15 @@ static cudaError_t launch_split(const AttnArgsOf<WIN>& a, const AttnMaps& maps, 
 #define KD_LAUNCH(HD_, GQ_)                                 \
     cfg.blockDim = dim3(AT_WARPS * 32);                     \
     cfg.dynamicSmemBytes = AttnSmem<HD_>::TOTAL;            \
-    return cudaLaunchKernelEx(&cfg, attn_split_kernel<HD_, GQ_, WIN>, a, maps.k, maps.k8, maps.v, maps.v8);
+    return cudaLaunchKernelEx(&cfg, attn_split_kernel<HD_, GQ_>, a, maps.k, maps.k8, maps.v, maps.v8);
     if (a.hd == 64) { KD_ATT_DISPATCH(64, KD_LAUNCH) } else if (a.hd == 128) { KD_ATT_DISPATCH(128, KD_LAUNCH) }
 #undef KD_LAUNCH
     return cudaErrorInvalidValue;
 }
-cudaError_t launch_attn_split(const AttnArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s) {
-    return launch_split<false>(a, maps, grid, pdl, s);
-}
-cudaError_t launch_attn_split(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s) {
-    return launch_split<true>(a, maps, grid, pdl, s);
-}
 
-// heads x rows up to which a windowed head's dims are shared by four blocks: one row of
-// 32 heads over 50000 keys 40.2 us against 42.9, over 8192 keys 12.2 against 12.6; at
-// 128 (4 rows, 8192 keys) 28.6 against 26.9, as every block reads the weights.
+// Heads x rows up to which a windowed head's dims are shared by four blocks, which leaves
+// fewer SMs idle: one row of 32 heads over 50000 keys of a Q8_0 cache 32.1 us against 34.7,
+// two over 4096 12.3 against 12.6.  Beyond, every block's own weights cost more.
 constexpr int WIN_COMB_SHARED = 64;
 template <bool WIN>
 static cudaError_t launch_combine(const AttnArgsOf<WIN>& a, bool pdl, cudaStream_t s) {
@@ -721,23 +636,25 @@ static cudaError_t launch_combine(const AttnArgsOf<WIN>& a, bool pdl, cudaStream
     cfg.blockDim = dim3(nw * 32);
     cfg.stream = s;
     if constexpr (WIN) {
-        // Few heads and rows leave most SMs idle: a head's dims go to four blocks then.
-        if (a.hd == 128 && a.nh * a.B <= WIN_COMB_SHARED) {
+        if (a.hd != 128) return cudaErrorInvalidValue;
+        if (a.nh * a.B <= WIN_COMB_SHARED) {
             cfg.gridDim.z = 4;
             return nw == 4   ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 4, true, 1>, a)
-                   : nw == 8 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 8, true, 1>, a)
+                   : nw == 16 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 16, true, 1>, a)
                              : cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 32, true, 1>, a);
         }
-        if (nw == 8 && a.hd == 64) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 8, true>, a);
-        if (nw == 8 && a.hd == 128) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 8, true>, a);
+        return nw == 4   ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 4, true>, a)
+               : nw == 16 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 16, true>, a)
+                         : cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 32, true>, a);
+    } else {
+        if (a.hd == 64)
+            return nw == 4 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 4, false>, a)
+                           : cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 32, false>, a);
+        if (a.hd == 128)
+            return nw == 4 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 4, false>, a)
+                           : cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 32, false>, a);
+        return cudaErrorInvalidValue;
     }
-    if (a.hd == 64)
-        return nw == 4 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 4, WIN>, a)
-                       : cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 32, WIN>, a);
-    if (a.hd == 128)
-        return nw == 4 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 4, WIN>, a)
-                       : cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 32, WIN>, a);
-    return cudaErrorInvalidValue;
 }
 cudaError_t launch_attn_combine(const AttnArgs& a, bool pdl, cudaStream_t s) { return launch_combine<false>(a, pdl, s); }
 cudaError_t launch_attn_combine(const AttnWinArgs& a, bool pdl, cudaStream_t s) { return launch_combine<true>(a, pdl, s); }

@@ -1,27 +1,37 @@
-// kd_attn_chain.cu -- windowed attention over fp16 rows in one launch, for windows
-// of up to WIN_CHAIN_ITEMS * 64 keys: no partial results in memory, no merge kernel.
+// kd_attn_chain.cu -- windowed attention over fp16 rows in one launch: KV append,
+// attention and merge, with few or no partial results in memory.
 //
 // A row's visible keys of one KV head -- the leading ones, then the window, as one
-// sequence -- are cut into pieces of 32; piece p belongs to chain p mod 2 NW, a
-// running maximum and sum over its pieces in order, and the 2 NW chains are merged
-// in order.  Pieces, chains and the merge depend on the row's own position, window
-// and sinks, so the result does not depend on the batch.  Where two CTAs per (row,
-// KV head) fit the GPU at once, a cluster of two takes them, a chain per warp, and
-// merges through distributed shared memory; else one CTA, whose warps take a chain
-// of the first half, then one of the second.
+// sequence -- are cut into pieces of 32; piece p belongs to chain p mod CHAINS, a
+// running maximum and sum over its pieces in order, and the chains are merged in a
+// fixed order.  Pieces, chains and the merge depend on the row's own position and on
+// the slot's capacity, window and sinks, so the result does not depend on the batch:
+// the chains of a (row, KV head) are taken by one CTA, each warp one after another,
+// or by a cluster of 2, 4 or 8 where that many fit the GPU at once, down to a chain
+// per warp; a cluster merges through distributed shared memory.
+//
+// Chains: 24 for capacities of up to WIN_CHAIN_ITEMS * 64 visible keys, 48 beyond (16
+// and 32 for groups of 8 heads, whose accumulators leave room for 8 warps).  More make
+// one row faster and many rows slower, as each ends in a record.  8192 keys of 8 KV
+// heads of 128, 1 / 4 / 16 rows: 24 chains 15.5 / 25.6 / 80.8 us, 48 chains 11.1 / 25.0 /
+// 84.9, 96 chains 10.8 / 25.1 / 91; at 2000 keys 24 chains 8.3 / 8.5 / 24.9, 48 chains
+// 8.5 / 9.2 / 27.2.  64-key splits with a record each and a second launch that merges
+// them: 12.2 / 26.9 / 95.1 and 6.9 / 11.1 / 27.5.
 //
 // Each warp copies its own pieces with 16-byte asynchronous copies into its own
-// buffer (a K and a V part, the next piece's copied while this one is computed),
+// buffers (a K and a V part each; CTAs with fewer warps keep several pieces in flight),
 // placed as the 128-byte swizzle does, so the products are the split kernel's.
-// Rows that do not exist are filled with zeros and never read.  No barrier is
+// Rows that do not exist are filled with zeros and never read.  No mbarrier is
 // waited on, so nothing can run out and the call's fault word is only cleared.
 //
-// What bounds it: with few rows the latency of a piece (copy, scores, softmax,
-// values) times the chain's length, and what one SM can draw (about 130 GB/s);
-// with many the copies, of which an SM holds 192 KB in flight.  Against split and merge: one launch instead of two,
-// and no 528-byte record per head and 64 keys written and read back.
+// What bounds it: with many rows HBM (16 rows over 8192 + 64 keys, 543 MB: 84.9 us,
+// 6.4 TB/s; 8 rows over 20000 keys 6.7), of which an SM holds 192 KB in flight; with few
+// the chain's latency, about 1 us a piece (copy, scores, softmax, values), after 4 us of
+// launch, first copies and merge.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "kd_attn_common.cuh"
 
@@ -49,13 +59,14 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool h
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the last committed group have landed, for every lane of the warp.
-__device__ __forceinline__ void cp_wait_but_one() {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+// All but the last N committed groups have landed, for every lane of the warp.
+template <int N>
+__device__ __forceinline__ void cp_wait_but() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
     __syncwarp();
 }
 
-// The other CTA of a cluster of two: its shared memory at the same offset, and a barrier of both.
+// Another CTA of the cluster: its shared memory at the same offset, and a barrier of all.
 __device__ __forceinline__ float4 ld_other4(uint32_t addr, uint32_t rank) {
     uint32_t ra;
     float4 v;
@@ -66,30 +77,54 @@ __device__ __forceinline__ float4 ld_other4(uint32_t addr, uint32_t rank) {
                  : "memory");
     return v;
 }
+__device__ __forceinline__ float2 ld_other2(uint32_t addr, uint32_t rank) {
+    uint32_t ra;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(ra) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_other(uint32_t addr, uint32_t rank) {
+    uint32_t ra;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra) : "memory");
+    return v;
+}
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// Bytes of the first half's records, which a single CTA keeps while its warps' buffers serve the second.
+// Bytes of a chain's record (its o by head, and m and l).
 template <int HD>
 __host__ __device__ constexpr int chain_record(int gq) { return gq * (HD + 4) * 4; }
+// R chains per warp of a full CTA (chain_warps), shared by a cluster of CS: a CTA's warps,
+// the chains that each takes one after another, and the pieces that it has in flight.
+__host__ __device__ constexpr int chain_cta_warps(int gq, int r, int cs) { return cs > r ? chain_warps(gq) * r / cs : chain_warps(gq); }
+__host__ __device__ constexpr int chain_turns(int r, int cs) { return cs > r ? 1 : r / cs; }
+__host__ __device__ constexpr int chain_depth(int r, int cs) { return cs > r ? cs / r : 1; }
+// The buffers, and behind them the records of the first turn while the buffers serve the others.
 template <int HD>
-constexpr int chain_smem_bytes(int gq, bool pair) {
-    return chain_warps(gq) * (ChainSmem<HD>::WARP + (pair ? 0 : chain_record<HD>(gq)));
+constexpr int chain_smem_bytes(int gq, int r, int cs) {
+    return chain_warps(gq) * (ChainSmem<HD>::WARP + (chain_turns(r, cs) > 1 ? chain_record<HD>(gq) : 0));
 }
 
-template <int HD, int GQ, bool PAIR>
-__global__ void __launch_bounds__(chain_warps(GQ) * 32, 1) attn_chain_kernel(const __grid_constant__ AttnWinArgs a) {
+template <int HD, int GQ, int R, int CS>
+__global__ void __launch_bounds__(chain_cta_warps(GQ, R, CS) * 32, 1)
+    attn_chain_kernel(const __grid_constant__ AttnWinArgs a) {
     using L = ChainSmem<HD>;
-    constexpr int NW = chain_warps(GQ);
+    constexpr int NW = chain_cta_warps(GQ, R, CS), P = chain_turns(R, CS), D = chain_depth(R, CS);
+    constexpr int CHAINS = R * chain_warps(GQ), AREA = D * L::WARP;
+    static_assert(P == 1 || D == 1, "one or the other");
     constexpr int KS = HD / 16, NU = HD / 8, CH = HD / 8;  // k-steps, 8-dim tiles, 16-byte chunks of a row
     constexpr int NQ = GQ > 4 ? GQ / 4 : 1;                // N-tiles of heads
     extern __shared__ __align__(1024) uint8_t chain_smem[];
     tl_entry(a.tl);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const int kvh = PAIR ? blockIdx.x >> 1 : blockIdx.x, b = blockIdx.y, rank = PAIR ? blockIdx.x & 1 : 0;
-    uint8_t* mine = chain_smem + warp * L::WARP;
+    const int kvh = blockIdx.x / CS, b = blockIdx.y, rank = blockIdx.x % CS;
+    uint8_t* mine = chain_smem + warp * AREA;
     const uint32_t kbase = smem_u32(mine), vbase = kbase + L::PART;
 
     const int pos = a.slot ? a.pos[b] : a.vpos[b], slot = a.slot ? a.slot[b] : a.vslot[b];
@@ -107,9 +142,9 @@ __global__ void __launch_bounds__(chain_warps(GQ) * 32, 1) attn_chain_kernel(con
     uint32_t place[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) place[j] = L::off(j * ROWS + lane / CH, lane % CH);
-    auto issue = [&](int item, int part) {
+    auto issue = [&](int item, int part, int slot) {
         if (item < n_items) {
-            const uint32_t dst = part ? vbase : kbase;
+            const uint32_t dst = (part ? vbase : kbase) + slot * L::WARP;
             const int v0 = item * CH_KEYS;
             const __half* src = (part ? vc : kc) + (lane % CH) * 8;
             if (v0 >= lead && v0 + CH_KEYS <= nread) {  // 32 rows of the window: consecutive
@@ -129,19 +164,18 @@ __global__ void __launch_bounds__(chain_warps(GQ) * 32, 1) attn_chain_kernel(con
         }
         cp_commit();
     };
-    // The warp's pieces: chain `first`, then (one CTA) the chain NW further.
-    const int first = warp + rank * NW;
-    auto after = [&](int item) {
-        const int nx = item + 2 * NW;
-        return PAIR || nx < n_items || item % (2 * NW) >= NW ? nx : first + NW;
-    };
-    // In the step the kernel before writes the new row and nothing else of the cache: a
-    // piece without that row is fetched before the wait.
-    const bool early = !append && (first + 1) * CH_KEYS < nvis;
+    // Piece p belongs to chain p mod CHAINS; the warp's chains are first, first + NW, ...
+    const int first = rank * P * NW + warp;
+    // In the step the kernel before writes the new row and nothing else of the cache:
+    // pieces without that row are fetched before the wait.
+    const bool early = !append && (first + (D - 1) * CHAINS + 1) * CH_KEYS < nvis;
     pdl_launch_dependents();
     if (!early) pdl_wait();
-    issue(first, 0);
-    issue(first, 1);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        issue(first + d * CHAINS, 0, d);
+        issue(first + d * CHAINS, 1, d);
+    }
     if (early) pdl_wait();
     tl_waited(a.tl);
     if (a.clear_err && b == 0 && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
@@ -177,9 +211,9 @@ __global__ void __launch_bounds__(chain_warps(GQ) * 32, 1) attn_chain_kernel(con
         }
     };
     start();
-    // The chain's (o, m, l), heads HD + 4 floats apart.
-    constexpr int REC = HD + 4;
-    auto finish = [&](float* rec) {
+    // The chain's o, heads HD + 4 floats apart, and its (m, l) behind it or to ml.
+    constexpr int REC = HD + 4, RECORDS = chain_record<HD>(GQ);
+    auto finish = [&](float* rec, float2* ml) {
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
 #pragma unroll
@@ -192,29 +226,50 @@ __global__ void __launch_bounds__(chain_warps(GQ) * 32, 1) attn_chain_kernel(con
                     dst[16 * mt + g] = __fadd_rn(o[mt][j][0], o[mt][j][1]);
                     dst[16 * mt + g + 8] = __fadd_rn(o[mt][j][2], o[mt][j][3]);
                 }
-                if (g == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(m[j], l[j]);
+                if (g == 0) *(ml ? ml + h : reinterpret_cast<float2*>(dst + HD)) = make_float2(m[j], l[j]);
             }
         }
     };
-    // Records: the CTA's last chains' in the warps' buffers, a single CTA's first ones' behind the buffers.
-    float* kept = reinterpret_cast<float*>(chain_smem + NW * L::WARP + warp * chain_record<HD>(GQ));
+    // The records of a turn, and the floats from warp to warp: the last in the buffers' place
+    // (with R == 2 at the CTA's rank, as the merge copies the others' there), the first
+    // behind the buffers, the others in the workspace, which has 24 records a head.
+    __shared__ float2 chain_ml[R > 2 ? CHAINS * GQ : 1];
+    auto records = [&](int turn, int& stride) -> float* {
+        if (turn == P - 1) {
+            stride = AREA / 4;
+            return reinterpret_cast<float*>(chain_smem + (R == 2 ? rank * RECORDS : 0));
+        }
+        stride = GQ * REC;
+        if (turn == 0) return reinterpret_cast<float*>(chain_smem + NW * AREA);
+        return a.part + (((size_t)b * a.nh + (size_t)kvh * GQ) * a.max_splits + (size_t)(turn - 1) * NW * GQ) * REC;
+    };
+    auto store = [&](int turn) {
+        int stride;
+        float* rec = records(turn, stride);
+        finish(rec + warp * stride, R > 2 ? chain_ml + ((rank * P + turn) * NW + warp) * GQ : nullptr);
+    };
     // the new row: converted, into the cache and into the warp's piece
-    auto put_new = [&](int item, int part) {
+    auto put_new = [&](int item, int part, int slot) {
         if (lane < CH) {
             const float* src = (part ? a.v_new : a.k_new) + ((size_t)b * a.nkv + kvh) * HD + 8 * lane;
             const uint4 w = make_uint4(f2_hi(src[0], src[1]), f2_hi(src[2], src[3]), f2_hi(src[4], src[5]), f2_hi(src[6], src[7]));
             *reinterpret_cast<uint4*>((__half*)(part ? a.v_dst : a.k_dst) + (row0 + pos) * HD + 8 * lane) = w;
-            *reinterpret_cast<uint4*>(mine + part * L::PART + L::off(nvis - 1 - item * CH_KEYS, lane)) = w;
+            *reinterpret_cast<uint4*>(mine + slot * L::WARP + part * L::PART + L::off(nvis - 1 - item * CH_KEYS, lane)) = w;
         }
         __syncwarp();
     };
 
-    for (int item = first, nx; item < n_items; item = nx) {
-        nx = after(item);
+    int turn = 0;
+    for (int item = first, nx, slot = 0; item < n_items; item = nx, slot = D > 1 ? (slot + 1) % D : 0) {
+        nx = item + CHAINS;
+        const bool ends = P > 1 && turn + 1 < P && nx >= n_items;  // a chain before the warp's last
+        if (ends) nx = first + (turn + 1) * NW;
+        const int fetch = D > 1 ? item + D * CHAINS : nx;  // the piece that takes this one's place
+        const uint32_t kb = kbase + slot * L::WARP, vb = vbase + slot * L::WARP;
         const int n = min(CH_KEYS, nvis - item * CH_KEYS);
         const bool has_new = append && item == n_items - 1;
-        cp_wait_but_one();  // the K part
-        if (has_new) put_new(item, 0);
+        cp_wait_but<2 * D - 1>();  // the K part
+        if (has_new) put_new(item, 0, slot);
         float sacc[CH_KT][NQ][4];
 #pragma unroll
         for (int t = 0; t < CH_KT; ++t)
@@ -222,21 +277,28 @@ __global__ void __launch_bounds__(chain_warps(GQ) * 32, 1) attn_chain_kernel(con
             for (int j = 0; j < NQ; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sacc[t][j][i] = 0.0f;
+        uint32_t ka[2][CH_KT][4];  // a k-step's keys, fetched a step ahead
+        auto load_k = [&](int ks) {
+#pragma unroll
+            for (int t = 0; t < CH_KT; ++t) {
+                uint32_t(&k)[4] = ka[ks & 1][t];
+                ldsm_x4(kb + L::off(16 * t + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * ks + (lane >> 4)), k[0], k[1], k[2], k[3]);
+            }
+        };
+        load_k(0);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            uint32_t ka[CH_KT][4];
-#pragma unroll
-            for (int t = 0; t < CH_KT; ++t)
-                ldsm_x4(kbase + L::off(16 * t + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * ks + (lane >> 4)), ka[t][0], ka[t][1],
-                        ka[t][2], ka[t][3]);
+            if (ks + 1 < KS) load_k(ks + 1);
 #pragma unroll
             for (int j = 0; j < NQ; ++j)
 #pragma unroll
-                for (int t = 0; t < CH_KT; ++t)
-                    mma_16816_acc(sacc[t][j], ka[t][0], ka[t][1], ka[t][2], ka[t][3], qb[j][ks][0], qb[j][ks][1]);
+                for (int t = 0; t < CH_KT; ++t) {
+                    const uint32_t(&k)[4] = ka[ks & 1][t];
+                    mma_16816_acc(sacc[t][j], k[0], k[1], k[2], k[3], qb[j][ks][0], qb[j][ks][1]);
+                }
         }
         __syncwarp();
-        issue(nx, 0);  // the next piece's K part
+        issue(fetch, 0, slot);
         // Softmax of head 4j + c over keys 16t + g and 16t + g + 8; the weights are taken
         // against the new running maximum (0 while every score is -inf).
         float sv[NQ][CH_KT][2], f[NQ];
@@ -276,12 +338,21 @@ __global__ void __launch_bounds__(chain_warps(GQ) * 32, 1) attn_chain_kernel(con
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[mt][j][i] = __fmul_rn(o[mt][j][i], f[j]);
         }
-        cp_wait_but_one();  // the V part
-        if (has_new) put_new(item, 1);
+        cp_wait_but<2 * D - 1>();  // the V part
+        if (has_new) put_new(item, 1, slot);
         const int src0 = (2 * c) * 4 + colh, src1 = src0 + 4;
 #pragma unroll
         for (int js = 0; js < CH_KT; ++js) {
             if (16 * js < n) {
+                constexpr int VB = 4;  // 16-dim tiles fetched at a time
+                uint32_t va[VB][4];
+                auto load_v = [&](int mt0) {
+#pragma unroll
+                    for (int u = 0; u < VB; ++u)
+                        ldsm_x4_trans(vb + L::off(16 * js + (lane >> 4) * 8 + (lane & 7), 2 * (mt0 + u) + ((lane >> 3) & 1)),
+                                      va[u][0], va[u][1], va[u][2], va[u][3]);
+                };
+                load_v(0);
                 uint32_t pb[NQ][2];
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
@@ -291,86 +362,173 @@ __global__ void __launch_bounds__(chain_warps(GQ) * 32, 1) attn_chain_kernel(con
                     pb[j][0] = !on ? 0u : (col_lo ? f2_lo(v00, v01) : f2_hi(v00, v01));
                     pb[j][1] = !on ? 0u : (col_lo ? f2_lo(v10, v11) : f2_hi(v10, v11));
                 }
+                static_assert(NU / 2 % VB == 0, "whole groups of tiles");
 #pragma unroll
-                for (int mt = 0; mt < NU / 2; ++mt) {
-                    uint32_t va[4];
-                    ldsm_x4_trans(vbase + L::off(16 * js + (lane >> 4) * 8 + (lane & 7), 2 * mt + ((lane >> 3) & 1)), va[0],
-                                  va[1], va[2], va[3]);
+                for (int mt0 = 0; mt0 < NU / 2; mt0 += VB) {
+                    if (mt0) load_v(mt0);
 #pragma unroll
-                    for (int j = 0; j < NQ; ++j) mma_16816_acc(o[mt][j], va[0], va[1], va[2], va[3], pb[j][0], pb[j][1]);
+                    for (int u = 0; u < VB; ++u)
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j)
+                            mma_16816_acc(o[mt0 + u][j], va[u][0], va[u][1], va[u][2], va[u][3], pb[j][0], pb[j][1]);
                 }
             }
         }
         __syncwarp();
-        issue(nx, 1);  // the next piece's V part
-        if (!PAIR && nx == first + NW && nx < n_items) {  // the first chain ends here
-            finish(kept);
+        issue(fetch, 1, slot);
+        if (ends && nx < n_items) {
+            store(turn++);
             start();
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
-    // The warp's last chain; one that only had a chain of the first half leaves it with those.
-    static_assert(GQ * REC * 4 <= L::WARP, "a chain's record fits its buffer");
-    if (!PAIR && first + NW >= n_items)
-        finish(kept);
-    else
-        finish(reinterpret_cast<float*>(mine));
+    static_assert((R == 2 ? CS * RECORDS : RECORDS + GQ * HD * 4) <= AREA, "records, or a record and a sum, fit a warp's buffers");
+    if (first < n_items) store(turn);
 
-    // The merge, chains in order.  A single CTA holds all records; of a cluster, rank 0
-    // those of chains 0 .. NW - 1, and each CTA merges half of the dims, after copying the
-    // other's records of them behind its own.
-    constexpr int RECORDS = chain_record<HD>(GQ);
-    static_assert(2 * RECORDS <= L::WARP, "two records fit a buffer");
-    const int chains = min(2 * NW, n_items);
-    constexpr int MD = PAIR ? HD / 2 : HD;  // dims merged here
-    const int d0 = PAIR ? rank * MD : 0;
-    __shared__ float weight[GQ][2 * NW], denom[GQ];
-    if (PAIR) {
-        cluster_sync();
-        // the other CTA's records of these dims, and its (m, l)
-        const uint32_t buf0 = smem_u32(chain_smem);
-        const int others = rank ? min(NW, n_items) : max(0, chains - NW);
-        constexpr int QUADS = MD / 4 + 1;
-        for (int t = threadIdx.x; t < others * GQ * QUADS; t += NW * 32) {
-            const int q = t % QUADS, wh = t / QUADS, w = wh / GQ, h = wh - w * GQ;
-            const int at = h * REC + (q < MD / 4 ? d0 + 4 * q : HD);
-            const float4 v = ld_other4(buf0 + w * L::WARP + at * 4, rank ^ 1);
-            *reinterpret_cast<float4*>(chain_smem + w * L::WARP + RECORDS + at * 4) = v;
+    const int chains = min(CHAINS, n_items);
+    // The merge.  No cluster size changes a bit of it.
+    if constexpr (R > 2) {
+        // M = max m_x, out = sum_x e^{m_x - M} o_x / sum_x e^{m_x - M} l_x: each CTA sums groups of
+        // its chains, in order, and the groups' sums are added in order.
+        if (CS > 1) {
+            cluster_sync();
+            for (int e = threadIdx.x; e < chains * GQ; e += NW * 32) {
+                const int owner = e / (P * NW * GQ);
+                if (owner != rank) chain_ml[e] = ld_other2(smem_u32(chain_ml + e), owner);
+            }
         }
-        asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // this CTA has read what it needs
-    }
-    __syncthreads();
-    // Chain x's record.
-    auto record = [&](int x) -> const float* {
-        const int w = x < NW ? x : x - NW;
-        if (PAIR) return reinterpret_cast<const float*>(chain_smem + w * L::WARP + ((x >= NW) != (rank != 0) ? RECORDS : 0));
-        return reinterpret_cast<const float*>(x < NW ? chain_smem + NW * L::WARP + w * chain_record<HD>(GQ)
-                                                     : chain_smem + w * L::WARP);
-    };
-    if (warp < GQ) {  // head `warp`: the chains' weights and the denominator
-        static_assert(2 * NW <= 32 && GQ <= NW, "a lane per chain, a warp per head");
-        const float2 ml = lane < chains ? *reinterpret_cast<const float2*>(record(lane) + warp * REC + HD)
-                                        : make_float2(-INFINITY, 0.0f);
-        float M = ml.x;
+        __syncthreads();
+        __shared__ float weight[GQ][CHAINS], denom[GQ];
+        for (int h = warp; h < GQ; h += NW) {  // the chains' weights and the denominator, a warp per head
+            constexpr int NL = (CHAINS + 31) / 32;
+            float2 v[NL];
+            float M = -INFINITY;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, x));
-        const float e = lane < chains ? expf(__fsub_rn(ml.x, M == -INFINITY ? 0.0f : M)) : 0.0f;
-        float den = __fmul_rn(e, ml.y);
+            for (int q = 0; q < NL; ++q) {
+                const int x = lane + 32 * q;
+                v[q] = x < chains ? chain_ml[x * GQ + h] : make_float2(-INFINITY, 0.0f);
+                M = fmaxf(M, v[q].x);
+            }
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) den = __fadd_rn(den, __shfl_xor_sync(FULL_MASK, den, x));
-        if (lane < 2 * NW) weight[warp][lane] = e;
-        if (lane == 0) denom[warp] = den;
+            for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, x));
+            const float ref = M == -INFINITY ? 0.0f : M;
+            float den = 0.0f;
+#pragma unroll
+            for (int q = 0; q < NL; ++q) {
+                const int x = lane + 32 * q;
+                if (32 * q < chains) {
+                    const float e = x < chains ? expf(__fsub_rn(v[q].x, ref)) : 0.0f;
+                    if (x < chains) weight[h][x] = e;
+                    den = __fmaf_rn(e, v[q].y, den);
+                }
+            }
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) den = __fadd_rn(den, __shfl_xor_sync(FULL_MASK, den, x));
+            if (lane == 0) denom[h] = den;
+        }
+        __syncthreads();
+        // Groups of chains: their weighted sums, in the buffers behind the records.
+        constexpr int G = CHAINS / 8, GROUPS = 8 / CS, QUADS = GQ * HD / 4;
+        static_assert(NW % G == 0, "a group's chains are of one turn");
+        auto sums = [&](int p) { return chain_smem + p * AREA + RECORDS; };
+        static_assert(GROUPS <= NW, "a sum per warp's buffers");
+        for (int u = threadIdx.x; u < GROUPS * QUADS; u += NW * 32) {
+            const int p = u / QUADS, q = u - p * QUADS, h = q / (HD / 4), x0 = (rank * GROUPS + p) * G, n = chains - x0;
+            int stride;
+            const float* rec = records(p * G / NW, stride);
+            rec += p * G % NW * stride + h * REC + 4 * (q % (HD / 4));
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float4 v[G];
+#pragma unroll
+            for (int w = 0; w < G; ++w)
+                if (w < n) v[w] = *reinterpret_cast<const float4*>(rec + w * stride);
+#pragma unroll
+            for (int w = 0; w < G; ++w)
+                if (w < n) {
+                    const float e = weight[h][x0 + w];
+                    acc.x = __fmaf_rn(e, v[w].x, acc.x);
+                    acc.y = __fmaf_rn(e, v[w].y, acc.y);
+                    acc.z = __fmaf_rn(e, v[w].z, acc.z);
+                    acc.w = __fmaf_rn(e, v[w].w, acc.w);
+                }
+            *reinterpret_cast<float4*>(sums(p) + 16 * q) = acc;
+        }
+        if (CS > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        // every CTA of the cluster writes its share of the heads' dims
+        constexpr int SHARE = GQ * HD / CS;
+        const int used = (chains + G - 1) / G;
+        for (int t = threadIdx.x; t < SHARE; t += NW * 32) {
+            const int i = rank * SHARE + t;
+            float v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < used) {
+                    const uint8_t* at = sums(r % GROUPS) + 4 * i;
+                    v[r] = CS > 1 ? ld_other(smem_u32(at), r / GROUPS) : *reinterpret_cast<const float*>(at);
+                }
+            float num = v[0];
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < used) num = __fadd_rn(num, v[r]);
+            a.out[(size_t)b * a.nh * HD + (size_t)kvh * GQ * HD + i] = __float2half_rn(__fdiv_rn(num, denom[i / HD]));
+        }
+        if (CS > 1) cluster_sync();  // the others have read this one's sums
+    } else {
+        // The merge, chains in order.  A single CTA holds all records; of a cluster each CTA
+        // merges its share of the dims, after copying the others' records of them to its own:
+        // chain x, of warp w of CTA r, is in warp w's buffers at r records' distance.
+        constexpr int MD = HD / CS;  // dims merged here
+        const int d0 = rank * MD;
+        __shared__ float weight[GQ][CHAINS], denom[GQ];
+        if (CS > 1) {
+            cluster_sync();
+            // the other CTAs' records of these dims, and their (m, l)
+            const uint32_t buf0 = smem_u32(chain_smem);
+            constexpr int QUADS = MD / 4 + 1;
+            for (int t = threadIdx.x; t < chains * GQ * QUADS; t += NW * 32) {
+                const int q = t % QUADS, xh = t / QUADS, x = xh / GQ, h = xh - x * GQ, r = x / NW;
+                const int at = (x - r * NW) * AREA + r * RECORDS + (h * REC + (q < MD / 4 ? d0 + 4 * q : HD)) * 4;
+                if (r != rank) *reinterpret_cast<float4*>(chain_smem + at) = ld_other4(buf0 + at, r);
+            }
+            __syncwarp();
+            asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // this CTA has read what it needs
+        }
+        __syncthreads();
+        // Chain x's record.
+        auto record = [&](int x) -> const float* {
+            const int r = x / NW, w = x - r * NW;
+            if (CS > 1) return reinterpret_cast<const float*>(chain_smem + w * AREA + r * RECORDS);
+            return reinterpret_cast<const float*>(r == 0 ? chain_smem + NW * AREA + w * RECORDS : chain_smem + w * AREA);
+        };
+        for (int h = warp; h < GQ; h += NW) {  // the chains' weights and the denominator, a warp per head
+            static_assert(CHAINS <= 32, "a lane per chain");
+            const float2 ml = lane < chains ? *reinterpret_cast<const float2*>(record(lane) + h * REC + HD)
+                                            : make_float2(-INFINITY, 0.0f);
+            float M = ml.x;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, x));
+            const float e = lane < chains ? expf(__fsub_rn(ml.x, M == -INFINITY ? 0.0f : M)) : 0.0f;
+            float den = __fmul_rn(e, ml.y);
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) den = __fadd_rn(den, __shfl_xor_sync(FULL_MASK, den, x));
+            if (lane < CHAINS) weight[h][lane] = e;
+            if (lane == 0) denom[h] = den;
+        }
+        __syncthreads();
+        for (int t = threadIdx.x; t < GQ * MD; t += NW * 32) {
+            const int h = t / MD, d = d0 + t - h * MD;
+            float num = 0.0f;
+#pragma unroll 8
+            for (int x = 0; x < chains; ++x) num = __fmaf_rn(weight[h][x], record(x)[h * REC + d], num);
+            a.out[(size_t)b * a.nh * HD + ((size_t)kvh * GQ + h) * HD + d] = __float2half_rn(__fdiv_rn(num, denom[h]));
+        }
+        __syncwarp();
+        if (CS > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the others have read this one's records
     }
-    __syncthreads();
-    for (int t = threadIdx.x; t < GQ * MD; t += NW * 32) {
-        const int h = t / MD, d = d0 + t - h * MD;
-        float num = 0.0f;
-#pragma unroll 4
-        for (int x = 0; x < chains; ++x) num = __fmaf_rn(weight[h][x], record(x)[h * REC + d], num);
-        a.out[(size_t)b * a.nh * HD + ((size_t)kvh * GQ + h) * HD + d] = __float2half_rn(__fdiv_rn(num, denom[h]));
-    }
-    if (PAIR) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the other has read this one's records
     tl_exit(a.tl);
 }
 
@@ -385,51 +543,96 @@ __global__ void __launch_bounds__(chain_warps(GQ) * 32, 1) attn_chain_kernel(con
 
 cudaError_t attn_chain_init_attributes() {
     cudaError_t e = cudaSuccess;
-#define KD_SET_ONE(HD_, GQ_, PAIR_)                                                                                     \
-    e = cudaFuncSetAttribute(attn_chain_kernel<HD_, GQ_, PAIR_>, cudaFuncAttributeMaxDynamicSharedMemorySize,           \
-                             chain_smem_bytes<HD_>(GQ_, PAIR_));                                                        \
-    if (e != cudaSuccess) return e;                                                                                     \
-    e = cudaFuncSetAttribute(attn_chain_kernel<HD_, GQ_, PAIR_>, cudaFuncAttributePreferredSharedMemoryCarveout,        \
-                             cudaSharedmemCarveoutMaxShared);                                                           \
+#define KD_SET_ONE(HD_, GQ_, R_, CS_)                                                                                 \
+    e = cudaFuncSetAttribute(attn_chain_kernel<HD_, GQ_, R_, CS_>, cudaFuncAttributeMaxDynamicSharedMemorySize,       \
+                             chain_smem_bytes<HD_>(GQ_, R_, CS_));                                                    \
+    if (e != cudaSuccess) return e;                                                                                   \
+    e = cudaFuncSetAttribute(attn_chain_kernel<HD_, GQ_, R_, CS_>, cudaFuncAttributePreferredSharedMemoryCarveout,    \
+                             cudaSharedmemCarveoutMaxShared);                                                         \
     if (e != cudaSuccess) return e;
-#define KD_SET(HD_, GQ_)           \
-    KD_SET_ONE(HD_, GQ_, false)    \
-    KD_SET_ONE(HD_, GQ_, true)
+#define KD_SET_R(HD_, GQ_, R_)   \
+    KD_SET_ONE(HD_, GQ_, R_, 1)  \
+    KD_SET_ONE(HD_, GQ_, R_, 2)  \
+    KD_SET_ONE(HD_, GQ_, R_, 4)  \
+    KD_SET_ONE(HD_, GQ_, R_, 8)
+#define KD_SET_2(HD_, GQ_) KD_SET_R(HD_, GQ_, 2)
+#define KD_SET_4(HD_, GQ_) KD_SET_R(HD_, GQ_, 4)
     for (int group : {1, 2, 4, 8}) {
-        KD_CHAIN_GROUPS(64, KD_SET)
-        KD_CHAIN_GROUPS(128, KD_SET)
+        KD_CHAIN_GROUPS(64, KD_SET_2)
+        KD_CHAIN_GROUPS(64, KD_SET_4)
+        KD_CHAIN_GROUPS(128, KD_SET_2)
+        KD_CHAIN_GROUPS(128, KD_SET_4)
     }
-#undef KD_SET
+#undef KD_SET_4
+#undef KD_SET_2
+#undef KD_SET_R
 #undef KD_SET_ONE
     return cudaSuccess;
 }
 
-cudaError_t launch_attn_chain(const AttnWinArgs& a, int max_keys, int num_sms, bool pdl, cudaStream_t s) {
-    const int group = a.nh / a.nkv;
-    // a cluster of two where both fit and a row has chains for the second
-    const bool pair = 2L * a.nkv * a.B <= num_sms && max_keys > chain_warps(group) * CH_KEYS;
+// Launch on clusters of CS, or, with `most`, ask how many of them the GPU holds at once.
+template <int HD, int GQ, int R, int CS>
+static cudaError_t launch_chain(const AttnWinArgs& a, bool pdl, cudaStream_t s, int* most = nullptr) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    if (pdl) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    if (pair) {
+    if (CS > 1) {
         attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attr[cfg.numAttrs].val.clusterDim.x = 2;
+        attr[cfg.numAttrs].val.clusterDim.x = CS;
         attr[cfg.numAttrs].val.clusterDim.y = 1;
         attr[cfg.numAttrs++].val.clusterDim.z = 1;
     }
+    if (pdl && !most) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.attrs = attr;
-    cfg.gridDim = dim3(pair ? 2 * a.nkv : a.nkv, a.B);
+    cfg.gridDim = dim3(CS * a.nkv, a.B);
+    cfg.blockDim = dim3(chain_cta_warps(GQ, R, CS) * 32);
+    cfg.dynamicSmemBytes = chain_smem_bytes<HD>(GQ, R, CS);
     cfg.stream = s;
-#define KD_LAUNCH(HD_, GQ_)                                                                                   \
-    cfg.blockDim = dim3(chain_warps(GQ_) * 32);                                                               \
-    cfg.dynamicSmemBytes = chain_smem_bytes<HD_>(GQ_, pair);                                                  \
-    return pair ? cudaLaunchKernelEx(&cfg, attn_chain_kernel<HD_, GQ_, true>, a)                              \
-                : cudaLaunchKernelEx(&cfg, attn_chain_kernel<HD_, GQ_, false>, a);
-    if (a.hd == 64) { KD_CHAIN_GROUPS(64, KD_LAUNCH) } else if (a.hd == 128) { KD_CHAIN_GROUPS(128, KD_LAUNCH) }
-#undef KD_LAUNCH
+    if (most) return cudaOccupancyMaxActiveClusters(most, attn_chain_kernel<HD, GQ, R, CS>, &cfg);
+    return cudaLaunchKernelEx(&cfg, attn_chain_kernel<HD, GQ, R, CS>, a);
+}
+
+// The largest cluster of which all fit the GPU at once and every CTA has a chain to take.
+template <int HD, int GQ, int R>
+static cudaError_t launch_chain(const AttnWinArgs& a, int max_keys, int num_sms, bool pdl, cudaStream_t s) {
+    static std::atomic<int> fit[2];  // clusters of 8 and 4 at once, asked once
+    const int units = a.nkv * a.B, pieces = (max_keys + CH_KEYS - 1) / CH_KEYS;
+    if (pieces <= chain_warps(GQ) || 2 * units > num_sms) return launch_chain<HD, GQ, R, 1>(a, pdl, s);
+    if (pieces > 2 * chain_warps(GQ))
+        for (int k = 0; k < 2; ++k) {
+            if (units * (8 >> k) > num_sms) continue;
+            int most = fit[k].load(std::memory_order_relaxed);
+            if (!most) {
+                const cudaError_t e = k == 0 ? launch_chain<HD, GQ, R, 8>(a, pdl, s, &most)
+                                             : launch_chain<HD, GQ, R, 4>(a, pdl, s, &most);
+                if (e != cudaSuccess) return e;
+                if (most < 1) most = -1;
+                fit[k].store(most, std::memory_order_relaxed);
+            }
+            if (units <= most)
+                return k == 0 ? launch_chain<HD, GQ, R, 8>(a, pdl, s) : launch_chain<HD, GQ, R, 4>(a, pdl, s);
+        }
+    return launch_chain<HD, GQ, R, 2>(a, pdl, s);
+}
+
+cudaError_t launch_attn_chain(const AttnWinArgs& a, int max_keys, int num_sms, bool pdl, cudaStream_t s) {
+    const int group = a.nh / a.nkv;
+#define KD_LAUNCH_2(HD_, GQ_) return launch_chain<HD_, GQ_, 2>(a, max_keys, num_sms, pdl, s);
+#define KD_LAUNCH_4(HD_, GQ_) return launch_chain<HD_, GQ_, 4>(a, max_keys, num_sms, pdl, s);
+    const bool wide = a.max_splits > WIN_CHAIN_ITEMS;
+    if (a.hd == 128 && wide) {
+        KD_CHAIN_GROUPS(128, KD_LAUNCH_4)
+    } else if (a.hd == 128) {
+        KD_CHAIN_GROUPS(128, KD_LAUNCH_2)
+    } else if (a.hd == 64 && wide) {
+        KD_CHAIN_GROUPS(64, KD_LAUNCH_4)
+    } else if (a.hd == 64) {
+        KD_CHAIN_GROUPS(64, KD_LAUNCH_2)
+    }
+#undef KD_LAUNCH_4
+#undef KD_LAUNCH_2
     return cudaErrorInvalidValue;
 }
 

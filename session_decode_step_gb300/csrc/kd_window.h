@@ -54,14 +54,14 @@ struct AttnWinArgs : AttnArgs {
     int vslot[16], vpos[16];
     int vbase[16], vitems;  // the rows' first items and the number of items, with vslot
     unsigned nkv_inv;       // ceil(2^32 / nkv): x / nkv = mulhi(x, nkv_inv) for x < 2^32 / nkv
-    // Op-level calls: the split kernel appends the new rows itself.  The warp whose
+    // Op-level calls: the kernel appends the new rows itself.  The warp whose
     // item ends in row b's new position converts the row (fp32 [B][nkv][hd]),
     // writes it to the cache (fp16 rows, or Q8_0 quants and scales) and into its
     // tile, whose copy may have read the old row.  nullptr: already appended.
     const float *k_new, *v_new;
     void *k_dst, *v_dst;
     __half *ks_dst, *vs_dst;
-    // The call's fault word is its own: the split kernel clears it, marks the
+    // The call's fault word is its own: the first kernel clears it, the Q8_0 split marks the
     // records of a CTA that gave up a wait, and the merge reports them (a word
     // cleared and set by CTAs of one launch would depend on their order).
     int clear_err;
@@ -79,13 +79,10 @@ inline void win_fill(AttnWinArgs& a, bool rows) {
         a.vitems += win_plan(a.vpos[b], a.window, a.sinks).ns * a.nkv;
     }
 }
-cudaError_t launch_attn_split(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s);
 cudaError_t launch_attn_split_q8(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s);
 cudaError_t launch_attn_combine(const AttnWinArgs& a, bool pdl, cudaStream_t s);
-// fp16 rows in one launch (kd_attn_chain.cu) where no row has more items than this.
-// By the slot's capacity, window and sinks alone: a row's bits do not depend on the
-// batch.  32 rows of 8 heads over a window of 1024: one launch 9.0 us, split and
-// merge 12.0; from about 2000 keys on, one row's chains take longer than the split.
+// fp16 rows, in one launch (kd_attn_chain.cu).  From WIN_CHAIN_ITEMS items of a row's
+// capacity on, the keys are shared out wider.
 constexpr int WIN_CHAIN_ITEMS = 32;
 cudaError_t attn_chain_init_attributes();
 // max_keys: no row sees more.

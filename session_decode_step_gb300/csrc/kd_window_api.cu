@@ -1,6 +1,6 @@
 // kd_window_api.cu -- the windowed attention's op-level entry points: KV append and
-// split attention over the leading and the last keys (kd_window.h) in one launch,
-// then the merge; for short fp16 windows everything in one launch.
+// attention over the leading and the last keys (kd_window.h) in one launch, after
+// which a Q8_0 cache needs a merge.
 // Slots and positions travel with the launches, so a call copies nothing to the
 // device and can be captured into a graph (they are then part of the graph).
 #include <cmath>
@@ -77,22 +77,14 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     win_fill(t, true);
     t.kc = (const __half*)kc;
     t.vc = (const __half*)vc;
-    if (!q8 && t.max_splits <= WIN_CHAIN_ITEMS) {
+    if (!q8) {
         KD_TRY(launch_attn_chain(t, max_keys, sms, true, s));
         return KD_OK;
     }
     AttnMaps maps;
-    const long rows = (long)n_slots * nkv * cap;
+    KD_TRY(make_attn_q8_maps((const uint8_t*)kc, (const uint8_t*)vc, (long)n_slots * nkv * cap, &maps));
     // persistent CTAs, no more than there are items
-    const int per = q8 ? sms : attn_split_grid(sms, hd, nh / nkv);
-    const int grid = t.vitems < per ? t.vitems : per;
-    if (q8) {
-        KD_TRY(make_attn_q8_maps((const uint8_t*)kc, (const uint8_t*)vc, rows, &maps));
-        KD_TRY(launch_attn_split_q8(t, maps, grid, true, s));
-    } else {
-        KD_TRY(make_attn_maps((const __half*)kc, (const __half*)vc, rows, hd, &maps));
-        KD_TRY(launch_attn_split(t, maps, grid, true, s));
-    }
+    KD_TRY(launch_attn_split_q8(t, maps, t.vitems < sms ? t.vitems : sms, true, s));
     KD_TRY(launch_attn_combine(t, true, s));
     return KD_OK;
 }

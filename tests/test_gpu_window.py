@@ -123,7 +123,7 @@ SHAPES = [(32, 8, 128), (8, 8, 128), (6, 3, 128), (16, 2, 128), (4, 4, 64), (14,
 RANGES = [(1, 0), (1, 1), (7, 4), (64, 0), (65, 3), (100, 64), (130, 200), (500, 1), (2 ** 31 - 1, 2 ** 31 - 1)]
 
 
-# cap: up to 2048 visible keys run in one launch, wider windows as split and merge
+# cap: up to 2048 visible keys are shared out over 16 or 24 chains, more over 32 or 48
 @pytest.mark.parametrize("nh,nkv,hd", SHAPES)
 @pytest.mark.parametrize("window,sinks,cap", [(w, s, 601) for w, s in RANGES] + [
     (2 ** 31 - 1, 5, 2101), (2500, 0, 2600), (2040, 3, 2301), (2100, 70, 4001), (300, 2000, 2301), (2080, 300, 2500)])
@@ -147,18 +147,18 @@ def test_window_q8(kdlib, nh, nkv, window, sinks):
 
 
 def test_window_of_everything_equals_the_plain_call(kdlib):
-    """A wide window that hides nothing: the same items, so the same bits as kd_attn_append_decode."""
+    """A wide Q8_0 window that hides nothing: the same items, so the same bits as kd_attn_append_decode_q8."""
     kd = kdlib
-    c = Case(False, 5, 32, 8, 128, 2300, [0, 63, 64, 300, 2299], 2300, 0)
+    c = Case(True, 5, 32, 8, 128, 2300, [0, 63, 64, 300, 2299], 2300, 0)
     got = c.run(kd)
     out = torch.empty(5, 32 * 128, dtype=torch.int16, device="cuda")
     ws = torch.empty(kd.kd_attn_workspace_bytes(5, 32, 128, 2300), dtype=torch.uint8, device="cuda")
-    kd.kd_attn_append_decode(c.dq, c.dk, c.dv, *c.dev, c.slots, c.pos, 32, 8, 128, c.n_slots, 2300, out, ws)
+    kd.kd_attn_append_decode_q8(c.dq, c.dk, c.dv, *c.dev, c.slots, c.pos, 32, 8, c.n_slots, 2300, out, ws)
     torch.cuda.synchronize()
     assert np.array_equal(out.cpu().numpy(), got.view(np.int16))
 
 
-# short windows run on two CTAs per row and KV head or on one, by the batch; both are met here
+# windows run on one to eight CTAs per row and KV head, by the batch
 @pytest.mark.parametrize("q8,nh,nkv,hd,window", [(False, 16, 4, 128, 700), (True, 16, 4, 128, 700), (False, 32, 8, 128, 1300),
                                                  (False, 8, 8, 64, 1990), (False, 64, 8, 128, 1024), (False, 8, 8, 128, 3000)])
 def test_window_rows_do_not_depend_on_the_batch(kdlib, q8, nh, nkv, hd, window):
@@ -168,6 +168,17 @@ def test_window_rows_do_not_depend_on_the_batch(kdlib, q8, nh, nkv, hd, window):
     for b in (0, 1, 7, 15):
         one = c.run(kdlib, slice(b, b + 1))
         assert np.array_equal(one[0].view(np.int16), got[b].view(np.int16)), b
+
+
+@pytest.mark.parametrize("nh,nkv,window", [(32, 8, 4500), (8, 8, 2200), (16, 2, 4990), (8, 4, 2500)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_wide_window_rows_in_batches_of_every_size(kdlib, hd, nh, nkv, window):
+    c = Case(False, 12, nh, nkv, hd, 5000, [4999, 4500, 4321, 60, 2048, 0, 1500, 3001] + list(range(17, 4900, 700)), window, 9)
+    got = c.run(kdlib)
+    c.check(got)
+    for n in (1, 2, 3, 4, 8):
+        some = c.run(kdlib, slice(0, n))
+        assert np.array_equal(some.view(np.int16), got[:n].view(np.int16)), n
 
 
 @pytest.mark.parametrize("q8", [False, True])
@@ -184,11 +195,11 @@ def test_window_large_scores(kdlib):
     c.check(c.run(kdlib))
 
 
-@pytest.mark.parametrize("q8", [False, True])
-def test_window_captured_graphs_share_a_workspace(kdlib, q8):
+@pytest.mark.parametrize("q8,cap,window", [(False, 400, 90), (True, 400, 90), (False, 4000, 3500)])
+def test_window_captured_graphs_share_a_workspace(kdlib, q8, cap, window):
     """Two captured calls on one workspace, replayed in turn on a side stream, each with its own inputs."""
     kd = kdlib
-    cs = [Case(q8, 40 + i, 8, 2, 128, 400, [399 - i, 70 + i, 3], 90, 5) for i in range(2)]
+    cs = [Case(q8, 40 + i, 8, 2, 128, cap, [cap - 1 - i, 70 + i, 3], window, 5) for i in range(2)]
     want = [c.run(kd) for c in cs]
     ws = cs[0].workspace(kd, 3)
     outs = [torch.zeros(3, 8 * 128, dtype=torch.int16, device="cuda") for _ in cs]
@@ -304,15 +315,25 @@ def test_model_window_steps(kdlib, name, flags):
         kd.kd_model_free(plain)
 
 
-@pytest.mark.parametrize("name", ["hd64", "q8"])
-def test_window_wait_timeout_is_reported(kdlib, name):
-    """A bounded wait of the windowed attention made to run out: KD_ERR_DEVICE once, then correct steps again."""
+def test_window_wait_timeout_is_reported(kdlib):
+    """A bounded wait of the windowed attention made to run out: KD_ERR_DEVICE once, then correct steps again.
+    Over an fp16 cache it waits on no barrier, and the hook says so."""
     kd = kdlib
-    shape = synth.TINY if name == "hd64" else synth.TINY_HD128
-    w = synth.model_weights(shape, 0)
-    m = kd.kd_model_load(kd.make_config(shape, 2, 4096, kd.KD_FLAG_KV_Q8_0 if name == "q8" else 0), w)
+    w = synth.model_weights(synth.TINY, 0)
+    m = kd.kd_model_load(kd.make_config(synth.TINY, 2, 4096), w)
     try:
-        kd.kd_model_set_window(m, 3500, 3)  # wide: the split kernel, whose waits are bounded
+        kd.kd_debug_inject_wait_timeout(m, "qkv")
+        kd.kd_model_set_window(m, 3500, 3)
+        with pytest.raises(kd.KdError) as e:
+            kd.kd_debug_inject_wait_timeout(m, "attn_split")
+        assert e.value.name == "KD_ERR_INVALID_ARG"
+    finally:
+        kd.kd_model_free(m)
+    shape = synth.TINY_HD128
+    w = synth.model_weights(shape, 0)
+    m = kd.kd_model_load(kd.make_config(shape, 2, 4096, kd.KD_FLAG_KV_Q8_0), w)
+    try:
+        kd.kd_model_set_window(m, 3500, 3)
         sid = kd.kd_session_bind(m)
         kd.kd_session_load_kv(m, sid, *synth.kv_prefill(shape, 0, 0, 150), 150)
         lg = torch.empty(1, shape.vocab, device="cuda")
