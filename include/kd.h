@@ -464,7 +464,7 @@ kd_status kd_attn_append_decode_q8(const float* q, const float* k_new, const flo
 /* ------------------------------------------------------------------------
  * Windowed attention, beam selection, cache reorder: the operators of long and
  * branching sessions on their own.  Calls copy nothing to the device, so they
- * can be captured into a graph; host arrays then belong to the graph.
+ * can be captured into a graph; what the host arrays held is then fixed in it.
  * ---------------------------------------------------------------------- */
 
 /* Bytes of device workspace a windowed attention call needs:
@@ -519,14 +519,15 @@ size_t kd_beam_workspace_bytes(int32_t n_groups, int32_t n_beams, int32_t V, int
  * beam (done[r] != 0) offers itself alone: token eos at s = scores[r], its logits
  * not used either.
  * The best come first: larger s, then the lower beam, then (within a beam) the
- * larger logit, then the lower token.  s is ordered in fp64 (the row sums are
- * good to about 1e-8) and stored as fp32; a row's s does not depend on the batch.
+ * larger logit, then the lower token.  s is formed and ordered with about 48 bits
+ * (the row sums are good to about 1e-6 relative) and stored as fp32; one that rounds
+ * to -inf is no candidate.  A row's s does not depend on the batch.
  *   parents_out, tokens_out: device int32 [n_groups][n_out], the beam w (not the
  *     row) and the token; -1 where fewer candidates exist.
  *   scores_out: device fp32 [n_groups][n_out], -inf there.
  *   done_out: NULL or device int32 [n_groups][n_out]: 1 where the parent was
  *     finished or the token is eos, else 0.
- * logits: device fp32, row r at logits + r * ld (ld >= V), 4-byte aligned; scores:
+ * logits: device fp32, row r at logits + r * ld (ld >= V); all buffers 4-byte aligned; scores:
  * NULL (zeros) or device fp32; done: NULL or device int32 (then eos must be a
  * token); eos: -1 for none.  No output may overlap an input.  workspace: device,
  * 16-byte aligned, kd_beam_workspace_bytes(...), used by one call at a time.

@@ -7,9 +7,9 @@
 // and the group's K best pairs are wanted, larger s first, then lower w, then
 // lower v.  Within a row the order is the logits' own, so one pass over the
 // logits does everything that touches all of them: a CTA walks a segment of one
-// row 4096 logits at a time, leaves (m, sum e^{x-m}) of every block (one or two
-// such steps) and the segment's K best logits, sorted.  A second kernel, one CTA per group, forms
-// L_w, merges each row's lists, and merges the rows by s.
+// row 4096 logits at a time, and leaves (m, sum e^{x-m}) of every block (one or two
+// such steps) and the segment's K best logits, sorted.  A second kernel, one CTA per
+// group, forms L_w, merges each row's lists, and merges the rows by s.
 //
 // The selection costs next to nothing once K candidates are known: a block whose
 // largest logit does not exceed the K-th best so far is passed over, so a random
@@ -26,6 +26,12 @@
 // that depends on nothing but the block, and exact 64-bit fixed point across
 // blocks.  So a row's result does not depend on the segments, hence not on the
 // rest of the batch.
+//
+// What bounds it (device time of both kernels): 512 rows of 128256 logits 46 us, 5.7
+// TB/s; 256 rows 28.6 us, 4.6 TB/s, where a CTA's 16 steps of about 0.9 us (the copies'
+// latency, 15 dependent operations and the shared pipes) do not overlap with another
+// CTA's as well as with four; 4 rows of 32000, 6.4 us: launch, one load's latency, one
+// block's candidates (4 us), the merge (2 us).
 #include <cuda_runtime.h>
 
 #include <cmath>

@@ -2,7 +2,7 @@
 // attention over the leading and the last keys (kd_window.h) in one launch, after
 // which a Q8_0 cache needs a merge.
 // Slots and positions travel with the launches, so a call copies nothing to the
-// device and can be captured into a graph (they are then part of the graph).
+// device and can be captured into a graph (they are then part of it).
 #include <cmath>
 
 #include "kd_host.h"
