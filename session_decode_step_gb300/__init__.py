@@ -169,15 +169,12 @@ def _ptr(obj):
     raise TypeError(f"cannot take the address of {type(obj)}")
 
 
-def _nbytes(buf) -> int:
-    """Bytes of a tensor or array."""
-    return buf.nbytes
-
-
 def _stream(stream):
     """The cudaStream_t of `stream`; None: the current stream of torch's current device (the default
     stream if torch, or its CUDA side, is not in use)."""
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream[0](_raw_stream[1]())
         torch = sys.modules.get("torch")
         if torch is None or not torch.cuda.is_initialized():
             return None
@@ -209,33 +206,18 @@ def _i32(a, n=None):
     return arr
 
 
-class _Arrays(dict):
-    """ctypes array types of one element type, by length."""
-
-    def __init__(self, element):
-        self.element = element
-
-    def __missing__(self, n):
-        t = self[n] = self.element * n
-        return t
+_call = None
 
 
-_ARRAYS, _POINTERS = _Arrays(C.c_int32), _Arrays(_vp)
-_INT32 = np.dtype(np.int32)
-
-
-def _c32(a, n=None):
-    """A ctypes int32 array of a host sequence or array, as an int32 pointer argument takes it.  A
-    contiguous, writable int32 array is handed over where it lies (its memory outlives the call)."""
-    if type(a) is not np.ndarray or a.dtype is not _INT32:
-        a = _i32(a)
-    size = a.size
-    if n is not None and size != n:
-        raise ValueError(f"expected {n} entries, got {size}")
-    try:
-        return _ARRAYS[size].from_buffer(a)
-    except (TypeError, ValueError, BufferError):  # read-only, strided or empty
-        return _ARRAYS[size](*a.ravel().tolist())
+def _fast():
+    """The marshalling module of the per-token calls (csrc/kd_py.c), beside libkd.so."""
+    global _call
+    if _call is None:
+        lib()
+        from . import _kdcall
+        _kdcall.setup(_ptr, _i32, _stream)
+        _call = _kdcall
+    return _call
 
 
 # ----------------------------------------------------------------- model ---
@@ -304,8 +286,10 @@ def kd_model_set_window(m, window: int, sinks: int = 0):
 
 def kd_session_reorder(m, session_ids, parents, stream=None):
     """Session ids[i] becomes a copy of what session parents[i] was (-1: stays as it is), all at once."""
-    ids = _c32(session_ids)
-    _check(lib().kd_session_reorder(m, ids, _c32(parents, len(ids)), len(ids), _stream(stream)))
+    ids = _i32(session_ids)
+    par = _i32(parents, ids.size)
+    i32p = C.POINTER(C.c_int32)
+    _check(lib().kd_session_reorder(m, ids.ctypes.data_as(i32p), par.ctypes.data_as(i32p), ids.size, _stream(stream)))
 
 
 def kd_session_fork(m, session_id: int, stream=None) -> int:
@@ -497,23 +481,15 @@ def kd_attn_window_workspace_bytes(B: int, n_heads: int, head_dim: int, cap: int
 def kd_attn_window_append_decode(q, k_new, v_new, k_cache, v_cache, slots, positions, n_heads, n_kv_heads, head_dim,
                                  n_slots, cap, window, sinks, out, workspace, stream=None):
     """kd_attn_append_decode with a sliding window: row b attends t < sinks and t > positions[b] - window."""
-    sl = _c32(slots)
-    B = len(sl)
-    _check(lib().kd_attn_window_append_decode(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), sl,
-                                              _c32(positions, B), B, n_heads, n_kv_heads, head_dim, n_slots, cap,
-                                              window, sinks, _ptr(out), _ptr(workspace), _nbytes(workspace),
-                                              _stream(stream)))
+    _check((_call or _fast()).window(q, k_new, v_new, k_cache, v_cache, slots, positions, n_heads, n_kv_heads, head_dim,
+                                     n_slots, cap, window, sinks, out, workspace, stream))
 
 
 def kd_attn_window_append_decode_q8(q, k_new, v_new, k_quants, k_scales, v_quants, v_scales, slots, positions, n_heads,
                                     n_kv_heads, n_slots, cap, window, sinks, out, workspace, stream=None):
     """kd_attn_window_append_decode over a Q8_0 cache of head_dim 128 (see include/kd.h)."""
-    sl = _c32(slots)
-    B = len(sl)
-    _check(lib().kd_attn_window_append_decode_q8(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_quants), _ptr(k_scales),
-                                                 _ptr(v_quants), _ptr(v_scales), sl, _c32(positions, B), B, n_heads,
-                                                 n_kv_heads, n_slots, cap, window, sinks, _ptr(out), _ptr(workspace),
-                                                 _nbytes(workspace), _stream(stream)))
+    _check((_call or _fast()).window_q8(q, k_new, v_new, k_quants, k_scales, v_quants, v_scales, slots, positions, n_heads,
+                                        n_kv_heads, n_slots, cap, window, sinks, out, workspace, stream))
 
 
 KD_BEAM_MAX_BEAMS = 16
@@ -530,29 +506,15 @@ def kd_beam_select(logits, n_groups: int, n_beams: int, V: int, scores, n_out: i
                    workspace, done=None, done_out=None, eos: int = -1, ld=None, stream=None):
     """Each group's n_out best (beam, token) continuations (see include/kd.h).  logits: device fp32
     [n_groups * n_beams] rows, `ld` (default V) apart; scores, done: device fp32 / int32 per row or None."""
-    _check(lib().kd_beam_select(_ptr(logits), V if ld is None else int(ld), n_groups, n_beams, V, _ptr(scores),
-                                _ptr(done), eos, n_out, _ptr(parents_out), _ptr(tokens_out), _ptr(scores_out),
-                                _ptr(done_out), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    _check((_call or _fast()).beam(logits, V if ld is None else ld, n_groups, n_beams, V, scores, done, eos, n_out,
+                                   parents_out, tokens_out, scores_out, done_out, workspace, stream))
 
 
 def kd_kv_reorder(planes, dst, src, lens, n_layers: int, n_slots: int, n_kv_heads: int, cap: int, window: int = 0,
                   sinks: int = 0, stream=None):
     """Slot dst[i] becomes what slot src[i] was, all at once and in place.  planes: device tensors
     [n_layers][n_slots][n_kv_heads][cap][...], the trailing dimensions being a row's bytes."""
-    d = _c32(dst)
-    m = len(d)
-    rows = n_layers * n_slots * n_kv_heads * cap
-    if rows < 1:
-        raise ValueError("n_layers, n_slots, n_kv_heads and cap must be positive")
-    k = len(planes)
-    ptrs, widths = _POINTERS[k](), _ARRAYS[k]()
-    for i, p in enumerate(planes):
-        ptrs[i] = _ptr(p)
-        widths[i], rest = divmod(_nbytes(p), rows)
-        if rest:
-            raise ValueError("a plane's size must be a whole number of bytes per row")
-    _check(lib().kd_kv_reorder(ptrs, widths, k, n_layers, n_slots, n_kv_heads, cap, d, _c32(src, m),
-                               _c32(lens, m), m, window, sinks, _stream(stream)))
+    _check((_call or _fast()).reorder(planes, dst, src, lens, n_layers, n_slots, n_kv_heads, cap, window, sinks, stream))
 
 
 def kd_attn_device_status(workspace=None, stream=None) -> int:

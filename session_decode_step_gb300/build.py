@@ -3,12 +3,15 @@
 Each .cu file compiles in parallel into _build/, then one shared library is
 linked next to this file.  No CMake; the static CUDA runtime is linked in, so
 loading the library needs no GPU (a call that reaches CUDA then fails cleanly).
+_kdcall.so, the binding's marshalling module, is compiled for the running Python
+and linked against it.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -18,6 +21,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = PKG / "libkd.so"
+CALL = PKG / "_kdcall.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v",
@@ -36,10 +40,10 @@ def _sources():
 
 
 def _stale() -> bool:
-    if not LIB.exists():
+    if not LIB.exists() or not CALL.exists():
         return True
-    t = LIB.stat().st_mtime
-    deps = list(_sources()) + list(CSRC.glob("*.h")) + list(CSRC.glob("*.cuh")) + list(INCLUDE.glob("*.h"))
+    t = min(LIB.stat().st_mtime, CALL.stat().st_mtime)
+    deps = list(_sources()) + list(CSRC.glob("*.c")) + list(CSRC.glob("*.h")) + list(CSRC.glob("*.cuh")) + list(INCLUDE.glob("*.h"))
     deps.append(Path(__file__))
     return any(d.stat().st_mtime > t for d in deps)
 
@@ -72,7 +76,21 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     if r.returncode != 0:
         raise RuntimeError(f"linking libkd.so failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_call()
     return LIB
+
+
+def _build_call():
+    cc = os.environ.get("CC") or shutil.which("cc") or shutil.which("gcc")
+    if not cc:
+        raise RuntimeError("no C compiler found (cc, gcc): it is required to build _kdcall.so")
+    tmp = str(CALL) + ".tmp"
+    cmd = [cc, "-O2", "-fPIC", "-shared", "-Wall", f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}",
+           str(CSRC / "kd_py.c"), "-o", tmp, f"-L{PKG}", "-l:libkd.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling _kdcall.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL)
 
 
 if __name__ == "__main__":

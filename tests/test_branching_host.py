@@ -138,3 +138,57 @@ def test_binding_checks_plane_sizes():
         kd.kd_kv_reorder([t], [0], [1], [5], 2, 4, 2, 65)
     with pytest.raises(ValueError):
         kd.kd_kv_reorder([t], [0, 1], [1], [5], 2, 4, 2, 64)
+
+
+def bound_window(slots, positions, cap=64, sinks=4, q8=False, **kw):
+    """The binding's call on host buffers: refused before CUDA is touched, and the message shows what arrived."""
+    ws = np.zeros(1 << 20, np.uint8)
+    x = np.zeros(4096, np.float32)
+    buf = {"q": x, "k_new": x, "v_new": x, **kw}
+    a = (buf["q"], buf["k_new"], buf["v_new"])
+    if q8:
+        return kd.kd_attn_window_append_decode_q8(*a, x, x, x, x, slots, positions, 4, 2, 8, cap, 16, sinks, x, ws)
+    return kd.kd_attn_window_append_decode(*a, x, x, slots, positions, 4, 2, 64, 8, cap, 16, sinks, x, ws)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("kind", [list, tuple, lambda v: np.array(v, np.int32), lambda v: np.array(v, np.int64),
+                                  lambda v: np.array([v, v], np.int32).T.copy()[:, 0], lambda v: np.array(v, ">i4")])
+def test_binding_takes_host_arrays_of_any_kind(lib, kind, q8):
+    with pytest.raises(kd.KdError, match="position 77 outside"):
+        bound_window(kind([3, 5, 1]), kind([1, 2, 77]), q8=q8)
+    with pytest.raises(kd.KdError, match="slot 5 repeated"):
+        bound_window(kind([5, 2, 5]), kind([1, 2, 3]), q8=q8)
+    with pytest.raises(ValueError, match="expected 3 entries, got 2"):
+        bound_window(kind([3, 5, 1]), kind([1, 2]), q8=q8)
+
+
+def test_binding_refuses_what_it_cannot_pass(lib):
+    torch = pytest.importorskip("torch")
+    with pytest.raises(ValueError, match="contiguous"):
+        bound_window([0], [0], q=torch.zeros(4, 4).t())
+    with pytest.raises(ValueError, match="contiguous"):
+        bound_window([0], [0], q=np.zeros((4, 4), np.float32).T)
+    with pytest.raises(TypeError):
+        bound_window([0], [0], q="a string")
+    with pytest.raises(kd.KdError, match="null argument"):
+        bound_window([0], [0], q=None)
+    with pytest.raises(OverflowError):
+        bound_window([0], [0], sinks=2 ** 31)
+    with pytest.raises(TypeError):
+        bound_window([0], [0], cap=1.5)
+    with pytest.raises(kd.KdError, match="B=0"):
+        bound_window([], [])
+    with pytest.raises(kd.KdError, match="sinks -1"):
+        bound_window([0], [0], sinks=np.int64(-1))
+    x = torch.zeros(2, 1000)
+    i = torch.zeros(8, dtype=torch.int32)
+    with pytest.raises(kd.KdError, match="ld=999"):
+        kd.kd_beam_select(x, 1, 2, 1000, None, 4, i, i, x, x, ld=999)
+    t = np.zeros((2, 4, 2, 64, 8), np.uint8)
+    with pytest.raises(kd.KdError, match="slot 3 <- 9 outside"):
+        kd.kd_kv_reorder([t], [3], [9], [5], 2, 4, 2, 64)
+    with pytest.raises(kd.KdError, match="n_planes=5"):
+        kd.kd_kv_reorder((t,) * 5, [3], [1], [5], 2, 4, 2, 64)
+    with pytest.raises(ValueError, match="positive"):
+        kd.kd_kv_reorder([t], [3], [1], [5], 2, 4, 0, 64)
