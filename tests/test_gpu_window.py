@@ -352,3 +352,21 @@ def test_window_wait_timeout_is_reported(kdlib):
         assert kd.kd_device_status(m) == 0
     finally:
         kd.kd_model_free(m)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_calls_on_two_streams_at_once(kdlib, q8):
+    """Two callers, each with its own cache, workspace and stream, wide and short windows in turn."""
+    kd = kdlib
+    cs = [Case(q8, 60 + i, 16, 4, 128, 3000, [2999 - i, 1500, 70], w, 5) for i, w in enumerate((2600, 300))]
+    want = [c.run(kd) for c in cs]
+    ws = [c.workspace(kd, 3) for c in cs]
+    outs = [torch.zeros(3, 16 * 128, dtype=torch.int16, device="cuda") for _ in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, o, w, s in zip(cs, outs, ws, streams):
+            c.call(kd, o, w, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert np.array_equal(o.cpu().numpy(), w.view(np.int16))
