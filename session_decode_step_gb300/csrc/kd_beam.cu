@@ -30,8 +30,8 @@
 // What bounds it (device time of both kernels): 512 rows of 128256 logits 46 us, 5.7
 // TB/s; 256 rows 28.6 us, 4.6 TB/s, where a CTA's 16 steps of about 0.9 us (the copies'
 // latency, 15 dependent operations and the shared pipes) do not overlap with another
-// CTA's as well as with four; 4 rows of 32000, 6.4 us: launch, one load's latency, one
-// block's candidates (4 us), the merge (2 us).
+// CTA's as well as with four; 4 rows of 32000, 5.7 us: launch, one load's latency, one
+// block's candidates, the merge.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -53,6 +53,13 @@ constexpr int BS_MAX_BLOCKS = 64;               // vocabulary up to 524288
 constexpr int BS_MAX_SEGS = 32;                 // segments (lists) per row: one per lane of the merge
 constexpr int BS_MAX_OUT = 32;
 constexpr int BS_CAP = 128;                     // a warp's candidates between cuts to the K best
+// Short lists are merged by counting, for each candidate, those above it: few beams wait less
+// so than for the merge networks' exchanges (1 x 4 of 128256, best 4: 6.4 us against 7.6; 4 x 4
+// of 50000: 6.7, 7.8).  More keys cost more than they save: 8 candidates counted in the scan
+// 14.95 against 14.0 us (8 x 8), 8 rows of 8 in the merge 14.5.
+constexpr int BS_COUNT_OUT = 4;    // candidates kept, of eight warps' lists
+constexpr int BS_COUNT_KEYS = 64;  // keys of a row's segments, by a warp
+constexpr int BS_COUNT_ROWS = 64;  // rows x candidates x (rows / 4, the warps that share an issue slot)
 constexpr int BS_STAGES = 2;                    // steps in flight behind the one being worked on
 static_assert(KD_BEAM_MAX_VOCAB == (BS_STEP << beam_block_shift(KD_BEAM_MAX_VOCAB)) * BS_MAX_BLOCKS && KD_BEAM_MAX_OUT == BS_MAX_OUT, "kd.h limits");
 
@@ -273,6 +280,17 @@ __device__ __noinline__ int beam_cut(unsigned long long* buf, unsigned long long
     return K;
 }
 
+// How many of the first n (even) keys of a list lie above k.
+__device__ __forceinline__ int beam_above(const unsigned long long* list, int n, unsigned long long k) {
+    int c = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(list + j);
+        c += (o.x > k ? 1 : 0) + (o.y > k ? 1 : 0);
+    }
+    return c;
+}
+
 // Warp 0: the 32 best of the warps' lists (each sorted, 0-padded to 32).
 __device__ __forceinline__ unsigned long long beam_merge_lists(const unsigned long long (*lists)[BS_CAP], int lane) {
     static_assert(BS_WARPS == 8, "merged in a tree of eight");
@@ -284,7 +302,7 @@ __device__ __forceinline__ unsigned long long beam_merge_lists(const unsigned lo
 
 template <bool VEC>
 __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
-    __shared__ unsigned long long cand[BS_WARPS][BS_CAP];
+    __shared__ __align__(16) unsigned long long cand[BS_WARPS][BS_CAP];
     __shared__ unsigned long long best[BS_WARPS][BS_MAX_OUT];
     extern __shared__ __align__(16) float beam_smem[];  // [stages][BS_STEP] logits, then the blocks' sums by warp
     __shared__ __align__(16) float subset[4][64];  // maxima by 8 or 4 threads of the blocks seen, at each renewal of the bound
@@ -452,9 +470,22 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
     if (cnt > 32) cnt = beam_cut(buf, best[warp], cnt, K, lane);
     beam_sort(buf, cnt, K, lane);
     __syncthreads();
-    if (warp == 0) {  // the segment's list
+    // The segment's list.
+    unsigned long long* list = a.keys + ((size_t)r * a.nseg + blockIdx.x) * K;
+    if (K <= BS_COUNT_OUT) {
+        static_assert(BS_WARPS * BS_COUNT_OUT == 32, "a lane per candidate");
+        if (warp == 0) {  // the warps' lists are 0-padded
+            const unsigned long long k = cand[lane / BS_COUNT_OUT][lane % BS_COUNT_OUT];
+            const int have = __popc(__ballot_sync(FULL_MASK, k != 0ull));
+            int rank = 0;
+#pragma unroll
+            for (int w = 0; w < BS_WARPS; ++w) rank += beam_above(cand[w], BS_COUNT_OUT, k);
+            if (k && rank < K) list[rank] = k;
+            if (lane >= have && lane < K) list[lane] = 0ull;
+        }
+    } else if (warp == 0) {
         const unsigned long long k = beam_merge_lists(cand, lane);
-        if (lane < K) a.keys[((size_t)r * a.nseg + blockIdx.x) * K + lane] = k;
+        if (lane < K) list[lane] = k;
     }
     const int b = t - BS_THREADS / 2;  // the blocks' sums, warps in order
     if (b >= 0 && b < nc) {
@@ -475,7 +506,7 @@ static_assert(BS_THREADS / 2 >= BS_MAX_BLOCKS, "a thread per block of a segment"
 // form the rows' log sums; then the rows are merged in a tree of warps.  Lists are
 // held a key per lane throughout.
 __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(const __grid_constant__ BeamArgs a) {
-    __shared__ unsigned long long xkey[KD_BEAM_MAX_BEAMS][32];  // lists on their way to another warp
+    __shared__ __align__(16) unsigned long long xkey[KD_BEAM_MAX_BEAMS][BS_COUNT_KEYS];  // lists on their way to another warp
     __shared__ int xfrom[KD_BEAM_MAX_BEAMS][32];
     __shared__ int row_v[KD_BEAM_MAX_BEAMS][32];  // the rows' tokens
     __shared__ Pair row_lg[KD_BEAM_MAX_BEAMS];
@@ -516,7 +547,26 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
         }
     } else if (live) {
         const unsigned long long* lists = a.keys + (size_t)r * a.nseg * K + lane;
-        for (int l = 0; l < a.nseg; l += 8) {
+        const int n = a.nseg * K;
+        if (a.nseg == 1) {
+            x = lane < K ? __ldcg(lists) : 0ull;
+        } else if (n <= BS_COUNT_KEYS) {
+            static_assert(BS_COUNT_KEYS == 64, "two keys per lane");
+            const unsigned long long k0 = lane < n ? __ldcg(lists) : 0ull, k1 = lane + 32 < n ? __ldcg(lists + 32) : 0ull;
+            unsigned long long* row = xkey[w];
+            row[lane] = k0;
+            row[lane + 32] = k1;
+            __syncwarp();
+            const int even = (n + 1) & ~1, r0 = beam_above(row, even, k0);
+            const int r1 = n > 32 ? beam_above(row, even, k1) : 32;
+            __syncwarp();
+            row[lane] = 0ull;
+            __syncwarp();
+            if (k0 && r0 < 32) row[r0] = k0;
+            if (k1 && r1 < 32) row[r1] = k1;
+            __syncwarp();
+            x = row[lane];
+        } else for (int l = 0; l < a.nseg; l += 8) {
             unsigned long long v[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = lane < K && l + q < a.nseg ? __ldcg(lists + (size_t)(l + q) * K) : 0ull;
@@ -539,6 +589,25 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
         } else if (!live && lane == 0 && a.done && a.done[r]) {
             key = pair_key({score, 0.0f});  // a finished beam stands for itself; a dead one offers nothing
         }
+    }
+    auto put = [&](int place, int beam, int tok, unsigned long long k) {
+        const int o = g * K + place;
+        a.parents[o] = k ? beam : -1;
+        a.tokens[o] = k ? tok : -1;
+        a.scores_out[o] = k ? beam_unord((unsigned)(k >> 32)) : -INFINITY;
+        if (a.done_out) a.done_out[o] = k && (tok == a.eos || (a.done && a.done[g * a.W + beam])) ? 1 : 0;
+    };
+    if ((a.W + 3) / 4 * a.W * K <= BS_COUNT_ROWS) {  // each candidate counts those before it: of lower beams also its equals
+        if (warp < a.W) xkey[warp][lane] = key;
+        const int have = __syncthreads_count(warp < a.W && key != 0ull);
+        if (warp < a.W && key) {
+            int place = lane;
+            for (int o = 0; o < a.W; ++o)
+                if (o != warp) place += beam_above(xkey[o], (K + 1) & ~1, o < warp ? key - 1 : key);
+            if (place < K) put(place, warp, row_v[warp][lane], key);
+        }
+        if ((int)threadIdx.x >= have && (int)threadIdx.x < K) put(threadIdx.x, 0, -1, 0ull);
+        return;
     }
     for (int h = 1; h < a.W; h *= 2) {
         const bool give = warp < a.W && (warp & (2 * h - 1)) == h, take = (warp & (2 * h - 1)) == 0 && warp + h < a.W;
@@ -568,14 +637,7 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
             }
         }
     }
-    if (warp == 0 && lane < K) {
-        const int o = g * K + lane;
-        const int beam = from / 32, tok = key ? row_v[beam][from % 32] : -1;
-        a.parents[o] = key ? beam : -1;
-        a.tokens[o] = tok;
-        a.scores_out[o] = key ? beam_unord((unsigned)(key >> 32)) : -INFINITY;
-        if (a.done_out) a.done_out[o] = key && (tok == a.eos || (a.done && a.done[g * a.W + beam])) ? 1 : 0;
-    }
+    if (warp == 0 && lane < K) put(lane, from / 32, key ? row_v[from / 32][from % 32] : -1, key);
 }
 
 // stages, and a warp's (m, sum) per block of a segment
