@@ -57,7 +57,7 @@ constexpr int BS_CAP = 128;                     // a warp's candidates between c
 // so than for the merge networks' exchanges (1 x 4 of 128256, best 4: 6.4 us against 7.6; 4 x 4
 // of 50000: 6.7, 7.8).  More keys cost more than they save: 8 candidates counted in the scan
 // 14.95 against 14.0 us (8 x 8), 8 rows of 8 in the merge 14.5.
-constexpr int BS_COUNT_OUT = 4;    // candidates kept, of eight warps' lists
+constexpr int BS_COUNT_OUT = 128;  // candidates of a segment, by a CTA
 constexpr int BS_COUNT_KEYS = 64;  // keys of a row's segments, by a warp
 constexpr int BS_COUNT_ROWS = 64;  // rows x candidates x (rows / 4, the warps that share an issue slot)
 constexpr int BS_STAGES = 2;                    // steps in flight behind the one being worked on
@@ -303,7 +303,9 @@ __device__ __forceinline__ unsigned long long beam_merge_lists(const unsigned lo
 template <bool VEC>
 __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
     __shared__ __align__(16) unsigned long long cand[BS_WARPS][BS_CAP];
-    __shared__ unsigned long long best[BS_WARPS][BS_MAX_OUT];
+    __shared__ __align__(16) unsigned long long best[BS_WARPS][BS_MAX_OUT];
+    __shared__ int counts[BS_WARPS];
+    __shared__ unsigned low[BS_WARPS];
     extern __shared__ __align__(16) float beam_smem[];  // [stages][BS_STEP] logits, then the blocks' sums by warp
     __shared__ __align__(16) float subset[4][64];  // maxima by 8 or 4 threads of the blocks seen, at each renewal of the bound
     pdl_launch_dependents();
@@ -423,16 +425,21 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
             } else {
                 if ((lane & 3) == 0) sub[t >> 2] = m8;
                 __syncthreads();
-                const float v = sub[lane], u = sub[lane + 32];
-                int rv = 0, ru = 0;
-#pragma unroll 4
-                for (int j = 0; j < 64; j += 4) {
-                    const float4 o = *reinterpret_cast<const float4*>(sub + j);
-                    rv += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
-                    ru += (o.x > u ? 1 : 0) + (o.y > u ? 1 : 0) + (o.z > u ? 1 : 0) + (o.w > u ? 1 : 0);
+                // eight of the 64 per warp, four lanes each
+                const float v = sub[8 * warp + (lane >> 2)];
+                const float* part = sub + 16 * (lane & 3);
+                int rank = 0;
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 o = *reinterpret_cast<const float4*>(part + j);
+                    rank += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
                 }
-                if (rv < K) least = beam_ord(v);
-                if (ru < K) least = min(least, beam_ord(u));
+                rank += __shfl_xor_sync(FULL_MASK, rank, 1);
+                rank += __shfl_xor_sync(FULL_MASK, rank, 2);
+                const unsigned mine = __reduce_min_sync(FULL_MASK, rank < K ? beam_ord(v) : 0xffffffffu);
+                if (lane == 0) low[warp] = mine;
+                __syncthreads();
+                least = low[lane & 7];
             }
             const float kth = beam_unord(__reduce_min_sync(FULL_MASK, least));
             lo = fmaxf(lo, kth);
@@ -467,25 +474,37 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
         }
         fetch(b + BS_STAGES);  // into the stage just read
     }
-    if (cnt > 32) cnt = beam_cut(buf, best[warp], cnt, K, lane);
-    beam_sort(buf, cnt, K, lane);
-    __syncthreads();
-    // The segment's list.
+    // The segment's list: as long as few candidates are left, a thread each, which counts those above it.
     unsigned long long* list = a.keys + ((size_t)r * a.nseg + blockIdx.x) * K;
-    if (K <= BS_COUNT_OUT) {
-        static_assert(BS_WARPS * BS_COUNT_OUT == 32, "a lane per candidate");
-        if (warp == 0) {  // the warps' lists are 0-padded
-            const unsigned long long k = cand[lane / BS_COUNT_OUT][lane % BS_COUNT_OUT];
-            const int have = __popc(__ballot_sync(FULL_MASK, k != 0ull));
-            int rank = 0;
+    if (lane == 0) counts[warp] = cnt;
+    __syncthreads();
+    int before = 0, total = 0;
 #pragma unroll
-            for (int w = 0; w < BS_WARPS; ++w) rank += beam_above(cand[w], BS_COUNT_OUT, k);
-            if (k && rank < K) list[rank] = k;
-            if (lane >= have && lane < K) list[lane] = 0ull;
+    for (int w = 0; w < BS_WARPS; ++w) {
+        if (w == warp) before = total;
+        total += counts[w];
+    }
+    if (total <= BS_COUNT_OUT) {
+        unsigned long long* all = best[0];
+        static_assert(BS_COUNT_OUT < BS_WARPS * BS_MAX_OUT && BS_COUNT_OUT <= BS_THREADS, "they fit, a thread each");
+        for (int i = lane; i < cnt; i += 32) all[before + i] = buf[i];
+        if (t == 0) all[total] = 0ull;
+        __syncthreads();
+        if (t < total) {
+            const unsigned long long k = all[t];
+            const int rank = beam_above(all, (total + 1) & ~1, k);
+            if (rank < K) list[rank] = k;
+        } else if (t < K) {
+            list[t] = 0ull;
         }
-    } else if (warp == 0) {
-        const unsigned long long k = beam_merge_lists(cand, lane);
-        if (lane < K) list[lane] = k;
+    } else {
+        if (cnt > 32) cnt = beam_cut(buf, best[warp], cnt, K, lane);
+        beam_sort(buf, cnt, K, lane);
+        __syncthreads();
+        if (warp == 0) {
+            const unsigned long long k = beam_merge_lists(cand, lane);
+            if (lane < K) list[lane] = k;
+        }
     }
     const int b = t - BS_THREADS / 2;  // the blocks' sums, warps in order
     if (b >= 0 && b < nc) {
