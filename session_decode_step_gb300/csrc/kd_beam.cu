@@ -53,12 +53,13 @@ constexpr int BS_MAX_BLOCKS = 64;               // vocabulary up to 524288
 constexpr int BS_MAX_SEGS = 32;                 // segments (lists) per row: one per lane of the merge
 constexpr int BS_MAX_OUT = 32;
 constexpr int BS_CAP = 128;                     // a warp's candidates between cuts to the K best
-// Short lists are merged by counting, for each candidate, those above it: few beams wait less
-// so than for the merge networks' exchanges (1 x 4 of 128256, best 4: 6.4 us against 7.6; 4 x 4
-// of 50000: 6.7, 7.8).  More keys cost more than they save: 8 candidates counted in the scan
-// 14.95 against 14.0 us (8 x 8), 8 rows of 8 in the merge 14.5.
+// Short lists are merged by counting, for each candidate, those above it: few keys wait less
+// so than for the merge networks' exchanges (4 x 128256, best 4: 6.4 us against 7.6; 8 x 151936,
+// best 8: 8.7, 10.1; 48 x 32003, best 32: 11.9, 13.8).  Networks where more keys would be left:
+// 8 rows of 8 in the merge 14.5 us counted, 14.0 by networks; 8 lists of 32 a row 13.0, 11.9.
 constexpr int BS_COUNT_OUT = 128;  // candidates of a segment, by a CTA
 constexpr int BS_COUNT_KEYS = 64;  // keys of a row's segments, by a warp
+constexpr int BS_COUNT_PICK = 16;  // best of more keys than those
 constexpr int BS_COUNT_ROWS = 64;  // rows x candidates x (rows / 4, the warps that share an issue slot)
 constexpr int BS_STAGES = 2;                    // steps in flight behind the one being worked on
 static_assert(KD_BEAM_MAX_VOCAB == (BS_STEP << beam_block_shift(KD_BEAM_MAX_VOCAB)) * BS_MAX_BLOCKS && KD_BEAM_MAX_OUT == BS_MAX_OUT, "kd.h limits");
@@ -569,28 +570,62 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
         const int n = a.nseg * K;
         if (a.nseg == 1) {
             x = lane < K ? __ldcg(lists) : 0ull;
-        } else if (n <= BS_COUNT_KEYS) {
+        } else {
+            // All keys, or, of more than BS_COUNT_KEYS, those that can be among the K best: where m
+            // lists reach a value with their p-th keys, m p >= K keys do.  Then by counting.
             static_assert(BS_COUNT_KEYS == 64, "two keys per lane");
-            const unsigned long long k0 = lane < n ? __ldcg(lists) : 0ull, k1 = lane + 32 < n ? __ldcg(lists + 32) : 0ull;
             unsigned long long* row = xkey[w];
-            row[lane] = k0;
-            row[lane + 32] = k1;
-            __syncwarp();
-            const int even = (n + 1) & ~1, r0 = beam_above(row, even, k0);
-            const int r1 = n > 32 ? beam_above(row, even, k1) : 32;
-            __syncwarp();
-            row[lane] = 0ull;
-            __syncwarp();
-            if (k0 && r0 < 32) row[r0] = k0;
-            if (k1 && r1 < 32) row[r1] = k1;
-            __syncwarp();
-            x = row[lane];
-        } else for (int l = 0; l < a.nseg; l += 8) {
-            unsigned long long v[8];
+            int left = n;
+            if (n > BS_COUNT_KEYS && K > BS_COUNT_PICK) {
+                // more would be left than pay
+            } else if (n <= BS_COUNT_KEYS) {
+                row[lane] = lane < n ? __ldcg(lists) : 0ull;
+                row[lane + 32] = lane + 32 < n ? __ldcg(lists + 32) : 0ull;
+            } else {
+                const int p = min(K, 2 * ((K + a.nseg - 1) / a.nseg)), m = (K + p - 1) / p;
+                const unsigned pth = lane < a.nseg ? (unsigned)(__ldcg(lists - lane + (size_t)lane * K + p - 1) >> 32) : 0u;
+                int rank = 0;
+                for (int l = 0; l < a.nseg; ++l) rank += __shfl_sync(FULL_MASK, pth, l) > pth ? 1 : 0;
+                const unsigned bound = max(1u, __reduce_min_sync(FULL_MASK, lane < a.nseg && rank < m ? pth : 0xffffffffu));
+                row[lane] = 0ull;
+                row[lane + 32] = 0ull;
+                __syncwarp();
+                left = 0;
+                for (int l = 0; l < a.nseg; l += 8) {
+                    unsigned long long v[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = lane < K && l + q < a.nseg ? __ldcg(lists + (size_t)(l + q) * K) : 0ull;
-            const unsigned long long y = warp_merge8(v, a.nseg - l, lane);
-            x = l ? warp_merge(x, y, lane) : y;
+                    for (int q = 0; q < 8; ++q) v[q] = lane < K && l + q < a.nseg ? __ldcg(lists + (size_t)(l + q) * K) : 0ull;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const bool in = (unsigned)(v[q] >> 32) >= bound;
+                        const unsigned who = __ballot_sync(FULL_MASK, in);
+                        const int at = left + __popc(who & ((1u << lane) - 1u));
+                        if (in && at < BS_COUNT_KEYS) row[at] = v[q];
+                        left += __popc(who);
+                    }
+                }
+            }
+            __syncwarp();
+            if (left <= BS_COUNT_KEYS) {
+                const unsigned long long k0 = row[lane], k1 = row[lane + 32];
+                const int even = (left + 1) & ~1, r0 = beam_above(row, even, k0);
+                const int r1 = left > 32 ? beam_above(row, even, k1) : 32;
+                __syncwarp();
+                row[lane] = 0ull;
+                __syncwarp();
+                if (k0 && r0 < 32) row[r0] = k0;
+                if (k1 && r1 < 32) row[r1] = k1;
+                __syncwarp();
+                x = row[lane];
+            } else {
+                for (int l = 0; l < a.nseg; l += 8) {
+                    unsigned long long v[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[q] = lane < K && l + q < a.nseg ? __ldcg(lists + (size_t)(l + q) * K) : 0ull;
+                    const unsigned long long y = warp_merge8(v, a.nseg - l, lane);
+                    x = l ? warp_merge(x, y, lane) : y;
+                }
+            }
         }
         row_v[w][lane] = beam_key_i(x);
     } else if (lane == 0) {
