@@ -27,8 +27,8 @@
 // blocks.  So a row's result does not depend on the segments, hence not on the
 // rest of the batch.
 //
-// What bounds it (device time of both kernels): 512 rows of 128256 logits 46 us, 5.7
-// TB/s; 256 rows 28.6 us, 4.6 TB/s, where a CTA's 16 steps of about 0.9 us (the copies'
+// What bounds it (device time of both kernels): 512 rows of 128256 logits 45.5 us, 5.8
+// TB/s; 256 rows 28.2 us, 4.7 TB/s, where a CTA's 16 steps of about 0.9 us (the copies'
 // latency, 15 dependent operations and the shared pipes) do not overlap with another
 // CTA's as well as with four; 4 rows of 32000, 5.7 us: launch, one load's latency, one
 // block's candidates, the merge.
@@ -55,7 +55,7 @@ constexpr int BS_MAX_OUT = 32;
 constexpr int BS_CAP = 128;                     // a warp's candidates between cuts to the K best
 // Short lists are merged by counting, for each candidate, those above it: few keys wait less
 // so than for the merge networks' exchanges (4 x 128256, best 4: 6.4 us against 7.6; 8 x 151936,
-// best 8: 8.7, 10.1; 48 x 32003, best 32: 11.9, 13.8).  Networks where more keys would be left:
+// best 8: 8.7, 10.1; 48 x 32003, best 32: 11.9, 13.5).  Networks where more keys would be left:
 // 8 rows of 8 in the merge 14.5 us counted, 14.0 by networks; 8 lists of 32 a row 13.0, 11.9.
 constexpr int BS_COUNT_OUT = 128;  // candidates of a segment, by a CTA
 constexpr int BS_COUNT_KEYS = 64;  // keys of a row's segments, by a warp
@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
     __shared__ __align__(16) unsigned long long best[BS_WARPS][BS_MAX_OUT];
     __shared__ int counts[BS_WARPS];
     __shared__ unsigned low[BS_WARPS];
-    extern __shared__ __align__(16) float beam_smem[];  // [stages][BS_STEP] logits, then the blocks' sums by warp
+    // [stages][BS_STEP] logits, then the blocks' sums by warp; off a 128-byte line the copies take 5% longer
+    extern __shared__ __align__(128) float beam_smem[];
     __shared__ __align__(16) float subset[4][64];  // maxima by 8 or 4 threads of the blocks seen, at each renewal of the bound
     pdl_launch_dependents();
     const int r = blockIdx.y, t = threadIdx.x, lane = t & 31, warp = t >> 5;
