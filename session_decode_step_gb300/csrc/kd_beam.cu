@@ -214,26 +214,53 @@ struct BeamArgs {
     float* scores_out;
 };
 
-// A step's logits on their way through shared memory: thread t copies, and later
-// reads, elements 4t .. 4t + 3 of each quarter, so no thread waits for another.
-// VEC: 16-byte copies (every row 16-byte aligned).  Elements from n on are not copied.
-template <bool VEC>
-__device__ __forceinline__ void beam_fetch(float* stage, const float* p, int n, int t) {
-    const uint32_t dst = smem_u32(stage + 4 * t);
-    p += 4 * t;
-    if (VEC && n >= BS_STEP) {
+// A step's logits on their way through shared memory: thread t reads elements 4t .. 4t + 3 of
+// each quarter.  Rows on 16-byte boundaries (ALIGNED) are copied by 16 bytes, by the threads that
+// read them, so none waits for another.  Others, which start `off` elements past one: where rows
+// are long (SHIFTED), a warp's 128 elements of a quarter are in 33 aligned pieces, which its
+// lanes copy for one another; else (SINGLY) an element at a time, which is less code to run once
+// (144 rows of 164879 33 us against 36; 76 of 645 6.2, 5.7).  Only what lies in the row is read.
+enum BeamRows : int { BEAM_ALIGNED, BEAM_SHIFTED, BEAM_SINGLY };
+constexpr int BS_SHIFTED_VOCAB = 32768;
+constexpr int BS_PIECES = 33 * 4;  // floats of a warp's quarter in pieces
+template <int ROWS>
+constexpr int BS_QUARTER = ROWS == BEAM_SHIFTED ? BS_WARPS * BS_PIECES : 4 * BS_THREADS;
+template <int ROWS>
+constexpr int BS_STAGE = BS_VPT / 4 * BS_QUARTER<ROWS>;
+// Where a thread's elements of the first quarter are in a stage (SHIFTED: `off` further).
+template <int ROWS>
+__device__ __forceinline__ int beam_place(int t) {
+    return ROWS == BEAM_SHIFTED ? (t >> 5) * BS_PIECES + 4 * (t & 31) : 4 * t;
+}
+__device__ __forceinline__ void beam_copy4(uint32_t dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void beam_copy16(uint32_t dst, const float* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int ROWS>
+__device__ __forceinline__ void beam_fetch(float* stage, const float* row, int e0, int V, int off, int t) {
+    constexpr bool SHIFTED = ROWS == BEAM_SHIFTED;
+    const int lane = t & 31, warp = t >> 5;
+    const uint32_t dst = smem_u32(stage + beam_place<ROWS>(t));
+    if (ROWS != BEAM_SINGLY && e0 + BS_STEP + (SHIFTED ? 4 : 0) <= V) {
+        const int e = e0 + 4 * t - off;
+        if (!SHIFTED || e >= 0)
+            beam_copy16(dst, row + e);
+        else  // the row's first piece
+            for (int j = off; j < 4; ++j) beam_copy4(dst + 4 * j, row + e + j);
 #pragma unroll
-        for (int i = 0; i < BS_VPT / 4; ++i)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 16 * BS_THREADS),
-                         "l"(p + i * 4 * BS_THREADS)
-                         : "memory");
-    } else {
-        const int left = n - 4 * t;
+        for (int i = 1; i < BS_VPT / 4; ++i) beam_copy16(dst + 4 * i * BS_QUARTER<ROWS>, row + e + i * 4 * BS_THREADS);
+        if (SHIFTED && lane < BS_VPT / 4)  // the 33rd pieces, one per quarter
+            beam_copy16(smem_u32(stage + lane * BS_QUARTER<ROWS> + warp * BS_PIECES + 128),
+                        row + e0 + lane * 4 * BS_THREADS + 128 * (warp + 1) - off);
+    } else {  // the row's end, an element at a time
+        const int left = V - e0 - 4 * t;
+        const float* p = row + e0 + 4 * t;
 #pragma unroll
         for (int i = 0; i < BS_VPT; ++i) {
             const int o = (i >> 2) * 4 * BS_THREADS + (i & 3);
-            if (o < left)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * o), "l"(p + o) : "memory");
+            if (o < left) beam_copy4(dst + 4 * ((i >> 2) * BS_QUARTER<ROWS> + (i & 3) + off), p + o);
         }
     }
 }
@@ -301,7 +328,7 @@ __device__ __forceinline__ unsigned long long beam_merge_lists(const unsigned lo
     return warp_merge8(v, 8, lane);
 }
 
-template <bool VEC>
+template <int ROWS>
 __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
     __shared__ __align__(16) unsigned long long cand[BS_WARPS][BS_CAP];
     __shared__ __align__(16) unsigned long long best[BS_WARPS][BS_MAX_OUT];
@@ -316,15 +343,17 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
     const int e_end = min(a.V, ((c0 + nc) << a.block_shift) * BS_STEP), e_begin = (c0 << a.block_shift) * BS_STEP;
     const int nb = (e_end - e_begin + BS_STEP - 1) / BS_STEP;  // its steps
     const float* row = a.logits + (size_t)r * a.ld;
+    const int off = ROWS != BEAM_SHIFTED ? 0 : (int)(reinterpret_cast<uintptr_t>(row) >> 2 & 3);
     unsigned long long* buf = cand[warp];
     int cnt = 0;
     float thr = -INFINITY;  // K logits seen are no less: later equals lose to them (higher indices)
     float mrun = -INFINITY; // the thread's largest so far
     float mt = -INFINITY, st = 0.0f;  // the thread's (m, sum) of the block
-    float2(*wpart)[BS_WARPS] = reinterpret_cast<float2(*)[BS_WARPS]>(beam_smem + BS_STAGES * BS_STEP);
+    float2(*wpart)[BS_WARPS] = reinterpret_cast<float2(*)[BS_WARPS]>(beam_smem + BS_STAGES * BS_STAGE<ROWS>);
     auto fetch = [&](int b) {
         const int e0 = e_begin + b * BS_STEP;
-        if (b < nb) beam_fetch<VEC>(beam_smem + (b % BS_STAGES) * BS_STEP, row + e0, a.V - e0, t);
+        if (ROWS == BEAM_SHIFTED) __syncwarp();  // the stage is read
+        if (b < nb) beam_fetch<ROWS>(beam_smem + (b % BS_STAGES) * BS_STAGE<ROWS>, row, e0, a.V, off, t);
         cp_async_commit();
     };
     pdl_wait();
@@ -337,16 +366,31 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
     for (int b = 1; b < BS_STAGES; ++b) fetch(b);
     for (int b = 0; b < nb; ++b) {
         const int e0 = e_begin + b * BS_STEP;
-        const float* stage = beam_smem + (b % BS_STAGES) * BS_STEP + 4 * t;
+        const float* stage = beam_smem + (b % BS_STAGES) * BS_STAGE<ROWS> + beam_place<ROWS>(t);
         float x[BS_VPT];
         cp_async_wait<BS_STAGES - 1>();
+        if (ROWS == BEAM_SHIFTED) __syncwarp();
 #pragma unroll
         for (int i = 0; i < BS_VPT / 4; ++i) {
-            const float4 v = *reinterpret_cast<const float4*>(stage + i * 4 * BS_THREADS);
+            const float4 v = *reinterpret_cast<const float4*>(stage + i * BS_QUARTER<ROWS>);
             x[4 * i] = v.x;
             x[4 * i + 1] = v.y;
             x[4 * i + 2] = v.z;
             x[4 * i + 3] = v.w;
+        }
+        if (ROWS == BEAM_SHIFTED && off) {
+#pragma unroll
+            for (int i = 0; i < BS_VPT / 4; ++i) {
+                const float4 n = *reinterpret_cast<const float4*>(stage + i * BS_QUARTER<ROWS> + 4);
+                float* y = x + 4 * i;
+                if (off == 1) {
+                    y[0] = y[1]; y[1] = y[2]; y[2] = y[3]; y[3] = n.x;
+                } else if (off == 2) {
+                    y[0] = y[2]; y[1] = y[3]; y[2] = n.x; y[3] = n.y;
+                } else {
+                    y[0] = y[3]; y[1] = n.x; y[2] = n.y; y[3] = n.z;
+                }
+            }
         }
         if (a.V - e0 < BS_STEP) {
             const int left = a.V - e0 - 4 * t;
@@ -453,7 +497,7 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
             for (int i = 0; i < BS_VPT; ++i) mine |= x[i] >= lo ? 1u << i : 0u;
             int quarter = 0;
             for (unsigned bits = __reduce_or_sync(FULL_MASK, mine); bits; bits &= bits - 1) {
-                const int i = __ffs(bits) - 1, o = (i >> 2) * 4 * BS_THREADS + (i & 3);
+                const int i = __ffs(bits) - 1;
                 if (b == 0 && i >> 2 != quarter) {
                     quarter = i >> 2;
                     if (cnt >= K) {
@@ -462,11 +506,11 @@ __global__ void __launch_bounds__(BS_THREADS, 4) beam_scan_kernel(const __grid_c
                         lo = fmaxf(lo, beam_unord(beam_ord(beam_key_x(buf[K - 1])) + 1u));
                     }
                 }
-                const float v = stage[o];
+                const float v = stage[(i >> 2) * BS_QUARTER<ROWS> + (i & 3) + off];
                 const bool in = (mine >> i & 1u) && v >= lo;
                 const unsigned who = __ballot_sync(FULL_MASK, in);
                 if (cnt + __popc(who) > BS_CAP) cnt = beam_cut(buf, best[warp], cnt, K, lane);
-                if (in) buf[cnt + __popc(who & ((1u << lane) - 1u))] = beam_key(v, e0 + o + 4 * t);
+                if (in) buf[cnt + __popc(who & ((1u << lane) - 1u))] = beam_key(v, e0 + (i >> 2) * 4 * BS_THREADS + (i & 3) + 4 * t);
                 cnt += __popc(who);
             }
             if (cnt > K + 8) {
@@ -696,16 +740,19 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
 }
 
 // stages, and a warp's (m, sum) per block of a segment
-static int beam_scan_smem(int blocks) { return BS_STAGES * BS_STEP * 4 + blocks * BS_WARPS * 8; }
+static int beam_scan_smem(int blocks, bool shifted) {
+    return BS_STAGES * (shifted ? BS_STAGE<BEAM_SHIFTED> : BS_STAGE<BEAM_ALIGNED>) * 4 + blocks * BS_WARPS * 8;
+}
 cudaError_t beam_init_attributes() {
     cudaError_t e = cudaSuccess;
-    for (const void* f : {(const void*)beam_scan_kernel<true>, (const void*)beam_scan_kernel<false>,
-                          (const void*)beam_merge_kernel})
+    for (const void* f : {(const void*)beam_scan_kernel<BEAM_ALIGNED>, (const void*)beam_scan_kernel<BEAM_SHIFTED>,
+                          (const void*)beam_scan_kernel<BEAM_SINGLY>, (const void*)beam_merge_kernel})
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                       cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
             return e;
-    for (const void* f : {(const void*)beam_scan_kernel<true>, (const void*)beam_scan_kernel<false>})
-        if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, beam_scan_smem(BS_MAX_BLOCKS))) !=
+    for (const void* f : {(const void*)beam_scan_kernel<BEAM_ALIGNED>, (const void*)beam_scan_kernel<BEAM_SHIFTED>,
+                          (const void*)beam_scan_kernel<BEAM_SINGLY>})
+        if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, beam_scan_smem(BS_MAX_BLOCKS, true))) !=
             cudaSuccess)
             return e;
     return cudaSuccess;
@@ -777,7 +824,8 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
     a.keys = reinterpret_cast<unsigned long long*>(workspace);
     a.part = reinterpret_cast<float2*>(a.keys + (size_t)rows * a.nseg * n_out);
     const dim3 grid(a.nseg, rows);
-    const int smem = beam_scan_smem(a.seg_blocks);
+    const bool aligned = ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0, shifted = !aligned && V >= BS_SHIFTED_VOCAB;
+    const int smem = beam_scan_smem(a.seg_blocks, shifted);
     // Both launches may start while the kernel before them ends; they wait for it first.
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -789,10 +837,12 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
     cfg.blockDim = dim3(BS_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    if (ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0)
-        KD_TRY(cudaLaunchKernelEx(&cfg, beam_scan_kernel<true>, a));
+    if (aligned)
+        KD_TRY(cudaLaunchKernelEx(&cfg, beam_scan_kernel<BEAM_ALIGNED>, a));
+    else if (shifted)
+        KD_TRY(cudaLaunchKernelEx(&cfg, beam_scan_kernel<BEAM_SHIFTED>, a));
     else
-        KD_TRY(cudaLaunchKernelEx(&cfg, beam_scan_kernel<false>, a));
+        KD_TRY(cudaLaunchKernelEx(&cfg, beam_scan_kernel<BEAM_SINGLY>, a));
     cfg.gridDim = dim3(n_groups);
     cfg.blockDim = dim3(64 * n_beams);
     cfg.dynamicSmemBytes = 0;

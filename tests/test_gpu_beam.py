@@ -249,3 +249,17 @@ def test_many_rows_of_which_some_offer_nothing(kdlib, G, W, dead):
     go(kdlib, x, W, n, scores=scores, done=done, eos=7)
     if dead in (0.0, 1.0):
         go(kdlib, np.where(np.isnan(x), 1, x).astype(np.float32), W, n)  # neither scores nor end marks
+
+
+@pytest.mark.parametrize("shift", [0, 1, 2, 3])
+@pytest.mark.parametrize("V", [32768, 32771, 36864, 36861, 45053, 70001])
+def test_long_rows_off_every_boundary(kdlib, V, shift):
+    """Rows whose starts lie 0 to 3 elements past a 16-byte boundary, against the same rows on one: bit for bit."""
+    rng = np.random.default_rng(V)
+    x = (rng.standard_normal((5, V)) * 2.5).astype(np.float32)
+    x[:, 0], x[:, -1] = [9, -np.inf, 30, np.nan, 9], [9, 30, -9, 31, np.nan]  # both ends count
+    sc = -3 * rng.random(5)
+    got = go(kdlib, x, 5, 9, scores=sc, shift=shift, pad=1)  # rows of V + 1: every offset in turn
+    want = Call(kdlib, x, 5, 9, scores=sc, pad=-V % 4).run()
+    for a, b in zip(got, want):
+        assert np.array_equal(a, b)
