@@ -5,16 +5,16 @@
 // some not at all).  Byte x of one slot's (layer, head) slab only ever depends on
 // byte x of others, so a thread that owns one piece of the slab in every slot of
 // a set of connected moves can make them all without a second buffer: it loads
-// before it stores.  Sets of up to four moves are loaded whole; for larger ones,
-// taken four moves at a time, the host orders the moves so that a slot is read
+// before it stores.  Sets of up to four moves (eight where few bytes move) are loaded
+// whole; for larger ones, taken so many moves at a time, the host orders the moves so that a slot is read
 // before it is overwritten, and as a set has at most one cycle (every destination
 // has one source), one overwritten piece held in a register is enough.
 //
 // No arithmetic: bound by HBM, one read per source row (a row taken several
 // times comes from L1 the second time) and one write per destination row.  What
 // it takes is bytes in flight: a thread issues 8 loads of 16 bytes before it
-// waits for the first -- over 8 pieces of one move, 4 of two, or 2 of four moves
-// at a time, whichever fits the set.  32 layers of fp16 K and V, 8 sessions of 1238
+// waits for the first -- over 8 pieces of one move, 4 of two, 2 of four or 1 of eight
+// moves at a time, whichever fits the set.  32 layers of fp16 K and V, 8 sessions of 1238
 // rows, 974 MB read and written: 142 us, 6.85 TB/s, a copy's rate.  A Q8_0 cache's
 // windows (430 MB): 68 us, 6.3 TB/s; its scale rows are 8 bytes, so loads are.
 #include <cuda_runtime.h>
@@ -26,6 +26,7 @@
 namespace kd {
 
 constexpr int RO_THREADS = 256;
+constexpr long RO_EIGHT_BYTES = 32 << 20;  // moved, up to which sets are taken by eights
 constexpr int RO_FULL = 3 * 152;  // blocks resident at once: 3 per SM keep 80 registers, so the loads of a set stay in flight
 
 struct ReorderMove {
@@ -54,8 +55,12 @@ struct ReorderArgs {
     ReorderMove move[CAP];
 };
 
-// How a set's moves are taken: MB at a time, P pieces of each.
-enum ReorderKind : int { RO_ONE, RO_TWO, RO_FOUR, RO_CYCLE };  // (1, 8), (2, 4), (4, 2), (4, 1) with a held piece
+// How a set's moves are taken: MB at a time, P pieces of each: (1, 8), (2, 4), (4, 2) and (8, 1),
+// with a held piece (4, 1) or (8, 1).  Eights are for calls of few bytes, which wait for each batch
+// of moves in turn (16 moves of up to 33 rows, 19 layers of Q8_0: 5.7 us against 7.5 in fours; 16 of
+// 837 rows, 1 layer: 3.3, 6.7); many bytes are the slower so (11 moves, 45 MB: 22.3, 19.5).
+// Their kernel leaves them the registers.
+enum ReorderKind : int { RO_ONE, RO_TWO, RO_FOUR, RO_EIGHT, RO_CYCLE };
 __host__ __device__ constexpr int reorder_pieces(int kind) {
     return kind == RO_ONE ? 8 : kind == RO_TWO ? 4 : kind == RO_FOUR ? 2 : 1;
 }
@@ -122,7 +127,7 @@ __device__ __forceinline__ void reorder_run(const ReorderMove* moves, const Reor
     }
 }
 
-template <typename T>
+template <typename T, int BATCH>
 __device__ __forceinline__ void reorder_plane(const ReorderMove* moves, const ReorderRange& s, char* slab, size_t slot_bytes,
                                               int row_bytes, int tile, int tiles) {
     if (s.kind == RO_ONE)
@@ -131,13 +136,16 @@ __device__ __forceinline__ void reorder_plane(const ReorderMove* moves, const Re
         reorder_run<T, 2, 4, false>(moves, s, slab, slot_bytes, row_bytes, tile, tiles);
     else if (s.kind == RO_FOUR)
         reorder_run<T, 4, 2, false>(moves, s, slab, slot_bytes, row_bytes, tile, tiles);
+    else if (BATCH == 8 && s.kind == RO_EIGHT)
+        reorder_run<T, 8, 1, false>(moves, s, slab, slot_bytes, row_bytes, tile, tiles);
     else
-        reorder_run<T, 4, 1, true>(moves, s, slab, slot_bytes, row_bytes, tile, tiles);
+        reorder_run<T, BATCH, 1, true>(moves, s, slab, slot_bytes, row_bytes, tile, tiles);
 }
 
 // Block (x, y): run x of the planes' ranges' tiles, (layer, head) y.
-template <int CAP>
-__global__ void __launch_bounds__(RO_THREADS, 3) kv_reorder_kernel(const __grid_constant__ ReorderArgs<CAP> a) {
+template <int CAP, int BATCH>
+__global__ void __launch_bounds__(RO_THREADS, BATCH == 8 ? 2 : 3)
+    kv_reorder_kernel(const __grid_constant__ ReorderArgs<CAP> a) {
     pdl_launch_dependents();
     int p = 0;
     while (p + 1 < a.n_planes && (int)blockIdx.x >= a.plane0[p + 1]) ++p;
@@ -152,14 +160,14 @@ __global__ void __launch_bounds__(RO_THREADS, 3) kv_reorder_kernel(const __grid_
     const int tile = (t - s.run0[p]) * a.run;
     pdl_wait();
     if (row_bytes % 16 == 0)
-        reorder_plane<uint4>(a.move, s, slab, slot_bytes, row_bytes, tile, a.run);
+        reorder_plane<uint4, BATCH>(a.move, s, slab, slot_bytes, row_bytes, tile, a.run);
     else
-        reorder_plane<uint2>(a.move, s, slab, slot_bytes, row_bytes, tile, a.run);
+        reorder_plane<uint2, BATCH>(a.move, s, slab, slot_bytes, row_bytes, tile, a.run);
 }
 
-// Order the moves into connected sets (see the file comment).
+// Order the moves into connected sets (see the file comment), to be taken at most `batch` (4 or 8) at a time.
 template <int CAP>
-static void plan_moves(const ReorderPlan& p, const int32_t* dst, const int32_t* src, const int32_t* len, int n,
+static void plan_moves(const ReorderPlan& p, const int32_t* dst, const int32_t* src, const int32_t* len, int n, int batch,
                        ReorderArgs<CAP>& a) {
     constexpr int N = CAP;
     int id[N], m = 0;  // the moves that move something
@@ -215,8 +223,8 @@ static void plan_moves(const ReorderPlan& p, const int32_t* dst, const int32_t* 
                 ++count;
                 cycle = cycle || hold[order[k]];
             }
-        cycle = cycle && count > 4;  // up to four moves are loaded before the first is stored
-        const int kind = cycle ? RO_CYCLE : count == 1 ? RO_ONE : count == 2 ? RO_TWO : RO_FOUR;
+        cycle = cycle && count > batch;  // a batch is loaded before the first of it is stored
+        const int kind = cycle ? RO_CYCLE : count == 1 ? RO_ONE : count == 2 ? RO_TWO : count <= 4 || batch == 4 ? RO_FOUR : RO_EIGHT;
         int hi = 0, lo = 0x7fffffff, all_hi = 0x7fffffff, all_lo = 0;
         for (int k = 0; k < no; ++k) {
             const int i = order[k];
@@ -244,7 +252,7 @@ static cudaError_t launch_reorder(const ReorderPlan& p, const int32_t* dst, cons
     a.slots = p.slots;
     a.heads = p.heads;
     a.cap = p.cap;
-    plan_moves(p, dst, src, len, n, a);
+    plan_moves(p, dst, src, len, n, 4, a);
     if (a.n_ranges == 0) return cudaSuccess;
     // Tiles of a range on a plane, and how many a block makes in a row: several once
     // the blocks fill the GPU a few times over (they share the block's set-up).
@@ -252,10 +260,25 @@ static cudaError_t launch_reorder(const ReorderPlan& p, const int32_t* dst, cons
         const int tile = reorder_pieces(r.kind) * RO_THREADS * (row_bytes % 16 ? 8 : 16);
         return ((r.hi - r.lo) * row_bytes + tile - 1) / tile;
     };
-    long total = 0;
-    for (int i = 0; i < p.n_planes; ++i)
-        for (int c = 0; c < a.n_ranges; ++c) total += tiles_of(a.range[c], p.plane[i].row_bytes);
-    total *= p.layers * p.heads;
+    long total = 0, bytes = 0;
+    auto add_up = [&]() {
+        total = bytes = 0;
+        for (int i = 0; i < p.n_planes; ++i)
+            for (int c = 0; c < a.n_ranges; ++c) {
+                const ReorderRange& r = a.range[c];
+                total += tiles_of(r, p.plane[i].row_bytes);
+                bytes += (long)(r.hi - r.lo) * p.plane[i].row_bytes * r.count;
+            }
+        total *= p.layers * p.heads;
+        bytes *= p.layers * p.heads;
+    };
+    add_up();
+    const bool eights = n > 4 && bytes <= RO_EIGHT_BYTES;
+    if (eights) {
+        a.n_ranges = 0;
+        plan_moves(p, dst, src, len, n, 8, a);
+        add_up();
+    }
     a.run = total >= 16L * RO_FULL ? 4 : total >= 8L * RO_FULL ? 2 : 1;
     for (int i = 0; i < p.n_planes; ++i) {
         a.plane[i] = p.plane[i];
@@ -276,7 +299,7 @@ static cudaError_t launch_reorder(const ReorderPlan& p, const int32_t* dst, cons
     cfg.gridDim = dim3(a.runs, p.layers * p.heads);
     cfg.blockDim = dim3(RO_THREADS);
     cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, kv_reorder_kernel<CAP>, a);
+    return eights ? cudaLaunchKernelEx(&cfg, kv_reorder_kernel<CAP, 8>, a) : cudaLaunchKernelEx(&cfg, kv_reorder_kernel<CAP, 4>, a);
 }
 
 cudaError_t launch_kv_reorder(const ReorderPlan& p, const int32_t* dst, const int32_t* src, const int32_t* len, int n,
