@@ -521,7 +521,9 @@ size_t kd_beam_workspace_bytes(int32_t n_groups, int32_t n_beams, int32_t V, int
  * The best come first: larger s, then the lower beam, then (within a beam) the
  * larger logit, then the lower token.  s is formed and ordered with about 48 bits
  * (the row sums are good to about 1e-6 relative) and stored as fp32; one that rounds
- * to -inf is no candidate.  A row's s does not depend on the batch.
+ * to -inf is no candidate.  Where two logits of a beam differ by less than its last
+ * bits, the larger one comes first and both may count with the lesser s.  A row's s
+ * does not depend on the batch.
  *   parents_out, tokens_out: device int32 [n_groups][n_out], the beam w (not the
  *     row) and the token; -1 where fewer candidates exist.
  *   scores_out: device fp32 [n_groups][n_out], -inf there.

@@ -688,6 +688,18 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
         } else if (!live && lane == 0 && a.done && a.done[r]) {
             key = pair_key({score, 0.0f});  // a finished beam stands for itself; a dead one offers nothing
         }
+        // The merges below rank a row's candidates by their lanes, so its keys must fall with the lane.  A pair's
+        // sum rounds the low parts first, and two logits whose s differ by less than its last bit can come out the
+        // other way round (where x - M passes the middle between two fp32 values, as 2^-17 and the next value under
+        // M = 250 with 2% of all scores): such a key takes the least of those before it, and the lane decides.
+        const unsigned long long up = __shfl_up_sync(FULL_MASK, key, 1);
+        if (__any_sync(FULL_MASK, lane > 0 && key > up)) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long b = __shfl_up_sync(FULL_MASK, key, o);
+                if (lane >= o) key = min(key, b);
+            }
+        }
     }
     auto put = [&](int place, int beam, int tok, unsigned long long k) {
         const int o = g * K + place;

@@ -263,3 +263,37 @@ def test_long_rows_off_every_boundary(kdlib, V, shift):
     want = Call(kdlib, x, 5, 9, scores=sc, pad=-V % 4).run()
     for a, b in zip(got, want):
         assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("W,n_out", [(1, 5), (2, 10), (2, 8), (4, 16), (8, 32), (16, 32)])
+def test_logits_closer_than_the_scores_last_bits(kdlib, W, n_out):
+    """Two adjacent logits on either side of where x - max changes its rounding to fp32: with about 2% of these scores
+    the pair sums of the two come out the other way round.  Whatever their sums, every place of the output is
+    written, no candidate appears twice, and a beam's larger logit comes before its smaller one: in the merge by
+    counting (up to four beams here) and in the tree's."""
+    G, V, top = 1500, 300, 3
+    lo = np.float32(2.0 ** -17)
+    hi = np.nextafter(lo, np.float32(1))
+    row = np.full(V, -np.inf, np.float32)
+    row[[9, 120, 280]] = 250.0  # e^-250 of the others vanishes: the sum is 3
+    row[30], row[31] = lo, hi
+    x = np.tile(row, (G * W, 1))
+    scores = np.repeat((-3000 * np.random.default_rng(5).random(G)).astype(np.float32), W)
+    par, tok, dn, sc = Call(kdlib, x, W, n_out, scores=scores).run()
+    order = {9: 0, 120: 1, 280: 2, 31: 3, 30: 4}
+    for g in range(G):
+        got = list(zip(par[g].tolist(), tok[g].tolist()))
+        n = min(n_out, 5 * W)
+        lead = [(w, t) for w in range(W) for t in (9, 120, 280)][:n]
+        assert got[:len(lead)] == lead, (g, got)
+        near = got[len(lead):n]
+        assert len(set(near)) == len(near) and all(0 <= w < W and t in (30, 31) for w, t in near), (g, got)
+        for w in range(W):
+            mine = [order[t] for b, t in near if b == w]
+            assert mine in ([], [3], [3, 4]), (g, got)
+        assert got[n:] == [(-1, -1)] * (n_out - n)
+        assert np.all(np.diff(sc[g][:n]) <= 0)
+        s0 = np.float64(scores[g * W])
+        for j in range(n):
+            s = s0 + np.float64(row[got[j][1]]) - 250.0 - np.log(3.0)
+            assert abs(float(sc[g, j]) - s) <= 2.0 ** -24 * abs(s) + 4 * 2.0 ** -22, (g, j)
