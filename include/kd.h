@@ -192,6 +192,8 @@ kd_status kd_model_set_window(kd_model* m, int32_t window, int32_t sinks);
  * last window - 1); a later step that would attend any other row of the copy (a
  * rewind, a wider or removed window) is refused with KD_ERR_POSITION.
  * ids, parents: host arrays of n, 1 <= n <= KD_REORDER_MAX (else KD_ERR_BATCH).
+ * More sessions take several calls, cut where no id of one call is a parent in a
+ * a later one: between the prompts of a beam search.
  * Enqueued on `stream` after the model's previous step.
  * Errors: KD_ERR_BAD_SESSION (an id or parent not bound, an id repeated). */
 #define KD_REORDER_MAX 64
@@ -553,6 +555,7 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
  * of 8, at most 1024): an fp16 cache has K and V of 2 * head_dim, a Q8_0 cache
  * quants of 128 and scales of 8 for each.  Planes must not overlap.
  * dst, src, lens: host arrays of n, 1 <= n <= KD_REORDER_MAX, 0 <= lens[i] <= cap.
+ * More slots take several calls, cut where no dst of one call is a src of a later one.
  * Errors: KD_ERR_BATCH (n), KD_ERR_BAD_SESSION (a slot out of range, or written
  * twice), KD_ERR_POSITION (lens), KD_ERR_UNSUPPORTED (row_bytes, cap above
  * KD_REORDER_MAX_CAP, n_layers * n_kv_heads above 65535), KD_ERR_INVALID_ARG. */

@@ -5,6 +5,10 @@ unmoved slots, sources outside the destinations), ragged lengths, windows, fp16
 and Q8_0 planes, odd row sizes; every byte of every plane compared with a copy
 made on the host.  Model level: a forked or reordered session's steps give the
 bits of a session that was loaded with the same rows."""
+import re
+import textwrap
+from pathlib import Path
+
 import numpy as np
 import pytest
 
@@ -281,4 +285,66 @@ def test_beam_search_equals_replayed_hypotheses(model, window):
         hyps = new
         scores, done = out.flatten().clone(), dn.flatten().clone()
     assert len({(r // W, *h) for r, h in enumerate(hyps)}) == G * W  # the beams stay apart
+    assert kd.kd_device_status(m) == 0
+
+
+@pytest.mark.parametrize("groups,beams", [(3, 4), (10, 8)])
+def test_the_readme_search_loop(model, groups, beams):
+    """README's search step as it stands there, run three times, for up to 80 sessions.  Prompt 0 and prompt 1 have
+    fewer candidates than beams in the first step, prompt 2 none at all in the second.  Every hypothesis that is
+    left goes on with the logits of a session that was fed its tokens one by one."""
+    kd, shape, load = model
+    readme = (Path(__file__).resolve().parent.parent / "README.md").read_text()
+    block, = [b for b in re.findall(r"```python\n(.*?)```", readme, re.S) if "kd_beam_select" in b]
+    code = compile(textwrap.dedent(block), "README.md", "exec")
+    V, n = shape.vocab, groups * beams
+    prompts = [20 + 7 * g % 50 for g in range(groups)]
+    m, ref = load(sessions=n), load(sessions=n)
+    bound = [kd.kd_session_bind(m) for _ in range(n)]
+    ids = np.random.default_rng(3).permutation(bound).astype(np.int32)
+    rid = [kd.kd_session_bind(ref) for _ in range(n)]
+    for r in range(n):
+        rows = synth.kv_prefill(shape, 0, r // beams, prompts[r // beams])
+        for x, sid in ((m, int(ids[r])), (ref, rid[r])):
+            kd.kd_session_load_kv(x, sid, *rows, prompts[r // beams])
+    t = 0
+    allowed = {(0, 0): 3, (0, 1): 2, (1, 2): 0}  # (step, prompt): tokens that a grammar leaves
+
+    class Masked:
+        def __getattr__(self, name):
+            return getattr(kd, name)
+
+        def kd_decode_step(self, m, ids, tokens, positions, logits, argmax):
+            kd.kd_decode_step(m, ids, tokens, positions, logits, argmax)
+            for (step_, g), k in allowed.items():
+                if step_ == t:
+                    logits[g * beams:(g + 1) * beams, k:] = -np.inf
+
+    first = np.repeat(synth.tokens(1, "loop", groups, V), beams)
+    ns = dict(kd=Masked(), np=np, m=m, ids=ids, groups=groups, beams=beams, V=V, tokens=first,
+              positions=np.repeat(np.array(prompts, np.int32), beams), logits=torch.empty(n, V, device="cuda"),
+              scores=torch.tensor([0.0 if r % beams == 0 else -np.inf for r in range(n)], device="cuda"),
+              parents=torch.empty(groups, beams, dtype=torch.int32, device="cuda"),
+              new_tokens=torch.empty(groups, beams, dtype=torch.int32, device="cuda"),
+              new_scores=torch.empty(groups, beams, device="cuda"),
+              workspace=torch.empty(kd.kd_beam_workspace_bytes(groups, beams, V, beams), dtype=torch.uint8, device="cuda"))
+    hyps = [[int(x)] for x in first]
+    for t in range(3):
+        exec(code, ns)
+        par, tok = ns["parents"].cpu().numpy(), ns["new_tokens"].cpu().numpy()
+        hyps = [hyps[r // beams * beams + par[r // beams, r % beams]] + [int(tok[r // beams, r % beams])]
+                if par[r // beams, r % beams] >= 0 else None for r in range(n)]
+        if t == 0:
+            assert [sum(h is not None for h in hyps[g * beams:(g + 1) * beams]) for g in range(3)] == [3, 2, beams]
+    live = [r for r in range(n) if hyps[r] is not None]
+    assert len(live) == n - beams and not set(live) & set(range(2 * beams, 3 * beams))
+    t = -1
+    got = torch.empty(n, V, device="cuda")
+    kd.kd_decode_step(m, ids, ns["tokens"], ns["positions"], got, None)
+    want = torch.empty(n, V, device="cuda")
+    for j in range(4):
+        kd.kd_decode_step(ref, rid, [h[j] if h else 0 for h in hyps], [prompts[r // beams] + j for r in range(n)], want, None)
+    assert np.array_equal(ns["positions"], [prompts[r // beams] + 3 for r in range(n)])
+    assert torch.equal(got[live], want[live])
+    assert torch.isfinite(ns["scores"].view(-1)[live]).all()
     assert kd.kd_device_status(m) == 0
