@@ -193,7 +193,7 @@ kd_status kd_model_set_window(kd_model* m, int32_t window, int32_t sinks);
  * rewind, a wider or removed window) is refused with KD_ERR_POSITION.
  * ids, parents: host arrays of n, 1 <= n <= KD_REORDER_MAX (else KD_ERR_BATCH).
  * More sessions take several calls, cut where no id of one call is a parent in a
- * a later one: between the prompts of a beam search.
+ * later one, as between the prompts of a beam search.
  * Enqueued on `stream` after the model's previous step.
  * Errors: KD_ERR_BAD_SESSION (an id or parent not bound, an id repeated). */
 #define KD_REORDER_MAX 64
