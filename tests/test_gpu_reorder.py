@@ -52,6 +52,40 @@ def test_cycles(kdlib, k):
     run(kdlib, rng, 2, S, 2, 9, (32, 8), dst[order], src[order], np.full(len(dst), 9))
 
 
+def connected_sets(rng, S, sets):
+    """Moves of connected sets over distinct slots, in any order: (cycle, more) is a cycle of that many slots (0: one
+    slot that nothing writes), then `more` slots that each continue one of the set's earlier."""
+    free, dst, src = list(rng.permutation(S)), [], []
+    for cycle, more in sets:
+        nodes = [free.pop() for _ in range(max(cycle, 1))]
+        if cycle:
+            dst += nodes
+            src += nodes[1:] + nodes[:1]
+        for _ in range(more):
+            nodes.append(free.pop())
+            dst.append(nodes[-1])
+            src.append(nodes[rng.integers(len(nodes) - 1)])
+    order = rng.permutation(len(dst))
+    return np.array(dst)[order], np.array(src)[order]
+
+
+# Calls of more than 32 MB take sets four moves at a time, smaller ones eight.
+@pytest.mark.parametrize("sets", [((0, 5), (0, 9)), ((5, 0), (9, 0)), ((5, 3), (2, 4)), ((9, 5),), ((0, 16),), ((6, 1), (0, 6)),
+                                  ((0, 17), (9, 8), (5, 0)), ((17, 4), (0, 8), (3, 2)), ((40, 8),)])
+@pytest.mark.parametrize("ragged,window", [(False, 0), (True, 0), (True, 1400)])
+def test_large_calls_with_sets_of_many_moves(kdlib, sets, ragged, window):
+    rng = np.random.default_rng(sum(map(sum, sets)) + window)
+    S = sum(max(c, 1) + m for c, m in sets) + 2
+    dst, src = connected_sets(rng, S, sets)
+    widths, nkv = (256, 8, 128), 3
+    cap = 1999 if len(dst) <= 16 else 1601
+    at = rng.integers(cap * 3 // 4, cap + 1, S) if ragged else np.full(S, cap)
+    lens, sinks = at[src], 33
+    row = sum(widths) * nkv * sum(len(kept(int(n), window, sinks)) for n in lens)
+    L = (32 << 20) // row + 1
+    run(kdlib, rng, L, S, nkv, cap, widths, dst, src, lens, window, sinks)
+
+
 @pytest.mark.parametrize("seed", range(30))
 def test_random_maps(kdlib, seed):
     rng = np.random.default_rng(100 + seed)
