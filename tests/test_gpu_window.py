@@ -370,3 +370,53 @@ def test_calls_on_two_streams_at_once(kdlib, q8):
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert np.array_equal(o.cpu().numpy(), w.view(np.int16))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_wide_windows_of_groups_of_eight(kdlib, hd):
+    """64 query heads over 8 KV heads, more than 2048 visible keys: a row and KV head on one CTA (12 rows; its records pass
+    through the workspace), on clusters of two (5 and 9), four (3, 4) and eight (1, 2).  The same bits in each."""
+    c = Case(False, 21, 64, 8, hd, 2700, [2699, 2500, 2050, 60, 2048, 0, 1500, 2301, 33, 1000, 2600, 2699], 2560, 9)
+    got = c.run(kdlib)
+    c.check(got)
+    for n in (1, 2, 3, 4, 5, 9):
+        some = c.run(kdlib, slice(0, n))
+        assert np.array_equal(some.view(np.int16), got[:n].view(np.int16)), n
+
+
+@pytest.mark.parametrize("name,flags", [("hd64", 0), ("hd64", 1), ("wide", 0), ("q8", 0)])
+def test_model_window_steps_of_more_than_sixteen_sessions(kdlib, name, flags):
+    """20 windowed sessions a step (rows in groups of 16 and 4), two steps: each session's logits are those of
+    the session stepped alone, bit for bit."""
+    kd = kdlib
+    shape = synth.TINY if name == "hd64" else synth.TINY_HD128
+    w = dict(synth.model_weights(shape, 0), **synth.norm_weights(shape, 5))
+    n, cap, window, sinks = (20, 256, 70, 3) if name != "wide" else (20, 2600, 2150, 3)
+    flags |= kd.KD_FLAG_KV_Q8_0 if name == "q8" else 0
+    lens = [1 + 11 * i for i in range(n)] if name != "wide" else [2590 - 130 * i for i in range(n)]
+    m = kd.kd_model_load(kd.make_config(shape, n, cap, flags), w)
+    one = kd.kd_model_load(kd.make_config(shape, 1, cap, flags), w)
+    try:
+        for x in (m, one):
+            kd.kd_model_set_window(x, window, sinks)
+        rows = [synth.kv_prefill(shape, 0, i, lens[i]) for i in range(n)]
+        ids = []
+        for i in range(n):
+            ids.append(kd.kd_session_bind(m))
+            kd.kd_session_load_kv(m, ids[i], *rows[i], lens[i])
+        toks = [synth.tokens(t, "many", n, shape.vocab) for t in range(2)]
+        lg = torch.empty(n, shape.vocab, device="cuda")
+        got = []
+        for t in range(2):
+            kd.kd_decode_step(m, ids, toks[t], [x + t for x in lens], lg, None)
+            got.append(lg.cpu().numpy().copy())
+        assert kd.kd_device_status(m) == 0
+        sid = kd.kd_session_bind(one)
+        for i in range(n):
+            kd.kd_session_load_kv(one, sid, *rows[i], lens[i])
+            for t in range(2):
+                kd.kd_decode_step(one, [sid], toks[t][i:i + 1], [lens[i] + t], lg[:1], None)
+                assert np.array_equal(lg[0].cpu().numpy(), got[t][i]), (i, t)
+    finally:
+        kd.kd_model_free(m)
+        kd.kd_model_free(one)
