@@ -297,3 +297,16 @@ def test_logits_closer_than_the_scores_last_bits(kdlib, W, n_out):
         for j in range(n):
             s = s0 + np.float64(row[got[j][1]]) - 250.0 - np.log(3.0)
             assert abs(float(sc[g, j]) - s) <= 2.0 ** -24 * abs(s) + 4 * 2.0 ** -22, (g, j)
+
+
+@pytest.mark.parametrize("W,V,n_out", [(1, 131072, 16), (2, 131072, 9), (2, 131072, 16), (3, 131071, 12), (2, 200003, 16),
+                                       (2, 65536, 16), (4, 131072, 10)])
+def test_many_equals_in_many_segments(kdlib, W, V, n_out):
+    """Rows of few values: more than 64 keys of a row's segments are left after the bound, with 9 to 16 outputs."""
+    rng = np.random.default_rng(V + n_out)
+    go(kdlib, np.zeros((W, V), np.float32), W, n_out)
+    x = rng.integers(0, 3, (W, V)).astype(np.float32)
+    go(kdlib, x, W, n_out, scores=-rng.random(W))
+    x[0] = np.arange(V)[::-1] // 5000  # the first segment holds them all
+    x[-1, : V // 2] = -np.inf
+    go(kdlib, x, W, n_out)
