@@ -56,21 +56,17 @@ kd_status fail(kd_status st, const char* fmt, ...) {
                         #call, cudaGetErrorString(e_), __FILE__, __LINE__);                      \
     } while (0)
 
-std::once_flag g_attr_once[64];
-cudaError_t g_attr_err[64];
-
+// The kernels of the step and of the plain op-level calls; windowed attention and beam selection
+// set up their own when they are first used.
 cudaError_t init_device_attributes(int dev) {
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    std::call_once(g_attr_once[dev], [dev] {
+    static kd::OncePerDevice once;
+    return once(dev, [] {
         cudaError_t e = kd::mmvq_init_attributes();
         if (e == cudaSuccess) e = kd::attn_init_attributes();
         if (e == cudaSuccess) e = kd::attn_q8_init_attributes();
         if (e == cudaSuccess) e = kd::rowops_init_attributes();
-        if (e == cudaSuccess) e = kd::beam_init_attributes();
-        if (e == cudaSuccess) e = kd::attn_chain_init_attributes();
-        g_attr_err[dev] = e;
+        return e;
     });
-    return g_attr_err[dev];
 }
 
 constexpr int RING = 4;        // pinned staging slots for the per-step descriptor
@@ -564,7 +560,8 @@ static cudaError_t enqueue_step(kd_model* m, int B, float* lg, int* am, cudaStre
         const bool chain = window_chain(m);
         if (chain) {
             KD_RUN(KD_K_ATTN_SPLIT, kd::launch_attn_chain(
-                                        tw, (int)std::min<int64_t>((int64_t)m->window + m->sinks, c.max_ctx), m->num_sms, pdl, s));
+                                        tw, (int)std::min<int64_t>((int64_t)m->window + m->sinks, c.max_ctx), m->dev, m->num_sms,
+                                        pdl, s));
         } else if (!m->kvq8) {
             KD_RUN(KD_K_ATTN_SPLIT, kd::launch_attn_split(t, m->kmaps, m->attn_grid, pdl, s));
         } else {  // quantised append of the new rows, then the attention over the Q8_0 cache
@@ -886,6 +883,10 @@ kd_status kd_model_set_window(kd_model* m, int32_t window, int32_t sinks) {
     KD_CK(cudaSetDevice(m->dev));
     KD_CK(cudaStreamSynchronize(m->cap_stream));
     KD_CK(cudaEventSynchronize(m->last_step));
+    if (window > 0) {  // the kernels' set-up, before steps are captured
+        const kd_config& c = m->cfg;
+        KD_CK(m->kvq8 ? kd::attn_q8_win_prepare(m->dev) : kd::attn_chain_prepare(c.head_dim, c.n_heads / c.n_kv_heads, kd::win_max_items(c.max_ctx, window, sinks), m->dev));
+    }
     for (auto& g : m->graphs) cudaGraphExecDestroy(g.second);
     m->graphs.clear();
     m->window = window;

@@ -536,10 +536,18 @@ cudaError_t attn_init_attributes() {
 #undef KD_SET
     for (const void* f : {(const void*)attn_combine_kernel<64, 4, false>, (const void*)attn_combine_kernel<128, 4, false>,
                           (const void*)attn_combine_kernel<64, 32, false>, (const void*)attn_combine_kernel<128, 32, false>,
-                          (const void*)attn_combine_kernel<128, 4, true>, (const void*)attn_combine_kernel<128, 4, true, 1>,
-                          (const void*)attn_combine_kernel<128, 16, true>, (const void*)attn_combine_kernel<128, 16, true, 1>,
-                          (const void*)attn_combine_kernel<128, 32, true>, (const void*)attn_combine_kernel<128, 32, true, 1>,
                           (const void*)kv_append_kernel})
+        if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                      cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
+            return e;
+    return cudaSuccess;
+}
+
+cudaError_t attn_win_combine_attributes() {
+    cudaError_t e = cudaSuccess;
+    for (const void* f : {(const void*)attn_combine_kernel<128, 4, true>, (const void*)attn_combine_kernel<128, 4, true, 1>,
+                          (const void*)attn_combine_kernel<128, 16, true>, (const void*)attn_combine_kernel<128, 16, true, 1>,
+                          (const void*)attn_combine_kernel<128, 32, true>, (const void*)attn_combine_kernel<128, 32, true, 1>})
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                       cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
             return e;

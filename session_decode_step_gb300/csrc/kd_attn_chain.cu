@@ -34,6 +34,7 @@
 #include <atomic>
 
 #include "kd_attn_common.cuh"
+#include "kd_host.h"
 
 namespace kd {
 
@@ -541,38 +542,33 @@ __global__ void __launch_bounds__(chain_cta_warps(GQ, R, CS) * 32, 1)
         default: return cudaErrorInvalidValue; \
     }
 
-cudaError_t attn_chain_init_attributes() {
-    cudaError_t e = cudaSuccess;
-#define KD_SET_ONE(HD_, GQ_, R_, CS_)                                                                                 \
-    e = cudaFuncSetAttribute(attn_chain_kernel<HD_, GQ_, R_, CS_>, cudaFuncAttributeMaxDynamicSharedMemorySize,       \
-                             chain_smem_bytes<HD_>(GQ_, R_, CS_));                                                    \
-    if (e != cudaSuccess) return e;                                                                                   \
-    e = cudaFuncSetAttribute(attn_chain_kernel<HD_, GQ_, R_, CS_>, cudaFuncAttributePreferredSharedMemoryCarveout,    \
-                             cudaSharedmemCarveoutMaxShared);                                                         \
-    if (e != cudaSuccess) return e;
-#define KD_SET_R(HD_, GQ_, R_)   \
-    KD_SET_ONE(HD_, GQ_, R_, 1)  \
-    KD_SET_ONE(HD_, GQ_, R_, 2)  \
-    KD_SET_ONE(HD_, GQ_, R_, 4)  \
-    KD_SET_ONE(HD_, GQ_, R_, 8)
-#define KD_SET_2(HD_, GQ_) KD_SET_R(HD_, GQ_, 2)
-#define KD_SET_4(HD_, GQ_) KD_SET_R(HD_, GQ_, 4)
-    for (int group : {1, 2, 4, 8}) {
-        KD_CHAIN_GROUPS(64, KD_SET_2)
-        KD_CHAIN_GROUPS(64, KD_SET_4)
-        KD_CHAIN_GROUPS(128, KD_SET_2)
-        KD_CHAIN_GROUPS(128, KD_SET_4)
-    }
-#undef KD_SET_4
-#undef KD_SET_2
-#undef KD_SET_R
-#undef KD_SET_ONE
-    return cudaSuccess;
+// The kernel's attributes on device dev (the current one), set before its first launch there: a process
+// uses few of the 64 kernels, and setting all of them up took 10 ms.
+template <int HD, int GQ, int R, int CS>
+static cudaError_t chain_attributes(int dev) {
+    static OncePerDevice once;
+    return once(dev, [] {
+        const cudaError_t e = cudaFuncSetAttribute(attn_chain_kernel<HD, GQ, R, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   chain_smem_bytes<HD>(GQ, R, CS));
+        if (e != cudaSuccess) return e;
+        return cudaFuncSetAttribute(attn_chain_kernel<HD, GQ, R, CS>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    cudaSharedmemCarveoutMaxShared);
+    });
+}
+template <int HD, int GQ, int R>
+static cudaError_t chain_attributes_all(int dev) {
+    cudaError_t e = chain_attributes<HD, GQ, R, 1>(dev);
+    if (e == cudaSuccess) e = chain_attributes<HD, GQ, R, 2>(dev);
+    if (e == cudaSuccess) e = chain_attributes<HD, GQ, R, 4>(dev);
+    if (e == cudaSuccess) e = chain_attributes<HD, GQ, R, 8>(dev);
+    return e;
 }
 
 // Launch on clusters of CS, or, with `most`, ask how many of them the GPU holds at once.
 template <int HD, int GQ, int R, int CS>
-static cudaError_t launch_chain(const AttnWinArgs& a, bool pdl, cudaStream_t s, int* most = nullptr) {
+static cudaError_t launch_chain(const AttnWinArgs& a, int dev, bool pdl, cudaStream_t s, int* most = nullptr) {
+    const cudaError_t e = chain_attributes<HD, GQ, R, CS>(dev);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     if (CS > 1) {
@@ -596,44 +592,55 @@ static cudaError_t launch_chain(const AttnWinArgs& a, bool pdl, cudaStream_t s, 
 
 // The largest cluster of which all fit the GPU at once and every CTA has a chain to take.
 template <int HD, int GQ, int R>
-static cudaError_t launch_chain(const AttnWinArgs& a, int max_keys, int num_sms, bool pdl, cudaStream_t s) {
+static cudaError_t launch_chain(const AttnWinArgs& a, int max_keys, int dev, int num_sms, bool pdl, cudaStream_t s) {
     static std::atomic<int> fit[2];  // clusters of 8 and 4 at once, asked once
     const int units = a.nkv * a.B, pieces = (max_keys + CH_KEYS - 1) / CH_KEYS;
-    if (pieces <= chain_warps(GQ) || 2 * units > num_sms) return launch_chain<HD, GQ, R, 1>(a, pdl, s);
+    if (pieces <= chain_warps(GQ) || 2 * units > num_sms) return launch_chain<HD, GQ, R, 1>(a, dev, pdl, s);
     if (pieces > 2 * chain_warps(GQ))
         for (int k = 0; k < 2; ++k) {
             if (units * (8 >> k) > num_sms) continue;
             int most = fit[k].load(std::memory_order_relaxed);
             if (!most) {
-                const cudaError_t e = k == 0 ? launch_chain<HD, GQ, R, 8>(a, pdl, s, &most)
-                                             : launch_chain<HD, GQ, R, 4>(a, pdl, s, &most);
+                const cudaError_t e = k == 0 ? launch_chain<HD, GQ, R, 8>(a, dev, pdl, s, &most)
+                                             : launch_chain<HD, GQ, R, 4>(a, dev, pdl, s, &most);
                 if (e != cudaSuccess) return e;
                 if (most < 1) most = -1;
                 fit[k].store(most, std::memory_order_relaxed);
             }
             if (units <= most)
-                return k == 0 ? launch_chain<HD, GQ, R, 8>(a, pdl, s) : launch_chain<HD, GQ, R, 4>(a, pdl, s);
+                return k == 0 ? launch_chain<HD, GQ, R, 8>(a, dev, pdl, s) : launch_chain<HD, GQ, R, 4>(a, dev, pdl, s);
         }
-    return launch_chain<HD, GQ, R, 2>(a, pdl, s);
+    return launch_chain<HD, GQ, R, 2>(a, dev, pdl, s);
 }
 
-cudaError_t launch_attn_chain(const AttnWinArgs& a, int max_keys, int num_sms, bool pdl, cudaStream_t s) {
-    const int group = a.nh / a.nkv;
-#define KD_LAUNCH_2(HD_, GQ_) return launch_chain<HD_, GQ_, 2>(a, max_keys, num_sms, pdl, s);
-#define KD_LAUNCH_4(HD_, GQ_) return launch_chain<HD_, GQ_, 4>(a, max_keys, num_sms, pdl, s);
-    const bool wide = a.max_splits > WIN_CHAIN_ITEMS;
-    if (a.hd == 128 && wide) {
-        KD_CHAIN_GROUPS(128, KD_LAUNCH_4)
-    } else if (a.hd == 128) {
-        KD_CHAIN_GROUPS(128, KD_LAUNCH_2)
-    } else if (a.hd == 64 && wide) {
-        KD_CHAIN_GROUPS(64, KD_LAUNCH_4)
-    } else if (a.hd == 64) {
-        KD_CHAIN_GROUPS(64, KD_LAUNCH_2)
-    }
+#define KD_CHAIN_SHAPES(M2, M4)                                       \
+    const bool wide = max_splits > WIN_CHAIN_ITEMS;                   \
+    if (hd == 128 && wide) {                                          \
+        KD_CHAIN_GROUPS(128, M4)                                      \
+    } else if (hd == 128) {                                           \
+        KD_CHAIN_GROUPS(128, M2)                                      \
+    } else if (hd == 64 && wide) {                                    \
+        KD_CHAIN_GROUPS(64, M4)                                       \
+    } else if (hd == 64) {                                            \
+        KD_CHAIN_GROUPS(64, M2)                                       \
+    }                                                                 \
+    return cudaErrorInvalidValue;
+
+cudaError_t attn_chain_prepare(int hd, int group, int max_splits, int dev) {
+#define KD_PREPARE_2(HD_, GQ_) return chain_attributes_all<HD_, GQ_, 2>(dev)
+#define KD_PREPARE_4(HD_, GQ_) return chain_attributes_all<HD_, GQ_, 4>(dev)
+    KD_CHAIN_SHAPES(KD_PREPARE_2, KD_PREPARE_4)
+#undef KD_PREPARE_4
+#undef KD_PREPARE_2
+}
+
+cudaError_t launch_attn_chain(const AttnWinArgs& a, int max_keys, int dev, int num_sms, bool pdl, cudaStream_t s) {
+    const int hd = a.hd, group = a.nh / a.nkv, max_splits = a.max_splits;
+#define KD_LAUNCH_2(HD_, GQ_) return launch_chain<HD_, GQ_, 2>(a, max_keys, dev, num_sms, pdl, s)
+#define KD_LAUNCH_4(HD_, GQ_) return launch_chain<HD_, GQ_, 4>(a, max_keys, dev, num_sms, pdl, s)
+    KD_CHAIN_SHAPES(KD_LAUNCH_2, KD_LAUNCH_4)
 #undef KD_LAUNCH_4
 #undef KD_LAUNCH_2
-    return cudaErrorInvalidValue;
 }
 
 }  // namespace kd

@@ -643,18 +643,24 @@ bool attn_q8_supported(int hd, int group) {
     return hd == AttnQ8Smem::HD && (group == 1 || group == 2 || group == 4 || group == 8);
 }
 
-cudaError_t attn_q8_init_attributes() {
+template <bool WIN>
+static cudaError_t split_q8_attributes() {
     cudaError_t e = cudaSuccess;
-    for (const void* f : {(const void*)attn_split_q8_kernel<1, false>, (const void*)attn_split_q8_kernel<1, true>,
-                          (const void*)attn_split_q8_kernel<2, false>, (const void*)attn_split_q8_kernel<2, true>,
-                          (const void*)attn_split_q8_kernel<4, false>, (const void*)attn_split_q8_kernel<4, true>,
-                          (const void*)attn_split_q8_kernel<8, false>, (const void*)attn_split_q8_kernel<8, true>}) {
+    for (const void* f : {(const void*)attn_split_q8_kernel<1, WIN>, (const void*)attn_split_q8_kernel<2, WIN>,
+                          (const void*)attn_split_q8_kernel<4, WIN>, (const void*)attn_split_q8_kernel<8, WIN>}) {
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnQ8Smem::TOTAL)) != cudaSuccess)
             return e;
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                       cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
             return e;
     }
+    return cudaSuccess;
+}
+cudaError_t attn_q8_win_split_attributes() { return split_q8_attributes<true>(); }
+
+cudaError_t attn_q8_init_attributes() {
+    cudaError_t e = split_q8_attributes<false>();
+    if (e != cudaSuccess) return e;
     for (const void* f : {(const void*)kvq8_append_kernel, (const void*)kvq8_rows_kernel<__half>,
                           (const void*)kvq8_rows_kernel<float>})
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,

@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(64 * KD_BEAM_MAX_BEAMS) beam_merge_kernel(cons
 static int beam_scan_smem(int blocks, bool shifted) {
     return BS_STAGES * (shifted ? BS_STAGE<BEAM_SHIFTED> : BS_STAGE<BEAM_ALIGNED>) * 4 + blocks * BS_WARPS * 8;
 }
-cudaError_t beam_init_attributes() {
+static cudaError_t beam_init_attributes() {
     cudaError_t e = cudaSuccess;
     for (const void* f : {(const void*)beam_scan_kernel<BEAM_ALIGNED>, (const void*)beam_scan_kernel<BEAM_SHIFTED>,
                           (const void*)beam_scan_kernel<BEAM_SINGLY>, (const void*)beam_merge_kernel})
@@ -824,7 +824,8 @@ kd_status kd_beam_select(const float* logits, int64_t ld, int32_t n_groups, int3
     cudaStream_t s = (cudaStream_t)stream;
     int dev = 0;
     KD_TRY(cudaGetDevice(&dev));
-    KD_TRY(ensure_device_attributes(dev));
+    static OncePerDevice once;
+    KD_TRY(once(dev, beam_init_attributes));
     // Segments: as many per row as fill the GPU with four CTAs on every SM, at most
     // 32 (the merge's lanes) and one block each; more rows than that, one segment.
     int sms = 0;

@@ -2,6 +2,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "kd.h"
 
 namespace kd {
@@ -9,7 +11,20 @@ namespace kd {
 // Set the calling thread's last-error message (printf form) and return st.
 kd_status failf(kd_status st, const char* fmt, ...);
 
-cudaError_t beam_init_attributes();
+// Set-up made once per device, by the first call there that needs it; its result stands.
+class OncePerDevice {
+    static constexpr int DEVICES = 64;
+    std::once_flag once_[DEVICES];
+    cudaError_t err_[DEVICES] = {};
+
+public:
+    template <typename F>
+    cudaError_t operator()(int dev, F f) {
+        if (dev < 0 || dev >= DEVICES) return cudaErrorInvalidDevice;
+        std::call_once(once_[dev], [&] { err_[dev] = f(); });
+        return err_[dev];
+    }
+};
 
 }  // namespace kd
 

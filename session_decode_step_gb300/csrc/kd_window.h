@@ -79,12 +79,17 @@ inline void win_fill(AttnWinArgs& a, bool rows) {
         a.vitems += win_plan(a.vpos[b], a.window, a.sinks).ns * a.nkv;
     }
 }
+// Set up the windowed Q8_0 kernels on device dev, the current one, before their first launch there.
+cudaError_t attn_q8_win_prepare(int dev);
+cudaError_t attn_q8_win_split_attributes();  // its parts
+cudaError_t attn_win_combine_attributes();
 cudaError_t launch_attn_split_q8(const AttnWinArgs& a, const AttnMaps& maps, int grid, bool pdl, cudaStream_t s);
 cudaError_t launch_attn_combine(const AttnWinArgs& a, bool pdl, cudaStream_t s);
 // fp16 rows, in one launch (kd_attn_chain.cu).  From WIN_CHAIN_ITEMS items of a row's
 // capacity on, the keys are shared out wider.
 constexpr int WIN_CHAIN_ITEMS = 32;
-cudaError_t attn_chain_init_attributes();
-// max_keys: no row sees more.
-cudaError_t launch_attn_chain(const AttnWinArgs& a, int max_keys, int num_sms, bool pdl, cudaStream_t s);
+// Set up the kernels of a shape on device dev, the current one (a launch does so for its own).
+cudaError_t attn_chain_prepare(int hd, int group, int max_splits, int dev);
+// max_keys: no row sees more.  dev: the current device, num_sms its SMs.
+cudaError_t launch_attn_chain(const AttnWinArgs& a, int max_keys, int dev, int num_sms, bool pdl, cudaStream_t s);
 }  // namespace kd

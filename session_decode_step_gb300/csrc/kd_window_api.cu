@@ -10,6 +10,14 @@
 
 namespace kd {
 
+cudaError_t attn_q8_win_prepare(int dev) {
+    static OncePerDevice once;
+    return once(dev, [] {
+        const cudaError_t e = attn_q8_win_split_attributes();
+        return e == cudaSuccess ? attn_win_combine_attributes() : e;
+    });
+}
+
 static kd_status window_call(const char* fn, bool q8, const float* q, const float* k_new, const float* v_new, void* kc,
                              void* vc, uint16_t* ks, uint16_t* vs, const int32_t* slots, const int32_t* positions,
                              int32_t B, int32_t nh, int32_t nkv, int32_t hd, int32_t n_slots, int32_t cap,
@@ -50,7 +58,6 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     int dev = 0, sms = 0;
     KD_TRY(cudaGetDevice(&dev));
     KD_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    KD_TRY(ensure_device_attributes(dev));
     cudaStream_t s = (cudaStream_t)stream;
     t.q = q;
     t.B = B;
@@ -78,9 +85,10 @@ static kd_status window_call(const char* fn, bool q8, const float* q, const floa
     t.kc = (const __half*)kc;
     t.vc = (const __half*)vc;
     if (!q8) {
-        KD_TRY(launch_attn_chain(t, max_keys, sms, true, s));
+        KD_TRY(launch_attn_chain(t, max_keys, dev, sms, true, s));
         return KD_OK;
     }
+    KD_TRY(attn_q8_win_prepare(dev));
     AttnMaps maps;
     KD_TRY(make_attn_q8_maps((const uint8_t*)kc, (const uint8_t*)vc, (long)n_slots * nkv * cap, &maps));
     // persistent CTAs, no more than there are items

@@ -13,6 +13,10 @@ k_ti| / sqrt(hd).  Weights: twice that (numerator and denominator) plus expf's a
 the roundings of p, 2^-21, and the sums over items, (items + 10) 2^-23.  So o moves
 by at most eps sum_t p_t |v_t|; then it is rounded to fp16 once: 2^-11 |o| (2^-25
 below the normal range)."""
+import subprocess
+import sys
+from pathlib import Path
+
 import numpy as np
 import pytest
 
@@ -420,3 +424,62 @@ def test_model_window_steps_of_more_than_sixteen_sessions(kdlib, name, flags):
     finally:
         kd.kd_model_free(m)
         kd.kd_model_free(one)
+
+
+FRESH = """
+import numpy as np, torch
+import session_decode_step_gb300 as kd
+kd.lib()
+x = torch.randn(1, 16, 128, device="cuda")
+cache = torch.randn(2, 2, 4, 4096, 128, device="cuda", dtype=torch.float16)
+out = torch.zeros(1, 16 * 128, device="cuda", dtype=torch.float16)
+ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+
+def window(hd, w, nkv=4):
+    kd.kd_attn_window_append_decode(x, x, x, cache[0], cache[1], [1], [3000], 16, nkv, hd, 2, 4096, w, 3, out, ws)
+
+def captured(call):
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        call()
+    return g
+"""
+
+
+def fresh(code):
+    """A process of its own, in which no kernel of the library has run."""
+    r = subprocess.run([sys.executable, "-c", FRESH + code], capture_output=True, text=True, timeout=300,
+                       cwd=Path(__file__).resolve().parent.parent)
+    assert r.returncode == 0, r.stdout + r.stderr
+    return r.stdout
+
+
+def test_a_first_call_sets_up_no_windowed_kernels(kdlib):
+    """The device memory that a process's first call takes is the kernels of the plain path and the workspaces'
+    (2.1 MB, in steps of 2 MB); the 64 windowed kernels of all shapes are another 4 MB."""
+    took = fresh("""
+torch.cuda.synchronize()
+before = torch.cuda.mem_get_info()[0]
+kd.kd_attn_append_decode(x, x, x, cache[0], cache[1], [1], [30], 16, 4, 128, 2, 4096, out, ws)
+torch.cuda.synchronize()
+print(before - torch.cuda.mem_get_info()[0])
+""")
+    assert int(took.split()[-1]) < 4 << 20, took
+
+
+@pytest.mark.parametrize("hd,w,nkv", [(128, 40, 4), (128, 4000, 4), (64, 4000, 2), (64, 1000, 8)])
+def test_a_first_windowed_call_may_be_captured(kdlib, hd, w, nkv):
+    """Captured without any call before it, or after another shape's; replayed, and compared with the call itself."""
+    for before in ("", "window(128, 7)"):
+        fresh(f"""
+{before}
+g = captured(lambda: window({hd}, {w}, {nkv}))
+out.zero_()
+g.replay()
+torch.cuda.synchronize()
+got = out.clone()
+window({hd}, {w}, {nkv})
+torch.cuda.synchronize()
+assert torch.isfinite(got).all() and got.abs().sum() > 0 and torch.equal(got, out)
+""")
