@@ -9,6 +9,9 @@ only to hand over device memory and streams.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.machinery
+import importlib.util
+import operator
 import sys
 from pathlib import Path
 
@@ -16,6 +19,7 @@ import numpy as np
 
 _PKG = Path(__file__).resolve().parent
 LIB_PATH = _PKG / "libkd.so"
+CALL_PATH = _PKG / ("_kdcall" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 KD_MAX_BATCH = 16
 KD_ATTN_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -206,17 +210,82 @@ def _i32(a, n=None):
     return arr
 
 
+_I32P = C.POINTER(C.c_int32)
+
+
+def _int(v, bits=32):
+    v = operator.index(v)
+    if not -1 << (bits - 1) <= v < 1 << (bits - 1):
+        raise OverflowError(f"{v} does not fit {bits} bits")
+    return v
+
+
+class _CtypesCalls:
+    """csrc/kd_py.c's calls through ctypes, with the same arguments, checks and errors and a few us more a
+    call: where that module was not built for this interpreter."""
+
+    @staticmethod
+    def _window(fn, tensors, slots, positions, ints, out, workspace, stream):
+        tensors = [_ptr(t) for t in tensors]
+        slots = _i32(slots)
+        positions = _i32(positions, slots.size)
+        return fn(*tensors, slots.ctypes.data_as(_I32P), positions.ctypes.data_as(_I32P), slots.size, *map(_int, ints),
+                  _ptr(out), _ptr(workspace), workspace.nbytes, _stream(stream))
+
+    @classmethod
+    def window(cls, q, k_new, v_new, k_cache, v_cache, slots, positions, *rest):
+        *ints, out, workspace, stream = rest
+        return cls._window(lib().kd_attn_window_append_decode, (q, k_new, v_new, k_cache, v_cache), slots, positions, ints,
+                           out, workspace, stream)
+
+    @classmethod
+    def window_q8(cls, q, k_new, v_new, k_quants, k_scales, v_quants, v_scales, slots, positions, *rest):
+        *ints, out, workspace, stream = rest
+        return cls._window(lib().kd_attn_window_append_decode_q8, (q, k_new, v_new, k_quants, k_scales, v_quants, v_scales),
+                           slots, positions, ints, out, workspace, stream)
+
+    @staticmethod
+    def beam(logits, ld, n_groups, n_beams, V, scores, done, eos, n_out, parents, tokens, scores_out, done_out, workspace,
+             stream):
+        return lib().kd_beam_select(_ptr(logits), _int(ld, 64), _int(n_groups), _int(n_beams), _int(V), _ptr(scores),
+                                    _ptr(done), _int(eos), _int(n_out), _ptr(parents), _ptr(tokens), _ptr(scores_out),
+                                    _ptr(done_out), _ptr(workspace), workspace.nbytes, _stream(stream))
+
+    @staticmethod
+    def reorder(planes, dst, src, lens, n_layers, n_slots, n_kv_heads, cap, window, sinks, stream):
+        planes = list(planes)
+        sizes = [_int(v) for v in (n_layers, n_slots, n_kv_heads, cap)]
+        window, sinks = _int(window), _int(sinks)
+        if min(sizes) < 1:
+            raise ValueError("n_layers, n_slots, n_kv_heads and cap must be positive")
+        rows = sizes[0] * sizes[1] * sizes[2] * sizes[3]
+        base, width = [_ptr(t) for t in planes], [t.nbytes // rows for t in planes]
+        if any(t.nbytes % rows or w >= 1 << 31 for t, w in zip(planes, width)):
+            raise ValueError("a plane's size must be a whole number of bytes per row")
+        dst = _i32(dst)
+        src, lens = _i32(src, dst.size), _i32(lens, dst.size)
+        return lib().kd_kv_reorder((C.c_void_p * len(base))(*base), (C.c_int32 * len(base))(*width), len(base), *sizes,
+                                   *(a.ctypes.data_as(_I32P) for a in (dst, src, lens)), dst.size, window, sinks,
+                                   _stream(stream))
+
+
 _call = None
 
 
 def _fast():
-    """The marshalling module of the per-token calls (csrc/kd_py.c), beside libkd.so."""
+    """The marshalling module of the per-token calls (csrc/kd_py.c), beside libkd.so; ctypes without it."""
     global _call
     if _call is None:
         lib()
-        from . import _kdcall
-        _kdcall.setup(_ptr, _i32, _stream)
-        _call = _kdcall
+        call = _CtypesCalls
+        if CALL_PATH.exists():  # by its path: another interpreter's module is never taken for this one's
+            name = f"{__name__}._kdcall"
+            spec = importlib.util.spec_from_file_location(name, CALL_PATH, loader=importlib.machinery.ExtensionFileLoader(
+                name, str(CALL_PATH)))
+            call = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(call)
+            call.setup(_ptr, _i32, _stream)
+        _call = call
     return _call
 
 

@@ -3,11 +3,13 @@
 Each .cu file compiles in parallel into _build/, then one shared library is
 linked next to this file.  No CMake; the static CUDA runtime is linked in, so
 loading the library needs no GPU (a call that reaches CUDA then fails cleanly).
-_kdcall.so, the binding's marshalling module, is compiled for the running Python
-and linked against it.
+The binding's marshalling module, _kdcall, is compiled for the running Python and
+linked against it; its file carries the interpreter's ABI suffix.  Without a C compiler
+or Python's headers it is left out, and the binding makes those calls through ctypes.
 """
 from __future__ import annotations
 
+import importlib.machinery
 import os
 import shutil
 import subprocess
@@ -21,7 +23,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = PKG / "libkd.so"
-CALL = PKG / "_kdcall.so"
+CALL = PKG / ("_kdcall" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v",
@@ -39,19 +41,37 @@ def _sources():
     return sorted(CSRC.glob("*.cu"))
 
 
-def _stale() -> bool:
-    if not LIB.exists() or not CALL.exists():
+def _older(target: Path, deps) -> bool:
+    """target is missing, or older than one of deps or than the headers and this file."""
+    if not target.exists():
         return True
-    t = min(LIB.stat().st_mtime, CALL.stat().st_mtime)
-    deps = list(_sources()) + list(CSRC.glob("*.c")) + list(CSRC.glob("*.h")) + list(CSRC.glob("*.cuh")) + list(INCLUDE.glob("*.h"))
-    deps.append(Path(__file__))
-    return any(d.stat().st_mtime > t for d in deps)
+    t = target.stat().st_mtime
+    return any(d.stat().st_mtime > t for d in [*deps, *INCLUDE.glob("*.h"), Path(__file__)])
+
+
+def _stale() -> bool:
+    return _older(LIB, [*_sources(), *CSRC.glob("*.h"), *CSRC.glob("*.cuh")])
+
+
+def _cc():
+    return os.environ.get("CC") or shutil.which("cc") or shutil.which("gcc")
+
+
+def _python_headers():
+    inc = Path(sysconfig.get_paths()["include"])
+    return inc if (inc / "Python.h").exists() else None
 
 
 def build(force: bool = False, verbose: bool = False) -> Path:
-    """Compile every CUDA source and link libkd.so; returns its path."""
-    if not force and not _stale():
-        return LIB
+    """Compile every CUDA source, link libkd.so and compile the marshalling module; returns libkd.so's path."""
+    if force or _stale():
+        _build_lib(verbose)
+    if force or _older(CALL, [CSRC / "kd_py.c"]):
+        _build_call()
+    return LIB
+
+
+def _build_lib(verbose: bool):
     BUILD.mkdir(exist_ok=True)
     nv = nvcc()
 
@@ -76,20 +96,19 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     if r.returncode != 0:
         raise RuntimeError(f"linking libkd.so failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_call()
-    return LIB
 
 
 def _build_call():
-    cc = os.environ.get("CC") or shutil.which("cc") or shutil.which("gcc")
-    if not cc:
-        raise RuntimeError("no C compiler found (cc, gcc): it is required to build _kdcall.so")
+    cc, headers = _cc(), _python_headers()
+    if not cc or not headers:
+        CALL.unlink(missing_ok=True)  # what is there is out of date
+        return
     tmp = str(CALL) + ".tmp"
-    cmd = [cc, "-O2", "-fPIC", "-shared", "-Wall", f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}",
+    cmd = [cc, "-O2", "-fPIC", "-shared", "-Wall", f"-I{headers}", f"-I{INCLUDE}",
            str(CSRC / "kd_py.c"), "-o", tmp, f"-L{PKG}", "-l:libkd.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"compiling _kdcall.so failed:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"compiling {CALL.name} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALL)
 
 
