@@ -565,6 +565,142 @@ kd_status kd_kv_reorder(void* const* planes, const int32_t* row_bytes, int32_t n
                         const int32_t* lens, int32_t n, int32_t window, int32_t sinks, kd_stream stream);
 
 /* ------------------------------------------------------------------------
+ * Paged sessions: rotary positions, and caches in pages that sessions can
+ * share.  A paged cache is [n_pages][n_kv_heads][page_size] rows of head_dim
+ * fp16 values (or Q8_0 rows, see KD_FLAG_KV_Q8_0); position p of session b is row
+ * p % page_size of page table[b * table_ld + p / page_size].  The table is
+ * device int32, read when the call's work runs; the other arrays of a call are host
+ * arrays and travel with the launches, so calls copy nothing to the device and
+ * can be captured into a graph (what the host arrays held is then fixed in it).
+ * A page is page_size rows, a multiple of 16 up to 65536.  Pages may be permuted, forked and
+ * joined by kd_kv_reorder: a paged plane is its [1][n_pages][n_kv_heads][page_size].
+ * Where the table names a page outside [0, n_pages), nothing is read or written
+ * there: such a new row is dropped, such a key is not attended, and *fault (device
+ * int32, or NULL) is set to 1; calls never clear it.
+ * ---------------------------------------------------------------------- */
+enum { KD_F32 = 0, KD_F16 = 1, KD_BF16 = 2 };
+
+#define KD_ROPE_MAX_DIM 256
+enum { KD_ROPE_HALF = 0, KD_ROPE_PAIRS = 1 };
+enum { KD_ROPE_UNSCALED = 0, KD_ROPE_LINEAR = 1, KD_ROPE_BANDS = 2, KD_ROPE_RAMP = 3 };
+
+/* Rotary positions.  The first rot_dim dims of a head turn in pairs (a, b):
+ * (i, i + rot_dim / 2) with KD_ROPE_HALF, (2i, 2i + 1) with KD_ROPE_PAIRS; the
+ * others pass unchanged.  At position p pair i becomes
+ *   m (x_a cos w - x_b sin w),  m (x_b cos w + x_a sin w),   w = p f_i,
+ * m = magnitude and f_i from theta^(-2i / rot_dim), scaled for long contexts:
+ *   KD_ROPE_LINEAR: f / factor;
+ *   KD_ROPE_BANDS: with n = original_ctx f / 2 pi (the turns it makes over the
+ *     trained context), f (k + (1 - k) / factor), k = (n - low) / (high - low)
+ *     within [0, 1]: fast pairs keep their pace, slow ones are slowed by factor;
+ *   KD_ROPE_RAMP: f (1 - r + r / factor), r = (i - a) / (b - a) within [0, 1],
+ *     a = max(0, floor(d(high))), b = min(rot_dim - 1, ceil(d(low))), d(n) =
+ *     rot_dim ln(original_ctx / 2 pi n) / (2 ln theta), b - a at least 0.001: the
+ *     blend of Peng et al., "YaRN: Efficient Context Window Extension of Large
+ *     Language Models" (2023), whose attention factor is `magnitude`. */
+typedef struct {
+    int32_t head_dim, rot_dim; /* head_dim <= KD_ROPE_MAX_DIM, rot_dim even, 2 <= rot_dim <= head_dim */
+    int32_t layout, scaling;
+    int32_t original_ctx;      /* BANDS, RAMP: >= 1 */
+    int32_t reserved;          /* 0 */
+    double theta;              /* > 1 */
+    double factor;             /* > 0; UNSCALED ignores it */
+    double low, high;          /* BANDS, RAMP: 0 < low < high */
+    double magnitude;          /* finite */
+} kd_rope_config;
+
+/* What the rotating calls take: pair i turns by turns[i] / 2^64 of a whole turn
+ * per position (so an integer position's angle is exact modulo a turn). */
+typedef struct {
+    int32_t head_dim, rot_dim, layout, reserved;
+    double magnitude;
+    uint64_t turns[KD_ROPE_MAX_DIM / 2];
+} kd_rope_table;
+
+/* Fill a table from a configuration: host only, no CUDA call.  Errors:
+ * KD_ERR_INVALID_ARG, KD_ERR_UNSUPPORTED (head_dim). */
+kd_status kd_rope_plan(const kd_rope_config* cfg, kd_rope_table* out);
+
+/* Rotate n_tokens rows of n_heads heads: head h of token t is the head_dim values
+ * at x + t * ld + h * head_dim, rotated by positions[t] (device int32; a
+ * negative position turns back, so the same call with -p undoes p and is the
+ * rotation's transpose) to out + t * ld_out + h * head_dim.  dtype: of x and out (fp32 is
+ * rounded once; fp16 and bf16 are computed in fp32 and rounded once more).  out may be x
+ * with ld_out = ld; otherwise they must not overlap.  x and out are aligned to
+ * their type.  n_tokens = 0 does nothing.
+ * Errors: KD_ERR_INVALID_ARG (null or misaligned pointers, a bad table, dtype, n_tokens < 0,
+ * n_heads < 1, ld or ld_out < n_heads * head_dim), KD_ERR_UNSUPPORTED (more
+ * than 2^31 - 1 heads in all). */
+kd_status kd_rope(const kd_rope_table* rope, const void* x, int32_t dtype, int64_t ld, const int32_t* positions,
+                  int32_t n_tokens, int32_t n_heads, void* out, int64_t ld_out, kd_stream stream);
+
+#define KD_PAGED_MAX_SEQS 256
+
+/* Append new keys, rotated, and values to a paged cache; rotate the queries alongside.
+ * Session b (< n_seqs <= KD_PAGED_MAX_SEQS) gets counts[b] >= 0 rows from position
+ * starts[b] >= 0 on; the new rows of all sessions lie one after another, session
+ * 0's first: row t's KV head h is the head_dim values at k_new + t * k_ld + h * head_dim
+ * (v_new, q alike, each with its own ld), all of type dtype.
+ *   K row = fp16(rotate(k, its position)), V row = fp16(v); the Q8_0 form takes
+ *   both in fp32 and quantises them as KD_FLAG_KV_Q8_0 states.
+ *   q_out[t][n_heads][head_dim] = rotate(q, its position), fp32: what the attention takes.
+ * rope: NULL for keys and queries that are not rotated; else its head_dim must be
+ * the cache's.  q, q_out: NULL, with n_heads = 0, for no queries.  Rows of pages
+ * that belong to no new position stay as they were.  No two new rows may share a
+ * place; outputs must not overlap inputs.
+ * starts[b] + counts[b] <= table_ld * page_size.  head_dim is 64 or 128 (Q8_0: 128).
+ * Pages and q_out 16-byte aligned, k_new, v_new and q to their type.
+ * Errors: KD_ERR_BATCH (n_seqs), KD_ERR_POSITION (starts, counts), KD_ERR_UNSUPPORTED
+ * (head_dim, page_size, 2^31 or more new heads in all), KD_ERR_INVALID_ARG. */
+kd_status kd_paged_append(const kd_rope_table* rope, const void* k_new, int64_t k_ld, const void* v_new, int64_t v_ld,
+                          const void* q, int64_t q_ld, int32_t dtype, uint16_t* k_pages, uint16_t* v_pages,
+                          const int32_t* table, int32_t table_ld, const int32_t* starts, const int32_t* counts,
+                          int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t n_pages,
+                          int32_t page_size, float* q_out, int32_t* fault, kd_stream stream);
+kd_status kd_paged_append_q8(const kd_rope_table* rope, const void* k_new, int64_t k_ld, const void* v_new, int64_t v_ld,
+                             const void* q, int64_t q_ld, int32_t dtype, uint8_t* k_quants, uint16_t* k_scales,
+                             uint8_t* v_quants, uint16_t* v_scales, const int32_t* table, int32_t table_ld,
+                             const int32_t* starts, const int32_t* counts, int32_t n_seqs, int32_t n_heads,
+                             int32_t n_kv_heads, int32_t n_pages, int32_t page_size, float* q_out, int32_t* fault,
+                             kd_stream stream);
+
+/* Bytes of device workspace a paged attention call needs at most, whatever its
+ * lengths and groups (0 for sizes a call refuses). */
+size_t kd_attn_paged_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+
+/* A decode step's attention over a paged cache, reading a prefix that sessions share once for all of them:
+ *   out[b][qh] = fp16(sum_{t < lens[b]} softmax_t(q[b][qh] . K_t / sqrt(head_dim)) V_t)
+ * over KV head qh / (n_heads / n_kv_heads); zeros where lens[b] is 0 (or no key's
+ * page exists).  Keys behind lens[b] are not used, whatever they hold.
+ * B sessions, 1 <= B <= KD_PAGED_MAX_SEQS.  Groups: sessions in order, group g the
+ * next group_rows[g] >= 1 of them (B in all), which share their first
+ * group_prefix[g] keys (0 <= group_prefix[g] <= each of their lens; it may end within a page):
+ * these are read through the table of the group's first session, and the others'
+ * tables are not read for whole pages of it.  n_groups = 0: nothing is shared
+ * (group_rows, group_prefix ignored).  Results do not depend on where pages lie;
+ * lengths and groups decide how the keys are split, so a session's result can differ in
+ * the last bits between batches.
+ * q: device fp32 [B][n_heads][head_dim]; out: device fp16 [B][n_heads * head_dim];
+ * lens, group_rows, group_prefix: host int32.  head_dim 64 or 128 (Q8_0: 128),
+ * n_heads 1, 2, 4 or 8 times n_kv_heads, n_kv_heads <= 1024.  lens[b] <= table_ld * page_size.
+ * workspace: kd_attn_paged_workspace_bytes(...) bytes, used by one call at a time.
+ * q, pages and workspace 16-byte aligned, out 2-byte.
+ * kd_attn_device_status(workspace, ...) reads the call's fault word.
+ * Errors: KD_ERR_BATCH (B), KD_ERR_POSITION (lens, group_prefix), KD_ERR_UNSUPPORTED (shapes, page_size,
+ * n_pages * n_kv_heads * page_size of 2^31 or more), KD_ERR_INVALID_ARG. */
+kd_status kd_attn_paged_decode(const float* q, const uint16_t* k_pages, const uint16_t* v_pages, const int32_t* table,
+                               int32_t table_ld, const int32_t* lens, int32_t B, const int32_t* group_rows,
+                               const int32_t* group_prefix, int32_t n_groups, int32_t n_heads, int32_t n_kv_heads,
+                               int32_t head_dim, int32_t n_pages, int32_t page_size, uint16_t* out, void* workspace,
+                               size_t workspace_bytes, int32_t* fault, kd_stream stream);
+kd_status kd_attn_paged_decode_q8(const float* q, const uint8_t* k_quants, const uint16_t* k_scales,
+                                  const uint8_t* v_quants, const uint16_t* v_scales, const int32_t* table,
+                                  int32_t table_ld, const int32_t* lens, int32_t B, const int32_t* group_rows,
+                                  const int32_t* group_prefix, int32_t n_groups, int32_t n_heads, int32_t n_kv_heads,
+                                  int32_t n_pages, int32_t page_size, uint16_t* out, void* workspace,
+                                  size_t workspace_bytes, int32_t* fault, kd_stream stream);
+
+/* ------------------------------------------------------------------------
  * Allocation-free variant (no counterpart on the batched-decode pages: it
  * exists for callers, not for the method).
  *

@@ -1,0 +1,51 @@
+// kd_paged.h -- attention over a paged cache: the plan of a call, made on the host, and the
+// launch interface (library internal).
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "kd.h"
+
+namespace kd {
+
+// The keys of the sessions that each reads for itself are cut into blocks of PAGED_BLOCK.
+// Blocks are numbered session by session, head by head; CTA i of G takes blocks
+// [i N / G, (i + 1) N / G) of the N: an equal share, which may end one (session, head)
+// and begin the next.  What a CTA finds of a (session, head) x is record i + x, so a
+// (session, head)'s records are consecutive and no record is used twice.
+constexpr int PAGED_WARPS = 4;
+constexpr int PAGED_KEYS = 32;  // keys of a warp's piece
+constexpr int PAGED_BLOCK = PAGED_WARPS * PAGED_KEYS;
+constexpr int PAGED_MAX_CTAS = 1024;
+__host__ __device__ constexpr int PAGED_REC(int hd) { return hd + 4; }  // floats of one head's record: o, m, l
+
+struct PagedArgs {
+    const float* q;
+    const void *k, *v;          // pages: fp16 rows, or quants
+    const __half *ks, *vs;      // scales (Q8_0)
+    const int* table;
+    __half* out;
+    float* part;                // records
+    int* fault;                 // nullable
+    int* err;
+    int table_ld, n_pages, ps, B, nh, nkv, ctas;
+    int late_wait;              // started beside the kernel before, whose end it awaits at its own
+    float scale;
+    int64_t blocks;             // N
+    // Session b reads keys [from[b], to[b]); those before lead_keys[b] through session lead[b]'s table.
+    int from[KD_PAGED_MAX_SEQS], to[KD_PAGED_MAX_SEQS], lead_keys[KD_PAGED_MAX_SEQS];
+    int first[KD_PAGED_MAX_SEQS + 1];  // first block of the session's first head, in blocks / nkv
+    uint8_t lead[KD_PAGED_MAX_SEQS];
+};
+static_assert(KD_PAGED_MAX_SEQS <= 256, "sessions in a byte");
+
+__host__ __device__ inline int paged_blocks(int keys) { return (keys + PAGED_BLOCK - 1) / PAGED_BLOCK; }
+// The CTA that takes block x.
+__host__ __device__ inline int paged_cta(int64_t x, int64_t blocks, int ctas) { return (int)(((x + 1) * ctas - 1) / blocks); }
+
+// CTAs of the kernel that device dev, the current one, holds at once (0 on a CUDA error, left in *e).
+int paged_slots(int hd, int group, bool q8, int dev, int num_sms, cudaError_t* e);
+cudaError_t launch_paged(const PagedArgs& a, int hd, bool q8, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedArgs& a, int hd, bool pdl, cudaStream_t s);
+
+}  // namespace kd

@@ -1,0 +1,140 @@
+// kd_paged_api.cu -- the paged attention's entry points: checks, the plan, the launches.
+// The plan travels with the launches, so a call copies nothing to the device and can be
+// captured into a graph (its lengths and groups are then part of it; the table is not).
+#include <cmath>
+
+#include "kd_host.h"
+#include "kd_paged.h"
+
+namespace kd {
+
+static bool paged_shape(int32_t nh, int32_t nkv, int32_t hd, bool q8) {
+    if (nkv < 1 || nh < 1 || nh % nkv) return false;
+    const int g = nh / nkv;
+    return (g == 1 || g == 2 || g == 4 || g == 8) && (hd == 128 || (hd == 64 && !q8));
+}
+constexpr int PAGED_MAX_KV_HEADS = 1024;
+constexpr int PAGED_HEAD_BYTES = 256;  // the workspace's words before its records
+
+static kd_status paged_call(const char* fn, bool q8, const float* q, const void* kp, const void* vp, const uint16_t* ks,
+                            const uint16_t* vs, const int32_t* table, int32_t table_ld, const int32_t* lens, int32_t B,
+                            const int32_t* group_rows, const int32_t* group_prefix, int32_t n_groups, int32_t nh,
+                            int32_t nkv, int32_t hd, int32_t n_pages, int32_t ps, uint16_t* out, void* ws, size_t ws_bytes,
+                            int32_t* fault, kd_stream stream) {
+    if (!q || !kp || !vp || (q8 && (!ks || !vs)) || !table || !lens || !out || !ws ||
+        (n_groups > 0 && (!group_rows || !group_prefix)))
+        return failf(KD_ERR_INVALID_ARG, "%s: null argument", fn);
+    if (B < 1 || B > KD_PAGED_MAX_SEQS) return failf(KD_ERR_BATCH, "%s: B=%d outside [1, %d]", fn, B, KD_PAGED_MAX_SEQS);
+    if (!paged_shape(nh, nkv, hd, q8) || nkv > PAGED_MAX_KV_HEADS)
+        return failf(KD_ERR_UNSUPPORTED, "%s: head_dim %d, %d query heads, %d KV heads", fn, hd, nh, nkv);
+    if (ps < 16 || ps % 16 || ps > 65536) return failf(KD_ERR_UNSUPPORTED, "%s: page_size %d", fn, ps);
+    if (n_pages < 1 || table_ld < 1 || n_groups < 0)
+        return failf(KD_ERR_INVALID_ARG, "%s: n_pages %d, table_ld %d, n_groups %d", fn, n_pages, table_ld, n_groups);
+    if ((int64_t)n_pages * nkv > 0x7fffffff / ps) return failf(KD_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 cache rows", fn);
+    if (ws_bytes < kd_attn_paged_workspace_bytes(B, nh, nkv, hd)) return failf(KD_ERR_INVALID_ARG, "%s: workspace too small", fn);
+    if (((uintptr_t)q | (uintptr_t)kp | (uintptr_t)vp | (uintptr_t)ks | (uintptr_t)vs | (uintptr_t)ws) & 15)
+        return failf(KD_ERR_INVALID_ARG, "%s: q, pages and workspace must be 16-byte aligned", fn);
+    if ((((uintptr_t)table | (uintptr_t)fault) & 3) || ((uintptr_t)out & 1))
+        return failf(KD_ERR_INVALID_ARG, "%s: table and fault must be 4-byte aligned, out 2-byte", fn);
+    PagedArgs a = {};
+    int64_t total = 0;
+    for (int b = 0; b < B; ++b) {
+        if (lens[b] < 0 || lens[b] > (int64_t)table_ld * ps)
+            return failf(KD_ERR_POSITION, "%s: length %d in tables of %d pages of %d", fn, lens[b], table_ld, ps);
+        a.to[b] = lens[b];
+        a.lead[b] = (uint8_t)b;
+    }
+    if (n_groups) {
+        int b = 0;
+        for (int g = 0; g < n_groups; ++g) {
+            if (group_rows[g] < 1 || group_rows[g] > B - b)
+                return failf(KD_ERR_INVALID_ARG, "%s: group %d of %d sessions", fn, g, group_rows[g]);
+            for (int i = b; i < b + group_rows[g]; ++i) {
+                if (group_prefix[g] < 0 || group_prefix[g] > lens[i])
+                    return failf(KD_ERR_POSITION, "%s: prefix %d of a session of length %d", fn, group_prefix[g], lens[i]);
+                a.lead[i] = (uint8_t)b;
+                a.lead_keys[i] = group_prefix[g] / ps * ps;  // the page that the prefix ends in is each session's own
+            }
+            b += group_rows[g];
+        }
+        if (b != B) return failf(KD_ERR_INVALID_ARG, "%s: groups of %d sessions in all, B=%d", fn, b, B);
+    }
+    for (int b = 0; b < B; ++b) {
+        a.first[b] = (int)total;
+        total += paged_blocks(a.to[b] - a.from[b]);
+        if (total > 0x7fffffff / nkv) return failf(KD_ERR_UNSUPPORTED, "%s: 2^31 or more blocks of keys", fn);
+    }
+    a.first[B] = (int)total;
+    int dev = 0, sms = 0;
+    KD_TRY(cudaGetDevice(&dev));
+    KD_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    cudaError_t e;
+    const int slots = paged_slots(hd, nh / nkv, q8, dev, sms, &e);
+    KD_TRY(e);
+    a.q = q;
+    a.k = kp;
+    a.v = vp;
+    a.ks = (const __half*)ks;
+    a.vs = (const __half*)vs;
+    a.table = table;
+    a.table_ld = table_ld;
+    a.out = (__half*)out;
+    a.part = (float*)((char*)ws + PAGED_HEAD_BYTES);
+    a.err = (int*)ws + 2 * KD_MAX_BATCH;  // where kd_attn_device_status looks
+    a.fault = fault;
+    a.n_pages = n_pages;
+    a.ps = ps;
+    a.B = B;
+    a.nh = nh;
+    a.nkv = nkv;
+    a.scale = 1.0f / std::sqrt((float)hd);
+    a.blocks = total * nkv;
+    a.ctas = a.blocks < 1 ? 1 : a.blocks < slots ? (int)a.blocks : slots;
+    bool merge = false;
+    for (int b = 0; b < B && !merge; ++b) {
+        const int nb = a.first[b + 1] - a.first[b];
+        for (int h = 0; h < nkv && nb && !merge; ++h) {
+            const int64_t s0 = (int64_t)a.first[b] * nkv + (int64_t)h * nb;
+            merge = paged_cta(s0, a.blocks, a.ctas) != paged_cta(s0 + nb - 1, a.blocks, a.ctas);
+        }
+    }
+    cudaStream_t s = (cudaStream_t)stream;
+    KD_TRY(launch_paged(a, hd, q8, true, s));
+    if (merge) KD_TRY(launch_paged_merge(a, hd, true, s));
+    return KD_OK;
+}
+
+}  // namespace kd
+
+extern "C" {
+
+size_t kd_attn_paged_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
+    using namespace kd;
+    if (B < 1 || B > KD_PAGED_MAX_SEQS || !paged_shape(n_heads, n_kv_heads, head_dim, false) || n_kv_heads > PAGED_MAX_KV_HEADS) return 0;
+    // a record per CTA and (session, head) at most
+    const size_t records = (size_t)PAGED_MAX_CTAS + (size_t)B * n_kv_heads;
+    return PAGED_HEAD_BYTES + records * (n_heads / n_kv_heads) * PAGED_REC(head_dim) * sizeof(float);
+}
+
+kd_status kd_attn_paged_decode(const float* q, const uint16_t* k_pages, const uint16_t* v_pages, const int32_t* table,
+                               int32_t table_ld, const int32_t* lens, int32_t B, const int32_t* group_rows,
+                               const int32_t* group_prefix, int32_t n_groups, int32_t n_heads, int32_t n_kv_heads,
+                               int32_t head_dim, int32_t n_pages, int32_t page_size, uint16_t* out, void* workspace,
+                               size_t workspace_bytes, int32_t* fault, kd_stream stream) {
+    return kd::paged_call("kd_attn_paged_decode", false, q, k_pages, v_pages, nullptr, nullptr, table, table_ld, lens, B,
+                          group_rows, group_prefix, n_groups, n_heads, n_kv_heads, head_dim, n_pages, page_size, out,
+                          workspace, workspace_bytes, fault, stream);
+}
+
+kd_status kd_attn_paged_decode_q8(const float* q, const uint8_t* k_quants, const uint16_t* k_scales,
+                                  const uint8_t* v_quants, const uint16_t* v_scales, const int32_t* table,
+                                  int32_t table_ld, const int32_t* lens, int32_t B, const int32_t* group_rows,
+                                  const int32_t* group_prefix, int32_t n_groups, int32_t n_heads, int32_t n_kv_heads,
+                                  int32_t n_pages, int32_t page_size, uint16_t* out, void* workspace,
+                                  size_t workspace_bytes, int32_t* fault, kd_stream stream) {
+    return kd::paged_call("kd_attn_paged_decode_q8", true, q, k_quants, v_quants, k_scales, v_scales, table, table_ld, lens,
+                          B, group_rows, group_prefix, n_groups, n_heads, n_kv_heads, 128, n_pages, page_size, out,
+                          workspace, workspace_bytes, fault, stream);
+}
+
+}  // extern "C"

@@ -241,6 +241,136 @@ done:
     return r;
 }
 
+static int get_i64(PyObject* o, int64_t* out) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) return -1;
+    *out = v;
+    return 0;
+}
+
+/* table, x, dtype, ld, positions, n_tokens, n_heads, out, ld_out, stream */
+static PyObject* py_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    void *table, *x, *pos, *out, *st;
+    int32_t dtype, tokens, heads;
+    int64_t ld, ld_out;
+    kd_status s;
+    (void)self;
+    if (arity("kd_rope", n, 10) < 0 || get_ptr(a[0], &table) < 0 || get_ptr(a[1], &x) < 0 || get_i32(a[2], &dtype) < 0 ||
+        get_i64(a[3], &ld) < 0 || get_ptr(a[4], &pos) < 0 || get_i32(a[5], &tokens) < 0 || get_i32(a[6], &heads) < 0 ||
+        get_ptr(a[7], &out) < 0 || get_i64(a[8], &ld_out) < 0 || get_stream(a[9], &st) < 0)
+        return NULL;
+    Py_BEGIN_ALLOW_THREADS
+    s = kd_rope(table, x, dtype, ld, pos, tokens, heads, out, ld_out, st);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(s);
+}
+
+/* The planes of a cache, 2 (fp16 rows) or 4 (Q8_0). */
+static int get_planes(PyObject* o, void** p) {
+    Py_ssize_t i, n;
+    PyObject* seq = PySequence_Fast(o, "planes must be a sequence");
+    if (!seq) return -1;
+    n = PySequence_Fast_GET_SIZE(seq);
+    if (n != 2 && n != 4) {
+        PyErr_SetString(PyExc_ValueError, "a cache has 2 or 4 planes");
+        n = -1;
+    }
+    for (i = 0; i < n; ++i)
+        if (get_ptr(PySequence_Fast_GET_ITEM(seq, i), &p[i]) < 0) {
+            n = -1;
+            break;
+        }
+    Py_DECREF(seq);
+    return (int)n;
+}
+
+/* rope, k, k_ld, v, v_ld, q, q_ld, dtype, rows, planes, table, table_ld, starts, counts, n_heads, n_kv_heads, head_dim,
+ * n_pages, page_size, q_out, fault, stream */
+static PyObject* py_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    void *rope, *x[3], *p[4], *table, *q_out, *fault, *st;
+    int64_t ld[3], rows, sum = 0;
+    int32_t dtype, table_ld, v[5], B = 0;
+    Ints starts = {.held = 0}, counts = {.held = 0};
+    PyObject* r = NULL;
+    int i, planes, below = 0;
+    kd_status s;
+    (void)self;
+    if (arity("kd_paged_append", n, 22) < 0 || get_ptr(a[0], &rope) < 0) return NULL;
+    for (i = 0; i < 3; ++i)
+        if (get_ptr(a[1 + 2 * i], &x[i]) < 0 || get_i64(a[2 + 2 * i], &ld[i]) < 0) return NULL;
+    if (get_i32(a[7], &dtype) < 0 || get_i64(a[8], &rows) < 0 || (planes = get_planes(a[9], p)) < 0 ||
+        get_ptr(a[10], &table) < 0 || get_i32(a[11], &table_ld) < 0)
+        return NULL;
+    if (get_ints(a[12], &starts, -1, &B) < 0 || get_ints(a[13], &counts, B, NULL) < 0) goto done;
+    for (i = 0; i < 5; ++i)
+        if (get_i32(a[14 + i], &v[i]) < 0) goto done;
+    if (get_ptr(a[19], &q_out) < 0 || get_ptr(a[20], &fault) < 0 || get_stream(a[21], &st) < 0) goto done;
+    for (i = 0; i < B; ++i) {
+        const int32_t c = ((const int32_t*)counts.b.buf)[i];
+        below |= c < 0;
+        sum += c;
+    }
+    if (!below && sum != rows) {
+        PyErr_Format(PyExc_ValueError, "%lld new rows for counts of %lld in all", (long long)rows, (long long)sum);
+        goto done;
+    }
+    Py_BEGIN_ALLOW_THREADS
+    if (planes == 2)
+        s = kd_paged_append(rope, x[0], ld[0], x[1], ld[1], x[2], ld[2], dtype, p[0], p[1], table, table_ld, starts.b.buf,
+                            counts.b.buf, B, v[0], v[1], v[2], v[3], v[4], q_out, fault, st);
+    else
+        s = kd_paged_append_q8(rope, x[0], ld[0], x[1], ld[1], x[2], ld[2], dtype, p[0], p[1], p[2], p[3], table, table_ld,
+                               starts.b.buf, counts.b.buf, B, v[0], v[1], v[3], v[4], q_out, fault, st);
+    Py_END_ALLOW_THREADS
+    r = PyLong_FromLong(s);
+done:
+    drop(&starts);
+    drop(&counts);
+    return r;
+}
+
+/* q, planes, table, table_ld, lens, group_rows, group_prefix, n_heads, n_kv_heads, head_dim, n_pages, page_size, out,
+ * workspace, fault, stream */
+static PyObject* py_paged(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    void *q, *p[4], *table, *out, *ws, *fault, *st;
+    int32_t table_ld, v[5], B = 0, G = 0;
+    size_t bytes;
+    Ints lens = {.held = 0}, rows = {.held = 0}, prefix = {.held = 0};
+    PyObject* r = NULL;
+    int i, planes;
+    kd_status s;
+    (void)self;
+    if (arity("kd_attn_paged_decode", n, 16) < 0 || get_ptr(a[0], &q) < 0 || (planes = get_planes(a[1], p)) < 0 ||
+        get_ptr(a[2], &table) < 0 || get_i32(a[3], &table_ld) < 0)
+        return NULL;
+    if (get_ints(a[4], &lens, -1, &B) < 0) goto done;
+    if (a[5] != Py_None && get_ints(a[5], &rows, -1, &G) < 0) goto done;
+    if (a[6] != Py_None && get_ints(a[6], &prefix, G, NULL) < 0) goto done;
+    if (a[6] == Py_None && G > 0) {
+        PyErr_SetString(PyExc_ValueError, "groups without prefixes");
+        goto done;
+    }
+    for (i = 0; i < 5; ++i)
+        if (get_i32(a[7 + i], &v[i]) < 0) goto done;
+    if (get_ptr(a[12], &out) < 0 || get_ptr(a[13], &ws) < 0 || get_nbytes(a[13], &bytes) < 0 || get_ptr(a[14], &fault) < 0 ||
+        get_stream(a[15], &st) < 0)
+        goto done;
+    Py_BEGIN_ALLOW_THREADS
+    if (planes == 2)
+        s = kd_attn_paged_decode(q, p[0], p[1], table, table_ld, lens.b.buf, B, G ? rows.b.buf : NULL, G ? prefix.b.buf : NULL,
+                                 G, v[0], v[1], v[2], v[3], v[4], out, ws, bytes, fault, st);
+    else
+        s = kd_attn_paged_decode_q8(q, p[0], p[1], p[2], p[3], table, table_ld, lens.b.buf, B, G ? rows.b.buf : NULL,
+                                    G ? prefix.b.buf : NULL, G, v[0], v[1], v[3], v[4], out, ws, bytes, fault, st);
+    Py_END_ALLOW_THREADS
+    r = PyLong_FromLong(s);
+done:
+    drop(&lens);
+    drop(&rows);
+    drop(&prefix);
+    return r;
+}
+
 /* setup(_ptr, _i32, _stream) */
 static PyObject* py_setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     (void)self;
@@ -260,6 +390,9 @@ static PyMethodDef methods[] = {
     {"window_q8", (PyCFunction)(void (*)(void))py_window_q8, METH_FASTCALL, NULL},
     {"beam", (PyCFunction)(void (*)(void))py_beam, METH_FASTCALL, NULL},
     {"reorder", (PyCFunction)(void (*)(void))py_reorder, METH_FASTCALL, NULL},
+    {"rope", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, NULL},
+    {"append", (PyCFunction)(void (*)(void))py_append, METH_FASTCALL, NULL},
+    {"paged", (PyCFunction)(void (*)(void))py_paged, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL},
 };
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kdcall", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -1,0 +1,258 @@
+// kd_rope.cu -- rotary positions: the plan on the host, and rows of heads rotated
+// in place or to another place.
+//
+// A thread holds both halves of P pairs (16 bytes each way where sizes and alignment
+// allow, P = 4 in fp32 and 8 in 16 bits; else two pairs or one at a time), forms their
+// angles once and takes them through its share of the token's heads, four heads' loads
+// in flight.  As the pair never leaves the thread, x may be written in place.  fp32
+// results are rounded once (the angle and the products are carried as pairs of fp32);
+// fp16 and bf16 ones are formed in fp32, whose error is 2^-13 and 2^-16 of theirs.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+#include <type_traits>
+
+#include "kd_host.h"
+#include "kd_rope.cuh"
+#include "kd_rope.h"
+
+namespace kd {
+
+struct RopeArgs {
+    const void* x;
+    void* out;
+    const int* pos;
+    int64_t ld, ld_out;
+    int tokens, heads, hd;
+    int per, groups;  // heads per thread, threads per token and chunk
+    int nr, nc;       // chunks of P pairs, and with the unrotated dims' chunks of P
+    RopeAngles<KD_ROPE_MAX_DIM / 2> r;
+};
+
+template <typename T, int P>
+struct alignas(sizeof(T) * P) RopeVec {
+    T v[P];
+};
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float x, float& o) { o = x; }
+__device__ __forceinline__ void from_f(float x, __half& o) { o = __float2half_rn(x); }
+__device__ __forceinline__ void from_f(float x, __nv_bfloat16& o) { o = __float2bfloat16_rn(x); }
+
+constexpr int ROPE_THREADS = 256;
+
+template <typename T, bool PAIRS, int P>
+__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constant__ RopeArgs a) {
+    using V = RopeVec<T, P>;
+    constexpr bool EXACT = std::is_same<T, float>::value;
+    constexpr int U = 4;  // heads in flight
+    __shared__ float2 tab[ROPE_TAB];
+    __shared__ unsigned long long turns[KD_ROPE_MAX_DIM / 2];
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x, n = blockDim.x * blockDim.y;
+    for (int i = tid; i < ROPE_TAB; i += n) tab[i] = ROPE_COS[i];
+    for (int i = tid; i < a.r.rot / 2; i += n) turns[i] = a.r.turns[i];
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t unit = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int token = (int)(unit / a.groups), chunk = threadIdx.x;
+    if (token >= a.tokens) return;
+    const int h0 = (int)(unit - (int64_t)token * a.groups) * a.per, h1 = min(a.heads, h0 + a.per);
+    const T* x = (const T*)a.x + token * a.ld;
+    T* out = (T*)a.out + token * a.ld_out;
+    if (chunk >= a.nr) {  // dims that pass unchanged
+        if (a.x == a.out) return;
+        const int d = a.r.rot + (chunk - a.nr) * P;
+        for (int h = h0; h < h1; ++h)
+            *reinterpret_cast<V*>(out + (int64_t)h * a.hd + d) = *reinterpret_cast<const V*>(x + (int64_t)h * a.hd + d);
+        return;
+    }
+    // the two vectors of the thread's pairs
+    const int d0 = PAIRS ? 2 * P * chunk : P * chunk, d1 = PAIRS ? d0 + P : d0 + a.r.rot / 2;
+    const int pos = a.pos[token];
+    V u[U], w[U];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (h + i < h1) {
+                u[i] = *reinterpret_cast<const V*>(x + (int64_t)(h + i) * a.hd + d0);
+                w[i] = *reinterpret_cast<const V*>(x + (int64_t)(h + i) * a.hd + d1);
+            }
+    };
+    load(h0);
+    float2 c[P], s[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) rope_angle<EXACT>(turns[P * chunk + i], pos, a.r.mh, a.r.ml, tab, c[i], s[i]);
+    for (int h = h0; h < h1; h += U) {
+        V y[U], z[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (h + k < h1) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    // pair i: HALF u[i], w[i]; PAIRS elements 2i and 2i + 1 of u and w in a row
+                    auto at = [&](int e) -> float { return e < P ? to_f(u[k].v[e < P ? e : 0]) : to_f(w[k].v[e >= P ? e - P : 0]); };
+                    const float p = PAIRS ? at(2 * i) : to_f(u[k].v[i]), q = PAIRS ? at(2 * i + 1) : to_f(w[k].v[i]);
+                    const float rp = rope_turn<EXACT>(p, q, c[i], s[i], -1.0f), rq = rope_turn<EXACT>(q, p, c[i], s[i], 1.0f);
+                    auto put = [&](int e, float v) { from_f(v, e < P ? y[k].v[e < P ? e : 0] : z[k].v[e >= P ? e - P : 0]); };
+                    put(PAIRS ? 2 * i : i, rp);
+                    put(PAIRS ? 2 * i + 1 : P + i, rq);
+                }
+            }
+        const int now = h;
+        if (h + U < h1) load(h + U);
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (now + k < h1) {
+                *reinterpret_cast<V*>(out + (int64_t)(now + k) * a.hd + d0) = y[k];
+                *reinterpret_cast<V*>(out + (int64_t)(now + k) * a.hd + d1) = z[k];
+            }
+    }
+}
+
+template <typename T, int P>
+static cudaError_t launch_rope_p(RopeArgs& a, cudaStream_t s) {
+    a.nr = a.r.rot / 2 / P;
+    a.nc = a.nr + (a.hd - a.r.rot) / P;
+    const int by = ROPE_THREADS / a.nc;
+    // Heads per thread: the angles are formed once for them, and a thread that loops keeps
+    // loads in flight; but every SM should have a thousand threads' worth of work first.
+    const int64_t threads = (int64_t)a.tokens * a.heads * a.nc;
+    int64_t per = threads / (152 * 2048);
+    per = per < 1 ? 1 : per > 8 ? 8 : per;
+    a.per = (int)per;
+    a.groups = (a.heads + a.per - 1) / a.per;
+    const int64_t units = (int64_t)a.tokens * a.groups;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)((units + by - 1) / by));
+    cfg.blockDim = dim3(a.nc, by);
+    cfg.stream = s;
+    return a.r.pairs ? cudaLaunchKernelEx(&cfg, rope_kernel<T, true, P>, a) : cudaLaunchKernelEx(&cfg, rope_kernel<T, false, P>, a);
+}
+
+template <typename T>
+static cudaError_t launch_rope(RopeArgs& a, cudaStream_t s) {
+    constexpr int W = 16 / (int)sizeof(T);
+    // P pairs at a time: both vectors, the row ends and all strides lie on multiples of P
+    auto fits = [&](int p) {
+        return a.r.rot % (2 * p) == 0 && a.hd % p == 0 && a.ld % p == 0 && a.ld_out % p == 0 &&
+               (((uintptr_t)a.x | (uintptr_t)a.out) & (p * sizeof(T) - 1)) == 0;
+    };
+    if (fits(W)) return launch_rope_p<T, W>(a, s);
+    if (fits(2)) return launch_rope_p<T, 2>(a, s);
+    return launch_rope_p<T, 1>(a, s);
+}
+
+kd_status rope_table_check(const char* fn, const kd_rope_table* t) {
+    if (t->head_dim < 2 || t->head_dim > KD_ROPE_MAX_DIM || t->rot_dim < 2 || t->rot_dim % 2 || t->rot_dim > t->head_dim ||
+        (t->layout != KD_ROPE_HALF && t->layout != KD_ROPE_PAIRS) || t->reserved || !std::isfinite((float)t->magnitude))
+        return failf(KD_ERR_INVALID_ARG, "%s: not a table that kd_rope_plan made (head_dim %d, rot_dim %d, layout %d)", fn,
+                     t->head_dim, t->rot_dim, t->layout);
+    return KD_OK;
+}
+
+}  // namespace kd
+
+extern "C" {
+
+kd_status kd_rope_plan(const kd_rope_config* c, kd_rope_table* out) {
+    using kd::failf;
+    const char* fn = "kd_rope_plan";
+    if (!c || !out) return failf(KD_ERR_INVALID_ARG, "%s: null argument", fn);
+    if (c->head_dim > KD_ROPE_MAX_DIM)
+        return failf(KD_ERR_UNSUPPORTED, "%s: head_dim %d (at most %d)", fn, c->head_dim, KD_ROPE_MAX_DIM);
+    if (c->rot_dim < 2 || c->rot_dim % 2 || c->rot_dim > c->head_dim)
+        return failf(KD_ERR_INVALID_ARG, "%s: rot_dim %d of head_dim %d", fn, c->rot_dim, c->head_dim);
+    if (c->layout != KD_ROPE_HALF && c->layout != KD_ROPE_PAIRS)
+        return failf(KD_ERR_INVALID_ARG, "%s: layout %d", fn, c->layout);
+    if (c->scaling < KD_ROPE_UNSCALED || c->scaling > KD_ROPE_RAMP)
+        return failf(KD_ERR_INVALID_ARG, "%s: scaling %d", fn, c->scaling);
+    if (c->reserved) return failf(KD_ERR_INVALID_ARG, "%s: reserved must be 0", fn);
+    if (!(c->theta > 1.0) || !std::isfinite(c->theta)) return failf(KD_ERR_INVALID_ARG, "%s: theta %g", fn, c->theta);
+    if (!std::isfinite((float)c->magnitude)) return failf(KD_ERR_INVALID_ARG, "%s: magnitude %g", fn, c->magnitude);
+    const bool blends = c->scaling == KD_ROPE_BANDS || c->scaling == KD_ROPE_RAMP;
+    if (c->scaling != KD_ROPE_UNSCALED && (!(c->factor > 0.0) || !std::isfinite(c->factor)))
+        return failf(KD_ERR_INVALID_ARG, "%s: factor %g", fn, c->factor);
+    if (blends && (c->original_ctx < 1 || !(c->low > 0.0) || !(c->high > c->low) || !std::isfinite(c->high)))
+        return failf(KD_ERR_INVALID_ARG, "%s: original_ctx %d, low %g, high %g", fn, c->original_ctx, c->low, c->high);
+    const double turn = 6.283185307179586476925286766559;
+    const int n = c->rot_dim;
+    double a = 0, b = 0;
+    if (c->scaling == KD_ROPE_RAMP) {
+        auto dim = [&](double turns) { return n * std::log(c->original_ctx / (turns * turn)) / (2 * std::log(c->theta)); };
+        a = std::fmax(0.0, std::floor(dim(c->high)));
+        b = std::fmin(n - 1.0, std::ceil(dim(c->low)));
+    }
+    kd_rope_table t = {};
+    t.head_dim = c->head_dim;
+    t.rot_dim = n;
+    t.layout = c->layout;
+    t.magnitude = c->magnitude;
+    for (int i = 0; i < n / 2; ++i) {
+        double f = std::pow(c->theta, -2.0 * i / n);
+        if (c->scaling == KD_ROPE_LINEAR) f /= c->factor;
+        if (blends) {
+            double slow;  // how much of the pair's pace is slowed
+            if (c->scaling == KD_ROPE_BANDS)
+                slow = 1.0 - std::fmin(1.0, std::fmax(0.0, (c->original_ctx * f / turn - c->low) / (c->high - c->low)));
+            else
+                slow = std::fmin(1.0, std::fmax(0.0, (i - a) / std::fmax(b - a, 0.001)));
+            f *= (1.0 - slow) + slow / c->factor;
+        }
+        // turns per position modulo 1, to 2^-64 (positions are whole, so whole turns drop out)
+        double r = f / turn;
+        r -= std::floor(r);
+        t.turns[i] = (uint64_t)std::ldexp(r, 32) << 32;
+        const double rest = std::ldexp(r, 32) - std::floor(std::ldexp(r, 32));
+        t.turns[i] += (uint64_t)std::floor(std::ldexp(rest, 32) + 0.5);
+    }
+    *out = t;
+    return KD_OK;
+}
+
+kd_status kd_rope(const kd_rope_table* rope, const void* x, int32_t dtype, int64_t ld, const int32_t* positions,
+                  int32_t n_tokens, int32_t n_heads, void* out, int64_t ld_out, kd_stream stream) {
+    using kd::failf;
+    const char* fn = "kd_rope";
+    if (!rope || !x || !positions || !out) return failf(KD_ERR_INVALID_ARG, "%s: null argument", fn);
+    const kd_status st = kd::rope_table_check(fn, rope);
+    if (st != KD_OK) return st;
+    if (dtype < KD_F32 || dtype > KD_BF16) return failf(KD_ERR_INVALID_ARG, "%s: dtype %d", fn, dtype);
+    if (n_tokens < 0 || n_heads < 1) return failf(KD_ERR_INVALID_ARG, "%s: %d tokens of %d heads", fn, n_tokens, n_heads);
+    const int64_t row = (int64_t)n_heads * rope->head_dim;
+    if (ld < row || ld_out < row || ld > INT64_MAX / 4 / ((int64_t)n_tokens + 1) || ld_out > INT64_MAX / 4 / ((int64_t)n_tokens + 1))
+        return failf(KD_ERR_INVALID_ARG, "%s: ld %lld, ld_out %lld for rows of %lld", fn, (long long)ld, (long long)ld_out,
+                     (long long)row);
+    const uintptr_t mask = dtype == KD_F32 ? 3 : 1;
+    if ((((uintptr_t)x | (uintptr_t)out) & mask) || ((uintptr_t)positions & 3))
+        return failf(KD_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+    if (x == out && ld != ld_out) return failf(KD_ERR_INVALID_ARG, "%s: in place, but ld %lld and ld_out %lld", fn, (long long)ld, (long long)ld_out);
+    if ((int64_t)n_tokens * n_heads > 0x7fffffff) return failf(KD_ERR_UNSUPPORTED, "%s: %d tokens of %d heads", fn, n_tokens, n_heads);
+    if (!n_tokens) return KD_OK;
+    kd::RopeArgs a = {};
+    a.x = x;
+    a.out = out;
+    a.pos = positions;
+    a.ld = ld;
+    a.ld_out = ld_out;
+    a.tokens = n_tokens;
+    a.heads = n_heads;
+    a.hd = rope->head_dim;
+    kd::rope_fill(a.r, *rope);
+    cudaStream_t s = (cudaStream_t)stream;
+    switch (dtype) {
+        case KD_F32: KD_TRY(kd::launch_rope<float>(a, s)); break;
+        case KD_F16: KD_TRY(kd::launch_rope<__half>(a, s)); break;
+        default: KD_TRY(kd::launch_rope<__nv_bfloat16>(a, s));
+    }
+    return KD_OK;
+}
+
+}  // extern "C"
