@@ -540,37 +540,60 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
 }
 
 // The merge of a (session, head) that several CTAs share: out = sum_i w_i o_i / sum_i w_i l_i
-// over its records, w_i = e^{m_i - max m}.  A block per (session, KV head).
+// over its records, w_i = e^{m_i - max m}: those of its own keys and those that the CTAs of
+// its group's shared keys left.  A block per (session, KV head).
 constexpr int PAGED_MERGE_THREADS = 128;
 template <int HD>
-__global__ void __launch_bounds__(PAGED_MERGE_THREADS) paged_merge_kernel(const __grid_constant__ PagedArgs a) {
+__global__ void __launch_bounds__(PAGED_MERGE_THREADS) paged_merge_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ SharedArgs sh) {
     constexpr int REC = PAGED_REC(HD);
     const int h = blockIdx.x, b = blockIdx.y, gq = a.nh / a.nkv;
     pdl_launch_dependents();
     pdl_wait();
-    const int nb = a.first[b + 1] - a.first[b];
-    if (!nb) return;
-    const int64_t s0 = (int64_t)a.first[b] * a.nkv + (int64_t)h * nb;
-    const int c0 = paged_cta(s0, a.blocks, a.ctas), c1 = paged_cta(s0 + nb - 1, a.blocks, a.ctas);
-    if (c0 == c1 && a.from[b] == 0) return;  // written by the CTA itself
-    const float* rec = a.part + ((size_t)c0 + (size_t)b * a.nkv + h) * gq * REC;
-    const int n = c1 - c0 + 1;
+    if (sh.n_groups && h == 0 && b == 0 && threadIdx.x < 32) {  // the call's fault word
+        int bad = 0;
+        for (int i = threadIdx.x; i < sh.sets * sh.side; i += 32) bad |= sh.status[i];
+        bad = __any_sync(FULL_MASK, bad != 0);
+        if (threadIdx.x == 0) *a.err = bad ? ERR_WAIT_TIMEOUT : 0;
+    }
+    const int nb = a.first[b + 1] - a.first[b], g = a.group[b];
+    if (!nb && g == SHARED_NONE) return;
+    const float* rec = nullptr;
+    int n = 0;
+    if (nb) {
+        const int64_t s0 = (int64_t)a.first[b] * a.nkv + (int64_t)h * nb;
+        const int c0 = paged_cta(s0, a.blocks, a.ctas), c1 = paged_cta(s0 + nb - 1, a.blocks, a.ctas);
+        if (c0 == c1 && g == SHARED_NONE) return;  // written by the CTA itself
+        rec = a.part + ((size_t)c0 + (size_t)b * a.nkv + h) * gq * REC;
+        n = c1 - c0 + 1;
+    }
     for (int i = threadIdx.x; i < gq * (HD / 4); i += PAGED_MERGE_THREADS) {
         const int qh = i / (HD / 4), d = i % (HD / 4) * 4;
-        float M = -INFINITY;
-        for (int k = 0; k < n; ++k) M = fmaxf(M, rec[((size_t)k * gq + qh) * REC + HD]);
-        const float ref = M == -INFINITY ? 0.0f : M;
-        float den = 0.0f;
+        float M = -INFINITY, den = 0.0f;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int k = 0; k < n; ++k) {
-            const float* r = rec + ((size_t)k * gq + qh) * REC;
-            const float w = expf(__fsub_rn(r[HD], ref));
-            den = __fmaf_rn(w, r[HD + 1], den);
+        auto add = [&](const float* r) {
+            const float2 ml = *reinterpret_cast<const float2*>(r + HD);
             const float4 v = *reinterpret_cast<const float4*>(r + d);
-            acc.x = __fmaf_rn(w, v.x, acc.x);
-            acc.y = __fmaf_rn(w, v.y, acc.y);
-            acc.z = __fmaf_rn(w, v.z, acc.z);
-            acc.w = __fmaf_rn(w, v.w, acc.w);
+            const float top = fmaxf(M, ml.x), ref = top == -INFINITY ? 0.0f : top;
+            const float f = expf(__fsub_rn(M, ref)), w = expf(__fsub_rn(ml.x, ref));
+            M = top;
+            den = __fmaf_rn(den, f, __fmul_rn(w, ml.y));
+            acc.x = __fmaf_rn(acc.x, f, __fmul_rn(w, v.x));
+            acc.y = __fmaf_rn(acc.y, f, __fmul_rn(w, v.y));
+            acc.z = __fmaf_rn(acc.z, f, __fmul_rn(w, v.z));
+            acc.w = __fmaf_rn(acc.w, f, __fmul_rn(w, v.w));
+        };
+        for (int k = 0; k < n; ++k) add(rec + ((size_t)k * gq + qh) * REC);
+        if (g != SHARED_NONE) {
+            const int query = (b - sh.lead[g]) * gq + qh, pass = query / (SHARED_QUERIES * sh.side), T = sh.tiles(g);
+            const int64_t s0 = (int64_t)sh.first[g] * sh.nkv + ((int64_t)h * sh.passes(g) + pass) * T;
+            const int c0 = paged_cta(s0, sh.total, sh.sets), c1 = paged_cta(s0 + T - 1, sh.total, sh.sets);
+            for (int c = c0; c <= c1; ++c) {
+                const int64_t x0 = (int64_t)c * sh.total / sh.sets, x1 = ((int64_t)c + 1) * sh.total / sh.sets;
+                const int tiles = (int)((x1 < s0 + T ? x1 : s0 + T) - (x0 > s0 ? x0 : s0));
+                const float* r = sh.part + shared_row(sh, g, h, pass, c, query - pass * SHARED_QUERIES * sh.side) * 2 * REC;
+                add(r);
+                if (tiles > 1) add(r + REC);
+            }
         }
         if (den == 0.0f) den = 1.0f;
         __half2* p = reinterpret_cast<__half2*>(a.out + ((size_t)b * a.nh + (size_t)h * gq + qh) * HD + d);
@@ -647,13 +670,13 @@ cudaError_t launch_paged(const PagedArgs& a, int hd, bool q8, bool pdl, cudaStre
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_paged_merge(const PagedArgs& a, int hd, bool pdl, cudaStream_t s) {
+cudaError_t launch_paged_merge(const PagedArgs& a, const SharedArgs& sh, int hd, bool pdl, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     paged_config(cfg, attr, pdl, s);
     cfg.gridDim = dim3(a.nkv, a.B);
     cfg.blockDim = dim3(PAGED_MERGE_THREADS);
-    return hd == 64 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64>, a) : cudaLaunchKernelEx(&cfg, paged_merge_kernel<128>, a);
+    return hd == 64 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64>, a, sh) : cudaLaunchKernelEx(&cfg, paged_merge_kernel<128>, a, sh);
 }
 
 }  // namespace kd

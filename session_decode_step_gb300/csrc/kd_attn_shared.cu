@@ -1,0 +1,477 @@
+// kd_attn_shared.cu -- attention of a group of sessions over the prefix that they share, on
+// the fifth-generation tensor cores: every key and value is read once for up to 128
+// queries (the sessions' heads of one KV head, 128 of them a tile).
+//
+// S = Q K^T and O += P V with tcgen05.mma, the queries as the 128 rows, keys 128 at a
+// time: K and V come by TMA (boxes of a page's rows, 128-byte swizzle, five buffers), one
+// thread issues the products, and two groups of four warps take turns at the tiles' softmax, each
+// with scores, weights and sums of its own in tensor memory, so that one's products run
+// under the other's exponentials.  A thread holds a query's row: its maximum and sum need
+// no exchange.  The sums are rescaled only when the maximum has grown by 2^8 or more (the
+// weights, at most 2^8 then, lose nothing: they are pairs of fp16).
+//
+// Queries and weights are fp16 pairs hi + lo, as in the kernel of the sessions' own
+// keys, two products each: 4 x 2 x 128^3 flops a tile of 128 keys and 128 queries, 1.1 us
+// at the SM's share of the bf16 rate, while its 64 KB take 1.4 us of the SM's share of the memory's.
+//
+// CTAs share the tiles of all (group, KV head)s equally (kd_shared.h); what one finds of a
+// (group, head) goes to a record that the merge reads.  Groups of more than 128 queries are taken by
+// CTAs side by side, one tile of queries each, that read the same keys at the same time.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "kd_attn_common.cuh"
+#include "kd_host.h"
+#include "kd_paged.h"
+
+namespace kd {
+
+// ---- tcgen05 ---------------------------------------------------------------
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// D (tensor memory) += or = A B: A by descriptor in shared memory, or in tensor memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((int)add)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((int)add)
+        : "memory");
+}
+// 32 columns of the warp's 32 rows, a row per lane.
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+        "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 2^x to 2^-22, 0 below fp32's normal range.
+__device__ __forceinline__ float tc_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A shared-memory operand in 128-byte swizzled rows, 8 of them 1024 bytes: sbo from 8 rows
+// to the next 8, lbo (operands whose rows run along K) from 64 columns to the next 64.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo) {
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// fp16 operands, fp32 sums, M = 128; b_cols: B's rows run along K (its columns are contiguous).
+__device__ __forceinline__ constexpr uint32_t tc_idesc(int n, bool b_cols) {
+    return 1u << 4 | (b_cols ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// ---- the kernel ---------------------------------------------------------------
+constexpr int SH_SOFT = 8;                      // softmax warps, two groups of four
+constexpr int SH_THREADS = (SH_SOFT + 2) * 32;  // and the copies' and the products' warps
+
+template <int HD>
+struct SharedSmem {
+    static constexpr int COLS = HD / 64;               // 128-byte columns of a row
+    static constexpr int COL = SHARED_TILE * 128;      // one of a tile
+    static constexpr int TILE = COLS * COL;            // K or V of a tile, or a part of the queries
+    static constexpr int SLOTS = HD == 128 ? 5 : 8;
+    static constexpr int Q = 0, RING = 2 * TILE, BARS = RING + SLOTS * TILE;
+    static constexpr int TOTAL = BARS + 256 + 1024;
+    static_assert(TOTAL <= 227 * 1024, "opt-in shared memory");
+};
+
+// A CTA's next tiles of one (group, KV head, pass).
+struct SharedSeg {
+    int g, h, pass, tile, n;  // tiles [tile, tile + n)
+    __device__ __forceinline__ void at(const SharedArgs& a, int64_t x, int left) {
+        int lo = 0, hi = a.n_groups;
+        const int64_t y = x / a.nkv;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.first[mid] <= y) lo = mid;
+            else hi = mid;
+        }
+        g = lo;
+        const int r = (int)(x - (int64_t)a.first[g] * a.nkv), T = a.tiles(g), u = r / T;
+        tile = r - u * T;
+        h = u / a.passes(g);
+        pass = u - h * a.passes(g);
+        n = min(T - tile, left);
+    }
+};
+
+template <int HD>
+__global__ void __launch_bounds__(SH_THREADS, 1)
+    shared_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+    using L = SharedSmem<HD>;
+    constexpr int NS = L::SLOTS;
+    extern __shared__ uint8_t shared_raw[];
+    uint8_t* smem = align1024(shared_raw);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BARS);
+    uint64_t *empty = full + NS, *s_full = empty + NS, *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *q_free = q_full + 1;
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(q_free + 1);
+    volatile int* failed = reinterpret_cast<volatile int*>(tmem_at + 1);
+    // The last tiles' 16-key runs that have a page, by tile: an entry is written again after 8 tiles, when the
+    // buffers (at most 8, two a tile) have gone round past its tile's values, so past its softmax.
+    volatile uint8_t* runs = reinterpret_cast<volatile uint8_t*>(tmem_at + 2);
+    static_assert(NS <= 8, "tiles in the buffers");
+
+    if (warp == SH_SOFT) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_at)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 128);
+            mbar_init(pv_done + i, 1);
+        }
+        mbar_init(q_full, 256);
+        mbar_init(q_free, 256);
+        mbar_init_fence();
+        *failed = 0;
+        prefetch_tmap(&tmk);
+        prefetch_tmap(&tmv);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_at;
+    pdl_wait();
+    pdl_launch_dependents();  // after the wait: the kernel behind this one relies on it, and reads at once
+
+    const int set = blockIdx.x / a.side, mine = blockIdx.x - set * a.side;  // of the CTAs side by side
+    const int64_t x0 = (int64_t)set * a.total / a.sets, x1 = ((int64_t)set + 1) * a.total / a.sets;
+    const int box = a.box_runs;  // 16-key runs of a copy's box
+    // The first of the CTA's queries in a segment's group, and how many (<= 0: none).
+    auto first_query = [&](const SharedSeg& s) { return (s.pass * a.side + mine) * SHARED_QUERIES; };
+    auto n_queries = [&](const SharedSeg& s) { return min(SHARED_QUERIES, a.queries[s.g] - first_query(s)); };
+
+    if (warp == SH_SOFT) {
+        // ---- copies: K and V of each tile, boxes of whole 16-key runs within a page
+        uint32_t slot = 0, phase = 0, tiles = 0;
+        bool ok = true;
+        for (int64_t x = x0; x < x1 && ok;) {
+            SharedSeg s;
+            s.at(a, x, (int)(x1 - x));
+            x += s.n;
+            if (n_queries(s) <= 0) continue;
+            const int keys = a.keys[s.g];
+            const int* row = a.table + (int64_t)a.lead[s.g] * a.table_ld;
+            auto look_up = [&](int t) {  // lane i: the page of the tile's run i
+                const int key = t * SHARED_TILE + 16 * lane;
+                return lane < SHARED_TILE / 16 && key < keys ? row[key / a.ps] : -1;
+            };
+            int page = look_up(s.tile);
+            for (int t = s.tile; t < s.tile + s.n && ok; ++t, ++tiles) {
+                const int key = t * SHARED_TILE + 16 * lane;
+                const int here = min(SHARED_TILE, keys - t * SHARED_TILE) / 16;  // runs
+                const bool good = lane < here && (unsigned)page < (unsigned)a.n_pages;
+                if (lane < here && !good && a.fault) *a.fault = 1;
+                const unsigned mask = __ballot_sync(FULL_MASK, good) & 0xffu;
+                // a page that does not exist: rows behind the last one, which read as zeros
+                const int y = good ? (page * a.nkv + s.h) * a.ps + key % a.ps : a.rows;
+                if (t + 1 < s.tile + s.n) page = look_up(t + 1);
+                for (int part = 0; part < 2 && ok; ++part) {
+                    if (lane == 0) ok = mbar_wait_bounded(empty + slot, phase ^ 1);
+                    ok = __shfl_sync(FULL_MASK, ok, 0);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (!part) runs[tiles & 7] = (uint8_t)mask;
+                        mbar_arrive_expect_tx(full + slot, (uint32_t)(here * 16 * HD * 2));
+                    }
+                    __syncwarp();
+                    if (lane < here && lane % box == 0) {
+                        uint8_t* dst = smem + L::RING + slot * L::TILE + lane * 16 * 128;
+#pragma unroll
+                        for (int c = 0; c < L::COLS; ++c) tma_load_2d(dst + c * L::COL, part ? &tmv : &tmk, 64 * c, y, full + slot);
+                    }
+                    __syncwarp();
+                    if (++slot == NS) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) *failed = 1;
+    } else if (warp == SH_SOFT + 1) {
+        // ---- products
+        if (lane == 0) {
+            uint32_t slot = 0, phase = 0, q_phase = 0;
+            uint32_t kslot[2], vslot[2], vphase[2];
+            unsigned pvs[2] = {0, 0}, ps[2] = {0, 0};  // products P V issued, weights awaited
+            bool ok = true;
+            const uint32_t qs = smem_u32(smem + L::Q), ring = smem_u32(smem + L::RING);
+            for (int64_t x = x0; x < x1 && ok;) {
+                SharedSeg s;
+                s.at(a, x, (int)(x1 - x));
+                x += s.n;
+                if (n_queries(s) <= 0) continue;
+                const int keys = a.keys[s.g];
+                ok = mbar_wait_bounded(q_full, q_phase);
+                q_phase ^= 1;
+                if (!ok) break;
+                tc_fence_after();
+                auto scores = [&](int j) {  // S of tile j of the segment
+                    const int w = j & 1, n = min(SHARED_TILE, keys - (s.tile + j) * SHARED_TILE);
+                    if (!mbar_wait_bounded(full + slot, phase)) return false;
+                    kslot[w] = slot;
+                    if (++slot == NS) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                    vslot[w] = slot;
+                    vphase[w] = phase;
+                    if (++slot == NS) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                    tc_fence_after();
+                    const uint32_t id = tc_idesc(n, false), kb = ring + kslot[w] * L::TILE;
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int k = 0; k < HD / 16; ++k) {
+                            const uint32_t off = (k / 4) * L::COL + (k % 4) * 32;
+                            tc_mma_ss(tmem + w * 128, tc_desc(qs + part * L::TILE + off, 0), tc_desc(kb + off, 0), id, part || k);
+                        }
+                    tc_commit(s_full + w);
+                    tc_commit(empty + kslot[w]);
+                    return true;
+                };
+                ok = scores(0) && (s.n < 2 || scores(1));
+                for (int j = 0; j < s.n && ok; ++j) {
+                    const int w = j & 1, n = min(SHARED_TILE, keys - (s.tile + j) * SHARED_TILE);
+                    ok = mbar_wait_bounded(p_full + w, ps[w]++ & 1) && mbar_wait_bounded(full + vslot[w], vphase[w]);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t id = tc_idesc(HD, true), vb = ring + vslot[w] * L::TILE;
+                    for (int k = 0; k < n / 16; ++k)
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+                            tc_mma_ts(tmem + 256 + w * HD, tmem + w * 128 + 32 * (k / 2) + 16 * part + 8 * (k & 1),
+                                      tc_desc(vb + k * 2048, L::COL), id, part || k || j >= 2);
+                    tc_commit(empty + vslot[w]);
+                    tc_commit(pv_done + w);
+                    // The next scores take the place of these weights, so not before the product is done.
+                    if (j + 2 < s.n) ok = mbar_wait_bounded(pv_done + w, pvs[w] & 1) && scores(j + 2);
+                    ++pvs[w];
+                }
+            }
+            if (!ok) *failed = 1;
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax: thread r of a group has query r
+        const int w = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
+        const uint32_t st = lane_base + w * 128, ot = lane_base + 256 + w * HD;
+        unsigned ss = 0, pv = 0;  // scores and products seen
+        uint32_t tiles = 0, segs = 0;
+        bool ok = true;
+        const float c = a.scale * 1.4426950408889634f;
+        for (int64_t x = x0; x < x1 && ok;) {
+            SharedSeg s;
+            s.at(a, x, (int)(x1 - x));
+            x += s.n;
+            const int nq = n_queries(s), q0 = first_query(s);
+            if (nq <= 0) continue;
+            const int keys = a.keys[s.g];
+            {   // the queries: thread t takes half of row t & 127
+                const int half = threadIdx.x >> 7, qi = q0 + r;
+                const float* src = a.q + ((size_t)(a.lead[s.g] + qi / a.gq) * a.nh + (size_t)s.h * a.gq + qi % a.gq) * HD + half * (HD / 2);
+#pragma unroll 4
+                for (int i = 0; i < HD / 16; ++i) {
+                    float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
+                    if (r < nq) {
+                        u = *reinterpret_cast<const float4*>(src + 8 * i);
+                        v = *reinterpret_cast<const float4*>(src + 8 * i + 4);
+                    }
+                    const int chunk = half * (HD / 16) + i;  // 8 dims
+                    uint8_t* dst = smem + L::Q + (chunk >> 3) * L::COL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(f2_hi(u.x, u.y), f2_hi(u.z, u.w), f2_hi(v.x, v.y), f2_hi(v.z, v.w));
+                    *reinterpret_cast<uint4*>(dst + L::TILE) = make_uint4(f2_lo(u.x, u.y), f2_lo(u.z, u.w), f2_lo(v.x, v.y), f2_lo(v.z, v.w));
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(q_full);
+            }
+            const bool idle = (warp & 3) * 32 >= nq;  // no query in the warp's rows: what its weights hold does not matter
+            float m = -INFINITY, l = 0.0f;            // the maximum that the weights are taken against, in units of 1 / c
+            for (int j = w; j < s.n && ok; j += 2) {
+                const int n = min(SHARED_TILE, keys - (s.tile + j) * SHARED_TILE);
+                ok = mbar_wait_bounded(s_full + w, ss++ & 1);
+                if (__any_sync(FULL_MASK, !ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const unsigned have = runs[(tiles + j) & 7];
+                if (!idle) {
+                    auto seen = [&](int i) { return i < n && ((have >> (i >> 4)) & 1); };  // key i of the tile
+                    const bool all = n == SHARED_TILE && have == 0xffu;
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (32 * k < n) {
+                            uint32_t v[32];
+                            tc_ld32(st + 32 * k, v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (all || seen(32 * k + i)) mx = fmaxf(mx, __uint_as_float(v[i]));
+                        }
+                    }
+                    float f = 1.0f;
+                    if (m == -INFINITY) {
+                        m = mx;
+                        f = 0.0f;
+                    } else if ((mx - m) * c > 8.0f) {
+                        f = exp2f((m - mx) * c);
+                        m = mx;
+                    }
+                    if (j >= 2 && __any_sync(FULL_MASK, f != 1.0f)) {
+                        l *= f;
+#pragma unroll 1
+                        for (int k = 0; k < HD / 32; ++k) {
+                            uint32_t v[32];
+                            tc_ld32(ot + 32 * k, v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                            tc_st32(ot + 32 * k, v);
+                        }
+                        tc_wait_st();
+                    }
+                    const float mc = m == -INFINITY ? 0.0f : m * c;
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        if (32 * k < n) {
+                            uint32_t v[32], p[32];
+                            tc_ld32(st + 32 * k, v);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                float e0 = tc_exp2(__fmaf_rn(__uint_as_float(v[i]), c, -mc));
+                                float e1 = tc_exp2(__fmaf_rn(__uint_as_float(v[i + 1]), c, -mc));
+                                if (!all) {
+                                    if (!seen(32 * k + i)) e0 = 0.0f;
+                                    if (!seen(32 * k + i + 1)) e1 = 0.0f;
+                                }
+                                l += e0 + e1;
+                                p[i / 2] = f2_hi(e0, e1);
+                                p[16 + i / 2] = f2_lo(e0, e1);
+                            }
+                            tc_st32(st + 32 * k, p);  // the weights in the scores' place: 16 columns hi, 16 lo
+                        }
+                    }
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(p_full + w);
+            }
+            tiles += s.n;
+            // ---- the record of the group's tiles
+            if (ok && s.n > w) {
+                const int last = (s.n - w + 1) / 2;  // products of this group in the segment
+                pv += last;
+                ok = mbar_wait_bounded(pv_done + w, (pv - 1) & 1);
+                if (__any_sync(FULL_MASK, !ok)) ok = false;
+                tc_fence_after();
+                if (ok && !idle) {
+                    float* rec = a.part + (shared_row(a, s.g, s.h, s.pass, set, q0 - s.pass * a.side * SHARED_QUERIES + r) * 2 + w) * PAGED_REC(HD);
+#pragma unroll 1
+                    for (int k = 0; k < HD / 32; ++k) {
+                        uint32_t v[32];
+                        tc_ld32(ot + 32 * k, v);
+                        if (r < nq) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                *reinterpret_cast<uint4*>(rec + 32 * k + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        }
+                    }
+                    if (r < nq) *reinterpret_cast<float2*>(rec + HD) = make_float2(m * a.scale, l);
+                }
+                tc_fence_before();
+            }
+            // Both groups are done with the queries and with tensor memory.
+            mbar_arrive(q_free);
+            ok = ok && mbar_wait_bounded(q_free, segs++ & 1);
+            ok = __all_sync(FULL_MASK, ok);
+        }
+        if (!ok) *failed = 1;
+    }
+    __syncthreads();
+    if (warp == SH_SOFT) {
+        if (*failed) {  // copies may be in flight: give them their time before the memory is given up
+            if (lane < NS)
+                for (int i = 0; i < 2; ++i) (void)mbar_wait_bounded(full + lane, i);
+            __syncwarp();
+        }
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        if (lane == 0) a.status[blockIdx.x] = *failed;
+    }
+}
+
+// ---- launch ----------------------------------------------------------------------
+cudaError_t encode_fp16_2d(CUtensorMap* out, const void* base, long inner, long rows, int box_inner, int box_rows);
+
+template <int HD>
+static cudaError_t launch_shared_hd(const SharedArgs& a, const __half* k, const __half* v, int dev, cudaStream_t s) {
+    static OncePerDevice once;
+    cudaError_t e = once(dev, [] {
+        return cudaFuncSetAttribute(shared_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, SharedSmem<HD>::TOTAL);
+    });
+    if (e != cudaSuccess) return e;
+    CUtensorMap mk, mv;
+    if ((e = encode_fp16_2d(&mk, k, HD, a.rows, 64, a.box_runs * 16)) != cudaSuccess) return e;
+    if ((e = encode_fp16_2d(&mv, v, HD, a.rows, 64, a.box_runs * 16)) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(a.sets * a.side);
+    cfg.blockDim = dim3(SH_THREADS);
+    cfg.dynamicSmemBytes = SharedSmem<HD>::TOTAL;
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, shared_kernel<HD>, a, mk, mv);
+}
+
+cudaError_t launch_shared(const SharedArgs& a, int hd, const __half* k, const __half* v, int dev, cudaStream_t s) {
+    return hd == 64 ? launch_shared_hd<64>(a, k, v, dev, s) : launch_shared_hd<128>(a, k, v, dev, s);
+}
+
+}  // namespace kd

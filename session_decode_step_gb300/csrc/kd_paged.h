@@ -36,16 +36,50 @@ struct PagedArgs {
     int from[KD_PAGED_MAX_SEQS], to[KD_PAGED_MAX_SEQS], lead_keys[KD_PAGED_MAX_SEQS];
     int first[KD_PAGED_MAX_SEQS + 1];  // first block of the session's first head, in blocks / nkv
     uint8_t lead[KD_PAGED_MAX_SEQS];
+    uint8_t group[KD_PAGED_MAX_SEQS];  // the session's group in SharedArgs, or SHARED_NONE
 };
+constexpr int SHARED_NONE = 255;
 static_assert(KD_PAGED_MAX_SEQS <= 256, "sessions in a byte");
 
 __host__ __device__ inline int paged_blocks(int keys) { return (keys + PAGED_BLOCK - 1) / PAGED_BLOCK; }
 // The CTA that takes block x.
 __host__ __device__ inline int paged_cta(int64_t x, int64_t blocks, int ctas) { return (int)(((x + 1) * ctas - 1) / blocks); }
 
+// Groups whose shared keys are read once for all their queries (kd_attn_shared.cu).  A pass of a
+// (group, KV head) is its keys, in tiles of SHARED_TILE, for up to `side` tiles of
+// SHARED_QUERIES queries, one for each of the CTAs side by side; the tiles of all passes are one
+// sequence, of which set i of the `sets` of CTAs takes [i total / sets, (i + 1) total / sets).
+// A set's CTAs leave two records (one for each half of their warps) of each query that has tiles there.
+constexpr int SHARED_TILE = 128, SHARED_QUERIES = 128, SHARED_MAX_SIDE = 8;
+constexpr int SHARED_MAX_GROUPS = KD_PAGED_MAX_SEQS / 2;  // of two sessions at least
+constexpr int SHARED_MAX_CTAS = 256;
+struct SharedArgs {
+    const float* q;
+    const int* table;
+    float* part;
+    int* fault;
+    int* status;  // [CTA]: 1 where a bounded wait ran out
+    int table_ld, n_pages, ps, rows, box_runs, nh, nkv, gq, n_groups, side, sets;
+    float scale;
+    int64_t total;
+    int keys[SHARED_MAX_GROUPS], queries[SHARED_MAX_GROUPS];  // shared keys (whole pages), sessions times gq
+    int before[SHARED_MAX_GROUPS];                            // queries of the groups before it
+    int first[SHARED_MAX_GROUPS + 1];                         // first tile of its first head's first pass, in tiles / nkv
+    uint8_t lead[SHARED_MAX_GROUPS];                          // first session
+    __host__ __device__ int tiles(int g) const { return (keys[g] + SHARED_TILE - 1) / SHARED_TILE; }
+    __host__ __device__ int passes(int g) const { return (queries[g] + SHARED_QUERIES * side - 1) / (SHARED_QUERIES * side); }
+};
+// The record pair of query `query` of a pass that set `set` leaves: pairs of different (pass, set)s do not
+// overlap, as each step along the sequence moves on by a pass's queries, or by a set's most.
+__host__ __device__ inline int64_t shared_row(const SharedArgs& a, int g, int h, int pass, int set, int query) {
+    const int pass_queries = SHARED_QUERIES * a.side;
+    return (int64_t)a.before[g] * a.nkv + (int64_t)h * a.queries[g] + (int64_t)pass * pass_queries + (int64_t)set * pass_queries + query;
+}
+cudaError_t launch_shared(const SharedArgs& a, int hd, const __half* k, const __half* v, int dev, cudaStream_t s);
+
 // CTAs of the kernel that device dev, the current one, holds at once (0 on a CUDA error, left in *e).
 int paged_slots(int hd, int group, bool q8, int dev, int num_sms, cudaError_t* e);
 cudaError_t launch_paged(const PagedArgs& a, int hd, bool q8, bool pdl, cudaStream_t s);
-cudaError_t launch_paged_merge(const PagedArgs& a, int hd, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedArgs& a, const SharedArgs& sh, int hd, bool pdl, cudaStream_t s);
 
 }  // namespace kd

@@ -14,7 +14,48 @@ static bool paged_shape(int32_t nh, int32_t nkv, int32_t hd, bool q8) {
     return (g == 1 || g == 2 || g == 4 || g == 8) && (hd == 128 || (hd == 64 && !q8));
 }
 constexpr int PAGED_MAX_KV_HEADS = 1024;
-constexpr int PAGED_HEAD_BYTES = 256;  // the workspace's words before its records
+constexpr int PAGED_HEAD_BYTES = 256 + SHARED_MAX_CTAS * 4;  // the workspace's words before its records: the call's, a CTA's status
+// Records of the sessions' own keys: one per CTA and (session, head) at most.
+static size_t paged_records(int B, int nkv) { return (size_t)PAGED_MAX_CTAS + (size_t)B * nkv; }
+
+// A group's shared keys go to the kernel that reads them once where that saves its other sessions
+// this many bytes of reading.
+constexpr int64_t SHARED_SAVES = 8 << 20;
+
+// Choose the sets of CTAs: `side` of them take a (group, head)'s tiles of queries side by side.
+// The time goes as the tiles of all passes over the sets; of equal ones the widest, which read each key
+// most often at the same time.
+static void shared_plan(SharedArgs& t, int sms) {
+    if (sms > SHARED_MAX_CTAS) sms = SHARED_MAX_CTAS;
+    double best = 0;
+    int most = 1;
+    for (int g = 0; g < t.n_groups; ++g)
+        if ((t.queries[g] + SHARED_QUERIES - 1) / SHARED_QUERIES > most) most = (t.queries[g] + SHARED_QUERIES - 1) / SHARED_QUERIES;
+    for (int side = 1; side <= most && side <= SHARED_MAX_SIDE && side <= sms; ++side) {
+        double work = 0;
+        for (int g = 0; g < t.n_groups; ++g) {
+            const int per = SHARED_QUERIES * side;
+            work += (double)t.tiles(g) * ((t.queries[g] + per - 1) / per);
+        }
+        const double time = work / (sms / side);
+        if (side == 1 || time <= best * 1.02) {
+            best = time < best || side == 1 ? time : best;
+            t.side = side;
+        }
+    }
+    int64_t first = 0;
+    int before = 0;
+    for (int g = 0; g < t.n_groups; ++g) {
+        t.first[g] = (int)first;
+        t.before[g] = before;
+        first += (int64_t)t.tiles(g) * t.passes(g);
+        before += t.queries[g];
+    }
+    t.first[t.n_groups] = (int)first;
+    t.total = first * t.nkv;
+    t.sets = sms / t.side;
+    if (t.sets > t.total) t.sets = (int)t.total;
+}
 
 static kd_status paged_call(const char* fn, bool q8, const float* q, const void* kp, const void* vp, const uint16_t* ks,
                             const uint16_t* vs, const int32_t* table, int32_t table_ld, const int32_t* lens, int32_t B,
@@ -37,23 +78,37 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
     if ((((uintptr_t)table | (uintptr_t)fault) & 3) || ((uintptr_t)out & 1))
         return failf(KD_ERR_INVALID_ARG, "%s: table and fault must be 4-byte aligned, out 2-byte", fn);
     PagedArgs a = {};
+    SharedArgs sh = {};
     int64_t total = 0;
     for (int b = 0; b < B; ++b) {
         if (lens[b] < 0 || lens[b] > (int64_t)table_ld * ps)
             return failf(KD_ERR_POSITION, "%s: length %d in tables of %d pages of %d", fn, lens[b], table_ld, ps);
         a.to[b] = lens[b];
         a.lead[b] = (uint8_t)b;
+        a.group[b] = SHARED_NONE;
     }
     if (n_groups) {
         int b = 0;
         for (int g = 0; g < n_groups; ++g) {
             if (group_rows[g] < 1 || group_rows[g] > B - b)
                 return failf(KD_ERR_INVALID_ARG, "%s: group %d of %d sessions", fn, g, group_rows[g]);
+            const int shared = group_prefix[g] / ps * ps;  // the page that the prefix ends in is each session's own
+            const bool once = !q8 && group_rows[g] > 1 && shared > 0 &&
+                              (int64_t)(group_rows[g] - 1) * shared * nkv * hd * 4 >= SHARED_SAVES;
             for (int i = b; i < b + group_rows[g]; ++i) {
                 if (group_prefix[g] < 0 || group_prefix[g] > lens[i])
                     return failf(KD_ERR_POSITION, "%s: prefix %d of a session of length %d", fn, group_prefix[g], lens[i]);
                 a.lead[i] = (uint8_t)b;
-                a.lead_keys[i] = group_prefix[g] / ps * ps;  // the page that the prefix ends in is each session's own
+                a.lead_keys[i] = shared;
+                if (once) {
+                    a.from[i] = shared;
+                    a.group[i] = (uint8_t)sh.n_groups;
+                }
+            }
+            if (once) {
+                sh.lead[sh.n_groups] = (uint8_t)b;
+                sh.keys[sh.n_groups] = shared;
+                sh.queries[sh.n_groups++] = group_rows[g] * (nh / nkv);
             }
             b += group_rows[g];
         }
@@ -90,7 +145,7 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
     a.scale = 1.0f / std::sqrt((float)hd);
     a.blocks = total * nkv;
     a.ctas = a.blocks < 1 ? 1 : a.blocks < slots ? (int)a.blocks : slots;
-    bool merge = false;
+    bool merge = sh.n_groups > 0;
     for (int b = 0; b < B && !merge; ++b) {
         const int nb = a.first[b + 1] - a.first[b];
         for (int h = 0; h < nkv && nb && !merge; ++h) {
@@ -99,8 +154,27 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
         }
     }
     cudaStream_t s = (cudaStream_t)stream;
+    if (sh.n_groups) {
+        sh.q = q;
+        sh.table = table;
+        sh.part = a.part + paged_records(B, nkv) * (nh / nkv) * PAGED_REC(hd);
+        sh.fault = fault;
+        sh.status = (int*)ws + 64;
+        sh.table_ld = table_ld;
+        sh.n_pages = n_pages;
+        sh.ps = ps;
+        sh.rows = n_pages * nkv * ps;
+        sh.box_runs = (ps & -ps) >= SHARED_TILE ? SHARED_TILE / 16 : (ps & -ps) / 16;
+        sh.nh = nh;
+        sh.nkv = nkv;
+        sh.gq = nh / nkv;
+        sh.scale = a.scale;
+        shared_plan(sh, sms);
+        a.late_wait = 1;
+        KD_TRY(launch_shared(sh, hd, (const __half*)kp, (const __half*)vp, dev, s));
+    }
     KD_TRY(launch_paged(a, hd, q8, true, s));
-    if (merge) KD_TRY(launch_paged_merge(a, hd, true, s));
+    if (merge) KD_TRY(launch_paged_merge(a, sh, hd, true, s));
     return KD_OK;
 }
 
@@ -111,9 +185,9 @@ extern "C" {
 size_t kd_attn_paged_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
     using namespace kd;
     if (B < 1 || B > KD_PAGED_MAX_SEQS || !paged_shape(n_heads, n_kv_heads, head_dim, false) || n_kv_heads > PAGED_MAX_KV_HEADS) return 0;
-    // a record per CTA and (session, head) at most
-    const size_t records = (size_t)PAGED_MAX_CTAS + (size_t)B * n_kv_heads;
-    return PAGED_HEAD_BYTES + records * (n_heads / n_kv_heads) * PAGED_REC(head_dim) * sizeof(float);
+    // of shared keys: two records for every query, and for as many as a CTA takes per CTA
+    const size_t shared = 2 * ((size_t)B * n_heads + (size_t)SHARED_MAX_CTAS * SHARED_QUERIES);
+    return PAGED_HEAD_BYTES + (paged_records(B, n_kv_heads) * (n_heads / n_kv_heads) + shared) * PAGED_REC(head_dim) * sizeof(float);
 }
 
 kd_status kd_attn_paged_decode(const float* q, const uint16_t* k_pages, const uint16_t* v_pages, const int32_t* table,
