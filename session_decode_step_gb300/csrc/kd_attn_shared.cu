@@ -4,10 +4,10 @@
 //
 // S = Q K^T and O += P V with tcgen05.mma, the queries as the 128 rows, keys 128 at a
 // time: K and V come by TMA (boxes of a page's rows, 128-byte swizzle, five buffers), one
-// thread issues the products, and two groups of four warps take turns at the tiles' softmax, each
+// thread issues the products, and two groups of eight warps take turns at the tiles' softmax, each
 // with scores, weights and sums of its own in tensor memory, so that one's products run
-// under the other's exponentials.  A thread holds a query's row: its maximum and sum need
-// no exchange.  The sums are rescaled only when the maximum has grown by 2^8 or more (the
+// under the other's exponentials.  Two threads hold a query's row, half of the tile's keys each,
+// and tell each other their maxima.  The sums are rescaled only when the maximum has grown by 2^8 or more (the
 // weights, at most 2^8 then, lose nothing: they are pairs of fp16).
 //
 // Queries and weights are fp16 pairs hi + lo, as in the kernel of the sessions' own
@@ -58,7 +58,12 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&v)[32]) {
           "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
           "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(addr));
+}
+// The loads before have arrived; v is theirs, so that no use of it is moved up.
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
 }
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) {
     asm volatile(
@@ -71,6 +76,23 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) 
         : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 operations in one.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 
 // 2^x to 2^-22, 0 below fp32's normal range.
 __device__ __forceinline__ float tc_exp2(float x) {
@@ -94,7 +116,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 
 // ---- the kernel ---------------------------------------------------------------
-constexpr int SH_SOFT = 8;                      // softmax warps, two groups of four
+constexpr int SH_SOFT = 16;                     // softmax warps: two groups of eight, two warps a quarter of the rows
 constexpr int SH_THREADS = (SH_SOFT + 2) * 32;  // and the copies' and the products' warps
 
 template <int HD>
@@ -104,7 +126,8 @@ struct SharedSmem {
     static constexpr int TILE = COLS * COL;            // K or V of a tile, or a part of the queries
     static constexpr int SLOTS = HD == 128 ? 5 : 8;
     static constexpr int Q = 0, RING = 2 * TILE, BARS = RING + SLOTS * TILE;
-    static constexpr int TOTAL = BARS + 256 + 1024;
+    static constexpr int MAXIMA = BARS + 320;  // [group][half][row]: what the two warps of a row tell each other
+    static constexpr int TOTAL = MAXIMA + 2 * 2 * SHARED_QUERIES * 4;
     static_assert(TOTAL <= 227 * 1024, "opt-in shared memory");
 };
 
@@ -133,18 +156,22 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     shared_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     using L = SharedSmem<HD>;
     constexpr int NS = L::SLOTS;
-    extern __shared__ uint8_t shared_raw[];
-    uint8_t* smem = align1024(shared_raw);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BARS);
-    uint64_t *empty = full + NS, *s_full = empty + NS, *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *q_free = q_full + 1;
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(q_free + 1);
+    uint64_t *empty = full + NS, *s_full = empty + NS, *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *q_free = q_full + 1, *pair = q_free + 1;
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(pair + SH_SOFT / 2);
     volatile int* failed = reinterpret_cast<volatile int*>(tmem_at + 1);
     // The last tiles' 16-key runs that have a page, by tile: an entry is written again after 8 tiles, when the
     // buffers (at most 8, two a tile) have gone round past its tile's values, so past its softmax.
     volatile uint8_t* runs = reinterpret_cast<volatile uint8_t*>(tmem_at + 2);
     static_assert(NS <= 8, "tiles in the buffers");
 
+    if (smem_u32(smem) & 1023) {  // the swizzle counts on it, and there is no room to move up
+        pdl_wait();
+        if (threadIdx.x == 0) a.status[blockIdx.x] = 1;
+        return;
+    }
     if (warp == SH_SOFT) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_at)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -156,11 +183,12 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, 128);
+            mbar_init(p_full + i, SH_SOFT / 2);
             mbar_init(pv_done + i, 1);
         }
-        mbar_init(q_full, 256);
-        mbar_init(q_free, 256);
+        mbar_init(q_full, SH_SOFT);
+        mbar_init(q_free, SH_SOFT);
+        for (int i = 0; i < SH_SOFT / 2; ++i) mbar_init(pair + i, 2);
         mbar_init_fence();
         *failed = 0;
         prefetch_tmap(&tmk);
@@ -231,9 +259,15 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     } else if (warp == SH_SOFT + 1) {
         // ---- products
         if (lane == 0) {
-            uint32_t slot = 0, phase = 0, q_phase = 0;
-            uint32_t kslot[2], vslot[2], vphase[2];
-            unsigned pvs[2] = {0, 0}, ps[2] = {0, 0};  // products P V issued, weights awaited
+            uint32_t kslot = 0, kphase = 0, vslot = 1, vphase = 0, q_phase = 0;  // K and V parts lie in turn
+            unsigned pv_phase = 0, p_phase = 0;  // a bit for each half of the softmax warps
+            auto step = [](uint32_t& slot, uint32_t& phase) {
+                slot += 2;
+                if (slot >= NS) {
+                    slot -= NS;
+                    phase ^= 1;
+                }
+            };
             bool ok = true;
             const uint32_t qs = smem_u32(smem + L::Q), ring = smem_u32(smem + L::RING);
             for (int64_t x = x0; x < x1 && ok;) {
@@ -248,20 +282,9 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 tc_fence_after();
                 auto scores = [&](int j) {  // S of tile j of the segment
                     const int w = j & 1, n = min(SHARED_TILE, keys - (s.tile + j) * SHARED_TILE);
-                    if (!mbar_wait_bounded(full + slot, phase)) return false;
-                    kslot[w] = slot;
-                    if (++slot == NS) {
-                        slot = 0;
-                        phase ^= 1;
-                    }
-                    vslot[w] = slot;
-                    vphase[w] = phase;
-                    if (++slot == NS) {
-                        slot = 0;
-                        phase ^= 1;
-                    }
+                    if (!mbar_wait_bounded(full + kslot, kphase)) return false;
                     tc_fence_after();
-                    const uint32_t id = tc_idesc(n, false), kb = ring + kslot[w] * L::TILE;
+                    const uint32_t id = tc_idesc(n, false), kb = ring + kslot * L::TILE;
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -270,40 +293,53 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                             tc_mma_ss(tmem + w * 128, tc_desc(qs + part * L::TILE + off, 0), tc_desc(kb + off, 0), id, part || k);
                         }
                     tc_commit(s_full + w);
-                    tc_commit(empty + kslot[w]);
+                    tc_commit(empty + kslot);
+                    step(kslot, kphase);
                     return true;
                 };
                 ok = scores(0) && (s.n < 2 || scores(1));
                 for (int j = 0; j < s.n && ok; ++j) {
                     const int w = j & 1, n = min(SHARED_TILE, keys - (s.tile + j) * SHARED_TILE);
-                    ok = mbar_wait_bounded(p_full + w, ps[w]++ & 1) && mbar_wait_bounded(full + vslot[w], vphase[w]);
+                    ok = mbar_wait_bounded(p_full + w, (p_phase >> w) & 1) && mbar_wait_bounded(full + vslot, vphase);
+                    p_phase ^= 1u << w;
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t id = tc_idesc(HD, true), vb = ring + vslot[w] * L::TILE;
+                    const uint32_t id = tc_idesc(HD, true), vb = ring + vslot * L::TILE;
                     for (int k = 0; k < n / 16; ++k)
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
                             tc_mma_ts(tmem + 256 + w * HD, tmem + w * 128 + 32 * (k / 2) + 16 * part + 8 * (k & 1),
                                       tc_desc(vb + k * 2048, L::COL), id, part || k || j >= 2);
-                    tc_commit(empty + vslot[w]);
+                    tc_commit(empty + vslot);
+                    step(vslot, vphase);
                     tc_commit(pv_done + w);
                     // The next scores take the place of these weights, so not before the product is done.
-                    if (j + 2 < s.n) ok = mbar_wait_bounded(pv_done + w, pvs[w] & 1) && scores(j + 2);
-                    ++pvs[w];
+                    if (j + 2 < s.n) ok = mbar_wait_bounded(pv_done + w, (pv_phase >> w) & 1) && scores(j + 2);
+                    pv_phase ^= 1u << w;
                 }
             }
             if (!ok) *failed = 1;
         }
         __syncwarp();
     } else {
-        // ---- softmax: thread r of a group has query r
-        const int w = warp >> 2, r = threadIdx.x & 127;
+        // ---- softmax: two threads have a query's row, a half of the tile's keys (then of the head's dims) each
+        const int w = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
-        const uint32_t st = lane_base + w * 128, ot = lane_base + 256 + w * HD;
-        unsigned ss = 0, pv = 0;  // scores and products seen
+        const uint32_t st = lane_base + w * 128 + half * 64, ot = lane_base + 256 + w * HD + half * (HD / 2);
+        float* maxima = reinterpret_cast<float*>(smem + L::MAXIMA) + w * 2 * SHARED_QUERIES;
+        uint64_t* partner = pair + w * 4 + (warp & 3);
+        unsigned ss = 0, pv = 0, met = 0;  // scores and products seen, meetings with the row's other warp
         uint32_t tiles = 0, segs = 0;
         bool ok = true;
         const float c = a.scale * 1.4426950408889634f;
+        // Tell the row's other half x and hear its own; every lane of the warp returns the same in `good`.
+        auto exchange = [&](float x, bool& good) {
+            maxima[half * SHARED_QUERIES + r] = x;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(partner);
+            good = __all_sync(FULL_MASK, mbar_wait_bounded(partner, met++ & 1));
+            return maxima[(half ^ 1) * SHARED_QUERIES + r];
+        };
         for (int64_t x = x0; x < x1 && ok;) {
             SharedSeg s;
             s.at(a, x, (int)(x1 - x));
@@ -311,86 +347,95 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             const int nq = n_queries(s), q0 = first_query(s);
             if (nq <= 0) continue;
             const int keys = a.keys[s.g];
-            {   // the queries: thread t takes half of row t & 127
-                const int half = threadIdx.x >> 7, qi = q0 + r;
-                const float* src = a.q + ((size_t)(a.lead[s.g] + qi / a.gq) * a.nh + (size_t)s.h * a.gq + qi % a.gq) * HD + half * (HD / 2);
-#pragma unroll 4
-                for (int i = 0; i < HD / 16; ++i) {
+            {   // the queries: a quarter of row r's dims
+                const int part = w * 2 + half, qi = q0 + r;
+                const float* src = a.q + ((size_t)(a.lead[s.g] + qi / a.gq) * a.nh + (size_t)s.h * a.gq + qi % a.gq) * HD + part * (HD / 4);
+#pragma unroll
+                for (int i = 0; i < HD / 32; ++i) {
                     float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
                     if (r < nq) {
                         u = *reinterpret_cast<const float4*>(src + 8 * i);
                         v = *reinterpret_cast<const float4*>(src + 8 * i + 4);
                     }
-                    const int chunk = half * (HD / 16) + i;  // 8 dims
+                    const int chunk = part * (HD / 32) + i;  // 8 dims
                     uint8_t* dst = smem + L::Q + (chunk >> 3) * L::COL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
                     *reinterpret_cast<uint4*>(dst) = make_uint4(f2_hi(u.x, u.y), f2_hi(u.z, u.w), f2_hi(v.x, v.y), f2_hi(v.z, v.w));
                     *reinterpret_cast<uint4*>(dst + L::TILE) = make_uint4(f2_lo(u.x, u.y), f2_lo(u.z, u.w), f2_lo(v.x, v.y), f2_lo(v.z, v.w));
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(q_full);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
             }
             const bool idle = (warp & 3) * 32 >= nq;  // no query in the warp's rows: what its weights hold does not matter
-            float m = -INFINITY, l = 0.0f;            // the maximum that the weights are taken against, in units of 1 / c
+            float m = -INFINITY;                      // the maximum that the weights are taken against, in units of 1 / c
+            float2 l = make_float2(0.0f, 0.0f);
             for (int j = w; j < s.n && ok; j += 2) {
-                const int n = min(SHARED_TILE, keys - (s.tile + j) * SHARED_TILE);
-                ok = mbar_wait_bounded(s_full + w, ss++ & 1);
-                if (__any_sync(FULL_MASK, !ok)) {
-                    ok = false;
-                    break;
-                }
+                // the thread's keys of the tile, and their 16-key runs with a page
+                const int n = min(64, keys - (s.tile + j) * SHARED_TILE - half * 64);
+                ok = __all_sync(FULL_MASK, mbar_wait_bounded(s_full + w, ss++ & 1));
+                if (!ok) break;
                 tc_fence_after();
-                const unsigned have = runs[(tiles + j) & 7];
+                const unsigned have = runs[(tiles + j) & 7] >> (half * 4);
                 if (!idle) {
-                    auto seen = [&](int i) { return i < n && ((have >> (i >> 4)) & 1); };  // key i of the tile
-                    const bool all = n == SHARED_TILE && have == 0xffu;
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (32 * k < n) {
-                            uint32_t v[32];
-                            tc_ld32(st + 32 * k, v);
+                    const bool all = n == 64 && (have & 15) == 15;
+                    uint32_t v[32];  // 32 keys' scores
+                    auto load = [&](int k) {
+                        tc_ld32(st + 32 * k, v);
+                        tc_wait_ld(v);
+                        if (!all) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (all || seen(32 * k + i)) mx = fmaxf(mx, __uint_as_float(v[i]));
+                                if (!(32 * k + i < n && ((have >> (2 * k + (i >> 4))) & 1))) v[i] = __float_as_uint(-INFINITY);
                         }
-                    }
+                    };
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (32 * k < n) {
+                            load(k);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(v[i]));
+                        }
+                    float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    mx = fmaxf(mx, exchange(mx, ok));
+                    if (!ok) break;
                     float f = 1.0f;
                     if (m == -INFINITY) {
                         m = mx;
                         f = 0.0f;
                     } else if ((mx - m) * c > 8.0f) {
-                        f = exp2f((m - mx) * c);
+                        f = tc_exp2((m - mx) * c);
                         m = mx;
                     }
                     if (j >= 2 && __any_sync(FULL_MASK, f != 1.0f)) {
-                        l *= f;
+                        l.x *= f;
+                        l.y *= f;
 #pragma unroll 1
-                        for (int k = 0; k < HD / 32; ++k) {
-                            uint32_t v[32];
-                            tc_ld32(ot + 32 * k, v);
+                        for (int k = 0; k < HD / 64; ++k) {
+                            uint32_t o[32];
+                            tc_ld32(ot + 32 * k, o);
+                            tc_wait_ld(o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                            tc_st32(ot + 32 * k, v);
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tc_st32(ot + 32 * k, o);
                         }
-                        tc_wait_st();
                     }
-                    const float mc = m == -INFINITY ? 0.0f : m * c;
-#pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-                        if (32 * k < n) {
-                            uint32_t v[32], p[32];
-                            tc_ld32(st + 32 * k, v);
+                    const float mc = m == -INFINITY ? 0.0f : m * c;  // 2^(-inf) where no key is seen
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float e0 = tc_exp2(__fmaf_rn(__uint_as_float(v[i]), c, -mc));
-                                float e1 = tc_exp2(__fmaf_rn(__uint_as_float(v[i + 1]), c, -mc));
-                                if (!all) {
-                                    if (!seen(32 * k + i)) e0 = 0.0f;
-                                    if (!seen(32 * k + i + 1)) e1 = 0.0f;
-                                }
-                                l += e0 + e1;
-                                p[i / 2] = f2_hi(e0, e1);
-                                p[16 + i / 2] = f2_lo(e0, e1);
+                    for (int k = 1; k >= 0; --k) {  // the second half is still here
+                        if (32 * k < n) {
+                            if (k == 0 && n > 32) load(0);
+                            uint32_t p[32];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 t = fma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                                      make_float2(c, c), make_float2(-mc, -mc));
+                                const float2 e = make_float2(tc_exp2(t.x), tc_exp2(t.y));
+                                l = add2(l, e);
+                                p[i] = f2_hi(e.x, e.y);
+                                const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+                                const float2 lo = fma2(hi, make_float2(-1.0f, -1.0f), e);
+                                p[16 + i] = f2_hi(lo.x, lo.y);
                             }
                             tc_st32(st + 32 * k, p);  // the weights in the scores' place: 16 columns hi, 16 lo
                         }
@@ -398,36 +443,37 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                     tc_wait_st();
                 }
                 tc_fence_before();
-                mbar_arrive(p_full + w);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + w);
             }
             tiles += s.n;
             // ---- the record of the group's tiles
             if (ok && s.n > w) {
-                const int last = (s.n - w + 1) / 2;  // products of this group in the segment
-                pv += last;
-                ok = mbar_wait_bounded(pv_done + w, (pv - 1) & 1);
-                if (__any_sync(FULL_MASK, !ok)) ok = false;
+                pv += (s.n - w + 1) / 2;  // products of this group in the segment
+                ok = __all_sync(FULL_MASK, mbar_wait_bounded(pv_done + w, (pv - 1) & 1));
                 tc_fence_after();
                 if (ok && !idle) {
+                    const float sum = l.x + l.y, other = exchange(sum, ok);
                     float* rec = a.part + (shared_row(a, s.g, s.h, s.pass, set, q0 - s.pass * a.side * SHARED_QUERIES + r) * 2 + w) * PAGED_REC(HD);
 #pragma unroll 1
-                    for (int k = 0; k < HD / 32; ++k) {
+                    for (int k = 0; k < HD / 64; ++k) {
                         uint32_t v[32];
                         tc_ld32(ot + 32 * k, v);
+                        tc_wait_ld(v);
                         if (r < nq) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<uint4*>(rec + 32 * k + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                                *reinterpret_cast<uint4*>(rec + half * (HD / 2) + 32 * k + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                         }
                     }
-                    if (r < nq) *reinterpret_cast<float2*>(rec + HD) = make_float2(m * a.scale, l);
+                    if (r < nq && !half) *reinterpret_cast<float2*>(rec + HD) = make_float2(m * a.scale, sum + other);
                 }
                 tc_fence_before();
             }
-            // Both groups are done with the queries and with tensor memory.
-            mbar_arrive(q_free);
-            ok = ok && mbar_wait_bounded(q_free, segs++ & 1);
-            ok = __all_sync(FULL_MASK, ok);
+            // All are done with the queries and with tensor memory.
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_free);
+            ok = ok && __all_sync(FULL_MASK, mbar_wait_bounded(q_free, segs++ & 1));
         }
         if (!ok) *failed = 1;
     }
