@@ -69,17 +69,16 @@ __device__ __forceinline__ uint32_t paged_u8(uint32_t v, uint32_t sel) {
 // A block of a (session, head), and the next ones in order.
 struct PagedAt {
     int b, h, blk, nb;  // session, KV head, block of nb
-    __device__ __forceinline__ void seek(const PagedArgs& a, int64_t x) {
-        int lo = 0, hi = a.B;
-        const int64_t y = x / a.nkv;  // first[lo] <= y < first[hi]: the session
+    __device__ __forceinline__ void seek(const PagedArgs& a, int x) {
+        int lo = 0, hi = a.B;  // first[lo] nkv <= x < first[hi] nkv: the session
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (a.first[mid] <= y) lo = mid;
+            if (a.first[mid] * a.nkv <= x) lo = mid;
             else hi = mid;
         }
         b = lo;
         nb = a.first[lo + 1] - a.first[lo];
-        const int r = (int)(x - (int64_t)a.first[lo] * a.nkv);
+        const int r = x - a.first[lo] * a.nkv;
         h = r / nb;
         blk = r - h * nb;
     }
@@ -119,8 +118,8 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
             if (a.to[b] == 0)
                 for (int i = threadIdx.x; i < a.nh * HD; i += PAGED_WARPS * 32) a.out[(size_t)b * a.nh * HD + i] = __float2half_rn(0.0f);
     }
-    const int64_t x0 = (int64_t)blockIdx.x * a.blocks / a.ctas, x1 = ((int64_t)blockIdx.x + 1) * a.blocks / a.ctas;
-    int left = (int)(x1 - x0);  // blocks still to take
+    const int x0 = a.share.begin(blockIdx.x), x1 = a.share.begin(blockIdx.x + 1);
+    int left = x1 - x0;  // blocks still to take
     if (left <= 0) {
         if (a.late_wait) pdl_wait();
         return;
@@ -487,7 +486,7 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
                 }
             }
             __syncthreads();
-            const int64_t s0 = (int64_t)a.first[at.b] * a.nkv + (int64_t)at.h * at.nb;  // the (session, head)'s blocks
+            const int s0 = a.first[at.b] * a.nkv + at.h * at.nb;  // the (session, head)'s blocks
             const bool whole = a.from[at.b] == 0 && x0 <= s0 && s0 + at.nb <= x1;
             float* rec = a.part + ((size_t)blockIdx.x + (size_t)at.b * a.nkv + at.h) * GQ * REC;
             __half* out = a.out + ((size_t)at.b * a.nh + (size_t)at.h * GQ) * HD;
@@ -541,64 +540,104 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
 
 // The merge of a (session, head) that several CTAs share: out = sum_i w_i o_i / sum_i w_i l_i
 // over its records, w_i = e^{m_i - max m}: those of its own keys and those that the CTAs of
-// its group's shared keys left.  A block per (session, KV head).
-constexpr int PAGED_MERGE_THREADS = 128;
+// its group's shared keys left.  A block per (session, query head): a warp forms the weights, then each
+// warp sums every fourth record, four of them in flight, and the warps' sums are added in order.
+constexpr int PAGED_MERGE_WARPS = 4;
+constexpr int PAGED_MAX_RECORDS = PAGED_MAX_CTAS + 2 * SHARED_MAX_CTAS;
 template <int HD>
-__global__ void __launch_bounds__(PAGED_MERGE_THREADS) paged_merge_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ SharedArgs sh) {
-    constexpr int REC = PAGED_REC(HD);
-    const int h = blockIdx.x, b = blockIdx.y, gq = a.nh / a.nkv;
+__global__ void __launch_bounds__(PAGED_MERGE_WARPS * 32) paged_merge_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ SharedArgs sh) {
+    constexpr int REC = PAGED_REC(HD), DIMS = HD / 32;  // a lane's dims
+    __shared__ float2 weight[PAGED_MAX_RECORDS];        // (m, l), then (w, -)
+    __shared__ float sums[PAGED_MERGE_WARPS][HD];
+    __shared__ float denom;
+    const int qh = blockIdx.x, b = blockIdx.y, gq = a.nh / a.nkv, h = qh / gq, i = qh - h * gq;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nb = a.first[b + 1] - a.first[b], g = a.group[b];
+    // n records of its own keys, then a pair of each set of CTAs that has some of the shared keys
+    const float *rec = nullptr, *pairs = nullptr;
+    int n = 0, sets = 0;
+    size_t set_step = 0;
+    if (nb) {
+        const int s0 = a.first[b] * a.nkv + h * nb, c0 = a.share.taker(s0);
+        n = a.share.taker(s0 + nb - 1) - c0 + 1;
+        rec = a.part + (((size_t)c0 + (size_t)b * a.nkv + h) * gq + i) * REC;
+    }
+    if (g != SHARED_NONE) {
+        const int per = SHARED_QUERIES * sh.side, query = (b - sh.lead[g]) * gq + i, pass = query / per, T = sh.tiles(g);
+        const int s0 = sh.first[g] * sh.nkv + (h * sh.passes(g) + pass) * T, c0 = sh.share.taker(s0);
+        sets = sh.share.taker(s0 + T - 1) - c0 + 1;
+        pairs = sh.part + shared_row(sh, g, h, pass, c0, query - pass * per) * 2 * REC;
+        set_step = (size_t)per * 2 * REC;
+    }
     pdl_launch_dependents();
     pdl_wait();
-    if (sh.n_groups && h == 0 && b == 0 && threadIdx.x < 32) {  // the call's fault word
+    if (sh.n_groups && qh == 0 && b == 0 && warp == PAGED_MERGE_WARPS - 1) {  // the call's fault word
         int bad = 0;
-        for (int i = threadIdx.x; i < sh.sets * sh.side; i += 32) bad |= sh.status[i];
+        for (int k = lane; k < sh.sets * sh.side; k += 32) bad |= sh.status[k];
         bad = __any_sync(FULL_MASK, bad != 0);
-        if (threadIdx.x == 0) *a.err = bad ? ERR_WAIT_TIMEOUT : 0;
+        if (lane == 0) *a.err = bad ? ERR_WAIT_TIMEOUT : 0;
     }
-    const int nb = a.first[b + 1] - a.first[b], g = a.group[b];
-    if (!nb && g == SHARED_NONE) return;
-    const float* rec = nullptr;
-    int n = 0;
-    if (nb) {
-        const int64_t s0 = (int64_t)a.first[b] * a.nkv + (int64_t)h * nb;
-        const int c0 = paged_cta(s0, a.blocks, a.ctas), c1 = paged_cta(s0 + nb - 1, a.blocks, a.ctas);
-        if (c0 == c1 && g == SHARED_NONE) return;  // written by the CTA itself
-        rec = a.part + ((size_t)c0 + (size_t)b * a.nkv + h) * gq * REC;
-        n = c1 - c0 + 1;
-    }
-    for (int i = threadIdx.x; i < gq * (HD / 4); i += PAGED_MERGE_THREADS) {
-        const int qh = i / (HD / 4), d = i % (HD / 4) * 4;
+    const int total = n + 2 * sets;
+    if (!total || (n == 1 && !sets)) return;  // no keys, or written by the CTA itself
+    auto record = [&](int k) {
+        return k < n ? rec + (size_t)k * gq * REC : pairs + ((k - n) >> 1) * set_step + ((k - n) & 1) * REC;
+    };
+    if (warp == 0) {
         float M = -INFINITY, den = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        auto add = [&](const float* r) {
-            const float2 ml = *reinterpret_cast<const float2*>(r + HD);
-            const float4 v = *reinterpret_cast<const float4*>(r + d);
-            const float top = fmaxf(M, ml.x), ref = top == -INFINITY ? 0.0f : top;
-            const float f = expf(__fsub_rn(M, ref)), w = expf(__fsub_rn(ml.x, ref));
-            M = top;
-            den = __fmaf_rn(den, f, __fmul_rn(w, ml.y));
-            acc.x = __fmaf_rn(acc.x, f, __fmul_rn(w, v.x));
-            acc.y = __fmaf_rn(acc.y, f, __fmul_rn(w, v.y));
-            acc.z = __fmaf_rn(acc.z, f, __fmul_rn(w, v.z));
-            acc.w = __fmaf_rn(acc.w, f, __fmul_rn(w, v.w));
-        };
-        for (int k = 0; k < n; ++k) add(rec + ((size_t)k * gq + qh) * REC);
-        if (g != SHARED_NONE) {
-            const int query = (b - sh.lead[g]) * gq + qh, pass = query / (SHARED_QUERIES * sh.side), T = sh.tiles(g);
-            const int64_t s0 = (int64_t)sh.first[g] * sh.nkv + ((int64_t)h * sh.passes(g) + pass) * T;
-            const int c0 = paged_cta(s0, sh.total, sh.sets), c1 = paged_cta(s0 + T - 1, sh.total, sh.sets);
-            for (int c = c0; c <= c1; ++c) {
-                const int64_t x0 = (int64_t)c * sh.total / sh.sets, x1 = ((int64_t)c + 1) * sh.total / sh.sets;
-                const int tiles = (int)((x1 < s0 + T ? x1 : s0 + T) - (x0 > s0 ? x0 : s0));
-                const float* r = sh.part + shared_row(sh, g, h, pass, c, query - pass * SHARED_QUERIES * sh.side) * 2 * REC;
-                add(r);
-                if (tiles > 1) add(r + REC);
+        for (int k = lane; k < total; k += 32) {
+            const float2 ml = *reinterpret_cast<const float2*>(record(k) + HD);
+            weight[k] = ml;
+            M = fmaxf(M, ml.x);
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, x));
+        const float ref = M == -INFINITY ? 0.0f : M;
+        for (int k = lane; k < total; k += 32) {
+            const float2 ml = weight[k];
+            const float w = expf(__fsub_rn(ml.x, ref));
+            weight[k].x = w;
+            den = __fmaf_rn(w, ml.y, den);
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) den = __fadd_rn(den, __shfl_xor_sync(FULL_MASK, den, x));
+        if (lane == 0) denom = den == 0.0f ? 1.0f : den;  // 0: no key has a page
+    }
+    __syncthreads();
+    float acc[DIMS];
+#pragma unroll
+    for (int d = 0; d < DIMS; ++d) acc[d] = 0.0f;
+    constexpr int U = 4;
+    for (int k0 = warp; k0 < total; k0 += U * PAGED_MERGE_WARPS) {
+        float v[U][DIMS], w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + u * PAGED_MERGE_WARPS;
+            w[u] = k < total ? weight[k].x : 0.0f;
+            if (w[u] != 0.0f) {  // what a record without keys holds is not read
+                const float* r = record(k) + lane * DIMS;
+                if constexpr (DIMS == 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(r);
+                    v[u][0] = f.x, v[u][1] = f.y, v[u][2] = f.z, v[u][3] = f.w;
+                } else {
+                    const float2 f = *reinterpret_cast<const float2*>(r);
+                    v[u][0] = f.x, v[u][1] = f.y;
+                }
             }
         }
-        if (den == 0.0f) den = 1.0f;
-        __half2* p = reinterpret_cast<__half2*>(a.out + ((size_t)b * a.nh + (size_t)h * gq + qh) * HD + d);
-        p[0] = __floats2half2_rn(__fdiv_rn(acc.x, den), __fdiv_rn(acc.y, den));
-        p[1] = __floats2half2_rn(__fdiv_rn(acc.z, den), __fdiv_rn(acc.w, den));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (w[u] != 0.0f)
+#pragma unroll
+                for (int d = 0; d < DIMS; ++d) acc[d] = __fmaf_rn(w[u], v[u][d], acc[d]);
+    }
+#pragma unroll
+    for (int d = 0; d < DIMS; ++d) sums[warp][lane * DIMS + d] = acc[d];
+    __syncthreads();
+    for (int d = threadIdx.x; d < HD; d += PAGED_MERGE_WARPS * 32) {
+        float o = sums[0][d];
+#pragma unroll
+        for (int k = 1; k < PAGED_MERGE_WARPS; ++k) o = __fadd_rn(o, sums[k][d]);
+        a.out[((size_t)b * a.nh + qh) * HD + d] = __float2half_rn(__fdiv_rn(o, denom));
     }
 }
 
@@ -674,8 +713,8 @@ cudaError_t launch_paged_merge(const PagedArgs& a, const SharedArgs& sh, int hd,
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     paged_config(cfg, attr, pdl, s);
-    cfg.gridDim = dim3(a.nkv, a.B);
-    cfg.blockDim = dim3(PAGED_MERGE_THREADS);
+    cfg.gridDim = dim3(a.nh, a.B);
+    cfg.blockDim = dim3(PAGED_MERGE_WARPS * 32);
     return hd == 64 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64>, a, sh) : cudaLaunchKernelEx(&cfg, paged_merge_kernel<128>, a, sh);
 }
 

@@ -117,7 +117,8 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 
 // ---- the kernel ---------------------------------------------------------------
 constexpr int SH_SOFT = 16;                     // softmax warps: two groups of eight, two warps a quarter of the rows
-constexpr int SH_THREADS = (SH_SOFT + 2) * 32;  // and the copies' and the products' warps
+constexpr int SH_COPY = SH_SOFT, SH_SCORES = SH_SOFT + 1, SH_VALUES = SH_SOFT + 2;  // the copies' and the products' warps
+constexpr int SH_THREADS = (SH_SOFT + 3) * 32;
 
 template <int HD>
 struct SharedSmem {
@@ -133,20 +134,18 @@ struct SharedSmem {
 
 // A CTA's next tiles of one (group, KV head, pass).
 struct SharedSeg {
-    int g, h, pass, tile, n;  // tiles [tile, tile + n)
-    __device__ __forceinline__ void at(const SharedArgs& a, int64_t x, int left) {
-        int lo = 0, hi = a.n_groups;
-        const int64_t y = x / a.nkv;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.first[mid] <= y) lo = mid;
-            else hi = mid;
-        }
-        g = lo;
-        const int r = (int)(x - (int64_t)a.first[g] * a.nkv), T = a.tiles(g), u = r / T;
+    int g = 0, h, pass, tile, n;  // tiles [tile, tile + n)
+    // from x on, at most `left` of them; g: a group at or before x's
+    __device__ __forceinline__ void at(const SharedArgs& a, int x, int left) {
+        while (x >= a.first[g + 1] * a.nkv) ++g;
+        const int r = x - a.first[g] * a.nkv, T = a.tiles(g), u = r / T;
         tile = r - u * T;
-        h = u / a.passes(g);
-        pass = u - h * a.passes(g);
+        h = u;
+        pass = 0;
+        if (a.passes(g) > 1) {
+            h = u / a.passes(g);
+            pass = u - h * a.passes(g);
+        }
         n = min(T - tile, left);
     }
 };
@@ -172,7 +171,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         if (threadIdx.x == 0) a.status[blockIdx.x] = 1;
         return;
     }
-    if (warp == SH_SOFT) {
+    if (warp == SH_COPY) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_at)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -202,19 +201,19 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     pdl_launch_dependents();  // after the wait: the kernel behind this one relies on it, and reads at once
 
     const int set = blockIdx.x / a.side, mine = blockIdx.x - set * a.side;  // of the CTAs side by side
-    const int64_t x0 = (int64_t)set * a.total / a.sets, x1 = ((int64_t)set + 1) * a.total / a.sets;
+    const int x0 = a.share.begin(set), x1 = a.share.begin(set + 1);
     const int box = a.box_runs;  // 16-key runs of a copy's box
     // The first of the CTA's queries in a segment's group, and how many (<= 0: none).
     auto first_query = [&](const SharedSeg& s) { return (s.pass * a.side + mine) * SHARED_QUERIES; };
     auto n_queries = [&](const SharedSeg& s) { return min(SHARED_QUERIES, a.queries[s.g] - first_query(s)); };
 
-    if (warp == SH_SOFT) {
+    if (warp == SH_COPY) {
         // ---- copies: K and V of each tile, boxes of whole 16-key runs within a page
         uint32_t slot = 0, phase = 0, tiles = 0;
         bool ok = true;
-        for (int64_t x = x0; x < x1 && ok;) {
-            SharedSeg s;
-            s.at(a, x, (int)(x1 - x));
+        SharedSeg s;
+        for (int x = x0; x < x1 && ok;) {
+            s.at(a, x, x1 - x);
             x += s.n;
             if (n_queries(s) <= 0) continue;
             const int keys = a.keys[s.g];
@@ -256,67 +255,64 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             }
         }
         if (!ok && lane == 0) *failed = 1;
-    } else if (warp == SH_SOFT + 1) {
-        // ---- products
+    } else if (warp == SH_SCORES || warp == SH_VALUES) {
+        // ---- products, S = Q K^T and O += P V by a thread each: one that has issued products
+        // goes on only when the tensor core has taken them (1200 cycles for a tile's), and the other's
+        // should be ready then.  K parts are in the buffers' even places of a round, V parts in the odd ones.
         if (lane == 0) {
-            uint32_t kslot = 0, kphase = 0, vslot = 1, vphase = 0, q_phase = 0;  // K and V parts lie in turn
-            unsigned pv_phase = 0, p_phase = 0;  // a bit for each half of the softmax warps
-            auto step = [](uint32_t& slot, uint32_t& phase) {
-                slot += 2;
-                if (slot >= NS) {
-                    slot -= NS;
-                    phase ^= 1;
-                }
-            };
+            const bool values = warp == SH_VALUES;
+            uint32_t slot = values, phase = 0, q_phase = 0;
+            unsigned half_phase = 0;  // of p_full (values) or pv_done (scores), a bit for each half of the softmax warps
             bool ok = true;
             const uint32_t qs = smem_u32(smem + L::Q), ring = smem_u32(smem + L::RING);
-            for (int64_t x = x0; x < x1 && ok;) {
-                SharedSeg s;
-                s.at(a, x, (int)(x1 - x));
+            SharedSeg s;
+            for (int x = x0; x < x1 && ok;) {
+                s.at(a, x, x1 - x);
                 x += s.n;
                 if (n_queries(s) <= 0) continue;
                 const int keys = a.keys[s.g];
-                ok = mbar_wait_bounded(q_full, q_phase);
-                q_phase ^= 1;
-                if (!ok) break;
-                tc_fence_after();
-                auto scores = [&](int j) {  // S of tile j of the segment
-                    const int w = j & 1, n = min(SHARED_TILE, keys - (s.tile + j) * SHARED_TILE);
-                    if (!mbar_wait_bounded(full + kslot, kphase)) return false;
-                    tc_fence_after();
-                    const uint32_t id = tc_idesc(n, false), kb = ring + kslot * L::TILE;
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int k = 0; k < HD / 16; ++k) {
-                            const uint32_t off = (k / 4) * L::COL + (k % 4) * 32;
-                            tc_mma_ss(tmem + w * 128, tc_desc(qs + part * L::TILE + off, 0), tc_desc(kb + off, 0), id, part || k);
-                        }
-                    tc_commit(s_full + w);
-                    tc_commit(empty + kslot);
-                    step(kslot, kphase);
-                    return true;
-                };
-                ok = scores(0) && (s.n < 2 || scores(1));
+                if (!values) {
+                    ok = mbar_wait_bounded(q_full, q_phase);  // the segment before is done with then, too
+                    q_phase ^= 1;
+                }
                 for (int j = 0; j < s.n && ok; ++j) {
                     const int w = j & 1, n = min(SHARED_TILE, keys - (s.tile + j) * SHARED_TILE);
-                    ok = mbar_wait_bounded(p_full + w, (p_phase >> w) & 1) && mbar_wait_bounded(full + vslot, vphase);
-                    p_phase ^= 1u << w;
+                    // weights that are there; or, for scores, weights in their place that are done with
+                    if (values || j >= 2) ok = mbar_wait_bounded((values ? p_full : pv_done) + w, (half_phase >> w) & 1);
+                    ok = ok && mbar_wait_bounded(full + slot, phase);
                     if (!ok) break;
+                    if (values || j >= 2) half_phase ^= 1u << w;
                     tc_fence_after();
-                    const uint32_t id = tc_idesc(HD, true), vb = ring + vslot * L::TILE;
-                    for (int k = 0; k < n / 16; ++k)
+                    const uint32_t part0 = ring + slot * L::TILE;
+                    if (!values) {
+                        const uint32_t id = tc_idesc(n, false);
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
-                            tc_mma_ts(tmem + 256 + w * HD, tmem + w * 128 + 32 * (k / 2) + 16 * part + 8 * (k & 1),
-                                      tc_desc(vb + k * 2048, L::COL), id, part || k || j >= 2);
-                    tc_commit(empty + vslot);
-                    step(vslot, vphase);
-                    tc_commit(pv_done + w);
-                    // The next scores take the place of these weights, so not before the product is done.
-                    if (j + 2 < s.n) ok = mbar_wait_bounded(pv_done + w, (pv_phase >> w) & 1) && scores(j + 2);
-                    pv_phase ^= 1u << w;
+#pragma unroll
+                            for (int k = 0; k < HD / 16; ++k) {
+                                const uint32_t off = (k / 4) * L::COL + (k % 4) * 32;
+                                tc_mma_ss(tmem + w * 128, tc_desc(qs + part * L::TILE + off, 0), tc_desc(part0 + off, 0), id, part || k);
+                            }
+                        tc_commit(s_full + w);
+                        tc_commit(empty + slot);
+                    } else {
+                        const uint32_t id = tc_idesc(HD, true);
+                        for (int k = 0; k < n / 16; ++k)
+#pragma unroll
+                            for (int part = 0; part < 2; ++part)
+                                tc_mma_ts(tmem + 256 + w * HD, tmem + w * 128 + 32 * (k / 2) + 16 * part + 8 * (k & 1),
+                                          tc_desc(part0 + k * 2048, L::COL), id, part || k || j >= 2);
+                        tc_commit(pv_done + w);
+                        tc_commit(empty + slot);
+                    }
+                    slot += 2;
+                    if (slot >= NS) {
+                        slot -= NS;
+                        phase ^= 1;
+                    }
                 }
+                // The last products of a half are not waited for here: keep its count.
+                if (!values) half_phase ^= (s.n > 0 ? 1u : 0u) | (s.n > 1 ? 2u : 0u);
             }
             if (!ok) *failed = 1;
         }
@@ -340,9 +336,9 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             good = __all_sync(FULL_MASK, mbar_wait_bounded(partner, met++ & 1));
             return maxima[(half ^ 1) * SHARED_QUERIES + r];
         };
-        for (int64_t x = x0; x < x1 && ok;) {
-            SharedSeg s;
-            s.at(a, x, (int)(x1 - x));
+        SharedSeg s;
+        for (int x = x0; x < x1 && ok;) {
+            s.at(a, x, x1 - x);
             x += s.n;
             const int nq = n_queries(s), q0 = first_query(s);
             if (nq <= 0) continue;
@@ -447,14 +443,16 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 if (lane == 0) mbar_arrive(p_full + w);
             }
             tiles += s.n;
-            // ---- the record of the group's tiles
-            if (ok && s.n > w) {
+            // ---- the half's record of the segment's tiles
+            float* rec = a.part + (shared_row(a, s.g, s.h, s.pass, set, q0 - s.pass * a.side * SHARED_QUERIES + r) * 2 + w) * PAGED_REC(HD);
+            if (s.n <= w) {  // one tile: the second half had none
+                if (r < nq && !half) *reinterpret_cast<float2*>(rec + HD) = make_float2(-INFINITY, 0.0f);
+            } else if (ok) {
                 pv += (s.n - w + 1) / 2;  // products of this group in the segment
                 ok = __all_sync(FULL_MASK, mbar_wait_bounded(pv_done + w, (pv - 1) & 1));
                 tc_fence_after();
                 if (ok && !idle) {
                     const float sum = l.x + l.y, other = exchange(sum, ok);
-                    float* rec = a.part + (shared_row(a, s.g, s.h, s.pass, set, q0 - s.pass * a.side * SHARED_QUERIES + r) * 2 + w) * PAGED_REC(HD);
 #pragma unroll 1
                     for (int k = 0; k < HD / 64; ++k) {
                         uint32_t v[32];
@@ -478,7 +476,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         if (!ok) *failed = 1;
     }
     __syncthreads();
-    if (warp == SH_SOFT) {
+    if (warp == SH_COPY) {
         if (*failed) {  // copies may be in flight: give them their time before the memory is given up
             if (lane < NS)
                 for (int i = 0; i < 2; ++i) (void)mbar_wait_bounded(full + lane, i);

@@ -8,10 +8,22 @@
 
 namespace kd {
 
+// `total` pieces of work in a row for `parts` takers, each a run of them: the first `more` take
+// `least` + 1.  (No division to find a taker's run; one to find a piece's taker.)
+struct Shares {
+    int least, more;
+    Shares() = default;
+    Shares(int total, int parts) : least(total / parts), more(total % parts) {}
+    __host__ __device__ int begin(int i) const { return i * least + (i < more ? i : more); }
+    __host__ __device__ int taker(int x) const {
+        const int big = more * (least + 1);
+        return x < big ? x / (least + 1) : more + (x - big) / least;
+    }
+};
+
 // The keys of the sessions that each reads for itself are cut into blocks of PAGED_BLOCK.
-// Blocks are numbered session by session, head by head; CTA i of G takes blocks
-// [i N / G, (i + 1) N / G) of the N: an equal share, which may end one (session, head)
-// and begin the next.  What a CTA finds of a (session, head) x is record i + x, so a
+// Blocks are numbered session by session, head by head, and every CTA takes an equal share of
+// them in a row, which may end one (session, head) and begin the next.  What a CTA finds of a (session, head) x is record i + x, so a
 // (session, head)'s records are consecutive and no record is used twice.
 constexpr int PAGED_WARPS = 4;
 constexpr int PAGED_KEYS = 32;  // keys of a warp's piece
@@ -31,7 +43,7 @@ struct PagedArgs {
     int table_ld, n_pages, ps, B, nh, nkv, ctas;
     int late_wait;              // started beside the kernel before, whose end it awaits at its own
     float scale;
-    int64_t blocks;             // N
+    Shares share;               // of all blocks, among the CTAs
     // Session b reads keys [from[b], to[b]); those before lead_keys[b] through session lead[b]'s table.
     int from[KD_PAGED_MAX_SEQS], to[KD_PAGED_MAX_SEQS], lead_keys[KD_PAGED_MAX_SEQS];
     int first[KD_PAGED_MAX_SEQS + 1];  // first block of the session's first head, in blocks / nkv
@@ -42,13 +54,11 @@ constexpr int SHARED_NONE = 255;
 static_assert(KD_PAGED_MAX_SEQS <= 256, "sessions in a byte");
 
 __host__ __device__ inline int paged_blocks(int keys) { return (keys + PAGED_BLOCK - 1) / PAGED_BLOCK; }
-// The CTA that takes block x.
-__host__ __device__ inline int paged_cta(int64_t x, int64_t blocks, int ctas) { return (int)(((x + 1) * ctas - 1) / blocks); }
 
 // Groups whose shared keys are read once for all their queries (kd_attn_shared.cu).  A pass of a
 // (group, KV head) is its keys, in tiles of SHARED_TILE, for up to `side` tiles of
 // SHARED_QUERIES queries, one for each of the CTAs side by side; the tiles of all passes are one
-// sequence, of which set i of the `sets` of CTAs takes [i total / sets, (i + 1) total / sets).
+// sequence, of which every one of the `sets` of CTAs takes an equal share.
 // A set's CTAs leave two records (one for each half of their warps) of each query that has tiles there.
 constexpr int SHARED_TILE = 128, SHARED_QUERIES = 128, SHARED_MAX_SIDE = 8;
 constexpr int SHARED_MAX_GROUPS = KD_PAGED_MAX_SEQS / 2;  // of two sessions at least
@@ -61,7 +71,7 @@ struct SharedArgs {
     int* status;  // [CTA]: 1 where a bounded wait ran out
     int table_ld, n_pages, ps, rows, box_runs, nh, nkv, gq, n_groups, side, sets;
     float scale;
-    int64_t total;
+    Shares share;  // of all tiles, among the sets
     int keys[SHARED_MAX_GROUPS], queries[SHARED_MAX_GROUPS];  // shared keys (whole pages), sessions times gq
     int before[SHARED_MAX_GROUPS];                            // queries of the groups before it
     int first[SHARED_MAX_GROUPS + 1];                         // first tile of its first head's first pass, in tiles / nkv

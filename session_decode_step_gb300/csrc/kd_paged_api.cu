@@ -52,9 +52,10 @@ static void shared_plan(SharedArgs& t, int sms) {
         before += t.queries[g];
     }
     t.first[t.n_groups] = (int)first;
-    t.total = first * t.nkv;
+    const int64_t total = first * t.nkv;
     t.sets = sms / t.side;
-    if (t.sets > t.total) t.sets = (int)t.total;
+    if (t.sets > total) t.sets = (int)total;
+    t.share = Shares((int)total, t.sets);
 }
 
 static kd_status paged_call(const char* fn, bool q8, const float* q, const void* kp, const void* vp, const uint16_t* ks,
@@ -79,7 +80,7 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
         return failf(KD_ERR_INVALID_ARG, "%s: table and fault must be 4-byte aligned, out 2-byte", fn);
     PagedArgs a = {};
     SharedArgs sh = {};
-    int64_t total = 0;
+    int64_t total = 0, shared_tiles = 0;
     for (int b = 0; b < B; ++b) {
         if (lens[b] < 0 || lens[b] > (int64_t)table_ld * ps)
             return failf(KD_ERR_POSITION, "%s: length %d in tables of %d pages of %d", fn, lens[b], table_ld, ps);
@@ -106,6 +107,8 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
                 }
             }
             if (once) {
+                shared_tiles += (int64_t)(shared / SHARED_TILE + 1) * (group_rows[g] * (nh / nkv) / SHARED_QUERIES + 1);
+                if (shared_tiles > 0x7fffffff / nkv) return failf(KD_ERR_UNSUPPORTED, "%s: 2^31 or more blocks of keys", fn);
                 sh.lead[sh.n_groups] = (uint8_t)b;
                 sh.keys[sh.n_groups] = shared;
                 sh.queries[sh.n_groups++] = group_rows[g] * (nh / nkv);
@@ -143,14 +146,15 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
     a.nh = nh;
     a.nkv = nkv;
     a.scale = 1.0f / std::sqrt((float)hd);
-    a.blocks = total * nkv;
-    a.ctas = a.blocks < 1 ? 1 : a.blocks < slots ? (int)a.blocks : slots;
+    const int blocks = (int)(total * nkv);
+    a.ctas = blocks < 1 ? 1 : blocks < slots ? blocks : slots;
+    a.share = Shares(blocks, a.ctas);
     bool merge = sh.n_groups > 0;
     for (int b = 0; b < B && !merge; ++b) {
         const int nb = a.first[b + 1] - a.first[b];
         for (int h = 0; h < nkv && nb && !merge; ++h) {
-            const int64_t s0 = (int64_t)a.first[b] * nkv + (int64_t)h * nb;
-            merge = paged_cta(s0, a.blocks, a.ctas) != paged_cta(s0 + nb - 1, a.blocks, a.ctas);
+            const int s0 = a.first[b] * nkv + h * nb;
+            merge = a.share.taker(s0) != a.share.taker(s0 + nb - 1);
         }
     }
     cudaStream_t s = (cudaStream_t)stream;
