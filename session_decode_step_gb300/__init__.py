@@ -299,35 +299,82 @@ class _CtypesCalls:
                                    _stream(stream))
 
     @staticmethod
-    def rope(table, x, dtype, ld, positions, n_tokens, n_heads, out, ld_out, stream):
-        return lib().kd_rope(table, x, dtype, _int(ld, 64), _ptr(positions), _int(n_tokens), _int(n_heads), out,
-                             _int(ld_out, 64), _stream(stream))
+    def rope(plan, x, positions, out, stream):
+        px, ld, t, h, d, dtype = _heads(x, "x")
+        po, ld_out, *shape, out_dtype = _heads(out, "out")
+        if shape != [t, h, d] or out_dtype != dtype or (plan is not None and d != plan.head_dim):
+            raise ValueError("x and out must be alike, in heads of the plan's head_dim")
+        if positions.numel() != t or positions.dtype != sys.modules["torch"].int32:
+            raise ValueError(f"expected {t} int32 positions")
+        return lib().kd_rope(_plan(plan), px, dtype, ld, _ptr(positions), _int(t), _int(h), po, ld_out, _stream(stream))
 
     @staticmethod
-    def append(rope, k, k_ld, v, v_ld, q, q_ld, dtype, rows, planes, table, table_ld, starts, counts, n_heads, n_kv_heads,
-               head_dim, n_pages, page_size, q_out, fault, stream):
+    def append(plan, k_new, v_new, planes, table, starts, counts, n_heads, n_kv_heads, head_dim, n_pages, page_size, q, q_out,
+               fault, stream):
+        pk, k_ld, rows, h, d, dtype = _heads(k_new, "k_new")
+        pv, v_ld, *shape = _heads(v_new, "v_new")
+        if shape != [rows, h, d, dtype] or (h, d) != (n_kv_heads, head_dim):
+            raise ValueError("k_new and v_new must be alike: [rows][n_kv_heads][head_dim]")
+        pq = po = None
+        q_ld = 0
+        if q is not None:
+            pq, q_ld, *shape = _heads(q, "q")
+            po, o_ld, *got = _heads(q_out, "q_out")
+            if shape != [rows, n_heads, d, dtype] or got != [rows, n_heads, d, KD_F32] or o_ld != n_heads * d:
+                raise ValueError("q must be [rows][n_heads][head_dim] of k_new's type, and q_out so in contiguous fp32")
         starts = _i32(starts)
         counts = _i32(counts, starts.size)
+        table_ld = _table(table, starts.size)
         if min(counts, default=0) >= 0 and int(counts.sum(dtype=np.int64)) != rows:
             raise ValueError(f"{rows} new rows for counts of {int(counts.sum(dtype=np.int64))} in all")
         fn = lib().kd_paged_append if len(planes) == 2 else lib().kd_paged_append_q8
         shape = (_int(head_dim),) if len(planes) == 2 else ()
-        return fn(rope, k, _int(k_ld, 64), v, _int(v_ld, 64), q, _int(q_ld, 64), dtype, *map(_ptr, planes), _ptr(table),
-                  _int(table_ld), starts.ctypes.data_as(_I32P), counts.ctypes.data_as(_I32P), starts.size, _int(n_heads),
-                  _int(n_kv_heads), *shape, _int(n_pages), _int(page_size), q_out, _ptr(fault), _stream(stream))
+        return fn(_plan(plan), pk, k_ld, pv, v_ld, pq, q_ld, dtype, *map(_ptr, planes), _ptr(table), table_ld,
+                  starts.ctypes.data_as(_I32P), counts.ctypes.data_as(_I32P), starts.size, _int(n_heads), _int(n_kv_heads),
+                  *shape, _int(n_pages), _int(page_size), po, _ptr(fault), _stream(stream))
 
     @staticmethod
-    def paged(q, planes, table, table_ld, lens, group_rows, group_prefix, n_heads, n_kv_heads, head_dim, n_pages, page_size,
-              out, workspace, fault, stream):
+    def paged(q, planes, table, lens, group_rows, group_prefix, n_heads, n_kv_heads, head_dim, n_pages, page_size, out,
+              workspace, fault, stream):
         lens = _i32(lens)
+        table_ld = _table(table, lens.size)
         rows = _i32(() if group_rows is None else group_rows)
         prefix = _i32(() if group_prefix is None else group_prefix, rows.size)
         fn = lib().kd_attn_paged_decode if len(planes) == 2 else lib().kd_attn_paged_decode_q8
         shape = (_int(head_dim),) if len(planes) == 2 else ()
-        return fn(_ptr(q), *map(_ptr, planes), _ptr(table), _int(table_ld), lens.ctypes.data_as(_I32P), lens.size,
+        return fn(_ptr(q), *map(_ptr, planes), _ptr(table), table_ld, lens.ctypes.data_as(_I32P), lens.size,
                   rows.ctypes.data_as(_I32P), prefix.ctypes.data_as(_I32P), rows.size, _int(n_heads), _int(n_kv_heads),
                   *shape, _int(n_pages), _int(page_size), _ptr(out), _ptr(workspace), workspace.nbytes, _ptr(fault),
                   _stream(stream))
+
+
+_dtypes = None
+
+
+def _heads(x, what):
+    """(address, row distance, rows, heads, head_dim, dtype) of a tensor [rows][heads][head_dim] whose heads lie
+    one after another; rows may be further apart (a part of a fused projection)."""
+    global _dtypes
+    if _dtypes is None:
+        torch = sys.modules["torch"]
+        _dtypes = {torch.float32: KD_F32, torch.float16: KD_F16, torch.bfloat16: KD_BF16}
+    if x.dim() == 3 and x.dtype in _dtypes:
+        t, h, d = x.shape
+        ld, sh, sd = x.stride()
+        if (sd == 1 or d <= 1) and (sh == d or h <= 1):
+            return x.data_ptr(), ld if t > 1 else max(ld, h * d), t, h, d, _dtypes[x.dtype]
+    raise ValueError(f"{what} must be fp32, fp16 or bf16 [rows][heads][head_dim] with its heads one after another")
+
+
+def _table(table, rows):
+    """Row distance of a page table, an int32 tensor [sessions][pages]."""
+    if table.dim() != 2 or table.dtype != sys.modules["torch"].int32 or table.shape[0] < rows:
+        raise ValueError(f"the page table must be int32 [sessions][pages], with {rows} sessions or more")
+    return _int(table.shape[1])
+
+
+def _plan(plan):
+    return None if plan is None else C.addressof(plan)
 
 
 _call = None
@@ -680,72 +727,24 @@ def kd_rope_plan(head_dim: int, theta: float, rot_dim=None, layout: int = KD_ROP
     return out
 
 
-_dtypes = None
-
-
-def _heads(x, what):
-    """(address, row distance, rows, heads, head_dim, dtype) of a tensor [rows][heads][head_dim] whose heads lie
-    one after another; rows may be further apart (a part of a fused projection)."""
-    global _dtypes
-    if _dtypes is None:
-        torch = sys.modules["torch"]
-        _dtypes = {torch.float32: KD_F32, torch.float16: KD_F16, torch.bfloat16: KD_BF16}
-    t, h, d = x.shape
-    ld, sh, sd = x.stride()
-    if (sd != 1 and d > 1) or (sh != d and h > 1) or x.dtype not in _dtypes:
-        raise ValueError(f"{what} must be fp32, fp16 or bf16 [rows][heads][head_dim] with its heads one after another")
-    return x.data_ptr(), ld if t > 1 else max(ld, h * d), t, h, d, _dtypes[x.dtype]
-
-
-def _table(table, rows):
-    """Row distance of a page table, an int32 tensor [sessions][pages]."""
-    if table.dim() != 2 or table.element_size() != 4 or table.is_floating_point() or table.shape[0] < rows:
-        raise ValueError(f"the page table must be int32 [sessions][pages], with {rows} sessions or more")
-    return table.shape[1]
-
-
 def kd_rope(plan: KdRopeTable, x, positions, out, stream=None):
     """Rotate x [tokens][heads][head_dim] by positions (device int32 [tokens]) into out, which may be x."""
-    px, ld, t, h, d, dtype = _heads(x, "x")
-    po, ld_out, *shape, out_dtype = _heads(out, "out")
-    if shape != [t, h, d] or out_dtype != dtype or d != plan.head_dim:
-        raise ValueError("x and out must be alike, in heads of the plan's head_dim")
-    if positions.numel() != t or positions.element_size() != 4 or positions.is_floating_point():
-        raise ValueError(f"expected {t} int32 positions")
-    _check((_call or _fast()).rope(C.addressof(plan), px, dtype, ld, positions, t, h, po, ld_out, stream))
-
-
-def _append(plan, k_new, v_new, planes, table, starts, counts, n_heads, n_kv_heads, head_dim, n_pages, page_size, q, q_out,
-            fault, stream):
-    pk, k_ld, rows, h, d, dtype = _heads(k_new, "k_new")
-    pv, v_ld, *shape = _heads(v_new, "v_new")
-    if shape != [rows, h, d, dtype] or (h, d) != (n_kv_heads, head_dim):
-        raise ValueError("k_new and v_new must be alike: [rows][n_kv_heads][head_dim]")
-    pq = po = None
-    q_ld = 0
-    if q is not None:
-        pq, q_ld, *shape = _heads(q, "q")
-        po, o_ld, *out = _heads(q_out, "q_out")
-        if shape != [rows, n_heads, d, dtype] or out != [rows, n_heads, d, KD_F32] or o_ld != n_heads * d:
-            raise ValueError("q must be [rows][n_heads][head_dim] of k_new's type, and q_out so in contiguous fp32")
-    _check((_call or _fast()).append(None if plan is None else C.addressof(plan), pk, k_ld, pv, v_ld, pq, q_ld, dtype, rows,
-                                     planes, table, _table(table, len(starts)), starts, counts, n_heads, n_kv_heads,
-                                     head_dim, n_pages, page_size, po, fault, stream))
+    _check((_call or _fast()).rope(plan, x, positions, out, stream))
 
 
 def kd_paged_append(plan, k_new, v_new, k_pages, v_pages, table, starts, counts, n_kv_heads: int, head_dim: int,
                     n_pages: int, page_size: int, q=None, q_out=None, n_heads: int = 0, fault=None, stream=None):
     """Append k_new (rotated by `plan`; None: as it is) and v_new [rows][n_kv_heads][head_dim] to a paged fp16 cache:
     session b's counts[b] rows at positions starts[b] on; q [rows][n_heads][head_dim] rotated into q_out (fp32)."""
-    _append(plan, k_new, v_new, (k_pages, v_pages), table, starts, counts, n_heads, n_kv_heads, head_dim, n_pages,
-            page_size, q, q_out, fault, stream)
+    _check((_call or _fast()).append(plan, k_new, v_new, (k_pages, v_pages), table, starts, counts, n_heads, n_kv_heads,
+                                     head_dim, n_pages, page_size, q, q_out, fault, stream))
 
 
 def kd_paged_append_q8(plan, k_new, v_new, k_quants, k_scales, v_quants, v_scales, table, starts, counts, n_kv_heads: int,
                        n_pages: int, page_size: int, q=None, q_out=None, n_heads: int = 0, fault=None, stream=None):
     """kd_paged_append to a Q8_0 cache of head_dim 128 (see include/kd.h)."""
-    _append(plan, k_new, v_new, (k_quants, k_scales, v_quants, v_scales), table, starts, counts, n_heads, n_kv_heads, 128,
-            n_pages, page_size, q, q_out, fault, stream)
+    _check((_call or _fast()).append(plan, k_new, v_new, (k_quants, k_scales, v_quants, v_scales), table, starts, counts,
+                                     n_heads, n_kv_heads, 128, n_pages, page_size, q, q_out, fault, stream))
 
 
 def kd_attn_paged_workspace_bytes(B: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -756,7 +755,7 @@ def kd_attn_paged_decode(q, k_pages, v_pages, table, lens, n_heads: int, n_kv_he
                          page_size: int, out, workspace, group_rows=None, group_prefix=None, fault=None, stream=None):
     """Attention of one query per session over a paged fp16 cache: session b sees its first lens[b] keys.  Sessions in
     order form groups of group_rows[g], whose first group_prefix[g] keys are shared and read once (see include/kd.h)."""
-    _check((_call or _fast()).paged(q, (k_pages, v_pages), table, _table(table, len(lens)), lens, group_rows, group_prefix,
+    _check((_call or _fast()).paged(q, (k_pages, v_pages), table, lens, group_rows, group_prefix,
                                     n_heads, n_kv_heads, head_dim, n_pages, page_size, out, workspace, fault, stream))
 
 
@@ -764,6 +763,6 @@ def kd_attn_paged_decode_q8(q, k_quants, k_scales, v_quants, v_scales, table, le
                             n_pages: int, page_size: int, out, workspace, group_rows=None, group_prefix=None, fault=None,
                             stream=None):
     """kd_attn_paged_decode over a Q8_0 cache of head_dim 128 (see include/kd.h)."""
-    _check((_call or _fast()).paged(q, (k_quants, k_scales, v_quants, v_scales), table, _table(table, len(lens)), lens,
+    _check((_call or _fast()).paged(q, (k_quants, k_scales, v_quants, v_scales), table, lens,
                                     group_rows, group_prefix, n_heads, n_kv_heads, 128, n_pages, page_size, out, workspace,
                                     fault, stream))

@@ -190,7 +190,7 @@ size_t kd_attn_paged_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_he
     using namespace kd;
     if (B < 1 || B > KD_PAGED_MAX_SEQS || !paged_shape(n_heads, n_kv_heads, head_dim, false) || n_kv_heads > PAGED_MAX_KV_HEADS) return 0;
     // of shared keys: two records for every query, and for as many as a CTA takes per CTA
-    const size_t shared = 2 * ((size_t)B * n_heads + (size_t)SHARED_MAX_CTAS * SHARED_QUERIES);
+    const size_t shared = B < 2 ? 0 : 2 * ((size_t)B * n_heads + (size_t)SHARED_MAX_CTAS * SHARED_QUERIES);
     return PAGED_HEAD_BYTES + (paged_records(B, n_kv_heads) * (n_heads / n_kv_heads) + shared) * PAGED_REC(head_dim) * sizeof(float);
 }
 

@@ -33,7 +33,6 @@ struct AppendArgs {
     int* fault;
     int table_ld, n_seqs, tokens, nh, nkv, n_pages, ps;
     int per, groups;    // heads of one warp, warps of a token
-    int vec;            // every input head starts on a multiple of 4 elements
     int rotate;
     RopeAngles<64> r;
     int start[KD_PAGED_MAX_SEQS], first[KD_PAGED_MAX_SEQS + 1];  // a session's first new position; its first new row
@@ -47,12 +46,46 @@ __device__ __forceinline__ float in_f(float x) { return x; }
 __device__ __forceinline__ float in_f(__half x) { return __half2float(x); }
 __device__ __forceinline__ float in_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-constexpr int APPEND_WARPS = 8;
+// Four codes q + 128, q = x / d in fp32 rounded half away from zero, within [-127, 127]; 0 for d = 0.
+// |x| <= 127 d but for a rounding.  x times the reciprocal of d is within 127 2^-22 = 3e-5 of the
+// rounded quotient, so where it lies farther than 6e-5 from the middle between two whole numbers
+// the nearest one is the quotient's, too; there, or for a d without a finite reciprocal, the
+// division decides (a thousandth of the warps: 61 us for 6340 rows of 16 heads with a division each, see
+// below for what is taken).
+__device__ __forceinline__ uint32_t q8_codes(const float (&x)[4], float d) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    const float2 rr = make_float2(r, r), big = make_float2(12582912.0f, 12582912.0f), back = make_float2(-12582912.0f, -12582912.0f);
+    const float2 y0 = f2_mul(make_float2(x[0], x[1]), rr), y1 = f2_mul(make_float2(x[2], x[3]), rr);
+    const float2 z0 = f2_add(y0, big), z1 = f2_add(y1, big);  // 1.5 2^23 + the nearest whole number: its low byte is there
+    const float2 minus = make_float2(-1.0f, -1.0f);
+    const float2 o0 = f2_fma(f2_add(z0, back), minus, y0), o1 = f2_fma(f2_add(z1, back), minus, y1);
+    const float off = fmaxf(fmaxf(fabsf(o0.x), fabsf(o0.y)), fmaxf(fabsf(o1.x), fabsf(o1.y)));
+    const float sum = __fadd_rn(__fadd_rn(o0.x, o0.y), __fadd_rn(o1.x, o1.y));  // NaN where one is
+    if (off < 0.49994f && sum == sum)
+        return __byte_perm(__byte_perm(__float_as_uint(z0.x), __float_as_uint(z0.y), 0x0040),
+                           __byte_perm(__float_as_uint(z1.x), __float_as_uint(z1.y), 0x0040), 0x5410) ^ 0x80808080u;
+    uint32_t code = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int q = d > 0.0f ? max(-127, min(127, (int)roundf(__fdiv_rn(x[e], d)))) : 0;
+        code |= (uint32_t)(q + 128) << (8 * e);
+    }
+    return code;
+}
 
-template <typename T, bool Q8, int HD>
-__global__ void __launch_bounds__(APPEND_WARPS * 32) paged_append_kernel(const __grid_constant__ AppendArgs a) {
+constexpr int APPEND_WARPS = 8;
+// Heads in flight per lane group: 16 registers of them.
+template <typename T>
+__host__ __device__ constexpr int append_flight() {
+    return 16 / (int)sizeof(T);
+}
+
+// VEC: every input head starts on a multiple of 4 elements.
+template <typename T, bool Q8, int HD, bool VEC>
+__global__ void __launch_bounds__(APPEND_WARPS * 32, 3) paged_append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int LANES = HD / 4, ROWS = 32 / LANES;  // lanes of a head, heads at a time
-    constexpr int U = 4;                              // of them in flight
+    constexpr int U = append_flight<T>();             // of them in flight
     __shared__ float2 tab[ROPE_TAB];
     __shared__ unsigned long long turns[64];
     if (threadIdx.x < ROPE_TAB) tab[threadIdx.x] = ROPE_COS[threadIdx.x];
@@ -61,11 +94,34 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) paged_append_kernel(const _
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t unit = (int64_t)blockIdx.x * APPEND_WARPS + warp;
-    const int token = (int)(unit / a.groups);
+    const int unit = blockIdx.x * APPEND_WARPS + warp;
+    const int token = unit / a.groups;
     if (token >= a.tokens) return;
     const int heads = 2 * a.nkv + a.nh;
-    const int h0 = (int)(unit - (int64_t)token * a.groups) * a.per, h1 = min(heads, h0 + a.per);
+    const int h0 = (unit - token * a.groups) * a.per, h1 = min(heads, h0 + a.per);
+    const int sub = lane / LANES, d = lane % LANES * 4;  // the head of the warp's, and the lane's dims d .. d + 3
+    auto source = [&](int h) -> const T* {
+        if (h < a.nkv) return (const T*)a.k + token * a.k_ld + (int64_t)h * HD;
+        if (h < 2 * a.nkv) return (const T*)a.v + token * a.v_ld + (int64_t)(h - a.nkv) * HD;
+        return (const T*)a.q + token * a.q_ld + (int64_t)(h - 2 * a.nkv) * HD;
+    };
+    Four<T> raw[U];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int hh = h + i * ROWS + sub;
+            if (hh < h1) {
+                const T* p = source(hh) + d;
+                if constexpr (VEC) {
+                    raw[i] = *reinterpret_cast<const Four<T>*>(p);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) raw[i].v[e] = p[e];
+                }
+            }
+        }
+    };
+    load(h0);
     // the token's session, its position and the row that it goes to
     int lo = 0, hi = a.n_seqs;  // first[lo] <= token < first[hi]
     while (hi - lo > 1) {
@@ -76,118 +132,91 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) paged_append_kernel(const _
     const int pos = a.start[lo] + (token - a.first[lo]);
     const int in_table = pos / a.ps, in_page = pos - in_table * a.ps;
     int page = -1;
-    if (h0 < 2 * a.nkv) {
-        page = a.table[(int64_t)lo * a.table_ld + in_table];
-        if ((unsigned)page >= (unsigned)a.n_pages) {
-            if (a.fault && lane == 0) *a.fault = 1;
-            page = -1;
-        }
-    }
-    const int sub = lane / LANES, d = lane % LANES * 4;  // the head of the warp's, and the lane's dims d .. d + 3
+    if (h0 < 2 * a.nkv) page = a.table[(int64_t)lo * a.table_ld + in_table];
 
-    float4 x[U], y[U];  // the lane's values, and their partners where no lane has them
     const int half = a.r.rot / 2;
     const bool turned = a.rotate && d < a.r.rot;
     const bool shuffles = half % 4 == 0;
     const int partner = lane + (a.r.pairs ? 0 : d < half ? half / 4 : -(half / 4));
-    auto source = [&](int h) -> const T* {
-        if (h < a.nkv) return (const T*)a.k + token * a.k_ld + (int64_t)h * HD;
-        if (h < 2 * a.nkv) return (const T*)a.v + token * a.v_ld + (int64_t)(h - a.nkv) * HD;
-        return (const T*)a.q + token * a.q_ld + (int64_t)(h - 2 * a.nkv) * HD;
-    };
-    auto load = [&](int h) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int hh = h + i * ROWS + sub;
-            if (hh >= h1) continue;
-            const T* p = source(hh);
-            if (a.vec) {
-                const Four<T> f = *reinterpret_cast<const Four<T>*>(p + d);
-                x[i] = make_float4(in_f(f.v[0]), in_f(f.v[1]), in_f(f.v[2]), in_f(f.v[3]));
-            } else {
-                x[i] = make_float4(in_f(p[d]), in_f(p[d + 1]), in_f(p[d + 2]), in_f(p[d + 3]));
-            }
-            if (turned && !a.r.pairs && !shuffles) {
-                float o[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = d + e < a.r.rot ? in_f(p[d + e < half ? d + e + half : d + e - half]) : 0.0f;
-                y[i] = make_float4(o[0], o[1], o[2], o[3]);
-            }
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < U; ++i) x[i] = y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    load(h0);
-    float2 c[4], s[4];
+    float ch[4], cl[4], sh[4], sl[4];  // the sines with the sign that they are added with
     if (turned) {
+        float2 c, s;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int pair = a.r.pairs ? (d + e) >> 1 : d + e < half ? d + e : d + e - half;
-            if (a.r.pairs && (e & 1)) {
-                c[e] = c[e - 1];
-                s[e] = s[e - 1];
-            } else {
-                rope_angle<true>(turns[min(pair, 63)], pos, a.r.mh, a.r.ml, tab, c[e], s[e]);
-            }
+            if (!a.r.pairs || !(e & 1)) rope_angle<true>(turns[min(pair, 63)], pos, a.r.mh, a.r.ml, tab, c, s);
+            const bool plus = a.r.pairs ? (e & 1) != 0 : d + e >= half;
+            ch[e] = c.x, cl[e] = c.y, sh[e] = plus ? s.x : -s.x, sl[e] = plus ? s.y : -s.y;
         }
     }
+    if ((unsigned)page >= (unsigned)a.n_pages) {
+        if (a.fault && h0 < 2 * a.nkv && lane == 0) *a.fault = 1;
+        page = -1;
+    }
     for (int h = h0; h < h1; h += U * ROWS) {
-        float4 out[U];
+        if (h > h0) load(h);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            float4 o = y[i];
-            if (!a.r.pairs && shuffles) {
-                o.x = __shfl_sync(FULL_MASK, x[i].x, partner);
-                o.y = __shfl_sync(FULL_MASK, x[i].y, partner);
-                o.z = __shfl_sync(FULL_MASK, x[i].z, partner);
-                o.w = __shfl_sync(FULL_MASK, x[i].w, partner);
-            } else if (a.r.pairs) {
-                o = make_float4(x[i].y, x[i].x, x[i].w, x[i].z);
-            }
+            if (h + i * ROWS >= h1) break;
             const int hh = h + i * ROWS + sub;
             const bool value = hh >= a.nkv && hh < 2 * a.nkv;
-            out[i] = x[i];
-            if (turned && !value) {
-                const float in[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, other[4] = {o.x, o.y, o.z, o.w};
-                float r[4];
+            float x[4], o[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float sign = (a.r.pairs ? (e & 1) != 0 : d + e >= half) ? 1.0f : -1.0f;
-                    r[e] = d + e < a.r.rot ? rope_turn<true>(in[e], other[e], c[e], s[e], sign) : in[e];
+            for (int e = 0; e < 4; ++e) x[e] = in_f(raw[i].v[e]);
+            if (a.rotate) {
+                if (a.r.pairs) {
+                    o[0] = x[1], o[1] = x[0], o[2] = x[3], o[3] = x[2];
+                } else if (shuffles) {
+                    if constexpr (sizeof(T) == 2) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(&raw[i]);
+                        uint2 r;
+                        r.x = __shfl_sync(FULL_MASK, w.x, partner);
+                        r.y = __shfl_sync(FULL_MASK, w.y, partner);
+                        const Four<T> f = *reinterpret_cast<const Four<T>*>(&r);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] = in_f(f.v[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] = __shfl_sync(FULL_MASK, x[e], partner);
+                    }
+                } else {
+                    const T* p = hh < h1 ? source(hh) : source(h0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = d + e < a.r.rot ? in_f(p[d + e < half ? d + e + half : d + e - half]) : 0.0f;
                 }
-                out[i] = make_float4(r[0], r[1], r[2], r[3]);
-            }
-        }
-        const int now = h;
-        if (h + U * ROWS < h1) load(h + U * ROWS);
+                if (turned && !value) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int hh = now + i * ROWS + sub;
-            const float4 o = out[i];
+                    for (int e = 0; e < 4; e += 2) {
+                        const float2 r = rope_turn2<true>(make_float2(x[e], x[e + 1]), make_float2(o[e], o[e + 1]),
+                                                          make_float2(ch[e], ch[e + 1]), make_float2(cl[e], cl[e + 1]),
+                                                          make_float2(sh[e], sh[e + 1]), make_float2(sl[e], sl[e + 1]));
+                        x[e] = d + e < a.r.rot ? r.x : x[e];
+                        x[e + 1] = d + e + 1 < a.r.rot ? r.y : x[e + 1];
+                    }
+                }
+            }
             uint32_t code = 0;
             __half scale{};
             if constexpr (Q8) {  // as q8_quant: 8 lanes hold a block
-                float m = fmaxf(fmaxf(fabsf(o.x), fabsf(o.y)), fmaxf(fabsf(o.z), fabsf(o.w)));
+                if (hh < 2 * a.nkv) {  // the whole warp's head
+                    float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
-                for (int b = 1; b < 8; b <<= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, b));
-                const float dd = __fdiv_rn(m, 127.0f);
-                scale = __float2half_rn(dd);
-                auto quant = [&](float v) -> uint32_t {
-                    return (uint32_t)((dd > 0.0f ? max(-127, min(127, (int)roundf(__fdiv_rn(v, dd)))) : 0) + 128);
-                };
-                code = quant(o.x) | quant(o.y) << 8 | quant(o.z) << 16 | quant(o.w) << 24;
+                    for (int b = 1; b < 8; b <<= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, b));
+                    const float dd = __fdiv_rn(m, 127.0f);
+                    scale = __float2half_rn(dd);
+                    code = q8_codes(x, dd);
+                }
             }
             if (hh >= h1) continue;
             if (hh >= 2 * a.nkv) {
-                *reinterpret_cast<float4*>(a.q_out + ((int64_t)token * a.nh + hh - 2 * a.nkv) * HD + d) = o;
+                *reinterpret_cast<float4*>(a.q_out + ((int64_t)token * a.nh + hh - 2 * a.nkv) * HD + d) = make_float4(x[0], x[1], x[2], x[3]);
             } else if (page >= 0) {
-                const bool value = hh >= a.nkv;
                 const int64_t row = ((int64_t)page * a.nkv + (value ? hh - a.nkv : hh)) * a.ps + in_page;
                 if constexpr (Q8) {
                     reinterpret_cast<uint32_t*>(value ? a.vp : a.kp)[row * (HD / 4) + lane] = code;
                     if ((lane & 7) == 0) (value ? a.vs : a.ks)[row * (HD / 32) + (lane >> 3)] = scale;
                 } else {
-                    const __half2 w0 = __floats2half2_rn(o.x, o.y), w1 = __floats2half2_rn(o.z, o.w);
+                    const __half2 w0 = __floats2half2_rn(x[0], x[1]), w1 = __floats2half2_rn(x[2], x[3]);
                     *reinterpret_cast<uint2*>((__half*)(value ? a.vp : a.kp) + row * HD + d) =
                         make_uint2(*reinterpret_cast<const uint32_t*>(&w0), *reinterpret_cast<const uint32_t*>(&w1));
                 }
@@ -199,12 +228,14 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) paged_append_kernel(const _
 template <typename T>
 static cudaError_t launch_append(AppendArgs& a, bool q8, int hd, cudaStream_t s) {
     auto fours = [&](const void* p, int64_t ld) { return ((uintptr_t)p & (4 * sizeof(T) - 1)) == 0 && ld % 4 == 0; };
-    a.vec = fours(a.k, a.k_ld) && fours(a.v, a.v_ld) && (!a.nh || fours(a.q, a.q_ld));
-    // Heads of a warp: as many as leave every SM some forty warps (the angles are formed once for them).
-    const int heads = 2 * a.nkv + a.nh;
-    int64_t per = (int64_t)a.tokens * heads / (152 * 48);
-    per = per < 4 ? 4 : per > heads ? heads : (per + 3) / 4 * 4;
-    a.per = (int)per;
+    const bool vec = fours(a.k, a.k_ld) && fours(a.v, a.v_ld) && (!a.nh || fours(a.q, a.q_ld));
+    // Heads of a warp: as many as leave every SM some forty warps (the angles are formed once for
+    // them), whole flights where it has several.
+    constexpr int U = append_flight<T>();
+    const int heads = 2 * a.nkv + a.nh, rows = hd == 64 ? 2 : 1;
+    int64_t per = (int64_t)a.tokens * heads / (152 * 40);
+    per = per < rows ? rows : per < U * rows ? per / rows * rows : per / (U * rows) * (U * rows);
+    a.per = (int)(per < heads ? per : heads);
     a.groups = (heads + a.per - 1) / a.per;
     const int64_t units = (int64_t)a.tokens * a.groups;
     cudaLaunchConfig_t cfg = {};
@@ -216,9 +247,13 @@ static cudaError_t launch_append(AppendArgs& a, bool q8, int hd, cudaStream_t s)
     cfg.gridDim = dim3((unsigned)((units + APPEND_WARPS - 1) / APPEND_WARPS));
     cfg.blockDim = dim3(APPEND_WARPS * 32);
     cfg.stream = s;
-    if (q8) return cudaLaunchKernelEx(&cfg, paged_append_kernel<T, true, 128>, a);
-    return hd == 64 ? cudaLaunchKernelEx(&cfg, paged_append_kernel<T, false, 64>, a)
-                    : cudaLaunchKernelEx(&cfg, paged_append_kernel<T, false, 128>, a);
+#define KD_APPEND(VEC_)                                                                                                       \
+    return q8 ? cudaLaunchKernelEx(&cfg, paged_append_kernel<T, true, 128, VEC_>, a)                                          \
+              : hd == 64 ? cudaLaunchKernelEx(&cfg, paged_append_kernel<T, false, 64, VEC_>, a)                               \
+                         : cudaLaunchKernelEx(&cfg, paged_append_kernel<T, false, 128, VEC_>, a)
+    if (vec) KD_APPEND(true);
+    KD_APPEND(false);
+#undef KD_APPEND
 }
 
 static kd_status append_call(const char* fn, bool q8, const kd_rope_table* rope, const void* k, int64_t k_ld, const void* v,

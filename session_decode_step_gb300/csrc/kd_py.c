@@ -11,7 +11,7 @@
 
 #include "kd.h"
 
-static PyObject *s_is_contiguous, *s_data_ptr, *s_nbytes;
+static PyObject *s_is_contiguous, *s_data_ptr, *s_nbytes, *s_shape, *s_stride, *s_dtype, *s_numel;
 static PyObject *h_ptr, *h_i32, *h_stream; /* _ptr, _i32, _stream */
 
 /* Address of a contiguous tensor, an int, or None (0); anything else through _ptr. */
@@ -248,21 +248,148 @@ static int get_i64(PyObject* o, int64_t* out) {
     return 0;
 }
 
-/* table, x, dtype, ld, positions, n_tokens, n_heads, out, ld_out, stream */
+/* torch's types, known once it is loaded (a tensor is at hand then). */
+static PyObject *t_f32, *t_f16, *t_bf16, *t_i32;
+static int find_types(void) {
+    PyObject* torch;
+    if (t_i32) return 0;
+    torch = PyImport_ImportModule("torch");
+    if (!torch) return -1;
+    t_f32 = PyObject_GetAttrString(torch, "float32");
+    t_f16 = PyObject_GetAttrString(torch, "float16");
+    t_bf16 = PyObject_GetAttrString(torch, "bfloat16");
+    t_i32 = PyObject_GetAttrString(torch, "int32");
+    Py_DECREF(torch);
+    return t_f32 && t_f16 && t_bf16 && t_i32 ? 0 : -1;
+}
+
+/* A tuple of n integers, the attribute `name` of o or what its method of that name returns (0: as many, -1: an error, 1: not n). */
+static int get_sizes(PyObject* o, PyObject* name, int method, Py_ssize_t n, int64_t* out) {
+    PyObject* v = method ? PyObject_CallMethodNoArgs(o, name) : PyObject_GetAttr(o, name);
+    Py_ssize_t i;
+    if (!v) return -1;
+    if (!PyTuple_Check(v) || PyTuple_GET_SIZE(v) != n) {
+        Py_DECREF(v);
+        return 1;
+    }
+    for (i = 0; i < n; ++i)
+        if (get_i64(PyTuple_GET_ITEM(v, i), &out[i]) < 0) {
+            Py_DECREF(v);
+            return -1;
+        }
+    Py_DECREF(v);
+    return 0;
+}
+static int is_type(PyObject* o, PyObject* want) { /* the tensor's type; -1: an error */
+    PyObject* v = PyObject_GetAttr(o, s_dtype);
+    if (!v) return -1;
+    Py_DECREF(v); /* torch keeps its types */
+    return v == want;
+}
+
+/* A tensor [rows][heads][head_dim] whose heads lie one after another; rows may be further apart. */
+typedef struct {
+    void* p;
+    int64_t ld, rows, heads, dim;
+    int32_t dtype;
+} Heads;
+static int get_heads(PyObject* o, const char* what, Heads* h) {
+    int64_t n[3], st[3];
+    PyObject* v;
+    int r;
+    if (find_types() < 0) return -1;
+    if ((r = get_sizes(o, s_shape, 0, 3, n)) < 0 || (!r && (r = get_sizes(o, s_stride, 1, 3, st)) < 0)) return -1;
+    if (!r) {
+        v = PyObject_GetAttr(o, s_dtype);
+        if (!v) return -1;
+        Py_DECREF(v);
+        h->dtype = v == t_f32 ? KD_F32 : v == t_f16 ? KD_F16 : v == t_bf16 ? KD_BF16 : -1;
+        r = h->dtype < 0 || (st[2] != 1 && n[2] > 1) || (st[1] != n[2] && n[1] > 1);
+    }
+    if (r) {
+        PyErr_Format(PyExc_ValueError, "%s must be fp32, fp16 or bf16 [rows][heads][head_dim] with its heads one after another", what);
+        return -1;
+    }
+    h->rows = n[0];
+    h->heads = n[1];
+    h->dim = n[2];
+    h->ld = n[0] > 1 || st[0] > n[1] * n[2] ? st[0] : n[1] * n[2];
+    v = PyObject_CallMethodNoArgs(o, s_data_ptr);
+    if (!v) return -1;
+    h->p = PyLong_AsVoidPtr(v);
+    Py_DECREF(v);
+    return h->p == NULL && PyErr_Occurred() ? -1 : 0;
+}
+static int alike(const Heads* a, const Heads* b) {
+    return a->rows == b->rows && a->heads == b->heads && a->dim == b->dim && a->dtype == b->dtype;
+}
+
+/* An int32 tensor [at least rows][pages]. */
+static int get_table(PyObject* o, int32_t rows, void** p, int32_t* ld) {
+    int64_t n[2];
+    int r, ok;
+    if (find_types() < 0 || (r = get_sizes(o, s_shape, 0, 2, n)) < 0 || (ok = is_type(o, t_i32)) < 0) return -1;
+    if (r || !ok || n[0] < rows || n[1] > INT32_MAX) {
+        PyErr_Format(PyExc_ValueError, "the page table must be int32 [sessions][pages], with %d sessions or more", (int)rows);
+        return -1;
+    }
+    *ld = (int32_t)n[1];
+    return get_ptr(o, p);
+}
+
+/* A kd_rope_table (a ctypes structure), or None. */
+static int get_rope(PyObject* o, Py_buffer* b, const kd_rope_table** out) {
+    *out = NULL;
+    b->obj = NULL;
+    if (o == Py_None) return 0;
+    if (PyObject_GetBuffer(o, b, PyBUF_SIMPLE) < 0) return -1;
+    if ((size_t)b->len < sizeof(kd_rope_table)) {
+        PyBuffer_Release(b);
+        PyErr_SetString(PyExc_TypeError, "expected the table that kd_rope_plan returns");
+        return -1;
+    }
+    *out = b->buf;
+    return 0;
+}
+
+/* plan, x, positions, out, stream */
 static PyObject* py_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    void *table, *x, *pos, *out, *st;
-    int32_t dtype, tokens, heads;
-    int64_t ld, ld_out;
+    const kd_rope_table* table;
+    Py_buffer plan;
+    Heads x, out;
+    PyObject *r = NULL, *v;
+    void *pos, *st;
+    int64_t count;
+    int ok;
     kd_status s;
     (void)self;
-    if (arity("kd_rope", n, 10) < 0 || get_ptr(a[0], &table) < 0 || get_ptr(a[1], &x) < 0 || get_i32(a[2], &dtype) < 0 ||
-        get_i64(a[3], &ld) < 0 || get_ptr(a[4], &pos) < 0 || get_i32(a[5], &tokens) < 0 || get_i32(a[6], &heads) < 0 ||
-        get_ptr(a[7], &out) < 0 || get_i64(a[8], &ld_out) < 0 || get_stream(a[9], &st) < 0)
-        return NULL;
+    if (arity("kd_rope", n, 5) < 0 || get_rope(a[0], &plan, &table) < 0) return NULL;
+    if (get_heads(a[1], "x", &x) < 0 || get_heads(a[3], "out", &out) < 0) goto done;
+    if (!alike(&x, &out) || (table && x.dim != table->head_dim)) {
+        PyErr_SetString(PyExc_ValueError, "x and out must be alike, in heads of the plan's head_dim");
+        goto done;
+    }
+    if (x.rows > INT32_MAX || x.heads > INT32_MAX) {
+        PyErr_SetString(PyExc_OverflowError, "too many rows");
+        goto done;
+    }
+    v = PyObject_CallMethodNoArgs(a[2], s_numel);
+    if (!v) goto done;
+    ok = get_i64(v, &count);
+    Py_DECREF(v);
+    if (ok < 0 || (ok = is_type(a[2], t_i32)) < 0) goto done;
+    if (!ok || count != x.rows) {
+        PyErr_Format(PyExc_ValueError, "expected %lld int32 positions", (long long)x.rows);
+        goto done;
+    }
+    if (get_ptr(a[2], &pos) < 0 || get_stream(a[4], &st) < 0) goto done;
     Py_BEGIN_ALLOW_THREADS
-    s = kd_rope(table, x, dtype, ld, pos, tokens, heads, out, ld_out, st);
+    s = kd_rope(table, x.p, x.dtype, x.ld, pos, (int32_t)x.rows, (int32_t)x.heads, out.p, out.ld, st);
     Py_END_ALLOW_THREADS
-    return PyLong_FromLong(s);
+    r = PyLong_FromLong(s);
+done:
+    if (plan.obj) PyBuffer_Release(&plan);
+    return r;
 }
 
 /* The planes of a cache, 2 (fp16 rows) or 4 (Q8_0). */
@@ -284,52 +411,65 @@ static int get_planes(PyObject* o, void** p) {
     return (int)n;
 }
 
-/* rope, k, k_ld, v, v_ld, q, q_ld, dtype, rows, planes, table, table_ld, starts, counts, n_heads, n_kv_heads, head_dim,
- * n_pages, page_size, q_out, fault, stream */
+/* plan, k_new, v_new, planes, table, starts, counts, n_heads, n_kv_heads, head_dim, n_pages, page_size, q, q_out, fault,
+ * stream */
 static PyObject* py_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    void *rope, *x[3], *p[4], *table, *q_out, *fault, *st;
-    int64_t ld[3], rows, sum = 0;
-    int32_t dtype, table_ld, v[5], B = 0;
+    const kd_rope_table* rope;
+    Py_buffer plan;
+    Heads k, v, q = {.p = NULL}, q_out = {.p = NULL};
+    void *p[4], *table, *fault, *st;
+    int64_t sum = 0;
+    int32_t table_ld, c[5], B = 0;
     Ints starts = {.held = 0}, counts = {.held = 0};
     PyObject* r = NULL;
     int i, planes, below = 0;
     kd_status s;
     (void)self;
-    if (arity("kd_paged_append", n, 22) < 0 || get_ptr(a[0], &rope) < 0) return NULL;
-    for (i = 0; i < 3; ++i)
-        if (get_ptr(a[1 + 2 * i], &x[i]) < 0 || get_i64(a[2 + 2 * i], &ld[i]) < 0) return NULL;
-    if (get_i32(a[7], &dtype) < 0 || get_i64(a[8], &rows) < 0 || (planes = get_planes(a[9], p)) < 0 ||
-        get_ptr(a[10], &table) < 0 || get_i32(a[11], &table_ld) < 0)
-        return NULL;
-    if (get_ints(a[12], &starts, -1, &B) < 0 || get_ints(a[13], &counts, B, NULL) < 0) goto done;
+    if (arity("kd_paged_append", n, 16) < 0 || get_rope(a[0], &plan, &rope) < 0) return NULL;
+    if (get_heads(a[1], "k_new", &k) < 0 || get_heads(a[2], "v_new", &v) < 0 || (planes = get_planes(a[3], p)) < 0) goto done;
     for (i = 0; i < 5; ++i)
-        if (get_i32(a[14 + i], &v[i]) < 0) goto done;
-    if (get_ptr(a[19], &q_out) < 0 || get_ptr(a[20], &fault) < 0 || get_stream(a[21], &st) < 0) goto done;
-    for (i = 0; i < B; ++i) {
-        const int32_t c = ((const int32_t*)counts.b.buf)[i];
-        below |= c < 0;
-        sum += c;
+        if (get_i32(a[7 + i], &c[i]) < 0) goto done;
+    if (!alike(&k, &v) || k.heads != c[1] || k.dim != c[2]) {
+        PyErr_SetString(PyExc_ValueError, "k_new and v_new must be alike: [rows][n_kv_heads][head_dim]");
+        goto done;
     }
-    if (!below && sum != rows) {
-        PyErr_Format(PyExc_ValueError, "%lld new rows for counts of %lld in all", (long long)rows, (long long)sum);
+    if (a[12] != Py_None) {
+        if (get_heads(a[12], "q", &q) < 0 || get_heads(a[13], "q_out", &q_out) < 0) goto done;
+        if (q.rows != k.rows || q.heads != c[0] || q.dim != c[2] || q.dtype != k.dtype || q_out.rows != k.rows ||
+            q_out.heads != c[0] || q_out.dim != c[2] || q_out.dtype != KD_F32 || q_out.ld != q.heads * q.dim) {
+            PyErr_SetString(PyExc_ValueError, "q must be [rows][n_heads][head_dim] of k_new's type, and q_out so in contiguous fp32");
+            goto done;
+        }
+    }
+    if (get_ints(a[5], &starts, -1, &B) < 0 || get_ints(a[6], &counts, B, NULL) < 0 || get_table(a[4], B, &table, &table_ld) < 0 ||
+        get_ptr(a[14], &fault) < 0 || get_stream(a[15], &st) < 0)
+        goto done;
+    for (i = 0; i < B; ++i) {
+        const int32_t count = ((const int32_t*)counts.b.buf)[i];
+        below |= count < 0;
+        sum += count;
+    }
+    if (!below && sum != k.rows) {
+        PyErr_Format(PyExc_ValueError, "%lld new rows for counts of %lld in all", (long long)k.rows, (long long)sum);
         goto done;
     }
     Py_BEGIN_ALLOW_THREADS
     if (planes == 2)
-        s = kd_paged_append(rope, x[0], ld[0], x[1], ld[1], x[2], ld[2], dtype, p[0], p[1], table, table_ld, starts.b.buf,
-                            counts.b.buf, B, v[0], v[1], v[2], v[3], v[4], q_out, fault, st);
+        s = kd_paged_append(rope, k.p, k.ld, v.p, v.ld, q.p, q.ld, k.dtype, p[0], p[1], table, table_ld, starts.b.buf, counts.b.buf,
+                            B, c[0], c[1], c[2], c[3], c[4], q_out.p, fault, st);
     else
-        s = kd_paged_append_q8(rope, x[0], ld[0], x[1], ld[1], x[2], ld[2], dtype, p[0], p[1], p[2], p[3], table, table_ld,
-                               starts.b.buf, counts.b.buf, B, v[0], v[1], v[3], v[4], q_out, fault, st);
+        s = kd_paged_append_q8(rope, k.p, k.ld, v.p, v.ld, q.p, q.ld, k.dtype, p[0], p[1], p[2], p[3], table, table_ld,
+                               starts.b.buf, counts.b.buf, B, c[0], c[1], c[3], c[4], q_out.p, fault, st);
     Py_END_ALLOW_THREADS
     r = PyLong_FromLong(s);
 done:
+    if (plan.obj) PyBuffer_Release(&plan);
     drop(&starts);
     drop(&counts);
     return r;
 }
 
-/* q, planes, table, table_ld, lens, group_rows, group_prefix, n_heads, n_kv_heads, head_dim, n_pages, page_size, out,
+/* q, planes, table, lens, group_rows, group_prefix, n_heads, n_kv_heads, head_dim, n_pages, page_size, out,
  * workspace, fault, stream */
 static PyObject* py_paged(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     void *q, *p[4], *table, *out, *ws, *fault, *st;
@@ -340,20 +480,18 @@ static PyObject* py_paged(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     int i, planes;
     kd_status s;
     (void)self;
-    if (arity("kd_attn_paged_decode", n, 16) < 0 || get_ptr(a[0], &q) < 0 || (planes = get_planes(a[1], p)) < 0 ||
-        get_ptr(a[2], &table) < 0 || get_i32(a[3], &table_ld) < 0)
-        return NULL;
-    if (get_ints(a[4], &lens, -1, &B) < 0) goto done;
-    if (a[5] != Py_None && get_ints(a[5], &rows, -1, &G) < 0) goto done;
-    if (a[6] != Py_None && get_ints(a[6], &prefix, G, NULL) < 0) goto done;
-    if (a[6] == Py_None && G > 0) {
+    if (arity("kd_attn_paged_decode", n, 15) < 0 || get_ptr(a[0], &q) < 0 || (planes = get_planes(a[1], p)) < 0) return NULL;
+    if (get_ints(a[3], &lens, -1, &B) < 0 || get_table(a[2], B, &table, &table_ld) < 0) goto done;
+    if (a[4] != Py_None && get_ints(a[4], &rows, -1, &G) < 0) goto done;
+    if (a[5] != Py_None && get_ints(a[5], &prefix, G, NULL) < 0) goto done;
+    if (a[5] == Py_None && G > 0) {
         PyErr_SetString(PyExc_ValueError, "groups without prefixes");
         goto done;
     }
     for (i = 0; i < 5; ++i)
-        if (get_i32(a[7 + i], &v[i]) < 0) goto done;
-    if (get_ptr(a[12], &out) < 0 || get_ptr(a[13], &ws) < 0 || get_nbytes(a[13], &bytes) < 0 || get_ptr(a[14], &fault) < 0 ||
-        get_stream(a[15], &st) < 0)
+        if (get_i32(a[6 + i], &v[i]) < 0) goto done;
+    if (get_ptr(a[11], &out) < 0 || get_ptr(a[12], &ws) < 0 || get_nbytes(a[12], &bytes) < 0 || get_ptr(a[13], &fault) < 0 ||
+        get_stream(a[14], &st) < 0)
         goto done;
     Py_BEGIN_ALLOW_THREADS
     if (planes == 2)
@@ -401,6 +539,10 @@ PyMODINIT_FUNC PyInit__kdcall(void) {
     s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_nbytes = PyUnicode_InternFromString("nbytes");
-    if (!s_is_contiguous || !s_data_ptr || !s_nbytes) return NULL;
+    s_shape = PyUnicode_InternFromString("shape");
+    s_stride = PyUnicode_InternFromString("stride");
+    s_dtype = PyUnicode_InternFromString("dtype");
+    s_numel = PyUnicode_InternFromString("numel");
+    if (!s_is_contiguous || !s_data_ptr || !s_nbytes || !s_shape || !s_stride || !s_dtype || !s_numel) return NULL;
     return PyModule_Create(&module);
 }

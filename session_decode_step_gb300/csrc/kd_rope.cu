@@ -44,7 +44,7 @@ __device__ __forceinline__ void from_f(float x, __nv_bfloat16& o) { o = __float2
 constexpr int ROPE_THREADS = 256;
 
 template <typename T, bool PAIRS, int P>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(ROPE_THREADS, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
     using V = RopeVec<T, P>;
     constexpr bool EXACT = std::is_same<T, float>::value;
     constexpr int U = 4;  // heads in flight
@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constan
     // the two vectors of the thread's pairs
     const int d0 = PAIRS ? 2 * P * chunk : P * chunk, d1 = PAIRS ? d0 + P : d0 + a.r.rot / 2;
     const int pos = a.pos[token];
+    float ch[P], cl[P], sh[P], sl[P];
     V u[U], w[U];
     auto load = [&](int h) {
 #pragma unroll
@@ -82,32 +83,49 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constan
             }
     };
     load(h0);
-    float2 c[P], s[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) rope_angle<EXACT>(turns[P * chunk + i], pos, a.r.mh, a.r.ml, tab, c[i], s[i]);
+    for (int i = 0; i < P; ++i) {
+        float2 c, s;
+        rope_angle<EXACT>(turns[P * chunk + i], pos, a.r.mh, a.r.ml, tab, c, s);
+        ch[i] = c.x, cl[i] = c.y, sh[i] = s.x, sl[i] = s.y;
+    }
+    // Elements e and e + 1 of the two vectors in a row (PAIRS), or of one (HALF, with the other's).
+    auto turn = [&](V& a0, V& a1) {
+        if constexpr (PAIRS) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {  // pair i: elements 2i, 2i + 1 of the row of both vectors
+                T &lo = 2 * i < P ? a0.v[2 * i < P ? 2 * i : 0] : a1.v[2 * i >= P ? 2 * i - P : 0];
+                T &hi = 2 * i + 1 < P ? a0.v[2 * i + 1 < P ? 2 * i + 1 : 0] : a1.v[2 * i + 1 >= P ? 2 * i + 1 - P : 0];
+                const float p = to_f(lo), q = to_f(hi);
+                const float2 r = rope_turn2<EXACT>(make_float2(p, q), make_float2(q, p), make_float2(ch[i], ch[i]),
+                                                   make_float2(cl[i], cl[i]), make_float2(-sh[i], sh[i]), make_float2(-sl[i], sl[i]));
+                from_f(r.x, lo);
+                from_f(r.y, hi);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+                constexpr int last = P - 1;
+                const int k = i + 1 < P ? i + 1 : last;  // P = 1: the same again
+                const float2 p = make_float2(to_f(a0.v[i]), to_f(a0.v[k])), q = make_float2(to_f(a1.v[i]), to_f(a1.v[k]));
+                const float2 c = make_float2(ch[i], ch[k]), s = make_float2(sh[i], sh[k]);
+                const float2 c2 = make_float2(cl[i], cl[k]), s2 = make_float2(sl[i], sl[k]);
+                const float2 rp = rope_turn2<EXACT>(p, q, c, c2, f2_neg(s), f2_neg(s2)), rq = rope_turn2<EXACT>(q, p, c, c2, s, s2);
+                from_f(rp.x, a0.v[i]);
+                from_f(rp.y, a0.v[k]);
+                from_f(rq.x, a1.v[i]);
+                from_f(rq.y, a1.v[k]);
+            }
+        }
+    };
     for (int h = h0; h < h1; h += U) {
-        V y[U], z[U];
+        if (h > h0) load(h);
 #pragma unroll
         for (int k = 0; k < U; ++k)
             if (h + k < h1) {
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    // pair i: HALF u[i], w[i]; PAIRS elements 2i and 2i + 1 of u and w in a row
-                    auto at = [&](int e) -> float { return e < P ? to_f(u[k].v[e < P ? e : 0]) : to_f(w[k].v[e >= P ? e - P : 0]); };
-                    const float p = PAIRS ? at(2 * i) : to_f(u[k].v[i]), q = PAIRS ? at(2 * i + 1) : to_f(w[k].v[i]);
-                    const float rp = rope_turn<EXACT>(p, q, c[i], s[i], -1.0f), rq = rope_turn<EXACT>(q, p, c[i], s[i], 1.0f);
-                    auto put = [&](int e, float v) { from_f(v, e < P ? y[k].v[e < P ? e : 0] : z[k].v[e >= P ? e - P : 0]); };
-                    put(PAIRS ? 2 * i : i, rp);
-                    put(PAIRS ? 2 * i + 1 : P + i, rq);
-                }
-            }
-        const int now = h;
-        if (h + U < h1) load(h + U);
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (now + k < h1) {
-                *reinterpret_cast<V*>(out + (int64_t)(now + k) * a.hd + d0) = y[k];
-                *reinterpret_cast<V*>(out + (int64_t)(now + k) * a.hd + d1) = z[k];
+                turn(u[k], w[k]);
+                *reinterpret_cast<V*>(out + (int64_t)(h + k) * a.hd + d0) = u[k];
+                *reinterpret_cast<V*>(out + (int64_t)(h + k) * a.hd + d1) = w[k];
             }
     }
 }

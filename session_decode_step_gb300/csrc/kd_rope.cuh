@@ -102,15 +102,49 @@ __device__ __forceinline__ void rope_cos_sin(uint64_t phase, const float2* tab, 
     if (q >= 2) s = make_float2(-s.x, -s.y);
 }
 
-// x cos - y sin (sign -1) or x cos + y sin (sign 1), rounded to fp32 once (EXACT) or
-// to within two roundings.
+// Two fp32 operations in one.
+__device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 f2_mul(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 f2_neg(float2 a) { return make_float2(-a.x, -a.y); }
+
+// Two results x c + y s at a time (the sign of the sine is the caller's); each of c and s the
+// sum of its two parts.  EXACT: rounded to fp32 once, up to about 2^-44 (products and the sum with
+// what their roundings left out); else to within two roundings, of the first parts alone.
 template <bool EXACT>
-__device__ __forceinline__ float rope_turn(float x, float y, float2 c, float2 s, float sign) {
-    if constexpr (!EXACT) return __fmaf_rn(x, c.x, __fmul_rn(__fmul_rn(sign, y), s.x));
-    const float2 p = two_prod(x, c.x), q = two_prod(__fmul_rn(sign, y), s.x), t = two_sum(p.x, q.x);
-    const float lo = __fadd_rn(__fadd_rn(t.y, __fadd_rn(p.y, q.y)), __fmaf_rn(x, c.y, __fmul_rn(__fmul_rn(sign, y), s.y)));
-    const float v = __fadd_rn(t.x, lo);
-    return fabsf(t.x) <= 3.402823466e38f ? v : t.x;  // infinite or NaN: as the plain sum has it
+__device__ __forceinline__ float2 rope_turn2(float2 x, float2 y, float2 ch, float2 cl, float2 sh, float2 sl) {
+    if constexpr (!EXACT) return f2_fma(x, ch, f2_mul(y, sh));
+    const float2 p = f2_mul(x, ch), q = f2_mul(y, sh), t = f2_add(p, q);
+    const float2 pe = f2_fma(x, ch, f2_neg(p)), qe = f2_fma(y, sh, f2_neg(q));
+    const float2 minus = make_float2(-1.0f, -1.0f);
+    const float2 b = f2_fma(p, minus, t);  // what of t is q, and what either is off by
+    const float2 te = f2_add(f2_fma(f2_fma(b, minus, t), minus, p), f2_fma(b, minus, q));
+    const float2 lo = f2_add(f2_add(te, f2_add(pe, qe)), f2_fma(x, cl, f2_mul(y, sl)));
+    float2 v = f2_add(t, lo);
+    if (!(fmaxf(fabsf(t.x), fabsf(t.y)) <= 3.402823466e38f)) {  // infinite: as the plain sum has it
+        if (!(fabsf(t.x) <= 3.402823466e38f)) v.x = t.x;
+        if (!(fabsf(t.y) <= 3.402823466e38f)) v.y = t.y;
+    }
+    return v;
 }
 
 // The table's entries for a launch: N of the plan's, and the magnitude as an fp32 pair.

@@ -278,7 +278,7 @@ def test_binding_append(calls):
 def test_binding_attention(calls):
     pages = torch.zeros(4, 2, 16, 64, dtype=torch.float16)
     q, out = torch.zeros(2, 4, 64), torch.zeros(2, 256, dtype=torch.float16)
-    tab, ws = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(1 << 22, dtype=torch.uint8)
+    tab, ws = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(kd.kd_attn_paged_workspace_bytes(2, 4, 2, 64), dtype=torch.uint8)
 
     def call(lens=(5, 6), tab=tab, ws=ws, **kw):
         kd.kd_attn_paged_decode(q, pages, pages, tab, lens, 4, 2, 64, 4, 16, out, ws, **kw)
