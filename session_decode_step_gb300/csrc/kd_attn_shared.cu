@@ -150,7 +150,7 @@ struct SharedSeg {
     }
 };
 
-template <int HD>
+template <int HD, bool Q8>
 __global__ void __launch_bounds__(SH_THREADS, 1)
     shared_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     using L = SharedSmem<HD>;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(full + i, 1);
+            mbar_init(full + i, Q8 ? SH_SOFT / 2 : 1);
             mbar_init(empty + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -190,8 +190,10 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         for (int i = 0; i < SH_SOFT / 2; ++i) mbar_init(pair + i, 2);
         mbar_init_fence();
         *failed = 0;
-        prefetch_tmap(&tmk);
-        prefetch_tmap(&tmv);
+        if (!Q8) {
+            prefetch_tmap(&tmk);
+            prefetch_tmap(&tmv);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -208,6 +210,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     auto n_queries = [&](const SharedSeg& s) { return min(SHARED_QUERIES, a.queries[s.g] - first_query(s)); };
 
     if (warp == SH_COPY) {
+        if constexpr (!Q8) {
         // ---- copies: K and V of each tile, boxes of whole 16-key runs within a page
         uint32_t slot = 0, phase = 0, tiles = 0;
         bool ok = true;
@@ -255,13 +258,16 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             }
         }
         if (!ok && lane == 0) *failed = 1;
+        }
     } else if (warp == SH_SCORES || warp == SH_VALUES) {
         // ---- products, S = Q K^T and O += P V by a thread each: one that has issued products
         // goes on only when the tensor core has taken them (1200 cycles for a tile's), and the other's
         // should be ready then.  K parts are in the buffers' even places of a round, V parts in the odd ones.
         if (lane == 0) {
             const bool values = warp == SH_VALUES;
-            uint32_t slot = values, phase = 0, q_phase = 0;
+            // buffers of a tile's K or V: one, or with Q8_0 the two parts of the pairs
+            constexpr int PARTS = Q8 ? 2 : 1;
+            uint32_t place = values ? PARTS : 0, q_phase = 0;
             unsigned half_phase = 0;  // of p_full (values) or pv_done (scores), a bit for each half of the softmax warps
             bool ok = true;
             const uint32_t qs = smem_u32(smem + L::Q), ring = smem_u32(smem + L::RING);
@@ -279,37 +285,39 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                     const int w = j & 1, n = min(SHARED_TILE, keys - (s.tile + j) * SHARED_TILE);
                     // weights that are there; or, for scores, weights in their place that are done with
                     if (values || j >= 2) ok = mbar_wait_bounded((values ? p_full : pv_done) + w, (half_phase >> w) & 1);
-                    ok = ok && mbar_wait_bounded(full + slot, phase);
+                    uint32_t slot[PARTS];
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) {
+                        slot[i] = (place + i) % NS;
+                        ok = ok && mbar_wait_bounded(full + slot[i], ((place + i) / NS) & 1);
+                    }
+                    place += 2 * PARTS;
                     if (!ok) break;
                     if (values || j >= 2) half_phase ^= 1u << w;
                     tc_fence_after();
-                    const uint32_t part0 = ring + slot * L::TILE;
+                    // hi hi, lo hi, hi lo (what is left out is 2^-22 of a product)
                     if (!values) {
                         const uint32_t id = tc_idesc(n, false);
 #pragma unroll
-                        for (int part = 0; part < 2; ++part)
+                        for (int part = 0; part < 1 + PARTS; ++part)
 #pragma unroll
                             for (int k = 0; k < HD / 16; ++k) {
                                 const uint32_t off = (k / 4) * L::COL + (k % 4) * 32;
-                                tc_mma_ss(tmem + w * 128, tc_desc(qs + part * L::TILE + off, 0), tc_desc(part0 + off, 0), id, part || k);
+                                tc_mma_ss(tmem + w * 128, tc_desc(qs + (part == 1 ? L::TILE : 0) + off, 0),
+                                          tc_desc(ring + slot[part / 2] * L::TILE + off, 0), id, part || k);
                             }
                         tc_commit(s_full + w);
-                        tc_commit(empty + slot);
                     } else {
                         const uint32_t id = tc_idesc(HD, true);
                         for (int k = 0; k < n / 16; ++k)
 #pragma unroll
-                            for (int part = 0; part < 2; ++part)
-                                tc_mma_ts(tmem + 256 + w * HD, tmem + w * 128 + 32 * (k / 2) + 16 * part + 8 * (k & 1),
-                                          tc_desc(part0 + k * 2048, L::COL), id, part || k || j >= 2);
+                            for (int part = 0; part < 1 + PARTS; ++part)
+                                tc_mma_ts(tmem + 256 + w * HD, tmem + w * 128 + 32 * (k / 2) + (part == 1 ? 16 : 0) + 8 * (k & 1),
+                                          tc_desc(ring + slot[part / 2] * L::TILE + k * 2048, L::COL), id, part || k || j >= 2);
                         tc_commit(pv_done + w);
-                        tc_commit(empty + slot);
                     }
-                    slot += 2;
-                    if (slot >= NS) {
-                        slot -= NS;
-                        phase ^= 1;
-                    }
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) tc_commit(empty + slot[i]);
                 }
                 // The last products of a half are not waited for here: keep its count.
                 if (!values) half_phase ^= (s.n > 0 ? 1u : 0u) | (s.n > 1 ? 2u : 0u);
@@ -337,6 +345,73 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             return maxima[(half ^ 1) * SHARED_QUERIES + r];
         };
         SharedSeg s;
+        // Q8_0: the group of warps that will weigh tile j of the segment makes its K and V, codes times
+        // scales as fp16 pairs hi + lo (19 bits, so exactly): thread t takes 16 codes of rows t / 8 + 32 i.
+        auto convert = [&](int j) {
+            const int t = threadIdx.x & 255, chunk = t & 7, key0 = (s.tile + j) * SHARED_TILE, keys = a.keys[s.g];
+            const int* row = a.table + (int64_t)a.lead[s.g] * a.table_ld;
+            int64_t at[4];
+            unsigned have = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = key0 + (t >> 3) + 32 * i;
+                at[i] = -1;
+                if (key < keys) {
+                    const int page = row[key / a.ps];
+                    if ((unsigned)page < (unsigned)a.n_pages)
+                        at[i] = ((int64_t)page * a.nkv + s.h) * a.ps + key % a.ps;
+                    else if (a.fault)
+                        *a.fault = 1;
+                }
+                // the warp's rows of i are of one 16-key run; warps 0 .. 3 of the group have runs 2i, 4 .. 7 runs 2i + 1
+                have |= (at[i] >= 0 ? 1u : 0u) << (2 * i + ((t >> 7) & 1));
+            }
+            const uint32_t T = tiles + j;
+            if ((t & 127) == 0) runs[(T & 7) * 2 + (t >> 7)] = (uint8_t)have;
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                const uint8_t* codes = part ? a.vq : a.kq;
+                const __half* scales = part ? a.vs : a.ks;
+                uint4 v[4];
+                __half d[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // 0
+                    d[i] = __ushort_as_half(0);
+                    if (at[i] >= 0) {
+                        v[i] = ldg_nc_v4(codes + at[i] * 128 + 16 * chunk);
+                        d[i] = __ldg(scales + at[i] * 4 + (chunk >> 1));
+                    }
+                }
+#pragma unroll
+                for (int lo = 0; lo < 2; ++lo) {
+                    const uint32_t place = 4 * T + 2 * part + lo, slot = place % NS;
+                    if (!__all_sync(FULL_MASK, mbar_wait_bounded(empty + slot, ((place / NS) & 1) ^ 1))) return false;
+                    uint8_t* dst = smem + L::RING + slot * L::TILE + (chunk >> 2) * L::COL;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = (t >> 3) + 32 * i;
+                        const __half2 dd = __half2half2(d[i]);
+                        auto two = [&](uint32_t q) {
+                            const __half2 codes = *reinterpret_cast<const __half2*>(&q);
+                            __half2 h = __hmul2_rn(codes, dd);
+                            if (lo) h = __hfma2(codes, dd, __hneg2(h));
+                            return *reinterpret_cast<const uint32_t*>(&h);
+                        };
+                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            *reinterpret_cast<uint4*>(dst + r * 128 + (((2 * (chunk & 3) + k) ^ (r & 7)) << 4)) =
+                                make_uint4(two(u8x2_lo_to_half2(w[2 * k])), two(u8x2_hi_to_half2(w[2 * k])),
+                                           two(u8x2_lo_to_half2(w[2 * k + 1])), two(u8x2_hi_to_half2(w[2 * k + 1])));
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full + slot);
+                }
+            }
+            return true;
+        };
         for (int x = x0; x < x1 && ok;) {
             s.at(a, x, x1 - x);
             x += s.n;
@@ -365,13 +440,20 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             const bool idle = (warp & 3) * 32 >= nq;  // no query in the warp's rows: what its weights hold does not matter
             float m = -INFINITY;                      // the maximum that the weights are taken against, in units of 1 / c
             float2 l = make_float2(0.0f, 0.0f);
+            if constexpr (Q8) ok = s.n <= w || convert(w);
             for (int j = w; j < s.n && ok; j += 2) {
                 // the thread's keys of the tile, and their 16-key runs with a page
                 const int n = min(64, keys - (s.tile + j) * SHARED_TILE - half * 64);
                 ok = __all_sync(FULL_MASK, mbar_wait_bounded(s_full + w, ss++ & 1));
                 if (!ok) break;
                 tc_fence_after();
-                const unsigned have = runs[(tiles + j) & 7] >> (half * 4);
+                unsigned have;
+                if constexpr (Q8) {
+                    const uint32_t e = ((tiles + j) & 7) * 2;
+                    have = (unsigned)(runs[e] | runs[e + 1]) >> (half * 4);
+                } else {
+                    have = runs[(tiles + j) & 7] >> (half * 4);
+                }
                 if (!idle) {
                     const bool all = n == 64 && (have & 15) == 15;
                     uint32_t v[32];  // 32 keys' scores
@@ -441,6 +523,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + w);
+                if constexpr (Q8) ok = j + 2 >= s.n || convert(j + 2);
             }
             tiles += s.n;
             // ---- the half's record of the segment's tiles
@@ -491,16 +574,18 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
 // ---- launch ----------------------------------------------------------------------
 cudaError_t encode_fp16_2d(CUtensorMap* out, const void* base, long inner, long rows, int box_inner, int box_rows);
 
-template <int HD>
-static cudaError_t launch_shared_hd(const SharedArgs& a, const __half* k, const __half* v, int dev, cudaStream_t s) {
+template <int HD, bool Q8>
+static cudaError_t launch_shared_as(const SharedArgs& a, const void* k, const void* v, int dev, cudaStream_t s) {
     static OncePerDevice once;
     cudaError_t e = once(dev, [] {
-        return cudaFuncSetAttribute(shared_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, SharedSmem<HD>::TOTAL);
+        return cudaFuncSetAttribute(shared_kernel<HD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SharedSmem<HD>::TOTAL);
     });
     if (e != cudaSuccess) return e;
-    CUtensorMap mk, mv;
-    if ((e = encode_fp16_2d(&mk, k, HD, a.rows, 64, a.box_runs * 16)) != cudaSuccess) return e;
-    if ((e = encode_fp16_2d(&mv, v, HD, a.rows, 64, a.box_runs * 16)) != cudaSuccess) return e;
+    CUtensorMap mk = {}, mv = {};
+    if (!Q8) {
+        if ((e = encode_fp16_2d(&mk, k, HD, a.rows, 64, a.box_runs * 16)) != cudaSuccess) return e;
+        if ((e = encode_fp16_2d(&mv, v, HD, a.rows, 64, a.box_runs * 16)) != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -511,11 +596,12 @@ static cudaError_t launch_shared_hd(const SharedArgs& a, const __half* k, const 
     cfg.blockDim = dim3(SH_THREADS);
     cfg.dynamicSmemBytes = SharedSmem<HD>::TOTAL;
     cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, shared_kernel<HD>, a, mk, mv);
+    return cudaLaunchKernelEx(&cfg, shared_kernel<HD, Q8>, a, mk, mv);
 }
 
-cudaError_t launch_shared(const SharedArgs& a, int hd, const __half* k, const __half* v, int dev, cudaStream_t s) {
-    return hd == 64 ? launch_shared_hd<64>(a, k, v, dev, s) : launch_shared_hd<128>(a, k, v, dev, s);
+cudaError_t launch_shared(const SharedArgs& a, int hd, bool q8, const void* k, const void* v, int dev, cudaStream_t s) {
+    if (q8) return launch_shared_as<128, true>(a, k, v, dev, s);
+    return hd == 64 ? launch_shared_as<64, false>(a, k, v, dev, s) : launch_shared_as<128, false>(a, k, v, dev, s);
 }
 
 }  // namespace kd

@@ -68,6 +68,8 @@ struct SharedArgs {
     const int* table;
     float* part;
     int* fault;
+    const uint8_t *kq, *vq;  // Q8_0: quants and scales
+    const __half *ks, *vs;
     int* status;  // [CTA]: 1 where a bounded wait ran out
     int table_ld, n_pages, ps, rows, box_runs, nh, nkv, gq, n_groups, side, sets;
     float scale;
@@ -85,7 +87,7 @@ __host__ __device__ inline int64_t shared_row(const SharedArgs& a, int g, int h,
     const int pass_queries = SHARED_QUERIES * a.side;
     return (int64_t)a.before[g] * a.nkv + (int64_t)h * a.queries[g] + (int64_t)pass * pass_queries + (int64_t)set * pass_queries + query;
 }
-cudaError_t launch_shared(const SharedArgs& a, int hd, const __half* k, const __half* v, int dev, cudaStream_t s);
+cudaError_t launch_shared(const SharedArgs& a, int hd, bool q8, const void* k, const void* v, int dev, cudaStream_t s);
 
 // CTAs of the kernel that device dev, the current one, holds at once (0 on a CUDA error, left in *e).
 int paged_slots(int hd, int group, bool q8, int dev, int num_sms, cudaError_t* e);

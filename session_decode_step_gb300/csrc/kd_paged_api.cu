@@ -94,8 +94,8 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
             if (group_rows[g] < 1 || group_rows[g] > B - b)
                 return failf(KD_ERR_INVALID_ARG, "%s: group %d of %d sessions", fn, g, group_rows[g]);
             const int shared = group_prefix[g] / ps * ps;  // the page that the prefix ends in is each session's own
-            const bool once = !q8 && group_rows[g] > 1 && shared > 0 &&
-                              (int64_t)(group_rows[g] - 1) * shared * nkv * hd * 4 >= SHARED_SAVES;
+            const bool once = group_rows[g] > 1 && shared > 0 &&
+                              (int64_t)(group_rows[g] - 1) * shared * nkv * (q8 ? 272 : hd * 4) >= SHARED_SAVES;
             for (int i = b; i < b + group_rows[g]; ++i) {
                 if (group_prefix[g] < 0 || group_prefix[g] > lens[i])
                     return failf(KD_ERR_POSITION, "%s: prefix %d of a session of length %d", fn, group_prefix[g], lens[i]);
@@ -175,7 +175,11 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
         sh.scale = a.scale;
         shared_plan(sh, sms);
         a.late_wait = 1;
-        KD_TRY(launch_shared(sh, hd, (const __half*)kp, (const __half*)vp, dev, s));
+        sh.kq = (const uint8_t*)kp;
+        sh.vq = (const uint8_t*)vp;
+        sh.ks = a.ks;
+        sh.vs = a.vs;
+        KD_TRY(launch_shared(sh, hd, q8, kp, vp, dev, s));
     }
     KD_TRY(launch_paged(a, hd, q8, true, s));
     if (merge) KD_TRY(launch_paged_merge(a, sh, hd, true, s));
