@@ -132,6 +132,10 @@ struct SharedSmem {
     static_assert(TOTAL <= 227 * 1024, "opt-in shared memory");
 };
 
+// Q8_0: the first of the two places, counted on round the buffers, of K (part 0) or V (1) of a CTA's tile t: in
+// the order K0 K1 V0 K2 V1 K3 V2 ..., as V is made when its tile has been weighed, and then the K after next.
+__device__ __forceinline__ uint32_t shared_place(uint32_t t, int part) { return 2 * (part ? 2 * t + 2 : t ? 2 * t - 1 : 0); }
+
 // A CTA's next tiles of one (group, KV head, pass).
 struct SharedSeg {
     int g = 0, h, pass, tile, n;  // tiles [tile, tile + n)
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             const bool values = warp == SH_VALUES;
             // buffers of a tile's K or V: one, or with Q8_0 the two parts of the pairs
             constexpr int PARTS = Q8 ? 2 : 1;
-            uint32_t place = values ? PARTS : 0, q_phase = 0;
+            uint32_t place = values, tile = 0, q_phase = 0;
             unsigned half_phase = 0;  // of p_full (values) or pv_done (scores), a bit for each half of the softmax warps
             bool ok = true;
             const uint32_t qs = smem_u32(smem + L::Q), ring = smem_u32(smem + L::RING);
@@ -285,13 +289,14 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                     const int w = j & 1, n = min(SHARED_TILE, keys - (s.tile + j) * SHARED_TILE);
                     // weights that are there; or, for scores, weights in their place that are done with
                     if (values || j >= 2) ok = mbar_wait_bounded((values ? p_full : pv_done) + w, (half_phase >> w) & 1);
+                    if constexpr (Q8) place = shared_place(tile++, values);
                     uint32_t slot[PARTS];
 #pragma unroll
                     for (int i = 0; i < PARTS; ++i) {
                         slot[i] = (place + i) % NS;
                         ok = ok && mbar_wait_bounded(full + slot[i], ((place + i) / NS) & 1);
                     }
-                    place += 2 * PARTS;
+                    place += 2;  // fp16: K and V parts lie in turn
                     if (!ok) break;
                     if (values || j >= 2) half_phase ^= 1u << w;
                     tc_fence_after();
@@ -345,70 +350,64 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             return maxima[(half ^ 1) * SHARED_QUERIES + r];
         };
         SharedSeg s;
-        // Q8_0: the group of warps that will weigh tile j of the segment makes its K and V, codes times
-        // scales as fp16 pairs hi + lo (19 bits, so exactly): thread t takes 16 codes of rows t / 8 + 32 i.
-        auto convert = [&](int j) {
+        // Q8_0: the group of warps that weighs tile j of the segment makes its K (part 0) and V (1), codes
+        // times scales as fp16 pairs hi + lo (19 bits, so exactly): thread t takes 16 codes of rows t / 8 + 32 i.
+        auto convert = [&](int j, int part) {
             const int t = threadIdx.x & 255, chunk = t & 7, key0 = (s.tile + j) * SHARED_TILE, keys = a.keys[s.g];
             const int* row = a.table + (int64_t)a.lead[s.g] * a.table_ld;
-            int64_t at[4];
+            const uint8_t* codes = part ? a.vq : a.kq;
+            const __half* scales = part ? a.vs : a.ks;
             unsigned have = 0;
+            uint4 v[4];
+            __half d[4];
+            int page[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int key = key0 + (t >> 3) + 32 * i;
-                at[i] = -1;
-                if (key < keys) {
-                    const int page = row[key / a.ps];
-                    if ((unsigned)page < (unsigned)a.n_pages)
-                        at[i] = ((int64_t)page * a.nkv + s.h) * a.ps + key % a.ps;
-                    else if (a.fault)
-                        *a.fault = 1;
+                page[i] = key < keys ? row[key / a.ps] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = key0 + (t >> 3) + 32 * i;
+                const bool good = key < keys && (unsigned)page[i] < (unsigned)a.n_pages;
+                if (key < keys && !good && a.fault) *a.fault = 1;
+                v[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // 0
+                d[i] = __ushort_as_half(0);
+                if (good) {
+                    const int64_t at = ((int64_t)page[i] * a.nkv + s.h) * a.ps + key % a.ps;
+                    v[i] = ldg_nc_v4(codes + at * 128 + 16 * chunk);
+                    d[i] = __ldg(scales + at * 4 + (chunk >> 1));
                 }
                 // the warp's rows of i are of one 16-key run; warps 0 .. 3 of the group have runs 2i, 4 .. 7 runs 2i + 1
-                have |= (at[i] >= 0 ? 1u : 0u) << (2 * i + ((t >> 7) & 1));
+                have |= (good ? 1u : 0u) << (2 * i + ((t >> 7) & 1));
             }
             const uint32_t T = tiles + j;
-            if ((t & 127) == 0) runs[(T & 7) * 2 + (t >> 7)] = (uint8_t)have;
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                const uint8_t* codes = part ? a.vq : a.kq;
-                const __half* scales = part ? a.vs : a.ks;
-                uint4 v[4];
-                __half d[4];
+            if (!part && (t & 127) == 0) runs[(T & 7) * 2 + (t >> 7)] = (uint8_t)have;
+#pragma unroll 1
+            for (int lo = 0; lo < 2; ++lo) {
+                const uint32_t place = shared_place(T, part) + lo, slot = place % NS;
+                if (!__all_sync(FULL_MASK, mbar_wait_bounded(empty + slot, ((place / NS) & 1) ^ 1))) return false;
+                uint8_t* dst = smem + L::RING + slot * L::TILE + (chunk >> 2) * L::COL;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    v[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // 0
-                    d[i] = __ushort_as_half(0);
-                    if (at[i] >= 0) {
-                        v[i] = ldg_nc_v4(codes + at[i] * 128 + 16 * chunk);
-                        d[i] = __ldg(scales + at[i] * 4 + (chunk >> 1));
-                    }
+                    const int r = (t >> 3) + 32 * i;
+                    const __half2 dd = __half2half2(d[i]);
+                    auto two = [&](uint32_t q) {
+                        const __half2 codes = *reinterpret_cast<const __half2*>(&q);
+                        __half2 h = __hmul2_rn(codes, dd);
+                        if (lo) h = __hfma2(codes, dd, __hneg2(h));
+                        return *reinterpret_cast<const uint32_t*>(&h);
+                    };
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<uint4*>(dst + r * 128 + (((2 * (chunk & 3) + k) ^ (r & 7)) << 4)) =
+                            make_uint4(two(u8x2_lo_to_half2(w[2 * k])), two(u8x2_hi_to_half2(w[2 * k])),
+                                       two(u8x2_lo_to_half2(w[2 * k + 1])), two(u8x2_hi_to_half2(w[2 * k + 1])));
                 }
-#pragma unroll
-                for (int lo = 0; lo < 2; ++lo) {
-                    const uint32_t place = 4 * T + 2 * part + lo, slot = place % NS;
-                    if (!__all_sync(FULL_MASK, mbar_wait_bounded(empty + slot, ((place / NS) & 1) ^ 1))) return false;
-                    uint8_t* dst = smem + L::RING + slot * L::TILE + (chunk >> 2) * L::COL;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = (t >> 3) + 32 * i;
-                        const __half2 dd = __half2half2(d[i]);
-                        auto two = [&](uint32_t q) {
-                            const __half2 codes = *reinterpret_cast<const __half2*>(&q);
-                            __half2 h = __hmul2_rn(codes, dd);
-                            if (lo) h = __hfma2(codes, dd, __hneg2(h));
-                            return *reinterpret_cast<const uint32_t*>(&h);
-                        };
-                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            *reinterpret_cast<uint4*>(dst + r * 128 + (((2 * (chunk & 3) + k) ^ (r & 7)) << 4)) =
-                                make_uint4(two(u8x2_lo_to_half2(w[2 * k])), two(u8x2_hi_to_half2(w[2 * k])),
-                                           two(u8x2_lo_to_half2(w[2 * k + 1])), two(u8x2_hi_to_half2(w[2 * k + 1])));
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full + slot);
-                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + slot);
             }
             return true;
         };
@@ -440,7 +439,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             const bool idle = (warp & 3) * 32 >= nq;  // no query in the warp's rows: what its weights hold does not matter
             float m = -INFINITY;                      // the maximum that the weights are taken against, in units of 1 / c
             float2 l = make_float2(0.0f, 0.0f);
-            if constexpr (Q8) ok = s.n <= w || convert(w);
+            if constexpr (Q8) ok = s.n <= w || convert(w, 0);
             for (int j = w; j < s.n && ok; j += 2) {
                 // the thread's keys of the tile, and their 16-key runs with a page
                 const int n = min(64, keys - (s.tile + j) * SHARED_TILE - half * 64);
@@ -523,7 +522,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + w);
-                if constexpr (Q8) ok = j + 2 >= s.n || convert(j + 2);
+                if constexpr (Q8) ok = convert(j, 1) && (j + 2 >= s.n || convert(j + 2, 0));
             }
             tiles += s.n;
             // ---- the half's record of the segment's tiles
