@@ -569,7 +569,6 @@ __global__ void __launch_bounds__(PAGED_MERGE_WARPS * 32) paged_merge_kernel(con
         pairs = sh.part + shared_row(sh, g, h, pass, c0, query - pass * per) * 2 * REC;
         set_step = (size_t)per * 2 * REC;
     }
-    pdl_launch_dependents();
     pdl_wait();
     if (sh.n_groups && qh == 0 && b == 0 && warp == PAGED_MERGE_WARPS - 1) {  // the call's fault word
         int bad = 0;
@@ -639,6 +638,7 @@ __global__ void __launch_bounds__(PAGED_MERGE_WARPS * 32) paged_merge_kernel(con
         for (int k = 1; k < PAGED_MERGE_WARPS; ++k) o = __fadd_rn(o, sums[k][d]);
         a.out[((size_t)b * a.nh + qh) * HD + d] = __float2half_rn(__fdiv_rn(o, denom));
     }
+    pdl_launch_dependents();
 }
 
 #define KD_PAGED_GROUPS(HD_, Q8_, MACRO)             \
