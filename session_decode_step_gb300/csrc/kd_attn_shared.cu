@@ -115,6 +115,10 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, int n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
 // ---- the kernel ---------------------------------------------------------------
 constexpr int SH_SOFT = 16;                     // softmax warps: two groups of eight, two warps a quarter of the rows
 constexpr int SH_COPY = SH_SOFT, SH_SCORES = SH_SOFT + 1, SH_VALUES = SH_SOFT + 2;  // the copies' and the products' warps
@@ -350,68 +354,115 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             return maxima[(half ^ 1) * SHARED_QUERIES + r];
         };
         SharedSeg s;
-        // Q8_0: the group of warps that weighs tile j of the segment makes its K (part 0) and V (1), codes
-        // times scales as fp16 pairs hi + lo (19 bits, so exactly): thread t takes 16 codes of rows t / 8 + 32 i.
-        auto convert = [&](int j, int part) {
-            const int t = threadIdx.x & 255, chunk = t & 7, key0 = (s.tile + j) * SHARED_TILE, keys = a.keys[s.g];
-            const int* row = a.table + (int64_t)a.lead[s.g] * a.table_ld;
-            const uint8_t* codes = part ? a.vq : a.kq;
-            const __half* scales = part ? a.vs : a.ks;
-            unsigned have = 0;
+        // Q8_0: eight warps make K (part 0) and V (1) of tile j of the segment, codes times scales as
+        // fp16 pairs hi + lo (19 bits, so exactly): thread t takes 16 codes of rows t / 8 + 32 i.  Where no group
+        // has more than 64 queries the warps of the upper 64 rows do nothing else; else the group of warps that
+        // weighs the tile does it in between.
+        const bool makes = Q8 && a.narrow && (warp & 2);
+        const int t = makes ? ((warp >> 2) * 2 + (warp & 1)) * 32 + lane : threadIdx.x & 255, chunk = t & 7;
+        struct Codes {
             uint4 v[4];
             __half d[4];
-            int page[4];
+        };
+        // Lane i < 8: the first cache row of run i of tile j (-1: there is none).
+        auto look_up = [&](const SharedSeg& s, int j) {
+            const int key = (s.tile + j) * SHARED_TILE + 16 * lane;
+            if (lane >= 8 || key >= a.keys[s.g]) return -1;
+            const int in_table = key / a.ps, page = a.table[(int64_t)a.lead[s.g] * a.table_ld + in_table];
+            if ((unsigned)page < (unsigned)a.n_pages) return (page * a.nkv + s.h) * a.ps + key - in_table * a.ps;
+            if (a.fault) *a.fault = 1;
+            return -1;
+        };
+        auto fetch = [&](int rows, int part, uint32_t T, Codes& f) {
+            const uint8_t* codes = (part ? a.vq : a.kq) + 16 * chunk;
+            const __half* scales = (part ? a.vs : a.ks) + (chunk >> 1);
+            const unsigned have = __ballot_sync(FULL_MASK, rows >= 0);
+            if (!part && t == 0) runs[T & 7] = (uint8_t)have;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // the warp's rows of i are of one run
+                const int first = __shfl_sync(FULL_MASK, rows, 2 * i + (t >> 7));
+                f.v[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // 0
+                f.d[i] = __ushort_as_half(0);
+                if (first >= 0) {
+                    const int64_t at = first + ((t >> 3) & 15);
+                    f.v[i] = ldg_nc_v4(codes + at * 128);
+                    f.d[i] = __ldg(scales + at * 4);
+                }
+            }
+        };
+        auto make = [&](int part, uint32_t T, const Codes& f) {
+            const uint32_t place = shared_place(T, part), s0 = place % NS, s1 = (place + 1) % NS;
+            const bool free = mbar_wait_bounded(empty + s0, ((place / NS) & 1) ^ 1) && mbar_wait_bounded(empty + s1, (((place + 1) / NS) & 1) ^ 1);
+            if (!__all_sync(FULL_MASK, free)) return false;
+            uint8_t* dst = smem + L::RING + (chunk >> 2) * L::COL + (t >> 3) * 128;
+            const uint32_t c0 = ((2 * (chunk & 3)) ^ ((t >> 3) & 7)) << 4;  // the second 8 dims are 16 bytes away in it
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int key = key0 + (t >> 3) + 32 * i;
-                page[i] = key < keys ? row[key / a.ps] : 0;
-            }
+                const __half2 dd = __half2half2(f.d[i]);
+                const uint32_t w[4] = {f.v[i].x, f.v[i].y, f.v[i].z, f.v[i].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = key0 + (t >> 3) + 32 * i;
-                const bool good = key < keys && (unsigned)page[i] < (unsigned)a.n_pages;
-                if (key < keys && !good && a.fault) *a.fault = 1;
-                v[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // 0
-                d[i] = __ushort_as_half(0);
-                if (good) {
-                    const int64_t at = ((int64_t)page[i] * a.nkv + s.h) * a.ps + key % a.ps;
-                    v[i] = ldg_nc_v4(codes + at * 128 + 16 * chunk);
-                    d[i] = __ldg(scales + at * 4 + (chunk >> 1));
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t q = (e & 1) ? u8x2_hi_to_half2(w[2 * k + (e >> 1)]) : u8x2_lo_to_half2(w[2 * k + (e >> 1)]);
+                        const __half2 c = *reinterpret_cast<const __half2*>(&q), h = __hmul2_rn(c, dd), l = __hfma2(c, dd, __hneg2(h));
+                        hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+                        lo[e] = *reinterpret_cast<const uint32_t*>(&l);
+                    }
+                    uint8_t* at = dst + i * 32 * 128 + (c0 ^ (k << 4));
+                    *reinterpret_cast<uint4*>(at + s0 * L::TILE) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(at + s1 * L::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                // the warp's rows of i are of one 16-key run; warps 0 .. 3 of the group have runs 2i, 4 .. 7 runs 2i + 1
-                have |= (good ? 1u : 0u) << (2 * i + ((t >> 7) & 1));
             }
-            const uint32_t T = tiles + j;
-            if (!part && (t & 127) == 0) runs[(T & 7) * 2 + (t >> 7)] = (uint8_t)have;
-#pragma unroll 1
-            for (int lo = 0; lo < 2; ++lo) {
-                const uint32_t place = shared_place(T, part) + lo, slot = place % NS;
-                if (!__all_sync(FULL_MASK, mbar_wait_bounded(empty + slot, ((place / NS) & 1) ^ 1))) return false;
-                uint8_t* dst = smem + L::RING + slot * L::TILE + (chunk >> 2) * L::COL;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = (t >> 3) + 32 * i;
-                    const __half2 dd = __half2half2(d[i]);
-                    auto two = [&](uint32_t q) {
-                        const __half2 codes = *reinterpret_cast<const __half2*>(&q);
-                        __half2 h = __hmul2_rn(codes, dd);
-                        if (lo) h = __hfma2(codes, dd, __hneg2(h));
-                        return *reinterpret_cast<const uint32_t*>(&h);
-                    };
-                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        *reinterpret_cast<uint4*>(dst + r * 128 + (((2 * (chunk & 3) + k) ^ (r & 7)) << 4)) =
-                            make_uint4(two(u8x2_lo_to_half2(w[2 * k])), two(u8x2_hi_to_half2(w[2 * k])),
-                                       two(u8x2_lo_to_half2(w[2 * k + 1])), two(u8x2_hi_to_half2(w[2 * k + 1])));
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full + slot);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(full + s0);
+                mbar_arrive(full + s1);
             }
             return true;
         };
-        for (int x = x0; x < x1 && ok;) {
+        auto convert = [&](int j, int part) {
+            Codes f;
+            fetch(look_up(s, j), part, tiles + j, f);
+            return make(part, tiles + j, f);
+        };
+        if (makes) {
+            // the parts in the order of their places, a part's codes fetched while the one before is made
+            for (int x = x0; x < x1 && ok;) {
+                s.at(a, x, x1 - x);
+                x += s.n;
+                if (n_queries(s) <= 0) continue;
+                // part k of 2 n: K0 [K1] V0 K2 V1 .., V last
+                auto part_of = [&](int k, int& j, int& part) {
+                    part = s.n == 1 ? k : k >= 2 && (k == 2 * s.n - 1 || !(k & 1));
+                    j = k < 2 ? (s.n > 1 ? k : 0) : part ? (k == 2 * s.n - 1 ? s.n - 1 : k / 2 - 1) : (k + 1) / 2;
+                };
+                Codes now, next;
+                int newest = 0, before = look_up(s, 0), rows = before, ahead = s.n > 1 ? look_up(s, 1) : -1;  // of K `newest`, the one before, the next
+                fetch(rows, 0, tiles, now);
+                for (int k = 0; k < 2 * s.n && ok; ++k) {
+                    int j, part, j2, part2;
+                    part_of(k, j, part);
+                    if (k + 1 < 2 * s.n) {
+                        part_of(k + 1, j2, part2);
+                        if (!part2) {
+                            before = rows;
+                            rows = ahead;
+                            newest = j2;
+                        }
+                        fetch(part2 && j2 < newest ? before : rows, part2, tiles + j2, next);
+                        if (!part2 && j2 + 1 < s.n) ahead = look_up(s, j2 + 1);
+                    }
+                    ok = make(part, tiles + j, now);
+                    now = next;
+                }
+                tiles += s.n;
+            }
+        }
+        const int share = Q8 && a.narrow ? 2 : 1;  // arrivals of a warp: for one that makes K and V, too
+        for (int x = makes ? x1 : x0; x < x1 && ok;) {
             s.at(a, x, x1 - x);
             x += s.n;
             const int nq = n_queries(s), q0 = first_query(s);
@@ -434,25 +485,19 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
+                if (lane == 0) mbar_arrive_n(q_full, share);
             }
             const bool idle = (warp & 3) * 32 >= nq;  // no query in the warp's rows: what its weights hold does not matter
             float m = -INFINITY;                      // the maximum that the weights are taken against, in units of 1 / c
             float2 l = make_float2(0.0f, 0.0f);
-            if constexpr (Q8) ok = s.n <= w || convert(w, 0);
+            if constexpr (Q8) ok = a.narrow || s.n <= w || convert(w, 0);
             for (int j = w; j < s.n && ok; j += 2) {
                 // the thread's keys of the tile, and their 16-key runs with a page
                 const int n = min(64, keys - (s.tile + j) * SHARED_TILE - half * 64);
                 ok = __all_sync(FULL_MASK, mbar_wait_bounded(s_full + w, ss++ & 1));
                 if (!ok) break;
                 tc_fence_after();
-                unsigned have;
-                if constexpr (Q8) {
-                    const uint32_t e = ((tiles + j) & 7) * 2;
-                    have = (unsigned)(runs[e] | runs[e + 1]) >> (half * 4);
-                } else {
-                    have = runs[(tiles + j) & 7] >> (half * 4);
-                }
+                const unsigned have = runs[(tiles + j) & 7] >> (half * 4);
                 if (!idle) {
                     const bool all = n == 64 && (have & 15) == 15;
                     uint32_t v[32];  // 32 keys' scores
@@ -521,8 +566,8 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + w);
-                if constexpr (Q8) ok = convert(j, 1) && (j + 2 >= s.n || convert(j + 2, 0));
+                if (lane == 0) mbar_arrive_n(p_full + w, share);
+                if constexpr (Q8) ok = a.narrow || (convert(j, 1) && (j + 2 >= s.n || convert(j + 2, 0)));
             }
             tiles += s.n;
             // ---- the half's record of the segment's tiles
@@ -552,7 +597,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             }
             // All are done with the queries and with tensor memory.
             __syncwarp();
-            if (lane == 0) mbar_arrive(q_free);
+            if (lane == 0) mbar_arrive_n(q_free, share);
             ok = ok && __all_sync(FULL_MASK, mbar_wait_bounded(q_free, segs++ & 1));
         }
         if (!ok) *failed = 1;

@@ -72,6 +72,7 @@ struct SharedArgs {
     const __half *ks, *vs;
     int* status;  // [CTA]: 1 where a bounded wait ran out
     int table_ld, n_pages, ps, rows, box_runs, nh, nkv, gq, n_groups, side, sets;
+    int narrow;  // no group has more than 64 queries
     float scale;
     Shares share;  // of all tiles, among the sets
     int keys[SHARED_MAX_GROUPS], queries[SHARED_MAX_GROUPS];  // shared keys (whole pages), sessions times gq

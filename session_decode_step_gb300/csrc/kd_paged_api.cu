@@ -31,6 +31,9 @@ static void shared_plan(SharedArgs& t, int sms) {
     int most = 1;
     for (int g = 0; g < t.n_groups; ++g)
         if ((t.queries[g] + SHARED_QUERIES - 1) / SHARED_QUERIES > most) most = (t.queries[g] + SHARED_QUERIES - 1) / SHARED_QUERIES;
+    t.narrow = 1;
+    for (int g = 0; g < t.n_groups; ++g)
+        if (t.queries[g] > SHARED_QUERIES / 2) t.narrow = 0;
     for (int side = 1; side <= most && side <= SHARED_MAX_SIDE && side <= sms; ++side) {
         double work = 0;
         for (int g = 0; g < t.n_groups; ++g) {
