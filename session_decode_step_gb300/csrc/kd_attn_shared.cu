@@ -124,16 +124,21 @@ constexpr int SH_SOFT = 16;                     // softmax warps: two groups of 
 constexpr int SH_COPY = SH_SOFT, SH_SCORES = SH_SOFT + 1, SH_VALUES = SH_SOFT + 2;  // the copies' and the products' warps
 constexpr int SH_THREADS = (SH_SOFT + 3) * 32;
 
-template <int HD>
+// NARROW: at most 64 queries, whose rows alone are kept (the tensor core reads 128, and what it makes of
+// the others is not used); with 128-wide heads that leaves room for a sixth buffer.
+template <int HD, bool NARROW>
 struct SharedSmem {
     static constexpr int COLS = HD / 64;               // 128-byte columns of a row
     static constexpr int COL = SHARED_TILE * 128;      // one of a tile
-    static constexpr int TILE = COLS * COL;            // K or V of a tile, or a part of the queries
-    static constexpr int SLOTS = HD == 128 ? 5 : 8;
-    static constexpr int Q = 0, RING = 2 * TILE, BARS = RING + SLOTS * TILE;
+    static constexpr int TILE = COLS * COL;            // K or V of a tile
+    static constexpr int QROWS = NARROW ? SHARED_QUERIES / 2 : SHARED_QUERIES;
+    static constexpr int QCOL = QROWS * 128, QTILE = COLS * QCOL;  // the queries' columns, and one of their parts
+    static constexpr int SLOTS = HD == 64 ? 8 : NARROW ? 6 : 5;
+    static constexpr int Q = 0, RING = 2 * QTILE, BARS = RING + SLOTS * TILE;
     static constexpr int MAXIMA = BARS + 320;  // [group][half][row]: what the two warps of a row tell each other
     static constexpr int TOTAL = MAXIMA + 2 * 2 * SHARED_QUERIES * 4;
     static_assert(TOTAL <= 227 * 1024, "opt-in shared memory");
+    static_assert(QCOL <= TILE, "the rows read behind the queries are in the buffers");
 };
 
 // Q8_0: the first of the two places, counted on round the buffers, of K (part 0) or V (1) of a CTA's tile t: in
@@ -158,10 +163,10 @@ struct SharedSeg {
     }
 };
 
-template <int HD, bool Q8>
+template <int HD, bool Q8, bool NARROW>
 __global__ void __launch_bounds__(SH_THREADS, 1)
     shared_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
-    using L = SharedSmem<HD>;
+    using L = SharedSmem<HD, NARROW>;
     constexpr int NS = L::SLOTS;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -312,7 +317,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
 #pragma unroll
                             for (int k = 0; k < HD / 16; ++k) {
                                 const uint32_t off = (k / 4) * L::COL + (k % 4) * 32;
-                                tc_mma_ss(tmem + w * 128, tc_desc(qs + (part == 1 ? L::TILE : 0) + off, 0),
+                                tc_mma_ss(tmem + w * 128, tc_desc(qs + (part == 1 ? L::QTILE : 0) + (k / 4) * L::QCOL + (k % 4) * 32, 0),
                                           tc_desc(ring + slot[part / 2] * L::TILE + off, 0), id, part || k);
                             }
                         tc_commit(s_full + w);
@@ -355,11 +360,13 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         };
         SharedSeg s;
         // Q8_0: eight warps make K (part 0) and V (1) of tile j of the segment, codes times scales as
-        // fp16 pairs hi + lo (19 bits, so exactly): thread t takes 16 codes of rows t / 8 + 32 i.  Where no group
+        // fp16 pairs hi + lo (19 bits, so exactly): a thread takes 16 codes of rows trow + 32 i.  Where no group
         // has more than 64 queries the warps of the upper 64 rows do nothing else; else the group of warps that
         // weighs the tile does it in between.
-        const bool makes = Q8 && a.narrow && (warp & 2);
-        const int t = makes ? ((warp >> 2) * 2 + (warp & 1)) * 32 + lane : threadIdx.x & 255, chunk = t & 7;
+        const bool makes = Q8 && NARROW && (warp & 2);
+        const int t = makes ? ((warp >> 2) * 2 + (warp & 1)) * 32 + lane : threadIdx.x & 255;
+        // 8 lanes write 4 chunks of two rows, which the swizzle puts into different banks
+        const int chunk = (lane & 3) | ((lane >> 4) << 2), trow = (t >> 5) * 4 + ((lane >> 2) & 3);
         struct Codes {
             uint4 v[4];
             __half d[4];
@@ -384,7 +391,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 f.v[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // 0
                 f.d[i] = __ushort_as_half(0);
                 if (first >= 0) {
-                    const int64_t at = first + ((t >> 3) & 15);
+                    const int64_t at = first + (trow & 15);
                     f.v[i] = ldg_nc_v4(codes + at * 128);
                     f.d[i] = __ldg(scales + at * 4);
                 }
@@ -394,8 +401,8 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             const uint32_t place = shared_place(T, part), s0 = place % NS, s1 = (place + 1) % NS;
             const bool free = mbar_wait_bounded(empty + s0, ((place / NS) & 1) ^ 1) && mbar_wait_bounded(empty + s1, (((place + 1) / NS) & 1) ^ 1);
             if (!__all_sync(FULL_MASK, free)) return false;
-            uint8_t* dst = smem + L::RING + (chunk >> 2) * L::COL + (t >> 3) * 128;
-            const uint32_t c0 = ((2 * (chunk & 3)) ^ ((t >> 3) & 7)) << 4;  // the second 8 dims are 16 bytes away in it
+            uint8_t* dst = smem + L::RING + (chunk >> 2) * L::COL + trow * 128;
+            const uint32_t c0 = ((2 * (chunk & 3)) ^ (trow & 7)) << 4;  // the second 8 dims are 16 bytes away in it
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const __half2 dd = __half2half2(f.d[i]);
@@ -439,29 +446,31 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                     part = s.n == 1 ? k : k >= 2 && (k == 2 * s.n - 1 || !(k & 1));
                     j = k < 2 ? (s.n > 1 ? k : 0) : part ? (k == 2 * s.n - 1 ? s.n - 1 : k / 2 - 1) : (k + 1) / 2;
                 };
-                Codes now, next;
+                Codes f[2];
                 int newest = 0, before = look_up(s, 0), rows = before, ahead = s.n > 1 ? look_up(s, 1) : -1;  // of K `newest`, the one before, the next
-                fetch(rows, 0, tiles, now);
-                for (int k = 0; k < 2 * s.n && ok; ++k) {
-                    int j, part, j2, part2;
-                    part_of(k, j, part);
-                    if (k + 1 < 2 * s.n) {
-                        part_of(k + 1, j2, part2);
-                        if (!part2) {
-                            before = rows;
-                            rows = ahead;
-                            newest = j2;
+                fetch(rows, 0, tiles, f[0]);
+                for (int k0 = 0; k0 < 2 * s.n && ok; k0 += 2)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int k = k0 + u;
+                        int j, part;
+                        if (k + 1 < 2 * s.n) {
+                            part_of(k + 1, j, part);
+                            if (!part) {
+                                before = rows;
+                                rows = ahead;
+                                newest = j;
+                            }
+                            fetch(part && j < newest ? before : rows, part, tiles + j, f[u ^ 1]);
+                            if (!part && j + 1 < s.n) ahead = look_up(s, j + 1);
                         }
-                        fetch(part2 && j2 < newest ? before : rows, part2, tiles + j2, next);
-                        if (!part2 && j2 + 1 < s.n) ahead = look_up(s, j2 + 1);
+                        part_of(k, j, part);
+                        ok = ok && make(part, tiles + j, f[u]);
                     }
-                    ok = make(part, tiles + j, now);
-                    now = next;
-                }
                 tiles += s.n;
             }
         }
-        const int share = Q8 && a.narrow ? 2 : 1;  // arrivals of a warp: for one that makes K and V, too
+        constexpr int share = Q8 && NARROW ? 2 : 1;  // arrivals of a warp: for one that makes K and V, too
         for (int x = makes ? x1 : x0; x < x1 && ok;) {
             s.at(a, x, x1 - x);
             x += s.n;
@@ -479,9 +488,10 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                         v = *reinterpret_cast<const float4*>(src + 8 * i + 4);
                     }
                     const int chunk = part * (HD / 32) + i;  // 8 dims
-                    uint8_t* dst = smem + L::Q + (chunk >> 3) * L::COL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+                    if (r >= L::QROWS) continue;
+                    uint8_t* dst = smem + L::Q + (chunk >> 3) * L::QCOL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
                     *reinterpret_cast<uint4*>(dst) = make_uint4(f2_hi(u.x, u.y), f2_hi(u.z, u.w), f2_hi(v.x, v.y), f2_hi(v.z, v.w));
-                    *reinterpret_cast<uint4*>(dst + L::TILE) = make_uint4(f2_lo(u.x, u.y), f2_lo(u.z, u.w), f2_lo(v.x, v.y), f2_lo(v.z, v.w));
+                    *reinterpret_cast<uint4*>(dst + L::QTILE) = make_uint4(f2_lo(u.x, u.y), f2_lo(u.z, u.w), f2_lo(v.x, v.y), f2_lo(v.z, v.w));
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -490,7 +500,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             const bool idle = (warp & 3) * 32 >= nq;  // no query in the warp's rows: what its weights hold does not matter
             float m = -INFINITY;                      // the maximum that the weights are taken against, in units of 1 / c
             float2 l = make_float2(0.0f, 0.0f);
-            if constexpr (Q8) ok = a.narrow || s.n <= w || convert(w, 0);
+            if constexpr (Q8 && !NARROW) ok = s.n <= w || convert(w, 0);
             for (int j = w; j < s.n && ok; j += 2) {
                 // the thread's keys of the tile, and their 16-key runs with a page
                 const int n = min(64, keys - (s.tile + j) * SHARED_TILE - half * 64);
@@ -567,7 +577,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_n(p_full + w, share);
-                if constexpr (Q8) ok = a.narrow || (convert(j, 1) && (j + 2 >= s.n || convert(j + 2, 0)));
+                if constexpr (Q8 && !NARROW) ok = convert(j, 1) && (j + 2 >= s.n || convert(j + 2, 0));
             }
             tiles += s.n;
             // ---- the half's record of the segment's tiles
@@ -618,11 +628,11 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
 // ---- launch ----------------------------------------------------------------------
 cudaError_t encode_fp16_2d(CUtensorMap* out, const void* base, long inner, long rows, int box_inner, int box_rows);
 
-template <int HD, bool Q8>
+template <int HD, bool Q8, bool NARROW>
 static cudaError_t launch_shared_as(const SharedArgs& a, const void* k, const void* v, int dev, cudaStream_t s) {
     static OncePerDevice once;
     cudaError_t e = once(dev, [] {
-        return cudaFuncSetAttribute(shared_kernel<HD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SharedSmem<HD>::TOTAL);
+        return cudaFuncSetAttribute(shared_kernel<HD, Q8, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, SharedSmem<HD, NARROW>::TOTAL);
     });
     if (e != cudaSuccess) return e;
     CUtensorMap mk = {}, mv = {};
@@ -638,14 +648,19 @@ static cudaError_t launch_shared_as(const SharedArgs& a, const void* k, const vo
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(a.sets * a.side);
     cfg.blockDim = dim3(SH_THREADS);
-    cfg.dynamicSmemBytes = SharedSmem<HD>::TOTAL;
+    cfg.dynamicSmemBytes = SharedSmem<HD, NARROW>::TOTAL;
     cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, shared_kernel<HD, Q8>, a, mk, mv);
+    return cudaLaunchKernelEx(&cfg, shared_kernel<HD, Q8, NARROW>, a, mk, mv);
 }
 
 cudaError_t launch_shared(const SharedArgs& a, int hd, bool q8, const void* k, const void* v, int dev, cudaStream_t s) {
-    if (q8) return launch_shared_as<128, true>(a, k, v, dev, s);
-    return hd == 64 ? launch_shared_as<64, false>(a, k, v, dev, s) : launch_shared_as<128, false>(a, k, v, dev, s);
+#define KD_SHARED(NARROW_)                                                            \
+    return q8         ? launch_shared_as<128, true, NARROW_>(a, k, v, dev, s)          \
+           : hd == 64 ? launch_shared_as<64, false, NARROW_>(a, k, v, dev, s)          \
+                      : launch_shared_as<128, false, NARROW_>(a, k, v, dev, s)
+    if (a.narrow) KD_SHARED(true);
+    KD_SHARED(false);
+#undef KD_SHARED
 }
 
 }  // namespace kd
