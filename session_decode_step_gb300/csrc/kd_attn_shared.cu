@@ -75,6 +75,13 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) 
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Two fp32 operations in one.
@@ -115,31 +122,28 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, int n) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
-}
-
 // ---- the kernel ---------------------------------------------------------------
 constexpr int SH_SOFT = 16;                     // softmax warps: two groups of eight, two warps a quarter of the rows
 constexpr int SH_COPY = SH_SOFT, SH_SCORES = SH_SOFT + 1, SH_VALUES = SH_SOFT + 2;  // the copies' and the products' warps
 constexpr int SH_THREADS = (SH_SOFT + 3) * 32;
 
-// NARROW: at most 64 queries, whose rows alone are kept (the tensor core reads 128, and what it makes of
-// the others is not used); with 128-wide heads that leaves room for a sixth buffer.
-template <int HD, bool NARROW>
+// NARROW: at most 64 queries.  They are held in tensor memory, which the products read beside the
+// buffers instead of from them, in the place of the second half's sums: one half of the softmax
+// warps weighs all tiles, and of it the four warps that have the queries' rows.
+template <int HD, bool Q8, bool NARROW>
 struct SharedSmem {
     static constexpr int COLS = HD / 64;               // 128-byte columns of a row
     static constexpr int COL = SHARED_TILE * 128;      // one of a tile
-    static constexpr int TILE = COLS * COL;            // K or V of a tile
-    static constexpr int QROWS = NARROW ? SHARED_QUERIES / 2 : SHARED_QUERIES;
-    static constexpr int QCOL = QROWS * 128, QTILE = COLS * QCOL;  // the queries' columns, and one of their parts
-    static constexpr int SLOTS = HD == 64 ? 8 : NARROW ? 6 : 5;
-    static constexpr int Q = 0, RING = 2 * QTILE, BARS = RING + SLOTS * TILE;
+    static constexpr int TILE = COLS * COL;            // K or V of a tile, or a part of the queries
+    static constexpr int SLOTS = HD == 64 ? 8 : !NARROW ? 5 : Q8 ? 6 : 7;
+    static constexpr int Q = 0, RING = NARROW ? 0 : 2 * TILE, BARS = RING + SLOTS * TILE;
     static constexpr int MAXIMA = BARS + 320;  // [group][half][row]: what the two warps of a row tell each other
-    static constexpr int TOTAL = MAXIMA + 2 * 2 * SHARED_QUERIES * 4;
+    static constexpr int CODES = MAXIMA + 2 * 2 * SHARED_QUERIES * 4;  // Q8_0: a part's codes and scales on their way, by thread
+    static constexpr int TOTAL = CODES + (Q8 && NARROW ? 256 * 4 * (16 + 4) : 0);
     static_assert(TOTAL <= 227 * 1024, "opt-in shared memory");
-    static_assert(QCOL <= TILE, "the rows read behind the queries are in the buffers");
 };
+// Columns of tensor memory: scores (then weights) of the two halves, their sums, and the queries.
+constexpr uint32_t TM_SUMS = 256, TM_QUERIES = 384;
 
 // Q8_0: the first of the two places, counted on round the buffers, of K (part 0) or V (1) of a CTA's tile t: in
 // the order K0 K1 V0 K2 V1 K3 V2 ..., as V is made when its tile has been weighed, and then the K after next.
@@ -166,7 +170,7 @@ struct SharedSeg {
 template <int HD, bool Q8, bool NARROW>
 __global__ void __launch_bounds__(SH_THREADS, 1)
     shared_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
-    using L = SharedSmem<HD, NARROW>;
+    using L = SharedSmem<HD, Q8, NARROW>;
     constexpr int NS = L::SLOTS;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -195,11 +199,11 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, SH_SOFT / 2);
+            mbar_init(p_full + i, NARROW ? 4 : SH_SOFT / 2);
             mbar_init(pv_done + i, 1);
         }
-        mbar_init(q_full, SH_SOFT);
-        mbar_init(q_free, SH_SOFT);
+        mbar_init(q_full, NARROW ? 4 : SH_SOFT);
+        mbar_init(q_free, NARROW ? 4 : SH_SOFT);
         for (int i = 0; i < SH_SOFT / 2; ++i) mbar_init(pair + i, 2);
         mbar_init_fence();
         *failed = 0;
@@ -317,8 +321,11 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
 #pragma unroll
                             for (int k = 0; k < HD / 16; ++k) {
                                 const uint32_t off = (k / 4) * L::COL + (k % 4) * 32;
-                                tc_mma_ss(tmem + w * 128, tc_desc(qs + (part == 1 ? L::QTILE : 0) + (k / 4) * L::QCOL + (k % 4) * 32, 0),
-                                          tc_desc(ring + slot[part / 2] * L::TILE + off, 0), id, part || k);
+                                const uint64_t kd = tc_desc(ring + slot[part / 2] * L::TILE + off, 0);
+                                if constexpr (NARROW)
+                                    tc_mma_ts(tmem + w * 128, tmem + TM_QUERIES + (part == 1 ? HD / 2 : 0) + 8 * k, kd, id, part || k);
+                                else
+                                    tc_mma_ss(tmem + w * 128, tc_desc(qs + (part == 1 ? L::TILE : 0) + off, 0), kd, id, part || k);
                             }
                         tc_commit(s_full + w);
                     } else {
@@ -326,8 +333,8 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                         for (int k = 0; k < n / 16; ++k)
 #pragma unroll
                             for (int part = 0; part < 1 + PARTS; ++part)
-                                tc_mma_ts(tmem + 256 + w * HD, tmem + w * 128 + 32 * (k / 2) + (part == 1 ? 16 : 0) + 8 * (k & 1),
-                                          tc_desc(ring + slot[part / 2] * L::TILE + k * 2048, L::COL), id, part || k || j >= 2);
+                                tc_mma_ts(tmem + TM_SUMS + (NARROW ? 0 : w * HD), tmem + w * 128 + 32 * (k / 2) + (part == 1 ? 16 : 0) + 8 * (k & 1),
+                                          tc_desc(ring + slot[part / 2] * L::TILE + k * 2048, L::COL), id, part || k || j >= (NARROW ? 1 : 2));
                         tc_commit(pv_done + w);
                     }
 #pragma unroll
@@ -343,10 +350,10 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         // ---- softmax: two threads have a query's row, a half of the tile's keys (then of the head's dims) each
         const int w = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
-        const uint32_t st = lane_base + w * 128 + half * 64, ot = lane_base + 256 + w * HD + half * (HD / 2);
+        const uint32_t st0 = lane_base + half * 64, ot = lane_base + TM_SUMS + (NARROW ? 0 : w * HD) + half * (HD / 2);
         float* maxima = reinterpret_cast<float*>(smem + L::MAXIMA) + w * 2 * SHARED_QUERIES;
         uint64_t* partner = pair + w * 4 + (warp & 3);
-        unsigned ss = 0, pv = 0, met = 0;  // scores and products seen, meetings with the row's other warp
+        unsigned s_phase = 0, t_phase = 0, met = 0;  // scores seen and tiles weighed, a bit for each half's place; meetings with the row's other warp
         uint32_t tiles = 0, segs = 0;
         bool ok = true;
         const float c = a.scale * 1.4426950408889634f;
@@ -361,10 +368,10 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         SharedSeg s;
         // Q8_0: eight warps make K (part 0) and V (1) of tile j of the segment, codes times scales as
         // fp16 pairs hi + lo (19 bits, so exactly): a thread takes 16 codes of rows trow + 32 i.  Where no group
-        // has more than 64 queries the warps of the upper 64 rows do nothing else; else the group of warps that
+        // has more than 64 queries the second half of the warps does nothing else; else the half that
         // weighs the tile does it in between.
-        const bool makes = Q8 && NARROW && (warp & 2);
-        const int t = makes ? ((warp >> 2) * 2 + (warp & 1)) * 32 + lane : threadIdx.x & 255;
+        const bool makes = Q8 && NARROW && w == 1;
+        const int t = threadIdx.x & 255;
         // 8 lanes write 4 chunks of two rows, which the swizzle puts into different banks
         const int chunk = (lane & 3) | ((lane >> 4) << 2), trow = (t >> 5) * 4 + ((lane >> 2) & 3);
         struct Codes {
@@ -380,7 +387,10 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             if (a.fault) *a.fault = 1;
             return -1;
         };
-        auto fetch = [&](int rows, int part, uint32_t T, Codes& f) {
+        // The thread's codes and scales of a part: to registers, or (ahead) to its own place in shared memory, as
+        // loads to registers would be waited for together with those of the part after.
+        const uint32_t mine_at = smem_u32(smem + L::CODES) + t * 16, scales_at = smem_u32(smem + L::CODES) + 256 * 4 * 16 + t * 4;
+        auto fetch = [&](int rows, int part, uint32_t T, Codes* f) {
             const uint8_t* codes = (part ? a.vq : a.kq) + 16 * chunk;
             const __half* scales = (part ? a.vs : a.ks) + (chunk >> 1);
             const unsigned have = __ballot_sync(FULL_MASK, rows >= 0);
@@ -388,14 +398,40 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // the warp's rows of i are of one run
                 const int first = __shfl_sync(FULL_MASK, rows, 2 * i + (t >> 7));
-                f.v[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // 0
-                f.d[i] = __ushort_as_half(0);
-                if (first >= 0) {
-                    const int64_t at = first + (trow & 15);
-                    f.v[i] = ldg_nc_v4(codes + at * 128);
-                    f.d[i] = __ldg(scales + at * 4);
+                const bool good = first >= 0;
+                const int64_t at = good ? first + (trow & 15) : 0;
+                if (f) {
+                    f->v[i] = make_uint4(0, 0, 0, 0);
+                    f->d[i] = __ushort_as_half(0);  // whatever the codes, 0
+                    if (good) {
+                        f->v[i] = ldg_nc_v4(codes + at * 128);
+                        f->d[i] = __ldg(scales + at * 4);
+                    }
+                } else {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mine_at + i * 256 * 16), "l"(codes + at * 128),
+                                 "r"(good ? 16 : 0)
+                                 : "memory");
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(scales_at + i * 256 * 4),
+                                 "l"((const __half*)((uintptr_t)(scales + at * 4) & ~(uintptr_t)3)), "r"(good ? 4 : 0)
+                                 : "memory");
                 }
             }
+        };
+        auto landed = [&](Codes& f) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t d;
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(f.v[i].x), "=r"(f.v[i].y), "=r"(f.v[i].z), "=r"(f.v[i].w)
+                             : "r"(mine_at + i * 256 * 16)
+                             : "memory");
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(d) : "r"(scales_at + i * 256 * 4) : "memory");
+                f.d[i] = __ushort_as_half((unsigned short)((chunk >> 1) & 1 ? d >> 16 : d));
+            }
+            // read before the next part's copies are issued
+#pragma unroll
+            for (int i = 0; i < 4; ++i) asm volatile("" : "+r"(f.v[i].x), "+r"(f.v[i].y), "+r"(f.v[i].z), "+r"(f.v[i].w)::"memory");
         };
         auto make = [&](int part, uint32_t T, const Codes& f) {
             const uint32_t place = shared_place(T, part), s0 = place % NS, s1 = (place + 1) % NS;
@@ -432,7 +468,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         };
         auto convert = [&](int j, int part) {
             Codes f;
-            fetch(look_up(s, j), part, tiles + j, f);
+            fetch(look_up(s, j), part, tiles + j, &f);
             return make(part, tiles + j, f);
         };
         if (makes) {
@@ -446,65 +482,85 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                     part = s.n == 1 ? k : k >= 2 && (k == 2 * s.n - 1 || !(k & 1));
                     j = k < 2 ? (s.n > 1 ? k : 0) : part ? (k == 2 * s.n - 1 ? s.n - 1 : k / 2 - 1) : (k + 1) / 2;
                 };
-                Codes f[2];
                 int newest = 0, before = look_up(s, 0), rows = before, ahead = s.n > 1 ? look_up(s, 1) : -1;  // of K `newest`, the one before, the next
-                fetch(rows, 0, tiles, f[0]);
-                for (int k0 = 0; k0 < 2 * s.n && ok; k0 += 2)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int k = k0 + u;
-                        int j, part;
-                        if (k + 1 < 2 * s.n) {
-                            part_of(k + 1, j, part);
-                            if (!part) {
-                                before = rows;
-                                rows = ahead;
-                                newest = j;
-                            }
-                            fetch(part && j < newest ? before : rows, part, tiles + j, f[u ^ 1]);
-                            if (!part && j + 1 < s.n) ahead = look_up(s, j + 1);
+                fetch(rows, 0, tiles, nullptr);
+                for (int k = 0; k < 2 * s.n && ok; ++k) {
+                    Codes f;
+                    landed(f);
+                    int j, part;
+                    if (k + 1 < 2 * s.n) {
+                        part_of(k + 1, j, part);
+                        if (!part) {
+                            before = rows;
+                            rows = ahead;
+                            newest = j;
                         }
-                        part_of(k, j, part);
-                        ok = ok && make(part, tiles + j, f[u]);
+                        fetch(part && j < newest ? before : rows, part, tiles + j, nullptr);
+                        if (!part && j + 1 < s.n) ahead = look_up(s, j + 1);
                     }
+                    part_of(k, j, part);
+                    ok = make(part, tiles + j, f);
+                }
                 tiles += s.n;
             }
         }
-        constexpr int share = Q8 && NARROW ? 2 : 1;  // arrivals of a warp: for one that makes K and V, too
-        for (int x = makes ? x1 : x0; x < x1 && ok;) {
+        const bool weighs = !NARROW || (w == 0 && (warp & 2) == 0);
+        for (int x = weighs ? x0 : x1; x < x1 && ok;) {
             s.at(a, x, x1 - x);
             x += s.n;
             const int nq = n_queries(s), q0 = first_query(s);
             if (nq <= 0) continue;
             const int keys = a.keys[s.g];
-            {   // the queries: a quarter of row r's dims
-                const int part = w * 2 + half, qi = q0 + r;
-                const float* src = a.q + ((size_t)(a.lead[s.g] + qi / a.gq) * a.nh + (size_t)s.h * a.gq + qi % a.gq) * HD + part * (HD / 4);
+            const int qi = q0 + r;
+            const float* src = a.q + ((size_t)(a.lead[s.g] + qi / a.gq) * a.nh + (size_t)s.h * a.gq + qi % a.gq) * HD;
+            if constexpr (NARROW) {  // the queries: half of row r's dims, hi and lo
+#pragma unroll
+                for (int k = 0; k < HD / 64; ++k) {  // 32 dims
+                    uint32_t p[32];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (r < nq) u = *reinterpret_cast<const float4*>(src + half * (HD / 2) + 32 * k + 4 * i);
+                        p[2 * i] = f2_hi(u.x, u.y), p[2 * i + 1] = f2_hi(u.z, u.w);
+                        p[16 + 2 * i] = f2_lo(u.x, u.y), p[16 + 2 * i + 1] = f2_lo(u.z, u.w);
+                    }
+                    const uint32_t qt = lane_base + TM_QUERIES + half * (HD / 4) + 16 * k;
+                    tc_st16(qt, p);
+                    tc_st16(qt + HD / 2, p + 16);
+                }
+                tc_wait_st();
+                tc_fence_before();
+            } else {  // a quarter of row r's dims
+                const int part = w * 2 + half;
 #pragma unroll
                 for (int i = 0; i < HD / 32; ++i) {
                     float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
                     if (r < nq) {
-                        u = *reinterpret_cast<const float4*>(src + 8 * i);
-                        v = *reinterpret_cast<const float4*>(src + 8 * i + 4);
+                        u = *reinterpret_cast<const float4*>(src + part * (HD / 4) + 8 * i);
+                        v = *reinterpret_cast<const float4*>(src + part * (HD / 4) + 8 * i + 4);
                     }
                     const int chunk = part * (HD / 32) + i;  // 8 dims
-                    if (r >= L::QROWS) continue;
-                    uint8_t* dst = smem + L::Q + (chunk >> 3) * L::QCOL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+                    uint8_t* dst = smem + L::Q + (chunk >> 3) * L::COL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
                     *reinterpret_cast<uint4*>(dst) = make_uint4(f2_hi(u.x, u.y), f2_hi(u.z, u.w), f2_hi(v.x, v.y), f2_hi(v.z, v.w));
-                    *reinterpret_cast<uint4*>(dst + L::QTILE) = make_uint4(f2_lo(u.x, u.y), f2_lo(u.z, u.w), f2_lo(v.x, v.y), f2_lo(v.z, v.w));
+                    *reinterpret_cast<uint4*>(dst + L::TILE) = make_uint4(f2_lo(u.x, u.y), f2_lo(u.z, u.w), f2_lo(v.x, v.y), f2_lo(v.z, v.w));
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive_n(q_full, share);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
             const bool idle = (warp & 3) * 32 >= nq;  // no query in the warp's rows: what its weights hold does not matter
             float m = -INFINITY;                      // the maximum that the weights are taken against, in units of 1 / c
             float2 l = make_float2(0.0f, 0.0f);
             if constexpr (Q8 && !NARROW) ok = s.n <= w || convert(w, 0);
-            for (int j = w; j < s.n && ok; j += 2) {
+            // A product P V of the tile before last, or earlier, of place b is done when its scores are there.
+            auto values_done = [&](int j) { return __all_sync(FULL_MASK, mbar_wait_bounded(pv_done + (j & 1), ((t_phase >> (j & 1)) & 1) ^ 1)); };
+            for (int j = NARROW ? 0 : w; j < s.n && ok; j += NARROW ? 1 : 2) {
+                const int b = j & 1;
+                const uint32_t st = st0 + b * 128;
                 // the thread's keys of the tile, and their 16-key runs with a page
                 const int n = min(64, keys - (s.tile + j) * SHARED_TILE - half * 64);
-                ok = __all_sync(FULL_MASK, mbar_wait_bounded(s_full + w, ss++ & 1));
+                ok = __all_sync(FULL_MASK, mbar_wait_bounded(s_full + b, (s_phase >> b) & 1));
+                s_phase ^= 1u << b;
                 if (!ok) break;
                 tc_fence_after();
                 const unsigned have = runs[(tiles + j) & 7] >> (half * 4);
@@ -539,7 +595,12 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                         f = tc_exp2((m - mx) * c);
                         m = mx;
                     }
-                    if (j >= 2 && __any_sync(FULL_MASK, f != 1.0f)) {
+                    if (j >= (NARROW ? 1 : 2) && __any_sync(FULL_MASK, f != 1.0f)) {
+                        if (NARROW) {
+                            ok = values_done(j - 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
                         l.x *= f;
                         l.y *= f;
 #pragma unroll 1
@@ -576,17 +637,17 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_n(p_full + w, share);
+                if (lane == 0) mbar_arrive(p_full + b);
+                t_phase ^= 1u << b;
                 if constexpr (Q8 && !NARROW) ok = convert(j, 1) && (j + 2 >= s.n || convert(j + 2, 0));
             }
             tiles += s.n;
             // ---- the half's record of the segment's tiles
             float* rec = a.part + (shared_row(a, s.g, s.h, s.pass, set, q0 - s.pass * a.side * SHARED_QUERIES + r) * 2 + w) * PAGED_REC(HD);
-            if (s.n <= w) {  // one tile: the second half had none
-                if (r < nq && !half) *reinterpret_cast<float2*>(rec + HD) = make_float2(-INFINITY, 0.0f);
-            } else if (ok) {
-                pv += (s.n - w + 1) / 2;  // products of this group in the segment
-                ok = __all_sync(FULL_MASK, mbar_wait_bounded(pv_done + w, (pv - 1) & 1));
+            float* second = NARROW ? rec + PAGED_REC(HD) : rec;
+            if ((NARROW || s.n <= w) && r < nq && !half) *reinterpret_cast<float2*>(second + HD) = make_float2(-INFINITY, 0.0f);  // none
+            if (ok && (NARROW || s.n > w)) {
+                ok = values_done(NARROW || ((s.n - 1) & 1) == w ? s.n - 1 : s.n - 2);
                 tc_fence_after();
                 if (ok && !idle) {
                     const float sum = l.x + l.y, other = exchange(sum, ok);
@@ -607,7 +668,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             }
             // All are done with the queries and with tensor memory.
             __syncwarp();
-            if (lane == 0) mbar_arrive_n(q_free, share);
+            if (lane == 0) mbar_arrive(q_free);
             ok = ok && __all_sync(FULL_MASK, mbar_wait_bounded(q_free, segs++ & 1));
         }
         if (!ok) *failed = 1;
@@ -632,7 +693,7 @@ template <int HD, bool Q8, bool NARROW>
 static cudaError_t launch_shared_as(const SharedArgs& a, const void* k, const void* v, int dev, cudaStream_t s) {
     static OncePerDevice once;
     cudaError_t e = once(dev, [] {
-        return cudaFuncSetAttribute(shared_kernel<HD, Q8, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, SharedSmem<HD, NARROW>::TOTAL);
+        return cudaFuncSetAttribute(shared_kernel<HD, Q8, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, SharedSmem<HD, Q8, NARROW>::TOTAL);
     });
     if (e != cudaSuccess) return e;
     CUtensorMap mk = {}, mv = {};
@@ -648,7 +709,7 @@ static cudaError_t launch_shared_as(const SharedArgs& a, const void* k, const vo
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(a.sets * a.side);
     cfg.blockDim = dim3(SH_THREADS);
-    cfg.dynamicSmemBytes = SharedSmem<HD, NARROW>::TOTAL;
+    cfg.dynamicSmemBytes = SharedSmem<HD, Q8, NARROW>::TOTAL;
     cfg.stream = s;
     return cudaLaunchKernelEx(&cfg, shared_kernel<HD, Q8, NARROW>, a, mk, mv);
 }
