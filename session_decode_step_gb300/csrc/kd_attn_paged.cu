@@ -540,16 +540,14 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
 
 // The merge of a (session, head) that several CTAs share: out = sum_i w_i o_i / sum_i w_i l_i
 // over its records, w_i = e^{m_i - max m}: those of its own keys and those that the CTAs of
-// its group's shared keys left.  A block per (session, query head): a warp forms the weights, then each
-// warp sums every fourth record, four of them in flight, and the warps' sums are added in order.
+// its group's shared keys left.  A block per (session, query head): a warp takes every fourth record, eight
+// of them in flight, with a running maximum, and the warps' sums are joined in order.
 constexpr int PAGED_MERGE_WARPS = 4;
-constexpr int PAGED_MAX_RECORDS = PAGED_MAX_CTAS + 2 * SHARED_MAX_CTAS;
 template <int HD>
 __global__ void __launch_bounds__(PAGED_MERGE_WARPS * 32) paged_merge_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ SharedArgs sh) {
     constexpr int REC = PAGED_REC(HD), DIMS = HD / 32;  // a lane's dims
-    __shared__ float2 weight[PAGED_MAX_RECORDS];        // (m, l), then (w, -)
     __shared__ float sums[PAGED_MERGE_WARPS][HD];
-    __shared__ float denom;
+    __shared__ float2 ends[PAGED_MERGE_WARPS];  // a warp's maximum and denominator
     const int qh = blockIdx.x, b = blockIdx.y, gq = a.nh / a.nkv, h = qh / gq, i = qh - h * gq;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nb = a.first[b + 1] - a.first[b], g = a.group[b];
@@ -581,62 +579,62 @@ __global__ void __launch_bounds__(PAGED_MERGE_WARPS * 32) paged_merge_kernel(con
     auto record = [&](int k) {
         return k < n ? rec + (size_t)k * gq * REC : pairs + ((k - n) >> 1) * set_step + ((k - n) & 1) * REC;
     };
-    if (warp == 0) {
-        float M = -INFINITY, den = 0.0f;
-        for (int k = lane; k < total; k += 32) {
-            const float2 ml = *reinterpret_cast<const float2*>(record(k) + HD);
-            weight[k] = ml;
-            M = fmaxf(M, ml.x);
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, x));
-        const float ref = M == -INFINITY ? 0.0f : M;
-        for (int k = lane; k < total; k += 32) {
-            const float2 ml = weight[k];
-            const float w = expf(__fsub_rn(ml.x, ref));
-            weight[k].x = w;
-            den = __fmaf_rn(w, ml.y, den);
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) den = __fadd_rn(den, __shfl_xor_sync(FULL_MASK, den, x));
-        if (lane == 0) denom = den == 0.0f ? 1.0f : den;  // 0: no key has a page
-    }
-    __syncthreads();
-    float acc[DIMS];
+    float acc[DIMS], M = -INFINITY, den = 0.0f;
 #pragma unroll
     for (int d = 0; d < DIMS; ++d) acc[d] = 0.0f;
-    constexpr int U = 4;
+    constexpr int U = 8;
     for (int k0 = warp; k0 < total; k0 += U * PAGED_MERGE_WARPS) {
-        float v[U][DIMS], w[U];
+        float v[U][DIMS];
+        float2 ml[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = k0 + u * PAGED_MERGE_WARPS;
-            w[u] = k < total ? weight[k].x : 0.0f;
-            if (w[u] != 0.0f) {  // what a record without keys holds is not read
-                const float* r = record(k) + lane * DIMS;
+            ml[u] = make_float2(-INFINITY, 0.0f);
+            if (k < total) {
+                const float* r = record(k);
+                ml[u] = *reinterpret_cast<const float2*>(r + HD);
                 if constexpr (DIMS == 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(r);
+                    const float4 f = *reinterpret_cast<const float4*>(r + lane * DIMS);
                     v[u][0] = f.x, v[u][1] = f.y, v[u][2] = f.z, v[u][3] = f.w;
                 } else {
-                    const float2 f = *reinterpret_cast<const float2*>(r);
+                    const float2 f = *reinterpret_cast<const float2*>(r + lane * DIMS);
                     v[u][0] = f.x, v[u][1] = f.y;
                 }
             }
         }
+        float top = M;
+#pragma unroll
+        for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+        const float ref = top == -INFINITY ? 0.0f : top, f = expf(__fsub_rn(M, ref));
+        M = top;
+        den = __fmul_rn(den, f);
+#pragma unroll
+        for (int d = 0; d < DIMS; ++d) acc[d] = __fmul_rn(acc[d], f);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (w[u] != 0.0f)
+            if (ml[u].x != -INFINITY) {  // else there are no keys, and what is in its place does not count
+                const float w = expf(__fsub_rn(ml[u].x, ref));
+                den = __fmaf_rn(w, ml[u].y, den);
 #pragma unroll
-                for (int d = 0; d < DIMS; ++d) acc[d] = __fmaf_rn(w[u], v[u][d], acc[d]);
+                for (int d = 0; d < DIMS; ++d) acc[d] = __fmaf_rn(w, v[u][d], acc[d]);
+            }
     }
 #pragma unroll
     for (int d = 0; d < DIMS; ++d) sums[warp][lane * DIMS + d] = acc[d];
+    if (lane == 0) ends[warp] = make_float2(M, den);
     __syncthreads();
     for (int d = threadIdx.x; d < HD; d += PAGED_MERGE_WARPS * 32) {
-        float o = sums[0][d];
+        float all = -INFINITY, o = 0.0f, l = 0.0f;
 #pragma unroll
-        for (int k = 1; k < PAGED_MERGE_WARPS; ++k) o = __fadd_rn(o, sums[k][d]);
-        a.out[((size_t)b * a.nh + qh) * HD + d] = __float2half_rn(__fdiv_rn(o, denom));
+        for (int k = 0; k < PAGED_MERGE_WARPS; ++k) all = fmaxf(all, ends[k].x);
+        const float ref = all == -INFINITY ? 0.0f : all;
+#pragma unroll
+        for (int k = 0; k < PAGED_MERGE_WARPS; ++k) {
+            const float w = expf(__fsub_rn(ends[k].x, ref));
+            o = __fmaf_rn(w, sums[k][d], o);
+            l = __fmaf_rn(w, ends[k].y, l);
+        }
+        a.out[((size_t)b * a.nh + qh) * HD + d] = __float2half_rn(l == 0.0f ? 0.0f : __fdiv_rn(o, l));  // 0: no key has a page
     }
     pdl_launch_dependents();
 }

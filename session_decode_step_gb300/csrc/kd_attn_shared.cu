@@ -216,11 +216,10 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
-    pdl_wait();
-    pdl_launch_dependents();  // after the wait: the kernel behind this one relies on it, and reads at once
-
     const int set = blockIdx.x / a.side, mine = blockIdx.x - set * a.side;  // of the CTAs side by side
     const int x0 = a.share.begin(set), x1 = a.share.begin(set + 1);
+    pdl_wait();
+    pdl_launch_dependents();  // after the wait: the kernel behind this one relies on it, and reads at once
     const int box = a.box_runs;  // 16-key runs of a copy's box
     // The first of the CTA's queries in a segment's group, and how many (<= 0: none).
     auto first_query = [&](const SharedSeg& s) { return (s.pass * a.side + mine) * SHARED_QUERIES; };
