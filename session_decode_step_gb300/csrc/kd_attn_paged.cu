@@ -551,8 +551,8 @@ __global__ void __launch_bounds__(PAGED_MERGE_WARPS * 32) paged_merge_kernel(con
     const int qh = blockIdx.x, b = blockIdx.y, gq = a.nh / a.nkv, h = qh / gq, i = qh - h * gq;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nb = a.first[b + 1] - a.first[b], g = a.group[b];
-    // n records of its own keys, then a pair of each set of CTAs that has some of the shared keys
-    const float *rec = nullptr, *pairs = nullptr;
+    // n records of its own keys, then one of each set of CTAs that has some of the shared keys
+    const float *rec = nullptr, *shared = nullptr;
     int n = 0, sets = 0;
     size_t set_step = 0;
     if (nb) {
@@ -561,11 +561,11 @@ __global__ void __launch_bounds__(PAGED_MERGE_WARPS * 32) paged_merge_kernel(con
         rec = a.part + (((size_t)c0 + (size_t)b * a.nkv + h) * gq + i) * REC;
     }
     if (g != SHARED_NONE) {
-        const int per = SHARED_QUERIES * sh.side, query = (b - sh.lead[g]) * gq + i, pass = query / per, T = sh.tiles(g);
+        const int per = sh.tile_queries * sh.side, query = (b - sh.lead[g]) * gq + i, pass = query / per, T = sh.tiles(g);
         const int s0 = sh.first[g] * sh.nkv + (h * sh.passes(g) + pass) * T, c0 = sh.share.taker(s0);
         sets = sh.share.taker(s0 + T - 1) - c0 + 1;
-        pairs = sh.part + shared_row(sh, g, h, pass, c0, query - pass * per) * 2 * REC;
-        set_step = (size_t)per * 2 * REC;
+        shared = sh.part + shared_row(sh, g, h, pass, c0, query - pass * per) * REC;
+        set_step = (size_t)per * REC;
     }
     pdl_wait();
     if (sh.n_groups && qh == 0 && b == 0 && warp == PAGED_MERGE_WARPS - 1) {  // the call's fault word
@@ -574,10 +574,10 @@ __global__ void __launch_bounds__(PAGED_MERGE_WARPS * 32) paged_merge_kernel(con
         bad = __any_sync(FULL_MASK, bad != 0);
         if (lane == 0) *a.err = bad ? ERR_WAIT_TIMEOUT : 0;
     }
-    const int total = n + 2 * sets;
+    const int total = n + sets;
     if (!total || (n == 1 && !sets)) return;  // no keys, or written by the CTA itself
     auto record = [&](int k) {
-        return k < n ? rec + (size_t)k * gq * REC : pairs + ((k - n) >> 1) * set_step + ((k - n) & 1) * REC;
+        return k < n ? rec + (size_t)k * gq * REC : shared + (k - n) * set_step;
     };
     float acc[DIMS], M = -INFINITY, den = 0.0f;
 #pragma unroll

@@ -1,21 +1,23 @@
 // kd_attn_shared.cu -- attention of a group of sessions over the prefix that they share, on
 // the fifth-generation tensor cores: every key and value is read once for up to 128
-// queries (the sessions' heads of one KV head, 128 of them a tile).
+// queries (64 on Q8_0 caches), the sessions' heads of one KV head.
 //
 // S = Q K^T and O += P V with tcgen05.mma, the queries as the 128 rows, keys 128 at a
-// time: K and V come by TMA (boxes of a page's rows, 128-byte swizzle, five buffers), one
-// thread issues the products, and two groups of eight warps take turns at the tiles' softmax, each
-// with scores, weights and sums of its own in tensor memory, so that one's products run
-// under the other's exponentials.  Two threads hold a query's row, half of the tile's keys each,
-// and tell each other their maxima.  The sums are rescaled only when the maximum has grown by 2^8 or more (the
-// weights, at most 2^8 then, lose nothing: they are pairs of fp16).
+// time.  K and V come by TMA (boxes of a page's rows, 128-byte swizzle, six buffers); the queries
+// and the weights are the products' operands in tensor memory, which leaves shared memory's
+// rate (one operand of 4 KB a product of 64 cycles takes half of it) to K and V; scores of two tiles are there
+// in turn, so that one's products run under the other's exponentials.  Four threads hold a query's row, a quarter of
+// the tile's keys each, and tell each other their maxima.  The sums are rescaled only when the
+// maximum has grown by 2^8 or more (the weights, at most 2^8 then, lose nothing: they are pairs
+// of fp16).
 //
 // Queries and weights are fp16 pairs hi + lo, as in the kernel of the sessions' own
-// keys, two products each: 4 x 2 x 128^3 flops a tile of 128 keys and 128 queries, 1.1 us
+// keys, two products each: 4 x 2 x 128^3 flops a tile of 128 keys and 128 queries, 2048 cycles, 1.1 us
 // at the SM's share of the bf16 rate, while its 64 KB take 1.4 us of the SM's share of the memory's.
+// Q8_0 rows become such pairs, too (three products each), made by eight warps of their own.
 //
-// CTAs share the tiles of all (group, KV head)s equally (kd_shared.h); what one finds of a
-// (group, head) goes to a record that the merge reads.  Groups of more than 128 queries are taken by
+// CTAs share the tiles of all (group, KV head)s equally (kd_paged.h); what one finds of a
+// (group, head) goes to a record that the merge reads.  Groups of more queries are taken by
 // CTAs side by side, one tile of queries each, that read the same keys at the same time.
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -82,6 +84,20 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* v) {
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+__device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t* v) {  // and waits
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Two fp32 operations in one.
@@ -123,26 +139,26 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 
 // ---- the kernel ---------------------------------------------------------------
-constexpr int SH_SOFT = 16;                     // softmax warps: two groups of eight, two warps a quarter of the rows
+constexpr int SH_SOFT = 16;  // softmax warps (Q8_0: four, and eight that make K and V)
 constexpr int SH_COPY = SH_SOFT, SH_SCORES = SH_SOFT + 1, SH_VALUES = SH_SOFT + 2;  // the copies' and the products' warps
 constexpr int SH_THREADS = (SH_SOFT + 3) * 32;
 
-// NARROW: at most 64 queries.  They are held in tensor memory, which the products read beside the
-// buffers instead of from them, in the place of the second half's sums: one half of the softmax
-// warps weighs all tiles, and of it the four warps that have the queries' rows.
-template <int HD, bool Q8, bool NARROW>
+template <int HD, bool Q8>
 struct SharedSmem {
+    static constexpr int QUERIES = shared_queries(Q8);
+    static constexpr int SHARE = Q8 ? 2 : 4;           // threads (warps) of a row
+    static constexpr int WEIGH = SHARE * QUERIES / 32; // softmax warps
     static constexpr int COLS = HD / 64;               // 128-byte columns of a row
     static constexpr int COL = SHARED_TILE * 128;      // one of a tile
-    static constexpr int TILE = COLS * COL;            // K or V of a tile, or a part of the queries
-    static constexpr int SLOTS = HD == 64 ? 8 : !NARROW ? 5 : Q8 ? 6 : 7;
-    static constexpr int Q = 0, RING = NARROW ? 0 : 2 * TILE, BARS = RING + SLOTS * TILE;
-    static constexpr int MAXIMA = BARS + 320;  // [group][half][row]: what the two warps of a row tell each other
-    static constexpr int CODES = MAXIMA + 2 * 2 * SHARED_QUERIES * 4;  // Q8_0: a part's codes and scales on their way, by thread
-    static constexpr int TOTAL = CODES + (Q8 && NARROW ? 256 * 4 * (16 + 4) : 0);
+    static constexpr int TILE = COLS * COL;            // K or V of a tile
+    static constexpr int SLOTS = HD == 64 ? 8 : 6;
+    static constexpr int RING = 0, BARS = SLOTS * TILE;
+    static constexpr int MAXIMA = BARS + 320;          // [2][share][row]: what the warps of a row tell each other
+    static constexpr int CODES = MAXIMA + 2 * SHARE * QUERIES * 4;  // Q8_0: a part's codes and scales on their way, by thread
+    static constexpr int TOTAL = CODES + (Q8 ? 256 * 4 * (16 + 4) : 0);
     static_assert(TOTAL <= 227 * 1024, "opt-in shared memory");
 };
-// Columns of tensor memory: scores (then weights) of the two halves, their sums, and the queries.
+// Columns of tensor memory: scores, then weights, of two tiles in turn (128 each); the sums; the queries, hi and lo.
 constexpr uint32_t TM_SUMS = 256, TM_QUERIES = 384;
 
 // Q8_0: the first of the two places, counted on round the buffers, of K (part 0) or V (1) of a CTA's tile t: in
@@ -167,16 +183,16 @@ struct SharedSeg {
     }
 };
 
-template <int HD, bool Q8, bool NARROW>
+template <int HD, bool Q8>
 __global__ void __launch_bounds__(SH_THREADS, 1)
     shared_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
-    using L = SharedSmem<HD, Q8, NARROW>;
+    using L = SharedSmem<HD, Q8>;
     constexpr int NS = L::SLOTS;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BARS);
     uint64_t *empty = full + NS, *s_full = empty + NS, *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *q_free = q_full + 1, *pair = q_free + 1;
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(pair + SH_SOFT / 2);
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(pair + 4);
     volatile int* failed = reinterpret_cast<volatile int*>(tmem_at + 1);
     // The last tiles' 16-key runs that have a page, by tile: an entry is written again after 8 tiles, when the
     // buffers (at most 8, two a tile) have gone round past its tile's values, so past its softmax.
@@ -199,12 +215,12 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, NARROW ? 4 : SH_SOFT / 2);
+            mbar_init(p_full + i, L::WEIGH);
             mbar_init(pv_done + i, 1);
         }
-        mbar_init(q_full, NARROW ? 4 : SH_SOFT);
-        mbar_init(q_free, NARROW ? 4 : SH_SOFT);
-        for (int i = 0; i < SH_SOFT / 2; ++i) mbar_init(pair + i, 2);
+        mbar_init(q_full, L::WEIGH);
+        mbar_init(q_free, L::WEIGH);
+        for (int i = 0; i < 4; ++i) mbar_init(pair + i, L::SHARE);
         mbar_init_fence();
         *failed = 0;
         if (!Q8) {
@@ -222,8 +238,8 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     pdl_launch_dependents();  // after the wait: the kernel behind this one relies on it, and reads at once
     const int box = a.box_runs;  // 16-key runs of a copy's box
     // The first of the CTA's queries in a segment's group, and how many (<= 0: none).
-    auto first_query = [&](const SharedSeg& s) { return (s.pass * a.side + mine) * SHARED_QUERIES; };
-    auto n_queries = [&](const SharedSeg& s) { return min(SHARED_QUERIES, a.queries[s.g] - first_query(s)); };
+    auto first_query = [&](const SharedSeg& s) { return (s.pass * a.side + mine) * L::QUERIES; };
+    auto n_queries = [&](const SharedSeg& s) { return min(L::QUERIES, a.queries[s.g] - first_query(s)); };
 
     if (warp == SH_COPY) {
         if constexpr (!Q8) {
@@ -284,9 +300,9 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             // buffers of a tile's K or V: one, or with Q8_0 the two parts of the pairs
             constexpr int PARTS = Q8 ? 2 : 1;
             uint32_t place = values, tile = 0, q_phase = 0;
-            unsigned half_phase = 0;  // of p_full (values) or pv_done (scores), a bit for each half of the softmax warps
+            unsigned turn_phase = 0;  // of p_full (values) or pv_done (scores), a bit for even and odd tiles
             bool ok = true;
-            const uint32_t qs = smem_u32(smem + L::Q), ring = smem_u32(smem + L::RING);
+            const uint32_t ring = smem_u32(smem + L::RING);
             SharedSeg s;
             for (int x = x0; x < x1 && ok;) {
                 s.at(a, x, x1 - x);
@@ -300,7 +316,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 for (int j = 0; j < s.n && ok; ++j) {
                     const int w = j & 1, n = min(SHARED_TILE, keys - (s.tile + j) * SHARED_TILE);
                     // weights that are there; or, for scores, weights in their place that are done with
-                    if (values || j >= 2) ok = mbar_wait_bounded((values ? p_full : pv_done) + w, (half_phase >> w) & 1);
+                    if (values || j >= 2) ok = mbar_wait_bounded((values ? p_full : pv_done) + w, (turn_phase >> w) & 1);
                     if constexpr (Q8) place = shared_place(tile++, values);
                     uint32_t slot[PARTS];
 #pragma unroll
@@ -310,7 +326,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                     }
                     place += 2;  // fp16: K and V parts lie in turn
                     if (!ok) break;
-                    if (values || j >= 2) half_phase ^= 1u << w;
+                    if (values || j >= 2) turn_phase ^= 1u << w;
                     tc_fence_after();
                     // hi hi, lo hi, hi lo (what is left out is 2^-22 of a product)
                     if (!values) {
@@ -321,10 +337,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                             for (int k = 0; k < HD / 16; ++k) {
                                 const uint32_t off = (k / 4) * L::COL + (k % 4) * 32;
                                 const uint64_t kd = tc_desc(ring + slot[part / 2] * L::TILE + off, 0);
-                                if constexpr (NARROW)
-                                    tc_mma_ts(tmem + w * 128, tmem + TM_QUERIES + (part == 1 ? HD / 2 : 0) + 8 * k, kd, id, part || k);
-                                else
-                                    tc_mma_ss(tmem + w * 128, tc_desc(qs + (part == 1 ? L::TILE : 0) + off, 0), kd, id, part || k);
+                                tc_mma_ts(tmem + w * 128, tmem + TM_QUERIES + (part == 1 ? HD / 2 : 0) + 8 * k, kd, id, part || k);
                             }
                         tc_commit(s_full + w);
                     } else {
@@ -332,44 +345,47 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                         for (int k = 0; k < n / 16; ++k)
 #pragma unroll
                             for (int part = 0; part < 1 + PARTS; ++part)
-                                tc_mma_ts(tmem + TM_SUMS + (NARROW ? 0 : w * HD), tmem + w * 128 + 32 * (k / 2) + (part == 1 ? 16 : 0) + 8 * (k & 1),
-                                          tc_desc(ring + slot[part / 2] * L::TILE + k * 2048, L::COL), id, part || k || j >= (NARROW ? 1 : 2));
+                                tc_mma_ts(tmem + TM_SUMS, tmem + w * 128 + 32 * (k / 2) + (part == 1 ? 16 : 0) + 8 * (k & 1),
+                                          tc_desc(ring + slot[part / 2] * L::TILE + k * 2048, L::COL), id, part || k || j);
                         tc_commit(pv_done + w);
                     }
 #pragma unroll
                     for (int i = 0; i < PARTS; ++i) tc_commit(empty + slot[i]);
                 }
-                // The last products of a half are not waited for here: keep its count.
-                if (!values) half_phase ^= (s.n > 0 ? 1u : 0u) | (s.n > 1 ? 2u : 0u);
+                // The last products of even and odd tiles are not waited for here: keep their count.
+                if (!values) turn_phase ^= (s.n > 0 ? 1u : 0u) | (s.n > 1 ? 2u : 0u);
             }
             if (!ok) *failed = 1;
         }
         __syncwarp();
     } else {
-        // ---- softmax: two threads have a query's row, a half of the tile's keys (then of the head's dims) each
-        const int w = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
+        // ---- softmax: SHARE threads have a query's row, an equal part of the tile's keys (then of the head's dims) each
+        constexpr int KEYS = SHARED_TILE / L::SHARE, DIMS = HD / L::SHARE;
+        const int part = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
-        const uint32_t st0 = lane_base + half * 64, ot = lane_base + TM_SUMS + (NARROW ? 0 : w * HD) + half * (HD / 2);
-        float* maxima = reinterpret_cast<float*>(smem + L::MAXIMA) + w * 2 * SHARED_QUERIES;
-        uint64_t* partner = pair + w * 4 + (warp & 3);
-        unsigned s_phase = 0, t_phase = 0, met = 0;  // scores seen and tiles weighed, a bit for each half's place; meetings with the row's other warp
+        const uint32_t ot = lane_base + TM_SUMS + part * DIMS;
+        float* maxima = reinterpret_cast<float*>(smem + L::MAXIMA);
+        unsigned s_phase = 0, t_phase = 0, met = 0;  // scores seen and tiles weighed, a bit for even and odd ones; meetings of a row's warps
         uint32_t tiles = 0, segs = 0;
         bool ok = true;
         const float c = a.scale * 1.4426950408889634f;
-        // Tell the row's other half x and hear its own; every lane of the warp returns the same in `good`.
-        auto exchange = [&](float x, bool& good) {
-            maxima[half * SHARED_QUERIES + r] = x;
+        // Tell the row's other threads x and have all of theirs joined.  (In turn in two places: who writes again
+        // has met them in between, so they have read.)
+        auto exchange = [&](float x, auto join) {
+            float* at = maxima + (met & 1) * L::SHARE * L::QUERIES + r;
+            at[part * L::QUERIES] = x;
             __syncwarp();
-            if (lane == 0) mbar_arrive(partner);
-            good = __all_sync(FULL_MASK, mbar_wait_bounded(partner, met++ & 1));
-            return maxima[(half ^ 1) * SHARED_QUERIES + r];
+            if (lane == 0) mbar_arrive(pair + (warp & 3));
+            ok = __all_sync(FULL_MASK, mbar_wait_bounded(pair + (warp & 3), met++ & 1));
+            float v = at[0];
+#pragma unroll
+            for (int i = 1; i < L::SHARE; ++i) v = join(v, at[i * L::QUERIES]);
+            return v;
         };
         SharedSeg s;
-        // Q8_0: eight warps make K (part 0) and V (1) of tile j of the segment, codes times scales as
-        // fp16 pairs hi + lo (19 bits, so exactly): a thread takes 16 codes of rows trow + 32 i.  Where no group
-        // has more than 64 queries the second half of the warps does nothing else; else the half that
-        // weighs the tile does it in between.
-        const bool makes = Q8 && NARROW && w == 1;
+        // Q8_0: warps 8 .. 15 make K (part 0) and V (1) of tile j of the segment, codes times scales as fp16
+        // pairs hi + lo (19 bits, so exactly): a thread takes 16 codes of rows trow + 32 i.
+        const bool makes = Q8 && warp >= 8;
         const int t = threadIdx.x & 255;
         // 8 lanes write 4 chunks of two rows, which the swizzle puts into different banks
         const int chunk = (lane & 3) | ((lane >> 4) << 2), trow = (t >> 5) * 4 + ((lane >> 2) & 3);
@@ -386,34 +402,25 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             if (a.fault) *a.fault = 1;
             return -1;
         };
-        // The thread's codes and scales of a part: to registers, or (ahead) to its own place in shared memory, as
-        // loads to registers would be waited for together with those of the part after.
+        // The thread's codes and scales of a part, to its own place in shared memory: loads to registers would be
+        // waited for together with those of the part after.
         const uint32_t mine_at = smem_u32(smem + L::CODES) + t * 16, scales_at = smem_u32(smem + L::CODES) + 256 * 4 * 16 + t * 4;
-        auto fetch = [&](int rows, int part, uint32_t T, Codes* f) {
+        auto fetch = [&](int rows, int part, uint32_t T) {
             const uint8_t* codes = (part ? a.vq : a.kq) + 16 * chunk;
-            const __half* scales = (part ? a.vs : a.ks) + (chunk >> 1);
+            const __half* scales = (part ? a.vs : a.ks) + (chunk >> 2) * 2;  // the pair that the chunk's is of
             const unsigned have = __ballot_sync(FULL_MASK, rows >= 0);
             if (!part && t == 0) runs[T & 7] = (uint8_t)have;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // the warp's rows of i are of one run
                 const int first = __shfl_sync(FULL_MASK, rows, 2 * i + (t >> 7));
-                const bool good = first >= 0;
+                const bool good = first >= 0;  // else zeros: a scale of 0, whatever the codes
                 const int64_t at = good ? first + (trow & 15) : 0;
-                if (f) {
-                    f->v[i] = make_uint4(0, 0, 0, 0);
-                    f->d[i] = __ushort_as_half(0);  // whatever the codes, 0
-                    if (good) {
-                        f->v[i] = ldg_nc_v4(codes + at * 128);
-                        f->d[i] = __ldg(scales + at * 4);
-                    }
-                } else {
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mine_at + i * 256 * 16), "l"(codes + at * 128),
-                                 "r"(good ? 16 : 0)
-                                 : "memory");
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(scales_at + i * 256 * 4),
-                                 "l"((const __half*)((uintptr_t)(scales + at * 4) & ~(uintptr_t)3)), "r"(good ? 4 : 0)
-                                 : "memory");
-                }
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mine_at + i * 256 * 16), "l"(codes + at * 128),
+                             "r"(good ? 16 : 0)
+                             : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(scales_at + i * 256 * 4), "l"(scales + at * 4),
+                             "r"(good ? 4 : 0)
+                             : "memory");
             }
         };
         auto landed = [&](Codes& f) {
@@ -465,11 +472,6 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             }
             return true;
         };
-        auto convert = [&](int j, int part) {
-            Codes f;
-            fetch(look_up(s, j), part, tiles + j, &f);
-            return make(part, tiles + j, f);
-        };
         if (makes) {
             // the parts in the order of their places, a part's codes fetched while the one before is made
             for (int x = x0; x < x1 && ok;) {
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                     j = k < 2 ? (s.n > 1 ? k : 0) : part ? (k == 2 * s.n - 1 ? s.n - 1 : k / 2 - 1) : (k + 1) / 2;
                 };
                 int newest = 0, before = look_up(s, 0), rows = before, ahead = s.n > 1 ? look_up(s, 1) : -1;  // of K `newest`, the one before, the next
-                fetch(rows, 0, tiles, nullptr);
+                fetch(rows, 0, tiles);
                 for (int k = 0; k < 2 * s.n && ok; ++k) {
                     Codes f;
                     landed(f);
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                             rows = ahead;
                             newest = j;
                         }
-                        fetch(part && j < newest ? before : rows, part, tiles + j, nullptr);
+                        fetch(part && j < newest ? before : rows, part, tiles + j);
                         if (!part && j + 1 < s.n) ahead = look_up(s, j + 1);
                     }
                     part_of(k, j, part);
@@ -503,68 +505,58 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 tiles += s.n;
             }
         }
-        const bool weighs = !NARROW || (w == 0 && (warp & 2) == 0);
+        const bool weighs = (warp & 3) * 32 < L::QUERIES && part < L::SHARE;
         for (int x = weighs ? x0 : x1; x < x1 && ok;) {
             s.at(a, x, x1 - x);
             x += s.n;
             const int nq = n_queries(s), q0 = first_query(s);
             if (nq <= 0) continue;
             const int keys = a.keys[s.g];
-            const int qi = q0 + r;
-            const float* src = a.q + ((size_t)(a.lead[s.g] + qi / a.gq) * a.nh + (size_t)s.h * a.gq + qi % a.gq) * HD;
-            if constexpr (NARROW) {  // the queries: half of row r's dims, hi and lo
+            {  // the queries, hi and lo: the thread's dims of row r
+                const int qi = q0 + r;
+                const float* src = a.q + ((size_t)(a.lead[s.g] + qi / a.gq) * a.nh + (size_t)s.h * a.gq + qi % a.gq) * HD + part * DIMS;
+                const uint32_t qt = lane_base + TM_QUERIES + part * (DIMS / 2);
+                constexpr int STEP = DIMS < 32 ? DIMS : 32;
 #pragma unroll
-                for (int k = 0; k < HD / 64; ++k) {  // 32 dims
-                    uint32_t p[32];
+                for (int k = 0; k < DIMS / STEP; ++k) {
+                    uint32_t p[STEP];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < STEP / 4; ++i) {
                         float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (r < nq) u = *reinterpret_cast<const float4*>(src + half * (HD / 2) + 32 * k + 4 * i);
+                        if (r < nq) u = *reinterpret_cast<const float4*>(src + STEP * k + 4 * i);
                         p[2 * i] = f2_hi(u.x, u.y), p[2 * i + 1] = f2_hi(u.z, u.w);
-                        p[16 + 2 * i] = f2_lo(u.x, u.y), p[16 + 2 * i + 1] = f2_lo(u.z, u.w);
+                        p[STEP / 2 + 2 * i] = f2_lo(u.x, u.y), p[STEP / 2 + 2 * i + 1] = f2_lo(u.z, u.w);
                     }
-                    const uint32_t qt = lane_base + TM_QUERIES + half * (HD / 4) + 16 * k;
-                    tc_st16(qt, p);
-                    tc_st16(qt + HD / 2, p + 16);
+                    if constexpr (STEP == 32) {
+                        tc_st16(qt + 16 * k, p);
+                        tc_st16(qt + 16 * k + HD / 2, p + 16);
+                    } else {
+                        tc_st8(qt, p);
+                        tc_st8(qt + HD / 2, p + 8);
+                    }
                 }
                 tc_wait_st();
                 tc_fence_before();
-            } else {  // a quarter of row r's dims
-                const int part = w * 2 + half;
-#pragma unroll
-                for (int i = 0; i < HD / 32; ++i) {
-                    float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
-                    if (r < nq) {
-                        u = *reinterpret_cast<const float4*>(src + part * (HD / 4) + 8 * i);
-                        v = *reinterpret_cast<const float4*>(src + part * (HD / 4) + 8 * i + 4);
-                    }
-                    const int chunk = part * (HD / 32) + i;  // 8 dims
-                    uint8_t* dst = smem + L::Q + (chunk >> 3) * L::COL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
-                    *reinterpret_cast<uint4*>(dst) = make_uint4(f2_hi(u.x, u.y), f2_hi(u.z, u.w), f2_hi(v.x, v.y), f2_hi(v.z, v.w));
-                    *reinterpret_cast<uint4*>(dst + L::TILE) = make_uint4(f2_lo(u.x, u.y), f2_lo(u.z, u.w), f2_lo(v.x, v.y), f2_lo(v.z, v.w));
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
             const bool idle = (warp & 3) * 32 >= nq;  // no query in the warp's rows: what its weights hold does not matter
             float m = -INFINITY;                      // the maximum that the weights are taken against, in units of 1 / c
             float2 l = make_float2(0.0f, 0.0f);
-            if constexpr (Q8 && !NARROW) ok = s.n <= w || convert(w, 0);
-            // A product P V of the tile before last, or earlier, of place b is done when its scores are there.
+            // The product P V of tile j, the last weighed of the even or odd ones, is done.
             auto values_done = [&](int j) { return __all_sync(FULL_MASK, mbar_wait_bounded(pv_done + (j & 1), ((t_phase >> (j & 1)) & 1) ^ 1)); };
-            for (int j = NARROW ? 0 : w; j < s.n && ok; j += NARROW ? 1 : 2) {
+            for (int j = 0; j < s.n && ok; ++j) {
                 const int b = j & 1;
-                const uint32_t st = st0 + b * 128;
-                // the thread's keys of the tile, and their 16-key runs with a page
-                const int n = min(64, keys - (s.tile + j) * SHARED_TILE - half * 64);
+                const uint32_t st = lane_base + b * 128 + part * KEYS;
+                const int n = min(KEYS, keys - (s.tile + j) * SHARED_TILE - part * KEYS);  // the thread's keys of the tile
                 ok = __all_sync(FULL_MASK, mbar_wait_bounded(s_full + b, (s_phase >> b) & 1));
                 s_phase ^= 1u << b;
                 if (!ok) break;
                 tc_fence_after();
-                const unsigned have = runs[(tiles + j) & 7] >> (half * 4);
+                const unsigned have = runs[(tiles + j) & 7] >> (part * (KEYS / 16));  // their 16-key runs that have a page
                 if (!idle) {
-                    const bool all = n == 64 && (have & 15) == 15;
+                    constexpr int STEPS = KEYS / 32;
+                    const bool all = n == KEYS && (have & ((1u << (KEYS / 16)) - 1)) == (1u << (KEYS / 16)) - 1;
                     uint32_t v[32];  // 32 keys' scores
                     auto load = [&](int k) {
                         tc_ld32(st + 32 * k, v);
@@ -577,14 +569,13 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                     };
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                    for (int k = 0; k < STEPS; ++k)
                         if (32 * k < n) {
                             load(k);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(v[i]));
                         }
-                    float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    mx = fmaxf(mx, exchange(mx, ok));
+                    const float mx = exchange(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), [](float x, float y) { return fmaxf(x, y); });
                     if (!ok) break;
                     float f = 1.0f;
                     if (m == -INFINITY) {
@@ -594,29 +585,26 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                         f = tc_exp2((m - mx) * c);
                         m = mx;
                     }
-                    if (j >= (NARROW ? 1 : 2) && __any_sync(FULL_MASK, f != 1.0f)) {
-                        if (NARROW) {
-                            ok = values_done(j - 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
+                    if (j && __any_sync(FULL_MASK, f != 1.0f)) {
+                        ok = values_done(j - 1);
+                        if (!ok) break;
+                        tc_fence_after();
                         l.x *= f;
                         l.y *= f;
 #pragma unroll 1
-                        for (int k = 0; k < HD / 64; ++k) {
-                            uint32_t o[32];
-                            tc_ld32(ot + 32 * k, o);
-                            tc_wait_ld(o);
+                        for (int k = 0; k < DIMS / 16; ++k) {
+                            uint32_t o[16];
+                            tc_ld16(ot + 16 * k, o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tc_st32(ot + 32 * k, o);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tc_st16(ot + 16 * k, o);
                         }
                     }
                     const float mc = m == -INFINITY ? 0.0f : m * c;  // 2^(-inf) where no key is seen
 #pragma unroll
-                    for (int k = 1; k >= 0; --k) {  // the second half is still here
+                    for (int k = STEPS - 1; k >= 0; --k) {  // the last are still here
                         if (32 * k < n) {
-                            if (k == 0 && n > 32) load(0);
+                            if (STEPS > 1 && k == 0 && n > 32) load(0);
                             uint32_t p[32];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
@@ -638,33 +626,29 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + b);
                 t_phase ^= 1u << b;
-                if constexpr (Q8 && !NARROW) ok = convert(j, 1) && (j + 2 >= s.n || convert(j + 2, 0));
             }
             tiles += s.n;
-            // ---- the half's record of the segment's tiles
-            float* rec = a.part + (shared_row(a, s.g, s.h, s.pass, set, q0 - s.pass * a.side * SHARED_QUERIES + r) * 2 + w) * PAGED_REC(HD);
-            float* second = NARROW ? rec + PAGED_REC(HD) : rec;
-            if ((NARROW || s.n <= w) && r < nq && !half) *reinterpret_cast<float2*>(second + HD) = make_float2(-INFINITY, 0.0f);  // none
-            if (ok && (NARROW || s.n > w)) {
-                ok = values_done(NARROW || ((s.n - 1) & 1) == w ? s.n - 1 : s.n - 2);
+            // ---- the record of the segment's tiles
+            if (ok) {
+                ok = values_done(s.n - 1);
                 tc_fence_after();
-                if (ok && !idle) {
-                    const float sum = l.x + l.y, other = exchange(sum, ok);
-#pragma unroll 1
-                    for (int k = 0; k < HD / 64; ++k) {
-                        uint32_t v[32];
-                        tc_ld32(ot + 32 * k, v);
-                        tc_wait_ld(v);
-                        if (r < nq) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<uint4*>(rec + half * (HD / 2) + 32 * k + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                        }
-                    }
-                    if (r < nq && !half) *reinterpret_cast<float2*>(rec + HD) = make_float2(m * a.scale, sum + other);
-                }
-                tc_fence_before();
             }
+            if (ok && !idle) {
+                float* rec = a.part + shared_row(a, s.g, s.h, s.pass, set, q0 - s.pass * a.side * L::QUERIES + r) * PAGED_REC(HD);
+                const float sum = exchange(l.x + l.y, [](float x, float y) { return x + y; });
+#pragma unroll 1
+                for (int k = 0; k < DIMS / 16; ++k) {
+                    uint32_t v[16];
+                    tc_ld16(ot + 16 * k, v);
+                    if (r < nq) {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            *reinterpret_cast<uint4*>(rec + part * DIMS + 16 * k + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    }
+                }
+                if (r < nq && !part) *reinterpret_cast<float2*>(rec + HD) = make_float2(m * a.scale, sum);
+            }
+            tc_fence_before();
             // All are done with the queries and with tensor memory.
             __syncwarp();
             if (lane == 0) mbar_arrive(q_free);
@@ -688,11 +672,11 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
 // ---- launch ----------------------------------------------------------------------
 cudaError_t encode_fp16_2d(CUtensorMap* out, const void* base, long inner, long rows, int box_inner, int box_rows);
 
-template <int HD, bool Q8, bool NARROW>
+template <int HD, bool Q8>
 static cudaError_t launch_shared_as(const SharedArgs& a, const void* k, const void* v, int dev, cudaStream_t s) {
     static OncePerDevice once;
     cudaError_t e = once(dev, [] {
-        return cudaFuncSetAttribute(shared_kernel<HD, Q8, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, SharedSmem<HD, Q8, NARROW>::TOTAL);
+        return cudaFuncSetAttribute(shared_kernel<HD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SharedSmem<HD, Q8>::TOTAL);
     });
     if (e != cudaSuccess) return e;
     CUtensorMap mk = {}, mv = {};
@@ -708,19 +692,14 @@ static cudaError_t launch_shared_as(const SharedArgs& a, const void* k, const vo
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(a.sets * a.side);
     cfg.blockDim = dim3(SH_THREADS);
-    cfg.dynamicSmemBytes = SharedSmem<HD, Q8, NARROW>::TOTAL;
+    cfg.dynamicSmemBytes = SharedSmem<HD, Q8>::TOTAL;
     cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, shared_kernel<HD, Q8, NARROW>, a, mk, mv);
+    return cudaLaunchKernelEx(&cfg, shared_kernel<HD, Q8>, a, mk, mv);
 }
 
 cudaError_t launch_shared(const SharedArgs& a, int hd, bool q8, const void* k, const void* v, int dev, cudaStream_t s) {
-#define KD_SHARED(NARROW_)                                                            \
-    return q8         ? launch_shared_as<128, true, NARROW_>(a, k, v, dev, s)          \
-           : hd == 64 ? launch_shared_as<64, false, NARROW_>(a, k, v, dev, s)          \
-                      : launch_shared_as<128, false, NARROW_>(a, k, v, dev, s)
-    if (a.narrow) KD_SHARED(true);
-    KD_SHARED(false);
-#undef KD_SHARED
+    if (q8) return launch_shared_as<128, true>(a, k, v, dev, s);
+    return hd == 64 ? launch_shared_as<64, false>(a, k, v, dev, s) : launch_shared_as<128, false>(a, k, v, dev, s);
 }
 
 }  // namespace kd

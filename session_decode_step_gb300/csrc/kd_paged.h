@@ -57,10 +57,11 @@ __host__ __device__ inline int paged_blocks(int keys) { return (keys + PAGED_BLO
 
 // Groups whose shared keys are read once for all their queries (kd_attn_shared.cu).  A pass of a
 // (group, KV head) is its keys, in tiles of SHARED_TILE, for up to `side` tiles of
-// SHARED_QUERIES queries, one for each of the CTAs side by side; the tiles of all passes are one
+// shared_queries() queries, one for each of the CTAs side by side; the tiles of all passes are one
 // sequence, of which every one of the `sets` of CTAs takes an equal share.
-// A set's CTAs leave two records (one for each half of their warps) of each query that has tiles there.
-constexpr int SHARED_TILE = 128, SHARED_QUERIES = 128, SHARED_MAX_SIDE = 8;
+// A set's CTAs leave a record of each query that has tiles there.
+constexpr int SHARED_TILE = 128, SHARED_MAX_QUERIES = 128, SHARED_MAX_SIDE = 8;
+__host__ __device__ constexpr int shared_queries(bool q8) { return q8 ? 64 : SHARED_MAX_QUERIES; }
 constexpr int SHARED_MAX_GROUPS = KD_PAGED_MAX_SEQS / 2;  // of two sessions at least
 constexpr int SHARED_MAX_CTAS = 256;
 struct SharedArgs {
@@ -72,7 +73,7 @@ struct SharedArgs {
     const __half *ks, *vs;
     int* status;  // [CTA]: 1 where a bounded wait ran out
     int table_ld, n_pages, ps, rows, box_runs, nh, nkv, gq, n_groups, side, sets;
-    int narrow;  // no group has more than 64 queries
+    int tile_queries;  // shared_queries()
     float scale;
     Shares share;  // of all tiles, among the sets
     int keys[SHARED_MAX_GROUPS], queries[SHARED_MAX_GROUPS];  // shared keys (whole pages), sessions times gq
@@ -80,12 +81,12 @@ struct SharedArgs {
     int first[SHARED_MAX_GROUPS + 1];                         // first tile of its first head's first pass, in tiles / nkv
     uint8_t lead[SHARED_MAX_GROUPS];                          // first session
     __host__ __device__ int tiles(int g) const { return (keys[g] + SHARED_TILE - 1) / SHARED_TILE; }
-    __host__ __device__ int passes(int g) const { return (queries[g] + SHARED_QUERIES * side - 1) / (SHARED_QUERIES * side); }
+    __host__ __device__ int passes(int g) const { return (queries[g] + tile_queries * side - 1) / (tile_queries * side); }
 };
-// The record pair of query `query` of a pass that set `set` leaves: pairs of different (pass, set)s do not
+// The record of query `query` of a pass that set `set` leaves: those of different (pass, set)s do not
 // overlap, as each step along the sequence moves on by a pass's queries, or by a set's most.
 __host__ __device__ inline int64_t shared_row(const SharedArgs& a, int g, int h, int pass, int set, int query) {
-    const int pass_queries = SHARED_QUERIES * a.side;
+    const int pass_queries = a.tile_queries * a.side;
     return (int64_t)a.before[g] * a.nkv + (int64_t)h * a.queries[g] + (int64_t)pass * pass_queries + (int64_t)set * pass_queries + query;
 }
 cudaError_t launch_shared(const SharedArgs& a, int hd, bool q8, const void* k, const void* v, int dev, cudaStream_t s);

@@ -29,15 +29,14 @@ static void shared_plan(SharedArgs& t, int sms) {
     if (sms > SHARED_MAX_CTAS) sms = SHARED_MAX_CTAS;
     double best = 0;
     int most = 1;
-    for (int g = 0; g < t.n_groups; ++g)
-        if ((t.queries[g] + SHARED_QUERIES - 1) / SHARED_QUERIES > most) most = (t.queries[g] + SHARED_QUERIES - 1) / SHARED_QUERIES;
-    t.narrow = 1;
-    for (int g = 0; g < t.n_groups; ++g)
-        if (t.queries[g] > SHARED_QUERIES / 2) t.narrow = 0;
+    for (int g = 0; g < t.n_groups; ++g) {
+        const int tiles = (t.queries[g] + t.tile_queries - 1) / t.tile_queries;
+        if (tiles > most) most = tiles;
+    }
     for (int side = 1; side <= most && side <= SHARED_MAX_SIDE && side <= sms; ++side) {
         double work = 0;
         for (int g = 0; g < t.n_groups; ++g) {
-            const int per = SHARED_QUERIES * side;
+            const int per = t.tile_queries * side;
             work += (double)t.tiles(g) * ((t.queries[g] + per - 1) / per);
         }
         const double time = work / (sms / side);
@@ -110,7 +109,7 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
                 }
             }
             if (once) {
-                shared_tiles += (int64_t)(shared / SHARED_TILE + 1) * (group_rows[g] * (nh / nkv) / SHARED_QUERIES + 1);
+                shared_tiles += (int64_t)(shared / SHARED_TILE + 1) * (group_rows[g] * (nh / nkv) / shared_queries(q8) + 1);
                 if (shared_tiles > 0x7fffffff / nkv) return failf(KD_ERR_UNSUPPORTED, "%s: 2^31 or more blocks of keys", fn);
                 sh.lead[sh.n_groups] = (uint8_t)b;
                 sh.keys[sh.n_groups] = shared;
@@ -176,6 +175,7 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
         sh.nkv = nkv;
         sh.gq = nh / nkv;
         sh.scale = a.scale;
+        sh.tile_queries = shared_queries(q8);
         shared_plan(sh, sms);
         a.late_wait = 1;
         sh.kq = (const uint8_t*)kp;
@@ -196,8 +196,8 @@ extern "C" {
 size_t kd_attn_paged_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
     using namespace kd;
     if (B < 1 || B > KD_PAGED_MAX_SEQS || !paged_shape(n_heads, n_kv_heads, head_dim, false) || n_kv_heads > PAGED_MAX_KV_HEADS) return 0;
-    // of shared keys: two records for every query, and for as many as a CTA takes per CTA
-    const size_t shared = B < 2 ? 0 : 2 * ((size_t)B * n_heads + (size_t)SHARED_MAX_CTAS * SHARED_QUERIES);
+    // of shared keys: a record for every query, and for as many as a CTA takes per CTA
+    const size_t shared = B < 2 ? 0 : (size_t)B * n_heads + (size_t)SHARED_MAX_CTAS * SHARED_MAX_QUERIES;
     return PAGED_HEAD_BYTES + (paged_records(B, n_kv_heads) * (n_heads / n_kv_heads) + shared) * PAGED_REC(head_dim) * sizeof(float);
 }
 
