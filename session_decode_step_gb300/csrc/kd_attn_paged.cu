@@ -69,16 +69,12 @@ __device__ __forceinline__ uint32_t paged_u8(uint32_t v, uint32_t sel) {
 // A block of a (session, head), and the next ones in order.
 struct PagedAt {
     int b, h, blk, nb;  // session, KV head, block of nb
+    // Block x, the first of the CTA's.
     __device__ __forceinline__ void seek(const PagedArgs& a, int x) {
-        int lo = 0, hi = a.B;  // first[lo] nkv <= x < first[hi] nkv: the session
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.first[mid] * a.nkv <= x) lo = mid;
-            else hi = mid;
-        }
-        b = lo;
-        nb = a.first[lo + 1] - a.first[lo];
-        const int r = x - a.first[lo] * a.nkv;
+        b = a.hint[(int)blockIdx.x * PAGED_HINTS / a.ctas];
+        while (x >= a.s[b + 1].first * a.nkv) ++b;
+        nb = a.s[b + 1].first - a.s[b].first;
+        const int r = x - a.s[b].first * a.nkv;
         h = r / nb;
         blk = r - h * nb;
     }
@@ -92,7 +88,7 @@ struct PagedAt {
                 nb = 1;
                 return;
             }
-            nb = a.first[b + 1] - a.first[b];
+            nb = a.s[b + 1].first - a.s[b].first;
         } while (nb == 0);
     }
 };
@@ -110,30 +106,32 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
     const uint32_t kbase = smem_u32(paged_smem + warp * L::WARP), vbase = kbase + L::PART;
     float* joined = reinterpret_cast<float*>(paged_smem + PAGED_WARPS * L::WARP);  // [warp][GQ][REC]
 
+    const int x0 = a.share.begin(blockIdx.x), x1 = a.share.begin(blockIdx.x + 1);
+    int left = x1 - x0;  // blocks still to take
+    PagedAt at;
+    if (left > 0) at.seek(a, x0);
     pdl_launch_dependents();
     if (!a.late_wait) pdl_wait();
     if (blockIdx.x == 0) {
         if (threadIdx.x == 0 && !a.late_wait) *a.err = 0;
-        for (int b = 0; b < a.B; ++b)  // sessions without keys
-            if (a.to[b] == 0)
+        for (int b = 0; a.empty && b < a.B; ++b)  // sessions without keys
+            if (a.s[b].to == 0)
                 for (int i = threadIdx.x; i < a.nh * HD; i += PAGED_WARPS * 32) a.out[(size_t)b * a.nh * HD + i] = __float2half_rn(0.0f);
     }
-    const int x0 = a.share.begin(blockIdx.x), x1 = a.share.begin(blockIdx.x + 1);
-    int left = x1 - x0;  // blocks still to take
     if (left <= 0) {
         if (a.late_wait) pdl_wait();
         return;
     }
 
     // The warp's piece of a block: keys [key, key + n) of the session (n <= 0: none).
-    auto first_key = [&](const PagedAt& t) { return a.from[t.b] + (t.blk * PAGED_WARPS + warp) * PAGED_KEYS; };
-    auto keys = [&](const PagedAt& t) { return min(PAGED_KEYS, a.to[t.b] - first_key(t)); };
+    auto first_key = [&](const PagedAt& t) { return a.s[t.b].from + (t.blk * PAGED_WARPS + warp) * PAGED_KEYS; };
+    auto keys = [&](const PagedAt& t) { return min(PAGED_KEYS, a.s[t.b].to - first_key(t)); };
     // The page of 16 keys (lane 0 and 1: the piece's two runs); -1 where there is none.
     auto look_up = [&](const PagedAt& t, bool have) {
         int page = -1;
         const int key = first_key(t) + 16 * lane;
-        if (have && lane < 2 && key < a.to[t.b]) {
-            page = a.table[(int64_t)(key < a.lead_keys[t.b] ? a.lead[t.b] : t.b) * a.table_ld + key / a.ps];
+        if (have && lane < 2 && key < a.s[t.b].to) {
+            page = a.table[(int64_t)(key < a.s[t.b].lead_keys ? a.s[t.b].lead : t.b) * a.table_ld + key / a.ps];
             if ((unsigned)page >= (unsigned)a.n_pages) {
                 if (a.fault) *a.fault = 1;
                 page = -1;
@@ -179,9 +177,7 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
         paged_commit();
     };
 
-    PagedAt at, nxt, nn;
-    at.seek(a, x0);
-    nxt = at;
+    PagedAt nxt = at, nn;
     nxt.next(a);
     nn = nxt;
     if (left > 1) nn.next(a);
@@ -486,8 +482,8 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
                 }
             }
             __syncthreads();
-            const int s0 = a.first[at.b] * a.nkv + at.h * at.nb;  // the (session, head)'s blocks
-            const bool whole = a.from[at.b] == 0 && x0 <= s0 && s0 + at.nb <= x1;
+            const int s0 = a.s[at.b].first * a.nkv + at.h * at.nb;  // the (session, head)'s blocks
+            const bool whole = a.s[at.b].from == 0 && x0 <= s0 && s0 + at.nb <= x1;
             float* rec = a.part + ((size_t)blockIdx.x + (size_t)at.b * a.nkv + at.h) * GQ * REC;
             __half* out = a.out + ((size_t)at.b * a.nh + (size_t)at.h * GQ) * HD;
             for (int i = threadIdx.x; i < GQ * (HD / 4); i += PAGED_WARPS * 32) {
@@ -550,19 +546,19 @@ __global__ void __launch_bounds__(PAGED_MERGE_WARPS * 32) paged_merge_kernel(con
     __shared__ float2 ends[PAGED_MERGE_WARPS];  // a warp's maximum and denominator
     const int qh = blockIdx.x, b = blockIdx.y, gq = a.nh / a.nkv, h = qh / gq, i = qh - h * gq;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nb = a.first[b + 1] - a.first[b], g = a.group[b];
+    const int nb = a.s[b + 1].first - a.s[b].first, g = a.s[b].group;
     // n records of its own keys, then one of each set of CTAs that has some of the shared keys
     const float *rec = nullptr, *shared = nullptr;
     int n = 0, sets = 0;
     size_t set_step = 0;
     if (nb) {
-        const int s0 = a.first[b] * a.nkv + h * nb, c0 = a.share.taker(s0);
+        const int s0 = a.s[b].first * a.nkv + h * nb, c0 = a.share.taker(s0);
         n = a.share.taker(s0 + nb - 1) - c0 + 1;
         rec = a.part + (((size_t)c0 + (size_t)b * a.nkv + h) * gq + i) * REC;
     }
     if (g != SHARED_NONE) {
-        const int per = sh.tile_queries * sh.side, query = (b - sh.lead[g]) * gq + i, pass = query / per, T = sh.tiles(g);
-        const int s0 = sh.first[g] * sh.nkv + (h * sh.passes(g) + pass) * T, c0 = sh.share.taker(s0);
+        const int per = sh.tile_queries * sh.side, query = (b - sh.g[g].lead) * gq + i, pass = query / per, T = sh.tiles(g);
+        const int s0 = sh.g[g].first * sh.nkv + (h * sh.passes(g) + pass) * T, c0 = sh.share.taker(s0);
         sets = sh.share.taker(s0 + T - 1) - c0 + 1;
         shared = sh.part + shared_row(sh, g, h, pass, c0, query - pass * per) * REC;
         set_step = (size_t)per * REC;

@@ -170,8 +170,8 @@ struct SharedSeg {
     int g = 0, h, pass, tile, n;  // tiles [tile, tile + n)
     // from x on, at most `left` of them; g: a group at or before x's
     __device__ __forceinline__ void at(const SharedArgs& a, int x, int left) {
-        while (x >= a.first[g + 1] * a.nkv) ++g;
-        const int r = x - a.first[g] * a.nkv, T = a.tiles(g), u = r / T;
+        while (x >= a.g[g + 1].first * a.nkv) ++g;
+        const int r = x - a.g[g].first * a.nkv, T = a.tiles(g), u = r / T;
         tile = r - u * T;
         h = u;
         pass = 0;
@@ -234,25 +234,27 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     const uint32_t tmem = *tmem_at;
     const int set = blockIdx.x / a.side, mine = blockIdx.x - set * a.side;  // of the CTAs side by side
     const int x0 = a.share.begin(set), x1 = a.share.begin(set + 1);
+    SharedSeg head;  // the CTA's first segment
+    head.at(a, x0, x1 - x0);
     pdl_wait();
     pdl_launch_dependents();  // after the wait: the kernel behind this one relies on it, and reads at once
     const int box = a.box_runs;  // 16-key runs of a copy's box
     // The first of the CTA's queries in a segment's group, and how many (<= 0: none).
     auto first_query = [&](const SharedSeg& s) { return (s.pass * a.side + mine) * L::QUERIES; };
-    auto n_queries = [&](const SharedSeg& s) { return min(L::QUERIES, a.queries[s.g] - first_query(s)); };
+    auto n_queries = [&](const SharedSeg& s) { return min(L::QUERIES, a.g[s.g].queries - first_query(s)); };
 
     if (warp == SH_COPY) {
         if constexpr (!Q8) {
         // ---- copies: K and V of each tile, boxes of whole 16-key runs within a page
         uint32_t slot = 0, phase = 0, tiles = 0;
         bool ok = true;
-        SharedSeg s;
+        SharedSeg s = head;
         for (int x = x0; x < x1 && ok;) {
-            s.at(a, x, x1 - x);
+            if (x != x0) s.at(a, x, x1 - x);
             x += s.n;
             if (n_queries(s) <= 0) continue;
-            const int keys = a.keys[s.g];
-            const int* row = a.table + (int64_t)a.lead[s.g] * a.table_ld;
+            const int keys = a.g[s.g].keys;
+            const int* row = a.table + (int64_t)a.g[s.g].lead * a.table_ld;
             auto look_up = [&](int t) {  // lane i: the page of the tile's run i
                 const int key = t * SHARED_TILE + 16 * lane;
                 return lane < SHARED_TILE / 16 && key < keys ? row[key / a.ps] : -1;
@@ -303,12 +305,12 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             unsigned turn_phase = 0;  // of p_full (values) or pv_done (scores), a bit for even and odd tiles
             bool ok = true;
             const uint32_t ring = smem_u32(smem + L::RING);
-            SharedSeg s;
+            SharedSeg s = head;
             for (int x = x0; x < x1 && ok;) {
-                s.at(a, x, x1 - x);
+                if (x != x0) s.at(a, x, x1 - x);
                 x += s.n;
                 if (n_queries(s) <= 0) continue;
-                const int keys = a.keys[s.g];
+                const int keys = a.g[s.g].keys;
                 if (!values) {
                     ok = mbar_wait_bounded(q_full, q_phase);  // the segment before is done with then, too
                     q_phase ^= 1;
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             for (int i = 1; i < L::SHARE; ++i) v = join(v, at[i * L::QUERIES]);
             return v;
         };
-        SharedSeg s;
+        SharedSeg s = head;
         // Q8_0: warps 8 .. 15 make K (part 0) and V (1) of tile j of the segment, codes times scales as fp16
         // pairs hi + lo (19 bits, so exactly): a thread takes 16 codes of rows trow + 32 i.
         const bool makes = Q8 && warp >= 8;
@@ -396,8 +398,8 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         // Lane i < 8: the first cache row of run i of tile j (-1: there is none).
         auto look_up = [&](const SharedSeg& s, int j) {
             const int key = (s.tile + j) * SHARED_TILE + 16 * lane;
-            if (lane >= 8 || key >= a.keys[s.g]) return -1;
-            const int in_table = key / a.ps, page = a.table[(int64_t)a.lead[s.g] * a.table_ld + in_table];
+            if (lane >= 8 || key >= a.g[s.g].keys) return -1;
+            const int in_table = key / a.ps, page = a.table[(int64_t)a.g[s.g].lead * a.table_ld + in_table];
             if ((unsigned)page < (unsigned)a.n_pages) return (page * a.nkv + s.h) * a.ps + key - in_table * a.ps;
             if (a.fault) *a.fault = 1;
             return -1;
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         if (makes) {
             // the parts in the order of their places, a part's codes fetched while the one before is made
             for (int x = x0; x < x1 && ok;) {
-                s.at(a, x, x1 - x);
+                if (x != x0) s.at(a, x, x1 - x);
                 x += s.n;
                 if (n_queries(s) <= 0) continue;
                 // part k of 2 n: K0 [K1] V0 K2 V1 .., V last
@@ -507,14 +509,14 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         }
         const bool weighs = (warp & 3) * 32 < L::QUERIES && part < L::SHARE;
         for (int x = weighs ? x0 : x1; x < x1 && ok;) {
-            s.at(a, x, x1 - x);
+            if (x != x0) s.at(a, x, x1 - x);
             x += s.n;
             const int nq = n_queries(s), q0 = first_query(s);
             if (nq <= 0) continue;
-            const int keys = a.keys[s.g];
+            const int keys = a.g[s.g].keys;
             {  // the queries, hi and lo: the thread's dims of row r
                 const int qi = q0 + r;
-                const float* src = a.q + ((size_t)(a.lead[s.g] + qi / a.gq) * a.nh + (size_t)s.h * a.gq + qi % a.gq) * HD + part * DIMS;
+                const float* src = a.q + ((size_t)(a.g[s.g].lead + qi / a.gq) * a.nh + (size_t)s.h * a.gq + qi % a.gq) * HD + part * DIMS;
                 const uint32_t qt = lane_base + TM_QUERIES + part * (DIMS / 2);
                 constexpr int STEP = DIMS < 32 ? DIMS : 32;
 #pragma unroll

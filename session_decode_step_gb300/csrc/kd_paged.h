@@ -28,7 +28,7 @@ struct Shares {
 constexpr int PAGED_WARPS = 4;
 constexpr int PAGED_KEYS = 32;  // keys of a warp's piece
 constexpr int PAGED_BLOCK = PAGED_WARPS * PAGED_KEYS;
-constexpr int PAGED_MAX_CTAS = 1024;
+constexpr int PAGED_MAX_CTAS = 1024, PAGED_HINTS = 64;
 __host__ __device__ constexpr int PAGED_REC(int hd) { return hd + 4; }  // floats of one head's record: o, m, l
 
 struct PagedArgs {
@@ -44,14 +44,19 @@ struct PagedArgs {
     int late_wait;              // started beside the kernel before, whose end it awaits at its own
     float scale;
     Shares share;               // of all blocks, among the CTAs
-    // Session b reads keys [from[b], to[b]); those before lead_keys[b] through session lead[b]'s table.
-    int from[KD_PAGED_MAX_SEQS], to[KD_PAGED_MAX_SEQS], lead_keys[KD_PAGED_MAX_SEQS];
-    int first[KD_PAGED_MAX_SEQS + 1];  // first block of the session's first head, in blocks / nkv
-    uint8_t lead[KD_PAGED_MAX_SEQS];
-    uint8_t group[KD_PAGED_MAX_SEQS];  // the session's group in SharedArgs, or SHARED_NONE
+    // Session b reads keys [from, to); those before lead_keys through session lead's table.  A session's
+    // words lie together: each cache line of a launch's arguments that is touched first costs a
+    // microsecond or so.
+    struct Session {
+        int first;      // first block of its first head, in blocks / nkv; session B has the end
+        int from, to, lead_keys;
+        short lead;
+        short group;    // in SharedArgs, or SHARED_NONE
+    } s[KD_PAGED_MAX_SEQS + 1];
+    int empty;                  // some session has no keys
+    short hint[PAGED_HINTS];    // a session at or before the first one of CTAs [i ctas / PAGED_HINTS, ..)
 };
-constexpr int SHARED_NONE = 255;
-static_assert(KD_PAGED_MAX_SEQS <= 256, "sessions in a byte");
+constexpr int SHARED_NONE = -1;
 
 __host__ __device__ inline int paged_blocks(int keys) { return (keys + PAGED_BLOCK - 1) / PAGED_BLOCK; }
 
@@ -76,18 +81,20 @@ struct SharedArgs {
     int tile_queries;  // shared_queries()
     float scale;
     Shares share;  // of all tiles, among the sets
-    int keys[SHARED_MAX_GROUPS], queries[SHARED_MAX_GROUPS];  // shared keys (whole pages), sessions times gq
-    int before[SHARED_MAX_GROUPS];                            // queries of the groups before it
-    int first[SHARED_MAX_GROUPS + 1];                         // first tile of its first head's first pass, in tiles / nkv
-    uint8_t lead[SHARED_MAX_GROUPS];                          // first session
-    __host__ __device__ int tiles(int g) const { return (keys[g] + SHARED_TILE - 1) / SHARED_TILE; }
-    __host__ __device__ int passes(int g) const { return (queries[g] + tile_queries * side - 1) / (tile_queries * side); }
+    struct Group {
+        int first;          // first tile of its first head's first pass, in tiles / nkv; group n_groups has the end
+        int keys, queries;  // shared keys (whole pages), sessions times gq
+        int before;         // queries of the groups before it
+        int lead;           // first session
+    } g[SHARED_MAX_GROUPS + 1];
+    __host__ __device__ int tiles(int i) const { return (g[i].keys + SHARED_TILE - 1) / SHARED_TILE; }
+    __host__ __device__ int passes(int i) const { return (g[i].queries + tile_queries * side - 1) / (tile_queries * side); }
 };
 // The record of query `query` of a pass that set `set` leaves: those of different (pass, set)s do not
 // overlap, as each step along the sequence moves on by a pass's queries, or by a set's most.
 __host__ __device__ inline int64_t shared_row(const SharedArgs& a, int g, int h, int pass, int set, int query) {
     const int pass_queries = a.tile_queries * a.side;
-    return (int64_t)a.before[g] * a.nkv + (int64_t)h * a.queries[g] + (int64_t)pass * pass_queries + (int64_t)set * pass_queries + query;
+    return (int64_t)a.g[g].before * a.nkv + (int64_t)h * a.g[g].queries + (int64_t)pass * pass_queries + (int64_t)set * pass_queries + query;
 }
 cudaError_t launch_shared(const SharedArgs& a, int hd, bool q8, const void* k, const void* v, int dev, cudaStream_t s);
 

@@ -30,14 +30,14 @@ static void shared_plan(SharedArgs& t, int sms) {
     double best = 0;
     int most = 1;
     for (int g = 0; g < t.n_groups; ++g) {
-        const int tiles = (t.queries[g] + t.tile_queries - 1) / t.tile_queries;
+        const int tiles = (t.g[g].queries + t.tile_queries - 1) / t.tile_queries;
         if (tiles > most) most = tiles;
     }
     for (int side = 1; side <= most && side <= SHARED_MAX_SIDE && side <= sms; ++side) {
         double work = 0;
         for (int g = 0; g < t.n_groups; ++g) {
             const int per = t.tile_queries * side;
-            work += (double)t.tiles(g) * ((t.queries[g] + per - 1) / per);
+            work += (double)t.tiles(g) * ((t.g[g].queries + per - 1) / per);
         }
         const double time = work / (sms / side);
         if (side == 1 || time <= best * 1.02) {
@@ -48,12 +48,12 @@ static void shared_plan(SharedArgs& t, int sms) {
     int64_t first = 0;
     int before = 0;
     for (int g = 0; g < t.n_groups; ++g) {
-        t.first[g] = (int)first;
-        t.before[g] = before;
+        t.g[g].first = (int)first;
+        t.g[g].before = before;
         first += (int64_t)t.tiles(g) * t.passes(g);
-        before += t.queries[g];
+        before += t.g[g].queries;
     }
-    t.first[t.n_groups] = (int)first;
+    t.g[t.n_groups].first = (int)first;
     const int64_t total = first * t.nkv;
     t.sets = sms / t.side;
     if (t.sets > total) t.sets = (int)total;
@@ -86,9 +86,10 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
     for (int b = 0; b < B; ++b) {
         if (lens[b] < 0 || lens[b] > (int64_t)table_ld * ps)
             return failf(KD_ERR_POSITION, "%s: length %d in tables of %d pages of %d", fn, lens[b], table_ld, ps);
-        a.to[b] = lens[b];
-        a.lead[b] = (uint8_t)b;
-        a.group[b] = SHARED_NONE;
+        a.s[b].to = lens[b];
+        a.s[b].lead = (short)b;
+        a.s[b].group = SHARED_NONE;
+        a.empty |= lens[b] == 0;
     }
     if (n_groups) {
         int b = 0;
@@ -101,30 +102,30 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
             for (int i = b; i < b + group_rows[g]; ++i) {
                 if (group_prefix[g] < 0 || group_prefix[g] > lens[i])
                     return failf(KD_ERR_POSITION, "%s: prefix %d of a session of length %d", fn, group_prefix[g], lens[i]);
-                a.lead[i] = (uint8_t)b;
-                a.lead_keys[i] = shared;
+                a.s[i].lead = (short)b;
+                a.s[i].lead_keys = shared;
                 if (once) {
-                    a.from[i] = shared;
-                    a.group[i] = (uint8_t)sh.n_groups;
+                    a.s[i].from = shared;
+                    a.s[i].group = (short)sh.n_groups;
                 }
             }
             if (once) {
                 shared_tiles += (int64_t)(shared / SHARED_TILE + 1) * (group_rows[g] * (nh / nkv) / shared_queries(q8) + 1);
                 if (shared_tiles > 0x7fffffff / nkv) return failf(KD_ERR_UNSUPPORTED, "%s: 2^31 or more blocks of keys", fn);
-                sh.lead[sh.n_groups] = (uint8_t)b;
-                sh.keys[sh.n_groups] = shared;
-                sh.queries[sh.n_groups++] = group_rows[g] * (nh / nkv);
+                sh.g[sh.n_groups].lead = (short)b;
+                sh.g[sh.n_groups].keys = shared;
+                sh.g[sh.n_groups++].queries = group_rows[g] * (nh / nkv);
             }
             b += group_rows[g];
         }
         if (b != B) return failf(KD_ERR_INVALID_ARG, "%s: groups of %d sessions in all, B=%d", fn, b, B);
     }
     for (int b = 0; b < B; ++b) {
-        a.first[b] = (int)total;
-        total += paged_blocks(a.to[b] - a.from[b]);
+        a.s[b].first = (int)total;
+        total += paged_blocks(a.s[b].to - a.s[b].from);
         if (total > 0x7fffffff / nkv) return failf(KD_ERR_UNSUPPORTED, "%s: 2^31 or more blocks of keys", fn);
     }
-    a.first[B] = (int)total;
+    a.s[B].first = (int)total;
     int dev = 0, sms = 0;
     KD_TRY(cudaGetDevice(&dev));
     KD_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
@@ -151,11 +152,16 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
     const int blocks = (int)(total * nkv);
     a.ctas = blocks < 1 ? 1 : blocks < slots ? blocks : slots;
     a.share = Shares(blocks, a.ctas);
+    for (int i = 0, b = 0; i < PAGED_HINTS && blocks; ++i) {
+        const int x = a.share.begin((int)((int64_t)i * a.ctas / PAGED_HINTS));
+        while (x >= a.s[b + 1].first * nkv) ++b;
+        a.hint[i] = (short)b;
+    }
     bool merge = sh.n_groups > 0;
     for (int b = 0; b < B && !merge; ++b) {
-        const int nb = a.first[b + 1] - a.first[b];
+        const int nb = a.s[b + 1].first - a.s[b].first;
         for (int h = 0; h < nkv && nb && !merge; ++h) {
-            const int s0 = a.first[b] * nkv + h * nb;
+            const int s0 = a.s[b].first * nkv + h * nb;
             merge = a.share.taker(s0) != a.share.taker(s0 + nb - 1);
         }
     }
