@@ -84,10 +84,13 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* v) {
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-__device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t* v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+// 8 columns of 16 rows: a lane has columns 2 (lane % 4) and the next of row lane / 4 (v0, v1) and of
+// the row 8 below (v2, v3).  Where rows lie apart in memory, four lanes read or write 32 bytes or more of one.
+__device__ __forceinline__ void tc_st_16x8(uint32_t addr, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v0), "r"(v1), "r"(v2), "r"(v3) : "memory");
+}
+__device__ __forceinline__ void tc_ld_16x8(uint32_t addr, uint32_t (&v)[4]) {  // (to be waited for)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
 __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t* v) {  // and waits
     asm volatile(
@@ -514,27 +517,27 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             const int nq = n_queries(s), q0 = first_query(s);
             if (nq <= 0) continue;
             const int keys = a.g[s.g].keys;
-            {  // the queries, hi and lo: the thread's dims of row r
-                const int qi = q0 + r;
-                const float* src = a.q + ((size_t)(a.g[s.g].lead + qi / a.gq) * a.nh + (size_t)s.h * a.gq + qi % a.gq) * HD + part * DIMS;
+            {  // the queries, hi and lo: the warp's dims of its 32 rows, 16 dims of 16 rows at a time
                 const uint32_t qt = lane_base + TM_QUERIES + part * (DIMS / 2);
-                constexpr int STEP = DIMS < 32 ? DIMS : 32;
 #pragma unroll
-                for (int k = 0; k < DIMS / STEP; ++k) {
-                    uint32_t p[STEP];
+                for (int rh = 0; rh < 2; ++rh) {
+                    float4 u[2][DIMS / 16];
 #pragma unroll
-                    for (int i = 0; i < STEP / 4; ++i) {
-                        float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (r < nq) u = *reinterpret_cast<const float4*>(src + STEP * k + 4 * i);
-                        p[2 * i] = f2_hi(u.x, u.y), p[2 * i + 1] = f2_hi(u.z, u.w);
-                        p[STEP / 2 + 2 * i] = f2_lo(u.x, u.y), p[STEP / 2 + 2 * i + 1] = f2_lo(u.z, u.w);
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = (warp & 3) * 32 + 16 * rh + 8 * e + (lane >> 2), qi = q0 + row;
+                        const float* src = a.q + ((size_t)(a.g[s.g].lead + qi / a.gq) * a.nh + (size_t)s.h * a.gq + qi % a.gq) * HD + part * DIMS + 4 * (lane & 3);
+#pragma unroll
+                        for (int k = 0; k < DIMS / 16; ++k) {
+                            u[e][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (row < nq) u[e][k] = *reinterpret_cast<const float4*>(src + 16 * k);
+                        }
                     }
-                    if constexpr (STEP == 32) {
-                        tc_st16(qt + 16 * k, p);
-                        tc_st16(qt + 16 * k + HD / 2, p + 16);
-                    } else {
-                        tc_st8(qt, p);
-                        tc_st8(qt + HD / 2, p + 8);
+#pragma unroll
+                    for (int k = 0; k < DIMS / 16; ++k) {
+                        const float4 x = u[0][k], y = u[1][k];
+                        const uint32_t at = qt + ((uint32_t)(16 * rh) << 16) + 8 * k;
+                        tc_st_16x8(at, f2_hi(x.x, x.y), f2_hi(x.z, x.w), f2_hi(y.x, y.y), f2_hi(y.z, y.w));
+                        tc_st_16x8(at + HD / 2, f2_lo(x.x, x.y), f2_lo(x.z, x.w), f2_lo(y.x, y.y), f2_lo(y.z, y.w));
                     }
                 }
                 tc_wait_st();
@@ -636,19 +639,22 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 tc_fence_after();
             }
             if (ok && !idle) {
-                float* rec = a.part + shared_row(a, s.g, s.h, s.pass, set, q0 - s.pass * a.side * L::QUERIES + r) * PAGED_REC(HD);
+                float* rec = a.part + shared_row(a, s.g, s.h, s.pass, set, q0 - s.pass * a.side * L::QUERIES) * PAGED_REC(HD);
                 const float sum = exchange(l.x + l.y, [](float x, float y) { return x + y; });
-#pragma unroll 1
-                for (int k = 0; k < DIMS / 16; ++k) {
-                    uint32_t v[16];
-                    tc_ld16(ot + 16 * k, v);
-                    if (r < nq) {
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            *reinterpret_cast<uint4*>(rec + part * DIMS + 16 * k + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                for (int rh = 0; rh < 2; ++rh) {
+                    const int row = (warp & 3) * 32 + 16 * rh + (lane >> 2);
+                    float* to = rec + (size_t)row * PAGED_REC(HD) + part * DIMS + 2 * (lane & 3);
+#pragma unroll 4
+                    for (int k = 0; k < DIMS / 8; ++k) {
+                        uint32_t v[4];
+                        tc_ld_16x8(ot + ((uint32_t)(16 * rh) << 16) + 8 * k, v);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3])::"memory");
+                        if (row < nq) *reinterpret_cast<uint2*>(to + 8 * k) = make_uint2(v[0], v[1]);
+                        if (row + 8 < nq) *reinterpret_cast<uint2*>(to + 8 * PAGED_REC(HD) + 8 * k) = make_uint2(v[2], v[3]);
                     }
                 }
-                if (r < nq && !part) *reinterpret_cast<float2*>(rec + HD) = make_float2(m * a.scale, sum);
+                if (r < nq && !part) *reinterpret_cast<float2*>(rec + (size_t)r * PAGED_REC(HD) + HD) = make_float2(m * a.scale, sum);
             }
             tc_fence_before();
             // All are done with the queries and with tensor memory.
