@@ -214,6 +214,9 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
             }
         }
     };
+    // Weights are held as e^UP times their value, so that those below fp16's normal range, 2^-14 of the
+    // largest, are whole pairs, too (Q8_0 scales them with the value scales).
+    constexpr float UP = Q8 ? 0.0f : 6.0f;
     // m: the running maximum of head 4j + c, l: the lane's part of its sum, o = sum p v
     // (Q8_0: times 2^oe, so that weights times scales stay in fp16's normal range).
     float m[NQ], l[NQ], o[NU / 2][NQ][4];
@@ -327,8 +330,8 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
                 for (int t = 0; t < KT; ++t) mx = fmaxf(mx, fmaxf(sv[j][t][0], sv[j][t][1]));
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, x));
-                const float ref = mx == -INFINITY ? 0.0f : mx;
-                f[j] = m[j] == mx ? 1.0f : expf(__fsub_rn(m[j], ref));
+                const float ref = mx == -INFINITY ? 0.0f : __fsub_rn(mx, UP);
+                f[j] = m[j] == mx ? 1.0f : expf(__fsub_rn(m[j], mx == -INFINITY ? 0.0f : mx));
                 same = same && f[j] == 1.0f;
                 m[j] = mx;
                 float s = 0.0f;
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
                             dst[16 * mt + g + 8] = hi;
                         }
                     }
-                    if (g == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(m[j], l[j]);
+                    if (g == 0) *reinterpret_cast<float2*>(dst + HD) = make_float2(__fsub_rn(m[j], UP), l[j]);
                 }
             }
             __syncthreads();

@@ -8,8 +8,8 @@
 // rate (one operand of 4 KB a product of 64 cycles takes half of it) to K and V; scores of two tiles are there
 // in turn, so that one's products run under the other's exponentials.  Four threads hold a query's row, a quarter of
 // the tile's keys each, and tell each other their maxima.  The sums are rescaled only when the
-// maximum has grown by 2^8 or more (the weights, at most 2^8 then, lose nothing: they are pairs
-// of fp16).
+// maximum has grown by 2^8 or more (the weights lose nothing: they are pairs of fp16, held as 2^7
+// times their value, at most 2^15 then, so that those below 2^-14 of the largest are whole pairs, too).
 //
 // Queries and weights are fp16 pairs hi + lo, as in the kernel of the sessions' own
 // keys, two products each: 4 x 2 x 128^3 flops a tile of 128 keys and 128 queries, 2048 cycles, 1.1 us
@@ -145,6 +145,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 constexpr int SH_SOFT = 16;  // softmax warps (Q8_0: four, and eight that make K and V)
 constexpr int SH_COPY = SH_SOFT, SH_SCORES = SH_SOFT + 1, SH_VALUES = SH_SOFT + 2;  // the copies' and the products' warps
 constexpr int SH_THREADS = (SH_SOFT + 3) * 32;
+constexpr float SH_UP = 7.0f;
 
 template <int HD, bool Q8>
 struct SharedSmem {
@@ -333,7 +334,8 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                     if (!ok) break;
                     if (values || j >= 2) turn_phase ^= 1u << w;
                     tc_fence_after();
-                    // hi hi, lo hi, hi lo (what is left out is 2^-22 of a product)
+                    // lo hi, hi lo, hi hi: the small ones first, so that the scores' sums are rounded at their
+                    // own size in the last 8 products only (what is left out is 2^-22 of a product)
                     if (!values) {
                         const uint32_t id = tc_idesc(n, false);
 #pragma unroll
@@ -341,8 +343,8 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
 #pragma unroll
                             for (int k = 0; k < HD / 16; ++k) {
                                 const uint32_t off = (k / 4) * L::COL + (k % 4) * 32;
-                                const uint64_t kd = tc_desc(ring + slot[part / 2] * L::TILE + off, 0);
-                                tc_mma_ts(tmem + w * 128, tmem + TM_QUERIES + (part == 1 ? HD / 2 : 0) + 8 * k, kd, id, part || k);
+                                const uint64_t kd = tc_desc(ring + slot[Q8 && part == 1 ? PARTS - 1 : 0] * L::TILE + off, 0);
+                                tc_mma_ts(tmem + w * 128, tmem + TM_QUERIES + (part == 0 ? HD / 2 : 0) + 8 * k, kd, id, part || k);
                             }
                         tc_commit(s_full + w);
                     } else {
@@ -605,7 +607,9 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                             tc_st16(ot + 16 * k, o);
                         }
                     }
-                    const float mc = m == -INFINITY ? 0.0f : m * c;  // 2^(-inf) where no key is seen
+                    // 2^SH_UP times the weights, up to 2^15 with what the maximum has grown: so that small ones are
+                    // whole pairs of fp16, too (2^(-inf) where no key is seen)
+                    const float mc = m == -INFINITY ? 0.0f : m * c - SH_UP;
 #pragma unroll
                     for (int k = STEPS - 1; k >= 0; --k) {  // the last are still here
                         if (32 * k < n) {
@@ -654,7 +658,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                         if (row + 8 < nq) *reinterpret_cast<uint2*>(to + 8 * PAGED_REC(HD) + 8 * k) = make_uint2(v[2], v[3]);
                     }
                 }
-                if (r < nq && !part) *reinterpret_cast<float2*>(rec + (size_t)r * PAGED_REC(HD) + HD) = make_float2(m * a.scale, sum);
+                if (r < nq && !part) *reinterpret_cast<float2*>(rec + (size_t)r * PAGED_REC(HD) + HD) = make_float2(m * a.scale - SH_UP * 0.6931471806f, sum);
             }
             tc_fence_before();
             // All are done with the queries and with tensor memory.

@@ -19,8 +19,11 @@ constexpr int PAGED_HEAD_BYTES = 256 + SHARED_MAX_CTAS * 4;  // the workspace's 
 static size_t paged_records(int B, int nkv) { return (size_t)PAGED_MAX_CTAS + (size_t)B * nkv; }
 
 // A group's shared keys go to the kernel that reads them once where that saves its other sessions
-// this many bytes of reading.
-constexpr int64_t SHARED_SAVES = 8 << 20;
+// this many bytes of reading: the kernel costs some 4 us (7 on Q8_0 caches) of its own before it gains.  32 heads over 8 KV
+// heads of 128, each session with 128 keys of its own, read once / by each: 8 sessions of 512 keys (14 MB saved) 9.8 / 7.5 us,
+// of 1024 (28 MB) 10.0 / 10.8, of 4096 15.3 / 19.4; 16 of 512 (30 MB) 10.7 / 10.9, of 2048 14.9 / 19.6, of 8192 19 / 55; on
+// Q8_0 caches 16 of 512 (16 MB) 13.9 / 12.3, 8 of 2048 (30 MB) 13.6 / 14.8, 32 of 8192 35 / 130.
+constexpr int64_t SHARED_SAVES = 24 << 20;
 
 // Choose the sets of CTAs: `side` of them take a (group, head)'s tiles of queries side by side.
 // The time goes as the tiles of all passes over the sets; of equal ones the widest, which read each key

@@ -478,6 +478,87 @@ def test_large_groups(kdlib, q8, nh, nkv, hd):
         c.check(c.run(kdlib))
 
 
+# Prefixes whose reading for every session would cost more than 24 MB: taken once, on the tensor
+# cores.  Tiles of 128 keys and 128 (Q8_0: 64) queries with nothing, one 16-key run or nearly all left over, pages
+# smaller and larger than a tile, one tile of queries and many, groups of which only some qualify.
+@pytest.mark.parametrize("q8,nh,nkv,hd,ps,groups,own", [
+    (False, 32, 8, 128, 16, [(9, 1024)], 40), (False, 32, 8, 128, 48, [(9, 1010), (2, 48)], 100), (False, 32, 8, 128, 256, [(20, 769), (1, 300)], 30),
+    (False, 6, 3, 128, 16, [(60, 528), (50, 656)], 9), (False, 16, 2, 128, 64, [(70, 460), (3, 128), (128, 512)], 20), (False, 8, 8, 128, 128, [(33, 256)], 0),
+    (False, 8, 1, 64, 16, [(200, 656)], 5), (False, 4, 4, 64, 32, [(64, 530), (64, 416)], 33), (False, 14, 7, 64, 48, [(40, 400), (17, 1100)], 60),
+    (True, 32, 8, 128, 16, [(12, 1104)], 40), (True, 3, 3, 128, 32, [(64, 600), (90, 417)], 17), (True, 8, 1, 128, 48, [(150, 700), (100, 1000)], 3),
+    (True, 4, 2, 128, 256, [(80, 600), (120, 512), (2, 256)], 12), (True, 16, 4, 128, 16, [(160, 160)], 7),
+])
+def test_prefixes_read_once(kdlib, q8, nh, nkv, hd, ps, groups, own):
+    rng = np.random.default_rng(nh + ps)
+    lens = [p + int(rng.integers(0, own + 1)) for n, p in groups for _ in range(n)]
+    c = Attn(q8, nh, nkv, hd, ps, lens, groups, seed=nh + ps)
+    assert max((n - 1) * (p // ps * ps) * nkv * (272 if q8 else 4 * hd) for n, p in groups) >= 24 << 20
+    c.check(c.run(kdlib))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_prefixes_read_once_far_scores(kdlib, q8):
+    """Maxima that grow from tile to tile: the sums are rescaled; large and tiny values; small scores."""
+    for kscale, vscale in ((30.0, 1.0), (1.0, 200.0), (0.01, 1e-3)):
+        c = Attn(q8, 32, 8, 128, 32, [1300 + i for i in range(12)], [(12, 1290)], seed=4, kscale=kscale, vscale=vscale)
+        c.check(c.run(kdlib))
+    # keys in growing order: every tile has a new maximum for all queries
+    c = Attn(False, 32, 8, 128, 32, [1300 + i for i in range(12)], [(12, 1280)], seed=4)
+    lead = c.kv[0][0]
+    for b in range(12):
+        n = int(c.lens[b])
+        grow = np.linspace(0.05, 40.0, 1280)[None, :, None]
+        c.kv[b][0][:, :1280] = (lead[:, :1280] * grow if b == 0 else c.kv[0][0][:, :1280]).astype(np.float16)
+        if b == 0:
+            page, row = torch.from_numpy(c.pool.table[0, np.arange(1280) // 32].astype(np.int64)).cuda(), torch.from_numpy(np.arange(1280) % 32).cuda()
+            c.pool.planes[0][page, :, row] = torch.from_numpy(c.kv[0][0][:, :1280].astype(np.float16)).cuda().transpose(0, 1)
+    c.check(c.run(kdlib))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("ps", [16, 64])
+def test_prefixes_read_once_bad_pages(kdlib, q8, ps):
+    """Pages of the shared part and of the sessions' own that do not exist, a whole tile of them among them."""
+    c = Attn(q8, 32, 8, 128, ps, [1200 + 20 * i for i in range(14)], [(14, 1200 // ps * ps)], seed=6)
+    bad = [2, *range(256 // ps, 384 // ps), 1088 // ps]
+    for i, page in enumerate(bad):
+        c.pool.table[0, page] = (-1, c.pool.n_pages, 2 ** 31 - 1, -2 ** 31)[i % 4]
+    own = 1216 // ps
+    c.pool.table[5, own] = -5
+    c.table = c.pool.device_table()
+    shared = 1200 // ps * ps
+    seen = []
+    for b in range(14):
+        t = np.arange(int(c.lens[b]))
+        hidden = np.isin(t // ps, bad) & (t < shared)
+        if b == 5:
+            hidden |= t // ps == own
+        seen.append(t[~hidden])
+    c.check(c.run(kdlib, fault_is=1), seen)
+
+
+def test_prefixes_read_once_repeats_and_streams(kdlib):
+    """Two streams at once with a workspace each, the same bits every time; smaller calls in between on the same workspace."""
+    kd = kdlib
+    cases = [Attn(False, 32, 8, 128, 16, [2000 + 9 * i for i in range(24)], [(14, 1800), (10, 1900)], seed=9),
+             Attn(True, 16, 4, 128, 32, [1500 + i for i in range(40)], [(30, 1490), (10, 1000)], seed=10)]
+    small = Attn(False, 32, 8, 128, 16, [50, 0, 300], seed=11)
+    want, wanted = [c.run(kd) for c in cases], small.run(kd)
+    for c, w in zip(cases, want):
+        c.check(w)
+    streams, outs, ws = [torch.cuda.Stream() for _ in cases], [c.new_out() for c in cases], [c.workspace(kd) for c in cases]
+    out = small.new_out()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, s, o, w in zip(cases, streams, outs, ws):
+            c.call(kd, o, w, stream=s)
+        small.call(kd, out, ws[0], stream=streams[0])
+    torch.cuda.synchronize()
+    for w, o in zip(want + [wanted], outs + [out]):
+        assert np.array_equal(w.view(np.int16), o.cpu().numpy().view(np.int16))
+    assert kd.kd_attn_device_status(ws[0]) == 0 and kd.kd_attn_device_status(ws[1]) == 0
+
+
 @pytest.mark.parametrize("q8", [False, True])
 def test_far_scores_and_extreme_values(kdlib, q8):
     """Scores far apart (the running maximum moves), large and tiny values."""
