@@ -98,7 +98,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, 3) rope_kernel(const __grid_cons
                 T &hi = 2 * i + 1 < P ? a0.v[2 * i + 1 < P ? 2 * i + 1 : 0] : a1.v[2 * i + 1 >= P ? 2 * i + 1 - P : 0];
                 const float p = to_f(lo), q = to_f(hi);
                 const float2 r = rope_turn2<EXACT>(make_float2(p, q), make_float2(q, p), make_float2(ch[i], ch[i]),
-                                                   make_float2(cl[i], cl[i]), make_float2(-sh[i], sh[i]), make_float2(-sl[i], sl[i]));
+                                                   make_float2(cl[i], cl[i]), make_float2(-sh[i], sh[i]), make_float2(-sl[i], sl[i]),
+                                                   make_float2(-ch[i], -ch[i]), make_float2(sh[i], -sh[i]));
                 from_f(r.x, lo);
                 from_f(r.y, hi);
             }
@@ -110,7 +111,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, 3) rope_kernel(const __grid_cons
                 const float2 p = make_float2(to_f(a0.v[i]), to_f(a0.v[k])), q = make_float2(to_f(a1.v[i]), to_f(a1.v[k]));
                 const float2 c = make_float2(ch[i], ch[k]), s = make_float2(sh[i], sh[k]);
                 const float2 c2 = make_float2(cl[i], cl[k]), s2 = make_float2(sl[i], sl[k]);
-                const float2 rp = rope_turn2<EXACT>(p, q, c, c2, f2_neg(s), f2_neg(s2)), rq = rope_turn2<EXACT>(q, p, c, c2, s, s2);
+                const float2 nc = f2_neg(c), ns = f2_neg(s);
+                const float2 rp = rope_turn2<EXACT>(p, q, c, c2, ns, f2_neg(s2), nc, s), rq = rope_turn2<EXACT>(q, p, c, c2, s, s2, nc, ns);
                 from_f(rp.x, a0.v[i]);
                 from_f(rp.y, a0.v[k]);
                 from_f(rq.x, a1.v[i]);

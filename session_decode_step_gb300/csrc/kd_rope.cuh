@@ -129,20 +129,21 @@ __device__ __forceinline__ float2 f2_neg(float2 a) { return make_float2(-a.x, -a
 
 // Two results x c + y s at a time (the sign of the sine is the caller's); each of c and s the
 // sum of its two parts.  EXACT: rounded to fp32 once, up to about 2^-44 (products and the sum with
-// what their roundings left out); else to within two roundings, of the first parts alone.
+// what their roundings left out, formed with their signs turned, as pairs of operations cannot turn an
+// operand's); else to within two roundings, of the first parts alone.  nc, ns: -ch, -sh.
 template <bool EXACT>
-__device__ __forceinline__ float2 rope_turn2(float2 x, float2 y, float2 ch, float2 cl, float2 sh, float2 sl) {
+__device__ __forceinline__ float2 rope_turn2(float2 x, float2 y, float2 ch, float2 cl, float2 sh, float2 sl, float2 nc, float2 ns) {
     if constexpr (!EXACT) return f2_fma(x, ch, f2_mul(y, sh));
-    const float2 p = f2_mul(x, ch), q = f2_mul(y, sh), t = f2_add(p, q);
-    const float2 pe = f2_fma(x, ch, f2_neg(p)), qe = f2_fma(y, sh, f2_neg(q));
+    const float2 p = f2_mul(x, nc), q = f2_mul(y, ns), t = f2_add(p, q);     // all negative
+    const float2 left = f2_add(f2_fma(x, ch, p), f2_fma(y, sh, q));         // what the products left out
     const float2 minus = make_float2(-1.0f, -1.0f);
-    const float2 b = f2_fma(p, minus, t);  // what of t is q, and what either is off by
+    const float2 b = f2_fma(p, minus, t);                                   // what of t is q, and what either is off by
     const float2 te = f2_add(f2_fma(f2_fma(b, minus, t), minus, p), f2_fma(b, minus, q));
-    const float2 lo = f2_add(f2_add(te, f2_add(pe, qe)), f2_fma(x, cl, f2_mul(y, sl)));
-    float2 v = f2_add(t, lo);
+    const float2 lo = f2_add(f2_fma(te, minus, left), f2_fma(x, cl, f2_mul(y, sl)));
+    float2 v = f2_fma(t, minus, lo);
     if (!(fmaxf(fabsf(t.x), fabsf(t.y)) <= 3.402823466e38f)) {  // infinite: as the plain sum has it
-        if (!(fabsf(t.x) <= 3.402823466e38f)) v.x = t.x;
-        if (!(fabsf(t.y) <= 3.402823466e38f)) v.y = t.y;
+        if (!(fabsf(t.x) <= 3.402823466e38f)) v.x = -t.x;
+        if (!(fabsf(t.y) <= 3.402823466e38f)) v.y = -t.y;
     }
     return v;
 }
