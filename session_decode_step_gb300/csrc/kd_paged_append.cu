@@ -99,18 +99,20 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, 3) paged_append_kernel(cons
     const int heads = 2 * a.nkv + a.nh;
     const int h0 = (unit - token * a.groups) * a.per, h1 = min(heads, h0 + a.per);
     const int sub = lane / LANES, d = lane % LANES * 4;  // the head of the warp's, and the lane's dims d .. d + 3
-    auto source = [&](int h) -> const T* {
-        if (h < a.nkv) return (const T*)a.k + token * a.k_ld + (int64_t)h * HD;
-        if (h < 2 * a.nkv) return (const T*)a.v + token * a.v_ld + (int64_t)(h - a.nkv) * HD;
-        return (const T*)a.q + token * a.q_ld + (int64_t)(h - 2 * a.nkv) * HD;
-    };
+    // The warp's heads: [k0, k1) of K, [v0, v1) of V, [q0, q1) of the queries.
+    const int k0 = min(h0, a.nkv), k1 = min(h1, a.nkv);
+    const int v0 = min(max(h0 - a.nkv, 0), a.nkv), v1 = min(max(h1 - a.nkv, 0), a.nkv);
+    const int q0 = max(h0 - 2 * a.nkv, 0), q1 = max(h1 - 2 * a.nkv, 0);
+    const T* ksrc = (const T*)a.k + token * a.k_ld + (k0 + sub) * HD;
+    const T* vsrc = (const T*)a.v + token * a.v_ld + (v0 + sub) * HD;
+    const T* qsrc = (const T*)a.q + token * a.q_ld + (int64_t)(q0 + sub) * HD;
     Four<T> raw[U];
-    auto load = [&](int h) {
+    // U flights of heads, `left` of them there
+    auto load = [&](const T* src, int left) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int hh = h + i * ROWS + sub;
-            if (hh < h1) {
-                const T* p = source(hh) + d;
+        for (int i = 0; i < U; ++i)
+            if (i * ROWS + sub < left) {
+                const T* p = src + i * ROWS * HD + d;
                 if constexpr (VEC) {
                     raw[i] = *reinterpret_cast<const Four<T>*>(p);
                 } else {
@@ -118,9 +120,11 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, 3) paged_append_kernel(cons
                     for (int e = 0; e < 4; ++e) raw[i].v[e] = p[e];
                 }
             }
-        }
     };
-    load(h0);
+    // the first flight before the angles
+    if (k0 < k1) load(ksrc, k1 - k0);
+    else if (v0 < v1) load(vsrc, v1 - v0);
+    else load(qsrc, q1 - q0);
     // the token's session, its position and the row that it goes to
     int lo = 0, hi = a.n_seqs;  // first[lo] <= token < first[hi]
     while (hi - lo > 1) {
@@ -138,7 +142,7 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, 3) paged_append_kernel(cons
     const bool shuffles = half % 4 == 0;
     const int partner = lane + (a.r.pairs ? 0 : d < half ? half / 4 : -(half / 4));
     float ch[4], cl[4], sh[4], sl[4];  // the sines with the sign that they are added with
-    if (turned) {
+    if (turned && (k0 < k1 || q0 < q1)) {
         float2 c, s;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -152,76 +156,90 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, 3) paged_append_kernel(cons
         if (a.fault && h0 < 2 * a.nkv && lane == 0) *a.fault = 1;
         page = -1;
     }
-    for (int h = h0; h < h1; h += U * ROWS) {
-        if (h > h0) load(h);
+    // The lane's values of flight i in fp32, rotated.
+    auto values = [&](int i, const T* src, bool have, bool rotates, float (&x)[4]) {
+        float o[4];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (h + i * ROWS >= h1) break;
-            const int hh = h + i * ROWS + sub;
-            const bool value = hh >= a.nkv && hh < 2 * a.nkv;
-            float x[4], o[4];
+        for (int e = 0; e < 4; ++e) x[e] = in_f(raw[i].v[e]);
+        if (!rotates || !a.rotate) return;
+        if (a.r.pairs) {
+            o[0] = x[1], o[1] = x[0], o[2] = x[3], o[3] = x[2];
+        } else if (shuffles) {
+            if constexpr (sizeof(T) == 2) {
+                const uint2 w = *reinterpret_cast<const uint2*>(&raw[i]);
+                uint2 r;
+                r.x = __shfl_sync(FULL_MASK, w.x, partner);
+                r.y = __shfl_sync(FULL_MASK, w.y, partner);
+                const Four<T> f = *reinterpret_cast<const Four<T>*>(&r);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = in_f(raw[i].v[e]);
-            if (a.rotate) {
-                if (a.r.pairs) {
-                    o[0] = x[1], o[1] = x[0], o[2] = x[3], o[3] = x[2];
-                } else if (shuffles) {
-                    if constexpr (sizeof(T) == 2) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(&raw[i]);
-                        uint2 r;
-                        r.x = __shfl_sync(FULL_MASK, w.x, partner);
-                        r.y = __shfl_sync(FULL_MASK, w.y, partner);
-                        const Four<T> f = *reinterpret_cast<const Four<T>*>(&r);
+                for (int e = 0; e < 4; ++e) o[e] = in_f(f.v[e]);
+            } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[e] = in_f(f.v[e]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[e] = __shfl_sync(FULL_MASK, x[e], partner);
-                    }
-                } else {
-                    const T* p = hh < h1 ? source(hh) : source(h0);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = d + e < a.r.rot ? in_f(p[d + e < half ? d + e + half : d + e - half]) : 0.0f;
-                }
-                if (turned && !value) {
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const float2 r = rope_turn2<true>(make_float2(x[e], x[e + 1]), make_float2(o[e], o[e + 1]),
-                                                          make_float2(ch[e], ch[e + 1]), make_float2(cl[e], cl[e + 1]),
-                                                          make_float2(sh[e], sh[e + 1]), make_float2(sl[e], sl[e + 1]),
-                                                          make_float2(-ch[e], -ch[e + 1]), make_float2(-sh[e], -sh[e + 1]));
-                        x[e] = r.x;  // rot is even, but the last lane may have two dims of it only
-                        x[e + 1] = r.y;
-                        if (d + e + 2 >= a.r.rot) break;
-                    }
-                }
+                for (int e = 0; e < 4; ++e) o[e] = __shfl_sync(FULL_MASK, x[e], partner);
             }
-            uint32_t code = 0;
-            __half scale{};
-            if constexpr (Q8) {  // as q8_quant: 8 lanes hold a block
-                if (hh < 2 * a.nkv) {  // the whole warp's head
+        } else {
+            const T* p = src + i * ROWS * HD;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = have && d + e < a.r.rot ? in_f(p[d + e < half ? d + e + half : d + e - half]) : 0.0f;
+        }
+        if (turned) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float2 r = rope_turn2<true>(make_float2(x[e], x[e + 1]), make_float2(o[e], o[e + 1]),
+                                                  make_float2(ch[e], ch[e + 1]), make_float2(cl[e], cl[e + 1]),
+                                                  make_float2(sh[e], sh[e + 1]), make_float2(sl[e], sl[e + 1]),
+                                                  make_float2(-ch[e], -ch[e + 1]), make_float2(-sh[e], -sh[e + 1]));
+                x[e] = r.x;  // rot is even, but the last lane may have two dims of it only
+                x[e + 1] = r.y;
+                if (d + e + 2 >= a.r.rot) break;
+            }
+        }
+    };
+    // Rows of K or V from head `first` on, `left` of them.
+    auto rows = [&](const T* src, bool loaded, bool rotates, int first, int left, void* dst, __half* scales) {
+        int64_t row = ((int64_t)page * a.nkv + first + sub) * a.ps + in_page;
+        for (; left > 0; left -= U * ROWS, src += U * ROWS * HD, row += (int64_t)U * ROWS * a.ps) {
+            if (!loaded) load(src, left);
+            loaded = false;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (i * ROWS >= left) break;
+                const bool have = i * ROWS + sub < left;
+                const int64_t at = row + (int64_t)i * ROWS * a.ps;
+                float x[4];
+                values(i, src, have, rotates, x);
+                if constexpr (Q8) {  // as q8_quant: 8 lanes hold a block
                     float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
                     for (int b = 1; b < 8; b <<= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, b));
                     const float dd = __fdiv_rn(m, 127.0f);
-                    scale = __float2half_rn(dd);
-                    code = q8_codes(x, dd);
-                }
-            }
-            if (hh >= h1) continue;
-            if (hh >= 2 * a.nkv) {
-                *reinterpret_cast<float4*>(a.q_out + ((int64_t)token * a.nh + hh - 2 * a.nkv) * HD + d) = make_float4(x[0], x[1], x[2], x[3]);
-            } else if (page >= 0) {
-                const int64_t row = ((int64_t)page * a.nkv + (value ? hh - a.nkv : hh)) * a.ps + in_page;
-                if constexpr (Q8) {
-                    reinterpret_cast<uint32_t*>(value ? a.vp : a.kp)[row * (HD / 4) + lane] = code;
-                    if ((lane & 7) == 0) (value ? a.vs : a.ks)[row * (HD / 32) + (lane >> 3)] = scale;
-                } else {
+                    const uint32_t code = q8_codes(x, dd);
+                    if (page >= 0) {
+                        reinterpret_cast<uint32_t*>(dst)[at * (HD / 4) + lane] = code;
+                        if ((lane & 7) == 0) scales[at * (HD / 32) + (lane >> 3)] = __float2half_rn(dd);
+                    }
+                } else if (have && page >= 0) {
                     const __half2 w0 = __floats2half2_rn(x[0], x[1]), w1 = __floats2half2_rn(x[2], x[3]);
-                    *reinterpret_cast<uint2*>((__half*)(value ? a.vp : a.kp) + row * HD + d) =
+                    *reinterpret_cast<uint2*>((__half*)dst + at * HD + d) =
                         make_uint2(*reinterpret_cast<const uint32_t*>(&w0), *reinterpret_cast<const uint32_t*>(&w1));
                 }
             }
+        }
+    };
+    rows(ksrc, true, true, k0, k1 - k0, a.kp, a.ks);
+    rows(vsrc, k0 >= k1, false, v0, v1 - v0, a.vp, a.vs);
+    bool loaded = k0 >= k1 && v0 >= v1;
+    float* out = a.q_out + ((int64_t)token * a.nh + q0 + sub) * HD + d;
+    for (int left = q1 - q0; left > 0; left -= U * ROWS, qsrc += U * ROWS * HD, out += U * ROWS * HD) {
+        if (!loaded) load(qsrc, left);
+        loaded = false;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (i * ROWS >= left) break;
+            const bool have = i * ROWS + sub < left;
+            float x[4];
+            values(i, qsrc, have, true, x);
+            if (have) *reinterpret_cast<float4*>(out + i * ROWS * HD) = make_float4(x[0], x[1], x[2], x[3]);
         }
     }
 }
