@@ -1,12 +1,15 @@
 // kd_rope.cu -- rotary positions: the plan on the host, and rows of heads rotated
 // in place or to another place.
 //
-// A thread holds both halves of P pairs (16 bytes each way where sizes and alignment
-// allow, P = 4 in fp32 and 8 in 16 bits; else two pairs or one at a time), forms their
-// angles once and takes them through its share of the token's heads, four heads' loads
-// in flight.  As the pair never leaves the thread, x may be written in place.  fp32
-// results are rounded once (the angle and the products are carried as pairs of fp32);
-// fp16 and bf16 ones are formed in fp32, whose error is 2^-13 and 2^-16 of theirs.
+// A thread holds both halves of four pairs (of two or one where sizes or alignment do not allow that), forms
+// their angles once and takes them through its share of the token's heads, four heads' loads in flight;
+// dims that pass move in the same chunks.  As a pair never leaves the thread, x may be written in place.  fp32
+// results are rounded once (the angle and the products are carried as pairs of fp32); fp16
+// and bf16 ones are formed in fp32, whose error is 2^-13 and 2^-16 of theirs.
+//
+// Bound by memory for many tokens: 8191 tokens of 40 fp16 heads of 128 (168 MB) 27.4 us, 6.1 TB/s, 0.90 of the measured
+// copy; with eight pairs a thread 30.4 us (half the threads fit), interleaved pairs of 8192 x 32 heads 25.5 against 26.7 us.
+// Eight tokens of 32 fp32 heads take 2.3 us, an empty launch 2.1.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -60,19 +63,13 @@ __global__ void __launch_bounds__(ROPE_THREADS, 3) rope_kernel(const __grid_cons
     const int token = (int)(unit / a.groups), chunk = threadIdx.x;
     if (token >= a.tokens) return;
     const int h0 = (int)(unit - (int64_t)token * a.groups) * a.per, h1 = min(a.heads, h0 + a.per);
+    // The chunk's two vectors: of P pairs, or behind them of dims that pass unchanged.
+    const bool turned = chunk < a.nr;
+    if (!turned && a.x == a.out) return;
+    const int d0 = PAIRS ? 2 * P * chunk : turned ? P * chunk : a.r.rot + 2 * P * (chunk - a.nr);
+    const int d1 = PAIRS || !turned ? d0 + P : d0 + a.r.rot / 2;
     const T* x = (const T*)a.x + token * a.ld;
     T* out = (T*)a.out + token * a.ld_out;
-    if (chunk >= a.nr) {  // dims that pass unchanged
-        if (a.x == a.out) return;
-        const int d = a.r.rot + (chunk - a.nr) * P;
-        for (int h = h0; h < h1; ++h)
-            *reinterpret_cast<V*>(out + (int64_t)h * a.hd + d) = *reinterpret_cast<const V*>(x + (int64_t)h * a.hd + d);
-        return;
-    }
-    // the two vectors of the thread's pairs
-    const int d0 = PAIRS ? 2 * P * chunk : P * chunk, d1 = PAIRS ? d0 + P : d0 + a.r.rot / 2;
-    const int pos = a.pos[token];
-    float ch[P], cl[P], sh[P], sl[P];
     V u[U], w[U];
     auto load = [&](int h) {
 #pragma unroll
@@ -83,25 +80,35 @@ __global__ void __launch_bounds__(ROPE_THREADS, 3) rope_kernel(const __grid_cons
             }
     };
     load(h0);
+    float ch[P], cl[P], sh[P], sl[P];
+    if (turned) {
+        const int pos = a.pos[token];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        float2 c, s;
-        rope_angle<EXACT>(turns[P * chunk + i], pos, a.r.mh, a.r.ml, tab, c, s);
-        ch[i] = c.x, cl[i] = c.y, sh[i] = s.x, sl[i] = s.y;
+        for (int i = 0; i < P; ++i) {
+            float2 c, s;
+            rope_angle<EXACT>(turns[min(P * chunk + i, KD_ROPE_MAX_DIM / 2 - 1)], pos, a.r.mh, a.r.ml, tab, c, s);
+            ch[i] = c.x, cl[i] = c.y, sh[i] = s.x, sl[i] = s.y;
+        }
     }
-    // Elements e and e + 1 of the two vectors in a row (PAIRS), or of one (HALF, with the other's).
+    // Pair i of the chunk, interleaved: p and q.  (The last chunk may hold dims that pass.)
+    auto turn_pair = [&](T& p, T& q, int i) {
+        const float pf = to_f(p), qf = to_f(q);
+        const float2 r = rope_turn2<EXACT>(make_float2(pf, qf), make_float2(qf, pf), make_float2(ch[i], ch[i]), make_float2(cl[i], cl[i]),
+                                           make_float2(-sh[i], sh[i]), make_float2(-sl[i], sl[i]), make_float2(-ch[i], -ch[i]),
+                                           make_float2(sh[i], -sh[i]));
+        if (P * chunk + i < a.r.rot / 2) {
+            from_f(r.x, p);
+            from_f(r.y, q);
+        }
+    };
     auto turn = [&](V& a0, V& a1) {
-        if constexpr (PAIRS) {
+        if constexpr (PAIRS && P == 1) {
+            turn_pair(a0.v[0], a1.v[0], 0);
+        } else if constexpr (PAIRS) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) {  // pair i: elements 2i, 2i + 1 of the row of both vectors
-                T &lo = 2 * i < P ? a0.v[2 * i < P ? 2 * i : 0] : a1.v[2 * i >= P ? 2 * i - P : 0];
-                T &hi = 2 * i + 1 < P ? a0.v[2 * i + 1 < P ? 2 * i + 1 : 0] : a1.v[2 * i + 1 >= P ? 2 * i + 1 - P : 0];
-                const float p = to_f(lo), q = to_f(hi);
-                const float2 r = rope_turn2<EXACT>(make_float2(p, q), make_float2(q, p), make_float2(ch[i], ch[i]),
-                                                   make_float2(cl[i], cl[i]), make_float2(-sh[i], sh[i]), make_float2(-sl[i], sl[i]),
-                                                   make_float2(-ch[i], -ch[i]), make_float2(sh[i], -sh[i]));
-                from_f(r.x, lo);
-                from_f(r.y, hi);
+            for (int i = 0; i < P / 2; ++i) {
+                turn_pair(a0.v[2 * i], a0.v[2 * i + 1], i);
+                turn_pair(a1.v[2 * i], a1.v[2 * i + 1], P / 2 + i);
             }
         } else {
 #pragma unroll
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, 3) rope_kernel(const __grid_cons
 #pragma unroll
         for (int k = 0; k < U; ++k)
             if (h + k < h1) {
-                turn(u[k], w[k]);
+                if (turned) turn(u[k], w[k]);
                 *reinterpret_cast<V*>(out + (int64_t)(h + k) * a.hd + d0) = u[k];
                 *reinterpret_cast<V*>(out + (int64_t)(h + k) * a.hd + d1) = w[k];
             }
@@ -134,13 +141,13 @@ __global__ void __launch_bounds__(ROPE_THREADS, 3) rope_kernel(const __grid_cons
 
 template <typename T, int P>
 static cudaError_t launch_rope_p(RopeArgs& a, cudaStream_t s) {
-    a.nr = a.r.rot / 2 / P;
-    a.nc = a.nr + (a.hd - a.r.rot) / P;
+    a.nr = a.r.pairs ? (a.r.rot + 2 * P - 1) / (2 * P) : a.r.rot / 2 / P;
+    a.nc = a.hd / (2 * P);
     const int by = ROPE_THREADS / a.nc;
     // Heads per thread: the angles are formed once for them, and a thread that loops keeps
     // loads in flight; but every SM should have a thousand threads' worth of work first.
     const int64_t threads = (int64_t)a.tokens * a.heads * a.nc;
-    int64_t per = threads / (152 * 2048);
+    int64_t per = threads / (152 * 512);
     per = per < 1 ? 1 : per > 8 ? 8 : per;
     a.per = (int)per;
     a.groups = (a.heads + a.per - 1) / a.per;
@@ -157,17 +164,60 @@ static cudaError_t launch_rope_p(RopeArgs& a, cudaStream_t s) {
     return a.r.pairs ? cudaLaunchKernelEx(&cfg, rope_kernel<T, true, P>, a) : cudaLaunchKernelEx(&cfg, rope_kernel<T, false, P>, a);
 }
 
+// Heads of an odd number of dims: a thread a dim.  Such heads rotate an even number of them.
+template <typename T>
+__global__ void __launch_bounds__(ROPE_THREADS) rope_odd_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr bool EXACT = std::is_same<T, float>::value;
+    __shared__ float2 tab[ROPE_TAB];
+    for (int i = threadIdx.x; i < ROPE_TAB; i += ROPE_THREADS) tab[i] = ROPE_COS[i];
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait();
+    // a pair, or one of the dims behind them
+    const int half = a.r.rot / 2, units = a.hd - half;
+    const int64_t i = (int64_t)blockIdx.x * ROPE_THREADS + threadIdx.x, head = i / units;
+    const int token = (int)(head / a.heads), e = (int)(i - head * units);
+    if (token >= a.tokens) return;
+    const int h = (int)(head - (int64_t)token * a.heads);
+    const T* x = (const T*)a.x + token * a.ld + (int64_t)h * a.hd;
+    T* out = (T*)a.out + token * a.ld_out + (int64_t)h * a.hd;
+    if (e >= half) {
+        out[e + half] = x[e + half];
+        return;
+    }
+    const int d0 = a.r.pairs ? 2 * e : e, d1 = a.r.pairs ? d0 + 1 : e + half;
+    const float p = to_f(x[d0]), q = to_f(x[d1]);
+    float2 c, s;
+    rope_angle<EXACT>(a.r.turns[e], a.pos[token], a.r.mh, a.r.ml, tab, c, s);
+    const float2 r = rope_turn2<EXACT>(make_float2(p, q), make_float2(q, p), make_float2(c.x, c.x), make_float2(c.y, c.y),
+                                       make_float2(-s.x, s.x), make_float2(-s.y, s.y), make_float2(-c.x, -c.x), make_float2(s.x, -s.x));
+    from_f(r.x, out[d0]);
+    from_f(r.y, out[d1]);
+}
+
 template <typename T>
 static cudaError_t launch_rope(RopeArgs& a, cudaStream_t s) {
-    constexpr int W = 16 / (int)sizeof(T);
-    // P pairs at a time: both vectors, the row ends and all strides lie on multiples of P
+    constexpr int W = 4;
+    // vectors of p: addresses and strides lie on multiples of p, heads are whole pairs of vectors, and so are the
+    // two halves of what is rotated
     auto fits = [&](int p) {
-        return a.r.rot % (2 * p) == 0 && a.hd % p == 0 && a.ld % p == 0 && a.ld_out % p == 0 &&
+        return a.hd % (2 * p) == 0 && a.ld % p == 0 && a.ld_out % p == 0 && (a.r.pairs || a.r.rot % (2 * p) == 0) &&
                (((uintptr_t)a.x | (uintptr_t)a.out) & (p * sizeof(T) - 1)) == 0;
     };
     if (fits(W)) return launch_rope_p<T, W>(a, s);
     if (fits(2)) return launch_rope_p<T, 2>(a, s);
-    return launch_rope_p<T, 1>(a, s);
+    if (a.hd % 2 == 0) return launch_rope_p<T, 1>(a, s);
+    const int64_t threads = (int64_t)a.tokens * a.heads * (a.hd - a.r.rot / 2);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)((threads + ROPE_THREADS - 1) / ROPE_THREADS));
+    cfg.blockDim = dim3(ROPE_THREADS);
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, rope_odd_kernel<T>, a);
 }
 
 kd_status rope_table_check(const char* fn, const kd_rope_table* t) {

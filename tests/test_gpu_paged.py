@@ -93,7 +93,7 @@ def normal(seed, shape, kind="fp32"):
 @pytest.mark.parametrize("kind", ["fp32", "fp16", "bf16"])
 @pytest.mark.parametrize("layout", [HALF, PAIRS])
 @pytest.mark.parametrize("hd,rot", [(128, 128), (128, 64), (64, 64), (64, 34), (128, 2), (256, 256), (24, 20), (96, 96),
-                                    (16, 16), (2, 2), (7, 6), (250, 12)])
+                                    (16, 16), (2, 2), (7, 6), (250, 12), (128, 86), (80, 6), (192, 190)])
 def test_rope_shapes(kdlib, kind, layout, hd, rot):
     for t, h in ((1, 1), (3, 5), (17, 33)):
         x = normal(hd + rot + t, (t, h, hd), kind)
