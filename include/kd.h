@@ -674,9 +674,11 @@ size_t kd_attn_paged_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_he
  * page exists).  Keys behind lens[b] are not used, whatever they hold.
  * B sessions, 1 <= B <= KD_PAGED_MAX_SEQS.  Groups: sessions in order, group g the
  * next group_rows[g] >= 1 of them (B in all), which share their first
- * group_prefix[g] keys (0 <= group_prefix[g] <= each of their lens; it may end within a page):
- * these are read through the table of the group's first session, and the others'
- * tables are not read for whole pages of it.  n_groups = 0: nothing is shared
+ * group_prefix[g] keys (0 <= group_prefix[g] <= each of their lens).  The whole pages of
+ * that prefix are read through the table of the group's first session (the others'
+ * tables are not read there), the page that it ends in through each session's own, which
+ * may hold a copy of it.  Where it pays, whole pages are read once for the group, else by each session;
+ * sharing is an equality of keys that the caller vouches for either way.  n_groups = 0: nothing is shared
  * (group_rows, group_prefix ignored).  Results do not depend on where pages lie;
  * lengths and groups decide how the keys are split, so a session's result can differ in
  * the last bits between batches.
