@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(PAGED_MERGE_WARPS * 32) paged_merge_kernel(con
         for (int d = 0; d < DIMS; ++d) acc[d] = __fmul_rn(acc[d], f);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (ml[u].x != -INFINITY) {  // else there are no keys, and what is in its place does not count
+            if (ml[u].x != -INFINITY || ml[u].y != 0.0f) {  // else there are no keys (without a maximum but with a sum: NaN)
                 const float w = expf(__fsub_rn(ml[u].x, ref));
                 den = __fmaf_rn(w, ml[u].y, den);
 #pragma unroll

@@ -18,8 +18,10 @@ Tolerances, per element (derived; u = x_a, w = x_b the pair, m the magnitude):
   denominator) plus 2^-21 (expf, p's pair); a key's weight passes at most len/32 + 20
   further sums or products with a rescaling factor (its chain's pieces, warps, records), 2^-22
   each.  So o moves by at most eps sum_t p_t |v_t|; then it is rounded to fp16 once."""
-import ctypes as C
 import math
+import subprocess
+import sys
+from pathlib import Path
 
 import numpy as np
 import pytest
@@ -625,6 +627,78 @@ def test_two_calls_at_once(kdlib):
     torch.cuda.synchronize()
     for w, o in zip(want, outs):
         assert np.array_equal(w.view(np.int16), o.cpu().numpy().view(np.int16))
+
+
+@pytest.mark.parametrize("groups", [[], [(14, 1200), (2, 0)]])
+@pytest.mark.parametrize("q8", [False, True])
+def test_not_a_number_stays_with_its_query(kdlib, q8, groups):
+    """A NaN in one query's dims, and (fp16) in one key that a session sees: NaN there and nowhere else."""
+    c = Attn(q8, 32, 8, 128, 16, [1290 + i for i in range(14)] + [300, 5], groups, seed=21)
+    q = c.dq.clone()
+    q[3, 17, 5] = float("nan")
+    q[15, 2, 100] = float("nan")
+    out, ws = c.new_out(), c.workspace(kdlib)
+    c.call(kdlib, out, ws, q=q)
+    bad = torch.isnan(out).view(16, 32, 128)
+    want = torch.zeros(16, 32, dtype=torch.bool, device="cuda")
+    want[3, 17] = want[15, 2] = True
+    assert torch.equal(bad.all(-1), want) and torch.equal(bad.any(-1), want)
+    if not q8:
+        page = int(c.pool.table[14, 200 // 16])
+        c.pool.planes[0][page, 6, 200 % 16, 3] = float("nan")
+        c.call(kdlib, out, ws)
+        want[:] = False
+        want[14, 24:28] = True
+        assert torch.equal(torch.isnan(out).view(16, 32, 128).all(-1), want)
+
+
+FIRST = """
+import numpy as np, torch
+import session_decode_step_gb300 as kd
+B, nh, nkv, hd, ps, n = 16, 32, 8, 128, 16, 1024
+pages = n // ps + 2 * B
+planes = {planes}
+table = torch.zeros(B, n // ps + 2, dtype=torch.int32)
+table[:, :n // ps] = torch.arange(n // ps)
+table[:, n // ps:] = n // ps + torch.arange(2 * B).view(B, 2)
+table = table.cuda()
+q, k = torch.randn(B, nh, hd, device="cuda"), torch.randn(B, nkv, hd, device="cuda")
+q_out, out = torch.empty_like(q), torch.zeros(B, nh * hd, dtype=torch.float16, device="cuda")
+pos = torch.arange(B, dtype=torch.int32, device="cuda")
+ws = torch.empty(kd.kd_attn_paged_workspace_bytes(B, nh, nkv, hd), dtype=torch.uint8, device="cuda")
+plan = kd.kd_rope_plan(hd, 1e4)
+def step():
+    kd.kd_rope(plan, q, pos, q_out)
+    {append}
+    {attend}
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):  # nothing of these has run in this process
+    step()
+g.replay()
+torch.cuda.synchronize()
+first = out.clone()
+assert kd.kd_attn_device_status(ws) == 0 and first.abs().sum() > 0
+out.zero_()
+step()
+torch.cuda.synchronize()
+assert torch.equal(first, out)
+print("same")
+"""
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_first_calls_of_a_process_in_a_capture(kdlib, q8):
+    if q8:
+        parts = dict(planes='[torch.randint(1, 255, (pages, nkv, ps, 128), dtype=torch.uint8, device="cuda"), torch.rand(pages, nkv, ps, 4, device="cuda").half()] * 2',
+                     append="kd.kd_paged_append_q8(plan, k, k, *planes, table, [n] * B, [1] * B, nkv, pages, ps, q=q, q_out=q_out, n_heads=nh)",
+                     attend="kd.kd_attn_paged_decode_q8(q_out, *planes, table, [n + 1] * B, nh, nkv, pages, ps, out, ws, group_rows=[B], group_prefix=[n])")
+    else:
+        parts = dict(planes='[torch.randn(pages, nkv, ps, hd, device="cuda").half() for _ in range(2)]',
+                     append="kd.kd_paged_append(plan, k, k, *planes, table, [n] * B, [1] * B, nkv, hd, pages, ps, q=q, q_out=q_out, n_heads=nh)",
+                     attend="kd.kd_attn_paged_decode(q_out, *planes, table, [n + 1] * B, nh, nkv, hd, pages, ps, out, ws, group_rows=[B], group_prefix=[n])")
+    r = subprocess.run([sys.executable, "-c", FIRST.format(**parts)], capture_output=True, text=True, timeout=300, cwd=Path(__file__).resolve().parents[1])
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 # ------------------------------------------------------------ used together ---
