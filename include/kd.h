@@ -635,6 +635,7 @@ kd_status kd_rope(const kd_rope_table* rope, const void* x, int32_t dtype, int64
                   int32_t n_tokens, int32_t n_heads, void* out, int64_t ld_out, kd_stream stream);
 
 #define KD_PAGED_MAX_SEQS 256
+#define KD_PAGED_MAX_LEN (1 << 30)
 
 /* Append new keys, rotated, and values to a paged cache; rotate the queries alongside.
  * Session b (< n_seqs <= KD_PAGED_MAX_SEQS) gets counts[b] >= 0 rows from position
@@ -648,7 +649,7 @@ kd_status kd_rope(const kd_rope_table* rope, const void* x, int32_t dtype, int64
  * the cache's.  q, q_out: NULL, with n_heads = 0, for no queries.  Rows of pages
  * that belong to no new position stay as they were.  No two new rows may share a
  * place; outputs must not overlap inputs.
- * starts[b] + counts[b] <= table_ld * page_size.  head_dim is 64 or 128 (Q8_0: 128).
+ * starts[b] + counts[b] <= table_ld * page_size, and below 2^31.  head_dim is 64 or 128 (Q8_0: 128).
  * Pages and q_out 16-byte aligned, k_new, v_new and q to their type.
  * Errors: KD_ERR_BATCH (n_seqs), KD_ERR_POSITION (starts, counts), KD_ERR_UNSUPPORTED
  * (head_dim, page_size, 2^31 or more new heads in all), KD_ERR_INVALID_ARG. */
@@ -684,7 +685,7 @@ size_t kd_attn_paged_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_he
  * the last bits between batches.
  * q: device fp32 [B][n_heads][head_dim]; out: device fp16 [B][n_heads * head_dim];
  * lens, group_rows, group_prefix: host int32.  head_dim 64 or 128 (Q8_0: 128),
- * n_heads 1, 2, 4 or 8 times n_kv_heads, n_kv_heads <= 1024.  lens[b] <= table_ld * page_size.
+ * n_heads 1, 2, 4 or 8 times n_kv_heads, n_kv_heads <= 1024.  lens[b] <= table_ld * page_size and <= KD_PAGED_MAX_LEN.
  * workspace: kd_attn_paged_workspace_bytes(...) bytes, used by one call at a time.
  * q, pages and workspace 16-byte aligned, out 2-byte.
  * kd_attn_device_status(workspace, ...) reads the call's fault word.

@@ -66,6 +66,7 @@ KD_ROPE_HALF, KD_ROPE_PAIRS = 0, 1
 KD_ROPE_UNSCALED, KD_ROPE_LINEAR, KD_ROPE_BANDS, KD_ROPE_RAMP = 0, 1, 2, 3
 KD_F32, KD_F16, KD_BF16 = 0, 1, 2
 KD_PAGED_MAX_SEQS = 256
+KD_PAGED_MAX_LEN = 1 << 30
 
 
 class KdRopeConfig(C.Structure):

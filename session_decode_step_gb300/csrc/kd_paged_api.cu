@@ -87,7 +87,7 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
     SharedArgs sh = {};
     int64_t total = 0, shared_tiles = 0;
     for (int b = 0; b < B; ++b) {
-        if (lens[b] < 0 || lens[b] > (int64_t)table_ld * ps)
+        if (lens[b] < 0 || lens[b] > (int64_t)table_ld * ps || lens[b] > KD_PAGED_MAX_LEN)
             return failf(KD_ERR_POSITION, "%s: length %d in tables of %d pages of %d", fn, lens[b], table_ld, ps);
         a.s[b].to = lens[b];
         a.s[b].lead = (short)b;

@@ -304,13 +304,14 @@ static kd_status append_call(const char* fn, bool q8, const kd_rope_table* rope,
     AppendArgs a = {};
     int64_t total = 0;
     for (int b = 0; b < n_seqs; ++b) {
-        if (starts[b] < 0 || counts[b] < 0 || (int64_t)starts[b] + counts[b] > (int64_t)table_ld * ps)
+        if (starts[b] < 0 || counts[b] < 0 || (int64_t)starts[b] + counts[b] > (int64_t)table_ld * ps ||
+            (int64_t)starts[b] + counts[b] > 0x7fffffff)
             return failf(KD_ERR_POSITION, "%s: %d rows from position %d on in tables of %d pages of %d", fn, counts[b],
                          starts[b], table_ld, ps);
         a.start[b] = starts[b];
         a.first[b] = (int)total;
         total += counts[b];
-        if (total * (2 * (int64_t)nkv + nh) > 0x7fffffff)
+        if (total * (2 * (int64_t)nkv + nh) > 0x7fffffff - APPEND_WARPS)
             return failf(KD_ERR_UNSUPPORTED, "%s: 2^31 or more new heads", fn);
     }
     a.first[n_seqs] = (int)total;

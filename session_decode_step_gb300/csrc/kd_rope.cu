@@ -276,6 +276,7 @@ kd_status kd_rope_plan(const kd_rope_config* c, kd_rope_table* out) {
                 slow = std::fmin(1.0, std::fmax(0.0, (i - a) / std::fmax(b - a, 0.001)));
             f *= (1.0 - slow) + slow / c->factor;
         }
+        if (!std::isfinite(f)) return failf(KD_ERR_INVALID_ARG, "%s: factor %g leaves no finite frequency", fn, c->factor);
         // turns per position modulo 1, to 2^-64 (positions are whole, so whole turns drop out)
         double r = f / turn;
         r -= std::floor(r);

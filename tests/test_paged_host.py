@@ -91,7 +91,7 @@ def test_plan_defaults(lib):
     (dict(theta=1.0), INVALID), (dict(theta=float("inf")), INVALID), (dict(theta=float("nan")), INVALID),
     (dict(magnitude=float("nan")), INVALID), (dict(magnitude=1e300), INVALID),
     (dict(scaling=1, factor=0.0), INVALID), (dict(scaling=1, factor=float("nan")), INVALID), (dict(scaling=1, factor=float("inf")), INVALID),
-    (dict(scaling=2, original_ctx=0), INVALID), (dict(scaling=2, original_ctx=8, low=4.0, high=4.0), INVALID),
+    (dict(scaling=1, factor=5e-324), INVALID), (dict(scaling=2, original_ctx=0), INVALID), (dict(scaling=2, original_ctx=8, low=4.0, high=4.0), INVALID),
     (dict(scaling=3, original_ctx=8, low=0.0), INVALID), (dict(scaling=3, original_ctx=8, high=float("inf")), INVALID),
 ])
 def test_plan_refusals(lib, change, status):
@@ -162,7 +162,7 @@ def append(lib, q8=False, rope=True, k=D, v=D, q=D, kld=1024, vld=1024, qld=4096
     (dict(k=D + 2), INVALID), (dict(kp=D + 8), INVALID), (dict(q_out=D + 8), INVALID), (dict(tab=D + 2), INVALID), (dict(fault=D + 1), INVALID),
     (dict(starts=arr(-1, 3)), POSITION), (dict(counts=arr(5, -1)), POSITION), (dict(starts=arr(0, 128)), POSITION),
     (dict(starts=arr(124, 3)), POSITION), (dict(starts=arr(2 ** 31 - 1, 0), counts=arr(2 ** 31 - 1, 0)), POSITION),
-    (dict(tld=2 ** 27, counts=arr(2 ** 30, 2 ** 30)), UNSUPPORTED),
+    (dict(tld=2 ** 27, counts=arr(2 ** 30, 2 ** 30)), UNSUPPORTED), (dict(tld=2 ** 30, starts=arr(2 ** 31 - 1, 0), counts=arr(1, 0)), POSITION),
     (dict(counts=arr(0, 0)), 0), (dict(counts=arr(0, 0), rope=None, fault=None, nh=0, q=None, q_out=None), 0),
 ])
 @pytest.mark.parametrize("q8", [False, True])
@@ -197,7 +197,7 @@ def attn(lib, q8=False, q=D, kp=D, vp=D, ks=D, tab=D, tld=8, lens=arr(5, 100), B
     (dict(n_pages=0), INVALID), (dict(tld=0), INVALID), (dict(G=-1), INVALID), (dict(n_pages=1 << 24), UNSUPPORTED),
     (dict(ws_bytes=4096), INVALID), (dict(ws=D + 8), INVALID), (dict(q=D + 8), INVALID), (dict(kp=D + 8), INVALID), (dict(tab=D + 2), INVALID),
     (dict(out=D + 1), INVALID), (dict(fault=D + 2), INVALID),
-    (dict(lens=arr(-1, 5)), POSITION), (dict(lens=arr(5, 129)), POSITION),
+    (dict(lens=arr(-1, 5)), POSITION), (dict(lens=arr(5, 129)), POSITION), (dict(tld=2 ** 27, lens=arr(5, 2 ** 30 + 1)), POSITION),
     (dict(G=1, rows=arr(2), prefix=arr(6)), POSITION), (dict(G=1, rows=arr(2), prefix=arr(-1)), POSITION),
     (dict(G=1, rows=arr(1), prefix=arr(0)), INVALID), (dict(G=2, rows=arr(1, 2), prefix=arr(0, 0)), INVALID),
     (dict(G=2, rows=arr(0, 2), prefix=arr(0, 0)), INVALID), (dict(G=2, rows=arr(2, 2 ** 31 - 1), prefix=arr(0, 0)), INVALID),
