@@ -313,6 +313,7 @@ class _CtypesCalls:
     def append(plan, k_new, v_new, planes, table, starts, counts, n_heads, n_kv_heads, head_dim, n_pages, page_size, q, q_out,
                fault, stream):
         pk, k_ld, rows, h, d, dtype = _heads(k_new, "k_new")
+        _check_planes(planes, n_kv_heads, head_dim, n_pages, page_size)
         pv, v_ld, *shape = _heads(v_new, "v_new")
         if shape != [rows, h, d, dtype] or (h, d) != (n_kv_heads, head_dim):
             raise ValueError("k_new and v_new must be alike: [rows][n_kv_heads][head_dim]")
@@ -341,6 +342,9 @@ class _CtypesCalls:
         table_ld = _table(table, lens.size)
         rows = _i32(() if group_rows is None else group_rows)
         prefix = _i32(() if group_prefix is None else group_prefix, rows.size)
+        _check_size(q, 4 * lens.size * n_heads * head_dim, "q")
+        _check_planes(planes, n_kv_heads, head_dim, n_pages, page_size)
+        _check_size(out, 2 * lens.size * n_heads * head_dim, "out")
         fn = lib().kd_attn_paged_decode if len(planes) == 2 else lib().kd_attn_paged_decode_q8
         shape = (_int(head_dim),) if len(planes) == 2 else ()
         return fn(_ptr(q), *map(_ptr, planes), _ptr(table), table_ld, lens.ctypes.data_as(_I32P), lens.size,
@@ -372,6 +376,17 @@ def _table(table, rows):
     if table.dim() != 2 or table.dtype != sys.modules["torch"].int32 or table.shape[0] < rows:
         raise ValueError(f"the page table must be int32 [sessions][pages], with {rows} sessions or more")
     return _int(table.shape[1])
+
+
+def _check_size(x, nbytes, what):
+    if x is not None and not isinstance(x, int) and x.nbytes < nbytes:
+        raise ValueError(f"{what} is smaller than the call's sizes")
+
+
+def _check_planes(planes, n_kv_heads, head_dim, n_pages, page_size):
+    for i, plane in enumerate(planes):
+        width = 2 * head_dim if len(planes) == 2 else 8 if i & 1 else 128
+        _check_size(plane, n_pages * n_kv_heads * page_size * width, "a plane of the cache")
 
 
 def _plan(plan):

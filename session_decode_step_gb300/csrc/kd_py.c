@@ -411,6 +411,27 @@ static int get_planes(PyObject* o, void** p) {
     return (int)n;
 }
 
+/* A tensor or array of `bytes` or more (addresses and None are taken as they are). */
+static int check_size(PyObject* o, double bytes, const char* what) {
+    size_t n;
+    if (o == Py_None || PyLong_Check(o)) return 0;
+    if (get_nbytes(o, &n) < 0) return -1;
+    if ((double)n >= bytes) return 0;
+    PyErr_Format(PyExc_ValueError, "%s is smaller than the call's sizes", what);
+    return -1;
+}
+/* c: n_heads, n_kv_heads, head_dim, n_pages, page_size */
+static int check_planes(PyObject* o, int planes, const int32_t* c) {
+    const double rows = (double)c[3] * c[1] * c[4];
+    PyObject* seq = PySequence_Fast(o, "planes must be a sequence");
+    int i, r = 0;
+    if (!seq) return -1;
+    for (i = 0; i < planes && !r; ++i)
+        r = check_size(PySequence_Fast_GET_ITEM(seq, i), rows * (planes == 2 ? 2.0 * c[2] : i & 1 ? 8 : 128), "a plane of the cache");
+    Py_DECREF(seq);
+    return r;
+}
+
 /* plan, k_new, v_new, planes, table, starts, counts, n_heads, n_kv_heads, head_dim, n_pages, page_size, q, q_out, fault,
  * stream */
 static PyObject* py_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
@@ -429,6 +450,7 @@ static PyObject* py_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     if (get_heads(a[1], "k_new", &k) < 0 || get_heads(a[2], "v_new", &v) < 0 || (planes = get_planes(a[3], p)) < 0) goto done;
     for (i = 0; i < 5; ++i)
         if (get_i32(a[7 + i], &c[i]) < 0) goto done;
+    if (check_planes(a[3], planes, c) < 0) goto done;
     if (!alike(&k, &v) || k.heads != c[1] || k.dim != c[2]) {
         PyErr_SetString(PyExc_ValueError, "k_new and v_new must be alike: [rows][n_kv_heads][head_dim]");
         goto done;
@@ -490,6 +512,9 @@ static PyObject* py_paged(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     }
     for (i = 0; i < 5; ++i)
         if (get_i32(a[6 + i], &v[i]) < 0) goto done;
+    if (check_size(a[0], 4.0 * B * v[0] * v[2], "q") < 0 || check_planes(a[1], planes, v) < 0 ||
+        check_size(a[11], 2.0 * B * v[0] * v[2], "out") < 0)
+        goto done;
     if (get_ptr(a[11], &out) < 0 || get_ptr(a[12], &ws) < 0 || get_nbytes(a[12], &bytes) < 0 || get_ptr(a[13], &fault) < 0 ||
         get_stream(a[14], &st) < 0)
         goto done;

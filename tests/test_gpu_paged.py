@@ -82,6 +82,10 @@ SCALED = [dict(), dict(scaling="linear", factor=4.0), dict(scaling="bands", fact
           dict(scaling="ramp", factor=10.0, low=1.0, high=32.0, original=2048)]
 
 
+def kd_plan(kd, hd):
+    return kd.kd_rope_plan(hd, 10000.0)
+
+
 def make_plan(kd, hd, rot, theta, layout, magnitude=1.0, scaling="none", factor=1.0, low=1.0, high=4.0, original=8192):
     code = {"none": kd.KD_ROPE_UNSCALED, "linear": kd.KD_ROPE_LINEAR, "bands": kd.KD_ROPE_BANDS, "ramp": kd.KD_ROPE_RAMP}
     return kd.kd_rope_plan(hd, theta, rot_dim=rot, layout=layout, scaling=code[scaling], factor=factor, low=low, high=high,
@@ -627,6 +631,56 @@ def test_two_calls_at_once(kdlib):
     torch.cuda.synchronize()
     for w, o in zip(want, outs):
         assert np.array_equal(w.view(np.int16), o.cpu().numpy().view(np.int16))
+
+
+@pytest.mark.parametrize("groups", [[], [(14, 1280), (2, 0)]])
+@pytest.mark.parametrize("q8", [False, True])
+def test_offsets_past_32_bits(kdlib, q8, groups):
+    """Pages of planes of more than 4 GB, half of them at their ends: the bits that a small pool gives."""
+    c = Attn(q8, 32, 8, 128, 64, [1290 + 11 * i for i in range(14)] + [300, 5], groups, seed=33)
+    small, n, table = c.pool.planes, c.pool.n_pages, c.pool.table
+    big_n = 70001 if q8 else 35001  # 2^32 bytes are 65536 and 32768 pages
+    page = np.arange(n)
+    page = np.where(page % 2, big_n - 1 - page, page)
+    at = torch.from_numpy(page).cuda()
+    big = [torch.empty((big_n, *p.shape[1:]), dtype=p.dtype, device="cuda") for p in small]
+    assert max(p.nbytes for p in big) > 2 ** 32
+    for b, p in zip(big, small):
+        b[at] = p
+    new = [normal(s, (16, 8, 128)) for s in (1, 2)]
+    plan, got = kd_plan(kdlib, 128), []
+    for planes, pages in ((small, n), (big, big_n)):
+        if pages == big_n:
+            c.pool.planes, c.pool.n_pages = big, big_n
+            c.pool.table = np.where((table >= 0) & (table < n), page[np.clip(table, 0, n - 1)], table).astype(np.int32)
+            c.table = c.pool.device_table()
+        if q8:
+            kdlib.kd_paged_append_q8(plan, *new, *planes, c.table, c.lens - 1, [1] * 16, 8, pages, 64)
+        else:
+            kdlib.kd_paged_append(plan, *new, *planes, c.table, c.lens - 1, [1] * 16, 8, 128, pages, 64)
+        got.append(c.run(kdlib))
+    assert all(torch.equal(b[at].view(torch.uint8), p.view(torch.uint8)) for b, p in zip(big, small))
+    assert np.array_equal(got[0], got[1])
+
+
+def test_rows_far_apart(kdlib):
+    """Rows 2^31 elements apart: rotated from there, to there and in place, and appended, as rows that lie together."""
+    far = torch.empty(2 * 2 ** 31 + 512, dtype=torch.float16, device="cuda").as_strided((3, 4, 128), (2 ** 31, 128, 1))
+    x, pos, plan = normal(3, (3, 4, 128), "fp16"), torch.arange(7, 10, dtype=torch.int32, device="cuda"), kd_plan(kdlib, 128)
+    want, got = torch.empty_like(x), torch.empty_like(x)
+    kdlib.kd_rope(plan, x, pos, want)
+    far.copy_(x)
+    kdlib.kd_rope(plan, far, pos, got)
+    assert torch.equal(got, want)
+    kdlib.kd_rope(plan, far, pos, far)
+    assert torch.equal(far, want)
+    pools = [torch.zeros(4, 4, 16, 128, dtype=torch.float16, device="cuda") for _ in range(4)]
+    table = torch.tensor([[2, 0]], dtype=torch.int32, device="cuda")
+    q_out = [torch.empty(3, 4, 128, device="cuda") for _ in range(2)]
+    for rows, planes, to in ((far, pools[:2], q_out[0]), (want, pools[2:], q_out[1])):
+        kdlib.kd_paged_append(plan, rows, rows, *planes, table, [14], [3], 4, 128, 4, 16, q=rows, q_out=to, n_heads=4)
+    assert torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3]) and torch.equal(*q_out)
+    assert pools[1][2, :, 14:].abs().sum() > 0 and pools[1][0, :, :1].abs().sum() > 0
 
 
 @pytest.mark.parametrize("groups", [[], [(14, 1200), (2, 0)]])

@@ -296,3 +296,26 @@ def test_binding_attention(calls):
         call(lens=[1, 2, 3])
     with pytest.raises(ValueError, match="contiguous"):
         kd.kd_attn_paged_decode(torch.zeros(2, 4, 128)[:, :, :64], pages, pages, tab, [1, 1], 4, 2, 64, 4, 16, out, ws)
+
+
+def test_binding_sizes(calls):
+    """q, out and the cache's planes have what the call's sizes say."""
+    pages, small = (torch.zeros(n, 2, 16, 64, dtype=torch.float16) for n in (4, 3))
+    k, tab = torch.zeros(1, 2, 64), torch.zeros(1, 3, dtype=torch.int32)
+    for planes in ((pages, small), (small, pages)):
+        with pytest.raises(ValueError, match="a plane of the cache"):
+            kd.kd_paged_append(None, k, k, *planes, tab, [0], [1], 2, 64, 4, 16)
+    q, out, ws = torch.zeros(1, 4, 64), torch.zeros(1, 256, dtype=torch.float16), torch.zeros(kd.kd_attn_paged_workspace_bytes(1, 4, 2, 64), dtype=torch.uint8)
+    for change, what in ((dict(q=q.half()), "q"), (dict(out=out[:, :255].contiguous()), "out"), (dict(k=small), "a plane"), (dict(v=small), "a plane")):
+        a = dict(q=q, k=pages, v=pages, out=out)
+        a.update(change)
+        with pytest.raises(ValueError, match=what + ".* is smaller"):
+            kd.kd_attn_paged_decode(a["q"], a["k"], a["v"], tab, [3], 4, 2, 64, 4, 16, a["out"], ws)
+    quants, scales = torch.zeros(4, 2, 16, 128, dtype=torch.uint8), torch.zeros(4, 2, 16, 4, dtype=torch.float16)
+    for i in range(4):
+        planes = [quants, scales, quants, scales]
+        planes[i] = planes[i][:3]
+        with pytest.raises(ValueError, match="a plane of the cache"):
+            kd.kd_attn_paged_decode_q8(torch.zeros(1, 4, 128), *planes, tab, [3], 4, 2, 4, 16, torch.zeros(1, 512, dtype=torch.float16), ws)
+        with pytest.raises(ValueError, match="a plane of the cache"):
+            kd.kd_paged_append_q8(None, torch.zeros(1, 2, 128), torch.zeros(1, 2, 128), *planes, tab, [0], [1], 2, 4, 16)
