@@ -162,8 +162,8 @@ struct SharedSmem {
     static constexpr int SLOTS = HD == 64 ? 8 : 6;
     static constexpr int RING = 0, BARS = SLOTS * TILE;
     static constexpr int MAXIMA = BARS + 320;          // [2][share][row]: what the warps of a row tell each other
-    static constexpr int CODES = MAXIMA + 2 * SHARE * QUERIES * 4;  // Q8_0: a part's codes and scales on their way, by thread
-    static constexpr int TOTAL = CODES + (Q8 ? 256 * 4 * (16 + 4) : 0);
+    static constexpr int CODES = MAXIMA + 2 * SHARE * QUERIES * 4;  // Q8_0: a part's codes, by thread, and scales, by warp, on their way
+    static constexpr int TOTAL = CODES + (Q8 ? 256 * 4 * 16 + 8 * 128 : 0);
     static_assert(TOTAL <= 227 * 1024, "opt-in shared memory");
 };
 // Columns of tensor memory: scores, then weights, of two tiles in turn (128 each); the sums; the queries, hi and lo.
@@ -329,11 +329,9 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                     if (values || j >= 2) ok = mbar_wait_bounded((values ? p_full : pv_done) + w, (turn_phase >> w) & 1);
                     if constexpr (Q8) place = shared_place(tile++, values);
                     uint32_t slot[PARTS];
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) {
-                        slot[i] = (place + i) % NS;
-                        ok = ok && mbar_wait_bounded(full + slot[i], ((place + i) / NS) & 1);
-                    }
+                    slot[0] = place % NS;
+                    if constexpr (Q8) slot[1] = slot[0] + 1;  // places are even, and so is the number of buffers
+                    ok = ok && mbar_wait_bounded(full + slot[0], (place / NS) & 1);
                     place += 2;  // fp16: K and V parts lie in turn
                     if (!ok) break;
                     if (values || j >= 2) turn_phase ^= 1u << w;
@@ -360,8 +358,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                                           tc_desc(ring + slot[part / 2] * L::TILE + k * 2048, L::COL), id, part || k || j);
                         tc_commit(pv_done + w);
                     }
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) tc_commit(empty + slot[i]);
+                    tc_commit(empty + slot[0]);
                 }
                 // The last products of even and odd tiles are not waited for here: keep their count.
                 if (!values) turn_phase ^= (s.n > 0 ? 1u : 0u) | (s.n > 1 ? 2u : 0u);
@@ -404,56 +401,51 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             uint4 v[4];
             __half d[4];
         };
-        // Lane i < 8: the first cache row of run i of tile j (-1: there is none).
-        auto look_up = [&](const SharedSeg& s, int j) {
-            const int key = (s.tile + j) * SHARED_TILE + 16 * lane;
-            if (lane >= 8 || key >= a.g[s.g].keys) return -1;
-            const int in_table = key / a.ps, page = a.table[(int64_t)a.g[s.g].lead * a.table_ld + in_table];
-            if ((unsigned)page < (unsigned)a.n_pages) return (page * a.nkv + s.h) * a.ps + key - in_table * a.ps;
-            if (a.fault) *a.fault = 1;
-            return -1;
-        };
         // The thread's codes and scales of a part, to its own place in shared memory: loads to registers would be
         // waited for together with those of the part after.
-        const uint32_t mine_at = smem_u32(smem + L::CODES) + t * 16, scales_at = smem_u32(smem + L::CODES) + 256 * 4 * 16 + t * 4;
+        const uint32_t mine_at = smem_u32(smem + L::CODES) + t * 16;
+        const uint32_t scales_at = smem_u32(smem + L::CODES) + 256 * 4 * 16 + (t >> 5) * 128;  // the warp's: 4 rows of each i, 8 bytes each
         auto fetch = [&](int rows, int part, uint32_t T) {
-            const uint8_t* codes = (part ? a.vq : a.kq) + 16 * chunk;
-            const __half* scales = (part ? a.vs : a.ks) + (chunk >> 2) * 2;  // the pair that the chunk's is of
+            const uint8_t* codes = (part ? a.vq : a.kq) + (trow & 15) * 128 + 16 * chunk;
             const unsigned have = __ballot_sync(FULL_MASK, rows >= 0);
             if (!part && t == 0) runs[T & 7] = (uint8_t)have;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // the warp's rows of i are of one run
                 const int first = __shfl_sync(FULL_MASK, rows, 2 * i + (t >> 7));
-                const bool good = first >= 0;  // else zeros: a scale of 0, whatever the codes
-                const int64_t at = good ? first + (trow & 15) : 0;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mine_at + i * 256 * 16), "l"(codes + at * 128),
-                             "r"(good ? 16 : 0)
+                // else zeros: a scale of 0, whatever the codes
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mine_at + i * 256 * 16), "l"(codes + (int64_t)max(first, 0) * 128),
+                             "r"(first >= 0 ? 16 : 0)
                              : "memory");
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(scales_at + i * 256 * 4), "l"(scales + at * 4),
-                             "r"(good ? 4 : 0)
+            }
+            const int first = __shfl_sync(FULL_MASK, rows, (lane & 6) + (t >> 7));
+            if (lane < 8) {  // two rows' scales of i = lane / 2
+                const uint8_t* scales = (const uint8_t*)(part ? a.vs : a.ks) + ((t >> 5) & 3) * 32 + (lane & 1) * 16;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(scales_at + lane * 16), "l"(scales + (int64_t)max(first, 0) * 8),
+                             "r"(first >= 0 ? 16 : 0)
                              : "memory");
             }
         };
         auto landed = [&](Codes& f) {
             asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t d;
+                unsigned short d;
                 asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(f.v[i].x), "=r"(f.v[i].y), "=r"(f.v[i].z), "=r"(f.v[i].w)
                              : "r"(mine_at + i * 256 * 16)
                              : "memory");
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(d) : "r"(scales_at + i * 256 * 4) : "memory");
-                f.d[i] = __ushort_as_half((unsigned short)((chunk >> 1) & 1 ? d >> 16 : d));
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(d) : "r"(scales_at + i * 32 + (trow & 3) * 8 + (chunk >> 1) * 2) : "memory");
+                f.d[i] = __ushort_as_half(d);
             }
             // read before the next part's copies are issued
 #pragma unroll
             for (int i = 0; i < 4; ++i) asm volatile("" : "+r"(f.v[i].x), "+r"(f.v[i].y), "+r"(f.v[i].z), "+r"(f.v[i].w)::"memory");
+            __syncwarp();
         };
         auto make = [&](int part, uint32_t T, const Codes& f) {
-            const uint32_t place = shared_place(T, part), s0 = place % NS, s1 = (place + 1) % NS;
-            const bool free = mbar_wait_bounded(empty + s0, ((place / NS) & 1) ^ 1) && mbar_wait_bounded(empty + s1, (((place + 1) / NS) & 1) ^ 1);
-            if (!__all_sync(FULL_MASK, free)) return false;
+            const uint32_t place = shared_place(T, part), s0 = place % NS, s1 = s0 + 1;
+            if (!__all_sync(FULL_MASK, mbar_wait_bounded(empty + s0, ((place / NS) & 1) ^ 1))) return false;
             uint8_t* dst = smem + L::RING + (chunk >> 2) * L::COL + trow * 128;
             const uint32_t c0 = ((2 * (chunk & 3)) ^ (trow & 7)) << 4;  // the second 8 dims are 16 bytes away in it
 #pragma unroll
@@ -477,41 +469,56 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(full + s0);
-                mbar_arrive(full + s1);
-            }
+            if (lane == 0) mbar_arrive(full + s0);
             return true;
         };
         if (makes) {
-            // the parts in the order of their places, a part's codes fetched while the one before is made
+            // the parts in the order of their places, K0 [K1] V0 K2 V1 .., a part's codes fetched while the one before is made
+            const int tile_pages = SHARED_TILE / a.ps, tile_rest = SHARED_TILE - tile_pages * a.ps;
             for (int x = x0; x < x1 && ok;) {
                 if (x != x0) s.at(a, x, x1 - x);
                 x += s.n;
                 if (n_queries(s) <= 0) continue;
-                // part k of 2 n: K0 [K1] V0 K2 V1 .., V last
-                auto part_of = [&](int k, int& j, int& part) {
-                    part = s.n == 1 ? k : k >= 2 && (k == 2 * s.n - 1 || !(k & 1));
-                    j = k < 2 ? (s.n > 1 ? k : 0) : part ? (k == 2 * s.n - 1 ? s.n - 1 : k / 2 - 1) : (k + 1) / 2;
+                const int keys = a.g[s.g].keys;
+                // Lane i < 8: run i of the next K's tile, its place in the table and in its page, and the page's number
+                // (-1: no run), which is not looked at before that K is fetched.
+                const int* row = a.table + (int64_t)a.g[s.g].lead * a.table_ld;
+                int key = s.tile * SHARED_TILE + 16 * lane, in_table = key / a.ps, in_page = key - in_table * a.ps, page;
+                auto look_up = [&] { page = lane < 8 && key < keys ? row[in_table] : -1; };
+                look_up();
+                int nk = 0, nv = 0, rows = -1, before = -1;  // K and V parts fetched; the cache rows of the last K's runs, and the one's before
+                auto fetch_k = [&] {
+                    before = rows;
+                    const bool good = (unsigned)page < (unsigned)a.n_pages;
+                    if (!good && lane < 8 && key < keys && a.fault) *a.fault = 1;
+                    rows = good ? (page * a.nkv + s.h) * a.ps + in_page : -1;
+                    fetch(rows, 0, tiles + nk);
+                    if (++nk < s.n) {
+                        key += SHARED_TILE;
+                        in_table += tile_pages;
+                        in_page += tile_rest;
+                        if (in_page >= a.ps) {
+                            in_page -= a.ps;
+                            ++in_table;
+                        }
+                        look_up();
+                    }
                 };
-                int newest = 0, before = look_up(s, 0), rows = before, ahead = s.n > 1 ? look_up(s, 1) : -1;  // of K `newest`, the one before, the next
-                fetch(rows, 0, tiles);
-                for (int k = 0; k < 2 * s.n && ok; ++k) {
+                fetch_k();
+                for (int part = 0, k = 0; k < 2 * s.n && ok; ++k) {
                     Codes f;
                     landed(f);
-                    int j, part;
+                    const int j = part ? nv - 1 : nk - 1, now = part;
                     if (k + 1 < 2 * s.n) {
-                        part_of(k + 1, j, part);
+                        part = part ? nk == s.n : s.n == 1 || nk > 1;
                         if (!part) {
-                            before = rows;
-                            rows = ahead;
-                            newest = j;
+                            fetch_k();
+                        } else {
+                            fetch(nk - 1 > nv ? before : rows, 1, tiles + nv);
+                            ++nv;
                         }
-                        fetch(part && j < newest ? before : rows, part, tiles + j);
-                        if (!part && j + 1 < s.n) ahead = look_up(s, j + 1);
                     }
-                    part_of(k, j, part);
-                    ok = make(part, tiles + j, f);
+                    ok = make(now, tiles + j, f);
                 }
                 tiles += s.n;
             }
@@ -674,7 +681,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     }
     __syncthreads();
     if (warp == SH_COPY) {
-        if (*failed) {  // copies may be in flight: give them their time before the memory is given up
+        if (!Q8 && *failed) {  // copies may be in flight: give them their time before the memory is given up
             if (lane < NS)
                 for (int i = 0; i < 2; ++i) (void)mbar_wait_bounded(full + lane, i);
             __syncwarp();
