@@ -2,8 +2,8 @@
 // Q8_0 caches, and the queries rotated alongside, in one launch.
 //
 // A lane owns 4 dims of a head, so a warp takes a head of 128 (two of 64) of one token:
-// K heads, V heads, then query heads, four of them in flight.  The lane's angles are
-// formed once per warp; the other half of a pair is a neighbour's register (a shuffle), or
+// K heads, V heads, then query heads, four of them in flight.  The token's angles are
+// formed once per warp, one or two by a lane; the other half of a pair is a neighbour's register (a shuffle), or
 // for rotated parts that do not split into lanes an element of the input again.  A row's
 // place comes from the page table by one look-up per warp.
 // Q8_0 rows: the 8 lanes of a 32-value block find its maximum by shuffles and store 4 codes
@@ -11,10 +11,11 @@
 // a code never depends on how the rotation was summed.
 //
 // Few tokens are bound by a launch and two dependent loads (a position's page, then the
-// row): 8 tokens of 32 + 8 heads take 2.7 us, an empty launch 2.1.  Many are bound by issue, near
-// memory's rate: 8.8 k bf16 tokens of 32 + 8 heads of 128 (277 MB) 52.4 us, 5.3 TB/s; with K, V and queries
-// in one loop, a head's kind asked for each time, 64.  6.3 k tokens of 8 heads into Q8_0 24.7 us (floor 5.9): the exact
-// rotation, three shuffles a maximum and the codes.
+// row): 8 tokens of 32 + 8 heads take 2.3 us, an empty launch 2.1.  Many are bound by issue, near
+// memory's rate: 8.8 k bf16 tokens of 32 + 8 heads of 128 (277 MB) 51 us, 5.4 TB/s; with K, V and queries
+// in one loop, a head's kind asked for each time, 64; with blocks that stay and take the next token, 62 (the last ones are
+// waited for).  6.3 k tokens of 8 heads into Q8_0 21.7 us (floor 5.9): the exact rotation, three shuffles a maximum and the codes;
+// with each lane forming its own four angles, twice each in a warp, 24.7 and 2.7 for the 8 tokens.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -76,7 +77,8 @@ __device__ __forceinline__ uint32_t q8_codes(const float (&x)[4], float d) {
     return code;
 }
 
-constexpr int APPEND_WARPS = 8;
+// Small blocks: a new one takes a finished one's place sooner (8 tokens 2.3 us, 2.5 with 8 warps; Q8_0 21.7, 23.2).
+constexpr int APPEND_WARPS = 4;
 // Heads in flight per lane group: 16 registers of them.
 template <typename T>
 __host__ __device__ constexpr int append_flight() {
@@ -85,23 +87,29 @@ __host__ __device__ constexpr int append_flight() {
 
 // VEC: every input head starts on a multiple of 4 elements.
 template <typename T, bool Q8, int HD, bool VEC>
-__global__ void __launch_bounds__(APPEND_WARPS * 32, 3) paged_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(APPEND_WARPS * 32, 24 / APPEND_WARPS) paged_append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int LANES = HD / 4, ROWS = 32 / LANES;  // lanes of a head, heads at a time
     constexpr int U = append_flight<T>();             // of them in flight
     __shared__ float2 tab[ROPE_TAB];
     __shared__ unsigned long long turns[64];
+    __shared__ float4 angles[APPEND_WARPS][4 * 18];  // of the warp's token: pair p at [p % 4][p / 4], 18 apart, so in different banks
+    static_assert(APPEND_WARPS * 32 >= ROPE_TAB && APPEND_WARPS * 32 >= 64, "a thread an entry");
     if (threadIdx.x < ROPE_TAB) tab[threadIdx.x] = ROPE_COS[threadIdx.x];
-    if (threadIdx.x >= 128 && threadIdx.x < 192) turns[threadIdx.x - 128] = a.r.turns[threadIdx.x - 128];
+    if (threadIdx.x < 64) turns[threadIdx.x] = a.r.turns[threadIdx.x];
     __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int heads = 2 * a.nkv + a.nh;
+    const int sub = lane / LANES, d = lane % LANES * 4;  // the head of the warp's, and the lane's dims d .. d + 3
+    const int half = a.r.rot / 2;
+    const bool turned = a.rotate && d < a.r.rot;
+    const bool shuffles = half % 4 == 0;
+    const int partner = lane + (a.r.pairs ? 0 : d < half ? half / 4 : -(half / 4));
     const int unit = blockIdx.x * APPEND_WARPS + warp;
     const int token = unit / a.groups;
     if (token >= a.tokens) return;
-    const int heads = 2 * a.nkv + a.nh;
     const int h0 = (unit - token * a.groups) * a.per, h1 = min(heads, h0 + a.per);
-    const int sub = lane / LANES, d = lane % LANES * 4;  // the head of the warp's, and the lane's dims d .. d + 3
     // The warp's heads: [k0, k1) of K, [v0, v1) of V, [q0, q1) of the queries.
     const int k0 = min(h0, a.nkv), k1 = min(h1, a.nkv);
     const int v0 = min(max(h0 - a.nkv, 0), a.nkv), v1 = min(max(h1 - a.nkv, 0), a.nkv);
@@ -140,19 +148,23 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, 3) paged_append_kernel(cons
     int page = -1;
     if (h0 < 2 * a.nkv) page = a.table[(int64_t)lo * a.table_ld + in_table];
 
-    const int half = a.r.rot / 2;
-    const bool turned = a.rotate && d < a.r.rot;
-    const bool shuffles = half % 4 == 0;
-    const int partner = lane + (a.r.pairs ? 0 : d < half ? half / 4 : -(half / 4));
     float ch[4], cl[4], sh[4], sl[4];  // the sines with the sign that they are added with
-    if (turned && (k0 < k1 || q0 < q1)) {
-        float2 c, s;
+    if (a.rotate && (k0 < k1 || q0 < q1)) {
+        // each pair's angle by one lane, then to those that hold its dims
+        for (int p = lane; p < half; p += 32) {
+            float2 c, s;
+            rope_angle<true>(turns[p], pos, a.r.mh, a.r.ml, tab, c, s);
+            angles[warp][(p & 3) * 18 + (p >> 2)] = make_float4(c.x, c.y, s.x, s.y);
+        }
+        __syncwarp();
+        if (turned) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int pair = a.r.pairs ? (d + e) >> 1 : d + e < half ? d + e : d + e - half;
-            if (!a.r.pairs || !(e & 1)) rope_angle<true>(turns[min(pair, 63)], pos, a.r.mh, a.r.ml, tab, c, s);
-            const bool plus = a.r.pairs ? (e & 1) != 0 : d + e >= half;
-            ch[e] = c.x, cl[e] = c.y, sh[e] = plus ? s.x : -s.x, sl[e] = plus ? s.y : -s.y;
+            for (int e = 0; e < 4; ++e) {
+                const int pair = min(a.r.pairs ? (d + e) >> 1 : d + e < half ? d + e : d + e - half, half - 1);
+                const float4 v = angles[warp][(pair & 3) * 18 + (pair >> 2)];
+                const bool plus = a.r.pairs ? (e & 1) != 0 : d + e >= half;
+                ch[e] = v.x, cl[e] = v.y, sh[e] = plus ? v.z : -v.z, sl[e] = plus ? v.w : -v.w;
+            }
         }
     }
     if ((unsigned)page >= (unsigned)a.n_pages) {
