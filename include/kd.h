@@ -627,7 +627,7 @@ kd_status kd_rope_plan(const kd_rope_config* cfg, kd_rope_table* out);
  * rotation's transpose) to out + t * ld_out + h * head_dim.  dtype: of x and out (fp32 is
  * rounded once; fp16 and bf16 are computed in fp32 and rounded once more).  out may be x
  * with ld_out = ld; otherwise they must not overlap.  x and out are aligned to
- * their type.  n_tokens = 0 does nothing.
+ * their type.  n_tokens = 0 does nothing (the pointers may be null then).
  * Errors: KD_ERR_INVALID_ARG (null or misaligned pointers, a bad table, dtype, n_tokens < 0,
  * n_heads < 1, ld or ld_out < n_heads * head_dim), KD_ERR_UNSUPPORTED (more
  * than 2^31 - 1 heads in all). */
@@ -648,7 +648,8 @@ kd_status kd_rope(const kd_rope_table* rope, const void* x, int32_t dtype, int64
  * rope: NULL for keys and queries that are not rotated; else its head_dim must be
  * the cache's.  q, q_out: NULL, with n_heads = 0, for no queries.  Rows of pages
  * that belong to no new position stay as they were.  No two new rows may share a
- * place; outputs must not overlap inputs.
+ * place; outputs must not overlap inputs.  Counts that are all 0 do nothing (k_new, v_new, q and
+ * q_out may be null then).
  * starts[b] + counts[b] <= table_ld * page_size, and below 2^31.  head_dim is 64 or 128 (Q8_0: 128).
  * Pages and q_out 16-byte aligned, k_new, v_new and q to their type.
  * Errors: KD_ERR_BATCH (n_seqs), KD_ERR_POSITION (starts, counts), KD_ERR_UNSUPPORTED

@@ -295,7 +295,7 @@ static kd_status append_call(const char* fn, bool q8, const kd_rope_table* rope,
                              uint16_t* vs, const int32_t* table, int32_t table_ld, const int32_t* starts,
                              const int32_t* counts, int32_t n_seqs, int32_t nh, int32_t nkv, int32_t hd, int32_t n_pages,
                              int32_t ps, float* q_out, int32_t* fault, kd_stream stream) {
-    if (!k || !v || !kp || !vp || (q8 && (!ks || !vs)) || !table || !starts || !counts || (nh > 0 && (!q || !q_out)))
+    if (!kp || !vp || (q8 && (!ks || !vs)) || !table || !starts || !counts)
         return failf(KD_ERR_INVALID_ARG, "%s: null argument", fn);
     if (n_seqs < 1 || n_seqs > KD_PAGED_MAX_SEQS)
         return failf(KD_ERR_BATCH, "%s: n_seqs=%d outside [1, %d]", fn, n_seqs, KD_PAGED_MAX_SEQS);
@@ -334,6 +334,7 @@ static kd_status append_call(const char* fn, bool q8, const kd_rope_table* rope,
         k_ld > INT64_MAX / 4 / (total + 1) || v_ld > INT64_MAX / 4 / (total + 1) || (nh && q_ld > INT64_MAX / 4 / (total + 1)))
         return failf(KD_ERR_INVALID_ARG, "%s: k_ld %lld, v_ld %lld, q_ld %lld", fn, (long long)k_ld, (long long)v_ld, (long long)q_ld);
     if (!total) return KD_OK;
+    if (!k || !v || (nh > 0 && (!q || !q_out))) return failf(KD_ERR_INVALID_ARG, "%s: null argument", fn);
     a.k = k;
     a.v = v;
     a.q = q;

@@ -292,7 +292,7 @@ kd_status kd_rope(const kd_rope_table* rope, const void* x, int32_t dtype, int64
                   int32_t n_tokens, int32_t n_heads, void* out, int64_t ld_out, kd_stream stream) {
     using kd::failf;
     const char* fn = "kd_rope";
-    if (!rope || !x || !positions || !out) return failf(KD_ERR_INVALID_ARG, "%s: null argument", fn);
+    if (!rope || (n_tokens && (!x || !positions || !out))) return failf(KD_ERR_INVALID_ARG, "%s: null argument", fn);
     const kd_status st = kd::rope_table_check(fn, rope);
     if (st != KD_OK) return st;
     if (dtype < KD_F32 || dtype > KD_BF16) return failf(KD_ERR_INVALID_ARG, "%s: dtype %d", fn, dtype);
@@ -304,7 +304,7 @@ kd_status kd_rope(const kd_rope_table* rope, const void* x, int32_t dtype, int64
     const uintptr_t mask = dtype == KD_F32 ? 3 : 1;
     if ((((uintptr_t)x | (uintptr_t)out) & mask) || ((uintptr_t)positions & 3))
         return failf(KD_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
-    if (x == out && ld != ld_out) return failf(KD_ERR_INVALID_ARG, "%s: in place, but ld %lld and ld_out %lld", fn, (long long)ld, (long long)ld_out);
+    if (n_tokens && x == out && ld != ld_out) return failf(KD_ERR_INVALID_ARG, "%s: in place, but ld %lld and ld_out %lld", fn, (long long)ld, (long long)ld_out);
     if ((int64_t)n_tokens * n_heads > 0x7fffffff) return failf(KD_ERR_UNSUPPORTED, "%s: %d tokens of %d heads", fn, n_tokens, n_heads);
     if (!n_tokens) return KD_OK;
     kd::RopeArgs a = {};

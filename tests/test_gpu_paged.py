@@ -633,6 +633,61 @@ def test_two_calls_at_once(kdlib):
         assert np.array_equal(w.view(np.int16), o.cpu().numpy().view(np.int16))
 
 
+@pytest.mark.parametrize("q8", [False, True])
+def test_one_page_many_times(kdlib, q8):
+    """A page in every place of every table: each session sees its rows again and again, as it would see copies."""
+    ps, B = 32, 12
+    c = Attn(q8, 16, 4, 128, ps, [ps], seed=51)
+    lens = [ps * 64 - 5 * b for b in range(B)]
+    c.q = np.random.default_rng(5).standard_normal((B, 16, 128)).astype(np.float32)
+    c.dq, c.lens = torch.from_numpy(c.q).cuda(), np.array(lens, np.int32)
+    page = int(c.pool.table[0, 0])
+    c.pool.table = np.full((B, 64), page, np.int32)
+    c.table = c.pool.device_table()
+    one = c.kv[0]
+    c.kv = [[np.tile(x, (1, 64, 1))[:, :n] for x in one] for n in lens]
+    c.check(c.run(kdlib))
+    c.rows, c.prefix = np.array([B], np.int32), np.array([ps * 62], np.int32)
+    c.check(c.run(kdlib))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_keys_appended_on_another_stream(kdlib, q8):
+    """Rows appended on a stream that the attention's waits for, eager and in a graph of both."""
+    kd = kdlib
+    c = Attn(q8, 32, 8, 128, 16, [1300 + 31 * i for i in range(16)], [(16, 1290)], seed=61)
+    new, plan = [normal(s, (16, 8, 128)) for s in (3, 4)], kd_plan(kd, 128)
+    want, out, ws, side = c.run(kd), c.new_out(), c.workspace(kd), torch.cuda.Stream()
+
+    def step(k, v):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        args = (plan, k, v, *c.pool.planes, c.table, c.lens - 1, [1] * 16, 8)
+        if q8:
+            kd.kd_paged_append_q8(*args, c.pool.n_pages, 16, stream=side)
+        else:
+            kd.kd_paged_append(*args, 128, c.pool.n_pages, 16, stream=side)
+        main.wait_stream(side)
+        c.call(kd, out, ws, stream=main)
+    step(*new)
+    torch.cuda.synchronize()
+    with_new = out.cpu().numpy()
+    assert np.array_equal(with_new, c.run(kd)) and not np.array_equal(with_new, want)
+    k, v = (torch.zeros_like(x) for x in new)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(k, v)
+    for _ in range(3):
+        for x, y in ((k, new[0]), (v, new[1])):
+            x.zero_()
+        g.replay()
+        k.copy_(new[0])
+        v.copy_(new[1])
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(with_new, out.cpu().numpy())
+
+
 @pytest.mark.parametrize("groups", [[], [(14, 1280), (2, 0)]])
 @pytest.mark.parametrize("q8", [False, True])
 def test_offsets_past_32_bits(kdlib, q8, groups):

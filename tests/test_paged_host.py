@@ -127,7 +127,7 @@ def table(**kw):
     (dict(T=2 ** 31 - 1), UNSUPPORTED),
     (dict(rope=dict(rot_dim=0)), INVALID), (dict(rope=dict(rot_dim=130)), INVALID), (dict(rope=dict(head_dim=512)), INVALID),
     (dict(rope=dict(layout=2)), INVALID), (dict(rope=dict(reserved=1)), INVALID), (dict(rope=dict(magnitude=float("inf"))), INVALID),
-    (dict(T=0), 0),
+    (dict(T=0), 0), (dict(T=0, x=None, out=None, pos=None, ld_out=1024), 0), (dict(T=0, rope=None), INVALID),
 ])
 def test_rope_refusals(lib, change, status):
     a = dict(rope={}, x=D, dtype=0, ld=512, pos=D, T=8, H=4, out=2 * D, ld_out=512)
@@ -319,3 +319,17 @@ def test_binding_sizes(calls):
             kd.kd_attn_paged_decode_q8(torch.zeros(1, 4, 128), *planes, tab, [3], 4, 2, 4, 16, torch.zeros(1, 512, dtype=torch.float16), ws)
         with pytest.raises(ValueError, match="a plane of the cache"):
             kd.kd_paged_append_q8(None, torch.zeros(1, 2, 128), torch.zeros(1, 2, 128), *planes, tab, [0], [1], 2, 4, 16)
+
+
+def test_nothing_to_do(calls):
+    """No tokens, or no new row in any session: torch's empty tensors have no address."""
+    plan = kd.kd_rope_plan(64, 1e4)
+    x = torch.zeros(0, 2, 64)
+    assert x.data_ptr() == 0
+    kd.kd_rope(plan, x, torch.zeros(0, dtype=torch.int32), x)
+    kd.kd_rope(plan, torch.zeros(4, 4, 64)[:0, :2], torch.zeros(0, dtype=torch.int32), x)
+    pages, tab = torch.zeros(4, 2, 16, 64, dtype=torch.float16), torch.zeros(2, 3, dtype=torch.int32)
+    for kw in (dict(), dict(q=torch.zeros(0, 4, 64), q_out=torch.zeros(0, 4, 64), n_heads=4)):
+        kd.kd_paged_append(plan, x, x, pages, pages, tab, [5, 9], [0, 0], 2, 64, 4, 16, **kw)
+    with pytest.raises(kd.KdError, match="position"):
+        kd.kd_paged_append(plan, x, x, pages, pages, tab, [5, 49], [0, 0], 2, 64, 4, 16)
