@@ -12,9 +12,9 @@
 //
 // Few tokens are bound by a launch and two dependent loads (a position's page, then the
 // row): 8 tokens of 32 + 8 heads take 2.3 us, an empty launch 2.1.  Many are bound by issue, near
-// memory's rate: 8.8 k bf16 tokens of 32 + 8 heads of 128 (277 MB) 51 us, 5.4 TB/s; with K, V and queries
+// memory's rate: 8.8 k bf16 tokens of 32 + 8 heads of 128 (277 MB) 48 us, 5.7 TB/s; with K, V and queries
 // in one loop, a head's kind asked for each time, 64; with blocks that stay and take the next token, 62 (the last ones are
-// waited for).  6.3 k tokens of 8 heads into Q8_0 21.7 us (floor 5.9): the exact rotation, three shuffles a maximum and the codes;
+// waited for).  6.3 k tokens of 8 heads into Q8_0 21.4 us (floor 5.9): the exact rotation, three shuffles a maximum and the codes;
 // with each lane forming its own four angles, twice each in a warp, 24.7 and 2.7 for the 8 tokens.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -77,19 +77,21 @@ __device__ __forceinline__ uint32_t q8_codes(const float (&x)[4], float d) {
     return code;
 }
 
-// Small blocks: a new one takes a finished one's place sooner (8 tokens 2.3 us, 2.5 with 8 warps; Q8_0 21.7, 23.2).
+// Small blocks: a new one takes a finished one's place sooner (8 tokens 2.3 us, 2.5 with 8 warps; Q8_0 rows 21.7, 23.2).
 constexpr int APPEND_WARPS = 4;
-// Heads in flight per lane group: 16 registers of them.
-template <typename T>
+constexpr int APPEND_PER_SM = 7;  // 72 registers a thread: long prompts 48.4 us, 51.1 with 6 blocks, 51.5 with 8
+// Heads in flight per lane group: 16 registers of them (long prompts 48.4 us, 50.2 with 8); Q8_0, which needs more for its codes, 8
+// (21.4 us, 22.5 with 16).
+template <typename T, bool Q8>
 __host__ __device__ constexpr int append_flight() {
-    return 16 / (int)sizeof(T);
+    return (Q8 ? 8 : 16) / (int)sizeof(T);
 }
 
 // VEC: every input head starts on a multiple of 4 elements.
 template <typename T, bool Q8, int HD, bool VEC>
-__global__ void __launch_bounds__(APPEND_WARPS * 32, 24 / APPEND_WARPS) paged_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(APPEND_WARPS * 32, APPEND_PER_SM) paged_append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int LANES = HD / 4, ROWS = 32 / LANES;  // lanes of a head, heads at a time
-    constexpr int U = append_flight<T>();             // of them in flight
+    constexpr int U = append_flight<T, Q8>();         // of them in flight
     __shared__ float2 tab[ROPE_TAB];
     __shared__ unsigned long long turns[64];
     __shared__ float4 angles[APPEND_WARPS][4 * 18];  // of the warp's token: pair p at [p % 4][p / 4], 18 apart, so in different banks
@@ -265,7 +267,7 @@ static cudaError_t launch_append(AppendArgs& a, bool q8, int hd, cudaStream_t s)
     const bool vec = fours(a.k, a.k_ld) && fours(a.v, a.v_ld) && (!a.nh || fours(a.q, a.q_ld));
     // Heads of a warp: as many as leave every SM some forty warps (the angles are formed once for
     // them), whole flights where it has several.
-    constexpr int U = append_flight<T>();
+    const int U = q8 ? append_flight<T, true>() : append_flight<T, false>();
     const int heads = 2 * a.nkv + a.nh, rows = hd == 64 ? 2 : 1;
     int64_t per = (int64_t)a.tokens * heads / (152 * 40);
     per = per < rows ? rows : per < U * rows ? per / rows * rows : per / (U * rows) * (U * rows);

@@ -17,7 +17,8 @@ Tolerances, per element (derived; u = x_a, w = x_b the pair, m the magnitude):
   + 9 2^-23), S = max_t sum_i |q_i k_ti| / sqrt(hd).  Weights: twice that (numerator and
   denominator) plus 2^-21 (expf, p's pair); a key's weight passes at most len/32 + 20
   further sums or products with a rescaling factor (its chain's pieces, warps, records), 2^-22
-  each.  So o moves by at most eps sum_t p_t |v_t|; then it is rounded to fp16 once."""
+  each.  (On the fifth-generation tensor cores, where prefixes are read once, a sum takes up to three
+  times as many in the worst case; it is held to the same bound.)  So o moves by at most eps sum_t p_t |v_t|; then it is rounded to fp16 once."""
 import math
 import subprocess
 import sys
