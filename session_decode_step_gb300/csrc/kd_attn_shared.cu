@@ -532,27 +532,27 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             const int keys = a.g[s.g].keys;
             {  // the queries, hi and lo: the warp's dims of its 32 rows, 16 dims of 16 rows at a time
                 const uint32_t qt = lane_base + TM_QUERIES + part * (DIMS / 2);
+                const int lg = 31 - __clz(a.gq);  // a power of two
+                float4 u[4][DIMS / 16];           // rows 8 apart, all on their way at once
 #pragma unroll
-                for (int rh = 0; rh < 2; ++rh) {
-                    float4 u[2][DIMS / 16];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int row = (warp & 3) * 32 + 16 * rh + 8 * e + (lane >> 2), qi = q0 + row;
-                        const float* src = a.q + ((size_t)(a.g[s.g].lead + qi / a.gq) * a.nh + (size_t)s.h * a.gq + qi % a.gq) * HD + part * DIMS + 4 * (lane & 3);
-#pragma unroll
-                        for (int k = 0; k < DIMS / 16; ++k) {
-                            u[e][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (row < nq) u[e][k] = *reinterpret_cast<const float4*>(src + 16 * k);
-                        }
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const int row = (warp & 3) * 32 + 8 * e + (lane >> 2), qi = q0 + row;
+                    const float* src = a.q + ((size_t)(a.g[s.g].lead + (qi >> lg)) * a.nh + (size_t)(s.h << lg) + (qi & (a.gq - 1))) * HD + part * DIMS + 4 * (lane & 3);
 #pragma unroll
                     for (int k = 0; k < DIMS / 16; ++k) {
-                        const float4 x = u[0][k], y = u[1][k];
-                        const uint32_t at = qt + ((uint32_t)(16 * rh) << 16) + 8 * k;
+                        u[e][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (row < nq) u[e][k] = *reinterpret_cast<const float4*>(src + 16 * k);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e += 2)
+#pragma unroll
+                    for (int k = 0; k < DIMS / 16; ++k) {
+                        const float4 x = u[e][k], y = u[e + 1][k];
+                        const uint32_t at = qt + ((uint32_t)(8 * e) << 16) + 8 * k;
                         tc_st_16x8(at, f2_hi(x.x, x.y), f2_hi(x.z, x.w), f2_hi(y.x, y.y), f2_hi(y.z, y.w));
                         tc_st_16x8(at + HD / 2, f2_lo(x.x, x.y), f2_lo(x.z, x.w), f2_lo(y.x, y.y), f2_lo(y.z, y.w));
                     }
-                }
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
