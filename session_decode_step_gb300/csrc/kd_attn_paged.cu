@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
                 for (int i = threadIdx.x; i < a.nh * HD; i += PAGED_WARPS * 32) a.out[(size_t)b * a.nh * HD + i] = __float2half_rn(0.0f);
     }
     if (left <= 0) {
-        if (a.late_wait) pdl_wait();
+        if (a.late_wait) pdl_wait();  // (the only CTA)
         return;
     }
 
@@ -538,7 +538,8 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
         if (left > 2) nn.next(a);
         pg_nn = look_up(nn, left > 2);
     }
-    if (a.late_wait) pdl_wait();
+    // One CTA sees to it that this kernel does not end before the one beside it; the others leave their place to the next.
+    if (a.late_wait && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 // The merge of a (session, head) that several CTAs share: out = sum_i w_i o_i / sum_i w_i l_i

@@ -41,7 +41,7 @@ struct PagedArgs {
     int* fault;                 // nullable
     int* err;
     int table_ld, n_pages, ps, B, nh, nkv, ctas;
-    int late_wait;              // started beside the kernel before, whose end it awaits at its own
+    int late_wait;              // started beside the kernel before, whose end the last CTA awaits at its own
     float scale;
     Shares share;               // of all blocks, among the CTAs
     // Session b reads keys [from, to); those before lead_keys through session lead's table.  A session's

@@ -18,12 +18,16 @@ constexpr int PAGED_HEAD_BYTES = 256 + SHARED_MAX_CTAS * 4;  // the workspace's 
 // Records of the sessions' own keys: one per CTA and (session, head) at most.
 static size_t paged_records(int B, int nkv) { return (size_t)PAGED_MAX_CTAS + (size_t)B * nkv; }
 
-// A group's shared keys go to the kernel that reads them once where that saves its other sessions
-// this many bytes of reading: the kernel costs some 4 us (7 on Q8_0 caches) of its own before it gains.  32 heads over 8 KV
-// heads of 128, each session with 128 keys of its own, read once / by each: 8 sessions of 512 keys (14 MB saved) 9.8 / 7.5 us,
-// of 1024 (28 MB) 10.0 / 10.8, of 4096 15.3 / 19.4; 16 of 512 (30 MB) 10.7 / 10.9, of 2048 14.9 / 19.6, of 8192 19 / 55; on
-// Q8_0 caches 16 of 512 (16 MB) 13.9 / 12.3, 8 of 2048 (30 MB) 13.6 / 14.8, 32 of 8192 35 / 130.
-constexpr int64_t SHARED_SAVES = 24 << 20;
+// A group's shared keys go to the kernel that reads them once where that saves its other sessions this many bytes of
+// reading: the kernel costs some 3 us (5 on Q8_0 caches) of its own before it gains.  32 heads over 8 KV heads of 128, each session
+// with 128 keys of its own, caches not in L2, read once / by each: 3 sessions of 2048 keys (16 MB saved) 10.5 / 8.2 us, 4 of 2048
+// (24 MB) 11.0 / 11.4, 8 of 1024 (28 MB) 10.2 / 11.0, of 8192 17.9 / 33.0, 2 of 8192 (32 MB) 16.3 / 15.9, of 32768 36.7 / 48.0.  On Q8_0
+// caches 4 of 2048 (13 MB) 12.5 / 10.0, 3 of 4096 (17 MB) 14.0 / 14.4, 8 of 2048 (30 MB) 12.8 / 15.2, of 16384 31.3 / 68.5; there a tile takes
+// longer than two sessions' reading of it: 2 of 32768 46.3 / 40.1, 3 45.8 / 54.9.
+static bool shared_once(int rows, int keys, int nkv, int gq, int hd, bool q8) {
+    const int64_t saves = (int64_t)(rows - 1) * keys * nkv * (q8 ? 272 : hd * 4);
+    return rows > 1 && keys > 0 && (q8 ? saves >= 16 << 20 && rows * gq >= 12 : saves >= 24 << 20);
+}
 
 // Choose the sets of CTAs: `side` of them take a (group, head)'s tiles of queries side by side.
 // The time goes as the tiles of all passes over the sets; of equal ones the widest, which read each key
@@ -59,7 +63,10 @@ static void shared_plan(SharedArgs& t, int sms) {
     t.g[t.n_groups].first = (int)first;
     const int64_t total = first * t.nkv;
     t.sets = sms / t.side;
-    if (t.sets > total) t.sets = (int)total;
+    // No more sets than the longest share needs: the SMs left over take the sessions' own keys meanwhile (16 beams behind 8111
+    // keys, 4 tiles a CTA: 17.3 us with 128 CTAs, 19.9 with 152).
+    const int64_t most_tiles = (total + t.sets - 1) / t.sets;
+    t.sets = (int)((total + most_tiles - 1) / most_tiles);
     t.share = Shares((int)total, t.sets);
 }
 
@@ -100,8 +107,7 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
             if (group_rows[g] < 1 || group_rows[g] > B - b)
                 return failf(KD_ERR_INVALID_ARG, "%s: group %d of %d sessions", fn, g, group_rows[g]);
             const int shared = group_prefix[g] / ps * ps;  // the page that the prefix ends in is each session's own
-            const bool once = group_rows[g] > 1 && shared > 0 &&
-                              (int64_t)(group_rows[g] - 1) * shared * nkv * (q8 ? 272 : hd * 4) >= SHARED_SAVES;
+            const bool once = shared_once(group_rows[g], shared, nkv, nh / nkv, hd, q8);
             for (int i = b; i < b + group_rows[g]; ++i) {
                 if (group_prefix[g] < 0 || group_prefix[g] > lens[i])
                     return failf(KD_ERR_POSITION, "%s: prefix %d of a session of length %d", fn, group_prefix[g], lens[i]);

@@ -485,7 +485,7 @@ def test_large_groups(kdlib, q8, nh, nkv, hd):
         c.check(c.run(kdlib))
 
 
-# Prefixes whose reading for every session would cost more than 24 MB: taken once, on the tensor
+# Prefixes whose reading for every session would cost more than 24 MB (Q8_0: 16): taken once, on the tensor
 # cores.  Tiles of 128 keys and 128 (Q8_0: 64) queries with nothing, one 16-key run or nearly all left over, pages
 # smaller and larger than a tile, one tile of queries and many, groups of which only some qualify.
 @pytest.mark.parametrize("q8,nh,nkv,hd,ps,groups,own", [
