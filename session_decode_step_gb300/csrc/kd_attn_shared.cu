@@ -16,9 +16,10 @@
 // at the SM's share of the bf16 rate, while its 64 KB take 1.4 us of the SM's share of the memory's.
 // Q8_0 rows become such pairs, too (three products each), made by eight warps of their own.
 //
-// Two groups of 32 sessions behind 16384 and 15383 keys, 8 KV heads of 128, take 62 us with the sessions' own 91 MB and the
+// Two groups of 32 sessions behind 16384 and 15383 keys, 8 KV heads of 128, take 59 us with the sessions' own 91 MB and the
 // merge, 392 where each reads its prefix; a tile takes 3300 cycles then, so the tensor core bounds it, not memory.  Three
-// groups of 8 on Q8_0 caches behind 26 k keys: 101 us, 311 where each reads, 5600 cycles a tile, most of them for the pairs.
+// groups of 8 on Q8_0 caches behind 26 k keys: 94 us, 311 where each reads, 4400 cycles a tile: shared memory's rate (512 cycles
+// to write a part's pairs, 768 for three products to read them, 270 for the codes, of 2200 a part).
 //
 // CTAs share the tiles of all (group, KV head)s equally (kd_paged.h); what one finds of a
 // (group, head) goes to a record that the merge reads.  Groups of more queries are taken by

@@ -23,7 +23,7 @@ struct Shares {
 
 // The keys of the sessions that each reads for itself are cut into blocks of PAGED_BLOCK.
 // Blocks are numbered session by session, head by head, and every CTA takes an equal share of
-// them in a row, which may end one (session, head) and begin the next.  What a CTA finds of a (session, head) x is record i + x, so a
+// them in a row, which may end one (session, head) and begin the next.  What CTA i finds of (session, head) x is record i + x, so a
 // (session, head)'s records are consecutive and no record is used twice.
 constexpr int PAGED_WARPS = 4;
 constexpr int PAGED_KEYS = 32;  // keys of a warp's piece
