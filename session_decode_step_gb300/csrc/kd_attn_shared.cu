@@ -14,11 +14,13 @@
 // Queries and weights are fp16 pairs hi + lo, as in the kernel of the sessions' own
 // keys, two products each: 4 x 2 x 128^3 flops a tile of 128 keys and 128 queries, 2048 cycles, 1.1 us
 // at the SM's share of the bf16 rate, while its 64 KB take 1.4 us of the SM's share of the memory's.
-// Q8_0 rows become such pairs, too (three products each), made by eight warps of their own.
+// Q8_0 rows become such pairs, too (three products each), made by eight warps of their own.  A row that holds a scale of
+// 512 or more, whose values may leave fp16's range, is divided by a power of two; K's goes back to the scores, V's to the
+// weights, whose maximum such a tile always moves (to look for such rows costs 2 us of the 96 below).
 //
 // Two groups of 32 sessions behind 16384 and 15383 keys, 8 KV heads of 128, take 59 us with the sessions' own 91 MB and the
 // merge, 392 where each reads its prefix; a tile takes 3300 cycles then, so the tensor core bounds it, not memory.  Three
-// groups of 8 on Q8_0 caches behind 26 k keys: 94 us, 311 where each reads, 4400 cycles a tile: shared memory's rate (512 cycles
+// groups of 8 on Q8_0 caches behind 26 k keys: 96 us, 311 where each reads, 4400 cycles a tile: shared memory's rate (512 cycles
 // to write a part's pairs, 768 for three products to read them, 270 for the codes, of 2200 a part).
 //
 // CTAs share the tiles of all (group, KV head)s equally (kd_paged.h); what one finds of a
@@ -164,7 +166,10 @@ struct SharedSmem {
     static constexpr int RING = 0, BARS = SLOTS * TILE;
     static constexpr int MAXIMA = BARS + 320;          // [2][share][row]: what the warps of a row tell each other
     static constexpr int CODES = MAXIMA + 2 * SHARE * QUERIES * 4;  // Q8_0: a part's codes, by thread, and scales, by warp, on their way
-    static constexpr int TOTAL = CODES + (Q8 ? 256 * 4 * 16 + 8 * 128 : 0);
+    static constexpr int EARLY = CODES + 256 * 4 * 16 + 8 * 128;  // Q8_0: V's scales of the K part on its way, by warp
+    static constexpr int UPS = EARLY + 8 * 128;        // [tile % 8][K, V][row]: what rows whose scales are large were divided by
+    static constexpr int LARGE = UPS + 8 * 2 * SHARED_TILE * 4;  // [tile % 8][warp]: 1 where there is such a row, else the warp leaves no divisors
+    static constexpr int TOTAL = Q8 ? LARGE + 8 * 8 : CODES;
     static_assert(TOTAL <= 227 * 1024, "opt-in shared memory");
 };
 // Columns of tensor memory: scores, then weights, of two tiles in turn (128 each); the sums; the queries, hi and lo.
@@ -173,6 +178,16 @@ constexpr uint32_t TM_SUMS = 256, TM_QUERIES = 384;
 // Q8_0: the first of the two places, counted on round the buffers, of K (part 0) or V (1) of a CTA's tile t: in
 // the order K0 K1 V0 K2 V1 K3 V2 ..., as V is made when its tile has been weighed, and then the K after next.
 __device__ __forceinline__ uint32_t shared_place(uint32_t t, int part) { return 2 * (part ? 2 * t + 2 : t ? 2 * t - 1 : 0); }
+
+// Four block scales of a Q8_0 row in fp16: a power of two, 1 to 2^7, by which 128 times each of them is divided
+// into fp16's range (65504 is 128 times 511.75, so 1 for scales below 512).
+__device__ __forceinline__ bool shared_large(uint32_t x, uint32_t y) {
+    return ((((x & (x << 1)) | (y & (y << 1))) & 0x40004000u) != 0);  // an exponent of 2^9 or more
+}
+__device__ __forceinline__ int shared_down(uint32_t x, uint32_t y) {
+    const uint32_t e = __vmaxu2(__vmaxu2(x & 0x7c007c00u, y & 0x7c007c00u), 0x5c005c00u);
+    return min((int)(max(e & 0xffffu, e >> 16) >> 10) - 23, 7);
+}
 
 // A CTA's next tiles of one (group, KV head, pass).
 struct SharedSeg {
@@ -401,11 +416,14 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         struct Codes {
             uint4 v[4];
             __half d[4];
+            int large;   // rows of the warp's, of K or V, have large scales; then those of lanes 0 .. 7 (rows 2 (lane % 2) and
+            uint2 down;  // the next, of i = lane / 2) are divided by 2^x and 2^y
         };
         // The thread's codes and scales of a part, to its own place in shared memory: loads to registers would be
         // waited for together with those of the part after.
         const uint32_t mine_at = smem_u32(smem + L::CODES) + t * 16;
         const uint32_t scales_at = smem_u32(smem + L::CODES) + 256 * 4 * 16 + (t >> 5) * 128;  // the warp's: 4 rows of each i, 8 bytes each
+        const uint32_t early_at = smem_u32(smem + L::EARLY) + (t >> 5) * 128;
         auto fetch = [&](int rows, int part, uint32_t T) {
             const uint8_t* codes = (part ? a.vq : a.kq) + (trow & 15) * 128 + 16 * chunk;
             const unsigned have = __ballot_sync(FULL_MASK, rows >= 0);
@@ -424,9 +442,16 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(scales_at + lane * 16), "l"(scales + (int64_t)max(first, 0) * 8),
                              "r"(first >= 0 ? 16 : 0)
                              : "memory");
+                // V's, too: its tile's weights are formed before it is made
+                if (!part)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(early_at + lane * 16),
+                                 "l"((const uint8_t*)a.vs + ((t >> 5) & 3) * 32 + (lane & 1) * 16 + (int64_t)max(first, 0) * 8), "r"(first >= 0 ? 16 : 0)
+                                 : "memory");
             }
         };
-        auto landed = [&](Codes& f) {
+        unsigned v_large = 0;  // a bit for even and odd tiles
+        // Part `part` of tile T; with K the rows' divisors, V's among them, are left for the warps that weigh.
+        auto landed = [&](Codes& f, int part, uint32_t T) {
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
 #pragma unroll
@@ -439,6 +464,30 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(d) : "r"(scales_at + i * 32 + (trow & 3) * 8 + (chunk >> 1) * 2) : "memory");
                 f.d[i] = __ushort_as_half(d);
             }
+            // Rows with large scales: looked for in the thread's own ones, and with K in V's; all else only where there are any.
+            uint4 of_v = make_uint4(0, 0, 0, 0);
+            if (!part) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = max(top, (uint32_t)__half_as_ushort(f.d[i]) & 0x7fffu);
+                if (lane < 8) of_v = lds_v4(smem + L::EARLY + (t >> 5) * 128 + lane * 16);
+                f.large = __any_sync(FULL_MASK, top >= 0x6000u || shared_large(of_v.x, of_v.y) || shared_large(of_v.z, of_v.w));
+                v_large = (v_large & ~(1u << (T & 1))) | (f.large ? 1u << (T & 1) : 0u);
+                if (lane == 0) smem[L::LARGE + (T & 7) * 8 + (t >> 5)] = (uint8_t)f.large;
+            } else {
+                f.large = (v_large >> (T & 1)) & 1;
+            }
+            f.down = make_uint2(0, 0);
+            if (f.large) {
+                uint4 own = make_uint4(0, 0, 0, 0);
+                if (lane < 8) own = lds_v4(smem + L::CODES + 256 * 4 * 16 + (t >> 5) * 128 + lane * 16);
+                f.down = make_uint2(shared_down(own.x, own.y), shared_down(own.z, own.w));
+                if (!part && lane < 8) {
+                    float* up = reinterpret_cast<float*>(smem + L::UPS) + (T & 7) * 2 * SHARED_TILE + 32 * (lane >> 1) + 4 * (t >> 5) + 2 * (lane & 1);
+                    *reinterpret_cast<float2*>(up) = make_float2((float)(1 << f.down.x), (float)(1 << f.down.y));
+                    *reinterpret_cast<float2*>(up + SHARED_TILE) = make_float2((float)(1 << shared_down(of_v.x, of_v.y)), (float)(1 << shared_down(of_v.z, of_v.w)));
+                }
+            }
             // read before the next part's copies are issued
 #pragma unroll
             for (int i = 0; i < 4; ++i) asm volatile("" : "+r"(f.v[i].x), "+r"(f.v[i].y), "+r"(f.v[i].z), "+r"(f.v[i].w)::"memory");
@@ -449,25 +498,37 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             if (!__all_sync(FULL_MASK, mbar_wait_bounded(empty + s0, ((place / NS) & 1) ^ 1))) return false;
             uint8_t* dst = smem + L::RING + (chunk >> 2) * L::COL + trow * 128;
             const uint32_t c0 = ((2 * (chunk & 3)) ^ (trow & 7)) << 4;  // the second 8 dims are 16 bytes away in it
+            auto pairs = [&](auto large) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __half2 dd = __half2half2(f.d[i]);
-                const uint32_t w[4] = {f.v[i].x, f.v[i].y, f.v[i].z, f.v[i].w};
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t q = (e & 1) ? u8x2_hi_to_half2(w[2 * k + (e >> 1)]) : u8x2_lo_to_half2(w[2 * k + (e >> 1)]);
-                        const __half2 c = *reinterpret_cast<const __half2*>(&q), h = __hmul2_rn(c, dd), l = __hfma2(c, dd, __hneg2(h));
-                        hi[e] = *reinterpret_cast<const uint32_t*>(&h);
-                        lo[e] = *reinterpret_cast<const uint32_t*>(&l);
+                for (int i = 0; i < 4; ++i) {
+                    const __half2 dd = __half2half2(f.d[i]);
+                    const uint32_t w[4] = {f.v[i].x, f.v[i].y, f.v[i].z, f.v[i].w};
+                    __half2 div = dd;
+                    if constexpr (decltype(large)::value) {  // codes are divided, exactly, before the product: a smaller scale of the row keeps its bits
+                        const int from = 2 * i + ((trow >> 1) & 1);
+                        const unsigned k0 = __shfl_sync(FULL_MASK, f.down.x, from), k1 = __shfl_sync(FULL_MASK, f.down.y, from);
+                        div = __float2half2_rn(1.0f / (float)(1 << ((trow & 1) ? k1 : k0)));
                     }
-                    uint8_t* at = dst + i * 32 * 128 + (c0 ^ (k << 4));
-                    *reinterpret_cast<uint4*>(at + s0 * L::TILE) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(at + s1 * L::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t q = (e & 1) ? u8x2_hi_to_half2(w[2 * k + (e >> 1)]) : u8x2_lo_to_half2(w[2 * k + (e >> 1)]);
+                            __half2 c = *reinterpret_cast<const __half2*>(&q);
+                            if constexpr (decltype(large)::value) c = __hmul2_rn(c, div);
+                            const __half2 h = __hmul2_rn(c, dd), l = __hfma2(c, dd, __hneg2(h));
+                            hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+                            lo[e] = *reinterpret_cast<const uint32_t*>(&l);
+                        }
+                        uint8_t* at = dst + i * 32 * 128 + (c0 ^ (k << 4));
+                        *reinterpret_cast<uint4*>(at + s0 * L::TILE) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(at + s1 * L::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
                 }
-            }
+            };
+            if (f.large) pairs(std::true_type{});
+            else pairs(std::false_type{});
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(full + s0);
@@ -508,8 +569,8 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 fetch_k();
                 for (int part = 0, k = 0; k < 2 * s.n && ok; ++k) {
                     Codes f;
-                    landed(f);
                     const int j = part ? nv - 1 : nk - 1, now = part;
+                    landed(f, now, tiles + j);
                     if (k + 1 < 2 * s.n) {
                         part = part ? nk == s.n : s.n == 1 || nk > 1;
                         if (!part) {
@@ -573,6 +634,17 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const unsigned have = runs[(tiles + j) & 7] >> (part * (KEYS / 16));  // their 16-key runs that have a page
+                // (Q8_0) Rows that were divided, and by what: a warp that makes has 4 of 32 rows in a row, and a byte here.
+                uint2 large = make_uint2(0, 0);
+                const float* ups = nullptr;
+                if constexpr (Q8) {
+                    large = *reinterpret_cast<const uint2*>(smem + L::LARGE + ((tiles + j) & 7) * 8);
+                    ups = reinterpret_cast<const float*>(smem + L::UPS) + ((tiles + j) & 7) * 2 * SHARED_TILE + part * KEYS;
+                }
+                const bool any_large = (large.x | large.y) != 0;
+                auto divisors = [&](int v, int i) {  // of K's or V's rows i .. i + 3
+                    return ((i & 16 ? large.y : large.x) >> (2 * (i & 12))) & 0xff ? *reinterpret_cast<const float4*>(ups + v * SHARED_TILE + i) : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                };
                 if (!idle) {
                     constexpr int STEPS = KEYS / 32;
                     const bool all = n == KEYS && (have & ((1u << (KEYS / 16)) - 1)) == (1u << (KEYS / 16)) - 1;
@@ -586,6 +658,23 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                                 if (!(32 * k + i < n && ((have >> (2 * k + (i >> 4))) & 1))) v[i] = __float_as_uint(-INFINITY);
                         }
                     };
+                    if (Q8 && any_large) {  // scores times K's divisors, in their place
+#pragma unroll 1
+                        for (int k = 0; 32 * k < n; ++k) {
+                            tc_ld32(st + 32 * k, v);
+                            tc_wait_ld(v);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 u = divisors(0, 32 * k + i);
+                                v[i] = __float_as_uint(__uint_as_float(v[i]) * u.x);
+                                v[i + 1] = __float_as_uint(__uint_as_float(v[i + 1]) * u.y);
+                                v[i + 2] = __float_as_uint(__uint_as_float(v[i + 2]) * u.z);
+                                v[i + 3] = __float_as_uint(__uint_as_float(v[i + 3]) * u.w);
+                            }
+                            tc_st32(st + 32 * k, v);
+                        }
+                        tc_wait_st();
+                    }
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int k = 0; k < STEPS; ++k)
@@ -600,7 +689,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                     if (m == -INFINITY) {
                         m = mx;
                         f = 0.0f;
-                    } else if ((mx - m) * c > 8.0f) {
+                    } else if ((mx - m) * c > (Q8 && any_large ? 0.0f : 8.0f)) {  // weights of divided rows have their factor to hold, too
                         f = tc_exp2((m - mx) * c);
                         m = mx;
                     }
@@ -642,6 +731,26 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                         }
                     }
                     tc_wait_st();
+                    if (Q8 && any_large) {  // weights times V's divisors: at most 2^14
+#pragma unroll 1
+                        for (int k = 0; 32 * k < n; ++k) {
+                            tc_ld32(st + 32 * k, v);
+                            tc_wait_ld(v);
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float4 u = divisors(1, 32 * k + 2 * i);
+                                const __half2 u0 = __floats2half2_rn(u.x, u.y), u1 = __floats2half2_rn(u.z, u.w);
+#pragma unroll
+                                for (int w = i; w < 32; w += 16) {
+                                    const __half2 h0 = __hmul2(*reinterpret_cast<const __half2*>(&v[w]), u0), h1 = __hmul2(*reinterpret_cast<const __half2*>(&v[w + 1]), u1);
+                                    v[w] = *reinterpret_cast<const uint32_t*>(&h0);
+                                    v[w + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                                }
+                            }
+                            tc_st32(st + 32 * k, v);
+                        }
+                        tc_wait_st();
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();

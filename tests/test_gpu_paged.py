@@ -861,3 +861,67 @@ def test_a_prompt_shared_by_sessions_and_their_steps(kdlib, q8):
                 o, tol = reference(q_rot[b, h * g:(h + 1) * g].double().cpu().numpy(), K[:, h], V[:, h])
                 assert np.all(np.abs(got[b, h * g:(h + 1) * g] - o) <= tol)
     assert fault.item() == 0 and kd.kd_attn_device_status(ws) == 0
+
+
+# ------------------------------------------------- large scales of Q8_0 rows ---
+def plant(c, part, t, h, scale, codes=None, block=0):
+    """Another scale (and codes) for a block of row t of K (part 0) or V (1), a row that all sessions have from the first one's page."""
+    page, row, dims = int(c.pool.table[0, t // c.ps]), t % c.ps, slice(32 * block, 32 * block + 32)
+    quants, scales = c.pool.planes[2 * part:2 * part + 2]
+    scales[page, h, row, block] = scale
+    if codes is not None:
+        quants[page, h, row, dims] = torch.as_tensor(codes + 128, dtype=torch.uint8, device="cuda")
+    values = (quants[page, h, row, dims].cpu().numpy().astype(np.float64) - 128) * float(np.float16(scale))
+    for K_V in c.kv:
+        K_V[part][h, t, dims] = values
+
+
+def check_rounded(c, got):
+    """As Attn.check, where outputs may leave fp16's range: from 65520 on, the middle between its largest value and the
+    next one, rounding gives an infinity."""
+    group = c.nh // c.nkv
+    for b in range(len(c.lens)):
+        for h in range(c.nkv):
+            o, tol = reference(c.q[b, h * group:(h + 1) * group].astype(np.float64), c.kv[b][0][h], c.kv[b][1][h])
+            g = got[b].reshape(c.nh, c.hd)[h * group:(h + 1) * group].astype(np.float64)
+            inf = np.isinf(g)
+            assert np.all(inf | (np.abs(g - o) <= tol)) and np.all(~inf | ((np.abs(o) + tol >= 65520) & (np.sign(g) == np.sign(o)))), (b, h)
+
+
+@pytest.mark.parametrize("B", [2, 12])  # a prefix that each session reads, and one that is read once
+@pytest.mark.parametrize("scale", [511.5, 512.0, 516.0, 600.0, 1100.0, 9000.0, 65504.0])
+def test_large_scales_in_a_shared_prefix(kdlib, B, scale):
+    """Blocks whose values leave fp16's range, in rows of whole tiles and of the last one, in K, in V and in both."""
+    for parts in ((0,), (1,), (0, 1)):
+        c = Attn(True, 32, 8, 128, 16, [1310 + i for i in range(B)], [(B, 1300)], seed=71, kscale=0.3)
+        rng = np.random.default_rng(B)
+        if 0 in parts:
+            # Query dims of block 0 that are whole pairs of fp16 (a few 2^-24 and more) and give scores of ordinary size.
+            unit = 2.0 ** (-24 + math.floor(math.log2(65504 / scale)))
+            c.q[..., :32] = rng.integers(-8, 9, (B, 32, 32)) * unit
+            c.dq = torch.from_numpy(c.q).cuda()
+        for part in parts:
+            for h in range(8):
+                for t in (5 + h, 67, 127, 128 + 33 * h % 128, 1279 - h, 1290):
+                    plant(c, part, t, h, scale, rng.integers(-127, 128, 32))
+                    plant(c, part, t, h, 2.0 ** -7, block=2)  # a small block beside it
+        check_rounded(c, c.run(kdlib))
+
+
+@pytest.mark.parametrize("B", [2, 12])
+def test_large_scales_where_the_maximum_has_grown(kdlib, B):
+    """A tile whose scores are e^3.4 above the first one's, in which values are far out of fp16's range."""
+    c = Attn(True, 8, 8, 128, 16, [1310 + i for i in range(12)], [(12, 1300)], seed=72, kscale=0.05)
+    if B == 2:  # the same sessions, every one with its own reading
+        c.rows, c.prefix = np.array([2] * 6, np.int32), np.array([1300] * 6, np.int32)
+        c.pool.table[:, :81] = c.pool.table[0, :81]
+        c.table = c.pool.device_table()
+    c.q[..., 96:] = 1.0
+    c.dq = torch.from_numpy(c.q).cuda()
+    rng = np.random.default_rng(5)
+    for h in range(8):
+        for t in range(1296):
+            plant(c, 0, t, h, 1.2, np.full(32, 1 if 128 <= t < 256 else 0), block=3)
+        for t in (130 + h, 200, 255):
+            plant(c, 1, t, h, 40000.0, rng.integers(-127, 128, 32), block=1)
+    check_rounded(c, c.run(kdlib))
