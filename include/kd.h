@@ -685,6 +685,10 @@ size_t kd_attn_paged_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_he
  * lengths and groups decide how the keys are split, so a session's result can differ in
  * the last bits between batches.
  * q: device fp32 [B][n_heads][head_dim]; out: device fp16 [B][n_heads * head_dim];
+ * Values: |q| <= 65504, keys and values (Q8_0: scales) finite, scores below 10^7 in size.  A query is taken
+ * to 2^-22 of each of its values or 2^-25, whichever is more, a weight (Q8_0: times the scale of its value)
+ * to 2^-22 of itself or 2^-31 of its head's largest.  A query, key or value out of these bounds makes outputs of its KV head NaN, infinite or, where
+ * all scores are -infinity, zero: of its own session, or with a shared key of the group's.
  * lens, group_rows, group_prefix: host int32.  head_dim 64 or 128 (Q8_0: 128),
  * n_heads 1, 2, 4 or 8 times n_kv_heads, n_kv_heads <= 1024.  lens[b] <= table_ld * page_size and <= KD_PAGED_MAX_LEN.
  * workspace: kd_attn_paged_workspace_bytes(...) bytes, used by one call at a time.

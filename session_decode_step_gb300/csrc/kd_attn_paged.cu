@@ -11,7 +11,10 @@
 // no other CTA has a share of it, else to a record that the merge kernel reads.
 //
 // The products are m16n8k16 MMAs over transposed operands (keys are rows, the group's query
-// heads columns), with queries and weights as fp16 pairs hi + lo, 22 bits in all: the
+// heads columns), with queries and weights as fp16 pairs hi + lo: good to 2^-22 of a value, but no finer than half of
+// fp16's least step, 2^-25, which a value from 2^-3 on does not notice.  Queries are split as they are, so one of 2^-10 keeps 15 bits
+// (a power of two for each row of queries would keep them, and take queries beyond 65504: the merging of the rows' maxima cost shared prefixes
+// 2 to 8 % and this kernel 1.4, and was not kept).  Weights are scaled up first (UP below).  The
 // Q8_0 form scales each 32-dim block's partial scores by the key's block scale in fp32
 // and multiplies the value scales into the weights, so neither cache is rounded again.
 //
@@ -218,8 +221,8 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
             }
         }
     };
-    // Weights are held as e^UP times their value, so that those below fp16's normal range, 2^-14 of the
-    // largest, are whole pairs, too (Q8_0 scales them with the value scales).
+    // Weights are held as e^UP times their value, 403 times: a pair is then good to 2^-22 of a weight or 2^-33 of the
+    // largest (one of 2^-14 of it keeps 19 bits, one of 2^-23 10; Q8_0 scales them with the value scales).
     constexpr float UP = Q8 ? 0.0f : 6.0f;
     // m: the running maximum of head 4j + c, l: the lane's part of its sum, o = sum p v
     // (Q8_0: times 2^oe, so that weights times scales stay in fp16's normal range).

@@ -8,11 +8,11 @@
 // rate (one operand of 4 KB a product of 64 cycles takes half of it) to K and V; scores of two tiles are there
 // in turn, so that one's products run under the other's exponentials.  Four threads hold a query's row, a quarter of
 // the tile's keys each, and tell each other their maxima.  The sums are rescaled only when the
-// maximum has grown by 2^8 or more (the weights lose nothing: they are pairs of fp16, held as 2^7
-// times their value, at most 2^15 then, so that those below 2^-14 of the largest are whole pairs, too).
+// maximum has grown by 2^8 or more.
 //
 // Queries and weights are fp16 pairs hi + lo, as in the kernel of the sessions' own
-// keys, two products each: 4 x 2 x 128^3 flops a tile of 128 keys and 128 queries, 2048 cycles, 1.1 us
+// keys (kd_attn_paged.cu: what pairs are good to; weights are held as 2^7 times their value, at most 2^15 with what the maximum
+// has grown, which leaves room for the rounding of the maximum's product with the scale while scores are below 10^7), two products each: 4 x 2 x 128^3 flops a tile of 128 keys and 128 queries, 2048 cycles, 1.1 us
 // at the SM's share of the bf16 rate, while its 64 KB take 1.4 us of the SM's share of the memory's.
 // Q8_0 rows become such pairs, too (three products each), made by eight warps of their own.  A row that holds a scale of
 // 512 or more, whose values may leave fp16's range, is divided by a power of two; K's goes back to the scores, V's to the
@@ -708,8 +708,8 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                             tc_st16(ot + 16 * k, o);
                         }
                     }
-                    // 2^SH_UP times the weights, up to 2^15 with what the maximum has grown: so that small ones are
-                    // whole pairs of fp16, too (2^(-inf) where no key is seen)
+                    // 2^SH_UP times the weights, up to 2^15 with what the maximum has grown: so that small ones keep
+                    // more bits (2^(-inf) where no key is seen)
                     const float mc = m == -INFINITY ? 0.0f : m * c - SH_UP;
 #pragma unroll
                     for (int k = STEPS - 1; k >= 0; --k) {  // the last are still here

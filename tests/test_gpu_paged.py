@@ -925,3 +925,74 @@ def test_large_scales_where_the_maximum_has_grown(kdlib, B):
         for t in (130 + h, 200, 255):
             plant(c, 1, t, h, 40000.0, rng.integers(-127, 128, 32), block=1)
     check_rounded(c, c.run(kdlib))
+
+
+# ------------------------------------------------ the bounds that kd.h states ---
+def scale_keys(c, f):
+    """K's values times f, a power of two, rounded as the cache holds them."""
+    if c.q8:
+        s = c.pool.planes[1]
+        s.copy_((s.float() * f).half())
+        for b, kv in enumerate(c.kv):
+            quant, scale = c.raw[b][0]
+            kv[0] = (quant.astype(np.float64) * (scale.astype(np.float32) * f).astype(np.float16).astype(np.float64)[..., None]).reshape(kv[0].shape)
+    else:
+        p = c.pool.planes[0]
+        p.copy_((p.float() * f).half())
+        for kv in c.kv:
+            kv[0] = (kv[0] * f).astype(np.float16).astype(np.float64)
+
+
+def check_bounds(c, got):
+    """Attn.check with a query's least step: each of its values may be off by 2^-25, so a score by 2^-25 max_t sum_i |k_ti| /
+    sqrt(hd), and weights by twice that."""
+    group = c.nh // c.nkv
+    for b in range(len(c.lens)):
+        for h in range(c.nkv):
+            K, V = c.kv[b][0][h], c.kv[b][1][h]
+            q = c.q[b, h * group:(h + 1) * group].astype(np.float64)
+            o, tol = reference(q, K, V)
+            step = 2 * 2.0 ** -25 * np.abs(K).sum(1).max() / np.sqrt(c.hd)
+            p = np.exp(q @ K.T / np.sqrt(c.hd) - (q @ K.T).max(1, keepdims=True) / np.sqrt(c.hd))
+            tol = tol + step * ((p / p.sum(1, keepdims=True)) @ np.abs(V))
+            g = got[b].reshape(c.nh, c.hd)[h * group:(h + 1) * group].astype(np.float64)
+            assert np.all(np.abs(g - o) <= tol), (b, h, float((np.abs(g - o) / tol).max()))
+
+
+@pytest.mark.parametrize("B", [2, 12])  # a prefix that each session reads, and one that is read once
+@pytest.mark.parametrize("q8,nh,nkv,hd", [(False, 32, 8, 128), (False, 64, 8, 128), (False, 32, 8, 64), (True, 32, 8, 128), (True, 64, 8, 128)])
+def test_queries_within_their_bounds(kdlib, q8, nh, nkv, hd, B):
+    """Large queries of small keys, small queries of large keys: up to 65504 and down to a value's least step."""
+    n = 2600 if hd == 64 else 1300  # in the larger group past the border of being read once
+    for qscale, kscale in ((2.0 ** 13, 2.0 ** -12), (2.0 ** -7, 2.0 ** 7), (2.0 ** -12, 2.0 ** 12)):
+        c = Attn(q8, nh, nkv, hd, 16, [n + 9 + i for i in range(B)], [(B, n)], seed=81)
+        scale_keys(c, kscale)
+        c.q = np.clip(c.q * np.float32(qscale), -65504, 65504).astype(np.float32)
+        c.q[B - 1, 1] = 0.0
+        c.q[0, 0, :2] = 65504.0 * min(1.0, qscale), -65504.0 * min(1.0, qscale)
+        c.dq = torch.from_numpy(c.q).cuda()
+        check_bounds(c, c.run(kdlib))
+
+
+@pytest.mark.parametrize("B", [2, 12])
+@pytest.mark.parametrize("q8", [False, True])
+def test_scores_near_their_bound(kdlib, q8, B):
+    """Scores of a few 10^6, up to 10^7 in size: the key with the largest one alone, whichever comes first."""
+    c = Attn(q8, 32, 8, 128, 16, [1310 + i for i in range(B)], [(B, 1300)], seed=82)
+    scale_keys(c, 2.0 ** 6)
+    c.q *= np.float32(2.0 ** 15 / np.abs(c.q).max())
+    c.dq = torch.from_numpy(c.q).cuda()
+    got = c.run(kdlib).reshape(B, 32, 128).astype(np.float64)
+    sure = 0
+    for b in range(B):
+        for h in range(32):
+            q, K, V = c.q[b, h].astype(np.float64), c.kv[b][0][h // 4], c.kv[b][1][h // 4]
+            s = K @ q / np.sqrt(128)
+            assert 1e5 < np.abs(s).max() < 1e7
+            # a score is off by (2^-21 + 9 2^-23) sum_i |q_i k_i| / sqrt(hd): the second one is e^-40 of the first at least then
+            off = (2.0 ** -21 + 9 * 2.0 ** -23) * (np.abs(K) @ np.abs(q)).max() / np.sqrt(128)
+            first = s.argmax()
+            if np.sort(s)[-2] < s[first] - 2 * off - 40:
+                sure += 1
+                assert np.all(np.abs(got[b, h] - V[first]) <= 2.0 ** -11 * np.abs(V[first]) + 2.0 ** -19 * np.abs(V[first]) + 2.0 ** -25), (b, h)
+    assert sure >= B * 32 * 9 // 10 and np.isfinite(got).all()
