@@ -610,7 +610,8 @@ typedef struct {
 } kd_rope_config;
 
 /* What the rotating calls take: pair i turns by turns[i] / 2^64 of a whole turn
- * per position (so an integer position's angle is exact modulo a turn). */
+ * per position, its frequency rounded to that: position p's angle, a whole number of them
+ * modulo a turn, is off by |p| 2^-65 of a turn at most. */
 typedef struct {
     int32_t head_dim, rot_dim, layout, reserved;
     double magnitude;

@@ -228,12 +228,64 @@ kd_status rope_table_check(const char* fn, const kd_rope_table* t) {
     return KD_OK;
 }
 
+// Numbers of twice a double's length, as a sum hi + lo of two (|lo| at most half of hi's last bit), good to some 2^-100: a
+// frequency rounded to a double turns by 2^-55 of a turn too much a position, 2^-36 rad at 131072.
+struct Two {
+    double hi, lo;
+};
+static Two sum_of(double x, double y) {
+    const double s = x + y, b = s - x;
+    return {s, (x - (s - b)) + (y - b)};
+}
+static Two negative(Two x) { return {-x.hi, -x.lo}; }
+static Two plus(Two x, Two y) {
+    const Two s = sum_of(x.hi, y.hi), t = sum_of(x.lo, y.lo), u = sum_of(s.hi, s.lo + t.hi);
+    return sum_of(u.hi, u.lo + t.lo);
+}
+static Two times(Two x, Two y) {
+    const double p = x.hi * y.hi;
+    return sum_of(p, std::fma(x.hi, y.hi, -p) + (x.hi * y.lo + x.lo * y.hi));
+}
+static Two over(Two x, Two y) {
+    const double q = x.hi / y.hi;
+    if (!std::isfinite(q) || q == 0.0) return {q, 0.0};
+    const Two r = plus(x, negative(times(y, {q, 0.0})));
+    return sum_of(q, (r.hi + r.lo) / y.hi);
+}
+static Two power_of(Two x, int n) {
+    Two r = {1.0, 0.0};
+    for (; n; n >>= 1) {
+        if (n & 1) r = times(r, x);
+        x = times(x, x);
+    }
+    return r;
+}
+// theta^(-1 / n): a step of Newton's method from the double next to it.  (In two factors, as theta^-1 may leave a double's
+// normal range; n = 1 is nobody's: a single pair turns by 1.)
+static Two root_of_inverse(double theta, int n) {
+    const Two y = {std::pow(theta, -1.0 / n), 0.0};
+    if (n == 1) return y;
+    const Two r = times(times({theta, 0.0}, power_of(y, n / 2)), power_of(y, n - n / 2));  // 1 + n times y's relative error
+    const Two e = plus({1.0, 0.0}, negative(r));
+    return plus(y, over(times(y, e), {(double)n, 0.0}));
+}
+// x turns modulo 1 (positions are whole, so whole turns drop out), in 2^-64 of one, rounded.
+static uint64_t turns_of(Two x) {
+    if (std::fabs(x.lo) >= 1.0) x.lo -= std::floor(x.lo);
+    x = sum_of(x.hi - std::floor(x.hi), x.lo);
+    if (x.hi < 0.0) x = plus(x, {1.0, 0.0});
+    if (x.hi >= 1.0) x = plus(x, {-1.0, 0.0});
+    const double top = std::ldexp(x.hi, 32), whole = std::floor(top);
+    // (lo may be below 0, and the sum a whole turn: both are right modulo 2^64)
+    return ((uint64_t)(int64_t)whole << 32) + (uint64_t)(int64_t)std::floor(std::ldexp(top - whole, 32) + std::ldexp(x.lo, 64) + 0.5);
+}
+
 }  // namespace kd
 
 extern "C" {
 
 kd_status kd_rope_plan(const kd_rope_config* c, kd_rope_table* out) {
-    using kd::failf;
+    using namespace kd;
     const char* fn = "kd_rope_plan";
     if (!c || !out) return failf(KD_ERR_INVALID_ARG, "%s: null argument", fn);
     if (c->head_dim > KD_ROPE_MAX_DIM)
@@ -265,24 +317,24 @@ kd_status kd_rope_plan(const kd_rope_config* c, kd_rope_table* out) {
     t.rot_dim = n;
     t.layout = c->layout;
     t.magnitude = c->magnitude;
+    const Two one = {1.0, 0.0}, two_pi = {turn, 0x1.1a62633145c07p-52}, step = root_of_inverse(c->theta, n / 2);
+    Two power = one;  // theta^(-2i / n)
     for (int i = 0; i < n / 2; ++i) {
-        double f = std::pow(c->theta, -2.0 * i / n);
-        if (c->scaling == KD_ROPE_LINEAR) f /= c->factor;
+        Two f = power;
+        power = times(power, step);
+        if (c->scaling == KD_ROPE_LINEAR) f = over(f, {c->factor, 0.0});
         if (blends) {
-            double slow;  // how much of the pair's pace is slowed
+            Two slow;  // how much of the pair's pace is slowed
             if (c->scaling == KD_ROPE_BANDS)
-                slow = 1.0 - std::fmin(1.0, std::fmax(0.0, (c->original_ctx * f / turn - c->low) / (c->high - c->low)));
+                slow = plus(one, negative(over(plus(over(times({(double)c->original_ctx, 0.0}, f), two_pi), {-c->low, 0.0}), plus({c->high, 0.0}, {-c->low, 0.0}))));
             else
-                slow = std::fmin(1.0, std::fmax(0.0, (i - a) / std::fmax(b - a, 0.001)));
-            f *= (1.0 - slow) + slow / c->factor;
+                slow = over({i - a, 0.0}, {std::fmax(b - a, 0.001), 0.0});
+            if (slow.hi <= 0.0) slow = {0.0, 0.0};
+            if (slow.hi >= 1.0) slow = one;
+            f = times(f, plus(plus(one, negative(slow)), over(slow, {c->factor, 0.0})));
         }
-        if (!std::isfinite(f)) return failf(KD_ERR_INVALID_ARG, "%s: factor %g leaves no finite frequency", fn, c->factor);
-        // turns per position modulo 1, to 2^-64 (positions are whole, so whole turns drop out)
-        double r = f / turn;
-        r -= std::floor(r);
-        t.turns[i] = (uint64_t)std::ldexp(r, 32) << 32;
-        const double rest = std::ldexp(r, 32) - std::floor(std::ldexp(r, 32));
-        t.turns[i] += (uint64_t)std::floor(std::ldexp(rest, 32) + 0.5);
+        if (!std::isfinite(f.hi)) return failf(KD_ERR_INVALID_ARG, "%s: factor %g leaves no finite frequency", fn, c->factor);
+        t.turns[i] = turns_of(over(f, two_pi));
     }
     *out = t;
     return KD_OK;

@@ -2,7 +2,7 @@
 // number, and its cosine and sine.
 //
 // Pair i turns by turns[i] / 2^64 of a turn per position, so position p's angle is
-// the low 64 bits of p * turns[i]: exact modulo a turn at any position, where an fp32
+// the low 64 bits of p * turns[i], off by |p| 2^-65 of a turn (2^-45 rad at 131072), where an fp32
 // angle is off by 2e-3 at 32k positions and an fp64 one costs a range reduction on
 // two units per SM.  The angle is the nearest 256th of a turn, whose cosine and sine
 // come from a table of fp32 pairs, and a rest of at most pi / 256, whose sine and cosine

@@ -1,6 +1,7 @@
 """Rotary positions, paged append and paged attention without a GPU: the plan's frequencies,
 every refusal made on the host before CUDA is touched, the workspace size, the binding's checks."""
 import ctypes as C
+import decimal
 import math
 
 import numpy as np
@@ -76,6 +77,39 @@ def test_plan_frequencies(lib, rot, theta, kw):
     # modulo a turn: both are good to a few 2^-53 of the frequency, and the table to 2^-64 of a turn
     err = np.abs((turns(t) - want + 0.5) % 1.0 - 0.5)
     assert np.all(err <= np.abs(want) * 2.0 ** -50 + 2.0 ** -53)
+
+
+TWO_PI = decimal.Decimal("6.28318530717958647692528676655900576839433879875021164194989")
+
+
+@pytest.mark.parametrize("rot", [2, 6, 20, 64, 128, 250, 256])
+@pytest.mark.parametrize("theta", [10000.0, 500000.0, 1.5, 1e9 / 3, 1.0 + 2.0 ** -40, 1e300])
+@pytest.mark.parametrize("kw", [dict(), dict(scaling=1, factor=4.0), dict(scaling=1, factor=0.3), dict(scaling=1, factor=1e-30), dict(scaling=1, factor=1e25),
+                                dict(scaling=2, factor=8.1, low=1.1, high=4.0, original_ctx=8192),
+                                dict(scaling=3, factor=10.0, low=1.0, high=32.0, original_ctx=2048)])
+def test_plan_turns_to_the_last_bit(lib, rot, theta, kw):
+    """turns[] against 60 digits: half a unit for the rounding to 2^-64 of a turn, 2^-96 of the frequency for pairs of doubles
+    (2^-104 each in some 20 operations), and the digits of 2 pi here."""
+    t = kd.kd_rope_plan(256, theta, rot_dim=rot, **kw)
+    with decimal.localcontext(decimal.Context(prec=110)):
+        one, factor, low, high = (decimal.Decimal(x) for x in (1, kw.get("factor", 1.0), kw.get("low", 1.0), kw.get("high", 4.0)))
+        ln = decimal.Decimal(theta).ln()
+        for i in range(rot // 2):
+            f = (-2 * ln * i / rot).exp()
+            if kw.get("scaling") == 1:
+                f /= factor
+            elif kw.get("scaling") == 2:
+                keep = min(one, max(0 * one, (kw["original_ctx"] * f / TWO_PI - low) / (high - low)))
+                f *= keep + (1 - keep) / factor
+            elif kw.get("scaling") == 3:
+                a, b = (rot * math.log(kw["original_ctx"] / (2 * math.pi * x)) / (2 * math.log(theta)) for x in (kw["high"], kw["low"]))
+                a, b = max(0, math.floor(a)), min(rot - 1, math.ceil(b))
+                r = min(one, max(0 * one, decimal.Decimal(i - a) / decimal.Decimal(max(b - a, 0.001))))
+                f *= 1 - r + r / factor
+            want = f / TWO_PI * 2 ** 64
+            off = (decimal.Decimal(t.turns[i]) - want) % 2 ** 64
+            off = min(off, 2 ** 64 - off)
+            assert off <= decimal.Decimal("0.5") + f * 2 ** 64 / 2 ** 96 + f * 2 ** 64 / decimal.Decimal(10) ** 58, (i, off)
 
 
 def test_plan_defaults(lib):
