@@ -118,15 +118,29 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
     PagedAt at;
     if (left > 0) at.seek(a, x0);
     pdl_launch_dependents();
-    if (!a.late_wait) pdl_wait();
+    // Beside the prefix kernel: not its end is waited for, but that it has seen the end of all before it.  Its word, stored
+    // after its own wait and loaded here in acquire order, makes visible what was visible there.  It is stored before this
+    // kernel can start, or at most some instructions later; where it is not seen soon the wait is for the kernel's end.
+    const bool beside = a.started != nullptr;
+    bool seen = false;
+    if (beside) {
+        if (lane == 0)
+            for (int i = 0; i < 256 && !seen; ++i) {
+                unsigned long long x;
+                asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(a.started) : "memory");
+                seen = x == a.call;
+            }
+        seen = __any_sync(FULL_MASK, seen);
+    }
+    if (!seen) pdl_wait();
     if (blockIdx.x == 0) {
-        if (threadIdx.x == 0 && !a.late_wait) *a.err = 0;
+        if (threadIdx.x == 0 && !beside) *a.err = 0;
         for (int b = 0; a.empty && b < a.B; ++b)  // sessions without keys
             if (a.s[b].to == 0)
                 for (int i = threadIdx.x; i < a.nh * HD; i += PAGED_WARPS * 32) a.out[(size_t)b * a.nh * HD + i] = __float2half_rn(0.0f);
     }
     if (left <= 0) {
-        if (a.late_wait) pdl_wait();  // (the only CTA)
+        pdl_wait();  // (the only CTA)
         return;
     }
 
@@ -542,7 +556,7 @@ __global__ void __launch_bounds__(PAGED_WARPS * 32, paged_per_sm<HD, GQ, Q8>()) 
         pg_nn = look_up(nn, left > 2);
     }
     // One CTA sees to it that this kernel does not end before the one beside it; the others leave their place to the next.
-    if (a.late_wait && blockIdx.x == gridDim.x - 1) pdl_wait();
+    if (beside && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 // The merge of a (session, head) that several CTAs share: out = sum_i w_i o_i / sum_i w_i l_i
@@ -579,7 +593,10 @@ __global__ void __launch_bounds__(PAGED_MERGE_WARPS * 32) paged_merge_kernel(con
         int bad = 0;
         for (int k = lane; k < sh.sets * sh.side; k += 32) bad |= sh.status[k];
         bad = __any_sync(FULL_MASK, bad != 0);
-        if (lane == 0) *a.err = bad ? ERR_WAIT_TIMEOUT : 0;
+        if (lane == 0) {
+            *a.err = bad ? ERR_WAIT_TIMEOUT : 0;
+            *sh.started = 0;  // so that a graph's next run finds its word new
+        }
     }
     const int total = n + sets;
     if (!total || (n == 1 && !sets)) return;  // no keys, or written by the CTA itself

@@ -261,7 +261,9 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     SharedSeg head;  // the CTA's first segment
     head.at(a, x0, x1 - x0);
     pdl_wait();
-    pdl_launch_dependents();  // after the wait: the kernel behind this one relies on it, and reads at once
+    if (blockIdx.x == 0 && threadIdx.x == SH_VALUES * 32)  // the kernel behind this one reads what was written before both
+        asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(a.started), "l"(a.call) : "memory");
+    pdl_launch_dependents();  // after the wait, so that no CTA of that kernel starts before it
     const int box = a.box_runs;  // 16-key runs of a copy's box
     // The first of the CTA's queries in a segment's group, and how many (<= 0: none).
     auto first_query = [&](const SharedSeg& s) { return (s.pass * a.side + mine) * L::QUERIES; };

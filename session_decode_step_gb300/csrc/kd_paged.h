@@ -41,7 +41,9 @@ struct PagedArgs {
     int* fault;                 // nullable
     int* err;
     int table_ld, n_pages, ps, B, nh, nkv, ctas;
-    int late_wait;              // started beside the kernel before, whose end the last CTA awaits at its own
+    // Started beside the prefix kernel, which writes `call` here once all before it has ended; NULL: not, waits for the kernel before.
+    const unsigned long long* started;
+    unsigned long long call;
     float scale;
     Shares share;               // of all blocks, among the CTAs
     // Session b reads keys [from, to); those before lead_keys through session lead's table.  A session's
@@ -77,6 +79,8 @@ struct SharedArgs {
     const uint8_t *kq, *vq;  // Q8_0: quants and scales
     const __half *ks, *vs;
     int* status;  // [CTA]: 1 where a bounded wait ran out
+    unsigned long long* started;  // as PagedArgs'; the merge clears it
+    unsigned long long call;
     int table_ld, n_pages, ps, rows, box_runs, nh, nkv, gq, n_groups, side, sets;
     int tile_queries;  // shared_queries()
     float scale;

@@ -1,6 +1,7 @@
 // kd_paged_api.cu -- the paged attention's entry points: checks, the plan, the launches.
 // The plan travels with the launches, so a call copies nothing to the device and can be
 // captured into a graph (its lengths and groups are then part of it; the table is not).
+#include <atomic>
 #include <cmath>
 
 #include "kd_host.h"
@@ -15,6 +16,16 @@ static bool paged_shape(int32_t nh, int32_t nkv, int32_t hd, bool q8) {
 }
 constexpr int PAGED_MAX_KV_HEADS = 1024;
 constexpr int PAGED_HEAD_BYTES = 256 + SHARED_MAX_CTAS * 4;  // the workspace's words before its records: the call's, a CTA's status
+constexpr int PAGED_STARTED = 192;                          // byte of PagedArgs::started among them
+static_assert((2 * KD_MAX_BATCH + 1) * 4 <= PAGED_STARTED, "behind the fault word");
+
+// A word for PagedArgs::call that no other call has, and that memory nobody has written yet will not hold by chance.
+static unsigned long long paged_call_word() {
+    static std::atomic<unsigned long long> calls{0};
+    unsigned long long x = (calls.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9e3779b97f4a7c15ull;
+    x ^= x >> 32;
+    return x ? x : 1;
+}
 // Records of the sessions' own keys: one per CTA and (session, head) at most.
 static size_t paged_records(int B, int nkv) { return (size_t)PAGED_MAX_CTAS + (size_t)B * nkv; }
 
@@ -192,7 +203,8 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
         sh.scale = a.scale;
         sh.tile_queries = shared_queries(q8);
         shared_plan(sh, sms);
-        a.late_wait = 1;
+        a.started = sh.started = (unsigned long long*)((char*)ws + PAGED_STARTED);
+        a.call = sh.call = paged_call_word();
         sh.kq = (const uint8_t*)kp;
         sh.vq = (const uint8_t*)vp;
         sh.ks = a.ks;

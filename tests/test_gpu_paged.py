@@ -996,3 +996,60 @@ def test_scores_near_their_bound(kdlib, q8, B):
                 sure += 1
                 assert np.all(np.abs(got[b, h] - V[first]) <= 2.0 ** -11 * np.abs(V[first]) + 2.0 ** -19 * np.abs(V[first]) + 2.0 ** -25), (b, h)
     assert sure >= B * 32 * 9 // 10 and np.isfinite(got).all()
+
+
+# ------------------------------------------------- steps behind a shared prefix ---
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("q8", [False, True])
+def test_steps_behind_a_prefix_read_once(kdlib, q8, graph):
+    """Steps in one stream without a pause: each appends a key and a value, writes the queries that the attention behind it
+    reads at once, and overwrites what the step before read; every step against the formula."""
+    kd, B, nh, nkv, hd, ps, n, steps = kdlib, 12, 32, 8, 128, 16, 1300, 6
+    c = Attn(q8, nh, nkv, hd, ps, [n + 5 * i + steps for i in range(B)], [(B, n)], seed=91)
+    base, ws = c.lens - steps, c.workspace(kd)
+    for b in range(B):  # the last rows are the steps'
+        base[b] = max(base[b], n)
+    c.lens = base + steps
+    fresh = [[normal(1000 * part + t, (B, h, hd)) for t in range(steps)] for part, h in enumerate((nh, nkv, nkv))]
+    given = [[torch.zeros_like(x) for x in part] for part in fresh] if graph else fresh
+    q_out, outs = torch.empty(B, nh, hd, device="cuda"), [c.new_out() for _ in range(steps)]
+    full = c.lens.copy()
+
+    def run():
+        for t in range(steps):
+            args = (None, given[1][t], given[2][t], *c.pool.planes, c.table, base + t, [1] * B, nkv)
+            extra = dict(q=given[0][t], q_out=q_out, n_heads=nh)
+            if q8:
+                kd.kd_paged_append_q8(*args, c.pool.n_pages, ps, **extra)
+            else:
+                kd.kd_paged_append(*args, hd, c.pool.n_pages, ps, **extra)
+            c.lens = (base + t + 1).astype(np.int32)
+            c.call(kd, outs[t], ws, q=q_out)
+    torch.cuda.synchronize()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        g.replay()  # of zeros
+        for part, new in zip(given, fresh):
+            for x, y in zip(part, new):
+                x.copy_(y)
+        g.replay()
+    else:
+        run()
+    torch.cuda.synchronize()
+    assert kd.kd_attn_device_status(ws) == 0
+    c.lens = full
+    for b in range(B):  # the new rows as they lie in the pages (behind the prefix, in the session's own)
+        for part in range(2):
+            rows = c.pool.rows(part, b, int(base[b]), int(full[b]))
+            values = values_of(*rows) if q8 else rows[0].double().cpu().numpy()
+            c.kv[b][part][:, int(base[b]):int(full[b])] = values.transpose(1, 0, 2)
+            x = torch.stack([fresh[1 + part][t][b] for t in range(steps)]).double().cpu().numpy()
+            assert np.all(np.abs(values - x) <= (np.abs(x).max() / 250 if q8 else 2.0 ** -11 * np.abs(x) + 2.0 ** -25))
+    kv = c.kv
+    for t in range(steps):
+        c.lens = (base + t + 1).astype(np.int32)
+        c.q = fresh[0][t].cpu().numpy()
+        c.kv = [[x[:, :int(c.lens[b])] for x in kv[b]] for b in range(B)]
+        c.check(outs[t].cpu().numpy())
