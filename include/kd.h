@@ -709,6 +709,12 @@ kd_status kd_attn_paged_decode_q8(const float* q, const uint8_t* k_quants, const
                                   int32_t n_pages, int32_t page_size, uint16_t* out, void* workspace,
                                   size_t workspace_bytes, int32_t* fault, kd_stream stream);
 
+/* Debug fault hook, as kd_debug_inject_wait_timeout: the next call of this process that reads a shared
+ * prefix once has one barrier of its first tile's keys (part 0) or values (1) expect a few bytes more
+ * than come.  The waits behind it run out (half a second each), the kernel gives up, kd_attn_device_status
+ * reports it and outputs are not valid; the next call is as ever.  One-shot.  Errors: KD_ERR_INVALID_ARG. */
+kd_status kd_debug_attn_paged_inject_wait_timeout(int32_t part);
+
 /* ------------------------------------------------------------------------
  * Allocation-free variant (no counterpart on the batched-decode pages: it
  * exists for callers, not for the method).

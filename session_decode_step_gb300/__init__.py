@@ -144,6 +144,7 @@ def lib():
             "kd_beam_select": [_vp, C.c_int64, i32, i32, i32, _vp, _vp, i32, i32, _vp, _vp, _vp, _vp, _vp, C.c_size_t,
                                _vp],
             "kd_kv_reorder": [_vpp, i32p, i32, i32, i32, i32, i32, i32p, i32p, i32p, i32, i32, i32, _vp],
+            "kd_debug_attn_paged_inject_wait_timeout": [i32],
             "kd_rope_plan": [C.POINTER(KdRopeConfig), C.POINTER(KdRopeTable)],
             "kd_rope": [_vp, _vp, i32, C.c_int64, _vp, i32, i32, _vp, C.c_int64, _vp],
             "kd_paged_append": [_vp, _vp, C.c_int64, _vp, C.c_int64, _vp, C.c_int64, i32, _vp, _vp, _vp, i32, i32p, i32p,
@@ -782,3 +783,8 @@ def kd_attn_paged_decode_q8(q, k_quants, k_scales, v_quants, v_scales, table, le
     _check((_call or _fast()).paged(q, (k_quants, k_scales, v_quants, v_scales), table, lens,
                                     group_rows, group_prefix, n_heads, n_kv_heads, 128, n_pages, page_size, out, workspace,
                                     fault, stream))
+
+
+def kd_debug_attn_paged_inject_wait_timeout(part: int):
+    """The next call that reads a shared prefix once gives up waiting for its first tile's keys (0) or values (1)."""
+    _check(lib().kd_debug_attn_paged_inject_wait_timeout(int(part)))

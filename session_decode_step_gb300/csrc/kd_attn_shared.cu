@@ -215,13 +215,14 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BARS);
-    uint64_t *empty = full + NS, *s_full = empty + NS, *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *q_free = q_full + 1, *pair = q_free + 1;
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(pair + 4);
+    uint64_t *empty = full + NS, *s_full = empty + NS, *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *q_free = q_full + 1, *pair = q_free + 1, *drained = pair + 4;
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 2);
     volatile int* failed = reinterpret_cast<volatile int*>(tmem_at + 1);
     // The last tiles' 16-key runs that have a page, by tile: an entry is written again after 8 tiles, when the
     // buffers (at most 8, two a tile) have gone round past its tile's values, so past its softmax.
     volatile uint8_t* runs = reinterpret_cast<volatile uint8_t*>(tmem_at + 2);
     static_assert(NS <= 8, "tiles in the buffers");
+    static_assert((2 * NS + 14) * 8 + 16 <= 320, "barriers and words");
 
     if (smem_u32(smem) & 1023) {  // the swizzle counts on it, and there is no room to move up
         pdl_wait();
@@ -238,6 +239,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             mbar_init(empty + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(drained + i, 1);
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, L::WEIGH);
             mbar_init(pv_done + i, 1);
@@ -246,6 +248,8 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         mbar_init(q_free, L::WEIGH);
         for (int i = 0; i < 4; ++i) mbar_init(pair + i, L::SHARE);
         mbar_init_fence();
+        // debug fault hook: the first tile's K or V waits for bytes that nothing delivers
+        if (a.inject && blockIdx.x == 0) mbar_expect_tx(full + (Q8 ? shared_place(0, a.inject - 1) % NS : a.inject - 1), 16);
         *failed = 0;
         if (!Q8) {
             prefetch_tmap(&tmk);
@@ -382,6 +386,9 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 if (!values) turn_phase ^= (s.n > 0 ? 1u : 0u) | (s.n > 1 ? 2u : 0u);
             }
             if (!ok) *failed = 1;
+            // Products that are still under way, and what they signal, before the memory is given up.
+            tc_commit(drained + values);
+            if (!mbar_wait_bounded(drained + values, 0)) *failed = 1;
         }
         __syncwarp();
     } else {
@@ -790,6 +797,8 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
             ok = ok && __all_sync(FULL_MASK, mbar_wait_bounded(q_free, segs++ & 1));
         }
         if (!ok) *failed = 1;
+        if constexpr (Q8) asm volatile("cp.async.wait_all;" ::: "memory");  // (a warp that gave up has some on their way)
+        tc_fence_before();
     }
     __syncthreads();
     if (warp == SH_COPY) {

@@ -83,6 +83,7 @@ struct SharedArgs {
     unsigned long long call;
     int table_ld, n_pages, ps, rows, box_runs, nh, nkv, gq, n_groups, side, sets;
     int tile_queries;  // shared_queries()
+    int inject;        // debug fault hook (0 in normal use): 1 for K of the first CTA's first tile, 2 for V
     float scale;
     Shares share;  // of all tiles, among the sets
     struct Group {

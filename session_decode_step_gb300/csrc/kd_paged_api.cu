@@ -9,6 +9,8 @@
 
 namespace kd {
 
+static std::atomic<int> paged_inject{0};  // kd_debug_attn_paged_inject_wait_timeout
+
 static bool paged_shape(int32_t nh, int32_t nkv, int32_t hd, bool q8) {
     if (nkv < 1 || nh < 1 || nh % nkv) return false;
     const int g = nh / nkv;
@@ -209,6 +211,7 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
         sh.vq = (const uint8_t*)vp;
         sh.ks = a.ks;
         sh.vs = a.vs;
+        sh.inject = paged_inject.exchange(0, std::memory_order_relaxed);
         KD_TRY(launch_shared(sh, hd, q8, kp, vp, dev, s));
     }
     KD_TRY(launch_paged(a, hd, q8, true, s));
@@ -219,6 +222,12 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
 }  // namespace kd
 
 extern "C" {
+
+kd_status kd_debug_attn_paged_inject_wait_timeout(int32_t part) {
+    if (part < 0 || part > 1) return kd::failf(KD_ERR_INVALID_ARG, "kd_debug_attn_paged_inject_wait_timeout: part %d", part);
+    kd::paged_inject.store(part + 1, std::memory_order_relaxed);
+    return KD_OK;
+}
 
 size_t kd_attn_paged_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
     using namespace kd;

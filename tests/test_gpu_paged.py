@@ -1053,3 +1053,37 @@ def test_steps_behind_a_prefix_read_once(kdlib, q8, graph):
         c.q = fresh[0][t].cpu().numpy()
         c.kv = [[x[:, :int(c.lens[b])] for x in kv[b]] for b in range(B)]
         c.check(outs[t].cpu().numpy())
+
+
+# --------------------------------------------------------- a wait that runs out ---
+@pytest.mark.parametrize("part", [0, 1])
+@pytest.mark.parametrize("q8", [False, True])
+def test_a_wait_that_runs_out_is_reported(kdlib, q8, part):
+    """One barrier of the prefix kernel waits for bytes that nothing delivers: reported, and the next calls on the same
+    workspace, a smaller one and the same again, are right before the host has cleared anything."""
+    kd = kdlib
+    c = Attn(q8, 32, 8, 128, 16, [1310 + i for i in range(12)], [(12, 1300)], seed=95)
+    small = Attn(q8, 32, 8, 128, 16, [50, 0, 300], seed=11)
+    want, wanted = c.run(kd), small.run(kd)
+    c.check(want)
+    out, small_out, ws = c.new_out(), small.new_out(), c.workspace(kd)
+    kd.kd_debug_attn_paged_inject_wait_timeout(part)
+    small.call(kd, small_out, ws)  # has no prefix to wait for
+    assert kd.kd_attn_device_status(ws) == 0
+    c.call(kd, out, ws)
+    with pytest.raises(kd.KdError) as e:
+        kd.kd_attn_device_status(ws)
+    assert e.value.name == "KD_ERR_DEVICE"
+    kd.kd_debug_attn_paged_inject_wait_timeout(part)
+    c.call(kd, out, ws)  # again, and nothing asked in between
+    small.call(kd, small_out, ws)
+    c.call(kd, out, ws)
+    assert kd.kd_attn_device_status(ws) == 0
+    assert np.array_equal(out.cpu().numpy().view(np.int16), want.view(np.int16))
+    assert np.array_equal(small_out.cpu().numpy().view(np.int16), wanted.view(np.int16))
+
+
+def test_the_wait_hook_has_two_parts(kdlib):
+    for part in (-1, 2):
+        with pytest.raises(kdlib.KdError):
+            kdlib.kd_debug_attn_paged_inject_wait_timeout(part)
