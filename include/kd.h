@@ -671,6 +671,11 @@ kd_status kd_paged_append_q8(const kd_rope_table* rope, const void* k_new, int64
  * lengths and groups (0 for sizes a call refuses). */
 size_t kd_attn_paged_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
 
+/* 1 where kd_attn_paged_decode (q8: kd_attn_paged_decode_q8) reads the whole pages of a group's shared prefix once for its
+ * `rows` sessions, 0 where each session reads them, or for sizes a call refuses.  Host only. */
+int32_t kd_attn_paged_reads_once(int32_t rows, int32_t prefix, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                 int32_t page_size, int32_t q8);
+
 /* A decode step's attention over a paged cache, reading a prefix that sessions share once for all of them:
  *   out[b][qh] = fp16(sum_{t < lens[b]} softmax_t(q[b][qh] . K_t / sqrt(head_dim)) V_t)
  * over KV head qh / (n_heads / n_kv_heads); zeros where lens[b] is 0 (or no key's
@@ -680,7 +685,7 @@ size_t kd_attn_paged_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_he
  * group_prefix[g] keys (0 <= group_prefix[g] <= each of their lens).  The whole pages of
  * that prefix are read through the table of the group's first session (the others'
  * tables are not read there), the page that it ends in through each session's own, which
- * may hold a copy of it.  Where it pays, whole pages are read once for the group, else by each session;
+ * may hold a copy of it.  Where it pays (kd_attn_paged_reads_once), whole pages are read once for the group, else by each session;
  * sharing is an equality of keys that the caller vouches for either way.  n_groups = 0: nothing is shared
  * (group_rows, group_prefix ignored).  Results do not depend on where pages lie;
  * lengths and groups decide how the keys are split, so a session's result can differ in

@@ -172,6 +172,8 @@ def lib():
         L.kd_beam_workspace_bytes.restype = C.c_size_t
         L.kd_attn_paged_workspace_bytes.argtypes = [i32] * 4
         L.kd_attn_paged_workspace_bytes.restype = C.c_size_t
+        L.kd_attn_paged_reads_once.argtypes = [i32] * 7
+        L.kd_attn_paged_reads_once.restype = i32
         _lib = L
     return _lib
 
@@ -766,6 +768,12 @@ def kd_paged_append_q8(plan, k_new, v_new, k_quants, k_scales, v_quants, v_scale
 
 def kd_attn_paged_workspace_bytes(B: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
     return int(lib().kd_attn_paged_workspace_bytes(B, n_heads, n_kv_heads, head_dim))
+
+
+def kd_attn_paged_reads_once(rows: int, prefix: int, n_heads: int, n_kv_heads: int, head_dim: int, page_size: int,
+                             q8: bool = False) -> bool:
+    """Whether the paged attention reads a group's shared prefix once for its sessions, or each session reads it."""
+    return bool(lib().kd_attn_paged_reads_once(rows, prefix, n_heads, n_kv_heads, head_dim, page_size, q8))
 
 
 def kd_attn_paged_decode(q, k_pages, v_pages, table, lens, n_heads: int, n_kv_heads: int, head_dim: int, n_pages: int,

@@ -229,6 +229,15 @@ kd_status kd_debug_attn_paged_inject_wait_timeout(int32_t part) {
     return KD_OK;
 }
 
+int32_t kd_attn_paged_reads_once(int32_t rows, int32_t prefix, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t page_size,
+                                 int32_t q8) {
+    using namespace kd;
+    if (rows < 1 || rows > KD_PAGED_MAX_SEQS || prefix < 0 || prefix > KD_PAGED_MAX_LEN || !paged_shape(n_heads, n_kv_heads, head_dim, q8 != 0) ||
+        n_kv_heads > PAGED_MAX_KV_HEADS || page_size < 16 || page_size % 16 || page_size > 65536)
+        return 0;
+    return shared_once(rows, prefix / page_size * page_size, n_kv_heads, n_heads / n_kv_heads, head_dim, q8 != 0);
+}
+
 size_t kd_attn_paged_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
     using namespace kd;
     if (B < 1 || B > KD_PAGED_MAX_SEQS || !paged_shape(n_heads, n_kv_heads, head_dim, false) || n_kv_heads > PAGED_MAX_KV_HEADS) return 0;

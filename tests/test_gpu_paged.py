@@ -1087,3 +1087,14 @@ def test_the_wait_hook_has_two_parts(kdlib):
     for part in (-1, 2):
         with pytest.raises(kdlib.KdError):
             kdlib.kd_debug_attn_paged_inject_wait_timeout(part)
+
+
+# ------------------------------------------------ which prefixes are read once ---
+def test_the_cases_of_prefixes_read_once_are(kdlib):
+    """The largest groups of the cases above that are meant for the tensor cores go there."""
+    mark = next(m for m in test_prefixes_read_once.pytestmark if m.name == "parametrize")
+    for q8, nh, nkv, hd, ps, groups, own in mark.args[1]:
+        assert any(kdlib.kd_attn_paged_reads_once(n, p, nh, nkv, hd, ps, q8) for n, p in groups), (q8, nh, nkv, hd, groups)
+    for rows, prefix, q8 in ((12, 1290, False), (12, 1300, False), (12, 1300, True), (14, 1280, False), (14, 1280, True)):
+        assert kdlib.kd_attn_paged_reads_once(rows, prefix, 32, 8, 128, 16, q8)
+        assert not kdlib.kd_attn_paged_reads_once(2, prefix, 32, 8, 128, 16, q8)

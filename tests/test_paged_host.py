@@ -256,6 +256,14 @@ def test_workspace_bytes(lib):
         assert f(*a) == 0
 
 
+def test_reads_once_refuses_like_the_call(lib):
+    assert kd.kd_attn_paged_reads_once(16, 1 << 16, 32, 8, 128, 16)
+    for a in ((0, 1 << 16, 32, 8, 128, 16), (257, 1 << 16, 32, 8, 128, 16), (16, -1, 32, 8, 128, 16), (16, (1 << 30) + 1, 32, 8, 128, 16),
+              (16, 1 << 16, 30, 8, 128, 16), (16, 1 << 16, 32, 8, 96, 16), (16, 1 << 16, 32, 8, 128, 24), (16, 1 << 16, 32, 8, 128, 1 << 17),
+              (16, 1 << 16, 32, 8, 64, 16, True), (16, 1 << 16, 1025, 1025, 128, 16)):
+        assert not kd.kd_attn_paged_reads_once(*a), a
+
+
 # -------------------------------------------------------------------- binding ---
 def test_binding_shapes_and_types(calls):
     plan = kd.kd_rope_plan(64, 10000.0)
