@@ -31,15 +31,21 @@ static unsigned long long paged_call_word() {
 // Records of the sessions' own keys: one per CTA and (session, head) at most.
 static size_t paged_records(int B, int nkv) { return (size_t)PAGED_MAX_CTAS + (size_t)B * nkv; }
 
-// A group's shared keys go to the kernel that reads them once where that saves its other sessions this many bytes of
-// reading: the kernel costs some 3 us (5 on Q8_0 caches) of its own before it gains.  32 heads over 8 KV heads of 128, each session
-// with 128 keys of its own, caches not in L2, read once / by each: 3 sessions of 2048 keys (16 MB saved) 10.5 / 8.2 us, 4 of 2048
-// (24 MB) 11.0 / 11.4, 8 of 1024 (28 MB) 10.2 / 11.0, of 8192 17.9 / 33.0, 2 of 8192 (32 MB) 16.3 / 15.9, of 32768 36.7 / 48.0.  On Q8_0
-// caches 4 of 2048 (13 MB) 12.5 / 10.0, 3 of 4096 (17 MB) 14.0 / 14.4, 8 of 2048 (30 MB) 12.8 / 15.2, of 16384 31.3 / 68.5; there a tile takes
-// longer than two sessions' reading of it: 2 of 32768 46.3 / 40.1, 3 45.8 / 54.9.
+// A group's shared keys go to the kernel that reads them once where that saves its other sessions enough bytes of
+// reading: the kernel costs some 3 us (5 on Q8_0 caches) of its own before it gains, and a tile of it takes as long as two
+// or three sessions' reading of the tile.  Each session with 128 keys of its own, 8 KV heads, caches not in L2, read once / by each (us):
+//   fp16, heads of 128, 24 MB: one query a KV head, 3 sessions 13.3 / 14.7, 4 11.0 / 14.2; four, 2 15.3 / 14.0, 4 of 16 MB 11 / 9.6
+//     (of 24 11.0 / 11.4), 2 of 32768 keys 36.7 / 48.0; eight, 3 of 16 MB 11.7 / 13.0;
+//   heads of 64: 2 sessions lose at any length (24 MB 16.4 / 14.0, 65536 keys 47 / 42); 4 of 16 MB 10.3 / 8.2, of 24 10.5 / 11.4, of 48 14.1 / 16.0
+//     (between them, where shares of the tiles end within a head, 14.8 / 12.3); 16 of 24 MB 9.6 / 9.6, of 32 10.0 / 10.9;
+//   Q8_0, up to four queries a KV head: 2 and 3 sessions lose (24 MB 28.5 / 20.5 and 20.2 / 16.2; 3 gain from 128 MB on, 47.8 / 51.6);
+//     4 of 16 MB 15.0 / 12.6, of 24 15.4 / 15.3, of 128 37.9 / 45.5; 8 of 48 15.5 / 19.8;
+//   Q8_0, eight: 3 of 16 MB 15.7 / 19.3, 2 of 24 MB 28.7 / 27.0, of 48 40.4 / 45.8.
 static bool shared_once(int rows, int keys, int nkv, int gq, int hd, bool q8) {
-    const int64_t saves = (int64_t)(rows - 1) * keys * nkv * (q8 ? 272 : hd * 4);
-    return rows > 1 && keys > 0 && (q8 ? saves >= 16 << 20 && rows * gq >= 12 : saves >= 24 << 20);
+    if (rows < 2 || keys < 1) return false;
+    const int64_t saves = (int64_t)(rows - 1) * keys * nkv * (q8 ? 272 : hd * 4) >> 20;
+    if (q8) return gq == 8 ? saves >= (rows > 2 ? 16 : 40) : rows > 3 && saves >= 24;
+    return saves >= 24 && (hd == 128 || rows > 2);
 }
 
 // Choose the sets of CTAs: `side` of them take a (group, head)'s tiles of queries side by side.

@@ -1098,3 +1098,16 @@ def test_the_cases_of_prefixes_read_once_are(kdlib):
     for rows, prefix, q8 in ((12, 1290, False), (12, 1300, False), (12, 1300, True), (14, 1280, False), (14, 1280, True)):
         assert kdlib.kd_attn_paged_reads_once(rows, prefix, 32, 8, 128, 16, q8)
         assert not kdlib.kd_attn_paged_reads_once(2, prefix, 32, 8, 128, 16, q8)
+
+
+@pytest.mark.parametrize("q8,nh,nkv,hd,rows,mb", [(False, 32, 8, 128, 2, 24), (False, 8, 8, 128, 5, 24), (False, 16, 8, 64, 3, 24), (False, 64, 8, 64, 16, 24),
+                                                  (True, 32, 8, 128, 4, 24), (True, 8, 8, 128, 11, 24), (True, 24, 24, 128, 12, 24), (True, 64, 8, 128, 2, 40),
+                                                  (True, 64, 8, 128, 3, 16)])
+def test_both_sides_of_the_reading_rule(kdlib, q8, nh, nkv, hd, rows, mb):
+    """A prefix one page short of being read once, and the same with it: both as the formula has it."""
+    row = nkv * (272 if q8 else 4 * hd)
+    pages = -(-(mb << 20) // ((rows - 1) * row * 16))
+    for p, once in ((16 * pages - 16, False), (16 * pages, True)):
+        assert kdlib.kd_attn_paged_reads_once(rows, p, nh, nkv, hd, 16, q8) == once
+        c = Attn(q8, nh, nkv, hd, 16, [p + 7 + 3 * i for i in range(rows)], [(rows, p + 5)], seed=rows + mb)
+        c.check(c.run(kdlib))

@@ -256,6 +256,22 @@ def test_workspace_bytes(lib):
         assert f(*a) == 0
 
 
+# The rule's sides: (rows, 8 KV heads of gq queries, heads of hd, Q8_0) -> the least MB of other sessions' reading.
+@pytest.mark.parametrize("q8,hd,gq,rows,least", [(0, 128, 1, 2, 24), (0, 128, 8, 256, 24), (0, 64, 4, 2, None), (0, 64, 4, 3, 24), (0, 64, 1, 60, 24),
+                                                 (1, 128, 4, 2, None), (1, 128, 4, 3, None), (1, 128, 4, 4, 24), (1, 128, 1, 90, 24), (1, 128, 8, 2, 40),
+                                                 (1, 128, 8, 3, 16), (0, 128, 4, 1, None), (1, 128, 8, 1, None)])
+def test_reads_once(lib, q8, hd, gq, rows, least):
+    row = 8 * (272 if q8 else 4 * hd)
+    once = lambda keys, page=16: kd.kd_attn_paged_reads_once(rows, keys, 8 * gq, 8, hd, page, q8)
+    if least is None:
+        assert not once(1 << 30) and not once(0)
+        return
+    keys = -(-(least << 20) // ((rows - 1) * row))  # the fewest that save this much
+    pages = -(-keys // 16) * 16
+    assert once(pages) and not once(pages - 1) and once(1 << 30)  # whole pages count
+    assert once(pages, 65536) == (pages % 65536 == 0)
+
+
 def test_reads_once_refuses_like_the_call(lib):
     assert kd.kd_attn_paged_reads_once(16, 1 << 16, 32, 8, 128, 16)
     for a in ((0, 1 << 16, 32, 8, 128, 16), (257, 1 << 16, 32, 8, 128, 16), (16, -1, 32, 8, 128, 16), (16, (1 << 30) + 1, 32, 8, 128, 16),
