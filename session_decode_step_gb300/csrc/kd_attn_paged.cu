@@ -708,19 +708,19 @@ int paged_slots(int hd, int group, bool q8, int dev, int num_sms, cudaError_t* e
     return *e != cudaSuccess ? 0 : n < PAGED_MAX_CTAS ? n : PAGED_MAX_CTAS;
 }
 
-static void paged_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, bool pdl, cudaStream_t s) {
+static void paged_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = 1;
     cfg.stream = s;
 }
 
-cudaError_t launch_paged(const PagedArgs& a, int hd, bool q8, bool pdl, cudaStream_t s) {
+cudaError_t launch_paged(const PagedArgs& a, int hd, bool q8, cudaStream_t s) {
     const int group = a.nh / a.nkv;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    paged_config(cfg, attr, pdl, s);
+    paged_config(cfg, attr, s);
     cfg.gridDim = dim3(a.ctas);
     cfg.blockDim = dim3(PAGED_WARPS * 32);
 #define KD_LAUNCH(HD_, GQ_, Q8_)                                   \
@@ -731,10 +731,10 @@ cudaError_t launch_paged(const PagedArgs& a, int hd, bool q8, bool pdl, cudaStre
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_paged_merge(const PagedArgs& a, const SharedArgs& sh, int hd, bool pdl, cudaStream_t s) {
+cudaError_t launch_paged_merge(const PagedArgs& a, const SharedArgs& sh, int hd, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    paged_config(cfg, attr, pdl, s);
+    paged_config(cfg, attr, s);
     cfg.gridDim = dim3(a.nh, a.B);
     cfg.blockDim = dim3(PAGED_MERGE_WARPS * 32);
     return hd == 64 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64>, a, sh) : cudaLaunchKernelEx(&cfg, paged_merge_kernel<128>, a, sh);

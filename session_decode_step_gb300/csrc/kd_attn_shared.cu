@@ -42,14 +42,7 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// D (tensor memory) += or = A B: A by descriptor in shared memory, or in tensor memory.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((int)add)
-        : "memory");
-}
+// D (tensor memory) += or = A B: A in tensor memory, B by descriptor in shared memory.
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -109,23 +102,6 @@ __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t* v) {  // and wa
         : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Two fp32 operations in one.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
 
 // 2^x to 2^-22, 0 below fp32's normal range.
 __device__ __forceinline__ float tc_exp2(float x) {
@@ -727,13 +703,13 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                             uint32_t p[32];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                const float2 t = fma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                const float2 t = f2_fma(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
                                                       make_float2(c, c), make_float2(-mc, -mc));
                                 const float2 e = make_float2(tc_exp2(t.x), tc_exp2(t.y));
-                                l = add2(l, e);
+                                l = f2_add(l, e);
                                 p[i] = f2_hi(e.x, e.y);
                                 const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
-                                const float2 lo = fma2(hi, make_float2(-1.0f, -1.0f), e);
+                                const float2 lo = f2_fma(hi, make_float2(-1.0f, -1.0f), e);
                                 p[16 + i] = f2_hi(lo.x, lo.y);
                             }
                             tc_st32(st + 32 * k, p);  // the weights in the scores' place: 16 columns hi, 16 lo

@@ -105,7 +105,7 @@ cudaError_t launch_shared(const SharedArgs& a, int hd, bool q8, const void* k, c
 
 // CTAs of the kernel that device dev, the current one, holds at once (0 on a CUDA error, left in *e).
 int paged_slots(int hd, int group, bool q8, int dev, int num_sms, cudaError_t* e);
-cudaError_t launch_paged(const PagedArgs& a, int hd, bool q8, bool pdl, cudaStream_t s);
-cudaError_t launch_paged_merge(const PagedArgs& a, const SharedArgs& sh, int hd, bool pdl, cudaStream_t s);
+cudaError_t launch_paged(const PagedArgs& a, int hd, bool q8, cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedArgs& a, const SharedArgs& sh, int hd, cudaStream_t s);
 
 }  // namespace kd

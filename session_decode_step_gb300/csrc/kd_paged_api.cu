@@ -220,8 +220,8 @@ static kd_status paged_call(const char* fn, bool q8, const float* q, const void*
         sh.inject = paged_inject.exchange(0, std::memory_order_relaxed);
         KD_TRY(launch_shared(sh, hd, q8, kp, vp, dev, s));
     }
-    KD_TRY(launch_paged(a, hd, q8, true, s));
-    if (merge) KD_TRY(launch_paged_merge(a, sh, hd, true, s));
+    KD_TRY(launch_paged(a, hd, q8, s));
+    if (merge) KD_TRY(launch_paged_merge(a, sh, hd, s));
     return KD_OK;
 }
 

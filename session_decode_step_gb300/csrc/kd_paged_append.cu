@@ -46,10 +46,6 @@ template <typename T>
 struct alignas(sizeof(T) * 4) Four {
     T v[4];
 };
-__device__ __forceinline__ float in_f(float x) { return x; }
-__device__ __forceinline__ float in_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ float in_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-
 // Four codes q + 128, q = x / d in fp32 rounded half away from zero, within [-127, 127]; 0 for d = 0.
 // |x| <= 127 d but for a rounding.  x times the reciprocal of d is within 127 2^-22 = 3e-5 of the
 // rounded quotient, so where it lies farther than 6e-5 from the middle between two whole numbers
@@ -177,7 +173,7 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, APPEND_PER_SM) paged_append
     auto values = [&](int i, const T* src, bool have, bool rotates, float (&x)[4]) {
         float o[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = in_f(raw[i].v[e]);
+        for (int e = 0; e < 4; ++e) x[e] = to_f(raw[i].v[e]);
         if (!rotates || !a.rotate) return;
         if (a.r.pairs) {
             o[0] = x[1], o[1] = x[0], o[2] = x[3], o[3] = x[2];
@@ -189,7 +185,7 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, APPEND_PER_SM) paged_append
                 r.y = __shfl_sync(FULL_MASK, w.y, partner);
                 const Four<T> f = *reinterpret_cast<const Four<T>*>(&r);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = in_f(f.v[e]);
+                for (int e = 0; e < 4; ++e) o[e] = to_f(f.v[e]);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[e] = __shfl_sync(FULL_MASK, x[e], partner);
@@ -197,7 +193,7 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, APPEND_PER_SM) paged_append
         } else {
             const T* p = src + i * ROWS * HD;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = have && d + e < a.r.rot ? in_f(p[d + e < half ? d + e + half : d + e - half]) : 0.0f;
+            for (int e = 0; e < 4; ++e) o[e] = have && d + e < a.r.rot ? to_f(p[d + e < half ? d + e + half : d + e - half]) : 0.0f;
         }
         if (turned) {
 #pragma unroll

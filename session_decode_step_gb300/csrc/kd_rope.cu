@@ -37,9 +37,6 @@ template <typename T, int P>
 struct alignas(sizeof(T) * P) RopeVec {
     T v[P];
 };
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_f(float x, float& o) { o = x; }
 __device__ __forceinline__ void from_f(float x, __half& o) { o = __float2half_rn(x); }
 __device__ __forceinline__ void from_f(float x, __nv_bfloat16& o) { o = __float2bfloat16_rn(x); }

@@ -8,6 +8,8 @@
 // come from a table of fp32 pairs, and a rest of at most pi / 256, whose sine and cosine
 // are two terms of their series; the sum theorem joins them.
 #pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "kd.h"
@@ -41,6 +43,11 @@ static __device__ const float2 ROPE_COS[ROPE_TAB] = {
     {0x1.917a6c0000000p-4f, -0x1.eb25ea0000000p-31f}, {0x1.2d520a0000000p-4f, -0x1.a63cc20000000p-29f}, {0x1.91f6600000000p-5f, -0x1.de44fe0000000p-30f},
     {0x1.9215600000000p-6f, -0x1.0b93300000000p-31f}, {0x0.0p+0f, 0x0.0p+0f},
 };
+
+// A value in fp32.
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 // x + y and x * y as fp32 pairs (the rounded result and what the rounding left out).
 __device__ __forceinline__ float2 two_sum(float x, float y) {
@@ -101,31 +108,6 @@ __device__ __forceinline__ void rope_cos_sin(uint64_t phase, const float2* tab, 
     if (q == 1 || q == 2) c = make_float2(-c.x, -c.y);
     if (q >= 2) s = make_float2(-s.x, -s.y);
 }
-
-// Two fp32 operations in one.
-__device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 f2_mul(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 f2_neg(float2 a) { return make_float2(-a.x, -a.y); }
 
 // Two results x c + y s at a time (the sign of the sine is the caller's); each of c and s the
 // sum of its two parts.  EXACT: rounded to fp32 once, up to about 2^-44 (products and the sum with
