@@ -13,7 +13,10 @@ kd_status failf(kd_status st, const char* fmt, ...);
 
 // Set-up made once per device, by the first call there that needs it; its result stands.
 class OncePerDevice {
+public:
     static constexpr int DEVICES = 64;
+
+private:
     std::once_flag once_[DEVICES];
     cudaError_t err_[DEVICES] = {};
 
@@ -25,6 +28,17 @@ public:
         return err_[dev];
     }
 };
+
+// The current device's number of SMs, asked for once per device.
+inline cudaError_t current_sms(int* n) {
+    static OncePerDevice once;
+    static int counts[OncePerDevice::DEVICES];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = once(dev, [dev] { return cudaDeviceGetAttribute(&counts[dev], cudaDevAttrMultiProcessorCount, dev); });
+    if (e == cudaSuccess) *n = counts[dev];
+    return e;
+}
 
 }  // namespace kd
 

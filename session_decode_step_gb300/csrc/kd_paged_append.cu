@@ -265,7 +265,10 @@ static cudaError_t launch_append(AppendArgs& a, bool q8, int hd, cudaStream_t s)
     // them), whole flights where it has several.
     const int U = q8 ? append_flight<T, true>() : append_flight<T, false>();
     const int heads = 2 * a.nkv + a.nh, rows = hd == 64 ? 2 : 1;
-    int64_t per = (int64_t)a.tokens * heads / (152 * 40);
+    int sms = 0;
+    const cudaError_t e = current_sms(&sms);
+    if (e != cudaSuccess) return e;
+    int64_t per = (int64_t)a.tokens * heads / (sms * 40);
     per = per < rows ? rows : per < U * rows ? per / rows * rows : per / (U * rows) * (U * rows);
     a.per = (int)(per < heads ? per : heads);
     a.groups = (heads + a.per - 1) / a.per;

@@ -137,14 +137,14 @@ __global__ void __launch_bounds__(ROPE_THREADS, 3) rope_kernel(const __grid_cons
 }
 
 template <typename T, int P>
-static cudaError_t launch_rope_p(RopeArgs& a, cudaStream_t s) {
+static cudaError_t launch_rope_p(RopeArgs& a, int sms, cudaStream_t s) {
     a.nr = a.r.pairs ? (a.r.rot + 2 * P - 1) / (2 * P) : a.r.rot / 2 / P;
     a.nc = a.hd / (2 * P);
     const int by = ROPE_THREADS / a.nc;
     // Heads per thread: the angles are formed once for them, and a thread that loops keeps
     // loads in flight; but every SM should have a thousand threads' worth of work first.
     const int64_t threads = (int64_t)a.tokens * a.heads * a.nc;
-    int64_t per = threads / (152 * 512);
+    int64_t per = threads / ((int64_t)sms * 512);
     per = per < 1 ? 1 : per > 8 ? 8 : per;
     a.per = (int)per;
     a.groups = (a.heads + a.per - 1) / a.per;
@@ -201,9 +201,12 @@ static cudaError_t launch_rope(RopeArgs& a, cudaStream_t s) {
         return a.hd % (2 * p) == 0 && a.ld % p == 0 && a.ld_out % p == 0 && (a.r.pairs || a.r.rot % (2 * p) == 0) &&
                (((uintptr_t)a.x | (uintptr_t)a.out) & (p * sizeof(T) - 1)) == 0;
     };
-    if (fits(W)) return launch_rope_p<T, W>(a, s);
-    if (fits(2)) return launch_rope_p<T, 2>(a, s);
-    if (a.hd % 2 == 0) return launch_rope_p<T, 1>(a, s);
+    int sms = 0;
+    const cudaError_t e = current_sms(&sms);
+    if (e != cudaSuccess) return e;
+    if (fits(W)) return launch_rope_p<T, W>(a, sms, s);
+    if (fits(2)) return launch_rope_p<T, 2>(a, sms, s);
+    if (a.hd % 2 == 0) return launch_rope_p<T, 1>(a, sms, s);
     const int64_t threads = (int64_t)a.tokens * a.heads * (a.hd - a.r.rot / 2);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
