@@ -142,8 +142,8 @@ struct SharedSmem {
     static constexpr int RING = 0, BARS = SLOTS * TILE;
     static constexpr int MAXIMA = BARS + 320;          // [2][share][row]: what the warps of a row tell each other
     static constexpr int CODES = MAXIMA + 2 * SHARE * QUERIES * 4;  // Q8_0: a part's codes, by thread, and scales, by warp, on their way
-    static constexpr int EARLY = CODES + 256 * 4 * 16 + 8 * 128;  // Q8_0: V's scales of the K part on its way, by warp
-    static constexpr int UPS = EARLY + 8 * 128;        // [tile % 8][K, V][row]: what rows whose scales are large were divided by
+    static constexpr int EARLY = CODES + 256 * 4 * 16 + 8 * 128;  // [tile % 2]: V's scales, with K on their way, by warp
+    static constexpr int UPS = EARLY + 2 * 8 * 128;        // [tile % 8][K, V][row]: what rows whose scales are large were divided by
     static constexpr int LARGE = UPS + 8 * 2 * SHARED_TILE * 4;  // [tile % 8][warp]: 1 where there is such a row, else the warp leaves no divisors
     static constexpr int TOTAL = Q8 ? LARGE + 8 * 8 : CODES;
     static_assert(TOTAL <= 227 * 1024, "opt-in shared memory");
@@ -401,8 +401,6 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
         struct Codes {
             uint4 v[4];
             __half d[4];
-            int large;   // rows of the warp's, of K or V, have large scales; then those of lanes 0 .. 7 (rows 2 (lane % 2) and
-            uint2 down;  // the next, of i = lane / 2) are divided by 2^x and 2^y
         };
         // The thread's codes and scales of a part, to its own place in shared memory: loads to registers would be
         // waited for together with those of the part after.
@@ -429,14 +427,12 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                              : "memory");
                 // V's, too: its tile's weights are formed before it is made
                 if (!part)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(early_at + lane * 16),
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(early_at + (T & 1) * 1024 + lane * 16),
                                  "l"((const uint8_t*)a.vs + ((t >> 5) & 3) * 32 + (lane & 1) * 16 + (int64_t)max(first, 0) * 8), "r"(first >= 0 ? 16 : 0)
                                  : "memory");
             }
         };
-        unsigned v_large = 0;  // a bit for even and odd tiles
-        // Part `part` of tile T; with K the rows' divisors, V's among them, are left for the warps that weigh.
-        auto landed = [&](Codes& f, int part, uint32_t T) {
+        auto landed = [&](Codes& f) {
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
 #pragma unroll
@@ -449,50 +445,47 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(d) : "r"(scales_at + i * 32 + (trow & 3) * 8 + (chunk >> 1) * 2) : "memory");
                 f.d[i] = __ushort_as_half(d);
             }
-            // Rows with large scales: looked for in the thread's own ones, and with K in V's; all else only where there are any.
-            uint4 of_v = make_uint4(0, 0, 0, 0);
-            if (!part) {
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top = max(top, (uint32_t)__half_as_ushort(f.d[i]) & 0x7fffu);
-                if (lane < 8) of_v = lds_v4(smem + L::EARLY + (t >> 5) * 128 + lane * 16);
-                f.large = __any_sync(FULL_MASK, top >= 0x6000u || shared_large(of_v.x, of_v.y) || shared_large(of_v.z, of_v.w));
-                v_large = (v_large & ~(1u << (T & 1))) | (f.large ? 1u << (T & 1) : 0u);
-                if (lane == 0) smem[L::LARGE + (T & 7) * 8 + (t >> 5)] = (uint8_t)f.large;
-            } else {
-                f.large = (v_large >> (T & 1)) & 1;
-            }
-            f.down = make_uint2(0, 0);
-            if (f.large) {
-                uint4 own = make_uint4(0, 0, 0, 0);
-                if (lane < 8) own = lds_v4(smem + L::CODES + 256 * 4 * 16 + (t >> 5) * 128 + lane * 16);
-                f.down = make_uint2(shared_down(own.x, own.y), shared_down(own.z, own.w));
-                if (!part && lane < 8) {
-                    float* up = reinterpret_cast<float*>(smem + L::UPS) + (T & 7) * 2 * SHARED_TILE + 32 * (lane >> 1) + 4 * (t >> 5) + 2 * (lane & 1);
-                    *reinterpret_cast<float2*>(up) = make_float2((float)(1 << f.down.x), (float)(1 << f.down.y));
-                    *reinterpret_cast<float2*>(up + SHARED_TILE) = make_float2((float)(1 << shared_down(of_v.x, of_v.y)), (float)(1 << shared_down(of_v.z, of_v.w)));
-                }
-            }
             // read before the next part's copies are issued
 #pragma unroll
             for (int i = 0; i < 4; ++i) asm volatile("" : "+r"(f.v[i].x), "+r"(f.v[i].y), "+r"(f.v[i].z), "+r"(f.v[i].w)::"memory");
             __syncwarp();
         };
+        unsigned v_large = 0;  // a bit for even and odd tiles
         auto make = [&](int part, uint32_t T, const Codes& f) {
+            // Rows of the warp's with large scales: with K looked for in the thread's own scales and in V's; all else only where there are any.
+            const uint8_t* early = smem + L::EARLY + (T & 1) * 1024 + (t >> 5) * 128;
+            bool large = (v_large >> (T & 1)) & 1;
+            if (!part) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = max(top, (uint32_t)__half_as_ushort(f.d[i]) & 0x7fffu);
+                uint4 of_v = make_uint4(0, 0, 0, 0);
+                if (lane < 8) of_v = lds_v4(early + lane * 16);
+                large = __any_sync(FULL_MASK, top >= 0x6000u || shared_large(of_v.x, of_v.y) || shared_large(of_v.z, of_v.w));
+                v_large = (v_large & ~(1u << (T & 1))) | (large ? 1u << (T & 1) : 0u);
+                if (lane == 0) smem[L::LARGE + (T & 7) * 8 + (t >> 5)] = large;
+                if (large && lane < 8) {  // V's divisors, for the warps that weigh
+                    float* up = reinterpret_cast<float*>(smem + L::UPS) + ((T & 7) * 2 + 1) * SHARED_TILE + 32 * (lane >> 1) + 4 * (t >> 5) + 2 * (lane & 1);
+                    *reinterpret_cast<float2*>(up) = make_float2((float)(1 << shared_down(of_v.x, of_v.y)), (float)(1 << shared_down(of_v.z, of_v.w)));
+                }
+            }
             const uint32_t place = shared_place(T, part), s0 = place % NS, s1 = s0 + 1;
             if (!__all_sync(FULL_MASK, mbar_wait_bounded(empty + s0, ((place / NS) & 1) ^ 1))) return false;
             uint8_t* dst = smem + L::RING + (chunk >> 2) * L::COL + trow * 128;
             const uint32_t c0 = ((2 * (chunk & 3)) ^ (trow & 7)) << 4;  // the second 8 dims are 16 bytes away in it
-            auto pairs = [&](auto large) {
+            auto pairs = [&](auto divided) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const __half2 dd = __half2half2(f.d[i]);
                     const uint32_t w[4] = {f.v[i].x, f.v[i].y, f.v[i].z, f.v[i].w};
                     __half2 div = dd;
-                    if constexpr (decltype(large)::value) {  // codes are divided, exactly, before the product: a smaller scale of the row keeps its bits
-                        const int from = 2 * i + ((trow >> 1) & 1);
-                        const unsigned k0 = __shfl_sync(FULL_MASK, f.down.x, from), k1 = __shfl_sync(FULL_MASK, f.down.y, from);
-                        div = __float2half2_rn(1.0f / (float)(1 << ((trow & 1) ? k1 : k0)));
+                    if constexpr (decltype(divided)::value) {  // codes are divided, exactly, before the product: a smaller scale of the row keeps its bits
+                        uint32_t d = (uint32_t)__half_as_ushort(f.d[i]) & 0x7fffu;  // the largest of the row's four
+                        d = max(d, __shfl_xor_sync(FULL_MASK, d, 2));
+                        d = max(d, __shfl_xor_sync(FULL_MASK, d, 16));
+                        const float up = (float)(1 << shared_down(d, 0));
+                        if (!part && (lane & 19) == 0) reinterpret_cast<float*>(smem + L::UPS)[(T & 7) * 2 * SHARED_TILE + 32 * i + trow] = up;
+                        div = __float2half2_rn(1.0f / up);
                     }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -501,7 +494,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                         for (int e = 0; e < 4; ++e) {
                             const uint32_t q = (e & 1) ? u8x2_hi_to_half2(w[2 * k + (e >> 1)]) : u8x2_lo_to_half2(w[2 * k + (e >> 1)]);
                             __half2 c = *reinterpret_cast<const __half2*>(&q);
-                            if constexpr (decltype(large)::value) c = __hmul2_rn(c, div);
+                            if constexpr (decltype(divided)::value) c = __hmul2_rn(c, div);
                             const __half2 h = __hmul2_rn(c, dd), l = __hfma2(c, dd, __hneg2(h));
                             hi[e] = *reinterpret_cast<const uint32_t*>(&h);
                             lo[e] = *reinterpret_cast<const uint32_t*>(&l);
@@ -512,7 +505,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                     }
                 }
             };
-            if (f.large) pairs(std::true_type{});
+            if (large) pairs(std::true_type{});
             else pairs(std::false_type{});
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -554,8 +547,8 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
                 fetch_k();
                 for (int part = 0, k = 0; k < 2 * s.n && ok; ++k) {
                     Codes f;
+                    landed(f);
                     const int j = part ? nv - 1 : nk - 1, now = part;
-                    landed(f, now, tiles + j);
                     if (k + 1 < 2 * s.n) {
                         part = part ? nk == s.n : s.n == 1 || nk > 1;
                         if (!part) {
