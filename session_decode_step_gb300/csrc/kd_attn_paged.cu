@@ -18,9 +18,10 @@
 // Q8_0 form scales each 32-dim block's partial scores by the key's block scale in fp32
 // and multiplies the value scales into the weights, so neither cache is rounded again.
 //
-// Long sessions are bound by memory: 48 of 0 to 16384 keys (462 MB, 8 KV heads of 128) take 82 us with the merge, 5.9 TB/s
+// Long sessions are bound by memory: 48 of 0 to 16384 keys (462 MB, 8 KV heads of 128) take 84 us with the merge, 5.8 TB/s
 // without it (a CTA at its share of the rate would need 560 for one (session, head) of 16384).  Few keys are bound by
-// latency: 37 of one session 3.9 us (launch, page, keys), 8 sessions of 1300 10.2 (640 blocks on 456 CTAs, merge 2.5).
+// latency: 37 of one session 3.6 us (launch, page, keys), 8 sessions of 1238 to 1365 13.7, 10.3 where the keys are in L2 (664
+// blocks on 456 CTAs, merge 2.5).  The Q8_0 form is bound by instructions: the 48 sessions (246 MB) 73 us, issue 0.62.
 //
 // Nothing waits on an mbarrier, so nothing can run out.
 #include <cuda_fp16.h>

@@ -16,11 +16,12 @@
 // at the SM's share of the bf16 rate, while its 64 KB take 1.4 us of the SM's share of the memory's.
 // Q8_0 rows become such pairs, too (three products each), made by eight warps of their own.  A row that holds a scale of
 // 512 or more, whose values may leave fp16's range, is divided by a power of two; K's goes back to the scores, V's to the
-// weights, whose maximum such a tile always moves (to look for such rows costs 2 us of the 96 below).
+// weights, whose maximum such a tile always moves (to look for such rows costs 1 to 2 us of the 97 below).
 //
-// Two groups of 32 sessions behind 16384 and 15383 keys, 8 KV heads of 128, take 59 us with the sessions' own 91 MB and the
-// merge, 392 where each reads its prefix; a tile takes 3300 cycles then, so the tensor core bounds it, not memory.  Three
-// groups of 8 on Q8_0 caches behind 26 k keys: 96 us, 311 where each reads, 4400 cycles a tile: shared memory's rate (512 cycles
+// Two groups of 32 sessions behind 16384 and 15383 keys, 8 KV heads of 128, take 61 us with the sessions' own 91 MB and the
+// merge, 392 where each reads its prefix; a tile takes 3300 cycles then: neither memory nor the tensor core (active 0.44) bounds it, but the chain of
+// scores, maximum, exchange, weights and products, of which two tiles are in turn.  Three
+// groups of 8 on Q8_0 caches behind 26 k keys: 97 us, 311 where each reads, 4400 cycles a tile: shared memory's rate (512 cycles
 // to write a part's pairs, 768 for three products to read them, 270 for the codes, of 2200 a part).
 //
 // CTAs share the tiles of all (group, KV head)s equally (kd_paged.h); what one finds of a

@@ -12,9 +12,9 @@
 //
 // Few tokens are bound by a launch and two dependent loads (a position's page, then the
 // row): 8 tokens of 32 + 8 heads take 2.3 us, an empty launch 2.1.  Many are bound by issue, near
-// memory's rate: 8.8 k bf16 tokens of 32 + 8 heads of 128 (277 MB) 48 us, 5.7 TB/s; with K, V and queries
+// memory's rate: 8.8 k bf16 tokens of 32 + 8 heads of 128 (277 MB) 49 us, 5.6 TB/s; with K, V and queries
 // in one loop, a head's kind asked for each time, 64; with blocks that stay and take the next token, 62 (the last ones are
-// waited for).  6.3 k tokens of 8 heads into Q8_0 21.4 us (floor 5.9): the exact rotation, three shuffles a maximum and the codes;
+// waited for).  6.3 k tokens of 8 heads into Q8_0 21.4 us, 23 with inputs that are not in L2 (floor 5.9): the exact rotation, three shuffles a maximum and the codes;
 // with each lane forming its own four angles, twice each in a warp, 24.7 and 2.7 for the 8 tokens.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
