@@ -8,7 +8,8 @@
 // place comes from the page table by one look-up per warp.
 // Q8_0 rows: the 8 lanes of a 32-value block find its maximum by shuffles and store 4 codes
 // each.  There k is rounded to fp32 exactly once (kd_rope.cuh) before the division, so that
-// a code never depends on how the rotation was summed.
+// a code never depends on how the rotation was summed.  (Keys below 2^-120 aside: what their products' roundings leave out is
+// less than fp32 holds.  Their scales are 0.)
 //
 // Few tokens are bound by a launch and two dependent loads (a position's page, then the
 // row): 8 tokens of 32 + 8 heads take 2.3 us, an empty launch 2.1.  Many are bound by issue, near
