@@ -326,7 +326,7 @@ kd_status kd_rope_plan(const kd_rope_config* c, kd_rope_table* out) {
         if (blends) {
             Two slow;  // how much of the pair's pace is slowed
             if (c->scaling == KD_ROPE_BANDS)
-                slow = plus(one, negative(over(plus(over(times({(double)c->original_ctx, 0.0}, f), two_pi), {-c->low, 0.0}), plus({c->high, 0.0}, {-c->low, 0.0}))));
+                slow = over(plus({c->high, 0.0}, negative(over(times({(double)c->original_ctx, 0.0}, f), two_pi))), plus({c->high, 0.0}, {-c->low, 0.0}));
             else
                 slow = over({i - a, 0.0}, {std::fmax(b - a, 0.001), 0.0});
             if (slow.hi <= 0.0) slow = {0.0, 0.0};

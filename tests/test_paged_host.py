@@ -112,6 +112,21 @@ def test_plan_turns_to_the_last_bit(lib, rot, theta, kw):
             assert off <= decimal.Decimal("0.5") + f * 2 ** 64 / 2 ** 96 + f * 2 ** 64 / decimal.Decimal(10) ** 58, (i, off)
 
 
+@pytest.mark.parametrize("scaling", [2, 3])
+@pytest.mark.parametrize("low,high", [(1.0, 1.0 + 2.0 ** -52), (5e-324, 1e-323), (1e-320, 1e308), (1e307, 1.7e308), (2.0 ** -1022, 1.0)])
+@pytest.mark.parametrize("factor", [8.0, 1e-300, 1e308])
+def test_plan_bands_of_any_width(lib, scaling, low, high, factor):
+    """Bands so narrow or so far out that a quotient leaves a double's range: pairs keep their pace, are slowed, or between."""
+    t = kd.kd_rope_plan(128, 10000.0, scaling=scaling, factor=factor, low=low, high=high, original_ctx=8192)
+    keep, slowed = (kd.kd_rope_plan(128, 10000.0, **kw) for kw in (dict(), dict(scaling=1, factor=factor)))
+    ends = sum(a in (b, c) for a, b, c in zip(t.turns[:64], keep.turns, slowed.turns))
+    assert ends >= (0 if high == 1e308 or low == 2.0 ** -1022 else 62)
+    if scaling == 2 and high < 1e-300:
+        assert list(t.turns[:64]) == list(keep.turns[:64])
+    if scaling == 2 and low == 1e307:
+        assert list(t.turns[:64]) == list(slowed.turns[:64])
+
+
 def test_plan_defaults(lib):
     t = kd.kd_rope_plan(128, 10000.0)
     assert (t.rot_dim, t.layout, t.magnitude) == (128, kd.KD_ROPE_HALF, 1.0)
